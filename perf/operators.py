@@ -347,6 +347,11 @@ def run(state):
 _GRID = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
 
 
+def _exact_power(e):
+    """2^e in binary64 for whole e, from its bits (pow on the GPU is off by an ulp for some)."""
+    return ((e.to(torch.int64) + 1023) << 52).view(torch.float64)
+
+
 def _exact_round_trip(x):
     """MXFP4 of each row from its definition, in binary64: the quantum of the E2M1 grid at |y| is 1/2 below 2,
     1 below 4 and 2 above, and torch.round takes ties to even multiples of it, which are the even codes."""
@@ -354,11 +359,11 @@ def _exact_round_trip(x):
     b = torch.cat((x.double(), x.new_zeros(*x.shape[:-1], -cols % 32, dtype=torch.float64)), -1).unflatten(-1, (-1, 32))
     a = b.abs().amax(-1, keepdim=True).clamp(min=2.0 ** -125)
     one = torch.floor(torch.log2(a))  # off by one where log2 rounds up to a whole number: put right below
-    one = torch.where(2.0 ** one > a, one - 1, torch.where(2.0 ** (one + 1) <= a, one + 1, one))
-    y = b.abs() / 2.0 ** (one - 2)
+    one = torch.where(_exact_power(one) > a, one - 1, torch.where(_exact_power(one + 1) <= a, one + 1, one))
+    y = b.abs() / _exact_power(one - 2)
     quantum = torch.where(y < 2, 0.5, torch.where(y < 4, 1.0, 2.0)).double()
     y = (torch.round(y / quantum) * quantum).clamp(max=6.0)
-    return (torch.copysign(y, b) * 2.0 ** (one - 2)).flatten(-2)[..., :cols]
+    return (torch.copysign(y, b) * _exact_power(one - 2)).flatten(-2)[..., :cols]
 
 
 def _exact_decode(packed, scales):
@@ -366,7 +371,7 @@ def _exact_decode(packed, scales):
     grid = torch.tensor(_GRID + tuple(-v for v in _GRID), dtype=torch.float64, device=packed.device)
     lo, hi = grid[(packed % 16).long()], grid[(packed // 16).long()]
     x = torch.stack((lo, hi), -1).reshape(*packed.shape[:-1], -1)
-    return x * torch.pow(2.0, scales.double() - 127).repeat_interleave(32, -1)
+    return x * _exact_power(scales.long() - 127).repeat_interleave(32, -1)
 
 
 def exact(case, seed):

@@ -9,6 +9,9 @@ of the same name; PyTorch provides device memory and the current stream.
     out  = fc2(gate_up_bf16, w_q)                        # both per-step calls
     out  = fc2_host(gate_up_host, w_q)                   # host in, host out
 
+The MXFP4 operators (mxfp4.py) serve language models beside it: quantisation,
+product, a paged 4-bit KV cache and attention over it.
+
 Sources: "FC2 NVFP4 Scheduling Results" (Canonical Operation; Production
 Integration: forward_swiglu = accepted producer, then the FC2 GEMM) and
 "GB10 component-2 nsys summary" (nvfp4; native_pack_validation).
@@ -21,9 +24,11 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
+from . import mxfp4
 from ._lib import NVFP4Error, load  # noqa: F401
+from .mxfp4 import *  # noqa: F401,F403
 
-__all__ = ["NVFP4Tensor", "NVFP4Error", "load", "padded_rows", "qdata_bytes", "scale_bytes", "scale_offset",
+__all__ = mxfp4.__all__ + ["NVFP4Tensor", "NVFP4Error", "load", "padded_rows", "qdata_bytes", "scale_bytes", "scale_offset",
            "nvfp4_quantize_weight", "swiglu_nvfp4_quantize", "nvfp4_fc2_gemm", "nvfp4_fc1_swiglu", "fc2", "fc2_host",
            "empty_nvfp4", "read_rec"]
 

@@ -31,7 +31,34 @@ EXPORTED = ["nvfp4_padded_rows", "nvfp4_qdata_bytes", "nvfp4_scale_bytes", "nvfp
             "nvfp4_diag_wait_timeout", "nvfp4_diag_mma_peak", "nvfp4_diag_mma_peak_pairs",
             "nvfp4_diag_quotient_codes", "nvfp4_fc1_swiglu", "nvfp4_quantize_with_amax",
             "nvfp4_diag_silu_epilogue", "nvfp4_diag_block_scale_codes", "nvfp4_diag_tc_e2m1_read", "nvfp4_fc2_host",
-            "nvfp4_fc2_host_noalloc", "nvfp4_diag_fc2_gemm_clock"]
+            "nvfp4_fc2_host_noalloc", "nvfp4_diag_fc2_gemm_clock",
+            "mxfp4_padded_cols", "mxfp4_qdata_bytes", "mxfp4_scale_bytes", "mxfp4_scale_offset", "mxfp4_quantize",
+            "mxfp4_dequantize", "mxfp4_gemm", "mxfp4_linear_workspace_bytes", "mxfp4_linear", "mxfp4_cache_write",
+            "mxfp4_cache_read", "mxfp4_attention_workspace_bytes", "mxfp4_cache_attention"]
+
+MXFP4_BF16 = 0
+MXFP4_FP16 = 1
+MXFP4_FP32 = 2
+
+
+class CacheStruct(ctypes.Structure):
+    """mxfp4_cache of mxfp4.h."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class AttentionStruct(ctypes.Structure):
+    """mxfp4_attention of mxfp4.h."""
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("q_starts", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("dev_status", ctypes.c_void_p), ("q_st", ctypes.c_int64),
+                ("q_sh", ctypes.c_int64), ("o_st", ctypes.c_int64), ("o_sh", ctypes.c_int64),
+                ("table_ld", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64), ("seqs", ctypes.c_int32),
+                ("total_q", ctypes.c_int32), ("max_queries", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("sinks", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
 
 _lock = threading.Lock()
 _lib = None
@@ -104,6 +131,33 @@ def load(path: str | None = None) -> ctypes.CDLL:
         L.nvfp4_fc2_host_noalloc.restype = st
         L.nvfp4_fc2_host_noalloc.argtypes = [vp, i64, i64, i64, vp, vp, vp, i64, vp, vp, vp]
         L.nvfp4_diag_tc_e2m1_read.argtypes = [vp, vp, vp, vp]
+        i32 = ctypes.c_int32
+        L.mxfp4_padded_cols.restype = i64
+        L.mxfp4_padded_cols.argtypes = [i64]
+        L.mxfp4_qdata_bytes.restype = i64
+        L.mxfp4_qdata_bytes.argtypes = [i64, i64]
+        L.mxfp4_scale_bytes.restype = i64
+        L.mxfp4_scale_bytes.argtypes = [i64, i64]
+        L.mxfp4_scale_offset.restype = i64
+        L.mxfp4_scale_offset.argtypes = [i64, i64, i64]
+        L.mxfp4_quantize.restype = st
+        L.mxfp4_quantize.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+        L.mxfp4_dequantize.restype = st
+        L.mxfp4_dequantize.argtypes = [vp, vp, i64, i64, vp, i32, i64, vp]
+        L.mxfp4_gemm.restype = st
+        L.mxfp4_gemm.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, i32, i64, vp, vp]
+        L.mxfp4_linear_workspace_bytes.restype = i64
+        L.mxfp4_linear_workspace_bytes.argtypes = [i64, i64]
+        L.mxfp4_linear.restype = st
+        L.mxfp4_linear.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, vp, i32, i64, vp, i64, vp, vp]
+        L.mxfp4_cache_write.restype = st
+        L.mxfp4_cache_write.argtypes = [vp, vp, vp, i32, i64, i64, i64, i64, i64, vp, vp]
+        L.mxfp4_cache_read.restype = st
+        L.mxfp4_cache_read.argtypes = [vp, vp, i64, i64, vp, i64, vp, vp, i32, vp]
+        L.mxfp4_attention_workspace_bytes.restype = i64
+        L.mxfp4_attention_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.mxfp4_cache_attention.restype = st
+        L.mxfp4_cache_attention.argtypes = [vp, vp, vp]
         _lib = L
         return _lib
 

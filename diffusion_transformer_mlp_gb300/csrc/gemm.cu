@@ -749,11 +749,13 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+}  // namespace
+
 nvfp4_status make_map(CUtensorMap* map, CUtensorMapDataType dt, const void* base, int rank, const cuuint64_t* dims,
                       const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle, const char* what) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return fail(NVFP4_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  const cuuint32_t estr[3] = {1, 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   const CUresult r = fn(map, dt, cuuint32_t(rank), const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -764,6 +766,8 @@ nvfp4_status make_map(CUtensorMap* map, CUtensorMapDataType dt, const void* base
   }
   return NVFP4_OK;
 }
+
+namespace {
 
 // CTA pairs of k_fc2_gemm<gated> that are resident at once on the current
 // device (two-CTA clusters at `smem` bytes each: SMs / 2 on a GB300, fewer

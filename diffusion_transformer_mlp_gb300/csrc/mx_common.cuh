@@ -1,0 +1,175 @@
+// Device helpers of the MXFP4 operators: the element types outside the 4-bit
+// format, the block encoder and the E2M1 / E8M0 decoders.
+//
+// A block is 32 consecutive elements with one E8M0 scale 2^(E-127), E - 127 =
+// floor(log2 max|x|) - 2, so the block's largest element lands in [4, 8) and
+// E2M1 (largest value 6) saturates it.  Scaling by a power of two is exact,
+// which leaves the E2M1 rounding as the only one.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "mxfp4.h"
+
+namespace nvfp4 {
+
+inline int mx_elem_bytes(int32_t dtype) { return dtype == MXFP4_FP32 ? 4 : 2; }
+inline bool mx_dtype_ok(int32_t dtype) { return dtype == MXFP4_BF16 || dtype == MXFP4_FP16 || dtype == MXFP4_FP32; }
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Two 16-bit elements of a 32-bit word as binary32.
+template <typename T>
+__device__ __forceinline__ float2 word_to_f32(uint32_t w);
+template <>
+__device__ __forceinline__ float2 word_to_f32<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <>
+__device__ __forceinline__ float2 word_to_f32<__nv_bfloat16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+// Two binary32 values rounded to nearest even into one word (lo in bits 0..15).
+template <typename T>
+__device__ __forceinline__ uint32_t f32_to_word(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t f32_to_word<__half>(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <>
+__device__ __forceinline__ uint32_t f32_to_word<__nv_bfloat16>(float lo, float hi) {
+  return bf16x2_rn(lo, hi);
+}
+
+// 16 consecutive elements at a 16-byte aligned address.
+template <typename T>
+__device__ __forceinline__ void load16(const T* __restrict__ p, float (&f)[16]) {
+  if constexpr (sizeof(T) == 4) {
+    const float4* q = reinterpret_cast<const float4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = q[i];
+      f[4 * i] = v.x, f[4 * i + 1] = v.y, f[4 * i + 2] = v.z, f[4 * i + 3] = v.w;
+    }
+  } else {
+    const uint4* q = reinterpret_cast<const uint4*>(p);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 v = q[i];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 t = word_to_f32<T>(w[k]);
+        f[8 * i + 2 * k] = t.x, f[8 * i + 2 * k + 1] = t.y;
+      }
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store16(T* __restrict__ p, const float (&f)[16]) {
+  if constexpr (sizeof(T) == 4) {
+    float4* q = reinterpret_cast<float4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+  } else {
+    uint4* q = reinterpret_cast<uint4*>(p);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      q[i] = make_uint4(f32_to_word<T>(f[8 * i], f[8 * i + 1]), f32_to_word<T>(f[8 * i + 2], f[8 * i + 3]),
+                        f32_to_word<T>(f[8 * i + 4], f[8 * i + 5]), f32_to_word<T>(f[8 * i + 6], f[8 * i + 7]));
+  }
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Eight E2M1 codes of a word, element i in bits 4i .. 4i+3.
+__device__ __forceinline__ uint32_t e2m1x8(const float* q) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+  return w;
+}
+
+// Half of a block: the lane and its neighbour (lane ^ 1) hold 16 elements
+// each.  Returns the lane's 16 codes and the block's scale code.  A block
+// with an infinity or a NaN gets E = 255 and zero codes.
+__device__ __forceinline__ uint2 mx_encode_half(float (&f)[16], uint32_t& scale) {
+  float am = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) am = max_nan(am, fabsf(f[i]));
+  am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+  const uint32_t eb = (__float_as_uint(am) >> 23) & 0xFFu;  // biased exponent: floor(log2 am) + 127 for normal am
+  if (eb == 255u) {
+    scale = 255u;
+    return make_uint2(0u, 0u);
+  }
+  const uint32_t e = eb > 2u ? eb - 2u : 0u;
+  scale = e;
+  const float inv = __uint_as_float((254u - e) << 23);  // 2^(127 - E), E <= 252
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] *= inv;
+  return make_uint2(e2m1x8(f), e2m1x8(f + 8));
+}
+
+// The eight E2M1 values of a word as four pairs of FP16 (exact).
+__device__ __forceinline__ void e2m1x8_to_half(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+// Value of an E8M0 code: 2^(E-127), NaN for 255.
+__device__ __forceinline__ float e8m0_value(uint32_t e) {
+  return __uint_as_float(e == 0u ? 0x00400000u : (e == 255u ? 0x7FFFFFFFu : e << 23));
+}
+
+// 16 values of one lane's codes under one scale.
+__device__ __forceinline__ void mx_decode16(uint2 q, uint32_t scale, float (&f)[16]) {
+  const float s = e8m0_value(scale);
+  uint32_t h[4];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    e2m1x8_to_half(half ? q.y : q.x, h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 t = word_to_f32<__half>(h[i]);
+      f[8 * half + 2 * i] = t.x * s, f[8 * half + 2 * i + 1] = t.y * s;
+    }
+  }
+}
+
+}  // namespace nvfp4

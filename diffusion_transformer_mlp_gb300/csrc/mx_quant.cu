@@ -1,0 +1,218 @@
+// MXFP4 quantisation of a matrix and its way back.
+//
+// Both are one streaming pass: 16 elements a lane (two lanes a block), 512 a
+// warp, the block maximum by one shuffle, codes as one 8-byte store a lane and
+// scales as one 4-byte store for every eight lanes (four scale columns of the
+// tiled layout).  They are bound by HBM: sizeof(T) + 17/32 bytes an element
+// each way.
+//
+// Rows that are not 16-byte aligned (an odd row stride, an odd base) go
+// through a per-warp slice of shared memory, so that global accesses stay
+// coalesced one element a lane while each lane still owns 16 consecutive
+// elements.
+#include <string>
+
+#include "mx_common.cuh"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kUnit = 512;  // elements of one row that a warp takes at a time
+// Element i of a warp's slice lies at i + i / 16: lane l's 16 elements start
+// at 17 l, so the lanes of a column access fall into different banks.
+constexpr int kSlice = kUnit + kUnit / 16;
+
+struct MatParams {
+  int64_t rows, cols, ld;
+  int64_t units;         // rows * units_per_row
+  int32_t units_per_row;
+  int32_t groups;        // cols_pad / 128
+};
+
+__device__ __forceinline__ int64_t scale_word(const MatParams& p, int64_t r, int32_t group) {
+  return ((r >> 7) * p.groups + group) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+}
+
+template <typename T, bool kAligned>
+__global__ void __launch_bounds__(kThreads) k_mx_quantize(const T* __restrict__ x, uint8_t* __restrict__ qdata,
+                                                          uint8_t* __restrict__ scales, const MatParams p) {
+  __shared__ T slice[kAligned ? 1 : kWarps * kSlice];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int64_t u = int64_t(blockIdx.x) * kWarps + warp; u < p.units; u += int64_t(gridDim.x) * kWarps) {
+    const int64_t row = p.units <= 0x7FFFFFFF ? int64_t(uint32_t(u) / uint32_t(p.units_per_row)) : u / p.units_per_row;
+    const int32_t c0 = int32_t(u - row * p.units_per_row) * kUnit;
+    const int32_t cb = c0 + lane * 16;
+    const int32_t left = int32_t(p.cols) - cb;  // elements of this lane inside the row
+    const T* src = x + row * p.ld;
+    float f[16];
+    if constexpr (kAligned) {
+      if (left >= 16) {
+        load16(src + cb, f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = i < left ? to_f32(src[cb + i]) : 0.0f;
+      }
+    } else {
+      T* s = slice + warp * kSlice;
+      const int32_t n = int32_t(p.cols) - c0 < kUnit ? int32_t(p.cols) - c0 : kUnit;
+      T v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int32_t c = i * 32 + lane;
+        v[i] = c < n ? src[c0 + c] : from_f32<T>(0.0f);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int32_t c = i * 32 + lane;
+        s[c + c / 16] = v[i];
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) f[i] = to_f32(s[lane * 17 + i]);
+    }
+    uint32_t e;
+    const uint2 q = mx_encode_half(f, e);
+    const uint32_t e1 = __shfl_down_sync(0xFFFFFFFFu, e, 2), e2 = __shfl_down_sync(0xFFFFFFFFu, e, 4),
+                   e3 = __shfl_down_sync(0xFFFFFFFFu, e, 6);
+    if (cb < p.groups * 128) {
+      *reinterpret_cast<uint2*>(qdata + row * (int64_t(p.groups) * 64) + cb / 2) = q;
+      if ((lane & 7) == 0)
+        *reinterpret_cast<uint32_t*>(scales + scale_word(p, row, cb >> 7)) = e | e1 << 8 | e2 << 16 | e3 << 24;
+    }
+  }
+}
+
+template <typename T, bool kAligned>
+__global__ void __launch_bounds__(kThreads) k_mx_dequantize(const uint8_t* __restrict__ qdata,
+                                                            const uint8_t* __restrict__ scales, T* __restrict__ out,
+                                                            const MatParams p) {
+  __shared__ T slice[kAligned ? 1 : kWarps * kSlice];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int64_t u = int64_t(blockIdx.x) * kWarps + warp; u < p.units; u += int64_t(gridDim.x) * kWarps) {
+    const int64_t row = p.units <= 0x7FFFFFFF ? int64_t(uint32_t(u) / uint32_t(p.units_per_row)) : u / p.units_per_row;
+    const int32_t c0 = int32_t(u - row * p.units_per_row) * kUnit;
+    const int32_t cb = c0 + lane * 16;
+    const int32_t left = int32_t(p.cols) - cb;
+    T* dst = out + row * p.ld;
+    float f[16];
+    if (left > 0) {
+      const uint2 q = *reinterpret_cast<const uint2*>(qdata + row * (int64_t(p.groups) * 64) + cb / 2);
+      mx_decode16(q, scales[scale_word(p, row, cb >> 7) + ((cb >> 5) & 3)], f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) f[i] = 0.0f;
+    }
+    if constexpr (kAligned) {
+      if (left >= 16) {
+        store16(dst + cb, f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < left) dst[cb + i] = from_f32<T>(f[i]);
+      }
+    } else {
+      T* s = slice + warp * kSlice;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[lane * 17 + i] = from_f32<T>(f[i]);
+      __syncwarp();
+      const int32_t n = int32_t(p.cols) - c0 < kUnit ? int32_t(p.cols) - c0 : kUnit;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int32_t c = i * 32 + lane;
+        if (c < n) dst[c0 + c] = s[c + c / 16];
+      }
+    }
+  }
+}
+
+nvfp4_status mat_params(MatParams& p, int64_t rows, int64_t cols, int64_t ld, int32_t dtype, const std::string& nm) {
+  if (!mx_dtype_ok(dtype)) return fail(NVFP4_EINVAL, nm + ": unknown element type");
+  if (rows < 1 || cols < 1) return fail(NVFP4_EINVAL, nm + ": rows and cols must be positive");
+  if (ld < cols) return fail(NVFP4_EINVAL, nm + ": row stride smaller than a row");
+  if (cols > (int64_t(1) << 24) || rows > (int64_t(1) << 40) / mxfp4_padded_cols(cols))
+    return fail(NVFP4_EUNSUPPORTED, nm + ": matrix too large");
+  p.rows = rows, p.cols = cols, p.ld = ld;
+  p.groups = int32_t(mxfp4_padded_cols(cols) / 128);
+  p.units_per_row = (p.groups * 128 + kUnit - 1) / kUnit;
+  p.units = rows * p.units_per_row;
+  return NVFP4_OK;
+}
+
+int mat_grid(const MatParams& p) {
+  const int64_t blocks = (p.units + kWarps - 1) / kWarps, most = int64_t(sm_count()) * 8;
+  return int(blocks < most ? blocks : most);
+}
+
+bool vector_rows(const void* x, int64_t ld, int32_t dtype) {
+  return aligned16(x) && ld * mx_elem_bytes(dtype) % 16 == 0;
+}
+
+template <typename T>
+void quantize_launch(const void* x, void* q, void* s, const MatParams& p, bool vec, cudaStream_t stream) {
+  auto k = vec ? k_mx_quantize<T, true> : k_mx_quantize<T, false>;
+  k<<<mat_grid(p), kThreads, 0, stream>>>(static_cast<const T*>(x), static_cast<uint8_t*>(q), static_cast<uint8_t*>(s),
+                                          p);
+}
+template <typename T>
+void dequantize_launch(const void* q, const void* s, void* out, const MatParams& p, bool vec, cudaStream_t stream) {
+  auto k = vec ? k_mx_dequantize<T, true> : k_mx_dequantize<T, false>;
+  k<<<mat_grid(p), kThreads, 0, stream>>>(static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(s),
+                                          static_cast<T*>(out), p);
+}
+
+}  // namespace
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" int64_t mxfp4_padded_cols(int64_t cols) { return cols <= 0 ? 0 : (cols + 127) / 128 * 128; }
+
+extern "C" int64_t mxfp4_qdata_bytes(int64_t rows, int64_t cols) {
+  return rows <= 0 ? 0 : rows * (mxfp4_padded_cols(cols) / 2);
+}
+
+extern "C" int64_t mxfp4_scale_bytes(int64_t rows, int64_t cols) {
+  return nvfp4_padded_rows(rows) * (mxfp4_padded_cols(cols) / 32);
+}
+
+extern "C" int64_t mxfp4_scale_offset(int64_t r, int64_t c, int64_t cols) {
+  return ((r / 128) * (mxfp4_padded_cols(cols) / 128) + c / 4) * 512 + (r % 32) * 16 + ((r / 32) % 4) * 4 + (c % 4);
+}
+
+extern "C" nvfp4_status mxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                                       void* qdata, void* scales, nvfp4_stream_t stream) {
+  const std::string nm("mxfp4_quantize");
+  if (!x || !qdata || !scales) return fail(NVFP4_EINVAL, nm + ": null pointer");
+  MatParams p;
+  const nvfp4_status st = mat_params(p, rows, cols, ld, dtype, nm);
+  if (st != NVFP4_OK) return st;
+  if (!aligned16(qdata) || !aligned16(scales) || reinterpret_cast<uintptr_t>(x) % mx_elem_bytes(dtype) != 0)
+    return fail(NVFP4_EALIGN, nm + ": qdata and scales must be 16-byte aligned, x aligned to its element");
+  const bool vec = vector_rows(x, ld, dtype);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == MXFP4_BF16) quantize_launch<__nv_bfloat16>(x, qdata, scales, p, vec, s);
+  else if (dtype == MXFP4_FP16) quantize_launch<__half>(x, qdata, scales, p, vec, s);
+  else quantize_launch<float>(x, qdata, scales, p, vec, s);
+  return cuda_check(cudaGetLastError(), "launch k_mx_quantize");
+}
+
+extern "C" nvfp4_status mxfp4_dequantize(const void* qdata, const void* scales, int64_t rows, int64_t cols, void* out,
+                                         int32_t dtype, int64_t ld, nvfp4_stream_t stream) {
+  const std::string nm("mxfp4_dequantize");
+  if (!out || !qdata || !scales) return fail(NVFP4_EINVAL, nm + ": null pointer");
+  MatParams p;
+  const nvfp4_status st = mat_params(p, rows, cols, ld, dtype, nm);
+  if (st != NVFP4_OK) return st;
+  if (!aligned16(qdata) || !aligned16(scales) || reinterpret_cast<uintptr_t>(out) % mx_elem_bytes(dtype) != 0)
+    return fail(NVFP4_EALIGN, nm + ": qdata and scales must be 16-byte aligned, out aligned to its element");
+  const bool vec = vector_rows(out, ld, dtype);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == MXFP4_BF16) dequantize_launch<__nv_bfloat16>(qdata, scales, out, p, vec, s);
+  else if (dtype == MXFP4_FP16) dequantize_launch<__half>(qdata, scales, out, p, vec, s);
+  else dequantize_launch<float>(qdata, scales, out, p, vec, s);
+  return cuda_check(cudaGetLastError(), "launch k_mx_dequantize");
+}

@@ -1,0 +1,309 @@
+// MXFP4 product for few rows: out [m, n] = A [m, k] W [n, k]^T on tcgen05.
+//
+// With few rows the weight's bytes are the work (17/32 byte an element), so
+// the weight is the tensor core's M operand: a CTA takes 128 weight rows and
+// up to 128 activation rows (the MMA's N: 16, 32, 64 or 128), streams its
+// weight rows through a TMA ring and accumulates D[weight row][activation
+// row] in tensor memory with kind::mxf4 MMAs (block 32, E8M0 scales), which
+// read the 4-bit codes and the scales as stored: nothing is decoded.
+//
+//   warp 0      TMA producer: a k-tile of 256 elements is a 128-byte swizzled
+//               box of each operand and one 1 KB piece of each scale array
+//               (two 512-byte tiles of 128 rows x 4 scale columns)
+//   warp 1      MMA issuer: per k-tile four tcgen05.cp (the scale tiles into
+//               tensor memory) and four MMAs of K = 64
+//   warps 2-5   epilogue: a lane is one weight row, so stores run along n
+//
+// One weight tile per 128 rows fills few SMs (42 tiles at n = 5,376), so k is
+// split over the CTAs of a cluster: each leaves its float32 partial in its
+// shared memory and sums the columns it owns over the cluster in rank order.
+// The split depends on the shape alone, so results are reproducible.
+#include <algorithm>
+#include <string>
+
+#include "mx_gemm.cuh"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kWRows = 128;
+constexpr int kWBytes = kWRows * 128;  // one k-tile of the weight
+constexpr int kSfBytes = 1024;         // one k-tile of one scale array
+constexpr int kMaxSplit = 8;           // portable cluster size
+constexpr uint32_t kSfSlots = 2;       // scale columns alternate between two places
+constexpr uint32_t kSfCols = 16;       // of one k-tile: 2 x 4 columns for W, 2 x 4 for A
+
+template <int NT>
+struct Shape {
+  static constexpr int kABytes = NT * 128;
+  static constexpr int kStage = kWBytes + kABytes + 2 * kSfBytes;
+  // two CTAs an SM: 5 x 20, 5 x 22, 4 x 26 and 3 x 34 KB
+  static constexpr int kStages = NT <= 32 ? 5 : (NT == 64 ? 4 : 3);
+  static constexpr int kSmem = 1024 + kStages * kStage + 256;
+  static constexpr uint32_t kTmem = NT <= 32 ? 64u : (NT == 64 ? 128u : 256u);
+  static_assert(NT + kSfSlots * kSfCols <= kTmem, "tensor memory");
+  static_assert(NT * 512 <= kStages * kStage, "the partial sums reuse the ring");
+  static_assert(2 * (kSmem + 1024) <= 233472, "two CTAs an SM");
+};
+
+struct RowsParams {
+  const uint8_t* a_s;
+  const uint8_t* w_s;
+  void* out;
+  int64_t ldo;
+  int32_t m, n, dtype;
+  int32_t groups;   // 128-element groups of k
+  int32_t split;    // CTAs of the cluster along k
+  uint32_t* dev_status;
+  uint64_t wait_limit_cycles;
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d_plain(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t x,
+                                                  int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+
+// Scale tile (32 lanes x 16 bytes, unswizzled) into 4 tensor-memory columns of
+// all four lane quarters.
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint32_t saddr) {
+  const uint64_t desc = uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(128 >> 4) << 32) |
+                        (uint64_t(1) << 46);
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                            uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void store_out(const RowsParams& p, int64_t row, int32_t col, float v) {
+  const int64_t at = row * p.ldo + col;
+  if (p.dtype == MXFP4_BF16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+  else if (p.dtype == MXFP4_FP16) static_cast<__half*>(p.out)[at] = __float2half_rn(v);
+  else static_cast<float*>(p.out)[at] = v;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kThreads, 2)
+    k_mx_rows(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
+              const RowsParams p) {
+  using S = Shape<NT>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + S::kStages * S::kStage);
+  uint64_t* empty = full + S::kStages;
+  uint64_t* done = empty + S::kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = p.split > 1 ? int(cluster_ctarank()) : 0;
+  const int w_row = (int(blockIdx.x) / p.split) * kWRows;
+  const int a_row = int(blockIdx.y) * NT;
+  const int tiles = (p.groups + 1) / 2;
+  const int kt0 = int(int64_t(tiles) * rank / p.split), kt1 = int(int64_t(tiles) * (rank + 1) / p.split);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tmap(&tmap_a);
+    prefetch_tmap(&tmap_w);
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, S::kTmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0 && lane == 0) {
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int kt = kt0; kt < kt1; ++kt) {
+      if (!mbar_wait_bounded(&empty[slot], phase ^ 1u, p.wait_limit_cycles, const_cast<const int*>(abort_flag))) {
+        *abort_flag = 1;
+        break;
+      }
+      uint8_t* st = ring + slot * S::kStage;
+      // the last k-tile may hold one 128-element group only: the boxes are
+      // zero-filled past the operand, the scale pieces are half as long
+      const uint32_t sf = (2 * kt + 1 < p.groups) ? kSfBytes : kSfBytes / 2;
+      mbar_arrive_expect_tx(&full[slot], kWBytes + S::kABytes + 2 * sf);
+      tma_load_2d_plain(st, &tmap_w, &full[slot], kt * 128, w_row);
+      bulk_load(st + kWBytes + S::kABytes, p.w_s + (int64_t(w_row >> 7) * p.groups + 2 * kt) * 512, sf, &full[slot]);
+      tma_load_2d_plain(st + kWBytes, &tmap_a, &full[slot], kt * 128, a_row);
+      bulk_load(st + kWBytes + S::kABytes + kSfBytes, p.a_s + (int64_t(a_row >> 7) * p.groups + 2 * kt) * 512, sf,
+                &full[slot]);
+      if (++slot == S::kStages) slot = 0, phase ^= 1u;
+    }
+  } else if (warp == 1 && lane == 0) {
+    // M = 128 weight rows, N = NT activation rows, both E2M1 and K-major
+    constexpr uint32_t kIdesc =
+        (1u << 7) | (1u << 10) | (uint32_t(NT >> 3) << 17) | kIdescE8m0 | (uint32_t(kWRows >> 4) << 24);
+    int slot = 0;
+    uint32_t phase = 0, sf_slot = 0;
+    bool ok = true;
+    for (int kt = kt0; kt < kt1; ++kt) {
+      if (!mbar_wait_bounded(&full[slot], phase, p.wait_limit_cycles, const_cast<const int*>(abort_flag))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t st = smem_u32(ring + slot * S::kStage);
+      const uint32_t sfw = tmem + NT + sf_slot * kSfCols, sfa = sfw + 8;
+      const uint64_t dw = desc_k128(st), da = desc_k128(st + kWBytes);
+      const int ng = 2 * kt + 1 < p.groups ? 2 : 1;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        if (g >= ng) break;
+        tc_cp_scales(sfw + 4 * g, st + kWBytes + S::kABytes + 512 * g);
+        tc_cp_scales(sfa + 4 * g, st + kWBytes + S::kABytes + kSfBytes + 512 * g);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // K = 64 step: 32 bytes further along the row; its two scales are
+          // bytes 2h, 2h + 1 of the group's scale word
+          const uint32_t id = kIdesc | (uint32_t(2 * h) << 4) | (uint32_t(2 * h) << 29);
+          tc_mma_mxf4(tmem, dw + 4 * g + 2 * h, da + 4 * g + 2 * h, id, sfw + 4 * g, sfa + 4 * g,
+                      (kt > kt0 || g > 0 || h > 0) ? 1u : 0u);
+        }
+      }
+      tc_commit(&empty[slot]);
+      sf_slot ^= 1u;
+      if (++slot == S::kStages) slot = 0, phase ^= 1u;
+    }
+    if (!ok) *abort_flag = 1;
+    tc_commit(done);
+  }
+
+  // The accumulators: warps 2..5, lane quarter warp % 4.
+  const bool epi = warp >= 2;
+  const int q = warp & 3;
+  float* part = reinterpret_cast<float*>(ring);  // [NT][128], the ring is idle once `done` completes
+  if (epi) {
+    int ok = 1;
+    if (lane == 0) ok = mbar_wait_bounded(done, 0, p.wait_limit_cycles, nullptr);
+    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    if (lane == 0 && (!ok || *abort_flag) && p.dev_status != nullptr)
+      atomicExch(p.dev_status, static_cast<uint32_t>(NVFP4_ETIMEOUT));
+    tc_fence_after();
+    const int valid = min(NT, p.m - a_row);
+    const int col = w_row + q * 32 + lane;
+#pragma unroll 1
+    for (int c = 0; c < NT; c += 16) {
+      if (c >= valid) break;
+      uint32_t r[16];
+      tmem_ld_32x32b_x16(tmem + (uint32_t(q * 32) << 16) + c, r);
+      tc_wait_ld();
+      tmem_ld_fence_regs<16>(r);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (p.split == 1) {
+          if (c + i < valid && col < p.n) store_out(p, a_row + c + i, col, __uint_as_float(r[i]));
+        } else {
+          part[(c + i) * 128 + q * 32 + lane] = __uint_as_float(r[i]);
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  if (p.split > 1) {
+    cluster_sync();  // every CTA's partial is in its shared memory
+    if (epi) {
+      const int valid = min(NT, p.m - a_row);
+      const int col = w_row + q * 32 + lane;
+      const uint32_t mine = smem_u32(part) + uint32_t(q * 32 + lane) * 4u;
+      for (int c = rank; c < valid; c += p.split) {
+        float v = 0.0f;
+        for (int s = 0; s < p.split; ++s) v += ld_cluster_f32(mapa_shared(mine + uint32_t(c) * 512u, uint32_t(s)));
+        if (col < p.n) store_out(p, a_row + c, col, v);
+      }
+    }
+    cluster_sync();  // nobody leaves while its partial is read
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tmem, S::kTmem);
+  }
+}
+
+template <int NT>
+nvfp4_status rows_launch(const void* a_q, const void* w_q, int64_t m, int64_t n, int64_t k, RowsParams& p,
+                         cudaStream_t stream) {
+  using S = Shape<NT>;
+  CUtensorMap ta, tw;
+  nvfp4_status st = mx_operand_map(&ta, a_q, m, k, NT, "A");
+  if (st == NVFP4_OK) st = mx_operand_map(&tw, w_q, n, k, kWRows, "W");
+  if (st != NVFP4_OK) return st;
+  const int64_t w_tiles = (n + kWRows - 1) / kWRows, a_tiles = (m + NT - 1) / NT;
+  const int tiles = (p.groups + 1) / 2;
+  // fill two CTAs an SM, no CTA without a k-tile
+  int64_t split = 2 * int64_t(sm_count()) / (w_tiles * a_tiles);
+  split = std::max<int64_t>(1, std::min<int64_t>(split, std::min(tiles, kMaxSplit)));
+  p.split = int32_t(split);
+  st = cuda_check(cudaFuncSetAttribute(k_mx_rows<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem),
+                  "cudaFuncSetAttribute(k_mx_rows)");
+  if (st != NVFP4_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(w_tiles * split), unsigned(a_tiles));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, k_mx_rows<NT>, ta, tw, static_cast<const RowsParams>(p)),
+                    "launch k_mx_rows");
+}
+
+}  // namespace
+
+nvfp4_status mx_rows(const void* a_q, const void* a_s, const void* w_q, const void* w_s, int64_t m, int64_t n,
+                     int64_t k, void* out, int32_t dtype, int64_t ldo, uint32_t* dev_status, cudaStream_t stream) {
+  RowsParams p;
+  p.a_s = static_cast<const uint8_t*>(a_s);
+  p.w_s = static_cast<const uint8_t*>(w_s);
+  p.out = out;
+  p.ldo = ldo;
+  p.m = int32_t(m), p.n = int32_t(n), p.dtype = dtype;
+  p.groups = int32_t(mxfp4_padded_cols(k) / 128);
+  p.dev_status = dev_status;
+  p.wait_limit_cycles = kMxWaitLimitCycles;
+  if (m <= 16) return rows_launch<16>(a_q, w_q, m, n, k, p, stream);
+  if (m <= 32) return rows_launch<32>(a_q, w_q, m, n, k, p, stream);
+  if (m <= 64) return rows_launch<64>(a_q, w_q, m, n, k, p, stream);
+  return rows_launch<128>(a_q, w_q, m, n, k, p, stream);
+}
+
+}  // namespace nvfp4

@@ -14,21 +14,24 @@
 //             elements below that lose bits that weigh nothing).  Each 32-wide
 //             block of the head is one MMA pair whose FP32 result is
 //             multiplied by the key's block scale.
-//   softmax   running maximum and sum in FP32, weights p 2^14.
+//   softmax   running maximum and sum in FP32; weights p 2^14 rounded to FP16
+//             for the second MMA (11 bits; BF16 would keep 8).
 //   p v       a value's block scale varies along the contraction, so it goes
 //             onto the weights: p 2^14 2^(E - R) with R the largest E of the
 //             block column so far (a running maximum like the softmax's).  The
 //             factor 2^14 leaves 28 binades below the largest before FP16
 //             loses bits.
-//   split     kSplit: up to 8 rows, whose weights go in twice, FP16(p) in MMA
-//             rows 0..7 and FP16(p - FP16(p)) in rows 8..15, rows that would
-//             be idle: the weights then carry 22 bits.  Otherwise 16 rows and
-//             weights of 11 bits (FP16; BF16 would keep 8).
 //
+// The decoding cvt gives two neighbours (d, d + 1) of one token, while an MMA
+// contracts over pairs of tokens.  Up to 8 rows (kRows = 8, every decoding
+// step of 8 heads a kv head) need no transposition for that: the contraction
+// pair is (d, d + 1), MMA row g holds (p, 0) and row g + 8, idle otherwise,
+// (0, p), so that rows 0..7 collect the even and rows 8..15 the odd columns.
+// With 16 rows the halves are put together by PRMT, one for each register.
 // The ldmatrix layouts fit the format: a 16-byte row of an 8x8 matrix is one
 // block of one token, so for K a lane gets 8 codes of one block, and with
 // .trans for V it gets 4 codes of token t in its low and of token t + 1 in
-// its high half, the pairs that the second MMA contracts over.
+// its high half.
 //
 // Work is dealt in equal runs of tiles over all warps of the grid, whatever
 // the sequences' lengths: the tiles of all (sequence, row tile, kv head)
@@ -54,31 +57,35 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxSeqs = 1024;  // sequences of one launch (their tile counts sit in shared memory)
 
-template <int D>
+// kRows = 8 takes 32 keys of 128 at a time (64 of 64, 16 of 256) and 16 warps
+// an SM, which hides the latency of the MMA and softmax chains; 16 rows need
+// twice the registers and run with 8.
+template <int D, int kRows>
 struct Tile {
-  static constexpr int C = D / 32;                 // blocks of a row
-  static constexpr int kTok = D == 256 ? 32 : 64;  // keys of a tile
-  static constexpr int kCodes = kTok * D / 2;      // bytes of K (or V) codes
+  static constexpr int C = D / 32;  // blocks of a row
+  static constexpr int kTok = D == 64 ? 64 : 32;
+  static constexpr int kCodes = kTok * D / 2;  // bytes of K (or V) codes
   static constexpr int kScales = kTok * C;
+  static constexpr int kCtas = (kRows == 8 && D <= 128) ? 4 : 2;  // blocks an SM
   static constexpr int kStages = 3;
   static constexpr int kKf = kTok * C * 4;  // K scales as float [token][C]
-  static constexpr int kVf = kTok * C * 2;  // V factors as half [C][token]
+  static constexpr int kVf = kTok * C * (kRows == 8 ? 4 : 2);  // V factors [C][token]: (f, f), or f
   static constexpr int kWarpCodes = kStages * 2 * kCodes;
   static constexpr int kWarpRest = kStages * 2 * kScales + kKf + kVf;
   // [warp codes x 4][warp rest x 4][barriers]; the tile counts of the
   // sequences lie where the codes go, before the first load
   static constexpr int kBars = kWarps * kStages * 8;
-  static constexpr int kSmem = 1024 + kWarps * (kWarpCodes + kWarpRest) + kBars;
-  static_assert((kMaxSeqs + 1) * 8 <= kWarps * kWarpCodes, "tile counts");
+  static constexpr int kSmem = kWarps * (kWarpCodes + kWarpRest) + kBars;
+  static_assert((kMaxSeqs + 1 + kThreads) * 8 <= kWarps * kWarpCodes, "tile counts");
   static_assert(kCodes % 1024 == 0, "swizzle atoms");
+  static_assert(kCtas * (kSmem + 1024) <= 233472, "blocks an SM");
 };
 
 struct StreamParams {
   AttnParams a;
   int32_t workers;
-  int32_t rows;      // rows of a row tile: 8 (split) or 16
-  float* part_o;     // [2 * workers][rows][D]
-  float2* part_ml;   // [2 * workers][rows]  (maximum, sum)
+  float* part_o;     // [2 * workers][kRows][D]
+  float2* part_ml;   // [2 * workers][kRows]  (maximum, sum)
   int64_t* prefix;   // [seqs + 1] tiles before each sequence, written by block 0 for k_attn_combine
 };
 
@@ -186,6 +193,13 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same with a zero accumulator.
+__device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -198,12 +212,6 @@ template <int D>
 __device__ __forceinline__ uint32_t swz(int t, int c) {
   constexpr int C = D / 32;
   return uint32_t(t * (D / 2) + ((c ^ ((t / (8 / C)) & (C - 1))) << 4));
-}
-
-// FP16 2^(e - r) for e <= r (0 once it underflows).
-__device__ __forceinline__ uint32_t half_pow2(uint32_t e, uint32_t r) {
-  const uint32_t d = r - e;
-  return d <= 14u ? (15u - d) << 10 : (d <= 24u ? 1u << (24u - d) : 0u);
 }
 
 // Eight consecutive elements of a query row, to binary32.
@@ -238,22 +246,30 @@ __device__ __forceinline__ void store_o8(const AttnParams& a, uint16_t* dst, con
   }
 }
 
-template <int D, bool kSplit>
-__global__ void __launch_bounds__(kThreads, 2)
+// Scale word of a block in the high exponent bits: 2^(E-127) for 1 <= E <= 254,
+// 0 for E = 0 (a block below 2^-124 has no weight in a score), infinity for
+// 255, whose zero codes then give NaN.
+__device__ __forceinline__ float e8m0_byte(uint32_t w, int i) {
+  const uint32_t v = i == 0 ? w << 23 : (i == 1 ? w << 15 : (i == 2 ? w << 7 : w >> 1));
+  return __uint_as_float(v & 0x7F800000u);
+}
+
+template <int D, int kRows>
+__global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
     k_attn_stream(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                   const __grid_constant__ StreamParams sp) {
-  using T = Tile<D>;
-  constexpr int C = T::C, kTok = T::kTok, NT = kTok / 8, KK = kTok / 16;
-  constexpr int kRows = kSplit ? 8 : 16;
-  constexpr int R = kSplit ? 1 : 2;  // real rows of a thread: g, and g + 8
+  using T = Tile<D, kRows>;
+  constexpr int C = T::C, kTok = T::kTok, NT = kTok / 8;
+  constexpr int R = kRows / 8;   // rows of a thread: g, and g + 8
+  constexpr int Y = 2 * R;       // accumulators of a block: 8 rows hold two columns in each
+  constexpr int U = kTok / 32;   // keys of a lane in the scale work
   const AttnParams& a = sp.a;
-  extern __shared__ uint8_t raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t base[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
   uint8_t* codes = base + warp * T::kWarpCodes;
   uint8_t* rest = base + kWarps * T::kWarpCodes + warp * T::kWarpRest;
   float* kf = reinterpret_cast<float*>(rest + T::kStages * 2 * T::kScales);
-  uint16_t* vf = reinterpret_cast<uint16_t*>(rest + T::kStages * 2 * T::kScales + T::kKf);
+  uint8_t* vf = rest + T::kStages * 2 * T::kScales + T::kKf;
   uint8_t* tail = base + kWarps * (T::kWarpCodes + T::kWarpRest);
   uint64_t* full = reinterpret_cast<uint64_t*>(tail) + warp * T::kStages;
   int64_t* prefix = reinterpret_cast<int64_t*>(base);
@@ -267,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // tiles before each sequence: every thread sums a run of sequences, the
   // first warp scans the runs' sums
   {
-    __shared__ int64_t run[kThreads];
+    int64_t* run = prefix + kMaxSeqs + 1;
     const int per = (a.seqs + kThreads - 1) / kThreads;
     const int b0 = min(int(threadIdx.x) * per, a.seqs), b1 = min(b0 + per, a.seqs);
     int64_t sum = 0;
@@ -302,22 +318,31 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int b = threadIdx.x; b <= a.seqs; b += kThreads) sp.prefix[b] = prefix[b];
   }
 
+  // k_attn_combine may be set up from here on; it waits for this grid's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t total = prefix[a.seqs];
   // the first workers lie in different blocks: few tiles spread over all SMs
   const int32_t worker = warp * int32_t(gridDim.x) + int32_t(blockIdx.x);
   const int32_t workers = live_workers(total, sp.workers);
   const int64_t x0 = worker < workers ? worker_start(total, worker, workers) : 0;
   const int32_t tiles = worker < workers ? int32_t(worker_start(total, worker + 1, workers) - x0) : 0;
-  Cursor ld;
-  if (tiles > 0) cursor_at(ld, a, prefix, x0, kRows, kTok);
+  Cursor cu;
+  if (tiles > 0) cursor_at(cu, a, prefix, x0, kRows, kTok);
   fence_proxy_async_smem();  // the counts are read, the TMA may write there
   __syncthreads();
   if (tiles <= 0) return;
 
-  // ---- loads: lane i < boxes takes box i of a tile (a page's share of it)
-  const int32_t page = 1 << a.page_shift;
-  const int32_t box = min(page, kTok), boxes = kTok / box;
-  Cursor cu = ld;
+  // ---- loads: lane i < boxes takes box i of a tile (a page's share of it);
+  // its page is looked up when the tile before is issued
+  const int32_t box = min(1 << a.page_shift, kTok), boxes = kTok / box;
+  Cursor ld = cu;
+  int32_t page;
+  auto look_up = [&]() {
+    const int32_t tok = ld.s.tile(ld.t) * kTok + lane * box;
+    page = 0;
+    if (lane < boxes && tok < ld.len)
+      page = a.table[int64_t(ld.b) * a.table_ld + min(int64_t(tok >> a.page_shift), a.table_ld - 1)];
+  };
   auto issue = [&](int slot) {
     const int32_t tok0 = ld.s.tile(ld.t) * kTok;
     const int32_t nb = min(boxes, (ld.len - tok0 + box - 1) / box);  // boxes that hold a token
@@ -326,11 +351,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0) mbar_arrive_expect_tx(&full[slot], uint32_t(nb * box) * (D + 2 * C));
     __syncwarp();
     if (lane < nb) {
-      const int32_t tok = tok0 + lane * box;
-      const int32_t col = min(int64_t(tok >> a.page_shift), a.table_ld - 1);
-      int64_t pg = a.table[int64_t(ld.b) * a.table_ld + col];
-      pg = min(max(pg, int64_t(0)), a.pages - 1);
-      const int32_t z = int32_t(pg * a.kv_heads + ld.h), off = tok & (page - 1);
+      const int64_t pg = min(max(int64_t(page), int64_t(0)), a.pages - 1);
+      const int32_t z = int32_t(pg * a.kv_heads + ld.h), off = (tok0 + lane * box) & ((1 << a.page_shift) - 1);
       tma_load_3d_plain(st + lane * box * (D / 2), &tmap_k, &full[slot], 0, off, z);
       tma_load_3d_plain(st + T::kCodes + lane * box * (D / 2), &tmap_v, &full[slot], 0, off, z);
       const int64_t srow = ((int64_t(z) << a.page_shift) + off) * C;
@@ -343,18 +365,23 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   };
   int32_t issued = 0;
-  for (; issued < min(T::kStages, tiles); ++issued) {
+  look_up();
+#pragma unroll 1
+  while (issued < min(T::kStages, tiles)) {
     issue(issued);
-    if (issued + 1 < tiles) cursor_next(ld, a, kRows, kTok);
+    if (++issued < tiles) {
+      cursor_next(ld, a, kRows, kTok);
+      look_up();
+    }
   }
 
   // ---- state of the segment
-  uint32_t qa[C][2][2 * R];       // Q fragments: block, MMA of the block
-  float qf[R];                    // row factor of the scores (log2 domain)
-  int32_t pos[R];                 // position of the row's query
-  float o[C][4][4];               // block, column within the lane's four, MMA accumulator
+  uint32_t qa[C][2][2 * R];  // Q fragments: block, MMA of the block
+  float qf[R];               // row factor of the scores (log2 domain)
+  int32_t pos[R];            // position of the row's query
+  float o[C][Y][4];          // block, MMA of the block, accumulator
   float m[R], l[R];
-  uint32_t rmax[C];               // R of the block columns
+  int32_t rmax[C];           // R of the block columns
   auto begin_segment = [&]() {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -363,32 +390,36 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int32_t qi = real ? row / a.group : 0, hq = cu.h * a.group + (real ? row - qi * a.group : 0);
       pos[r] = cu.len - cu.nq + qi;
       const uint16_t* src = static_cast<const uint16_t*>(a.q) + int64_t(cu.q0 + qi) * a.q_st + int64_t(hq) * a.q_sh;
-      float f[C][8];
       float am = 0.0f;
 #pragma unroll
-      for (int j = 0; j < C; ++j) {
-        if (real) load_q8(a, src + 32 * j + 8 * tig, f[j]);
-        else
+      for (int pass = 0; pass < 2; ++pass) {  // the row's largest element, then its fragments
+        float mul = 1.0f;
+        if (pass == 1) {
+          am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+          am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+          // the row's largest element goes to [2^13, 2^14); rows of zeros, and
+          // rows with an infinity or a NaN, are taken as they are
+          const int32_t eb = int32_t(__float_as_uint(am) >> 23) & 0xFF;
+          const int32_t up = (eb == 0 || eb == 255) ? 0 : min(126, 140 - eb);
+          mul = pow2i(up);
+          qf[r] = a.scale_log2 * pow2i(-up);
+        }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[j][i] = 0.0f;
+        for (int j = 0; j < C; ++j) {
+          float f[8] = {};
+          if (real) load_q8(a, src + 32 * j + 8 * tig, f);
+          if (pass == 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) am = max_nan(am, fabsf(f[j][i]));
+            for (int i = 0; i < 8; ++i) am = max_nan(am, fabsf(f[i]));
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+                qa[j][h][u * R + r] = f32_to_word<__half>(f[4 * h + 2 * u] * mul, f[4 * h + 2 * u + 1] * mul);
+          }
+        }
       }
-      am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-      am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-      // the row's largest element goes to [2^13, 2^14); rows of zeros, and
-      // rows with an infinity or a NaN, are taken as they are
-      const int32_t eb = int32_t(__float_as_uint(am) >> 23) & 0xFF;
-      const int32_t up = (eb == 0 || eb == 255) ? 0 : min(126, 140 - eb);
-      const float mul = pow2i(up);
-      qf[r] = a.scale_log2 * pow2i(-up);
-#pragma unroll
-      for (int j = 0; j < C; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            qa[j][h][u * R + r] = f32_to_word<__half>(f[j][4 * h + 2 * u] * mul, f[j][4 * h + 2 * u + 1] * mul);
       m[r] = -INFINITY;
       l[r] = 0.0f;
     }
@@ -396,9 +427,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int j = 0; j < C; ++j) {
       rmax[j] = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int y = 0; y < Y; ++y)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][i][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) o[j][y][e] = 0.0f;
     }
   };
   auto end_segment = [&](bool whole, int slot) {
@@ -413,17 +444,14 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int j = 0; j < C; ++j) {
         // the accumulators hold p 2^14 v 2^(127 - R), the sum p 2^14
-        const float s = pow2i(int32_t(rmax[j]) - 127) * (whole ? inv : 1.0f);
-        float f[8];
+        const float s = pow2i(rmax[j] - 127) * (whole ? inv : 1.0f);
+        float f[8];  // columns 32 j + 8 tig + 0 .. 7
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if constexpr (kSplit) {
-            f[i] = (o[j][i][0] + o[j][i][2]) * s;
-            f[4 + i] = (o[j][i][1] + o[j][i][3]) * s;
-          } else {
-            f[i] = o[j][i][2 * r] * s;
-            f[4 + i] = o[j][i][2 * r + 1] * s;
-          }
+          // column n = 2 tig (or 2 tig + 1) of an MMA is code group n of the
+          // block: columns 4 n .. 4 n + 3
+          f[i] = (kRows == 8 ? o[j][i >> 1][2 * (i & 1)] : o[j][i % Y][2 * r]) * s;
+          f[4 + i] = (kRows == 8 ? o[j][i >> 1][2 * (i & 1) + 1] : o[j][i % Y][2 * r + 1]) * s;
         }
         if (whole) {
           if (row < head_rows)
@@ -449,23 +477,22 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   };
 
-  bool timed_out = false;
   bool from_start = cu.t == 0;  // the segment's first tile is ours
   int part_slot = 0;            // workspace slot of a partial: 0 for the run's first segment, 1 for a later one
-  begin_segment();
+  bool fresh = true;
   int slot = 0;
   uint32_t phase = 0;
+#pragma unroll 1
   for (int32_t n = 0; n < tiles; ++n) {
-    if (!timed_out) {
+    if (fresh) begin_segment();
+    {
       int ok = 1;
       if (lane == 0) ok = mbar_wait_bounded(&full[slot], phase, a.wait_limit_cycles, nullptr);
       if (__shfl_sync(0xFFFFFFFFu, ok, 0) == 0) {
-        timed_out = true;
         if (lane == 0 && a.dev_status != nullptr) atomicExch(a.dev_status, static_cast<uint32_t>(NVFP4_ETIMEOUT));
+        return;
       }
     }
-    __syncwarp();
-    if (timed_out) break;
     const uint32_t kc = smem_u32(codes + slot * 2 * T::kCodes), vc = kc + T::kCodes;
     const uint8_t* ks = rest + slot * 2 * T::kScales;
     const uint8_t* vs = ks + T::kScales;
@@ -473,53 +500,67 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int32_t lim = cu.s.hi - tok0;  // keys of the tile that some row may see: those below
 
     // scales: K as floats; V as FP16 factors against the running maximum
-    bool nan_scale = false, new_max = false;
+    uint32_t nan_keys[U][C] = {};  // keys whose block holds NaN (E = 255)
+    bool nan_scale = false, rescale = false;
     float vbeta[C];
     {
-      uint32_t ve[kTok / 32][C];
+      uint32_t kw[U][(C + 3) / 4], vw[U][(C + 3) / 4];
 #pragma unroll
-      for (int u = 0; u < kTok / 32; ++u) {
+      for (int u = 0; u < U; ++u) {
         const int t = lane + 32 * u;
         if constexpr (C == 2) {
-          const uint16_t w = *reinterpret_cast<const uint16_t*>(ks + t * 2);
-          *reinterpret_cast<float2*>(kf + t * 2) = make_float2(e8m0_value(w & 0xFF), e8m0_value(w >> 8));
-          const uint16_t x = *reinterpret_cast<const uint16_t*>(vs + t * 2);
-          ve[u][0] = x & 0xFF, ve[u][1] = x >> 8;
+          kw[u][0] = *reinterpret_cast<const uint16_t*>(ks + t * 2);
+          vw[u][0] = *reinterpret_cast<const uint16_t*>(vs + t * 2);
+          *reinterpret_cast<float2*>(kf + t * 2) = make_float2(e8m0_byte(kw[u][0], 0), e8m0_byte(kw[u][0], 1));
         } else {
 #pragma unroll
           for (int h = 0; h < C / 4; ++h) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(ks + t * C + 4 * h);
+            kw[u][h] = *reinterpret_cast<const uint32_t*>(ks + t * C + 4 * h);
+            vw[u][h] = *reinterpret_cast<const uint32_t*>(vs + t * C + 4 * h);
             *reinterpret_cast<float4*>(kf + t * C + 4 * h) =
-                make_float4(e8m0_value(w & 0xFF), e8m0_value((w >> 8) & 0xFF), e8m0_value((w >> 16) & 0xFF),
-                            e8m0_value(w >> 24));
-            const uint32_t x = *reinterpret_cast<const uint32_t*>(vs + t * C + 4 * h);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ve[u][4 * h + i] = (x >> (8 * i)) & 0xFF;
+                make_float4(e8m0_byte(kw[u][h], 0), e8m0_byte(kw[u][h], 1), e8m0_byte(kw[u][h], 2),
+                            e8m0_byte(kw[u][h], 3));
           }
         }
       }
+      int32_t e[U][C];  // -400: a key that no row sees, whose bytes may be anything: its factor is 0
+      bool up = false;
 #pragma unroll
-      for (int j = 0; j < C; ++j) {
-        uint32_t mx = 0;
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int u = 0; u < kTok / 32; ++u) {
-          const bool in = lane + 32 * u < lim;
-          if (in && ve[u][j] == 255u) nan_scale = true;
-          if (in && ve[u][j] != 255u) mx = max(mx, ve[u][j]);
+        for (int j = 0; j < C; ++j) {
+          e[u][j] = lane + 32 * u < lim ? int32_t((vw[u][j / 4] >> (8 * (j % 4))) & 0xFF) : -400;
+          up = up || e[u][j] > rmax[j];
         }
-        mx = max(__reduce_max_sync(0xFFFFFFFFu, mx), rmax[j]);
-        vbeta[j] = pow2i(int32_t(rmax[j]) - int32_t(mx));
-        new_max = new_max || mx != rmax[j];
-        rmax[j] = mx;
 #pragma unroll
-        for (int u = 0; u < kTok / 32; ++u) {
-          const int t = lane + 32 * u;
-          // keys that no row sees may hold any byte: factor 0
-          vf[j * kTok + t] =
-              uint16_t(t >= lim ? 0u : (ve[u][j] == 255u ? 0x7FFFu : half_pow2(ve[u][j], mx)));
+      for (int j = 0; j < C; ++j) vbeta[j] = 1.0f;
+      if (__any_sync(0xFFFFFFFFu, up)) {
+        rescale = true;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          int32_t mx = 0;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            nan_keys[u][j] = __ballot_sync(0xFFFFFFFFu, e[u][j] == 255);
+            nan_scale = nan_scale || nan_keys[u][j] != 0;
+            if (e[u][j] == 255) e[u][j] = -400;
+            mx = max(mx, e[u][j]);
+          }
+          mx = max(__reduce_max_sync(0xFFFFFFFFu, mx), rmax[j]);
+          vbeta[j] = pow2i(rmax[j] - mx);
+          rmax[j] = mx;
         }
       }
-      nan_scale = __any_sync(0xFFFFFFFFu, nan_scale);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          // 2^(E - R) through binary32, rounded (to a subnormal, to zero) by the conversion
+          const float f = __uint_as_float(uint32_t(max(e[u][j] - rmax[j] + 127, 0)) << 23);
+          const uint32_t w = f32_to_word<__half>(f, f);
+          if constexpr (kRows == 8) reinterpret_cast<uint32_t*>(vf)[j * kTok + lane + 32 * u] = w;
+          else reinterpret_cast<uint16_t*>(vf)[j * kTok + lane + 32 * u] = uint16_t(w);
+        }
       __syncwarp();
     }
 
@@ -533,11 +574,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int gi = 0; gi < NT * C / 4; ++gi) {
       uint32_t w[4];
       {
-        const int idx = gi * 4 + (lane >> 3);  // matrix (key tile, block) of this lane's row address
-        const int t = idx / C * 8 + (lane & 7), c = idx % C;
-        ldsm_x4(kc + swz<D>(t, c), w);
+        const int idx = gi * 4 + (lane >> 3);  // matrix (key group, block) of this lane's row address
+        ldsm_x4(kc + swz<D>(idx / C * 8 + (lane & 7), idx % C), w);
       }
-      // block scales of this lane's two keys of each key tile of the four matrices
+      // block scales of this lane's two keys of each key group of the four matrices
       constexpr int kV = C < 4 ? C : 4;
       float fk[4 / kV][2][kV];
 #pragma unroll
@@ -560,13 +600,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int idx = gi * 4 + x, nt = idx / C, j = idx % C;
         uint32_t h[4];
         e2m1x8_to_half(w[x], h);
-        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if constexpr (kSplit) {
-          mma_f16(c, qa[j][0][0], 0u, qa[j][0][1], 0u, h[0], h[1]);
+        float c[4];
+        if constexpr (kRows == 8) {
+          mma_f16_zero(c, qa[j][0][0], 0u, qa[j][0][1], 0u, h[0], h[1]);
           mma_f16(c, qa[j][1][0], 0u, qa[j][1][1], 0u, h[2], h[3]);
         } else {
-          mma_f16(c, qa[j][0][0], qa[j][0][1], qa[j][0][2], qa[j][0][3], h[0], h[1]);
-          mma_f16(c, qa[j][1][0], qa[j][1][1], qa[j][1][2], qa[j][1][3], h[2], h[3]);
+          mma_f16_zero(c, qa[j][0][0], qa[j][0][1], qa[j][0][2 % (2 * R)], qa[j][0][3 % (2 * R)], h[0], h[1]);
+          mma_f16(c, qa[j][1][0], qa[j][1][1], qa[j][1][2 % (2 * R)], qa[j][1][3 % (2 * R)], h[2], h[3]);
         }
         const float f0 = fk[x / kV][0][x % kV], f1 = fk[x / kV][1][x % kV];
 #pragma unroll
@@ -579,95 +619,130 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     // mask, running maximum, weights
     float alpha[R];
-    uint32_t ph[NT][R], pl[NT];  // weights in FP16: high parts, and the split's low parts
+    // 8 rows: words (p, 0) of the lane's two keys; 16 rows: pairs of the two keys
+    uint32_t pw[NT][2];
+    bool all = true;  // do the rows see the whole tile?
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      // is the whole tile seen by this row?
-      const bool all = tok0 + kTok <= cu.len && (!a.causal || tok0 + kTok - 1 <= pos[r]) &&
-                       (a.window <= 0 || tok0 > pos[r] - a.window || tok0 + kTok <= a.sinks);
-      float mx = -INFINITY;
+      all = all && tok0 + kTok <= cu.len && (!a.causal || tok0 + kTok - 1 <= pos[r]) &&
+            (a.window <= 0 || tok0 > pos[r] - a.window || tok0 + kTok <= a.sinks);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float v = s[nt][2 * r + e] * qf[r];
-          if (!all) {
+        for (int e = 0; e < 2; ++e) s[nt][2 * r + e] *= qf[r];
+    }
+    if (!__all_sync(0xFFFFFFFFu, all)) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
             const int32_t j = tok0 + nt * 8 + 2 * tig + e;
-            if (j >= cu.len || !sees(a, pos[r], j)) v = -INFINITY;
+            if (j >= cu.len || !sees(a, pos[r], j)) s[nt][2 * r + e] = -INFINITY;
           }
-          s[nt][2 * r + e] = v;
-          mx = fmaxf(mx, v);
-        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float mx = m[r];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(s[nt][2 * r], s[nt][2 * r + 1]));
       mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-      const float mn = fmaxf(m[r], mx);
-      const float ms = mn == -INFINITY ? 0.0f : mn;  // no key seen yet: every weight is 2^-inf = 0
+      const float ms = mx == -INFINITY ? 0.0f : mx;  // no key seen yet: every weight is 2^-inf = 0
       alpha[r] = exp2_approx(m[r] - ms);
-      m[r] = mn;
+      rescale = rescale || alpha[r] != 1.0f;
+      m[r] = mx;
       float sum = 0.0f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float p0 = exp2_approx(s[nt][2 * r] - ms + 14.0f), p1 = exp2_approx(s[nt][2 * r + 1] - ms + 14.0f);
+        const float p0 = exp2_approx(s[nt][2 * r] - (ms - 14.0f)), p1 = exp2_approx(s[nt][2 * r + 1] - (ms - 14.0f));
         sum += p0 + p1;
-        ph[nt][r] = f32_to_word<__half>(p0, p1);
-        if constexpr (kSplit) {
-          const float2 h = word_to_f32<__half>(ph[nt][r]);
-          pl[nt] = f32_to_word<__half>(p0 - h.x, p1 - h.y);
+        if constexpr (kRows == 8) {
+          pw[nt][0] = f32_to_word<__half>(p0, 0.0f);
+          pw[nt][1] = f32_to_word<__half>(p1, 0.0f);
+        } else {
+          pw[nt][r] = f32_to_word<__half>(p0, p1);
         }
       }
       l[r] = l[r] * alpha[r] + sum;
     }
-    bool scaled = new_max;
-#pragma unroll
-    for (int r = 0; r < R; ++r) scaled = scaled || alpha[r] != 1.0f;
-    if (__any_sync(0xFFFFFFFFu, scaled)) {
+    if (__any_sync(0xFFFFFFFFu, rescale)) {
 #pragma unroll
       for (int j = 0; j < C; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int y = 0; y < Y; ++y)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[j][i][e] *= vbeta[j] * alpha[kSplit ? 0 : e >> 1];
+          for (int e = 0; e < 4; ++e) o[j][y][e] *= vbeta[j] * alpha[kRows == 8 ? 0 : (e >> 1) % R];
+    }
+
+    // a block of NaN reaches the rows that see its key, and only those
+    if (nan_scale) {
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        bool hit[R] = {};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const bool bad = (nan_keys[nt / 4][j] >> ((nt % 4) * 8 + 2 * tig + e)) & 1u;
+            if constexpr (kRows == 8) {
+              hit[0] = hit[0] || (bad && pw[nt][e] != 0);
+            } else {
+#pragma unroll
+              for (int r = 0; r < R; ++r) hit[r] = hit[r] || (bad && (pw[nt][r] & (e ? 0xFFFF0000u : 0xFFFFu)) != 0);
+            }
+          }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const uint32_t row_hits = __ballot_sync(0xFFFFFFFFu, hit[r]) >> (lane & ~3) & 0xFu;
+          if (row_hits != 0) {
+#pragma unroll
+            for (int y = 0; y < Y; ++y)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (kRows == 8 || (e >> 1) == r) o[j][y][e] = __uint_as_float(0x7FFFFFFFu);
+          }
+        }
+      }
     }
 
     // output
 #pragma unroll
     for (int j = 0; j < C; ++j) {
 #pragma unroll
-      for (int k2 = 0; k2 < KK / 2; ++k2) {
+      for (int n4 = 0; n4 < NT / 4; ++n4) {
         uint32_t w[4];
-        // four groups of eight keys, block j
-        ldsm_x4_t(vc + swz<D>(k2 * 32 + lane, j), w);
-#pragma unroll
-        for (int k1 = 0; k1 < 2; ++k1) {
-          const int kk = k2 * 2 + k1;
-          const uint32_t fa = *reinterpret_cast<const uint32_t*>(vf + j * kTok + kk * 16 + 2 * tig);
-          const uint32_t fb = *reinterpret_cast<const uint32_t*>(vf + j * kTok + kk * 16 + 8 + 2 * tig);
-          uint32_t a0, a1, a2, a3;
-          if constexpr (kSplit) {
-            a0 = hmul2(ph[2 * kk][0], fa), a1 = hmul2(pl[2 * kk], fa);
-            a2 = hmul2(ph[2 * kk + 1][0], fb), a3 = hmul2(pl[2 * kk + 1], fb);
-          } else {
-            a0 = hmul2(ph[2 * kk][0], fa), a1 = hmul2(ph[2 * kk][R - 1], fa);
-            a2 = hmul2(ph[2 * kk + 1][0], fb), a3 = hmul2(ph[2 * kk + 1][R - 1], fb);
-          }
-          if (nan_scale) {
-            // a NaN factor (E = 255) reaches only rows that see its key: a
-            // zero weight stays zero
-            auto keep0 = [](uint32_t v, uint32_t w2) {
-              return ((w2 & 0x7FFFu) ? v & 0xFFFFu : 0u) | ((w2 & 0x7FFF0000u) ? v & 0xFFFF0000u : 0u);
-            };
-            a0 = keep0(a0, ph[2 * kk][0]), a2 = keep0(a2, ph[2 * kk + 1][0]);
-            a1 = keep0(a1, kSplit ? pl[2 * kk] : ph[2 * kk][R - 1]);
-            a3 = keep0(a3, kSplit ? pl[2 * kk + 1] : ph[2 * kk + 1][R - 1]);
-          }
-          uint32_t x[4], y[4];
-          e2m1x8_to_half(w[2 * k1], x);      // (t, d0 d1) (t, d2 d3) (t+1, d0 d1) (t+1, d2 d3)
-          e2m1x8_to_half(w[2 * k1 + 1], y);  // the same eight keys on
+        ldsm_x4_t(vc + swz<D>(n4 * 32 + lane, j), w);  // four groups of eight keys, block j
+        if constexpr (kRows == 8) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t sel = (i & 1) ? 0x7632u : 0x5410u;
-            mma_f16(o[j][i], a0, a1, a2, a3, __byte_perm(x[i >> 1], x[2 + (i >> 1)], sel),
-                    __byte_perm(y[i >> 1], y[2 + (i >> 1)], sel));
+            const int nt = n4 * 4 + i;
+            const uint2 f = *reinterpret_cast<const uint2*>(vf + 4 * (j * kTok + nt * 8 + 2 * tig));
+            const uint32_t a0 = hmul2(pw[nt][0], f.x), a1 = hmul2(pw[nt][0] << 16, f.x);
+            const uint32_t a2 = hmul2(pw[nt][1], f.y), a3 = hmul2(pw[nt][1] << 16, f.y);
+            uint32_t x[4];
+            e2m1x8_to_half(w[i], x);  // (t, d0 d1) (t, d2 d3) (t+1, d0 d1) (t+1, d2 d3)
+            mma_f16(o[j][0], a0, a1, a2, a3, x[0], x[2]);
+            mma_f16(o[j][1], a0, a1, a2, a3, x[1], x[3]);
+          }
+        } else {
+#pragma unroll
+          for (int k1 = 0; k1 < 2; ++k1) {
+            const int nt = n4 * 4 + 2 * k1;
+            const uint32_t fa = *reinterpret_cast<const uint32_t*>(vf + 2 * (j * kTok + nt * 8 + 2 * tig));
+            const uint32_t fb = *reinterpret_cast<const uint32_t*>(vf + 2 * (j * kTok + nt * 8 + 8 + 2 * tig));
+            const uint32_t a0 = hmul2(pw[nt][0], fa), a1 = hmul2(pw[nt][1], fa);
+            const uint32_t a2 = hmul2(pw[nt + 1][0], fb), a3 = hmul2(pw[nt + 1][1], fb);
+            uint32_t x[4], y[4];
+            e2m1x8_to_half(w[2 * k1], x);
+            e2m1x8_to_half(w[2 * k1 + 1], y);  // the same eight keys on
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t sel = (i & 1) ? 0x7632u : 0x5410u;
+              mma_f16(o[j][i % Y], a0, a1, a2, a3, __byte_perm(x[i >> 1], x[2 + (i >> 1)], sel),
+                      __byte_perm(y[i >> 1], y[2 + (i >> 1)], sel));
+            }
           }
         }
       }
@@ -678,106 +753,172 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
     if (issued < tiles) {
       issue(slot);
-      if (++issued < tiles) cursor_next(ld, a, kRows, kTok);
+      if (++issued < tiles) {
+        cursor_next(ld, a, kRows, kTok);
+        look_up();
+      }
     }
     if (++slot == T::kStages) slot = 0, phase ^= 1u;
 
-    const bool seg_end = cu.t + 1 == cu.s.n;
-    if (seg_end || n + 1 == tiles) end_segment(from_start && seg_end, part_slot);
+    fresh = cu.t + 1 == cu.s.n;
+    if (fresh || n + 1 == tiles) end_segment(from_start && fresh, part_slot);
     if (n + 1 < tiles) {
       cursor_next(cu, a, kRows, kTok);
-      if (seg_end) {
-        from_start = true;
-        part_slot = 1;
-        begin_segment();
-      }
+      if (fresh) from_start = true, part_slot = 1;
     }
   }
 }
 
 // Joins the partials of the segments that more than one worker had, and
-// writes the rows that see no key at all.
-template <int D>
-__global__ void __launch_bounds__(128) k_attn_combine(const __grid_constant__ StreamParams sp) {
+// writes the rows that see no key at all.  One block a segment: the rows'
+// weights of all partials first (a thread each), then the outputs, eight
+// columns a thread with the partials dealt over kSlices threads.
+constexpr int kCombineThreads = 256;
+constexpr int kMostParts = 512;  // partials whose weights are held at a time
+
+template <int D, int kRows>
+__global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_constant__ StreamParams sp) {
   const AttnParams& a = sp.a;
-  constexpr int kTok = Tile<D>::kTok;
+  constexpr int kTok = Tile<D, kRows>::kTok;
+  constexpr int kItems = kRows * D / 8;
+  constexpr int kSlices = kItems < kCombineThreads ? kCombineThreads / kItems : 1;
+  constexpr int kPass = kItems < kCombineThreads ? kItems : kCombineThreads;
+  __shared__ float weight[kMostParts / 8][kRows];
+  __shared__ float red_m[kCombineThreads / 32][kRows], row_m[kRows], row_l[kRows];
+  __shared__ float4 sum[kSlices > 1 ? (kSlices - 1) * kPass * 2 : 1];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are written
   const int32_t h = blockIdx.x, rt = blockIdx.y, b = blockIdx.z;
-  const int32_t rows = sp.rows;
   const int32_t len = a.lens[b], nq = seq_queries(a, b);
   const int32_t q0 = a.q_starts != nullptr ? a.q_starts[b] : b;
-  const int32_t live = min(rows, nq * a.group - rt * rows);
+  const int32_t live = min(kRows, nq * a.group - rt * kRows);
   if (live <= 0) return;
   int64_t first = sp.prefix[b];
-  for (int32_t r = 0; r < rt; ++r) first += int64_t(row_span(a, len, nq, r, rows, kTok).n) * a.kv_heads;
-  const int32_t n = row_span(a, len, nq, rt, rows, kTok).n;
+  for (int32_t r = 0; r < rt; ++r) first += int64_t(row_span(a, len, nq, r, kRows, kTok).n) * a.kv_heads;
+  const int32_t n = row_span(a, len, nq, rt, kRows, kTok).n;
   first += int64_t(h) * n;
   const int64_t total = sp.prefix[a.seqs];
   const int32_t workers = live_workers(total, sp.workers);
-  int32_t w0 = 0, w1 = -1, slot0 = 0;
+  int32_t w0 = 0, parts = 0, slot0 = 0;
   if (n > 0) {
-    w0 = worker_of(total, first, workers), w1 = worker_of(total, first + n - 1, workers);
-    if (w0 == w1) return;  // written by its worker
+    w0 = worker_of(total, first, workers);
+    parts = worker_of(total, first + n - 1, workers) - w0 + 1;
+    if (parts == 1) return;  // written by its worker
     slot0 = worker_start(total, w0, workers) == first ? 0 : 1;
   }
-  for (int32_t i = threadIdx.x; i < live * (D / 8); i += blockDim.x) {
-    const int32_t r = i / (D / 8), d = (i - r * (D / 8)) * 8;
-    float m = -INFINITY, l = 0.0f;
-    float f[8] = {};
-    for (int32_t w = w0; w <= w1; ++w) {
-      const float2 ml = sp.part_ml[(int64_t(w) * 2 + (w == w0 ? slot0 : 0)) * rows + r];
-      if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // this worker's tiles hold no key of the row
-      const float mn = fmaxf(m, ml.x);
-      const float ms = mn == -INFINITY ? 0.0f : mn;
-      const float ca = exp2_approx(m - ms), cb = exp2_approx(ml.x - ms);
-      const float4* src =
-          reinterpret_cast<const float4*>(sp.part_o + ((int64_t(w) * 2 + (w == w0 ? slot0 : 0)) * rows + r) * D + d);
-      const float4 u = src[0], v = src[1];
-      const float in[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+  auto slot_of = [&](int32_t i) { return int64_t(w0 + i) * 2 + (i == 0 ? slot0 : 0); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the rows' maxima over all partials: kRows threads a partial
+  {
+    const int r = threadIdx.x % kRows;
+    float m = -INFINITY;
+    for (int32_t i = threadIdx.x / kRows; i < parts; i += kCombineThreads / kRows)
+      m = fmaxf(m, sp.part_ml[slot_of(i) * kRows + r].x);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = f[k] * ca + in[k] * cb;
-      l = l * ca + ml.y * cb;
-      m = mn;
+    for (int o = kRows; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    if (lane < kRows) red_m[warp][lane] = m;
+    __syncthreads();
+    if (threadIdx.x < kRows) {
+      m = red_m[0][threadIdx.x];
+#pragma unroll
+      for (int i = 1; i < kCombineThreads / 32; ++i) m = fmaxf(m, red_m[i][threadIdx.x]);
+      row_m[threadIdx.x] = m;
     }
-    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+    __syncthreads();
+  }
+  const int item = threadIdx.x % kPass, slice = threadIdx.x / kPass;
+  float lsum = 0.0f;  // of row threadIdx.x, in partial order (first kRows threads)
+  for (int32_t pass = 0; pass < kItems; pass += kPass) {
+    const int32_t r = (pass + item) / (D / 8), d = (pass + item) % (D / 8) * 8;
+    float f[8] = {};
+    for (int32_t i0 = 0; i0 < parts; i0 += kMostParts / 8) {
+      const int32_t cnt = min(parts - i0, kMostParts / 8);
+      for (int32_t i = threadIdx.x; i < cnt * kRows; i += kCombineThreads) {
+        const float m = row_m[i % kRows], pm = sp.part_ml[slot_of(i0 + i / kRows) * kRows + i % kRows].x;
+        weight[i / kRows][i % kRows] = exp2_approx(pm - (m == -INFINITY ? 0.0f : m));
+      }
+      __syncthreads();
+      if (pass == 0 && threadIdx.x < kRows)
+        for (int32_t i = 0; i < cnt; ++i)
+          lsum += sp.part_ml[slot_of(i0 + i) * kRows + threadIdx.x].y * weight[i][threadIdx.x];
+#pragma unroll 4
+      for (int32_t i = slice; i < cnt; i += kSlices) {
+        const float4* src = reinterpret_cast<const float4*>(sp.part_o + (slot_of(i0 + i) * kRows + r) * D + d);
+        const float4 u = src[0], v = src[1];
+        const float c = weight[i][r];
+        f[0] += u.x * c, f[1] += u.y * c, f[2] += u.z * c, f[3] += u.w * c;
+        f[4] += v.x * c, f[5] += v.y * c, f[6] += v.z * c, f[7] += v.w * c;
+      }
+      __syncthreads();
+    }
+    if (pass == 0 && threadIdx.x < kRows) row_l[threadIdx.x] = lsum;
+    if (kSlices > 1 && slice > 0) {
+      sum[((slice - 1) * kPass + item) * 2] = make_float4(f[0], f[1], f[2], f[3]);
+      sum[((slice - 1) * kPass + item) * 2 + 1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    __syncthreads();
+    if (slice == 0 && r < live) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] *= inv;
-    const int32_t row = rt * rows + r, qi = row / a.group, hq = h * a.group + row - qi * a.group;
-    store_o8(a, static_cast<uint16_t*>(a.out) + int64_t(q0 + qi) * a.o_st + int64_t(hq) * a.o_sh + d, f);
-    if (d == 0 && a.lse != nullptr)
-      a.lse[int64_t(q0 + qi) * (a.kv_heads * a.group) + hq] =
-          l == 0.0f ? -INFINITY : (m - 14.0f + log2f(l)) * 0.6931471805599453f;
+      for (int x = 0; x < kSlices - 1; ++x) {
+        const float4 u = sum[(x * kPass + item) * 2], v = sum[(x * kPass + item) * 2 + 1];
+        f[0] += u.x, f[1] += u.y, f[2] += u.z, f[3] += u.w;
+        f[4] += v.x, f[5] += v.y, f[6] += v.z, f[7] += v.w;
+      }
+      const float l = row_l[r];
+      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] *= inv;
+      const int32_t row = rt * kRows + r, qi = row / a.group, hq = h * a.group + row - qi * a.group;
+      store_o8(a, static_cast<uint16_t*>(a.out) + int64_t(q0 + qi) * a.o_st + int64_t(hq) * a.o_sh + d, f);
+      if (d == 0 && a.lse != nullptr)
+        a.lse[int64_t(q0 + qi) * (a.kv_heads * a.group) + hq] =
+            l == 0.0f ? -INFINITY : (row_m[r] - 14.0f + log2f(l)) * 0.6931471805599453f;
+    }
+    __syncthreads();
   }
 }
 
-template <int D, bool kSplit>
+template <int D, int kRows>
 nvfp4_status stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, const StreamParams& sp, int row_tiles,
                            cudaStream_t stream) {
-  using T = Tile<D>;
-  auto kern = k_attn_stream<D, kSplit>;
+  using T = Tile<D, kRows>;
+  auto kern = k_attn_stream<D, kRows>;
   nvfp4_status st = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem),
                                "cudaFuncSetAttribute(k_attn_stream)");
   if (st != NVFP4_OK) return st;
-  kern<<<sp.workers / kWarps, kThreads, T::kSmem, stream>>>(tk, tv, sp);
+  StreamParams p = sp;
+  p.workers = T::kCtas * sm_count() * kWarps;
+  kern<<<p.workers / kWarps, kThreads, T::kSmem, stream>>>(tk, tv, p);
   if ((st = cuda_check(cudaGetLastError(), "launch k_attn_stream")) != NVFP4_OK) return st;
-  k_attn_combine<D><<<dim3(unsigned(sp.a.kv_heads), unsigned(row_tiles), unsigned(sp.a.seqs)), 128, 0, stream>>>(sp);
-  return cuda_check(cudaGetLastError(), "launch k_attn_combine");
+  // launched while the stream kernel drains; it waits for it at its start
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(p.a.kv_heads), unsigned(row_tiles), unsigned(p.a.seqs));
+  cfg.blockDim = dim3(kCombineThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, k_attn_combine<D, kRows>, static_cast<const StreamParams>(p)),
+                    "launch k_attn_combine");
 }
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
-int stream_workers() { return 2 * sm_count() * kWarps; }
+// Rows of partials: two a worker, the most of any variant (16 rows of 2 blocks
+// an SM, 8 rows of 4).
+int64_t partial_rows() { return 2 * int64_t(sm_count()) * kWarps * 32; }
 
 }  // namespace
 
 int64_t attn_stream_workspace(int32_t dim) {
-  const int64_t slots = 2 * int64_t(stream_workers());
-  return align256(slots * 16 * dim * 4) + align256(slots * 16 * 8) + align256((kMaxSeqs + 1) * 8);
+  return align256(partial_rows() * dim * 4) + align256(partial_rows() * 8) + align256((kMaxSeqs + 1) * 8);
 }
 
 nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32_t max_queries, void* workspace,
                          cudaStream_t stream) {
   const int32_t dim = cache->dim;
   CUtensorMap tk, tv;
-  const int box = std::min(cache->page_size, dim == 256 ? 32 : 64);
+  const int box = std::min(cache->page_size, dim == 64 ? 64 : 32);
   const cuuint64_t dims[3] = {cuuint64_t(dim / 2), cuuint64_t(cache->page_size),
                               cuuint64_t(cache->pages * cache->kv_heads)};
   const cuuint64_t strides[2] = {cuuint64_t(dim / 2), cuuint64_t(dim / 2) * cuuint64_t(cache->page_size)};
@@ -791,16 +932,14 @@ nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32
   if (st != NVFP4_OK) return st;
   StreamParams sp;
   sp.a = base;
-  sp.workers = stream_workers();
   const int64_t rows_max = int64_t(max_queries) * base.group;
-  const bool split = rows_max <= 8;
-  sp.rows = split ? 8 : 16;
-  const int64_t slots = 2 * int64_t(sp.workers);
+  const int32_t rows = rows_max <= 8 ? 8 : 16;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   sp.part_o = reinterpret_cast<float*>(ws);
-  sp.part_ml = reinterpret_cast<float2*>(ws + align256(slots * 16 * dim * 4));
-  sp.prefix = reinterpret_cast<int64_t*>(ws + align256(slots * 16 * dim * 4) + align256(slots * 16 * 8));
-  const int64_t row_tiles = (rows_max + sp.rows - 1) / sp.rows;
+  sp.part_ml = reinterpret_cast<float2*>(ws + align256(partial_rows() * dim * 4));
+  sp.prefix =
+      reinterpret_cast<int64_t*>(ws + align256(partial_rows() * dim * 4) + align256(partial_rows() * 8));
+  const int64_t row_tiles = (rows_max + rows - 1) / rows;
   if (row_tiles > 65535) return fail(NVFP4_EUNSUPPORTED, "mxfp4_cache_attention: too many query rows a sequence");
   // kMaxSeqs sequences a launch; the workspace is reused in stream order
   for (int32_t b = 0; b < base.seqs; b += kMaxSeqs) {
@@ -814,12 +953,12 @@ nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32
       sp.a.out = static_cast<uint16_t*>(base.out) + int64_t(b) * base.o_st;
       if (base.lse != nullptr) sp.a.lse = base.lse + int64_t(b) * base.kv_heads * base.group;
     }
-    if (dim == 64) st = split ? stream_launch<64, true>(tk, tv, sp, int(row_tiles), stream)
-                              : stream_launch<64, false>(tk, tv, sp, int(row_tiles), stream);
-    else if (dim == 128) st = split ? stream_launch<128, true>(tk, tv, sp, int(row_tiles), stream)
-                                    : stream_launch<128, false>(tk, tv, sp, int(row_tiles), stream);
-    else st = split ? stream_launch<256, true>(tk, tv, sp, int(row_tiles), stream)
-                    : stream_launch<256, false>(tk, tv, sp, int(row_tiles), stream);
+    if (dim == 64) st = rows == 8 ? stream_launch<64, 8>(tk, tv, sp, int(row_tiles), stream)
+                                  : stream_launch<64, 16>(tk, tv, sp, int(row_tiles), stream);
+    else if (dim == 128) st = rows == 8 ? stream_launch<128, 8>(tk, tv, sp, int(row_tiles), stream)
+                                        : stream_launch<128, 16>(tk, tv, sp, int(row_tiles), stream);
+    else st = rows == 8 ? stream_launch<256, 8>(tk, tv, sp, int(row_tiles), stream)
+                        : stream_launch<256, 16>(tk, tv, sp, int(row_tiles), stream);
     if (st != NVFP4_OK) return st;
   }
   return NVFP4_OK;

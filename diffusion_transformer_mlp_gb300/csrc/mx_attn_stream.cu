@@ -68,8 +68,8 @@ struct Tile {
   static constexpr int kScales = kTok * C;
   static constexpr int kCtas = (kRows == 8 && D <= 128) ? 4 : 2;  // blocks an SM
   static constexpr int kStages = 3;
-  static constexpr int kKf = kTok * C * 4;  // K scales as float [token][C]
-  static constexpr int kVf = kTok * C * (kRows == 8 ? 4 : 2);  // V factors [C][token]: (f, f), or f
+  static constexpr int kKf = kTok * C * 4;  // K scales as float [position][C]
+  static constexpr int kVf = kTok * C * (kRows == 8 ? 4 : 2);  // V factors [C][position]: (f, f), or f
   static constexpr int kWarpCodes = kStages * 2 * kCodes;
   static constexpr int kWarpRest = kStages * 2 * kScales + kKf + kVf;
   // [warp codes x 4][warp rest x 4][barriers]; the tile counts of the
@@ -206,12 +206,23 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Byte offset of 16-byte chunk c of row t in a tile whose rows are D/2 bytes,
-// as the TMA's swizzle of that width lays it out.
+// A tile lies in shared memory as rows of 128 bytes, P = 256 / D tokens each,
+// under the TMA's 128-byte swizzle.  An 8x8 matrix takes the same part of
+// eight consecutive rows, which the swizzle spreads over all banks: its
+// columns are tokens P apart.  Position pos = 8 nt + column of the MMAs is
+// token token_of(pos) of the tile.
 template <int D>
-__device__ __forceinline__ uint32_t swz(int t, int c) {
-  constexpr int C = D / 32;
-  return uint32_t(t * (D / 2) + ((c ^ ((t / (8 / C)) & (C - 1))) << 4));
+__device__ __forceinline__ int token_of(int pos) {
+  constexpr int P = 256 / D;
+  const int nt = pos >> 3;
+  return nt / P * (8 * P) + (pos & 7) * P + nt % P;
+}
+// Byte offset of 16-byte chunk (block) c of the token at pos.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int pos, int c) {
+  constexpr int P = 256 / D, C = D / 32;
+  const int nt = pos >> 3, row = nt / P * 8 + (pos & 7);
+  return uint32_t(row * 128 + (((nt % P * C + c) ^ (row & 7)) << 4));
 }
 
 // Eight consecutive elements of a query row, to binary32.
@@ -353,8 +364,8 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
     if (lane < nb) {
       const int64_t pg = min(max(int64_t(page), int64_t(0)), a.pages - 1);
       const int32_t z = int32_t(pg * a.kv_heads + ld.h), off = (tok0 + lane * box) & ((1 << a.page_shift) - 1);
-      tma_load_3d_plain(st + lane * box * (D / 2), &tmap_k, &full[slot], 0, off, z);
-      tma_load_3d_plain(st + T::kCodes + lane * box * (D / 2), &tmap_v, &full[slot], 0, off, z);
+      tma_load_3d_plain(st + lane * box * (D / 2), &tmap_k, &full[slot], 0, off / (256 / D), z);
+      tma_load_3d_plain(st + T::kCodes + lane * box * (D / 2), &tmap_v, &full[slot], 0, off / (256 / D), z);
       const int64_t srow = ((int64_t(z) << a.page_shift) + off) * C;
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv)
@@ -507,17 +518,17 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
       uint32_t kw[U][(C + 3) / 4], vw[U][(C + 3) / 4];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int t = lane + 32 * u;
+        const int pos = lane + 32 * u, t = token_of<D>(pos);
         if constexpr (C == 2) {
           kw[u][0] = *reinterpret_cast<const uint16_t*>(ks + t * 2);
           vw[u][0] = *reinterpret_cast<const uint16_t*>(vs + t * 2);
-          *reinterpret_cast<float2*>(kf + t * 2) = make_float2(e8m0_byte(kw[u][0], 0), e8m0_byte(kw[u][0], 1));
+          *reinterpret_cast<float2*>(kf + pos * 2) = make_float2(e8m0_byte(kw[u][0], 0), e8m0_byte(kw[u][0], 1));
         } else {
 #pragma unroll
           for (int h = 0; h < C / 4; ++h) {
             kw[u][h] = *reinterpret_cast<const uint32_t*>(ks + t * C + 4 * h);
             vw[u][h] = *reinterpret_cast<const uint32_t*>(vs + t * C + 4 * h);
-            *reinterpret_cast<float4*>(kf + t * C + 4 * h) =
+            *reinterpret_cast<float4*>(kf + pos * C + 4 * h) =
                 make_float4(e8m0_byte(kw[u][h], 0), e8m0_byte(kw[u][h], 1), e8m0_byte(kw[u][h], 2),
                             e8m0_byte(kw[u][h], 3));
           }
@@ -529,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-          e[u][j] = lane + 32 * u < lim ? int32_t((vw[u][j / 4] >> (8 * (j % 4))) & 0xFF) : -400;
+          e[u][j] = token_of<D>(lane + 32 * u) < lim ? int32_t((vw[u][j / 4] >> (8 * (j % 4))) & 0xFF) : -400;
           up = up || e[u][j] > rmax[j];
         }
 #pragma unroll
@@ -575,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
       uint32_t w[4];
       {
         const int idx = gi * 4 + (lane >> 3);  // matrix (key group, block) of this lane's row address
-        ldsm_x4(kc + swz<D>(idx / C * 8 + (lane & 7), idx % C), w);
+        ldsm_x4(kc + chunk_at<D>(idx / C * 8 + (lane & 7), idx % C), w);
       }
       // block scales of this lane's two keys of each key group of the four matrices
       constexpr int kV = C < 4 ? C : 4;
@@ -638,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int32_t j = tok0 + nt * 8 + 2 * tig + e;
+            const int32_t j = tok0 + token_of<D>(nt * 8 + 2 * tig + e);
             if (j >= cu.len || !sees(a, pos[r], j)) s[nt][2 * r + e] = -INFINITY;
           }
     }
@@ -713,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
 #pragma unroll
       for (int n4 = 0; n4 < NT / 4; ++n4) {
         uint32_t w[4];
-        ldsm_x4_t(vc + swz<D>(n4 * 32 + lane, j), w);  // four groups of eight keys, block j
+        ldsm_x4_t(vc + chunk_at<D>(n4 * 32 + lane, j), w);  // four groups of eight keys, block j
         if constexpr (kRows == 8) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -919,13 +930,12 @@ nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32
   const int32_t dim = cache->dim;
   CUtensorMap tk, tv;
   const int box = std::min(cache->page_size, dim == 64 ? 64 : 32);
-  const cuuint64_t dims[3] = {cuuint64_t(dim / 2), cuuint64_t(cache->page_size),
-                              cuuint64_t(cache->pages * cache->kv_heads)};
-  const cuuint64_t strides[2] = {cuuint64_t(dim / 2), cuuint64_t(dim / 2) * cuuint64_t(cache->page_size)};
-  const cuuint32_t bx[3] = {cuuint32_t(dim / 2), cuuint32_t(box), 1};
-  const CUtensorMapSwizzle swz = dim == 64    ? CU_TENSOR_MAP_SWIZZLE_32B
-                                 : dim == 128 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                              : CU_TENSOR_MAP_SWIZZLE_128B;
+  // rows of 128 bytes: 256 / dim tokens of one head and page
+  const int per_row = 256 / dim;
+  const cuuint64_t dims[3] = {128, cuuint64_t(cache->page_size / per_row), cuuint64_t(cache->pages * cache->kv_heads)};
+  const cuuint64_t strides[2] = {128, cuuint64_t(dim / 2) * cuuint64_t(cache->page_size)};
+  const cuuint32_t bx[3] = {128, cuuint32_t(box / per_row), 1};
+  const CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B;
   nvfp4_status st = make_map(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, cache->k_codes, 3, dims, strides, bx, swz, "K codes");
   if (st == NVFP4_OK)
     st = make_map(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, cache->v_codes, 3, dims, strides, bx, swz, "V codes");

@@ -14,12 +14,14 @@
 //             elements below that lose bits that weigh nothing).  Each 32-wide
 //             block of the head is one MMA pair whose FP32 result is
 //             multiplied by the key's block scale.
-//   softmax   running maximum and sum in FP32; weights p 2^14 rounded to FP16
-//             for the second MMA (11 bits; BF16 would keep 8).
+//   softmax   sum in FP32 against a reference that follows the running
+//             maximum once it is 2^5 behind, so that the output is rarely
+//             rescaled; weights p 2^10 <= 2^15 rounded to FP16 for the second
+//             MMA (11 bits; BF16 would keep 8).
 //   p v       a value's block scale varies along the contraction, so it goes
-//             onto the weights: p 2^14 2^(E - R) with R the largest E of the
+//             onto the weights: p 2^10 2^(E - R) with R the largest E of the
 //             block column so far (a running maximum like the softmax's).  The
-//             factor 2^14 leaves 28 binades below the largest before FP16
+//             factor 2^10 leaves 24 binades below the reference before FP16
 //             loses bits.
 //
 // The decoding cvt gives two neighbours (d, d + 1) of one token, while an MMA
@@ -27,6 +29,8 @@
 // step of 8 heads a kv head) need no transposition for that: the contraction
 // pair is (d, d + 1), MMA row g holds (p, 0) and row g + 8, idle otherwise,
 // (0, p), so that rows 0..7 collect the even and rows 8..15 the odd columns.
+// In q k^T their rows 8..15 hold the other half of the block, and each of a
+// block's two MMAs gives its result in one half of the rows.
 // With 16 rows the halves are put together by PRMT, one for each register.
 // The ldmatrix layouts fit the format: a 16-byte row of an 8x8 matrix is one
 // block of one token, so for K a lane gets 8 codes of one block, and with
@@ -57,19 +61,19 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxSeqs = 1024;  // sequences of one launch (their tile counts sit in shared memory)
 
-// kRows = 8 takes 32 keys of 128 at a time (64 of 64, 16 of 256) and 16 warps
-// an SM, which hides the latency of the MMA and softmax chains; 16 rows need
-// twice the registers and run with 8.
+// A stage of the ring holds kTok keys, worked off kSub at a time.
 template <int D, int kRows>
 struct Tile {
   static constexpr int C = D / 32;  // blocks of a row
-  static constexpr int kTok = D == 64 ? 64 : 32;
+  static constexpr int kTok = D == 256 ? 32 : (D == 128 ? 64 : 128);
+  static constexpr int kSub = D == 64 ? 64 : 32;
   static constexpr int kCodes = kTok * D / 2;  // bytes of K (or V) codes
   static constexpr int kScales = kTok * C;
-  static constexpr int kCtas = (kRows == 8 && D <= 128) ? 4 : 2;  // blocks an SM
-  static constexpr int kStages = 3;
-  static constexpr int kKf = kTok * C * 4;  // K scales as float [position][C]
-  static constexpr int kVf = kTok * C * (kRows == 8 ? 4 : 2);  // V factors [C][position]: (f, f), or f
+  static constexpr int kCtas = (kRows == 8 && D <= 128) ? 3 : 2;  // blocks an SM
+  static constexpr int kStages = kCtas == 3 ? 2 : 3;
+  static constexpr int kKf = kSub * C * 4;  // K scales as float [position][C]
+  // V factors: (f, f) [position][C] for 8 rows, f [position pair][C][2] for 16
+  static constexpr int kVf = kSub * C * (kRows == 8 ? 4 : 2);
   static constexpr int kWarpCodes = kStages * 2 * kCodes;
   static constexpr int kWarpRest = kStages * 2 * kScales + kKf + kVf;
   // [warp codes x 4][warp rest x 4][barriers]; the tile counts of the
@@ -80,6 +84,9 @@ struct Tile {
   static_assert(kCodes % 1024 == 0, "swizzle atoms");
   static_assert(kCtas * (kSmem + 1024) <= 233472, "blocks an SM");
 };
+
+constexpr float kWeightLog2 = 10.0f;  // weights are held times 2^10
+constexpr float kLag = 5.0f;          // the softmax reference may lag the maximum by 2^5
 
 struct StreamParams {
   AttnParams a;
@@ -270,10 +277,10 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
     k_attn_stream(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                   const __grid_constant__ StreamParams sp) {
   using T = Tile<D, kRows>;
-  constexpr int C = T::C, kTok = T::kTok, NT = kTok / 8;
+  constexpr int C = T::C, kTok = T::kTok, kSub = T::kSub, NT = kSub / 8;
   constexpr int R = kRows / 8;   // rows of a thread: g, and g + 8
   constexpr int Y = 2 * R;       // accumulators of a block: 8 rows hold two columns in each
-  constexpr int U = kTok / 32;   // keys of a lane in the scale work
+  constexpr int U = kSub / 32;   // keys of a lane in the scale work
   const AttnParams& a = sp.a;
   extern __shared__ __align__(1024) uint8_t base[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
@@ -345,33 +352,34 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
 
   // ---- loads: lane i < boxes takes box i of a tile (a page's share of it);
   // its page is looked up when the tile before is issued
-  const int32_t box = min(1 << a.page_shift, kTok), boxes = kTok / box;
+  const int32_t box_shift = min(a.page_shift, kTok == 32 ? 5 : (kTok == 64 ? 6 : 7));
+  const int32_t box = 1 << box_shift, boxes = kTok >> box_shift;
   Cursor ld = cu;
   int32_t page;
   auto look_up = [&]() {
-    const int32_t tok = ld.s.tile(ld.t) * kTok + lane * box;
+    const int32_t tok = ld.s.tile(ld.t) * kTok + (lane << box_shift);
     page = 0;
     if (lane < boxes && tok < ld.len)
-      page = a.table[int64_t(ld.b) * a.table_ld + min(int64_t(tok >> a.page_shift), a.table_ld - 1)];
+      page = a.table[int64_t(ld.b) * a.table_ld + min(tok >> a.page_shift, int32_t(a.table_ld) - 1)];
   };
   auto issue = [&](int slot) {
     const int32_t tok0 = ld.s.tile(ld.t) * kTok;
-    const int32_t nb = min(boxes, (ld.len - tok0 + box - 1) / box);  // boxes that hold a token
-    uint8_t* st = codes + slot * 2 * T::kCodes;
-    uint8_t* sc = rest + slot * 2 * T::kScales;
-    if (lane == 0) mbar_arrive_expect_tx(&full[slot], uint32_t(nb * box) * (D + 2 * C));
+    const int32_t nb = min(boxes, (ld.len - tok0 + box - 1) >> box_shift);  // boxes that hold a token
+    if (lane == 0) mbar_arrive_expect_tx(&full[slot], uint32_t(nb << box_shift) * (D + 2 * C));
     __syncwarp();
     if (lane < nb) {
-      const int64_t pg = min(max(int64_t(page), int64_t(0)), a.pages - 1);
-      const int32_t z = int32_t(pg * a.kv_heads + ld.h), off = (tok0 + lane * box) & ((1 << a.page_shift) - 1);
-      tma_load_3d_plain(st + lane * box * (D / 2), &tmap_k, &full[slot], 0, off / (256 / D), z);
-      tma_load_3d_plain(st + T::kCodes + lane * box * (D / 2), &tmap_v, &full[slot], 0, off / (256 / D), z);
+      uint8_t* st = codes + slot * 2 * T::kCodes + (lane << box_shift) * (D / 2);
+      uint8_t* sc = rest + slot * 2 * T::kScales + (lane << box_shift) * C;
+      const int32_t pg = min(max(page, 0), int32_t(a.pages) - 1);
+      const int32_t z = pg * a.kv_heads + ld.h, off = (tok0 + (lane << box_shift)) & ((1 << a.page_shift) - 1);
+      tma_load_3d_plain(st, &tmap_k, &full[slot], 0, off / (256 / D), z);
+      tma_load_3d_plain(st + T::kCodes, &tmap_v, &full[slot], 0, off / (256 / D), z);
       const int64_t srow = ((int64_t(z) << a.page_shift) + off) * C;
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv)
         asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                         smem_u32(sc + kv * T::kScales + lane * box * C)),
-                     "l"((kv ? a.v_scales : a.k_scales) + srow), "r"(box * C), "r"(smem_u32(&full[slot]))
+                         smem_u32(sc + kv * T::kScales)),
+                     "l"((kv ? a.v_scales : a.k_scales) + srow), "r"(C << box_shift), "r"(smem_u32(&full[slot]))
                      : "memory");
     }
   };
@@ -389,17 +397,20 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
   // ---- state of the segment
   uint32_t qa[C][2][2 * R];  // Q fragments: block, MMA of the block
   float qf[R];               // row factor of the scores (log2 domain)
-  int32_t pos[R];            // position of the row's query
-  float o[C][Y][4];          // block, MMA of the block, accumulator
-  float m[R], l[R];
-  int32_t rmax[C];           // R of the block columns
+  // the row sees keys j < end with j >= from or j < a.sinks
+  int32_t end[R], from[R];
+  float o[C][Y][4];  // block, MMA of the block, accumulator
+  float m[R], l[R];  // softmax reference; sum of this lane's weights, times 2^10
+  int32_t rmax[C];   // R of the block columns
   auto begin_segment = [&]() {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int32_t row = cu.rt * kRows + g + 8 * r;
       const bool real = row < cu.nq * a.group;
       const int32_t qi = real ? row / a.group : 0, hq = cu.h * a.group + (real ? row - qi * a.group : 0);
-      pos[r] = cu.len - cu.nq + qi;
+      const int32_t pos = cu.len - cu.nq + qi;
+      end[r] = a.causal ? min(cu.len, pos + 1) : cu.len;
+      from[r] = a.window > 0 ? pos - a.window + 1 : 0;
       const uint16_t* src = static_cast<const uint16_t*>(a.q) + int64_t(cu.q0 + qi) * a.q_st + int64_t(hq) * a.q_sh;
       float am = 0.0f;
 #pragma unroll
@@ -454,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
       const int32_t qi = row / a.group, hq = cu.h * a.group + row - qi * a.group;
 #pragma unroll
       for (int j = 0; j < C; ++j) {
-        // the accumulators hold p 2^14 v 2^(127 - R), the sum p 2^14
+        // the accumulators hold p 2^10 v 2^(127 - R), the sum p 2^10
         const float s = pow2i(rmax[j] - 127) * (whole ? inv : 1.0f);
         float f[8];  // columns 32 j + 8 tig + 0 .. 7
 #pragma unroll
@@ -482,71 +493,48 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
           sp.part_ml[(int64_t(worker) * 2 + slot) * kRows + g + 8 * r] = make_float2(m[r], l[r]);
         } else if (a.lse != nullptr && row < head_rows) {
           a.lse[int64_t(cu.q0 + qi) * (a.kv_heads * a.group) + hq] =
-              l[r] == 0.0f ? -INFINITY : (m[r] - 14.0f + log2f(l[r])) * 0.6931471805599453f;
+              l[r] == 0.0f ? -INFINITY : (m[r] - kWeightLog2 + log2f(l[r])) * 0.6931471805599453f;
         }
       }
     }
   };
 
-  bool from_start = cu.t == 0;  // the segment's first tile is ours
-  int part_slot = 0;            // workspace slot of a partial: 0 for the run's first segment, 1 for a later one
-  bool fresh = true;
-  int slot = 0;
-  uint32_t phase = 0;
-#pragma unroll 1
-  for (int32_t n = 0; n < tiles; ++n) {
-    if (fresh) begin_segment();
-    {
-      int ok = 1;
-      if (lane == 0) ok = mbar_wait_bounded(&full[slot], phase, a.wait_limit_cycles, nullptr);
-      if (__shfl_sync(0xFFFFFFFFu, ok, 0) == 0) {
-        if (lane == 0 && a.dev_status != nullptr) atomicExch(a.dev_status, static_cast<uint32_t>(NVFP4_ETIMEOUT));
-        return;
-      }
-    }
-    const uint32_t kc = smem_u32(codes + slot * 2 * T::kCodes), vc = kc + T::kCodes;
-    const uint8_t* ks = rest + slot * 2 * T::kScales;
-    const uint8_t* vs = ks + T::kScales;
-    const int32_t tok0 = cu.s.tile(cu.t) * kTok;
-    const int32_t lim = cu.s.hi - tok0;  // keys of the tile that some row may see: those below
-
+  // kSub keys from smem: `sub` of the stage at codes kc, vc, scales ks, vs
+  auto work = [&](uint32_t kc, uint32_t vc, const uint8_t* ks, const uint8_t* vs, int32_t tok0) {
+    const int32_t lim = cu.s.hi - tok0;  // keys that some row may see: those below
+    uint32_t nan_keys[U][C] = {};        // keys whose block holds NaN (E = 255)
+    bool nan_scale = false;
     // scales: K as floats; V as FP16 factors against the running maximum
-    uint32_t nan_keys[U][C] = {};  // keys whose block holds NaN (E = 255)
-    bool nan_scale = false, rescale = false;
-    float vbeta[C];
     {
-      uint32_t kw[U][(C + 3) / 4], vw[U][(C + 3) / 4];
+      int32_t e[U][C];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int pos = lane + 32 * u, t = token_of<D>(pos);
         if constexpr (C == 2) {
-          kw[u][0] = *reinterpret_cast<const uint16_t*>(ks + t * 2);
-          vw[u][0] = *reinterpret_cast<const uint16_t*>(vs + t * 2);
-          *reinterpret_cast<float2*>(kf + pos * 2) = make_float2(e8m0_byte(kw[u][0], 0), e8m0_byte(kw[u][0], 1));
+          const uint32_t kw = *reinterpret_cast<const uint16_t*>(ks + t * 2);
+          uint32_t vw = *reinterpret_cast<const uint16_t*>(vs + t * 2);
+          if (t >= lim) vw = 0;  // a key that no row sees, whose bytes may be anything
+          *reinterpret_cast<float2*>(kf + pos * 2) = make_float2(e8m0_byte(kw, 0), e8m0_byte(kw, 1));
+          e[u][0] = vw & 0xFF, e[u][1] = vw >> 8;
         } else {
 #pragma unroll
           for (int h = 0; h < C / 4; ++h) {
-            kw[u][h] = *reinterpret_cast<const uint32_t*>(ks + t * C + 4 * h);
-            vw[u][h] = *reinterpret_cast<const uint32_t*>(vs + t * C + 4 * h);
+            const uint32_t kw = *reinterpret_cast<const uint32_t*>(ks + t * C + 4 * h);
+            uint32_t vw = *reinterpret_cast<const uint32_t*>(vs + t * C + 4 * h);
+            if (t >= lim) vw = 0;
             *reinterpret_cast<float4*>(kf + pos * C + 4 * h) =
-                make_float4(e8m0_byte(kw[u][h], 0), e8m0_byte(kw[u][h], 1), e8m0_byte(kw[u][h], 2),
-                            e8m0_byte(kw[u][h], 3));
+                make_float4(e8m0_byte(kw, 0), e8m0_byte(kw, 1), e8m0_byte(kw, 2), e8m0_byte(kw, 3));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[u][(4 * h + i) % C] = (vw >> (8 * i)) & 0xFF;
           }
         }
       }
-      int32_t e[U][C];  // -400: a key that no row sees, whose bytes may be anything: its factor is 0
       bool up = false;
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int j = 0; j < C; ++j) {
-          e[u][j] = token_of<D>(lane + 32 * u) < lim ? int32_t((vw[u][j / 4] >> (8 * (j % 4))) & 0xFF) : -400;
-          up = up || e[u][j] > rmax[j];
-        }
-#pragma unroll
-      for (int j = 0; j < C; ++j) vbeta[j] = 1.0f;
+        for (int j = 0; j < C; ++j) up = up || e[u][j] > rmax[j];
       if (__any_sync(0xFFFFFFFFu, up)) {
-        rescale = true;
 #pragma unroll
         for (int j = 0; j < C; ++j) {
           int32_t mx = 0;
@@ -554,24 +542,40 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
           for (int u = 0; u < U; ++u) {
             nan_keys[u][j] = __ballot_sync(0xFFFFFFFFu, e[u][j] == 255);
             nan_scale = nan_scale || nan_keys[u][j] != 0;
-            if (e[u][j] == 255) e[u][j] = -400;
+            if (e[u][j] == 255) e[u][j] = 0;
             mx = max(mx, e[u][j]);
           }
           mx = max(__reduce_max_sync(0xFFFFFFFFu, mx), rmax[j]);
-          vbeta[j] = pow2i(rmax[j] - mx);
+          const float beta = pow2i(rmax[j] - mx);
           rmax[j] = mx;
+#pragma unroll
+          for (int y = 0; y < Y; ++y)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[j][y][i] *= beta;
         }
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int u = 0; u < U; ++u) {
+        const int pos = lane + 32 * u;
+        uint32_t w[C];
 #pragma unroll
         for (int j = 0; j < C; ++j) {
           // 2^(E - R) through binary32, rounded (to a subnormal, to zero) by the conversion
           const float f = __uint_as_float(uint32_t(max(e[u][j] - rmax[j] + 127, 0)) << 23);
-          const uint32_t w = f32_to_word<__half>(f, f);
-          if constexpr (kRows == 8) reinterpret_cast<uint32_t*>(vf)[j * kTok + lane + 32 * u] = w;
-          else reinterpret_cast<uint16_t*>(vf)[j * kTok + lane + 32 * u] = uint16_t(w);
+          w[j] = f32_to_word<__half>(f, f);
+          if constexpr (kRows == 16) reinterpret_cast<uint16_t*>(vf)[(pos / 2 * C + j) * 2 + pos % 2] = uint16_t(w[j]);
         }
+        if constexpr (kRows == 8) {
+          if constexpr (C == 2) {
+            *reinterpret_cast<uint2*>(vf + pos * 8) = make_uint2(w[0], w[1]);
+          } else {
+#pragma unroll
+            for (int h = 0; h < C / 4; ++h)
+              *reinterpret_cast<uint4*>(vf + pos * C * 4 + h * 16) =
+                  make_uint4(w[(4 * h) % C], w[(4 * h + 1) % C], w[(4 * h + 2) % C], w[(4 * h + 3) % C]);
+          }
+        }
+      }
       __syncwarp();
     }
 
@@ -611,32 +615,36 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
         const int idx = gi * 4 + x, nt = idx / C, j = idx % C;
         uint32_t h[4];
         e2m1x8_to_half(w[x], h);
+        const float f0 = fk[x / kV][0][x % kV], f1 = fk[x / kV][1][x % kV];
         float c[4];
         if constexpr (kRows == 8) {
-          mma_f16_zero(c, qa[j][0][0], 0u, qa[j][0][1], 0u, h[0], h[1]);
-          mma_f16(c, qa[j][1][0], 0u, qa[j][1][1], 0u, h[2], h[3]);
+          // rows 0..7 hold the block's first, rows 8..15 its second half
+          float d[4];
+          mma_f16_zero(c, qa[j][0][0], qa[j][1][0], qa[j][0][1], qa[j][1][1], h[0], h[1]);
+          mma_f16_zero(d, qa[j][0][0], qa[j][1][0], qa[j][0][1], qa[j][1][1], h[2], h[3]);
+          s[nt][0] = fmaf(c[0], f0, s[nt][0]);
+          s[nt][1] = fmaf(c[1], f1, s[nt][1]);
+          s[nt][0] = fmaf(d[2], f0, s[nt][0]);
+          s[nt][1] = fmaf(d[3], f1, s[nt][1]);
         } else {
           mma_f16_zero(c, qa[j][0][0], qa[j][0][1], qa[j][0][2 % (2 * R)], qa[j][0][3 % (2 * R)], h[0], h[1]);
           mma_f16(c, qa[j][1][0], qa[j][1][1], qa[j][1][2 % (2 * R)], qa[j][1][3 % (2 * R)], h[2], h[3]);
-        }
-        const float f0 = fk[x / kV][0][x % kV], f1 = fk[x / kV][1][x % kV];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          s[nt][2 * r] = fmaf(c[2 * r], f0, s[nt][2 * r]);
-          s[nt][2 * r + 1] = fmaf(c[2 * r + 1], f1, s[nt][2 * r + 1]);
+          for (int r = 0; r < R; ++r) {
+            s[nt][2 * r] = fmaf(c[2 * r], f0, s[nt][2 * r]);
+            s[nt][2 * r + 1] = fmaf(c[2 * r + 1], f1, s[nt][2 * r + 1]);
+          }
         }
       }
     }
 
-    // mask, running maximum, weights
-    float alpha[R];
+    // mask, reference, weights
     // 8 rows: words (p, 0) of the lane's two keys; 16 rows: pairs of the two keys
     uint32_t pw[NT][2];
-    bool all = true;  // do the rows see the whole tile?
+    bool all = true;  // do the rows see all these keys?
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      all = all && tok0 + kTok <= cu.len && (!a.causal || tok0 + kTok - 1 <= pos[r]) &&
-            (a.window <= 0 || tok0 > pos[r] - a.window || tok0 + kTok <= a.sinks);
+      all = all && tok0 + kSub <= end[r] && (tok0 >= from[r] || tok0 + kSub <= a.sinks);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -650,25 +658,43 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int32_t j = tok0 + token_of<D>(nt * 8 + 2 * tig + e);
-            if (j >= cu.len || !sees(a, pos[r], j)) s[nt][2 * r + e] = -INFINITY;
+            if (j >= end[r] || (j < from[r] && j >= a.sinks)) s[nt][2 * r + e] = -INFINITY;
           }
+    }
+    float mx[R];
+    bool raise = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mx[r] = fmaxf(s[0][2 * r], s[0][2 * r + 1]);
+#pragma unroll
+      for (int nt = 1; nt < NT; ++nt) mx[r] = fmaxf(mx[r], fmaxf(s[nt][2 * r], s[nt][2 * r + 1]));
+      raise = raise || mx[r] > m[r] + kLag;
+    }
+    if (__any_sync(0xFFFFFFFFu, raise)) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xFFFFFFFFu, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xFFFFFFFFu, mx[r], 2));
+        mx[r] = fmaxf(mx[r], m[r]);
+        const float alpha = exp2_approx(m[r] - (mx[r] == -INFINITY ? 0.0f : mx[r]));
+        m[r] = mx[r];
+        l[r] *= alpha;
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+          for (int y = 0; y < Y; ++y)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (kRows == 8 || (e >> 1) == r) o[j][y][e] *= alpha;
+      }
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float mx = m[r];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(s[nt][2 * r], s[nt][2 * r + 1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-      const float ms = mx == -INFINITY ? 0.0f : mx;  // no key seen yet: every weight is 2^-inf = 0
-      alpha[r] = exp2_approx(m[r] - ms);
-      rescale = rescale || alpha[r] != 1.0f;
-      m[r] = mx;
-      float sum = 0.0f;
+      const float ms = (m[r] == -INFINITY ? 0.0f : m[r]) - kWeightLog2;  // no key seen yet: every weight is 2^-inf = 0
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float p0 = exp2_approx(s[nt][2 * r] - (ms - 14.0f)), p1 = exp2_approx(s[nt][2 * r + 1] - (ms - 14.0f));
-        sum += p0 + p1;
+        const float p0 = exp2_approx(s[nt][2 * r] - ms), p1 = exp2_approx(s[nt][2 * r + 1] - ms);
+        l[r] += p0 + p1;
         if constexpr (kRows == 8) {
           pw[nt][0] = f32_to_word<__half>(p0, 0.0f);
           pw[nt][1] = f32_to_word<__half>(p1, 0.0f);
@@ -676,15 +702,6 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
           pw[nt][r] = f32_to_word<__half>(p0, p1);
         }
       }
-      l[r] = l[r] * alpha[r] + sum;
-    }
-    if (__any_sync(0xFFFFFFFFu, rescale)) {
-#pragma unroll
-      for (int j = 0; j < C; ++j)
-#pragma unroll
-        for (int y = 0; y < Y; ++y)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[j][y][e] *= vbeta[j] * alpha[kRows == 8 ? 0 : (e >> 1) % R];
     }
 
     // a block of NaN reaches the rows that see its key, and only those
@@ -719,35 +736,60 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
     }
 
     // output
+    if constexpr (kRows == 8) {
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-#pragma unroll
-      for (int n4 = 0; n4 < NT / 4; ++n4) {
+      for (int gi = 0; gi < NT * C / 4; ++gi) {
         uint32_t w[4];
-        ldsm_x4_t(vc + chunk_at<D>(n4 * 32 + lane, j), w);  // four groups of eight keys, block j
-        if constexpr (kRows == 8) {
+        {
+          const int idx = gi * 4 + (lane >> 3);
+          ldsm_x4_t(vc + chunk_at<D>(idx / C * 8 + (lane & 7), idx % C), w);
+        }
+        constexpr int kV = C < 4 ? C : 4;
+        uint32_t f[4 / kV][2][kV];  // factors of the lane's two keys
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int nt = n4 * 4 + i;
-            const uint2 f = *reinterpret_cast<const uint2*>(vf + 4 * (j * kTok + nt * 8 + 2 * tig));
-            const uint32_t a0 = hmul2(pw[nt][0], f.x), a1 = hmul2(pw[nt][0] << 16, f.x);
-            const uint32_t a2 = hmul2(pw[nt][1], f.y), a3 = hmul2(pw[nt][1] << 16, f.y);
-            uint32_t x[4];
-            e2m1x8_to_half(w[i], x);  // (t, d0 d1) (t, d2 d3) (t+1, d0 d1) (t+1, d2 d3)
-            mma_f16(o[j][0], a0, a1, a2, a3, x[0], x[2]);
-            mma_f16(o[j][1], a0, a1, a2, a3, x[1], x[3]);
+        for (int y = 0; y < 4 / kV; ++y) {
+          const int idx = gi * 4 + y * kV, nt = idx / C, j = idx % C;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint8_t* src = vf + ((nt * 8 + 2 * tig + e) * C + j) * 4;
+            if constexpr (kV == 4) {
+              const uint4 v = *reinterpret_cast<const uint4*>(src);
+              f[y][e][0] = v.x, f[y][e][1] = v.y, f[y][e][2] = v.z, f[y][e][3] = v.w;
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(src);
+              f[y][e][0] = v.x, f[y][e][1] = v.y;
+            }
           }
-        } else {
+        }
 #pragma unroll
-          for (int k1 = 0; k1 < 2; ++k1) {
-            const int nt = n4 * 4 + 2 * k1;
-            const uint32_t fa = *reinterpret_cast<const uint32_t*>(vf + 2 * (j * kTok + nt * 8 + 2 * tig));
-            const uint32_t fb = *reinterpret_cast<const uint32_t*>(vf + 2 * (j * kTok + nt * 8 + 8 + 2 * tig));
+        for (int x = 0; x < 4; ++x) {
+          const int idx = gi * 4 + x, nt = idx / C, j = idx % C;
+          const uint32_t f0 = f[x / kV][0][x % kV], f1 = f[x / kV][1][x % kV];
+          const uint32_t a0 = hmul2(pw[nt][0], f0), a1 = hmul2(pw[nt][0] << 16, f0);
+          const uint32_t a2 = hmul2(pw[nt][1], f1), a3 = hmul2(pw[nt][1] << 16, f1);
+          uint32_t v[4];
+          e2m1x8_to_half(w[x], v);  // (t, d0 d1) (t, d2 d3) (t', d0 d1) (t', d2 d3)
+          mma_f16(o[j][0], a0, a1, a2, a3, v[0], v[2]);
+          mma_f16(o[j][1], a0, a1, a2, a3, v[1], v[3]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int n2 = 0; n2 < NT / 2; ++n2) {  // sixteen keys: groups 2 n2 and 2 n2 + 1
+#pragma unroll
+        for (int j2 = 0; j2 < C / 2; ++j2) {  // two blocks
+          uint32_t w[4];  // (group, block): (0, 0) (1, 0) (0, 1) (1, 1)
+          ldsm_x4_t(vc + chunk_at<D>((n2 * 2 + ((lane >> 3) & 1)) * 8 + (lane & 7), j2 * 2 + (lane >> 4)), w);
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj) {
+            const int j = j2 * 2 + jj, nt = n2 * 2;
+            const uint32_t fa = *reinterpret_cast<const uint32_t*>(vf + 4 * ((nt * 4 + tig) * C + j));
+            const uint32_t fb = *reinterpret_cast<const uint32_t*>(vf + 4 * ((nt * 4 + 4 + tig) * C + j));
             const uint32_t a0 = hmul2(pw[nt][0], fa), a1 = hmul2(pw[nt][1], fa);
             const uint32_t a2 = hmul2(pw[nt + 1][0], fb), a3 = hmul2(pw[nt + 1][1], fb);
             uint32_t x[4], y[4];
-            e2m1x8_to_half(w[2 * k1], x);
-            e2m1x8_to_half(w[2 * k1 + 1], y);  // the same eight keys on
+            e2m1x8_to_half(w[2 * jj], x);
+            e2m1x8_to_half(w[2 * jj + 1], y);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t sel = (i & 1) ? 0x7632u : 0x5410u;
@@ -758,7 +800,37 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
         }
       }
     }
+    __syncwarp();  // before the factors are overwritten
+  };
 
+  bool from_start = cu.t == 0;  // the segment's first tile is ours
+  int part_slot = 0;            // workspace slot of a partial: 0 for the run's first segment, 1 for a later one
+  bool fresh = true;
+  int slot = 0;
+  uint32_t phase = 0;
+#pragma unroll 1
+  for (int32_t n = 0; n < tiles; ++n) {
+    if (fresh) begin_segment();
+    {
+      int ok = 1;
+      if (lane == 0) ok = mbar_wait_bounded(&full[slot], phase, a.wait_limit_cycles, nullptr);
+      if (__shfl_sync(0xFFFFFFFFu, ok, 0) == 0) {
+        if (lane == 0 && a.dev_status != nullptr) atomicExch(a.dev_status, static_cast<uint32_t>(NVFP4_ETIMEOUT));
+        return;
+      }
+    }
+    {
+      uint32_t kc = smem_u32(codes + slot * 2 * T::kCodes);
+      const uint8_t* ks = rest + slot * 2 * T::kScales;
+      const int32_t first = cu.s.tile(cu.t) * kTok;
+      const int32_t last = min(first + kTok, cu.s.hi);
+#pragma unroll 1
+      for (int32_t tok0 = first; tok0 < last; tok0 += T::kSub) {
+        work(kc, kc + T::kCodes, ks, ks + T::kScales, tok0);
+        kc += T::kSub * (D / 2);
+        ks += T::kSub * C;
+      }
+    }
     // hand the slot back: these generic reads come before the next TMA write
     fence_proxy_async_smem();
     __syncwarp();
@@ -882,7 +954,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_c
       store_o8(a, static_cast<uint16_t*>(a.out) + int64_t(q0 + qi) * a.o_st + int64_t(hq) * a.o_sh + d, f);
       if (d == 0 && a.lse != nullptr)
         a.lse[int64_t(q0 + qi) * (a.kv_heads * a.group) + hq] =
-            l == 0.0f ? -INFINITY : (row_m[r] - 14.0f + log2f(l)) * 0.6931471805599453f;
+            l == 0.0f ? -INFINITY : (row_m[r] - kWeightLog2 + log2f(l)) * 0.6931471805599453f;
     }
     __syncthreads();
   }
@@ -929,7 +1001,7 @@ nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32
                          cudaStream_t stream) {
   const int32_t dim = cache->dim;
   CUtensorMap tk, tv;
-  const int box = std::min(cache->page_size, dim == 64 ? 64 : 32);
+  const int box = std::min(cache->page_size, dim == 64 ? 128 : (dim == 128 ? 64 : 32));
   // rows of 128 bytes: 256 / dim tokens of one head and page
   const int per_row = 256 / dim;
   const cuuint64_t dims[3] = {128, cuuint64_t(cache->page_size / per_row), cuuint64_t(cache->pages * cache->kv_heads)};

@@ -36,30 +36,6 @@ EXPORTED = ["nvfp4_padded_rows", "nvfp4_qdata_bytes", "nvfp4_scale_bytes", "nvfp
             "mxfp4_dequantize", "mxfp4_gemm", "mxfp4_linear_workspace_bytes", "mxfp4_linear", "mxfp4_cache_write",
             "mxfp4_cache_read", "mxfp4_attention_workspace_bytes", "mxfp4_cache_attention"]
 
-MXFP4_BF16 = 0
-MXFP4_FP16 = 1
-MXFP4_FP32 = 2
-
-
-class CacheStruct(ctypes.Structure):
-    """mxfp4_cache of mxfp4.h."""
-    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
-                ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
-                ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32), ("reserved", ctypes.c_int32)]
-
-
-class AttentionStruct(ctypes.Structure):
-    """mxfp4_attention of mxfp4.h."""
-    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
-                ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("q_starts", ctypes.c_void_p),
-                ("workspace", ctypes.c_void_p), ("dev_status", ctypes.c_void_p), ("q_st", ctypes.c_int64),
-                ("q_sh", ctypes.c_int64), ("o_st", ctypes.c_int64), ("o_sh", ctypes.c_int64),
-                ("table_ld", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64), ("seqs", ctypes.c_int32),
-                ("total_q", ctypes.c_int32), ("max_queries", ctypes.c_int32), ("q_heads", ctypes.c_int32),
-                ("dtype", ctypes.c_int32), ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
-                ("sinks", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
-
-
 _lock = threading.Lock()
 _lib = None
 

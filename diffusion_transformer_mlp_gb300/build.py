@@ -1,10 +1,12 @@
-"""Build libnvfp4fc2.so in-tree for sm_103a (nvcc, no cmake).
+"""Build libnvfp4fc2.so and the Python module of the MXFP4 functions in-tree
+for sm_103a (nvcc, g++, no cmake).
 
 Steps: generate the BF16 silu table header, compile each .cu in parallel
 with ``-gencode arch=compute_103a,code=sm_103a -lineinfo -O3`` (IEEE
 division and square root, no flush-to-zero, no fast math), link a shared
-library with the CUDA runtime linked statically.  Output:
-``diffusion_transformer_mlp_gb300/_build/libnvfp4fc2.so``.
+library with the CUDA runtime linked statically; g++ compiles binding.cpp
+against PyTorch's headers.  Output:
+``diffusion_transformer_mlp_gb300/_build/libnvfp4fc2.so`` and ``_mxfp4.so``.
 """
 from __future__ import annotations
 
@@ -35,6 +37,23 @@ def nvcc() -> str:
     return cand
 
 
+def _binding_job():
+    """(target, command) of the Python module."""
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    out = os.path.join(BUILD, "_mxfp4.so")
+    inc = [INCLUDE, os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + [a for i in inc for a in ("-I", i)]
+           + [os.path.join(CSRC, "binding.cpp"), "-o", out + f".tmp{os.getpid()}", "-L", os.path.join(t, "lib"),
+              "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_cuda"])
+    return out, cmd
+
+
 def _newer(target: str, deps: list[str]) -> bool:
     if not os.path.exists(target):
         return True
@@ -56,6 +75,10 @@ def build(verbose: bool = False, force: bool = False) -> str:
         subprocess.check_call([sys.executable, gen, table])
     deps = _headers() + [table]
     objs, jobs = [], []
+    ext = os.path.join(BUILD, "_mxfp4.so")
+    binding = force or _newer(ext, [os.path.join(CSRC, "binding.cpp")] + deps)
+    if binding:
+        jobs.append(("binding.cpp", _binding_job()[1]))
     for src in SOURCES:
         s = os.path.join(CSRC, src)
         o = os.path.join(BUILD, src.replace(".cu", ".o"))
@@ -78,6 +101,8 @@ def build(verbose: bool = False, force: bool = False) -> str:
                 f.write(log)
             if verbose:
                 print(log)
+    if binding:
+        os.replace(ext + f".tmp{os.getpid()}", ext)
     if force or jobs or not os.path.exists(LIB):
         tmp = LIB + f".tmp{os.getpid()}"
         subprocess.check_call([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs)

@@ -46,6 +46,7 @@
 // worker order.  The split depends on the lengths alone, so results are
 // reproducible.
 #include <algorithm>
+#include <atomic>
 #include <string>
 
 #include "mx_attn.cuh"
@@ -965,8 +966,8 @@ nvfp4_status stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, const S
                            cudaStream_t stream) {
   using T = Tile<D, kRows>;
   auto kern = k_attn_stream<D, kRows>;
-  nvfp4_status st = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem),
-                               "cudaFuncSetAttribute(k_attn_stream)");
+  static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
+  nvfp4_status st = allow_smem(reinterpret_cast<const void*>(kern), T::kSmem, ready);
   if (st != NVFP4_OK) return st;
   StreamParams p = sp;
   p.workers = T::kCtas * sm_count() * kWarps;

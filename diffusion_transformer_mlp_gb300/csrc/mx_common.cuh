@@ -9,10 +9,27 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "mxfp4.h"
 
 namespace nvfp4 {
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device,
+// once a device (bit of `ready`): the attribute call costs as much as a small
+// kernel's launch.
+inline nvfp4_status allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  nvfp4_status st = cuda_check(cudaGetDevice(&dev), "cudaGetDevice");
+  if (st != NVFP4_OK) return st;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev < 64 && (ready.load(std::memory_order_acquire) & bit)) return NVFP4_OK;
+  st = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes),
+                  "cudaFuncSetAttribute");
+  if (st == NVFP4_OK && dev < 64) ready.fetch_or(bit, std::memory_order_release);
+  return st;
+}
 
 inline int mx_elem_bytes(int32_t dtype) { return dtype == MXFP4_FP32 ? 4 : 2; }
 inline bool mx_dtype_ok(int32_t dtype) { return dtype == MXFP4_BF16 || dtype == MXFP4_FP16 || dtype == MXFP4_FP32; }

@@ -19,6 +19,7 @@
 // shared memory and sums the columns it owns over the cluster in rank order.
 // The split depends on the shape alone, so results are reproducible.
 #include <algorithm>
+#include <atomic>
 #include <string>
 
 #include "mx_gemm.cuh"
@@ -268,8 +269,8 @@ nvfp4_status rows_launch(const void* a_q, const void* w_q, int64_t m, int64_t n,
   int64_t split = 2 * int64_t(sm_count()) / (w_tiles * a_tiles);
   split = std::max<int64_t>(1, std::min<int64_t>(split, std::min(tiles, kMaxSplit)));
   p.split = int32_t(split);
-  st = cuda_check(cudaFuncSetAttribute(k_mx_rows<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem),
-                  "cudaFuncSetAttribute(k_mx_rows)");
+  static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
+  st = allow_smem(reinterpret_cast<const void*>(k_mx_rows<NT>), S::kSmem, ready);
   if (st != NVFP4_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(w_tiles * split), unsigned(a_tiles));

@@ -59,6 +59,15 @@
 // order inside one CTA: no split-K, no workspace, no atomics, and an output
 // row does not depend on M.
 //
+// k_fc2_gemm<false, Mxfp4> is the MXFP4 product (mxfp4.h) on the same pipeline:
+// blocks of 32 with E8M0 scales, so a scale word serves two K = 64 steps
+// (scale-factor ids 0 and 2) and a stage holds half the scale bytes; no global
+// scales; operands of any row and column count, the boxes zero-filled past
+// them and the K steps past the last 128-element group left out; BF16, FP16 or
+// FP32 output.  An output that a tensor map cannot describe (FP32, a row
+// stride or a base off 16 bytes) leaves through the same shared-memory slots
+// and coalesced stores.
+//
 // k_fc2_gemm<true> is FC1 with the SwiGLU producer's first pass in the
 // epilogue (nvfp4_fc1_swiglu).  W holds the gate rows then the up rows; a
 // pair tile takes 128 gate rows from CTA 0 and the matching 128 up rows
@@ -73,7 +82,7 @@
 #include <cstdio>
 #include <mutex>
 
-#include "common.cuh"
+#include "mx_gemm.cuh"
 
 namespace nvfp4 {
 namespace {
@@ -89,24 +98,39 @@ constexpr int A_BYTES = KT * KTILE_BYTES;      // this CTA's 128 A rows x KT k-t
 constexpr int B_BYTES = KT * KTILE_BYTES;      // this CTA's 128 W rows x KT k-tiles
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int KSTEPS = 4 * KT;                 // K=64 MMA steps per stage
-// Scale ring: per stage 4*KT blocks of 512 bytes for this CTA's A panel,
+// Scale ring: per stage STEPS blocks of 512 bytes for this CTA's A panel,
 // then the same for W panel 0 and W panel 1 of the tile.
 constexpr int SF_RING = 2;
-constexpr int SFA_BYTES = KSTEPS * 512;
-constexpr int SFW_PANEL_BYTES = KSTEPS * 512;
-constexpr int SF_STAGE_BYTES = SFA_BYTES + 2 * SFW_PANEL_BYTES;  // 12 KB
+// A block-scaled format: its scale blocks (512 bytes: 128 rows x 4 scales) per
+// stage, and what follows from them.
+template <int kSteps>
+struct ScaleShape {
+  static constexpr int STEPS = kSteps;
+  static constexpr int SFA_BYTES = kSteps * 512;
+  static constexpr int SFW_PANEL_BYTES = kSteps * 512;
+  static constexpr int SF_STAGE_BYTES = SFA_BYTES + 2 * SFW_PANEL_BYTES;  // NVFP4 12 KB, MXFP4 6 KB
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SF_RING * SF_STAGE_BYTES + 256;
+  static constexpr uint32_t SFW_COL = 4 * kSteps;
+  static constexpr uint32_t SF_SLOT_COLS = 12 * kSteps;
+};
+struct Nvfp4 : ScaleShape<KSTEPS> {  // blocks of 16: four scales a K = 64 step
+  static constexpr bool kMx = false;
+};
+struct Mxfp4 : ScaleShape<KSTEPS / 2> {  // blocks of 32: two
+  static constexpr bool kMx = true;
+};
 constexpr int EPI_WARPS = 8;  // two per TMEM lane quarter, 128 columns each
 constexpr int SF_WARPS = 4;
 constexpr int WARP_EPI0 = 2;
 constexpr int WARP_SF0 = WARP_EPI0 + EPI_WARPS;
 constexpr int WARP_SFP = WARP_SF0 + SF_WARPS;
 constexpr int BAR_BYTES = 256;
-constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SF_RING * SF_STAGE_BYTES + BAR_BYTES;
+static_assert(BAR_BYTES == 256, "SMEM_BYTES");
 constexpr int THREADS = (WARP_SFP + 1) * 32;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t ACC_COL = 0;  // 256 FP32 columns
-// Block scales in tensor memory, two slots used by alternate stages
-// (KSTEPS K=64 steps j each):
+// Block scales in tensor memory, two slots used by alternate stages (STEPS
+// scale blocks j each, one K=64 step of NVFP4, two of MXFP4):
 //   A: step j at columns slot + 4j .. + 3; the scales of accumulator row i
 //      are read from lane i, column slot + 4j + i/32, and only that column
 //      is written.
@@ -114,20 +138,20 @@ constexpr uint32_t ACC_COL = 0;  // 256 FP32 columns
 //      quarter g read the scales of W row n from lane 32g + n % 32, column
 //      slot + SFW_COL + 8j + n/32, so every quarter holds a copy.
 constexpr uint32_t SF_COL = 256;
-constexpr uint32_t SFW_COL = 4 * KSTEPS;
-constexpr uint32_t SF_SLOT_COLS = 12 * KSTEPS;
 constexpr int SF_SLOTS = 2;
-static_assert(SF_COL + SF_SLOTS * SF_SLOT_COLS <= TMEM_COLS, "tensor memory budget");
+static_assert(SF_COL + SF_SLOTS * Nvfp4::SF_SLOT_COLS <= TMEM_COLS, "tensor memory budget");
 static_assert(STAGES > SF_SLOTS, "a stage's scale slot is free once the stage SF_SLOTS back has completed");
 static_assert(KSTEPS == 8, "scale stores are written 32 columns at a time");
-static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-static_assert(STAGE_BYTES % 1024 == 0 && SF_STAGE_BYTES % 1024 == 0, "stage alignment");
+static_assert(Nvfp4::SMEM_BYTES <= 232448, "shared memory budget");
+static_assert(STAGE_BYTES % 1024 == 0 && Mxfp4::SF_STAGE_BYTES % 1024 == 0, "stage alignment");
 
 // Instruction descriptor, kind::mxf4nvf4: A and B E2M1 (format 1), both
 // K-major, UE4M3 scales (scale format 0), scale-factor ids 0, N>>3 at bit
 // 17, M>>4 at bit 24; M = 256 across the CTA pair.
 constexpr uint32_t kIdesc =
     (1u << 7) | (1u << 10) | (uint32_t(PAIR_N >> 3) << 17) | (uint32_t(PAIR_M >> 4) << 24);
+// The same with E8M0 scales (scale format 1); the step ors in its scale-factor ids.
+constexpr uint32_t kIdescMx = kIdesc | (1u << 23);
 
 // Shared-memory matrix descriptor for a K-major operand tile whose rows are
 // 128 bytes with the 128-byte swizzle: 8-row atoms 1024 bytes apart (SBO),
@@ -198,12 +222,13 @@ struct Smem {
   uint8_t* out_stage;   // the plain epilogue's output slots (k_fc2_gemm<false> only; the same bytes)
 };
 
+template <class F>
 __device__ __forceinline__ Smem carve(uint8_t* raw) {
   Smem s;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   s.stage = base;
   s.sf = base + STAGES * STAGE_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s.sf + SF_RING * SF_STAGE_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s.sf + SF_RING * F::SF_STAGE_BYTES);
   s.full = bars;
   s.full_kt1 = s.full + STAGES;
   s.empty = s.full_kt1 + STAGES;
@@ -219,11 +244,14 @@ __device__ __forceinline__ Smem carve(uint8_t* raw) {
   return s;
 }
 static_assert((3 * STAGES + 2 * SF_RING + 3) * 8 + 8 <= BAR_BYTES, "barrier area");
-static_assert(SMEM_BYTES + kSiluSmemBytes <= 232448, "shared memory budget of the SwiGLU epilogue");
+static_assert(Nvfp4::SMEM_BYTES + kSiluSmemBytes <= 232448, "shared memory budget of the SwiGLU epilogue");
 // the plain epilogue's output slots: one per warp, 32 rows x 16 BF16 columns
 constexpr int kOutSlotBytes = 32 * 16 * 2;
-static_assert(SMEM_BYTES + EPI_WARPS * kOutSlotBytes <= 232448, "shared memory budget of the plain epilogue");
-static_assert((SMEM_BYTES - 1024 - BAR_BYTES) % 1024 == 0 && BAR_BYTES % 128 == 0, "output slots 128-byte aligned");
+static_assert(Nvfp4::SMEM_BYTES + EPI_WARPS * kOutSlotBytes <= 232448, "shared memory budget of the plain epilogue");
+// MXFP4: 32 rows x 16 columns of up to 4 bytes
+constexpr int kMxSlotBytes = 32 * 16 * 4;
+static_assert(Mxfp4::SMEM_BYTES + EPI_WARPS * kMxSlotBytes <= 232448, "shared memory budget of the MXFP4 epilogue");
+static_assert((Nvfp4::SMEM_BYTES - 1024 - BAR_BYTES) % 1024 == 0 && BAR_BYTES % 128 == 0, "output slots 128-byte aligned");
 
 struct Params {
   const nvfp4_scale_rec* a_rec;
@@ -249,6 +277,11 @@ struct Params {
   // Diagnostic launches only (else null): block 0 writes {start ns, end ns,
   // start cycle, end cycle} of its run, globaltimer and its SM's clock64.
   uint64_t* clk;
+  // MXFP4 only: the output's element type, whether it leaves by TMA stores,
+  // and the K = 64 steps that hold data (twice the 128-element groups).
+  int dtype;
+  int tma_out;
+  int k_steps;
 };
 
 // Tile order: the N tiles are cut into groups of group_n; a group is walked
@@ -300,34 +333,37 @@ struct Ring {
 // panel and step).  In a ring slot (tiled layout, one 512-byte block per
 // step and panel): the A word at j*512 + 16l + 4q, the W line of panel h at
 // SFA_BYTES + h*SFW_PANEL_BYTES + j*512 + 16l.
+template <class F>
 struct ScaleWords {
-  uint32_t a[KSTEPS];
-  uint4 w[2 * KSTEPS];  // [2j + panel]
+  uint32_t a[F::STEPS];
+  uint4 w[2 * F::STEPS];  // [2j + panel]
 };
 
-__device__ __forceinline__ void read_scales(ScaleWords& v, const uint8_t* slot, int q, int lane) {
+template <class F>
+__device__ __forceinline__ void read_scales(ScaleWords<F>& v, const uint8_t* slot, int q, int lane) {
 #pragma unroll
-  for (int j = 0; j < KSTEPS; ++j) {
+  for (int j = 0; j < F::STEPS; ++j) {
     v.a[j] = *reinterpret_cast<const uint32_t*>(slot + j * 512 + lane * 16 + q * 4);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      v.w[2 * j + h] = *reinterpret_cast<const uint4*>(slot + SFA_BYTES + h * SFW_PANEL_BYTES + j * 512 + lane * 16);
+      v.w[2 * j + h] = *reinterpret_cast<const uint4*>(slot + F::SFA_BYTES + h * F::SFW_PANEL_BYTES + j * 512 + lane * 16);
   }
 }
 
 // A: a lane of quarter q reads only column 4j + q of step j, so the writer
 // of quarter q stores its word there alone (one column per step).
-__device__ __forceinline__ void store_scales(uint32_t taddr, const ScaleWords& v, int q) {
+template <class F>
+__device__ __forceinline__ void store_scales(uint32_t taddr, const ScaleWords<F>& v, int q) {
 #pragma unroll
-  for (int j = 0; j < KSTEPS; ++j)
+  for (int j = 0; j < F::STEPS; ++j)
     asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr + 4 * j + q), "r"(v.a[j]) : "memory");
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
+  for (int half = 0; half < F::STEPS / 4; ++half) {
     const uint4* x = v.w + 8 * half;
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
         "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr + SFW_COL + 32 * half),
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr + F::SFW_COL + 32 * half),
         "r"(x[0].x), "r"(x[0].y), "r"(x[0].z), "r"(x[0].w), "r"(x[1].x), "r"(x[1].y), "r"(x[1].z), "r"(x[1].w),
         "r"(x[2].x), "r"(x[2].y), "r"(x[2].z), "r"(x[2].w), "r"(x[3].x), "r"(x[3].y), "r"(x[3].z), "r"(x[3].w),
         "r"(x[4].x), "r"(x[4].y), "r"(x[4].z), "r"(x[4].w), "r"(x[5].x), "r"(x[5].y), "r"(x[5].z), "r"(x[5].w),
@@ -347,13 +383,62 @@ struct StageWalk {
   }
 };
 
-template <bool kGated>
+// MXFP4 output past the tensor map: the warp's 32 rows x 16 columns (lane l
+// holds row l, eight words) through its slot, two rows of 16 elements an
+// instruction.
+__device__ __forceinline__ void mx_store16(const Params& p, const uint32_t* w, uint8_t* slot, int y, int x, int lane) {
+  __syncwarp();
+  uint4* d = reinterpret_cast<uint4*>(slot + lane * 32);
+  d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  __syncwarp();
+  const int col = lane & 15, r0 = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int r = 2 * i + r0;
+    const uint16_t v = reinterpret_cast<const uint16_t*>(slot)[r * 16 + col];
+    if (y + r < p.m && x + col < p.n) reinterpret_cast<uint16_t*>(p.out)[int64_t(y + r) * p.ldo + x + col] = v;
+  }
+}
+
+// The same for FP32, straight from the accumulator (which is handed back
+// after it): 32 rows x 128 columns, 16 columns at a time.
+__device__ __forceinline__ void mx_store_fp32(const Params& p, uint32_t taddr, uint8_t* slot, int mt, int nt,
+                                              uint32_t rank, int q, int col0, int lane) {
+  const int y = mt * PAIR_M + int(rank) * HALF + q * 32, x0 = nt * PAIR_N + col0;
+  float* out = reinterpret_cast<float*>(p.out);
+#pragma unroll 1
+  for (int c = 0; c < 128; c += 32) {
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(taddr + c, r);
+    tc_wait_ld();
+    tmem_ld_fence_regs<32>(r);
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        reinterpret_cast<uint4*>(slot + lane * 64)[i] =
+            make_uint4(r[16 * hh + 4 * i], r[16 * hh + 4 * i + 1], r[16 * hh + 4 * i + 2], r[16 * hh + 4 * i + 3]);
+      __syncwarp();
+      const int col = lane & 15, r0 = lane >> 4, x = x0 + c + 16 * hh;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int row = 2 * i + r0;
+        const float v = reinterpret_cast<const float*>(slot)[row * 16 + col];
+        if (y + row < p.m && x + col < p.n) out[int64_t(y + row) * p.ldo + x + col] = v;
+      }
+    }
+  }
+}
+
+template <bool kGated, class F>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     k_fc2_gemm(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
                const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ CUtensorMap tmap_sw,
                const __grid_constant__ CUtensorMap tmap_out, const Params p) {
   extern __shared__ uint8_t smem_raw[];
-  const Smem sm = carve(smem_raw);
+  const Smem sm = carve<F>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
@@ -433,10 +518,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           mbar_arrive_expect_tx(&sm.full[r.slot], STAGE_BYTES);
           mbar_arrive_expect_tx(&sm.full_kt1[r.slot], STAGE_BYTES);
         }
-        tma_load_3d_pair(st, &tmap_a, full_leader, 0, a_row, w.ks * KT, pol_a);
-        tma_load_3d_pair(st + A_BYTES, &tmap_w, full_leader, 0, b_row, w.ks * KT, pol_w);
-        tma_load_3d_pair(st + KTILE_BYTES, &tmap_a, kt1_leader, 0, a_row, w.ks * KT + 1, pol_a);
-        tma_load_3d_pair(st + A_BYTES + KTILE_BYTES, &tmap_w, kt1_leader, 0, b_row, w.ks * KT + 1, pol_w);
+        if constexpr (F::kMx) {
+          // [row][bytes of the row]: a row may end inside a k-tile
+          const int x = w.ks * KT * BK_BYTES;
+          tma_load_2d_pair(st, &tmap_a, full_leader, x, a_row, pol_a);
+          tma_load_2d_pair(st + A_BYTES, &tmap_w, full_leader, x, b_row, pol_w);
+          tma_load_2d_pair(st + KTILE_BYTES, &tmap_a, kt1_leader, x + BK_BYTES, a_row, pol_a);
+          tma_load_2d_pair(st + A_BYTES + KTILE_BYTES, &tmap_w, kt1_leader, x + BK_BYTES, b_row, pol_w);
+        } else {
+          tma_load_3d_pair(st, &tmap_a, full_leader, 0, a_row, w.ks * KT, pol_a);
+          tma_load_3d_pair(st + A_BYTES, &tmap_w, full_leader, 0, b_row, w.ks * KT, pol_w);
+          tma_load_3d_pair(st + KTILE_BYTES, &tmap_a, kt1_leader, 0, a_row, w.ks * KT + 1, pol_a);
+          tma_load_3d_pair(st + A_BYTES + KTILE_BYTES, &tmap_w, kt1_leader, 0, b_row, w.ks * KT + 1, pol_w);
+        }
       }
     }
   } else if (warp == WARP_SFP) {
@@ -462,16 +556,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // Rows past K (an odd k-tile count) or past the operand are read
         // as whatever the box holds or zero fill and never multiplied or
         // stored.
-        uint8_t* sl = sm.sf + r.slot * SF_STAGE_BYTES;
-        const int row0 = w.ks * KSTEPS * 2;  // two 256-byte rows per 512-byte block
-        mbar_arrive_expect_tx(&sm.sf_full[r.slot], SF_STAGE_BYTES);
+        uint8_t* sl = sm.sf + r.slot * F::SF_STAGE_BYTES;
+        const int row0 = w.ks * F::STEPS * 2;  // two 256-byte rows per 512-byte block
+        mbar_arrive_expect_tx(&sm.sf_full[r.slot], F::SF_STAGE_BYTES);
         tma_load_2d(sl, &tmap_sa, &sm.sf_full[r.slot], 0, (mt * 2 + int(rank)) * p.sf_rows + row0, pol_a);
         if constexpr (kGated) {
           // the gate and the up panel of the tile, one box each
-          tma_load_3d(sl + SFA_BYTES, &tmap_sw, &sm.sf_full[r.slot], 0, row0, nt, pol_w);
-          tma_load_3d(sl + SFA_BYTES + SFW_PANEL_BYTES, &tmap_sw, &sm.sf_full[r.slot], 0, row0, p.f / HALF + nt, pol_w);
+          tma_load_3d(sl + F::SFA_BYTES, &tmap_sw, &sm.sf_full[r.slot], 0, row0, nt, pol_w);
+          tma_load_3d(sl + F::SFA_BYTES + F::SFW_PANEL_BYTES, &tmap_sw, &sm.sf_full[r.slot], 0, row0, p.f / HALF + nt, pol_w);
         } else {
-          tma_load_3d(sl + SFA_BYTES, &tmap_sw, &sm.sf_full[r.slot], 0, row0, nt * 2, pol_w);
+          tma_load_3d(sl + F::SFA_BYTES, &tmap_sw, &sm.sf_full[r.slot], 0, row0, nt * 2, pol_w);
         }
       }
     }
@@ -496,7 +590,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           tc_fence_after();
           const uint32_t st = smem_u32(sm.stage + ab.slot * STAGE_BYTES);
-          const uint32_t sf_tmem = tmem + SF_COL + uint32_t(sf_slot) * SF_SLOT_COLS;
+          const uint32_t sf_tmem = tmem + SF_COL + uint32_t(sf_slot) * F::SF_SLOT_COLS;
           const int kk_end = (ks * KT + KT <= nk) ? KT : nk - ks * KT;
 #pragma unroll
           for (int kk = 0; kk < KT; ++kk) {
@@ -514,8 +608,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               // K step j: 64 elements = 32 bytes further along the swizzled row
-              tc_mma_pair_nvf4(tmem + ACC_COL, a_desc + 2 * j, b_desc + 2 * j, kIdesc, sf_tmem + 4 * (4 * kk + j),
-                               sf_tmem + SFW_COL + 8 * (4 * kk + j), (ks | kk | j) != 0);
+              if constexpr (F::kMx) {
+                if ((ks * KT + kk) * 4 + j >= p.k_steps) break;  // past the last group
+                // two steps share a scale block: its bytes 0, 1 and 2, 3 of each word
+                const int sb = 2 * kk + j / 2;
+                const uint32_t id = kIdescMx | (uint32_t(2 * (j & 1)) << 4) | (uint32_t(2 * (j & 1)) << 29);
+                tc_mma_pair_mxf4(tmem + ACC_COL, a_desc + 2 * j, b_desc + 2 * j, id, sf_tmem + 4 * sb,
+                                 sf_tmem + F::SFW_COL + 8 * sb, (ks | kk | j) != 0);
+              } else {
+                tc_mma_pair_nvf4(tmem + ACC_COL, a_desc + 2 * j, b_desc + 2 * j, kIdesc, sf_tmem + 4 * (4 * kk + j),
+                                 sf_tmem + F::SFW_COL + 8 * (4 * kk + j), (ks | kk | j) != 0);
+              }
             }
           }
           if (!ok) break;
@@ -532,8 +635,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3;  // TMEM lane quarter this warp may access
     const int col0 = ((warp - WARP_EPI0) / 4) * (PAIR_N / 2);  // this warp's half of the columns
-    uint8_t* out_slot = sm.out_stage + (warp - WARP_EPI0) * kOutSlotBytes;  // plain epilogue only
-    const float alpha = __fmul_rn(p.a_rec->global_scale, p.w_rec->global_scale);
+    uint8_t* out_slot = sm.out_stage + (warp - WARP_EPI0) * (F::kMx ? kMxSlotBytes : kOutSlotBytes);  // plain epilogue only
+    float alpha = 1.0f;
+    if constexpr (!F::kMx) alpha = __fmul_rn(p.a_rec->global_scale, p.w_rec->global_scale);
     const uint32_t tempty_leader = mapa_shared(smem_u32(sm.tempty), 0);
     // the output is written once and never read back here: evict it first,
     // so that it does not push the activation panels and the weight out of L2
@@ -620,6 +724,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         break;
       }
       tc_fence_after();
+      if constexpr (F::kMx) {
+        if (p.dtype == MXFP4_FP32) {
+          mx_store_fp32(p, tmem + (uint32_t(q * 32) << 16) + ACC_COL + col0, out_slot, mt, nt, rank, q, col0, lane);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader);
+          continue;
+        }
+      }
       // The warp's 32 rows x 128 columns into registers as BF16 pairs, the
       // accumulator back to the issuer, then the output through the warp's
       // shared-memory slot and TMA stores.  Row-per-lane global stores
@@ -635,8 +748,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         tc_wait_ld();
         tmem_ld_fence_regs<32>(r);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          wb[c][i] = bf16x2_rn(__fmul_rn(__uint_as_float(r[2 * i]), alpha), __fmul_rn(__uint_as_float(r[2 * i + 1]), alpha));
+        for (int i = 0; i < 16; ++i) {
+          if constexpr (F::kMx)
+            wb[c][i] = p.dtype == MXFP4_FP16
+                           ? f32_to_word<__half>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]))
+                           : bf16x2_rn(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+          else
+            wb[c][i] =
+                bf16x2_rn(__fmul_rn(__uint_as_float(r[2 * i]), alpha), __fmul_rn(__uint_as_float(r[2 * i + 1]), alpha));
+        }
       }
       // accumulator drained: hand it back to the MMA issuer of the pair (the
       // loads are complete: wait::ld, fence::before_thread_sync)
@@ -648,6 +768,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // until the previous store has read the slot
       const int y = mt * PAIR_M + int(rank) * HALF + q * 32;
       const int x0 = nt * PAIR_N + col0;
+      if constexpr (F::kMx) {
+        if (!p.tma_out) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) mx_store16(p, wb[c] + 8 * hh, out_slot, y, x0 + c * 32 + hh * 16, lane);
+          }
+          continue;
+        }
+      }
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
 #pragma unroll
@@ -689,8 +819,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // The next TMA into the slot writes through the async proxy: the
       // proxy fence orders these generic-proxy reads before it (without it
       // the refill was seen to race the reads).
-      ScaleWords v;
-      read_scales(v, sm.sf + sr.slot * SF_STAGE_BYTES, q, lane);
+      ScaleWords<F> v;
+      read_scales<F>(v, sm.sf + sr.slot * F::SF_STAGE_BYTES, q, lane);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.sf_empty[sr.slot]);
@@ -702,7 +832,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         back.next(STAGES);
       }
       tc_fence_after();
-      store_scales(tmem + lane_base + SF_COL + uint32_t(sf_slot) * SF_SLOT_COLS, v, q);
+      store_scales<F>(tmem + lane_base + SF_COL + uint32_t(sf_slot) * F::SF_SLOT_COLS, v, q);
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -774,22 +904,23 @@ namespace {
 // where the GPCs cannot all hold pairs), cached per device and variant.
 // The persistent grid is sized to this so that no pair waits for a second
 // wave.
-nvfp4_status resident_pairs(bool gated, int smem, int* pairs) {
+using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, Params);
+nvfp4_status resident_pairs(int variant, Kernel kernel, int smem, int* pairs) {
   static std::mutex mu;
-  static int cache[64][2] = {};
+  static int cache[64][3] = {};
   int dev = 0;
   nvfp4_status st = cuda_check(cudaGetDevice(&dev), "cudaGetDevice");
   if (st != NVFP4_OK) return st;
   if (dev < 0 || dev >= 64) return fail(NVFP4_EUNSUPPORTED, "device ordinal above 63");
   std::lock_guard<std::mutex> lock(mu);
-  int& c = cache[dev][gated ? 1 : 0];
+  int& c = cache[dev][variant];
   if (c == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (sm_count() / 2));
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     int clusters = 0;
-    st = cuda_check(cudaOccupancyMaxActiveClusters(&clusters, gated ? k_fc2_gemm<true> : k_fc2_gemm<false>, &cfg),
+    st = cuda_check(cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg),
                     "cudaOccupancyMaxActiveClusters(k_fc2_gemm)");
     if (st != NVFP4_OK) return st;
     if (clusters < 1) return fail(NVFP4_ECUDA, "k_fc2_gemm: no two-CTA cluster fits on this device");
@@ -918,18 +1049,88 @@ nvfp4_status gemm_launch(const void* a_q, const void* a_s, const nvfp4_scale_rec
     if (st != NVFP4_OK) return st;
   }
 
-  auto kernel = gated ? k_fc2_gemm<true> : k_fc2_gemm<false>;
-  const int smem = gated ? SMEM_BYTES + kSiluSmemBytes : SMEM_BYTES + EPI_WARPS * kOutSlotBytes;
+  prm.dtype = MXFP4_BF16;
+  prm.tma_out = 1;
+  prm.k_steps = 0;
+  auto kernel = gated ? k_fc2_gemm<true, Nvfp4> : k_fc2_gemm<false, Nvfp4>;
+  const int smem = gated ? Nvfp4::SMEM_BYTES + kSiluSmemBytes : Nvfp4::SMEM_BYTES + EPI_WARPS * kOutSlotBytes;
   st = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
                   "cudaFuncSetAttribute(k_fc2_gemm)");
   if (st != NVFP4_OK) return st;
   const int tiles = prm.num_m_tiles * prm.num_n_tiles;
   int max_pairs = 0;
-  st = resident_pairs(gated, smem, &max_pairs);
+  st = resident_pairs(gated ? 1 : 0, kernel, smem, &max_pairs);
   if (st != NVFP4_OK) return st;
   const int pairs = tiles < max_pairs ? tiles : max_pairs;
   kernel<<<2 * pairs, THREADS, smem, stream>>>(ta, tw, tsa, tsw, tout, prm);
   return cuda_check(cudaGetLastError(), "launch k_fc2_gemm");
+}
+
+// The MXFP4 product (the caller has checked the arguments).
+nvfp4_status mx_pairs(const void* a_q, const void* a_s, const void* w_q, const void* w_s, int64_t m, int64_t n,
+                      int64_t k, void* out, int32_t dtype, int64_t ldo, uint32_t* dev_status, cudaStream_t stream) {
+  const int64_t groups = mxfp4_padded_cols(k) / 128;
+  CUtensorMap ta, tw, tsa, tsw, tout = {};
+  nvfp4_status st = mx_operand_map(&ta, a_q, m, k, HALF, "A");
+  if (st == NVFP4_OK) st = mx_operand_map(&tw, w_q, n, k, HALF, "W");
+  if (st != NVFP4_OK) return st;
+  {
+    const cuuint64_t dims[2] = {256, cuuint64_t(mxfp4_scale_bytes(m, k) / 256)};
+    const cuuint64_t strides[1] = {256};
+    const cuuint32_t box[2] = {256, 2 * Mxfp4::STEPS};
+    if ((st = make_map(&tsa, CU_TENSOR_MAP_DATA_TYPE_UINT8, a_s, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE,
+                       "A scales")) != NVFP4_OK)
+      return st;
+  }
+  {
+    const cuuint64_t dims[3] = {256, cuuint64_t(groups * 2), cuuint64_t((n + HALF - 1) / HALF)};
+    const cuuint64_t strides[2] = {256, cuuint64_t(groups) * 512};
+    const cuuint32_t box[3] = {256, 2 * Mxfp4::STEPS, 2};
+    if ((st = make_map(&tsw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_s, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE,
+                       "W scales")) != NVFP4_OK)
+      return st;
+  }
+  Params prm = {};
+  // a TMA store clips whole 16-byte units: a ragged last unit would be written in full
+  prm.tma_out = dtype != MXFP4_FP32 && aligned16(out) && ldo % 8 == 0 && n % 8 == 0;
+  if (prm.tma_out) {
+    const cuuint64_t dims[2] = {cuuint64_t(n), cuuint64_t(m)};
+    const cuuint64_t strides[1] = {cuuint64_t(ldo) * 2};
+    const cuuint32_t box[2] = {16, 32};
+    if ((st = make_map(&tout, CU_TENSOR_MAP_DATA_TYPE_UINT16, out, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE,
+                       "output")) != NVFP4_OK)
+      return st;
+  }
+  prm.out = static_cast<__nv_bfloat16*>(out);
+  prm.ldo = ldo;
+  prm.dtype = dtype;
+  prm.m = static_cast<int>(m);
+  prm.n = static_cast<int>(n);
+  prm.num_m_tiles = static_cast<int>((m + PAIR_M - 1) / PAIR_M);
+  prm.num_n_tiles = static_cast<int>((n + PAIR_N - 1) / PAIR_N);
+  {
+    // as gemm_launch: a weight of up to 48 MB in one group, else groups of 16 MB
+    const int64_t tile_bytes = int64_t(PAIR_N) * groups * 68;
+    const int64_t g =
+        tile_bytes * prm.num_n_tiles <= (int64_t(48) << 20) ? prm.num_n_tiles : (int64_t(16) << 20) / tile_bytes;
+    prm.group_n = static_cast<int>(g < 1 ? 1 : (g > prm.num_n_tiles ? prm.num_n_tiles : g));
+  }
+  prm.num_k_tiles = static_cast<int>((groups + 1) / 2);
+  prm.k_steps = static_cast<int>(groups * 2);
+  prm.sf_rows = static_cast<int>(groups * 2);
+  prm.dev_status = dev_status;
+  prm.wait_limit_cycles = kMxWaitLimitCycles;
+  auto kernel = k_fc2_gemm<false, Mxfp4>;
+  constexpr int smem = Mxfp4::SMEM_BYTES + EPI_WARPS * kMxSlotBytes;
+  static std::atomic<uint64_t> ready{0};
+  if ((st = allow_smem(reinterpret_cast<const void*>(kernel), smem, ready)) != NVFP4_OK) return st;
+  const int64_t tiles = int64_t(prm.num_m_tiles) * prm.num_n_tiles;
+  if (tiles > 0x7FFFFFFF) return fail(NVFP4_EUNSUPPORTED, "mxfp4_gemm: problem too large");
+  int max_pairs = 0;
+  if ((st = resident_pairs(2, kernel, smem, &max_pairs)) != NVFP4_OK) return st;
+  const int pairs = tiles < max_pairs ? static_cast<int>(tiles) : max_pairs;
+  kernel<<<2 * pairs, THREADS, smem, stream>>>(ta, tw, tsa, tsw, tout, prm);
+  return cuda_check(cudaGetLastError(), "launch k_fc2_gemm<Mxfp4>");
 }
 
 // ---- diagnostics: the bounded wait on a barrier nothing arrives at ---------

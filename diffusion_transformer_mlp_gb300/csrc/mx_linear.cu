@@ -31,6 +31,12 @@ nvfp4_status check_product(const void* w_q, const void* w_s, int64_t m, int64_t 
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
+nvfp4_status product(const void* a_q, const void* a_s, const void* w_q, const void* w_s, int64_t m, int64_t n,
+                     int64_t k, void* out, int32_t dtype, int64_t ldo, uint32_t* dev_status, nvfp4_stream_t stream) {
+  auto kernel = m <= 128 ? mx_rows : mx_pairs;
+  return kernel(a_q, a_s, w_q, w_s, m, n, k, out, dtype, ldo, dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 }  // namespace nvfp4
 
@@ -44,7 +50,7 @@ extern "C" nvfp4_status mxfp4_gemm(const void* a_q, const void* a_s, const void*
   const nvfp4_status st = check_product(w_q, w_s, m, n, k, out, dtype, ldo, nm);
   if (st != NVFP4_OK) return st;
   if (!aligned16(a_q) || !aligned16(a_s)) return fail(NVFP4_EALIGN, nm + ": operands must be 16-byte aligned");
-  return mx_rows(a_q, a_s, w_q, w_s, m, n, k, out, dtype, ldo, dev_status, reinterpret_cast<cudaStream_t>(stream));
+  return product(a_q, a_s, w_q, w_s, m, n, k, out, dtype, ldo, dev_status, stream);
 }
 
 extern "C" int64_t mxfp4_linear_workspace_bytes(int64_t m, int64_t k) {
@@ -69,5 +75,5 @@ extern "C" nvfp4_status mxfp4_linear(const void* x, int32_t x_dtype, int64_t m, 
   uint8_t* a_q = static_cast<uint8_t*>(workspace);
   uint8_t* a_s = a_q + align256(mxfp4_qdata_bytes(m, k));
   if ((st = mxfp4_quantize(x, x_dtype, m, k, ldx, a_q, a_s, stream)) != NVFP4_OK) return st;
-  return mx_rows(a_q, a_s, w_q, w_s, m, n, k, out, dtype, ldo, dev_status, reinterpret_cast<cudaStream_t>(stream));
+  return product(a_q, a_s, w_q, w_s, m, n, k, out, dtype, ldo, dev_status, stream);
 }

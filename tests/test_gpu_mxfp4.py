@@ -165,7 +165,7 @@ def test_gemm_exact_when_sums_are_exact(m, n, k):
         assert torch.equal(fc2.mxfp4_gemm(a, b, dtype=dtype), ref.to(dtype))
 
 
-@pytest.mark.parametrize("m,n", [(5, 333), (200, 400), (600, 391)])
+@pytest.mark.parametrize("m,n", [(5, 333), (200, 400), (600, 391), (300, 392), (257, 520)])
 def test_gemm_output_view_leaves_the_rest(m, n):
     k = 320
     x, w = rnd((m, k), 1), rnd((n, k), 2)

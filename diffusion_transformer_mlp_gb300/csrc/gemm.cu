@@ -477,6 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync();  // barriers of both CTAs initialised, tensor memory allocated in both
   tc_fence_after();
   const uint32_t tmem = *sm.tmem_slot;
+  if constexpr (F::kMx) grid_wait();
   if (p.clk != nullptr && blockIdx.x == 0 && threadIdx.x == 0) {
     p.clk[0] = globaltimer_ns();
     p.clk[2] = clock64();
@@ -1129,8 +1130,8 @@ nvfp4_status mx_pairs(const void* a_q, const void* a_s, const void* w_q, const v
   int max_pairs = 0;
   if ((st = resident_pairs(2, kernel, smem, &max_pairs)) != NVFP4_OK) return st;
   const int pairs = tiles < max_pairs ? static_cast<int>(tiles) : max_pairs;
-  kernel<<<2 * pairs, THREADS, smem, stream>>>(ta, tw, tsa, tsw, tout, prm);
-  return cuda_check(cudaGetLastError(), "launch k_fc2_gemm<Mxfp4>");
+  return launch("launch k_fc2_gemm<Mxfp4>", kernel, dim3(unsigned(2 * pairs)), dim3(THREADS), smem, 0, stream, ta, tw, tsa,
+                tsw, tout, prm);
 }
 
 // ---- diagnostics: the bounded wait on a barrier nothing arrives at ---------

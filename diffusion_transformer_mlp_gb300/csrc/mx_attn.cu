@@ -9,6 +9,7 @@ namespace nvfp4 {
 
 nvfp4_status check_cache(const mxfp4_cache* cache, int* page_shift, const std::string& nm);
 int64_t attn_stream_workspace(int32_t dim);
+nvfp4_status attn_chunk(const mxfp4_cache* cache, const AttnParams& p, int32_t max_queries, cudaStream_t stream);
 nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32_t max_queries, void* workspace,
                          cudaStream_t stream);
 
@@ -66,5 +67,7 @@ extern "C" nvfp4_status mxfp4_cache_attention(const mxfp4_cache* cache, const mx
   p.o_vec = aligned16(g.out) && g.o_st % 8 == 0 && g.o_sh % 8 == 0;
   p.scale_log2 = g.scale * 1.4426950408889634f;
   p.wait_limit_cycles = kAttnWaitLimitCycles;
+  if (int64_t(g.max_queries) * group > 16)
+    return attn_chunk(cache, p, g.max_queries, reinterpret_cast<cudaStream_t>(stream));
   return attn_stream(cache, p, g.max_queries, g.workspace, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
   }
+  grid_wait();
   // tiles before each sequence: every thread sums a run of sequences, the
   // first warp scans the runs' sums
   {
@@ -337,8 +338,6 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
       for (int b = threadIdx.x; b <= a.seqs; b += kThreads) sp.prefix[b] = prefix[b];
   }
 
-  // k_attn_combine may be set up from here on; it waits for this grid's end
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t total = prefix[a.seqs];
   // the first workers lie in different blocks: few tiles spread over all SMs
   const int32_t worker = warp * int32_t(gridDim.x) + int32_t(blockIdx.x);
@@ -870,7 +869,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_c
   __shared__ float weight[kMostParts / 8][kRows];
   __shared__ float red_m[kCombineThreads / 32][kRows], row_m[kRows], row_l[kRows];
   __shared__ float4 sum[kSlices > 1 ? (kSlices - 1) * kPass * 2 : 1];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are written
+  grid_wait();
   const int32_t h = blockIdx.x, rt = blockIdx.y, b = blockIdx.z;
   const int32_t len = a.lens[b], nq = seq_queries(a, b);
   const int32_t q0 = a.q_starts != nullptr ? a.q_starts[b] : b;
@@ -971,20 +970,12 @@ nvfp4_status stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, const S
   if (st != NVFP4_OK) return st;
   StreamParams p = sp;
   p.workers = T::kCtas * sm_count() * kWarps;
-  kern<<<p.workers / kWarps, kThreads, T::kSmem, stream>>>(tk, tv, p);
-  if ((st = cuda_check(cudaGetLastError(), "launch k_attn_stream")) != NVFP4_OK) return st;
-  // launched while the stream kernel drains; it waits for it at its start
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(p.a.kv_heads), unsigned(row_tiles), unsigned(p.a.seqs));
-  cfg.blockDim = dim3(kCombineThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, k_attn_combine<D, kRows>, static_cast<const StreamParams>(p)),
-                    "launch k_attn_combine");
+  st = launch("launch k_attn_stream", kern, dim3(unsigned(p.workers / kWarps)), dim3(kThreads), T::kSmem, 0, stream, tk,
+              tv, p);
+  if (st != NVFP4_OK) return st;
+  return launch("launch k_attn_combine", k_attn_combine<D, kRows>,
+                dim3(unsigned(p.a.kv_heads), unsigned(row_tiles), unsigned(p.a.seqs)), dim3(kCombineThreads), 0, 0,
+                stream, p);
 }
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }

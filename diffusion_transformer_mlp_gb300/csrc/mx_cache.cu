@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(kThreads)
     k_mx_cache_write(const T* __restrict__ k, const T* __restrict__ v, int64_t k_st, int64_t k_sh, int64_t v_st,
                      int64_t v_sh, const int64_t* __restrict__ slots, int64_t tokens, uint8_t* __restrict__ kc,
                      uint8_t* __restrict__ ks, uint8_t* __restrict__ vc, uint8_t* __restrict__ vs, const CacheDims c) {
+  grid_wait();
   const bool is_v = blockIdx.y != 0;
   const T* x = is_v ? v : k;
   const int64_t st = is_v ? v_st : k_st, sh = is_v ? v_sh : k_sh;
@@ -88,6 +89,7 @@ __global__ void __launch_bounds__(kThreads)
                     T* __restrict__ v, const uint8_t* __restrict__ kc, const uint8_t* __restrict__ ks,
                     const uint8_t* __restrict__ vc, const uint8_t* __restrict__ vs, const CacheDims c) {
   __shared__ int64_t base[kReadTokens];  // row of (page, head 0, offset)
+  grid_wait();
   const int64_t t0 = int64_t(blockIdx.x) * chunk;
   const int32_t n = int32_t(total - t0 < chunk ? total - t0 : chunk);
   if (threadIdx.x < n) {
@@ -151,7 +153,7 @@ nvfp4_status check_cache(const mxfp4_cache* cache, int* page_shift, const std::s
 namespace {
 
 template <typename T>
-void write_launch(const mxfp4_cache* cache, const CacheDims& c, const void* k, const void* v, int64_t tokens,
+nvfp4_status write_launch(const mxfp4_cache* cache, const CacheDims& c, const void* k, const void* v, int64_t tokens,
                   int64_t k_st, int64_t k_sh, int64_t v_st, int64_t v_sh, const int64_t* slots, cudaStream_t s) {
   constexpr int64_t el = 16 / sizeof(T);
   const bool vec = aligned16(k) && aligned16(v) && k_st % el == 0 && k_sh % el == 0 && v_st % el == 0 && v_sh % el == 0;
@@ -159,21 +161,22 @@ void write_launch(const mxfp4_cache* cache, const CacheDims& c, const void* k, c
   const int64_t blocks = (items + kThreads - 1) / kThreads, most = int64_t(sm_count()) * 8;
   const dim3 grid(unsigned(blocks < most ? blocks : most), 2);
   auto kern = vec ? k_mx_cache_write<T, true> : k_mx_cache_write<T, false>;
-  kern<<<grid, kThreads, 0, s>>>(static_cast<const T*>(k), static_cast<const T*>(v), k_st, k_sh, v_st, v_sh, slots,
-                                 tokens, static_cast<uint8_t*>(cache->k_codes), static_cast<uint8_t*>(cache->k_scales),
-                                 static_cast<uint8_t*>(cache->v_codes), static_cast<uint8_t*>(cache->v_scales), c);
+  return launch("launch k_mx_cache_write", kern, grid, dim3(kThreads), 0, 0, s, static_cast<const T*>(k),
+                static_cast<const T*>(v), k_st, k_sh, v_st, v_sh, slots, tokens,
+                static_cast<uint8_t*>(cache->k_codes), static_cast<uint8_t*>(cache->k_scales),
+                static_cast<uint8_t*>(cache->v_codes), static_cast<uint8_t*>(cache->v_scales), c);
 }
 
 template <typename T>
-void read_launch(const mxfp4_cache* cache, const CacheDims& c, const int32_t* table, int64_t table_ld, int64_t seqs,
+nvfp4_status read_launch(const mxfp4_cache* cache, const CacheDims& c, const int32_t* table, int64_t table_ld, int64_t seqs,
                  const int32_t* starts, int64_t total, void* k, void* v, cudaStream_t s) {
   int64_t chunk = total / (int64_t(sm_count()) * 8);
   chunk = chunk < 1 ? 1 : (chunk > kReadTokens ? kReadTokens : chunk);
   const int64_t blocks = (total + chunk - 1) / chunk;
-  k_mx_cache_read<T><<<unsigned(blocks), kThreads, 0, s>>>(
-      table, table_ld, int32_t(seqs), starts, total, int32_t(chunk), static_cast<T*>(k), static_cast<T*>(v),
-      static_cast<const uint8_t*>(cache->k_codes), static_cast<const uint8_t*>(cache->k_scales),
-      static_cast<const uint8_t*>(cache->v_codes), static_cast<const uint8_t*>(cache->v_scales), c);
+  return launch("launch k_mx_cache_read", k_mx_cache_read<T>, dim3(unsigned(blocks)), dim3(kThreads), 0, 0, s, table,
+                table_ld, int32_t(seqs), starts, total, int32_t(chunk), static_cast<T*>(k), static_cast<T*>(v),
+                static_cast<const uint8_t*>(cache->k_codes), static_cast<const uint8_t*>(cache->k_scales),
+                static_cast<const uint8_t*>(cache->v_codes), static_cast<const uint8_t*>(cache->v_scales), c);
 }
 
 }  // namespace
@@ -199,10 +202,9 @@ extern "C" nvfp4_status mxfp4_cache_write(const mxfp4_cache* cache, const void* 
     return fail(NVFP4_EALIGN, nm + ": k, v and slots must be aligned to their elements");
   const CacheDims c{cache->pages, sh, cache->kv_heads, cache->dim};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == MXFP4_BF16) write_launch<__nv_bfloat16>(cache, c, k, v, tokens, k_st, k_sh, v_st, v_sh, slots, s);
-  else if (dtype == MXFP4_FP16) write_launch<__half>(cache, c, k, v, tokens, k_st, k_sh, v_st, v_sh, slots, s);
-  else write_launch<float>(cache, c, k, v, tokens, k_st, k_sh, v_st, v_sh, slots, s);
-  return cuda_check(cudaGetLastError(), "launch k_mx_cache_write");
+  if (dtype == MXFP4_BF16) return write_launch<__nv_bfloat16>(cache, c, k, v, tokens, k_st, k_sh, v_st, v_sh, slots, s);
+  if (dtype == MXFP4_FP16) return write_launch<__half>(cache, c, k, v, tokens, k_st, k_sh, v_st, v_sh, slots, s);
+  return write_launch<float>(cache, c, k, v, tokens, k_st, k_sh, v_st, v_sh, slots, s);
 }
 
 extern "C" nvfp4_status mxfp4_cache_read(const mxfp4_cache* cache, const int32_t* table, int64_t table_ld,
@@ -223,8 +225,7 @@ extern "C" nvfp4_status mxfp4_cache_read(const mxfp4_cache* cache, const int32_t
     return fail(NVFP4_EALIGN, nm + ": k and v must be 16-byte aligned, table and starts aligned to their elements");
   const CacheDims c{cache->pages, sh, cache->kv_heads, cache->dim};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == MXFP4_BF16) read_launch<__nv_bfloat16>(cache, c, table, table_ld, seqs, starts, total, k, v, s);
-  else if (dtype == MXFP4_FP16) read_launch<__half>(cache, c, table, table_ld, seqs, starts, total, k, v, s);
-  else read_launch<float>(cache, c, table, table_ld, seqs, starts, total, k, v, s);
-  return cuda_check(cudaGetLastError(), "launch k_mx_cache_read");
+  if (dtype == MXFP4_BF16) return read_launch<__nv_bfloat16>(cache, c, table, table_ld, seqs, starts, total, k, v, s);
+  if (dtype == MXFP4_FP16) return read_launch<__half>(cache, c, table, table_ld, seqs, starts, total, k, v, s);
+  return read_launch<float>(cache, c, table, table_ld, seqs, starts, total, k, v, s);
 }

@@ -31,6 +31,35 @@ inline nvfp4_status allow_smem(const void* kernel, int bytes, std::atomic<uint64
   return st;
 }
 
+// Launches `kernel` so that it may be set up while the kernel before it in the
+// stream drains (programmatic dependent launch).  Every kernel launched this
+// way calls grid_wait() before it touches global memory: it waits until the
+// kernel before it has ended and its writes are visible, so that the order of
+// the stream holds.  Back to back launches of small kernels come 1-2 us closer.
+// No kernel lets the next one start before its own blocks end: waiting blocks
+// then held places on the SMs (decoding a batch took 128 us instead of 92).
+template <class... Params, class... Args>
+nvfp4_status launch(const char* what, void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, int cluster,
+                    cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...), what);
+}
+
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 inline int mx_elem_bytes(int32_t dtype) { return dtype == MXFP4_FP32 ? 4 : 2; }
 inline bool mx_dtype_ok(int32_t dtype) { return dtype == MXFP4_BF16 || dtype == MXFP4_FP16 || dtype == MXFP4_FP32; }
 
@@ -155,6 +184,24 @@ __device__ __forceinline__ uint2 mx_encode_half(float (&f)[16], uint32_t& scale)
 #pragma unroll
   for (int i = 0; i < 16; ++i) f[i] *= inv;
   return make_uint2(e2m1x8(f), e2m1x8(f + 8));
+}
+
+// A whole block in one lane: its 32 codes and its scale code.
+__device__ __forceinline__ uint4 mx_encode_block(float (&f)[32], uint32_t& scale) {
+  float am = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) am = max_nan(am, fabsf(f[i]));
+  const uint32_t eb = (__float_as_uint(am) >> 23) & 0xFFu;
+  if (eb == 255u) {
+    scale = 255u;
+    return make_uint4(0u, 0u, 0u, 0u);
+  }
+  const uint32_t e = eb > 2u ? eb - 2u : 0u;
+  scale = e;
+  const float inv = __uint_as_float((254u - e) << 23);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] *= inv;
+  return make_uint4(e2m1x8(f), e2m1x8(f + 8), e2m1x8(f + 16), e2m1x8(f + 24));
 }
 
 // The eight E2M1 values of a word as four pairs of FP16 (exact).

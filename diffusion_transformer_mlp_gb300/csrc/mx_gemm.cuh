@@ -42,6 +42,12 @@ nvfp4_status make_map(CUtensorMap* map, CUtensorMapDataType dt, const void* base
 nvfp4_status mx_rows(const void* a_q, const void* a_s, const void* w_q, const void* w_s, int64_t m, int64_t n,
                      int64_t k, void* out, int32_t dtype, int64_t ldo, uint32_t* dev_status, cudaStream_t stream);
 
+// The same for up to kMxRowsX rows of x before quantisation.
+constexpr int64_t kMxRowsX = 32;
+nvfp4_status mx_rows_x(const void* x, int32_t x_dtype, int64_t ldx, const void* w_q, const void* w_s, int64_t m,
+                       int64_t n, int64_t k, void* out, int32_t dtype, int64_t ldo, uint32_t* dev_status,
+                       cudaStream_t stream);
+
 // The CTA-pair kernel (gemm.cu).
 nvfp4_status mx_pairs(const void* a_q, const void* a_s, const void* w_q, const void* w_s, int64_t m, int64_t n,
                       int64_t k, void* out, int32_t dtype, int64_t ldo, uint32_t* dev_status, cudaStream_t stream);

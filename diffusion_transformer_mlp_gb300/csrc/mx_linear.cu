@@ -33,7 +33,14 @@ int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
 nvfp4_status product(const void* a_q, const void* a_s, const void* w_q, const void* w_s, int64_t m, int64_t n,
                      int64_t k, void* out, int32_t dtype, int64_t ldo, uint32_t* dev_status, nvfp4_stream_t stream) {
-  auto kernel = m <= 128 ? mx_rows : mx_pairs;
+  // mx_rows reads the weight once for every 128 rows and splits k, mx_pairs
+  // keeps 256 x 256 tiles on two SMs each and walks k whole.  Up to 128 rows
+  // the first wins at every shape tried (128 x 5376 x 14336: 16.8 against
+  // 27.7 us); beyond, as long as its 128 x 128 tiles leave SMs to split k over
+  // (512 x 2048 x 14336, 64 tiles: 20.3 against 26.9; 192 x 5376 x 14336, 84
+  // tiles: 32.5 against 27.7).
+  const bool few = m <= 128 || ((m + 127) / 128) * ((n + 127) / 128) <= sm_count() / 2;
+  auto kernel = few ? mx_rows : mx_pairs;
   return kernel(a_q, a_s, w_q, w_s, m, n, k, out, dtype, ldo, dev_status, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -54,7 +61,7 @@ extern "C" nvfp4_status mxfp4_gemm(const void* a_q, const void* a_s, const void*
 }
 
 extern "C" int64_t mxfp4_linear_workspace_bytes(int64_t m, int64_t k) {
-  return align256(mxfp4_qdata_bytes(m, k)) + mxfp4_scale_bytes(m, k);
+  return m <= kMxRowsX ? 0 : align256(mxfp4_qdata_bytes(m, k)) + mxfp4_scale_bytes(m, k);
 }
 
 extern "C" nvfp4_status mxfp4_linear(const void* x, int32_t x_dtype, int64_t m, int64_t ldx, const void* w_q,
@@ -62,7 +69,7 @@ extern "C" nvfp4_status mxfp4_linear(const void* x, int32_t x_dtype, int64_t m, 
                                      void* workspace, int64_t workspace_bytes, uint32_t* dev_status,
                                      nvfp4_stream_t stream) {
   const std::string nm("mxfp4_linear");
-  if (!x || !workspace) return fail(NVFP4_EINVAL, nm + ": null pointer");
+  if (!x || (!workspace && m > kMxRowsX)) return fail(NVFP4_EINVAL, nm + ": null pointer");
   nvfp4_status st = check_product(w_q, w_s, m, n, k, out, dtype, ldo, nm);
   if (st != NVFP4_OK) return st;
   if (!mx_dtype_ok(x_dtype)) return fail(NVFP4_EINVAL, nm + ": unknown element type");
@@ -72,6 +79,9 @@ extern "C" nvfp4_status mxfp4_linear(const void* x, int32_t x_dtype, int64_t m, 
   if (workspace_bytes < mxfp4_linear_workspace_bytes(m, k))
     return fail(NVFP4_EINVAL, nm + ": workspace too small, " + std::to_string(mxfp4_linear_workspace_bytes(m, k)) +
                                   " bytes are needed");
+  if (m <= kMxRowsX)
+    return mx_rows_x(x, x_dtype, ldx, w_q, w_s, m, n, k, out, dtype, ldo, dev_status,
+                     reinterpret_cast<cudaStream_t>(stream));
   uint8_t* a_q = static_cast<uint8_t*>(workspace);
   uint8_t* a_s = a_q + align256(mxfp4_qdata_bytes(m, k));
   if ((st = mxfp4_quantize(x, x_dtype, m, k, ldx, a_q, a_s, stream)) != NVFP4_OK) return st;

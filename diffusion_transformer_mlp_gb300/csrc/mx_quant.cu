@@ -40,6 +40,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_quantize(const T* __restrict__ 
                                                           uint8_t* __restrict__ scales, const MatParams p) {
   __shared__ T slice[kAligned ? 1 : kWarps * kSlice];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_wait();
   for (int64_t u = int64_t(blockIdx.x) * kWarps + warp; u < p.units; u += int64_t(gridDim.x) * kWarps) {
     const int64_t row = p.units <= 0x7FFFFFFF ? int64_t(uint32_t(u) / uint32_t(p.units_per_row)) : u / p.units_per_row;
     const int32_t c0 = int32_t(u - row * p.units_per_row) * kUnit;
@@ -91,6 +92,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_dequantize(const uint8_t* __res
                                                             const MatParams p) {
   __shared__ T slice[kAligned ? 1 : kWarps * kSlice];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_wait();
   for (int64_t u = int64_t(blockIdx.x) * kWarps + warp; u < p.units; u += int64_t(gridDim.x) * kWarps) {
     const int64_t row = p.units <= 0x7FFFFFFF ? int64_t(uint32_t(u) / uint32_t(p.units_per_row)) : u / p.units_per_row;
     const int32_t c0 = int32_t(u - row * p.units_per_row) * kUnit;
@@ -152,16 +154,16 @@ bool vector_rows(const void* x, int64_t ld, int32_t dtype) {
 }
 
 template <typename T>
-void quantize_launch(const void* x, void* q, void* s, const MatParams& p, bool vec, cudaStream_t stream) {
+nvfp4_status quantize_launch(const void* x, void* q, void* s, const MatParams& p, bool vec, cudaStream_t stream) {
   auto k = vec ? k_mx_quantize<T, true> : k_mx_quantize<T, false>;
-  k<<<mat_grid(p), kThreads, 0, stream>>>(static_cast<const T*>(x), static_cast<uint8_t*>(q), static_cast<uint8_t*>(s),
-                                          p);
+  return launch("launch k_mx_quantize", k, dim3(unsigned(mat_grid(p))), dim3(kThreads), 0, 0, stream,
+                static_cast<const T*>(x), static_cast<uint8_t*>(q), static_cast<uint8_t*>(s), p);
 }
 template <typename T>
-void dequantize_launch(const void* q, const void* s, void* out, const MatParams& p, bool vec, cudaStream_t stream) {
+nvfp4_status dequantize_launch(const void* q, const void* s, void* out, const MatParams& p, bool vec, cudaStream_t stream) {
   auto k = vec ? k_mx_dequantize<T, true> : k_mx_dequantize<T, false>;
-  k<<<mat_grid(p), kThreads, 0, stream>>>(static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(s),
-                                          static_cast<T*>(out), p);
+  return launch("launch k_mx_dequantize", k, dim3(unsigned(mat_grid(p))), dim3(kThreads), 0, 0, stream,
+                static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(s), static_cast<T*>(out), p);
 }
 
 }  // namespace
@@ -194,10 +196,9 @@ extern "C" nvfp4_status mxfp4_quantize(const void* x, int32_t dtype, int64_t row
     return fail(NVFP4_EALIGN, nm + ": qdata and scales must be 16-byte aligned, x aligned to its element");
   const bool vec = vector_rows(x, ld, dtype);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == MXFP4_BF16) quantize_launch<__nv_bfloat16>(x, qdata, scales, p, vec, s);
-  else if (dtype == MXFP4_FP16) quantize_launch<__half>(x, qdata, scales, p, vec, s);
-  else quantize_launch<float>(x, qdata, scales, p, vec, s);
-  return cuda_check(cudaGetLastError(), "launch k_mx_quantize");
+  if (dtype == MXFP4_BF16) return quantize_launch<__nv_bfloat16>(x, qdata, scales, p, vec, s);
+  if (dtype == MXFP4_FP16) return quantize_launch<__half>(x, qdata, scales, p, vec, s);
+  return quantize_launch<float>(x, qdata, scales, p, vec, s);
 }
 
 extern "C" nvfp4_status mxfp4_dequantize(const void* qdata, const void* scales, int64_t rows, int64_t cols, void* out,
@@ -211,8 +212,7 @@ extern "C" nvfp4_status mxfp4_dequantize(const void* qdata, const void* scales, 
     return fail(NVFP4_EALIGN, nm + ": qdata and scales must be 16-byte aligned, out aligned to its element");
   const bool vec = vector_rows(out, ld, dtype);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == MXFP4_BF16) dequantize_launch<__nv_bfloat16>(qdata, scales, out, p, vec, s);
-  else if (dtype == MXFP4_FP16) dequantize_launch<__half>(qdata, scales, out, p, vec, s);
-  else dequantize_launch<float>(qdata, scales, out, p, vec, s);
-  return cuda_check(cudaGetLastError(), "launch k_mx_dequantize");
+  if (dtype == MXFP4_BF16) return dequantize_launch<__nv_bfloat16>(qdata, scales, out, p, vec, s);
+  if (dtype == MXFP4_FP16) return dequantize_launch<__half>(qdata, scales, out, p, vec, s);
+  return dequantize_launch<float>(qdata, scales, out, p, vec, s);
 }

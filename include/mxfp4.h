@@ -93,7 +93,8 @@ int64_t mxfp4_linear_workspace_bytes(int64_t m, int64_t k);
 /* out = mxfp4(x) W^T: the rows of x [m, k] (row stride ldx, element type
  * x_dtype) are quantised and multiplied with an MXFP4 weight [n, k], as
  * mxfp4_quantize and mxfp4_gemm would.  workspace: 16-byte aligned, at least
- * mxfp4_linear_workspace_bytes(m, k) bytes; its contents before and after do
+ * mxfp4_linear_workspace_bytes(m, k) bytes (0 for few rows, which need none:
+ * NULL then); its contents before and after do
  * not matter. */
 nvfp4_status mxfp4_linear(const void* x, int32_t x_dtype, int64_t m, int64_t ldx, const void* w_q, const void* w_s,
                           int64_t n, int64_t k, void* out, int32_t dtype, int64_t ldo, void* workspace,

@@ -18,11 +18,11 @@
 // The tensor pipe alternates between the row tiles: P V and the next Q K^T of
 // one run while the softmax of the other does.
 //
-// FP16 operands are exact: a code times 2^(E - R), R the tile's largest key
-// scale (its power of two goes onto the scores) or a running reference of the
-// value scales (onto the output), is exact for E >= R - 23 and below that
-// weighs less than 2^-20 of the tile's largest; Q is scaled by a power of two
-// per row.  Weights are held times 2^10 against a reference that lags the
+// FP16 operands are exact: a code times 2^(E - R + 13), R the tile's largest
+// key scale (its power of two goes onto the scores), is exact for E >= R - 36,
+// and a code times 2^(E - R + 5), R a running reference of the value scales of
+// its block column (its power of two goes onto the output's columns), for E >=
+// R - 28.  Q is scaled by a power of two per row.  Weights are held times 2^10 against a reference that lags the
 // running maximum by up to 2^5, so that the output is rarely rescaled (an
 // 11-bit rounding; sums and statistics in FP32).
 #include <algorithm>
@@ -38,6 +38,7 @@ constexpr float kWeightLog2 = 10.0f;
 constexpr float kLag = 5.0f;
 constexpr int kMeta = 4;       // tiles whose references are kept
 constexpr int kHeadroom = 8;   // value scales may exceed their reference by 2^8 before it is raised
+constexpr int kLiftK = 13, kLiftV = 5;  // largest elements: 6 * 2^13
 
 template <int D>
 struct Chunk {
@@ -49,14 +50,14 @@ struct Chunk {
   static constexpr int kWarpK = kNQ * 4, kWarpV = kWarpK + 4, kWarpMma = kWarpV + 4;
   static constexpr int kThreads = (kWarpMma + 1) * 32;
   static constexpr int kPart = D * kTK / 128;         // elements of a decoding thread
-  static constexpr int kSmem = kNQ * kQBytes + 4 * kKvBytes + 1024;
+  static constexpr int kSmem = kNQ * kQBytes + 4 * kKvBytes + 2048;
   static constexpr uint32_t kS = 0, kO = kNQ * kTK;   // tensor-memory columns: scores, outputs
   static constexpr uint32_t kTmem = 512;
   static_assert(kNQ * (kTK + D) <= 512, "tensor memory");
   static_assert(kSmem <= 232448, "shared memory");
 };
 
-// Small shared state behind the operands (1 KB).
+// Small shared state behind the operands.
 struct Shared {
   uint64_t q_full, done;
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
@@ -64,13 +65,14 @@ struct Shared {
   uint32_t tmem;
   int abort_flag;
   int32_t rk[kMeta];           // reference of the keys' scales
-  int32_t rv[kMeta];           // of the values' scales, as the outputs have it from this tile on
-  float vfac[kMeta];           // factor onto the outputs before this tile (2^(old - new reference))
-  int32_t red[2][2][4];        // [K, V][parity][warp]: largest scale codes
-  uint32_t nan_any[kMeta];     // a block of values holds NaN
+  int32_t rv[kMeta][8];        // of the values' scales by block, as the outputs have it from this tile on
+  float vfac[kMeta][8];        // factor onto the outputs before this tile (2^(old - new reference))
+  uint32_t raised[kMeta];      // warps whose factors are not all 1
+  int32_t red[2][2][4][4];     // [K, V][parity][warp][block of the thread]: largest scale codes
+  uint32_t nan_any[kMeta];     // a block of values holds NaN: the warps that met one
   uint32_t nan_bits[kMeta][8][4];  // [block][32 tokens]
 };
-static_assert(sizeof(Shared) <= 1024, "shared state");
+static_assert(sizeof(Shared) <= 2048, "shared state");
 
 __device__ __forceinline__ uint64_t desc_mn128(uint32_t saddr, uint32_t atom_bytes) {
   // MN-major, 128-byte swizzle: 64 elements x 8 rows of the contraction an
@@ -167,7 +169,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
       mbar_init(&sh.o_full[i], 1);
     }
     sh.abort_flag = 0;
-    for (int i = 0; i < kMeta; ++i) sh.nan_any[i] = 0;
+    for (int i = 0; i < kMeta; ++i) sh.nan_any[i] = sh.raised[i] = 0;
     fence_barrier_init();
   }
   if (warp == T::kWarpMma) tmem_alloc(&sh.tmem, T::kTmem);
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     float m = -INFINITY;
     float2 l2 = make_float2(0.0f, 0.0f);
     uint32_t nan_cols = 0;  // blocks of the output that are NaN
-    int32_t rv = 0;
+    int last_meta = 0;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       if (!wait(&sh.s_full[qt], j & 1)) {
@@ -261,9 +263,8 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
       tc_fence_after();
       const int ms_ = j & (kMeta - 1);
       const int32_t tok0 = span.tile(j) * kTK;
-      const float c1 = qf * pow2i(sh.rk[ms_] - 127);
-      const float vfac = sh.vfac[ms_];
-      rv = sh.rv[ms_];
+      const float c1 = qf * pow2i(sh.rk[ms_] - 127 - kLiftK);
+      last_meta = ms_;
       const bool all = tok0 + kTK <= end && (tok0 >= from || tok0 + kTK <= a.sinks);
       const bool plain = __all_sync(0xFFFFFFFFu, all);
       // keys of the tile that the row sees: [lo, hi) and [0, sk_)
@@ -284,11 +285,11 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
         for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
       }
       const float top = mx == -INFINITY ? -INFINITY : mx * c1;
-      float alpha = vfac;
-      bool raise = vfac != 1.0f;
+      float alpha = 1.0f;
+      bool raise = sh.raised[ms_] != 0;
       if (top > m + kLag) {
-        alpha *= exp2_approx(m - top);
-        l2.x *= exp2_approx(m - top), l2.y *= exp2_approx(m - top);
+        alpha = exp2_approx(m - top);
+        l2.x *= alpha, l2.y *= alpha;
         m = top;
         raise = true;
       }
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
           tc_wait_ld();
           tmem_ld_fence_regs<16>(v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * (alpha * sh.vfac[ms_][c / 32]));
           tmem_st_x16(t_o + c, v);
         }
       }
@@ -353,7 +354,6 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     tc_fence_after();
     const float l = l2.x + l2.y;
     const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-    const float fac = pow2i(rv - 127) * inv;
     if (ok) {
       uint16_t* dst = static_cast<uint16_t*>(a.out) + int64_t(q0 + qi) * a.o_st + int64_t(hq) * a.o_sh;
 #pragma unroll 1
@@ -363,6 +363,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
         tc_wait_ld();
         tmem_ld_fence_regs<32>(v);
         const bool nan = (nan_cols >> (c / 32)) & 1u;
+        const float fac = l == 0.0f ? 0.0f : pow2i(sh.rv[last_meta][c / 32] - 127 - kLiftV) * inv;
 #pragma unroll
         for (int i = 0; i < 32; i += 8) {
           uint32_t w[4];
@@ -427,7 +428,10 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
         sc = 0;
       }
     };
-    int32_t page = page_of(0), rv = -1;
+    int32_t page = page_of(0);
+    int32_t rv[kWords];  // V: the references of the thread's blocks
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) rv[i] = -1;
     bool dead = false;  // a wait ran out: the loop goes on, for the barrier of the group, without its work
     fetch(0, page);
     page = page_of(1);
@@ -439,49 +443,61 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
       const uint32_t scale = sc;
       fetch(j + 1, page);
       page = page_of(j + 2);
-      // the largest finite scale of the tile
-      int32_t mx = 0;
+      // the largest finite scales of the tile, by block
+      int32_t ref[kWords];
       bool nan = false;
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         const int32_t e = (scale >> (8 * i)) & 0xFF;
-        if (e == 255) nan = true;
-        else mx = max(mx, e);
+        nan = nan || e == 255;
+        ref[i] = __reduce_max_sync(0xFFFFFFFFu, e == 255 ? 0 : e);
+        if (lane == 0) sh.red[is_v][slot][warp & 3][i] = ref[i];
       }
-      mx = __reduce_max_sync(0xFFFFFFFFu, mx);
-      if (lane == 0) sh.red[is_v][slot][warp & 3] = mx;
       if (is_v) asm volatile("bar.sync 2, 128;" ::: "memory");
       else asm volatile("bar.sync 1, 128;" ::: "memory");
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mx = max(mx, sh.red[is_v][slot][i]);
-      int32_t ref = mx;
       if (is_v) {
-        // a running reference: raised only when the headroom is used up
-        float fac = 1.0f;
-        if (rv < 0) {
-          rv = mx;
-        } else if (mx > rv + kHeadroom) {
-          fac = pow2i(rv - mx);
-          rv = mx;
-        }
-        ref = rv;
+        // running references, raised only when the headroom is used up
+        bool up = false;
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
+          // the warps that hold the same share of the rows
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            if (w / (kTK / 32) == part) ref[i] = max(ref[i], sh.red[1][slot][w][i]);
+          float fac = 1.0f;
+          if (rv[i] < 0) {
+            rv[i] = ref[i];
+          } else if (ref[i] > rv[i] + kHeadroom) {
+            fac = pow2i(rv[i] - ref[i]);
+            rv[i] = ref[i];
+            up = true;
+          }
+          ref[i] = rv[i] - kLiftV;
+          if (tok == 0) {
+            sh.vfac[meta][part * kWords + i] = fac;
+            sh.rv[meta][part * kWords + i] = rv[i];
+          }
           const uint32_t bits = __ballot_sync(0xFFFFFFFFu, ((scale >> (8 * i)) & 0xFF) == 255u);
           if (lane == 0) sh.nan_bits[meta][part * kWords + i][tok / 32] = bits;
         }
         const bool any = __any_sync(0xFFFFFFFFu, nan);
-        if (t == 0) {
-          sh.vfac[meta] = fac;
-          sh.rv[meta] = rv;
-        }
         if (lane == 0) {
-          // one bit a warp: no warp waits for another here
-          if (any) atomicOr(&sh.nan_any[meta], 1u << (warp & 3));
-          else atomicAnd(&sh.nan_any[meta], ~(1u << (warp & 3)));
+          // a bit a warp: no warp waits for another here
+          const uint32_t bit = 1u << (warp & 3);
+          if (any) atomicOr(&sh.nan_any[meta], bit);
+          else atomicAnd(&sh.nan_any[meta], ~bit);
+          if (up) atomicOr(&sh.raised[meta], bit);
+          else atomicAnd(&sh.raised[meta], ~bit);
         }
-      } else if (t == 0) {
-        sh.rk[meta] = ref;
+      } else {
+        int32_t mx = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) mx = max(mx, sh.red[0][slot][w][i]);
+        if (t == 0) sh.rk[meta] = mx;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) ref[i] = mx - kLiftK;
       }
       if (!dead && !wait(&empty[slot], ((j >> 1) & 1) ^ 1)) dead = true;
       if (dead) continue;
@@ -489,7 +505,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         const int32_t e = (scale >> (8 * i)) & 0xFF;
-        const float f = __uint_as_float(uint32_t(max(e - ref + 127, 0)) << 23);
+        const float f = __uint_as_float(uint32_t(max(e - ref[i] + 127, 0)) << 23);
         uint32_t fw = f32_to_word<__half>(f, f);
         if (e == 255) fw = is_v ? 0u : 0x7FFF7FFFu;
         const uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};

@@ -9,9 +9,10 @@
 //   warps 0-3, 4-7  softmax of row tile 0, 1: a thread is a row.  Scores come
 //                   from tensor memory, the weights go back there as FP16 over
 //                   the scores they came from (the A operand of p v)
-//   K warps         decode the tile's keys to FP16 in shared memory: a thread
-//   V warps         takes one token (of kTK), loads its codes and scales one
-//                   tile ahead, and writes its row under the 128-byte swizzle
+//   four warps      decode the tile's keys and values to FP16 in shared memory:
+//                   a thread takes one token (of kTK), loads its codes and
+//                   scales one tile ahead, and writes its rows under the
+//                   128-byte swizzle
 //   last warp       issues the MMAs: S = Q K^T (both from shared memory,
 //                   K-major), O += P V (P from tensor memory, V MN-major)
 //
@@ -28,6 +29,7 @@
 #include <algorithm>
 #include <atomic>
 #include <string>
+#include <type_traits>
 
 #include "mx_attn.cuh"
 
@@ -47,7 +49,7 @@ struct Chunk {
   static constexpr int kTK = D == 256 ? 64 : 128;
   static constexpr int kQBytes = 128 * D * 2;         // one row tile
   static constexpr int kKvBytes = kTK * D * 2;        // one decoded tile of K or V
-  static constexpr int kWarpK = kNQ * 4, kWarpV = kWarpK + 4, kWarpMma = kWarpV + 4;
+  static constexpr int kWarpD = kNQ * 4, kWarpMma = kWarpD + 4;
   static constexpr int kThreads = (kWarpMma + 1) * 32;
   static constexpr int kPart = D * kTK / 128;         // elements of a decoding thread
   static constexpr int kSmem = kNQ * kQBytes + 4 * kKvBytes + 2048;
@@ -68,7 +70,7 @@ struct Shared {
   int32_t rv[kMeta][8];        // of the values' scales by block, as the outputs have it from this tile on
   float vfac[kMeta][8];        // factor onto the outputs before this tile (2^(old - new reference))
   uint32_t raised[kMeta];      // warps whose factors are not all 1
-  int32_t red[2][2][4][4];     // [K, V][parity][warp][block of the thread]: largest scale codes
+  int32_t red[2][2][4][4];     // [parity][K, V][warp][block of the thread]: largest scale codes
   uint32_t nan_any[kMeta];     // a block of values holds NaN: the warps that met one
   uint32_t nan_bits[kMeta][8][4];  // [block][32 tokens]
 };
@@ -111,21 +113,31 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// (a.x * b.x + c.x, a.y * b.y + c.y)
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+// Pairs of binary32 in 64 bits.  A pair of equal constants is made once, by a
+// volatile move: left to the compiler it is made again at every use.
+__device__ __forceinline__ uint64_t pair_const(float v) {
+  uint64_t r;
+  asm volatile("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
   return r;
 }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+__device__ __forceinline__ uint64_t pair_of(uint32_t x, uint32_t y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
   float2 r;
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 
@@ -179,16 +191,15 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
   const uint32_t tmem = sh.tmem;
   const volatile int* abort_flag = &sh.abort_flag;
   const int n = span.n;
-  // one lane waits for the warp; false once a bounded wait anywhere ran out
+  // false once a bounded wait anywhere ran out, for the whole warp alike
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    int ok = 1;
-    if (lane == 0) ok = mbar_wait_bounded(bar, parity, a.wait_limit_cycles, abort_flag);
-    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-    if (!ok) sh.abort_flag = 1;
-    return ok != 0;
+    const bool ok = mbar_wait_bounded(bar, parity, a.wait_limit_cycles, abort_flag);
+    if (__all_sync(0xFFFFFFFFu, ok)) return true;
+    sh.abort_flag = 1;
+    return false;
   };
 
-  if (warp < T::kWarpK) {
+  if (warp < T::kWarpD) {
     // ------------------------------------------------------------ softmax
     const int qt = warp >> 2, q = warp & 3;
     const int r = q * 32 + lane;  // row of the tile, lane of tensor memory
@@ -206,44 +217,57 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     float qf;
     {
       const uint16_t* src = static_cast<const uint16_t*>(a.q) + int64_t(q0 + qi) * a.q_st + int64_t(hq) * a.q_sh;
-      auto load8 = [&](int d, float (&f)[8]) {
-        uint32_t w[4] = {0, 0, 0, 0};
-        if (real) {
-          if (a.q_vec) {
-            const uint4 v = *reinterpret_cast<const uint4*>(src + d);
-            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-          } else {
+      // up to 128 elements at a time, their loads all in flight; the row twice,
+      // for its largest element and for the conversion, unless it fits
+      constexpr int kRound = D < 128 ? D : 128;
+      uint32_t w[kRound / 2];
+      auto load = [&](int d0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = uint32_t(src[d + 2 * i]) | uint32_t(src[d + 2 * i + 1]) << 16;
+        for (int i = 0; i < kRound / 8; ++i) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (real) {
+            const uint16_t* e = src + d0 + 8 * i;
+            if (a.q_vec) {
+              v = *reinterpret_cast<const uint4*>(e);
+            } else {
+              v.x = uint32_t(e[0]) | uint32_t(e[1]) << 16, v.y = uint32_t(e[2]) | uint32_t(e[3]) << 16;
+              v.z = uint32_t(e[4]) | uint32_t(e[5]) << 16, v.w = uint32_t(e[6]) | uint32_t(e[7]) << 16;
+            }
           }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 t = a.bf16 ? word_to_f32<__nv_bfloat16>(w[i]) : word_to_f32<__half>(w[i]);
-          f[2 * i] = t.x, f[2 * i + 1] = t.y;
+          w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
         }
       };
+      auto value = [&](uint32_t x) { return a.bf16 ? word_to_f32<__nv_bfloat16>(x) : word_to_f32<__half>(x); };
       float am = 0.0f;
-#pragma unroll 4
-      for (int d = 0; d < D; d += 8) {
-        float f[8];
-        load8(d, f);
+#pragma unroll 1
+      for (int d0 = 0; d0 < D; d0 += kRound) {
+        load(d0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) am = max_nan(am, fabsf(f[i]));
+        for (int i = 0; i < kRound / 2; ++i) {
+          const float2 t = value(w[i]);
+          am = max_nan(am, max_nan(fabsf(t.x), fabsf(t.y)));
+        }
       }
       const int32_t eb = int32_t(__float_as_uint(am) >> 23) & 0xFF;
       const int32_t up = (eb == 0 || eb == 255) ? 0 : min(126, 140 - eb);
       const float mul = a.scale_log2 < 0.0f ? -pow2i(up) : pow2i(up);
       qf = fabsf(a.scale_log2) * pow2i(-up);
       uint8_t* dst = sq + qt * T::kQBytes + r * 128;
-#pragma unroll 4
-      for (int d = 0; d < D; d += 8) {
-        float f[8];
-        load8(d, f);
-        uint4 w;
-        w.x = f32_to_word<__half>(f[0] * mul, f[1] * mul), w.y = f32_to_word<__half>(f[2] * mul, f[3] * mul);
-        w.z = f32_to_word<__half>(f[4] * mul, f[5] * mul), w.w = f32_to_word<__half>(f[6] * mul, f[7] * mul);
-        *reinterpret_cast<uint4*>(dst + (d / 64) * (128 * 128) + ((((d % 64) / 8) ^ (r & 7)) << 4)) = w;
+#pragma unroll 1
+      for (int d0 = 0; d0 < D; d0 += kRound) {
+        if (kRound < D) load(d0);
+#pragma unroll
+        for (int i = 0; i < kRound / 8; ++i) {
+          uint32_t h[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float2 t = value(w[4 * i + x]);
+            h[x] = f32_to_word<__half>(t.x * mul, t.y * mul);
+          }
+          const int d = d0 + 8 * i;
+          *reinterpret_cast<uint4*>(dst + (d / 64) * (128 * 128) + ((((d % 64) / 8) ^ (r & 7)) << 4)) =
+              make_uint4(h[0], h[1], h[2], h[3]);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -269,32 +293,57 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
       const bool plain = __all_sync(0xFFFFFFFFu, all);
       // keys of the tile that the row sees: [lo, hi) and [0, sk_)
       const int32_t hi = end - tok0, lo = from - tok0, sk_ = a.sinks - tok0;
-      float mx = -INFINITY;
+      // Weights against the reference as it stands, in registers; where a
+      // row's maximum is too far ahead of it, it is raised and the weights are
+      // formed again (the scores are still there).
+      uint32_t w[kTK / 2];
+      uint64_t sum;
+      float top;
+      const uint64_t c1p = pair_const(c1);
+      auto weights = [&](auto masked) {
+        const float sub = kWeightLog2 - (m == -INFINITY ? 0.0f : m);
+        const uint64_t subp = pair_const(sub);
+        sum = 0;
+        top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < kTK; c += 32) {
-        uint32_t s[32];
-        tmem_ld_32x32b_x32(t_s + c, s);
-        tc_wait_ld();
-        tmem_ld_fence_regs<32>(s);
-        if (!plain) {
+        for (int c = 0; c < kTK; c += 32) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(t_s + c, v);
+          tc_wait_ld();
+          tmem_ld_fence_regs<32>(v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c + i >= hi || (c + i < lo && c + i >= sk_)) s[i] = 0xFF800000u;
+          for (int i = 0; i < 32; i += 2) {
+            float2 t = unpair(fma2(pair_of(v[i], v[i + 1]), c1p, subp));
+            if constexpr (decltype(masked)::value) {
+              if (c + i >= hi || (c + i < lo && c + i >= sk_)) t.x = -INFINITY;
+              if (c + i + 1 >= hi || (c + i + 1 < lo && c + i + 1 >= sk_)) t.y = -INFINITY;
+            }
+            top = fmaxf(top, fmaxf(t.x, t.y));
+            t.x = exp2_approx(t.x), t.y = exp2_approx(t.y);
+            sum = add2(sum, pair_of(__float_as_uint(t.x), __float_as_uint(t.y)));
+            w[(c + i) / 2] = f32_to_word<__half>(t.x, t.y);
+          }
         }
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
-      }
-      const float top = mx == -INFINITY ? -INFINITY : mx * c1;
+        top -= sub;  // back to the score's logarithm
+      };
       float alpha = 1.0f;
-      bool raise = sh.raised[ms_] != 0;
-      if (top > m + kLag) {
-        alpha = exp2_approx(m - top);
-        l2.x *= alpha, l2.y *= alpha;
-        m = top;
-        raise = true;
+      bool raised = sh.raised[ms_] != 0;
+#pragma unroll 1
+      for (int attempt = 0; attempt < 2; ++attempt) {
+        if (plain) weights(std::false_type{});
+        else weights(std::true_type{});
+        const bool raise = top > m + kLag;
+        if (!__any_sync(0xFFFFFFFFu, raise) || attempt == 1) break;
+        if (raise) {
+          alpha = exp2_approx(m - top);
+          l2.x *= alpha, l2.y *= alpha;
+          m = top;
+        }
+        raised = true;
       }
+      l2.x += unpair(sum).x, l2.y += unpair(sum).y;
       // s_full also says that the p v of the tile before is complete
-      if (j > 0 && __any_sync(0xFFFFFFFFu, raise)) {
+      if (j > 0 && raised) {
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
           uint32_t v[16];
@@ -311,27 +360,8 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
           tmem_st_x16(t_o + c, v);
         }
       }
-      const float sub = kWeightLog2 - (m == -INFINITY ? 0.0f : m);
 #pragma unroll
-      for (int c = 0; c < kTK; c += 32) {
-        uint32_t s[32], w[16];
-        tmem_ld_32x32b_x32(t_s + c, s);
-        tc_wait_ld();
-        tmem_ld_fence_regs<32>(s);
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          float2 t = fma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(c1, c1),
-                          make_float2(sub, sub));
-          if (!plain) {
-            if (c + i >= hi || (c + i < lo && c + i >= sk_)) t.x = -INFINITY;
-            if (c + i + 1 >= hi || (c + i + 1 < lo && c + i + 1 >= sk_)) t.y = -INFINITY;
-          }
-          t.x = exp2_approx(t.x), t.y = exp2_approx(t.y);
-          l2 = add2(l2, t);
-          w[i / 2] = f32_to_word<__half>(t.x, t.y);
-        }
-        tmem_st_x16(t_s + c / 2, w);  // over scores that have been read
-      }
+      for (int c = 0; c < kTK / 2; c += 16) tmem_st_x16(t_s + c, reinterpret_cast<const uint32_t(&)[16]>(w[c]));
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -395,41 +425,37 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     tc_fence_before();
   } else if (warp < T::kWarpMma) {
     // ------------------------------------------------------------ decoding
-    const bool is_v = warp >= T::kWarpV;
-    const int t = int(threadIdx.x) - (is_v ? T::kWarpV : T::kWarpK) * 32;
-    const int tok = t % kTK, part = t / kTK;        // the token, and its share of the row
-    constexpr int kWords = T::kPart / 32;           // blocks of a thread
-    const uint8_t* codes = is_v ? v_codes : k_codes;
-    const uint8_t* scales = is_v ? a.v_scales : a.k_scales;
-    uint8_t* ring = is_v ? sv : sk;
-    uint64_t* full = is_v ? sh.v_full : sh.k_full;
-    uint64_t* empty = is_v ? sh.v_empty : sh.k_empty;
+    const int t = int(threadIdx.x) - T::kWarpD * 32, dw = t >> 5;
+    const int tok = t % kTK, part = t / kTK;        // the token, and the thread's share of its rows
+    constexpr int kWords = T::kPart / 32;           // blocks of a share
     const int32_t* table = a.table + int64_t(b) * a.table_ld;
     auto page_of = [&](int j) -> int32_t {
       const int32_t at = span.tile(j) * kTK + tok;
       return j < n && at < span.hi ? table[min(at >> a.page_shift, int32_t(a.table_ld) - 1)] : 0;
     };
-    uint4 raw[kWords];
-    uint32_t sc = 0;
+    uint4 raw[2][kWords];  // codes of K and V
+    uint32_t sc[2] = {0, 0};
     auto fetch = [&](int j, int32_t page) {
       const int32_t at = span.tile(j) * kTK + tok;
-      if (j < n && at < span.hi) {
-        const int64_t pg = min(max(page, 0), int32_t(a.pages) - 1);
-        const int64_t rowi = ((pg * a.kv_heads + head) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
-        const uint8_t* src = codes + rowi * (D / 2) + part * (T::kPart / 2);
+      const bool in = j < n && at < span.hi;
+      const int64_t pg = min(max(page, 0), int32_t(a.pages) - 1);
+      const int64_t rowi = ((pg * a.kv_heads + head) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) raw[i] = *reinterpret_cast<const uint4*>(src + 16 * i);
-        const uint8_t* s = scales + rowi * C + part * kWords;
-        if constexpr (kWords == 2) sc = *reinterpret_cast<const uint16_t*>(s);
-        else sc = *reinterpret_cast<const uint32_t*>(s);
-      } else {
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint8_t* src = (kv ? v_codes : k_codes) + rowi * (D / 2) + part * (T::kPart / 2);
+        const uint8_t* s = (kv ? a.v_scales : a.k_scales) + rowi * C + part * kWords;
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) raw[i] = make_uint4(0, 0, 0, 0);
-        sc = 0;
+        for (int i = 0; i < kWords; ++i)
+          raw[kv][i] = in ? *reinterpret_cast<const uint4*>(src + 16 * i) : make_uint4(0, 0, 0, 0);
+        sc[kv] = 0;
+        if (in) {
+          if constexpr (kWords == 2) sc[kv] = *reinterpret_cast<const uint16_t*>(s);
+          else sc[kv] = *reinterpret_cast<const uint32_t*>(s);
+        }
       }
     };
     int32_t page = page_of(0);
-    int32_t rv[kWords];  // V: the references of the thread's blocks
+    int32_t rv[kWords];  // the references of the thread's value blocks
 #pragma unroll
     for (int i = 0; i < kWords; ++i) rv[i] = -1;
     bool dead = false;  // a wait ran out: the loop goes on, for the barrier of the group, without its work
@@ -437,90 +463,97 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     page = page_of(1);
     for (int j = 0; j < n; ++j) {
       const int slot = j & 1, meta = j & (kMeta - 1);
-      uint4 cur[kWords];
+      // this tile's codes make room for the next tile's, whose loads take as
+      // long as the decoding
+      uint4 cur[2][kWords];
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) cur[i] = raw[i];
-      const uint32_t scale = sc;
+      for (int i = 0; i < kWords; ++i) cur[0][i] = raw[0][i], cur[1][i] = raw[1][i];
+      // the largest finite scales of the tile, by block
+      int32_t ref[2][kWords];
+      const uint32_t scale[2] = {sc[0], sc[1]};
       fetch(j + 1, page);
       page = page_of(j + 2);
-      // the largest finite scales of the tile, by block
-      int32_t ref[kWords];
       bool nan = false;
 #pragma unroll
+      for (int i = 0; i < kWords; ++i)
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int32_t e = (scale[kv] >> (8 * i)) & 0xFF;
+          nan = nan || (kv == 1 && e == 255);
+          const int32_t mx = __reduce_max_sync(0xFFFFFFFFu, e == 255 ? 0 : e);
+          if (lane == 0) sh.red[slot][kv][dw][i] = mx;
+          ref[kv][i] = mx;
+        }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      // values: running references, raised only when the headroom is used up
+      bool up = false;
+#pragma unroll
       for (int i = 0; i < kWords; ++i) {
-        const int32_t e = (scale >> (8 * i)) & 0xFF;
-        nan = nan || e == 255;
-        ref[i] = __reduce_max_sync(0xFFFFFFFFu, e == 255 ? 0 : e);
-        if (lane == 0) sh.red[is_v][slot][warp & 3][i] = ref[i];
+        // the warps that hold the same share of the rows
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          if (w / (kTK / 32) == part) ref[1][i] = max(ref[1][i], sh.red[slot][1][w][i]);
+        float fac = 1.0f;
+        if (rv[i] < 0) {
+          rv[i] = ref[1][i];
+        } else if (ref[1][i] > rv[i] + kHeadroom) {
+          fac = pow2i(rv[i] - ref[1][i]);
+          rv[i] = ref[1][i];
+          up = true;
+        }
+        ref[1][i] = rv[i] - kLiftV;
+        if (tok == 0) {
+          sh.vfac[meta][part * kWords + i] = fac;
+          sh.rv[meta][part * kWords + i] = rv[i];
+        }
+        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, ((scale[1] >> (8 * i)) & 0xFF) == 255u);
+        if (lane == 0) sh.nan_bits[meta][part * kWords + i][tok / 32] = bits;
       }
-      if (is_v) asm volatile("bar.sync 2, 128;" ::: "memory");
-      else asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (is_v) {
-        // running references, raised only when the headroom is used up
-        bool up = false;
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-          // the warps that hold the same share of the rows
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            if (w / (kTK / 32) == part) ref[i] = max(ref[i], sh.red[1][slot][w][i]);
-          float fac = 1.0f;
-          if (rv[i] < 0) {
-            rv[i] = ref[i];
-          } else if (ref[i] > rv[i] + kHeadroom) {
-            fac = pow2i(rv[i] - ref[i]);
-            rv[i] = ref[i];
-            up = true;
-          }
-          ref[i] = rv[i] - kLiftV;
-          if (tok == 0) {
-            sh.vfac[meta][part * kWords + i] = fac;
-            sh.rv[meta][part * kWords + i] = rv[i];
-          }
-          const uint32_t bits = __ballot_sync(0xFFFFFFFFu, ((scale >> (8 * i)) & 0xFF) == 255u);
-          if (lane == 0) sh.nan_bits[meta][part * kWords + i][tok / 32] = bits;
-        }
-        const bool any = __any_sync(0xFFFFFFFFu, nan);
-        if (lane == 0) {
-          // a bit a warp: no warp waits for another here
-          const uint32_t bit = 1u << (warp & 3);
-          if (any) atomicOr(&sh.nan_any[meta], bit);
-          else atomicAnd(&sh.nan_any[meta], ~bit);
-          if (up) atomicOr(&sh.raised[meta], bit);
-          else atomicAnd(&sh.raised[meta], ~bit);
-        }
-      } else {
+      const bool any = __any_sync(0xFFFFFFFFu, nan);
+      if (lane == 0) {
+        // a bit a warp: no warp waits for another here
+        const uint32_t bit = 1u << dw;
+        if (any) atomicOr(&sh.nan_any[meta], bit);
+        else atomicAnd(&sh.nan_any[meta], ~bit);
+        if (up) atomicOr(&sh.raised[meta], bit);
+        else atomicAnd(&sh.raised[meta], ~bit);
+      }
+      {
         int32_t mx = 0;
 #pragma unroll
         for (int w = 0; w < 4; ++w)
 #pragma unroll
-          for (int i = 0; i < kWords; ++i) mx = max(mx, sh.red[0][slot][w][i]);
+          for (int i = 0; i < kWords; ++i) mx = max(mx, sh.red[slot][0][w][i]);
         if (t == 0) sh.rk[meta] = mx;
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) ref[i] = mx - kLiftK;
+        for (int i = 0; i < kWords; ++i) ref[0][i] = mx - kLiftK;
       }
-      if (!dead && !wait(&empty[slot], ((j >> 1) & 1) ^ 1)) dead = true;
-      if (dead) continue;
-      uint8_t* dst = ring + slot * T::kKvBytes + tok * 128;
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        const int32_t e = (scale >> (8 * i)) & 0xFF;
-        const float f = __uint_as_float(uint32_t(max(e - ref[i] + 127, 0)) << 23);
-        uint32_t fw = f32_to_word<__half>(f, f);
-        if (e == 255) fw = is_v ? 0u : 0x7FFF7FFFu;
-        const uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
+      for (int kv = 0; kv < 2; ++kv) {
+        if (!dead && !wait(kv ? &sh.v_empty[slot] : &sh.k_empty[slot], ((j >> 1) & 1) ^ 1)) dead = true;
+        if (!dead) {
+          uint8_t* dst = (kv ? sv : sk) + slot * T::kKvBytes + tok * 128;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          uint32_t h[4];
-          e2m1x8_to_half(w[x], h);
-          const int d = part * T::kPart + i * 32 + x * 8;
-          *reinterpret_cast<uint4*>(dst + (d / 64) * (kTK * 128) + ((((d % 64) / 8) ^ (tok & 7)) << 4)) =
-              make_uint4(hmul2(h[0], fw), hmul2(h[1], fw), hmul2(h[2], fw), hmul2(h[3], fw));
+          for (int i = 0; i < kWords; ++i) {
+            const int32_t e = (scale[kv] >> (8 * i)) & 0xFF;
+            const float f = __uint_as_float(uint32_t(max(e - ref[kv][i] + 127, 0)) << 23);
+            uint32_t fw = f32_to_word<__half>(f, f);
+            if (e == 255) fw = kv ? 0u : 0x7FFF7FFFu;
+            const uint32_t w[4] = {cur[kv][i].x, cur[kv][i].y, cur[kv][i].z, cur[kv][i].w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t h[4];
+              e2m1x8_to_half(w[x], h);
+              const int d = part * T::kPart + i * 32 + x * 8;
+              *reinterpret_cast<uint4*>(dst + (d / 64) * (kTK * 128) + ((((d % 64) / 8) ^ (tok & 7)) << 4)) =
+                  make_uint4(hmul2(h[0], fw), hmul2(h[1], fw), hmul2(h[2], fw), hmul2(h[3], fw));
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(kv ? &sh.v_full[slot] : &sh.k_full[slot]);
         }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[slot]);
     }
   } else if (lane == 0) {
     // ------------------------------------------------------------ MMA issue

@@ -13,11 +13,16 @@
 //                   a thread takes one token (of kTK), loads its codes and
 //                   scales one tile ahead, and writes its rows under the
 //                   128-byte swizzle
-//   last warp       issues the MMAs: S = Q K^T (both from shared memory,
-//                   K-major), O += P V (P from tensor memory, V MN-major)
+//   one warp        goes ahead of them over the scales: the references of each
+//                   tile (below) and its NaN blocks
+//   last warps      one a row tile, issue its MMAs: S = Q K^T (both from
+//                   shared memory, K-major), O += P V (P from tensor memory, V
+//                   MN-major)
 //
-// The tensor pipe alternates between the row tiles: P V and the next Q K^T of
-// one run while the softmax of the other does.
+// Every row tile has two score buffers: Q K^T of the next keys is under way
+// while the softmax of these runs, so that neither waits for the other's
+// latency (128 keys and one buffer: 4,300 cycles for 128 keys of both row
+// tiles; one issuing thread for both was slower still).
 //
 // FP16 operands are exact: a code times 2^(E - R + 13), R the tile's largest
 // key scale (its power of two goes onto the scores), is exact for E >= R - 36,
@@ -38,7 +43,8 @@ namespace {
 
 constexpr float kWeightLog2 = 10.0f;
 constexpr float kLag = 5.0f;
-constexpr int kMeta = 4;       // tiles whose references are kept
+constexpr int kMeta = 8;       // tiles whose references are kept: the decoders are up to 6 ahead of the softmax
+constexpr int kTK = 64;        // keys of a tile
 constexpr int kHeadroom = 8;   // value scales may exceed their reference by 2^8 before it is raised
 constexpr int kLiftK = 13, kLiftV = 5;  // largest elements: 6 * 2^13
 
@@ -46,58 +52,75 @@ template <int D>
 struct Chunk {
   static constexpr int C = D / 32;
   static constexpr int kNQ = D == 256 ? 1 : 2;
-  static constexpr int kTK = D == 256 ? 64 : 128;
+  static constexpr int kSlots = D == 256 ? 2 : 4;     // decoded tiles
   static constexpr int kQBytes = 128 * D * 2;         // one row tile
   static constexpr int kKvBytes = kTK * D * 2;        // one decoded tile of K or V
-  static constexpr int kWarpD = kNQ * 4, kWarpMma = kWarpD + 4;
-  static constexpr int kThreads = (kWarpMma + 1) * 32;
+  static constexpr int kWarpD = kNQ * 4, kWarpR = kWarpD + 4, kWarpMma = kWarpR + 1;
+  static constexpr int kThreads = (kWarpMma + kNQ) * 32;
   static constexpr int kPart = D * kTK / 128;         // elements of a decoding thread
-  static constexpr int kSmem = kNQ * kQBytes + 4 * kKvBytes + 2048;
-  static constexpr uint32_t kS = 0, kO = kNQ * kTK;   // tensor-memory columns: scores, outputs
+  static constexpr int kSmem = kNQ * kQBytes + 2 * kSlots * kKvBytes + 4096;
+  static constexpr uint32_t kS = 0, kO = kNQ * 2 * kTK;  // tensor-memory columns: scores, outputs
   static constexpr uint32_t kTmem = 512;
-  static_assert(kNQ * (kTK + D) <= 512, "tensor memory");
+  static_assert(kNQ * (2 * kTK + D) <= 512, "tensor memory");
   static_assert(kSmem <= 232448, "shared memory");
 };
 
 // Small shared state behind the operands.
 struct Shared {
   uint64_t q_full, done;
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t ref_full[4], kv_full[4], kv_empty[4];  // by slot: references, decoded tile, both row tiles' p v complete
+  uint64_t s_full[2][2], p_full[2][2];            // by row tile and score buffer
+  uint64_t o_full[2];                             // p v of the last tile is complete
   uint32_t tmem;
   int abort_flag;
   int32_t rk[kMeta];           // reference of the keys' scales
   int32_t rv[kMeta][8];        // of the values' scales by block, as the outputs have it from this tile on
   float vfac[kMeta][8];        // factor onto the outputs before this tile (2^(old - new reference))
-  uint32_t raised[kMeta];      // warps whose factors are not all 1
-  int32_t red[2][2][4][4];     // [parity][K, V][warp][block of the thread]: largest scale codes
-  uint32_t nan_any[kMeta];     // a block of values holds NaN: the warps that met one
-  uint32_t nan_bits[kMeta][8][4];  // [block][32 tokens]
+  uint32_t raised[kMeta];      // the factors are not all 1
+  uint32_t nan_any[kMeta];     // a block of values holds NaN
+  uint32_t nan_bits[kMeta][8][kTK / 32];  // [block][32 tokens]
 };
-static_assert(sizeof(Shared) <= 2048, "shared state");
+static_assert(sizeof(Shared) <= 4096, "shared state");
 
-__device__ __forceinline__ uint64_t desc_mn128(uint32_t saddr, uint32_t atom_bytes) {
-  // MN-major, 128-byte swizzle: 64 elements x 8 rows of the contraction an
-  // atom; next 64 elements atom_bytes on, next 8 rows 1,024 bytes on
-  return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(atom_bytes >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
-         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+// Shared-memory descriptors, 128-byte swizzle, descriptor version 1.  The high
+// word is the same for both forms (8-row groups 1,024 bytes apart); the low
+// word is the address and the leading offset, so a step along the operand is
+// one 32-bit addition.
+//   K-major: rows of 128 bytes; the leading offset is not used
+//   MN-major: 64 elements x 8 rows of the contraction an atom, the next 64
+//   elements atom_bytes on
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead_bytes) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lead_bytes >> 4) << 16);
 }
-__device__ __forceinline__ uint64_t desc_k128(uint32_t saddr) {
-  return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
-         (uint64_t(2) << 61);
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(uint32_t(accumulate))
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(uint32_t(accumulate))
+      : "memory");
+}
+// 32 columns of this warp's lanes, complete on return.
+__device__ __forceinline__ void tmem_load32(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -146,12 +169,12 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     k_attn_chunk(const uint8_t* __restrict__ k_codes, const uint8_t* __restrict__ v_codes,
                  const __grid_constant__ AttnParams a) {
   using T = Chunk<D>;
-  constexpr int C = T::C, kNQ = T::kNQ, kTK = T::kTK;
+  constexpr int C = T::C, kNQ = T::kNQ, kSlots = T::kSlots;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sq = smem;                          // [row tile][atom][128 rows][128 bytes]
   uint8_t* sk = sq + kNQ * T::kQBytes;         // [slot][atom][token][128 bytes]
-  uint8_t* sv = sk + 2 * T::kKvBytes;
-  Shared& sh = *reinterpret_cast<Shared*>(sv + 2 * T::kKvBytes);
+  uint8_t* sv = sk + kSlots * T::kKvBytes;
+  Shared& sh = *reinterpret_cast<Shared*>(sv + kSlots * T::kKvBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_wait();
 
@@ -170,18 +193,17 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(&sh.q_full, kNQ * 4);
-    mbar_init(&sh.done, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.k_full[i], 4);
-      mbar_init(&sh.k_empty[i], 1);
-      mbar_init(&sh.v_full[i], 4);
-      mbar_init(&sh.v_empty[i], 1);
-      mbar_init(&sh.s_full[i], 2);
-      mbar_init(&sh.p_full[i], 4);
-      mbar_init(&sh.o_full[i], 1);
+    mbar_init(&sh.done, kNQ);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sh.ref_full[i], 1);
+      mbar_init(&sh.kv_full[i], 4);
+      mbar_init(&sh.kv_empty[i], kNQ);
+      mbar_init(&sh.s_full[i >> 1][i & 1], 2);
+      mbar_init(&sh.p_full[i >> 1][i & 1], 4);
     }
+    mbar_init(&sh.o_full[0], 1);
+    mbar_init(&sh.o_full[1], 1);
     sh.abort_flag = 0;
-    for (int i = 0; i < kMeta; ++i) sh.nan_any[i] = sh.raised[i] = 0;
     fence_barrier_init();
   }
   if (warp == T::kWarpMma) tmem_alloc(&sh.tmem, T::kTmem);
@@ -211,7 +233,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     const int32_t end = !real ? 0 : (a.causal ? min(len, pos + 1) : len);
     const int32_t from = a.window > 0 ? pos - a.window + 1 : 0;
     const uint32_t t_lane = tmem + (uint32_t(q * 32) << 16);
-    const uint32_t t_s = t_lane + T::kS + qt * kTK, t_o = t_lane + T::kO + qt * D;
+    const uint32_t t_o = t_lane + T::kO + qt * D;
     // Q: the row's largest element goes to [2^13, 2^14), the sign of the
     // softmax scale onto the elements
     float qf;
@@ -280,7 +302,8 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     int last_meta = 0;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      if (!wait(&sh.s_full[qt], j & 1)) {
+      const uint32_t t_s = t_lane + T::kS + (qt * 2 + (j & 1)) * kTK;
+      if (!wait(&sh.s_full[qt][j & 1], (j >> 1) & 1)) {
         ok = false;
         break;
       }
@@ -296,76 +319,74 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
       // Weights against the reference as it stands, in registers; where a
       // row's maximum is too far ahead of it, it is raised and the weights are
       // formed again (the scores are still there).
-      uint32_t w[kTK / 2];
-      uint64_t sum;
-      float top;
       const uint64_t c1p = pair_const(c1);
-      auto weights = [&](auto masked) {
+      bool raised = sh.raised[ms_] != 0;
+      float alpha = 1.0f;
+      // one pass; true if the weights are in place
+      auto weights = [&](auto masked) -> bool {
         const float sub = kWeightLog2 - (m == -INFINITY ? 0.0f : m);
         const uint64_t subp = pair_const(sub);
-        sum = 0;
-        top = -INFINITY;
+        uint64_t sum = 0;
+        float top = -INFINITY;
+        uint32_t w[kTK / 32][16];
 #pragma unroll
-        for (int c = 0; c < kTK; c += 32) {
+        for (int c = 0; c < kTK / 32; ++c) {
           uint32_t v[32];
-          tmem_ld_32x32b_x32(t_s + c, v);
-          tc_wait_ld();
-          tmem_ld_fence_regs<32>(v);
+          tmem_load32(t_s + 32 * c, v);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             float2 t = unpair(fma2(pair_of(v[i], v[i + 1]), c1p, subp));
             if constexpr (decltype(masked)::value) {
-              if (c + i >= hi || (c + i < lo && c + i >= sk_)) t.x = -INFINITY;
-              if (c + i + 1 >= hi || (c + i + 1 < lo && c + i + 1 >= sk_)) t.y = -INFINITY;
+              const int x = 32 * c + i;
+              if (x >= hi || (x < lo && x >= sk_)) t.x = -INFINITY;
+              if (x + 1 >= hi || (x + 1 < lo && x + 1 >= sk_)) t.y = -INFINITY;
             }
             top = fmaxf(top, fmaxf(t.x, t.y));
             t.x = exp2_approx(t.x), t.y = exp2_approx(t.y);
             sum = add2(sum, pair_of(__float_as_uint(t.x), __float_as_uint(t.y)));
-            w[(c + i) / 2] = f32_to_word<__half>(t.x, t.y);
+            w[c][i / 2] = f32_to_word<__half>(t.x, t.y);
           }
         }
         top -= sub;  // back to the score's logarithm
-      };
-      float alpha = 1.0f;
-      bool raised = sh.raised[ms_] != 0;
-#pragma unroll 1
-      for (int attempt = 0; attempt < 2; ++attempt) {
-        if (plain) weights(std::false_type{});
-        else weights(std::true_type{});
         const bool raise = top > m + kLag;
-        if (!__any_sync(0xFFFFFFFFu, raise) || attempt == 1) break;
-        if (raise) {
-          alpha = exp2_approx(m - top);
-          l2.x *= alpha, l2.y *= alpha;
-          m = top;
+        if (__any_sync(0xFFFFFFFFu, raise)) {
+          if (raise) {
+            // not below the maximum by its rounding either, however large it is
+            const float ref = fmaf(fabsf(top), 0x1p-22f, top);
+            alpha *= exp2_approx(m - ref);
+            m = ref;
+          }
+          raised = true;
+          return false;
         }
-        raised = true;
-      }
-      l2.x += unpair(sum).x, l2.y += unpair(sum).y;
-      // s_full also says that the p v of the tile before is complete
-      if (j > 0 && raised) {
+        l2.x = l2.x * alpha + unpair(sum).x, l2.y = l2.y * alpha + unpair(sum).y;
+        if (j > 0 && raised) {
+          // The p v of the tile before has to be complete (its slot is filled
+          // again only after the weights of this tile).
+          if (!wait(&sh.kv_empty[(j - 1) % kSlots], ((j - 1) / kSlots) & 1)) return true;
+          tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          uint32_t v[16];
-          asm volatile(
-              "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-              : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-                "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-              : "r"(t_o + c)
-              : "memory");
-          tc_wait_ld();
-          tmem_ld_fence_regs<16>(v);
+          for (int c = 0; c < D; c += 32) {
+            const float f = alpha * sh.vfac[ms_][c / 32];
+            uint32_t v[32];
+            tmem_load32(t_o + c, v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * (alpha * sh.vfac[ms_][c / 32]));
-          tmem_st_x16(t_o + c, v);
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+            tmem_st_32x32b_x32(t_o + c, v);
+          }
         }
-      }
 #pragma unroll
-      for (int c = 0; c < kTK / 2; c += 16) tmem_st_x16(t_s + c, reinterpret_cast<const uint32_t(&)[16]>(w[c]));
+        for (int c = 0; c < kTK / 32; ++c) tmem_st_x16(t_s + 16 * c, w[c]);
+        return true;
+      };
+      // the second pass finds every maximum in reach of its reference
+#pragma unroll 1
+      for (int attempt = 0; attempt < 3; ++attempt)
+        if (plain ? weights(std::false_type{}) : weights(std::true_type{})) break;
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full[qt]);
+      if (lane == 0) mbar_arrive(&sh.p_full[qt][j & 1]);
       if (sh.nan_any[ms_]) {
         // a block of NaN among the values reaches the rows that see its key
         for (int blk = 0; blk < C; ++blk)
@@ -389,9 +410,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t v[32];
-        tmem_ld_32x32b_x32(t_o + c, v);
-        tc_wait_ld();
-        tmem_ld_fence_regs<32>(v);
+        tmem_load32(t_o + c, v);
         const bool nan = (nan_cols >> (c / 32)) & 1u;
         const float fac = l == 0.0f ? 0.0f : pow2i(sh.rv[last_meta][c / 32] - 127 - kLiftV) * inv;
 #pragma unroll
@@ -423,11 +442,11 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
             l == 0.0f ? -INFINITY : (m - kWeightLog2 + log2f(l)) * 0.6931471805599453f;
     }
     tc_fence_before();
-  } else if (warp < T::kWarpMma) {
+  } else if (warp < T::kWarpR) {
     // ------------------------------------------------------------ decoding
-    const int t = int(threadIdx.x) - T::kWarpD * 32, dw = t >> 5;
-    const int tok = t % kTK, part = t / kTK;        // the token, and the thread's share of its rows
-    constexpr int kWords = T::kPart / 32;           // blocks of a share
+    const int t = int(threadIdx.x) - T::kWarpD * 32;
+    const int tok = t % kTK, part = t / kTK;  // the token, and the thread's share of its rows
+    constexpr int kWords = T::kPart / 32;     // blocks of a share
     const int32_t* table = a.table + int64_t(b) * a.table_ld;
     auto page_of = [&](int j) -> int32_t {
       const int32_t at = span.tile(j) * kTK + tok;
@@ -438,8 +457,8 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     auto fetch = [&](int j, int32_t page) {
       const int32_t at = span.tile(j) * kTK + tok;
       const bool in = j < n && at < span.hi;
-      const int64_t pg = min(max(page, 0), int32_t(a.pages) - 1);
-      const int64_t rowi = ((pg * a.kv_heads + head) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
+      const int32_t z = min(max(page, 0), int32_t(a.pages) - 1) * a.kv_heads + head;
+      const int64_t rowi = (int64_t(z) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const uint8_t* src = (kv ? v_codes : k_codes) + rowi * (D / 2) + part * (T::kPart / 2);
@@ -449,158 +468,203 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
           raw[kv][i] = in ? *reinterpret_cast<const uint4*>(src + 16 * i) : make_uint4(0, 0, 0, 0);
         sc[kv] = 0;
         if (in) {
-          if constexpr (kWords == 2) sc[kv] = *reinterpret_cast<const uint16_t*>(s);
+          if constexpr (kWords == 1) sc[kv] = *s;
+          else if constexpr (kWords == 2) sc[kv] = *reinterpret_cast<const uint16_t*>(s);
           else sc[kv] = *reinterpret_cast<const uint32_t*>(s);
         }
       }
     };
     int32_t page = page_of(0);
-    int32_t rv[kWords];  // the references of the thread's value blocks
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) rv[i] = -1;
-    bool dead = false;  // a wait ran out: the loop goes on, for the barrier of the group, without its work
     fetch(0, page);
     page = page_of(1);
     for (int j = 0; j < n; ++j) {
-      const int slot = j & 1, meta = j & (kMeta - 1);
+      const int slot = j % kSlots, meta = j & (kMeta - 1);
+      const uint32_t ph = (j / kSlots) & 1;
       // this tile's codes make room for the next tile's, whose loads take as
       // long as the decoding
       uint4 cur[2][kWords];
 #pragma unroll
       for (int i = 0; i < kWords; ++i) cur[0][i] = raw[0][i], cur[1][i] = raw[1][i];
-      // the largest finite scales of the tile, by block
-      int32_t ref[2][kWords];
       const uint32_t scale[2] = {sc[0], sc[1]};
       fetch(j + 1, page);
       page = page_of(j + 2);
-      bool nan = false;
-#pragma unroll
-      for (int i = 0; i < kWords; ++i)
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const int32_t e = (scale[kv] >> (8 * i)) & 0xFF;
-          nan = nan || (kv == 1 && e == 255);
-          const int32_t mx = __reduce_max_sync(0xFFFFFFFFu, e == 255 ? 0 : e);
-          if (lane == 0) sh.red[slot][kv][dw][i] = mx;
-          ref[kv][i] = mx;
-        }
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      // values: running references, raised only when the headroom is used up
-      bool up = false;
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        // the warps that hold the same share of the rows
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          if (w / (kTK / 32) == part) ref[1][i] = max(ref[1][i], sh.red[slot][1][w][i]);
-        float fac = 1.0f;
-        if (rv[i] < 0) {
-          rv[i] = ref[1][i];
-        } else if (ref[1][i] > rv[i] + kHeadroom) {
-          fac = pow2i(rv[i] - ref[1][i]);
-          rv[i] = ref[1][i];
-          up = true;
-        }
-        ref[1][i] = rv[i] - kLiftV;
-        if (tok == 0) {
-          sh.vfac[meta][part * kWords + i] = fac;
-          sh.rv[meta][part * kWords + i] = rv[i];
-        }
-        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, ((scale[1] >> (8 * i)) & 0xFF) == 255u);
-        if (lane == 0) sh.nan_bits[meta][part * kWords + i][tok / 32] = bits;
-      }
-      const bool any = __any_sync(0xFFFFFFFFu, nan);
-      if (lane == 0) {
-        // a bit a warp: no warp waits for another here
-        const uint32_t bit = 1u << dw;
-        if (any) atomicOr(&sh.nan_any[meta], bit);
-        else atomicAnd(&sh.nan_any[meta], ~bit);
-        if (up) atomicOr(&sh.raised[meta], bit);
-        else atomicAnd(&sh.raised[meta], ~bit);
-      }
-      {
-        int32_t mx = 0;
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-#pragma unroll
-          for (int i = 0; i < kWords; ++i) mx = max(mx, sh.red[slot][0][w][i]);
-        if (t == 0) sh.rk[meta] = mx;
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) ref[0][i] = mx - kLiftK;
-      }
+      // the references come after their writer has seen the slot empty
+      if (!wait(&sh.ref_full[slot], ph) || !wait(&sh.kv_empty[slot], ph ^ 1)) break;
+      const int32_t rk = sh.rk[meta] - kLiftK;
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        if (!dead && !wait(kv ? &sh.v_empty[slot] : &sh.k_empty[slot], ((j >> 1) & 1) ^ 1)) dead = true;
-        if (!dead) {
-          uint8_t* dst = (kv ? sv : sk) + slot * T::kKvBytes + tok * 128;
+        uint8_t* dst = (kv ? sv : sk) + slot * T::kKvBytes + tok * 128;
 #pragma unroll
-          for (int i = 0; i < kWords; ++i) {
-            const int32_t e = (scale[kv] >> (8 * i)) & 0xFF;
-            const float f = __uint_as_float(uint32_t(max(e - ref[kv][i] + 127, 0)) << 23);
-            uint32_t fw = f32_to_word<__half>(f, f);
-            if (e == 255) fw = kv ? 0u : 0x7FFF7FFFu;
-            const uint32_t w[4] = {cur[kv][i].x, cur[kv][i].y, cur[kv][i].z, cur[kv][i].w};
+        for (int i = 0; i < kWords; ++i) {
+          const int32_t e = (scale[kv] >> (8 * i)) & 0xFF;
+          const int32_t ref = kv ? sh.rv[meta][part * kWords + i] - kLiftV : rk;
+          const float f = __uint_as_float(uint32_t(max(e - ref + 127, 0)) << 23);
+          uint32_t fw = f32_to_word<__half>(f, f);
+          if (e == 255) fw = kv ? 0u : 0x7FFF7FFFu;
+          const uint32_t w[4] = {cur[kv][i].x, cur[kv][i].y, cur[kv][i].z, cur[kv][i].w};
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint32_t h[4];
-              e2m1x8_to_half(w[x], h);
-              const int d = part * T::kPart + i * 32 + x * 8;
-              *reinterpret_cast<uint4*>(dst + (d / 64) * (kTK * 128) + ((((d % 64) / 8) ^ (tok & 7)) << 4)) =
-                  make_uint4(hmul2(h[0], fw), hmul2(h[1], fw), hmul2(h[2], fw), hmul2(h[3], fw));
+          for (int x = 0; x < 4; ++x) {
+            uint32_t h[4];
+            e2m1x8_to_half(w[x], h);
+            const int d = part * T::kPart + i * 32 + x * 8;
+            *reinterpret_cast<uint4*>(dst + (d / 64) * (kTK * 128) + ((((d % 64) / 8) ^ (tok & 7)) << 4)) =
+                make_uint4(hmul2(h[0], fw), hmul2(h[1], fw), hmul2(h[2], fw), hmul2(h[3], fw));
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.kv_full[slot]);
+    }
+  } else if (warp == T::kWarpR) {
+    // ------------------------------------------------------------ references
+    // a lane takes kTK / 32 tokens of each tile; the loads of kBatch tiles are
+    // in flight together, ahead of the batch that is worked off, and the pages
+    // are looked up a batch before that
+    constexpr int kPer = kTK / 32, kW = (C + 3) / 4, kBatch = 4;
+    const int32_t* table = a.table + int64_t(b) * a.table_ld;
+    uint32_t kw[kBatch][kPer][kW], vw[kBatch][kPer][kW];
+    int32_t pages[kBatch][kPer];
+    auto look_up = [&](int j0) {
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x)
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int32_t at = span.tile(j0 + x) * kTK + i * 32 + lane;
+          pages[x][i] =
+              j0 + x < n && at < span.hi ? table[min(at >> a.page_shift, int32_t(a.table_ld) - 1)] : 0;
+        }
+    };
+    auto fetch = [&](int j0) {
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x)
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int32_t at = span.tile(j0 + x) * kTK + i * 32 + lane;
+          const bool in = j0 + x < n && at < span.hi;
+          const int32_t z = min(max(pages[x][i], 0), int32_t(a.pages) - 1) * a.kv_heads + head;
+          const int64_t at_s = ((int64_t(z) << a.page_shift) + (at & ((1 << a.page_shift) - 1))) * C;
+#pragma unroll
+          for (int y = 0; y < kW; ++y) {
+            kw[x][i][y] = vw[x][i][y] = 0;
+            if (in) {
+              if constexpr (C == 2) {
+                kw[x][i][0] = *reinterpret_cast<const uint16_t*>(a.k_scales + at_s);
+                vw[x][i][0] = *reinterpret_cast<const uint16_t*>(a.v_scales + at_s);
+              } else {
+                kw[x][i][y] = *reinterpret_cast<const uint32_t*>(a.k_scales + at_s + 4 * y);
+                vw[x][i][y] = *reinterpret_cast<const uint32_t*>(a.v_scales + at_s + 4 * y);
+              }
             }
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(kv ? &sh.v_full[slot] : &sh.k_full[slot]);
         }
+    };
+    int32_t rv[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) rv[c] = -1;
+    look_up(0);
+    fetch(0);
+    look_up(kBatch);
+    bool ok = true;
+    for (int j0 = 0; j0 < n && ok; j0 += kBatch) {
+      int32_t mk[kBatch], mv[kBatch][C];
+      uint32_t nan[kBatch][C][kPer];
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        mk[x] = 0;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          mv[x][c] = 0;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int32_t ek = (kw[x][i][c / 4] >> (8 * (c % 4))) & 0xFF;
+            const int32_t ev = (vw[x][i][c / 4] >> (8 * (c % 4))) & 0xFF;
+            mk[x] = max(mk[x], ek == 255 ? 0 : ek);
+            mv[x][c] = max(mv[x][c], ev == 255 ? 0 : ev);
+            nan[x][c][i] = __ballot_sync(0xFFFFFFFFu, ev == 255);
+          }
+        }
+      }
+      fetch(j0 + kBatch);
+      look_up(j0 + 2 * kBatch);
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const int j = j0 + x;
+        if (j >= n || !ok) break;
+        const int slot = j % kSlots, meta = j & (kMeta - 1);
+        const int32_t top_k = __reduce_max_sync(0xFFFFFFFFu, mk[x]);
+        uint32_t up = 0, any = 0;
+        float fac[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          // values: running references, raised only when the headroom is used up
+          const int32_t top_v = __reduce_max_sync(0xFFFFFFFFu, mv[x][c]);
+          fac[c] = 1.0f;
+          if (rv[c] < 0) {
+            rv[c] = top_v;
+          } else if (top_v > rv[c] + kHeadroom) {
+            fac[c] = pow2i(rv[c] - top_v);
+            rv[c] = top_v;
+            up = 1;
+          }
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) any |= nan[x][c][i];
+        }
+        // whoever used this place kMeta tiles ago is done once the slot is empty
+        ok = wait(&sh.kv_empty[slot], ((j / kSlots) & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) {
+          sh.rk[meta] = top_k;
+          sh.raised[meta] = up;
+          sh.nan_any[meta] = any;
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            sh.rv[meta][c] = rv[c];
+            sh.vfac[meta][c] = fac[c];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) sh.nan_bits[meta][c][i] = nan[x][c][i];
+          }
+          mbar_arrive(&sh.ref_full[slot]);
+        }
+        __syncwarp();
       }
     }
   } else if (lane == 0) {
     // ------------------------------------------------------------ MMA issue
     constexpr uint32_t kIdS = (1u << 4) | (uint32_t(kTK >> 3) << 17) | (8u << 24);               // M = 128, N = kTK
     constexpr uint32_t kIdO = (1u << 4) | (1u << 16) | (uint32_t(D >> 3) << 17) | (8u << 24);    // N = D, B MN-major
+    const int qt = warp - T::kWarpMma;
     auto wait1 = [&](uint64_t* bar, uint32_t parity) -> bool {
       if (mbar_wait_bounded(bar, parity, a.wait_limit_cycles, abort_flag)) return true;
       sh.abort_flag = 1;
       return false;
     };
-    auto scores = [&](int qt, int j) {
-      const uint32_t qa = smem_u32(sq + qt * T::kQBytes), kb = smem_u32(sk + (j & 1) * T::kKvBytes);
+    const uint32_t q_lo = desc_lo(smem_u32(sq + qt * T::kQBytes), 16), k_lo = desc_lo(smem_u32(sk), 16),
+                   v_lo = desc_lo(smem_u32(sv), kTK * 128);
+    const uint32_t t_q = tmem + T::kS + qt * 2 * kTK, t_o = tmem + T::kO + qt * D;
+    auto scores = [&](int j) -> bool {
+      const int slot = j % kSlots;
+      if (!wait1(&sh.kv_full[slot], (j / kSlots) & 1)) return false;
+      tc_fence_after();
+      const uint32_t kb = k_lo + uint32_t(slot) * (T::kKvBytes >> 4), t_s = t_q + (j & 1) * kTK;
 #pragma unroll
       for (int d = 0; d < D; d += 16)
-        mma_ss(tmem + T::kS + qt * kTK, desc_k128(qa + (d / 64) * (128 * 128)) + (d % 64) / 8,
-               desc_k128(kb + (d / 64) * (kTK * 128)) + (d % 64) / 8, kIdS, d > 0);
-      tc_commit(&sh.s_full[qt]);
-      mbar_arrive(&sh.s_full[qt]);  // hands on what the decoders wrote for the softmax
+        mma_ss(t_s, q_lo + (d / 64) * (128 * 128 >> 4) + (d % 64) / 8, kb + (d / 64) * (kTK * 128 >> 4) + (d % 64) / 8,
+               kIdS, d > 0);
+      tc_commit(&sh.s_full[qt][j & 1]);
+      mbar_arrive(&sh.s_full[qt][j & 1]);  // hands on what the decoders wrote for the softmax
+      return true;
     };
-    bool ok = n > 0 && wait1(&sh.q_full, 0) && wait1(&sh.k_full[0], 0) && wait1(&sh.v_full[0], 0);
-    tc_fence_after();
-    if (ok) {
-      for (int qt = 0; qt < kNQ; ++qt) scores(qt, 0);
-      tc_commit(&sh.k_empty[0]);
-    }
+    bool ok = n > 0 && wait1(&sh.q_full, 0) && scores(0) && (n == 1 || scores(1));
     for (int j = 0; j < n && ok; ++j) {
-      const uint32_t vb = smem_u32(sv + (j & 1) * T::kKvBytes);
-      for (int qt = 0; qt < kNQ && ok; ++qt) {
-        if (!(ok = wait1(&sh.p_full[qt], j & 1))) break;
-        tc_fence_after();
+      if (!(ok = wait1(&sh.p_full[qt][j & 1], (j >> 1) & 1))) break;
+      tc_fence_after();
+      const uint32_t vb = v_lo + uint32_t(j % kSlots) * (T::kKvBytes >> 4), t_p = t_q + (j & 1) * kTK;
 #pragma unroll
-        for (int t = 0; t < kTK; t += 16)
-          mma_ts(tmem + T::kO + qt * D, tmem + T::kS + qt * kTK + t / 2, desc_mn128(vb, kTK * 128) + t * 8, kIdO,
-                 (j > 0 || t > 0) ? 1u : 0u);
-        if (qt == kNQ - 1) tc_commit(&sh.v_empty[j & 1]);
-        if (j + 1 < n) {
-          if (qt == 0) {
-            const uint32_t ph = ((j + 1) >> 1) & 1;
-            if (!(ok = wait1(&sh.k_full[(j + 1) & 1], ph) && wait1(&sh.v_full[(j + 1) & 1], ph))) break;
-            tc_fence_after();
-          }
-          scores(qt, j + 1);
-          if (qt == kNQ - 1) tc_commit(&sh.k_empty[(j + 1) & 1]);
-        } else {
-          tc_commit(&sh.o_full[qt]);
-        }
-      }
+      for (int t = 0; t < kTK; t += 16) mma_ts(t_o, t_p + t / 2, vb + t * 8, kIdO, j > 0 || t > 0);
+      tc_commit(&sh.kv_empty[j % kSlots]);
+      if (j + 1 == n) tc_commit(&sh.o_full[qt]);
+      if (j + 2 < n) ok = scores(j + 2);  // into the buffer that p v has read
     }
     tc_commit(&sh.done);
     if (!mbar_wait_bounded(&sh.done, 0, a.wait_limit_cycles, nullptr)) sh.abort_flag = 1;

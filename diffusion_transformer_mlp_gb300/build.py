@@ -25,7 +25,7 @@ GEN = os.path.join(BUILD, "gen")
 LIB = os.path.join(BUILD, "libnvfp4fc2.so")
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "mma_peak.cu", "tc_read.cu", "noalloc.cu",
            "mx_quant.cu", "mx_cache.cu", "mx_rows.cu", "mx_linear.cu", "mx_attn.cu", "mx_attn_stream.cu",
-           "mx_attn_chunk.cu"]
+           "mx_attn_chunk.cu", "mx_attn_combine.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-ftz=false", "-prec-div=true",
                      "-prec-sqrt=true", "-fmad=true", "-Xptxas", "-v"]

@@ -9,9 +9,16 @@ namespace nvfp4 {
 
 nvfp4_status check_cache(const mxfp4_cache* cache, int* page_shift, const std::string& nm);
 int64_t attn_stream_workspace(int32_t dim);
-nvfp4_status attn_chunk(const mxfp4_cache* cache, const AttnParams& p, int32_t max_queries, cudaStream_t stream);
+int64_t attn_chunk_workspace(int32_t dim);
+nvfp4_status attn_chunk(const mxfp4_cache* cache, const AttnParams& base, int32_t max_queries, void* workspace,
+                        cudaStream_t stream);
 nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32_t max_queries, void* workspace,
                          cudaStream_t stream);
+
+namespace {
+// Which kernel takes these rows of a (sequence, kv head): see attn_chunk.
+bool many_rows(int64_t max_queries, int64_t group) { return max_queries * group > 16; }
+}  // namespace
 
 }  // namespace nvfp4
 
@@ -20,7 +27,7 @@ using namespace nvfp4;
 extern "C" int64_t mxfp4_attention_workspace_bytes(int32_t kv_heads, int32_t q_heads, int32_t dim,
                                                    int32_t max_queries) {
   if (kv_heads < 1 || q_heads < 1 || max_queries < 1 || (dim != 64 && dim != 128 && dim != 256)) return 0;
-  return attn_stream_workspace(dim);
+  return many_rows(max_queries, q_heads / kv_heads) ? attn_chunk_workspace(dim) : attn_stream_workspace(dim);
 }
 
 extern "C" nvfp4_status mxfp4_cache_attention(const mxfp4_cache* cache, const mxfp4_attention* args,
@@ -67,7 +74,7 @@ extern "C" nvfp4_status mxfp4_cache_attention(const mxfp4_cache* cache, const mx
   p.o_vec = aligned16(g.out) && g.o_st % 8 == 0 && g.o_sh % 8 == 0;
   p.scale_log2 = g.scale * 1.4426950408889634f;
   p.wait_limit_cycles = kAttnWaitLimitCycles;
-  if (int64_t(g.max_queries) * group > 16)
-    return attn_chunk(cache, p, g.max_queries, reinterpret_cast<cudaStream_t>(stream));
+  if (many_rows(g.max_queries, group))
+    return attn_chunk(cache, p, g.max_queries, g.workspace, reinterpret_cast<cudaStream_t>(stream));
   return attn_stream(cache, p, g.max_queries, g.workspace, reinterpret_cast<cudaStream_t>(stream));
 }

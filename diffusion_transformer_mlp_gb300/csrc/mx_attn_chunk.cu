@@ -2,9 +2,11 @@
 // prompt by chunks) on tcgen05.
 //
 // A row is a (query, head of the group) pair: the heads that share a kv head
-// are rows of one tile, so the cache is decoded once for all of them.  A CTA
-// takes kNQ tiles of 128 rows of one (sequence, kv head) and walks the keys
-// that they see in tiles of kTK:
+// are rows of one tile, so the cache is decoded once for all of them.  A
+// segment is kNQ tiles of 128 rows of one (sequence, kv head) with the keys
+// that they see in tiles of kTK; one CTA an SM works through an equal run of
+// all segments' tiles (SplitParams).  Its warps walk the run each for itself,
+// so the decoders are in the next segment while the softmax finishes this one:
 //
 //   warps 0-3, 4-7  softmax of row tile 0, 1: a thread is a row.  Scores come
 //                   from tensor memory, the weights go back there as FP16 over
@@ -41,8 +43,8 @@
 namespace nvfp4 {
 namespace {
 
-constexpr float kWeightLog2 = 10.0f;
 constexpr float kLag = 5.0f;
+constexpr int kLeast = 4;      // tiles of a run at least
 constexpr int kMeta = 8;       // tiles whose references are kept: the decoders are up to 6 ahead of the softmax
 constexpr int kTK = 64;        // keys of a tile
 constexpr int kHeadroom = 8;   // value scales may exceed their reference by 2^8 before it is raised
@@ -58,21 +60,32 @@ struct Chunk {
   static constexpr int kWarpD = kNQ * 4, kWarpR = kWarpD + 4, kWarpMma = kWarpR + 1;
   static constexpr int kThreads = (kWarpMma + kNQ) * 32;
   static constexpr int kPart = D * kTK / 128;         // elements of a decoding thread
-  static constexpr int kSmem = kNQ * kQBytes + 2 * kSlots * kKvBytes + 4096;
+  static constexpr int kStage = 32 * 64;              // a softmax warp's outputs on their way, 32 columns at a time
+  static constexpr int kSmem = kNQ * kQBytes + 2 * kSlots * kKvBytes + kWarpD * kStage + 4096;
   static constexpr uint32_t kS = 0, kO = kNQ * 2 * kTK;  // tensor-memory columns: scores, outputs
   static constexpr uint32_t kTmem = 512;
   static_assert(kNQ * (2 * kTK + D) <= 512, "tensor memory");
   static_assert(kSmem <= 232448, "shared memory");
 };
 
+// A warp's place in the run of its block: a segment, of which the n tiles from
+// seg.t on belong to the run, after g tiles of it; `left` with these to go.
+struct Walk {
+  Cursor seg;
+  int32_t left, n, g;
+};
+
 // Small shared state behind the operands.
 struct Shared {
-  uint64_t q_full, done;
+  uint64_t done;
+  uint64_t q_full[2], o_empty[2];                 // by row tile: Q of a segment is there; its outputs are read
   uint64_t ref_full[4], kv_full[4], kv_empty[4];  // by slot: references, decoded tile, both row tiles' p v complete
   uint64_t s_full[2][2], p_full[2][2];            // by row tile and score buffer
-  uint64_t o_full[2];                             // p v of the last tile is complete
+  uint64_t o_full[2];                             // p v of a segment's last tile is complete
   uint32_t tmem;
   int abort_flag;
+  Cursor first;                // of the run
+  Walk walk[16][2];            // by warp; kept here, as registers are short
   int32_t rk[kMeta];           // reference of the keys' scales
   int32_t rv[kMeta][8];        // of the values' scales by block, as the outputs have it from this tile on
   float vfac[kMeta][8];        // factor onto the outputs before this tile (2^(old - new reference))
@@ -92,6 +105,11 @@ static_assert(sizeof(Shared) <= 4096, "shared state");
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead_bytes) {
   return ((saddr & 0x3FFFFu) >> 4) | ((lead_bytes >> 4) << 16);
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
   asm volatile(
@@ -164,35 +182,49 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// Eight 16-bit elements without the alignment of one load.
+__device__ __noinline__ uint4 load_8x16(const uint16_t* e) {
+  return make_uint4(uint32_t(e[0]) | uint32_t(e[1]) << 16, uint32_t(e[2]) | uint32_t(e[3]) << 16,
+                    uint32_t(e[4]) | uint32_t(e[5]) << 16, uint32_t(e[6]) | uint32_t(e[7]) << 16);
+}
+
 template <int D>
 __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     k_attn_chunk(const uint8_t* __restrict__ k_codes, const uint8_t* __restrict__ v_codes,
-                 const __grid_constant__ AttnParams a) {
+                 const __grid_constant__ SplitParams sp) {
   using T = Chunk<D>;
-  constexpr int C = T::C, kNQ = T::kNQ, kSlots = T::kSlots;
+  constexpr int C = T::C, kNQ = T::kNQ, kSlots = T::kSlots, kRows = 128 * kNQ;
+  const AttnParams& a = sp.a;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sq = smem;                          // [row tile][atom][128 rows][128 bytes]
   uint8_t* sk = sq + kNQ * T::kQBytes;         // [slot][atom][token][128 bytes]
   uint8_t* sv = sk + kSlots * T::kKvBytes;
-  Shared& sh = *reinterpret_cast<Shared*>(sv + kSlots * T::kKvBytes);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* staging = sv + kSlots * T::kKvBytes;
+  Shared& sh = *reinterpret_cast<Shared*>(staging + T::kWarpD * T::kStage);
+  const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   grid_wait();
 
-  const int b = blockIdx.z, head = blockIdx.y;
-  const int32_t len = a.lens[b];
-  const int32_t q0 = a.q_starts != nullptr ? a.q_starts[b] : b;
-  const int32_t nq = a.q_starts != nullptr ? a.q_starts[b + 1] - q0 : 1;
-  const int32_t rows = nq * a.group;
-  // the last rows see the most keys: they come first
-  const int32_t pairs = (rows + 128 * kNQ - 1) / (128 * kNQ);
-  const int32_t pair = pairs - 1 - int32_t(blockIdx.x);
-  if (pair < 0) return;
-  const int32_t row0 = pair * 128 * kNQ;
-  const int32_t last = min(row0 + 128 * kNQ, rows) - 1;
-  const Span span = span_of(a, len, nq, row0 / a.group, last / a.group, kTK);
+  // this block's run of tiles
+  int32_t tiles = 0;
+  {
+    int64_t* prefix = reinterpret_cast<int64_t*>(smem);
+    tile_counts<T::kThreads>(sp, prefix, kRows, kTK);
+    const int64_t total = prefix[a.seqs];
+    const int32_t workers = live_workers(sp, total), w = int32_t(blockIdx.x);
+    if (w < workers) {
+      const int64_t x0 = worker_start(total, w, workers);
+      tiles = int32_t(worker_start(total, w + 1, workers) - x0);
+      if (warp == 0) {
+        Cursor first;
+        cursor_at(first, a, prefix, x0, kRows, kTK);
+        if (lane == 0) sh.first = first, sp.start[w] = first;
+      }
+    }
+  }
+  if (tiles == 0) return;
+  __syncthreads();  // the counts are read, the first tile is known
 
   if (threadIdx.x == 0) {
-    mbar_init(&sh.q_full, kNQ * 4);
     mbar_init(&sh.done, kNQ);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sh.ref_full[i], 1);
@@ -201,8 +233,11 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
       mbar_init(&sh.s_full[i >> 1][i & 1], 2);
       mbar_init(&sh.p_full[i >> 1][i & 1], 4);
     }
-    mbar_init(&sh.o_full[0], 1);
-    mbar_init(&sh.o_full[1], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 4);
+      mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.o_empty[i], 4);
+    }
     sh.abort_flag = 0;
     fence_barrier_init();
   }
@@ -212,7 +247,31 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const volatile int* abort_flag = &sh.abort_flag;
-  const int n = span.n;
+  // Every warp walks the segments of the run for itself.
+  auto next_segment = [&](const Walk& from, Walk& to) {
+    Walk w = from;
+    w.left -= w.n;
+    w.g += w.n;
+    if (w.left > 0) {
+      if (w.n > 0) {
+        w.seg.t += w.n - 1;
+        cursor_next(w.seg, a, kRows, kTK);
+      }
+      w.n = min(w.seg.s.n - w.seg.t, w.left);
+    } else {
+      w.n = 0;
+    }
+    to = w;
+  };
+  // false at the end of the run
+  auto advance = [&](const Walk& from, Walk& to) -> bool {
+    __syncwarp();
+    if (lane == 0) next_segment(from, to);
+    __syncwarp();
+    return to.n > 0;
+  };
+  Walk& wk = sh.walk[warp][0];
+  if (lane == 0) wk.seg = sh.first, wk.left = tiles, wk.n = wk.g = 0;
   // false once a bounded wait anywhere ran out, for the whole warp alike
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     const bool ok = mbar_wait_bounded(bar, parity, a.wait_limit_cycles, abort_flag);
@@ -225,91 +284,100 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     // ------------------------------------------------------------ softmax
     const int qt = warp >> 2, q = warp & 3;
     const int r = q * 32 + lane;  // row of the tile, lane of tensor memory
-    const int32_t row = row0 + qt * 128 + r;
-    const bool real = row < rows;
-    const int32_t qi = real ? row / a.group : 0, hq = head * a.group + (real ? row - qi * a.group : 0);
-    const int32_t pos = len - nq + qi;
-    // the row sees keys j < end with j >= from or j < sinks
-    const int32_t end = !real ? 0 : (a.causal ? min(len, pos + 1) : len);
-    const int32_t from = a.window > 0 ? pos - a.window + 1 : 0;
     const uint32_t t_lane = tmem + (uint32_t(q * 32) << 16);
     const uint32_t t_o = t_lane + T::kO + qt * D;
-    // Q: the row's largest element goes to [2^13, 2^14), the sign of the
-    // softmax scale onto the elements
-    float qf;
-    {
-      const uint16_t* src = static_cast<const uint16_t*>(a.q) + int64_t(q0 + qi) * a.q_st + int64_t(hq) * a.q_sh;
-      // up to 128 elements at a time, their loads all in flight; the row twice,
-      // for its largest element and for the conversion, unless it fits
-      constexpr int kRound = D < 128 ? D : 128;
-      uint32_t w[kRound / 2];
-      auto load = [&](int d0) {
-#pragma unroll
-        for (int i = 0; i < kRound / 8; ++i) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (real) {
-            const uint16_t* e = src + d0 + 8 * i;
-            if (a.q_vec) {
-              v = *reinterpret_cast<const uint4*>(e);
-            } else {
-              v.x = uint32_t(e[0]) | uint32_t(e[1]) << 16, v.y = uint32_t(e[2]) | uint32_t(e[3]) << 16;
-              v.z = uint32_t(e[4]) | uint32_t(e[5]) << 16, v.w = uint32_t(e[6]) | uint32_t(e[7]) << 16;
-            }
-          }
-          w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-        }
-      };
-      auto value = [&](uint32_t x) { return a.bf16 ? word_to_f32<__nv_bfloat16>(x) : word_to_f32<__half>(x); };
-      float am = 0.0f;
-#pragma unroll 1
-      for (int d0 = 0; d0 < D; d0 += kRound) {
-        load(d0);
-#pragma unroll
-        for (int i = 0; i < kRound / 2; ++i) {
-          const float2 t = value(w[i]);
-          am = max_nan(am, max_nan(fabsf(t.x), fabsf(t.y)));
-        }
+    // The warp's queries into shared memory, a row's largest element going to
+    // [2^13, 2^14) and the sign of the softmax scale onto the elements.  D / 8
+    // lanes take a row, so that the loads are of whole rows (a thread that
+    // loads its own row: 13,000 cycles for all rows).  Returns the factor of
+    // this thread's scores.
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRound = 8;
+    auto load_q = [&](const Cursor& c) -> float {
+      const int32_t row = c.rt * kRows + qt * 128 + r;
+      int64_t off = -1;
+      if (row < c.nq * a.group) {
+        const int32_t qi = row / a.group;
+        off = int64_t(c.q0 + qi) * a.q_st + int64_t(c.h * a.group + row - qi * a.group) * a.q_sh;
       }
-      const int32_t eb = int32_t(__float_as_uint(am) >> 23) & 0xFF;
-      const int32_t up = (eb == 0 || eb == 255) ? 0 : min(126, 140 - eb);
-      const float mul = a.scale_log2 < 0.0f ? -pow2i(up) : pow2i(up);
-      qf = fabsf(a.scale_log2) * pow2i(-up);
-      uint8_t* dst = sq + qt * T::kQBytes + r * 128;
+      const int col = lane % kLanes;
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + 8 * col;
+      uint8_t* dst = sq + qt * T::kQBytes + (col / 8) * (128 * 128);
+      int32_t mine = 0;
+      auto place = [&](int i) {
+        const int rq = q * 32 + i * kAtOnce + lane / kLanes;
+        return reinterpret_cast<uint4*>(dst + rq * 128 + (((col & 7) ^ (rq & 7)) << 4));
+      };
+      // raw first, then scaled in place (by the threads that loaded them): two
+      // small loops, as straight-line code that runs once is slow to fetch
 #pragma unroll 1
-      for (int d0 = 0; d0 < D; d0 += kRound) {
-        if (kRound < D) load(d0);
+      for (int i0 = 0; i0 < kLanes; i0 += kRound) {
+        uint4 v[kRound];
 #pragma unroll
-        for (int i = 0; i < kRound / 8; ++i) {
-          uint32_t h[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float2 t = value(w[4 * i + x]);
-            h[x] = f32_to_word<__half>(t.x * mul, t.y * mul);
-          }
-          const int d = d0 + 8 * i;
-          *reinterpret_cast<uint4*>(dst + (d / 64) * (128 * 128) + ((((d % 64) / 8) ^ (r & 7)) << 4)) =
-              make_uint4(h[0], h[1], h[2], h[3]);
+        for (int i = 0; i < kRound; ++i) {
+          const int64_t o = __shfl_sync(0xFFFFFFFFu, off, (i0 + i) * kAtOnce + lane / kLanes);
+          const uint16_t* e = src + o;
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (o >= 0) v[i] = a.q_vec ? *reinterpret_cast<const uint4*>(e) : load_8x16(e);
         }
+#pragma unroll
+        for (int i = 0; i < kRound; ++i) *place(i0 + i) = v[i];
+      }
+#pragma unroll 2
+      for (int i = 0; i < kLanes; ++i) {
+        const uint4 v = *place(i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        // magnitudes of 16-bit floats are in the order of their bits (NaN above all)
+        uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        top = max(top & 0xFFFFu, top >> 16);
+        auto value = [&](uint32_t x) { return a.bf16 ? word_to_f32<__nv_bfloat16>(x) : word_to_f32<__half>(x); };
+        const int32_t eb = int32_t(__float_as_uint(value(top).x) >> 23) & 0xFF;
+        const int32_t up = (eb == 0 || eb == 255) ? 0 : min(126, 140 - eb);
+        const float mul = a.scale_log2 < 0.0f ? -pow2i(up) : pow2i(up);
+        uint32_t h[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float2 t = value(w[x]);
+          h[x] = f32_to_word<__half>(t.x * mul, t.y * mul);
+        }
+        *place(i) = make_uint4(h[0], h[1], h[2], h[3]);
+        const int32_t theirs = __shfl_sync(0xFFFFFFFFu, up, (lane % kAtOnce) * kLanes);
+        if (lane / kAtOnce == i) mine = theirs;
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.q_full);
-    }
-
+      if (lane == 0) mbar_arrive(&sh.q_full[qt]);
+      return fabsf(a.scale_log2) * pow2i(-mine);
+    };
+    advance(wk, wk);
+    float qf = load_q(wk.seg);
+    bool ok = true;
+    for (int seg = 0; ok; ++seg) {
+    const Walk& w = sh.walk[warp][seg & 1];
+    const Cursor& cu = w.seg;
+    const int32_t n = w.n, g = w.g;
+    const int32_t row = cu.rt * kRows + qt * 128 + r;
+    const bool real = row < cu.nq * a.group;
+    const int32_t pos = cu.len - cu.nq + (real ? row / a.group : 0);
+    // the row sees keys j < end with j >= from or j < sinks
+    const int32_t end = !real ? 0 : (a.causal ? min(cu.len, pos + 1) : cu.len);
+    const int32_t from = a.window > 0 ? pos - a.window + 1 : 0;
     float m = -INFINITY;
     float2 l2 = make_float2(0.0f, 0.0f);
     uint32_t nan_cols = 0;  // blocks of the output that are NaN
     int last_meta = 0;
-    bool ok = true;
     for (int j = 0; j < n; ++j) {
-      const uint32_t t_s = t_lane + T::kS + (qt * 2 + (j & 1)) * kTK;
-      if (!wait(&sh.s_full[qt][j & 1], (j >> 1) & 1)) {
+      const int x = g + j;  // of the run's tiles
+      const uint32_t t_s = t_lane + T::kS + (qt * 2 + (x & 1)) * kTK;
+      if (!wait(&sh.s_full[qt][x & 1], (x >> 1) & 1)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const int ms_ = j & (kMeta - 1);
-      const int32_t tok0 = span.tile(j) * kTK;
+      const int ms_ = x & (kMeta - 1);
+      const int32_t tok0 = cu.s.tile(cu.t + j) * kTK;
       const float c1 = qf * pow2i(sh.rk[ms_] - 127 - kLiftK);
       last_meta = ms_;
       const bool all = tok0 + kTK <= end && (tok0 >= from || tok0 + kTK <= a.sinks);
@@ -337,9 +405,9 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
           for (int i = 0; i < 32; i += 2) {
             float2 t = unpair(fma2(pair_of(v[i], v[i + 1]), c1p, subp));
             if constexpr (decltype(masked)::value) {
-              const int x = 32 * c + i;
-              if (x >= hi || (x < lo && x >= sk_)) t.x = -INFINITY;
-              if (x + 1 >= hi || (x + 1 < lo && x + 1 >= sk_)) t.y = -INFINITY;
+              const int y = 32 * c + i;
+              if (y >= hi || (y < lo && y >= sk_)) t.x = -INFINITY;
+              if (y + 1 >= hi || (y + 1 < lo && y + 1 >= sk_)) t.y = -INFINITY;
             }
             top = fmaxf(top, fmaxf(t.x, t.y));
             t.x = exp2_approx(t.x), t.y = exp2_approx(t.y);
@@ -363,7 +431,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
         if (j > 0 && raised) {
           // The p v of the tile before has to be complete (its slot is filled
           // again only after the weights of this tile).
-          if (!wait(&sh.kv_empty[(j - 1) % kSlots], ((j - 1) / kSlots) & 1)) return true;
+          if (!wait(&sh.kv_empty[(x - 1) % kSlots], ((x - 1) / kSlots) & 1)) return true;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
@@ -386,7 +454,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full[qt][j & 1]);
+      if (lane == 0) mbar_arrive(&sh.p_full[qt][x & 1]);
       if (sh.nan_any[ms_]) {
         // a block of NaN among the values reaches the rows that see its key
         for (int blk = 0; blk < C; ++blk)
@@ -400,64 +468,97 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
           }
       }
     }
+    if (!ok) break;
+    // the next segment's queries first: the MMAs that read this segment's are
+    // complete, and the next ones can start while the outputs are written
+    Walk& next = sh.walk[warp][(seg + 1) & 1];
+    const bool more = advance(w, next);
+    if (more) qf = load_q(next.seg);
     // ---- output
-    if (ok && n > 0) ok = wait(&sh.o_full[qt], 0);
+    ok = wait(&sh.o_full[qt], seg & 1);
     tc_fence_after();
+    if (!ok) break;
+    const bool whole = cu.t == 0 && w.n == cu.s.n;
+    const int32_t qi = real ? row / a.group : 0, hq = cu.h * a.group + (real ? row - qi * a.group : 0);
     const float l = l2.x + l2.y;
-    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-    if (ok) {
-      uint16_t* dst = static_cast<uint16_t*>(a.out) + int64_t(q0 + qi) * a.o_st + int64_t(hq) * a.o_sh;
+    const float inv = !whole ? 1.0f : (l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l));
+    const int64_t part = int64_t(blockIdx.x) * 2 + (seg > 0 ? 1 : 0);
+    const int64_t off = real ? int64_t(cu.q0 + qi) * a.o_st + int64_t(hq) * a.o_sh : -1;
+    uint8_t* stage = staging + warp * T::kStage;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t v[32];
-        tmem_load32(t_o + c, v);
-        const bool nan = (nan_cols >> (c / 32)) & 1u;
-        const float fac = l == 0.0f ? 0.0f : pow2i(sh.rv[last_meta][c / 32] - 127 - kLiftV) * inv;
-#pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-          uint32_t w[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            // nothing seen: tensor memory may hold anything
-            float e0 = l == 0.0f ? 0.0f : __uint_as_float(v[i + 2 * x]) * fac;
-            float e1 = l == 0.0f ? 0.0f : __uint_as_float(v[i + 2 * x + 1]) * fac;
-            if (nan) e0 = e1 = __uint_as_float(0x7FFFFFFFu);
-            w[x] = a.bf16 ? f32_to_word<__nv_bfloat16>(e0, e1) : f32_to_word<__half>(e0, e1);
-          }
-          if (real) {
-            if (a.o_vec) {
-              *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                dst[c + i + 2 * x] = uint16_t(w[x]);
-                dst[c + i + 2 * x + 1] = uint16_t(w[x] >> 16);
-              }
-            }
-          }
-        }
+    for (int c = 0; c < D; c += 32) {
+      uint32_t v[32];
+      tmem_load32(t_o + c, v);
+      if (c + 32 == D) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.o_empty[qt]);
       }
-      if (real && a.lse != nullptr)
-        a.lse[int64_t(q0 + qi) * (a.kv_heads * a.group) + hq] =
-            l == 0.0f ? -INFINITY : (m - kWeightLog2 + log2f(l)) * 0.6931471805599453f;
+      // c / 32 is a reference's block, and its factor the same for all rows
+      const float fac = pow2i(sh.rv[last_meta][c / 32] - 127 - kLiftV) * inv;
+      if ((nan_cols >> (c / 32)) & 1u) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0x7FFFFFFFu;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * fac);
+      }
+      if (!whole) {
+        // [D / 4][rows] of four columns: a warp writes 512 bytes at a time
+        uint4* d = reinterpret_cast<uint4*>(sp.part_o) + (part * (D / 4) + c / 4) * kRows + qt * 128 + r;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i * kRows] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        continue;
+      }
+      // through shared memory, so that four lanes write 64 bytes of a row
+      // (a thread that writes its own row: 4,400 to 10,000 cycles)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t h[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float f0 = __uint_as_float(v[8 * i + 2 * x]), f1 = __uint_as_float(v[8 * i + 2 * x + 1]);
+          h[x] = a.bf16 ? f32_to_word<__nv_bfloat16>(f0, f1) : f32_to_word<__half>(f0, f1);
+        }
+        *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rr = i * 8 + lane / 4;
+        const uint4 h = *reinterpret_cast<const uint4*>(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, rr);
+        if (o >= 0) store_o8_words(a, static_cast<uint16_t*>(a.out) + o + c + (lane & 3) * 8, h);
+      }
+      __syncwarp();
     }
-    tc_fence_before();
+    if (!whole)
+      sp.part_ml[part * kRows + qt * 128 + r] = make_float2(m, l);
+    else if (real && a.lse != nullptr)
+      a.lse[int64_t(cu.q0 + qi) * (a.kv_heads * a.group) + hq] =
+          l == 0.0f ? -INFINITY : (m - kWeightLog2 + log2f(l)) * 0.6931471805599453f;
+    if (!more) break;
+    }
   } else if (warp < T::kWarpR) {
     // ------------------------------------------------------------ decoding
     const int t = int(threadIdx.x) - T::kWarpD * 32;
     const int tok = t % kTK, part = t / kTK;  // the token, and the thread's share of its rows
     constexpr int kWords = T::kPart / 32;     // blocks of a share
-    const int32_t* table = a.table + int64_t(b) * a.table_ld;
+    bool ok = true;
+    while (ok && advance(wk, wk)) {
+    const Cursor cu = wk.seg;
+    const int32_t n = wk.n, g = wk.g;
+    const int32_t* table = a.table + int64_t(cu.b) * a.table_ld;
     auto page_of = [&](int j) -> int32_t {
-      const int32_t at = span.tile(j) * kTK + tok;
-      return j < n && at < span.hi ? table[min(at >> a.page_shift, int32_t(a.table_ld) - 1)] : 0;
+      const int32_t at = cu.s.tile(cu.t + j) * kTK + tok;
+      return j < n && at < cu.s.hi ? table[min(at >> a.page_shift, int32_t(a.table_ld) - 1)] : 0;
     };
     uint4 raw[2][kWords];  // codes of K and V
     uint32_t sc[2] = {0, 0};
     auto fetch = [&](int j, int32_t page) {
-      const int32_t at = span.tile(j) * kTK + tok;
-      const bool in = j < n && at < span.hi;
-      const int32_t z = min(max(page, 0), int32_t(a.pages) - 1) * a.kv_heads + head;
+      const int32_t at = cu.s.tile(cu.t + j) * kTK + tok;
+      const bool in = j < n && at < cu.s.hi;
+      const int32_t z = min(max(page, 0), int32_t(a.pages) - 1) * a.kv_heads + cu.h;
       const int64_t rowi = (int64_t(z) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
@@ -478,8 +579,8 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     fetch(0, page);
     page = page_of(1);
     for (int j = 0; j < n; ++j) {
-      const int slot = j % kSlots, meta = j & (kMeta - 1);
-      const uint32_t ph = (j / kSlots) & 1;
+      const int x0 = g + j, slot = x0 % kSlots, meta = x0 & (kMeta - 1);
+      const uint32_t ph = (x0 / kSlots) & 1;
       // this tile's codes make room for the next tile's, whose loads take as
       // long as the decoding
       uint4 cur[2][kWords];
@@ -489,19 +590,21 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
       fetch(j + 1, page);
       page = page_of(j + 2);
       // the references come after their writer has seen the slot empty
-      if (!wait(&sh.ref_full[slot], ph) || !wait(&sh.kv_empty[slot], ph ^ 1)) break;
+      ok = wait(&sh.ref_full[slot], ph) && wait(&sh.kv_empty[slot], ph ^ 1);
+      if (!ok) break;
       const int32_t rk = sh.rk[meta] - kLiftK;
-#pragma unroll
+#pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
         uint8_t* dst = (kv ? sv : sk) + slot * T::kKvBytes + tok * 128;
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
-          const int32_t e = (scale[kv] >> (8 * i)) & 0xFF;
+          const int32_t e = ((kv ? scale[1] : scale[0]) >> (8 * i)) & 0xFF;
           const int32_t ref = kv ? sh.rv[meta][part * kWords + i] - kLiftV : rk;
           const float f = __uint_as_float(uint32_t(max(e - ref + 127, 0)) << 23);
           uint32_t fw = f32_to_word<__half>(f, f);
           if (e == 255) fw = kv ? 0u : 0x7FFF7FFFu;
-          const uint32_t w[4] = {cur[kv][i].x, cur[kv][i].y, cur[kv][i].z, cur[kv][i].w};
+          const uint32_t w[4] = {kv ? cur[1][i].x : cur[0][i].x, kv ? cur[1][i].y : cur[0][i].y,
+                                 kv ? cur[1][i].z : cur[0][i].z, kv ? cur[1][i].w : cur[0][i].w};
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             uint32_t h[4];
@@ -516,157 +619,158 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.kv_full[slot]);
     }
+    }
   } else if (warp == T::kWarpR) {
     // ------------------------------------------------------------ references
-    // a lane takes kTK / 32 tokens of each tile; the loads of kBatch tiles are
-    // in flight together, ahead of the batch that is worked off, and the pages
-    // are looked up a batch before that
-    constexpr int kPer = kTK / 32, kW = (C + 3) / 4, kBatch = 4;
-    const int32_t* table = a.table + int64_t(b) * a.table_ld;
-    uint32_t kw[kBatch][kPer][kW], vw[kBatch][kPer][kW];
-    int32_t pages[kBatch][kPer];
-    auto look_up = [&](int j0) {
+    // a lane takes kTK / 32 tokens of each tile; scales are loaded a tile ahead,
+    // their pages looked up a tile before that
+    constexpr int kPer = kTK / 32, kW = (C + 3) / 4;
+    bool ok = true;
+    while (ok && advance(wk, wk)) {
+    const Cursor cu = wk.seg;
+    const int32_t n = wk.n, g = wk.g;
+    const int32_t* table = a.table + int64_t(cu.b) * a.table_ld;
+    uint32_t kw[kPer][kW], vw[kPer][kW];
+    int32_t pages[kPer];
+    auto look_up = [&](int j) {
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x)
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int32_t at = span.tile(j0 + x) * kTK + i * 32 + lane;
-          pages[x][i] =
-              j0 + x < n && at < span.hi ? table[min(at >> a.page_shift, int32_t(a.table_ld) - 1)] : 0;
-        }
+      for (int i = 0; i < kPer; ++i) {
+        const int32_t at = cu.s.tile(cu.t + j) * kTK + i * 32 + lane;
+        pages[i] = j < n && at < cu.s.hi ? table[min(at >> a.page_shift, int32_t(a.table_ld) - 1)] : 0;
+      }
     };
-    auto fetch = [&](int j0) {
+    auto fetch = [&](int j) {
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x)
+      for (int i = 0; i < kPer; ++i) {
+        const int32_t at = cu.s.tile(cu.t + j) * kTK + i * 32 + lane;
+        const int32_t z = min(max(pages[i], 0), int32_t(a.pages) - 1) * a.kv_heads + cu.h;
+        const int64_t at_s = ((int64_t(z) << a.page_shift) + (at & ((1 << a.page_shift) - 1))) * C;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int32_t at = span.tile(j0 + x) * kTK + i * 32 + lane;
-          const bool in = j0 + x < n && at < span.hi;
-          const int32_t z = min(max(pages[x][i], 0), int32_t(a.pages) - 1) * a.kv_heads + head;
-          const int64_t at_s = ((int64_t(z) << a.page_shift) + (at & ((1 << a.page_shift) - 1))) * C;
-#pragma unroll
-          for (int y = 0; y < kW; ++y) {
-            kw[x][i][y] = vw[x][i][y] = 0;
-            if (in) {
-              if constexpr (C == 2) {
-                kw[x][i][0] = *reinterpret_cast<const uint16_t*>(a.k_scales + at_s);
-                vw[x][i][0] = *reinterpret_cast<const uint16_t*>(a.v_scales + at_s);
-              } else {
-                kw[x][i][y] = *reinterpret_cast<const uint32_t*>(a.k_scales + at_s + 4 * y);
-                vw[x][i][y] = *reinterpret_cast<const uint32_t*>(a.v_scales + at_s + 4 * y);
-              }
+        for (int y = 0; y < kW; ++y) {
+          kw[i][y] = vw[i][y] = 0;
+          if (j < n && at < cu.s.hi) {
+            if constexpr (C == 2) {
+              kw[i][0] = *reinterpret_cast<const uint16_t*>(a.k_scales + at_s);
+              vw[i][0] = *reinterpret_cast<const uint16_t*>(a.v_scales + at_s);
+            } else {
+              kw[i][y] = *reinterpret_cast<const uint32_t*>(a.k_scales + at_s + 4 * y);
+              vw[i][y] = *reinterpret_cast<const uint32_t*>(a.v_scales + at_s + 4 * y);
             }
           }
         }
+      }
     };
-    int32_t rv[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) rv[c] = -1;
+    int32_t rv = -1;  // of block `lane`
     look_up(0);
     fetch(0);
-    look_up(kBatch);
-    bool ok = true;
-    for (int j0 = 0; j0 < n && ok; j0 += kBatch) {
-      int32_t mk[kBatch], mv[kBatch][C];
-      uint32_t nan[kBatch][C][kPer];
+    look_up(1);
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      int32_t mk = 0, mv[C];
+      uint32_t nan[C][kPer], any = 0;
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) {
-        mk[x] = 0;
+      for (int c = 0; c < C; ++c) {
+        mv[c] = 0;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          mv[x][c] = 0;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int32_t ek = (kw[x][i][c / 4] >> (8 * (c % 4))) & 0xFF;
-            const int32_t ev = (vw[x][i][c / 4] >> (8 * (c % 4))) & 0xFF;
-            mk[x] = max(mk[x], ek == 255 ? 0 : ek);
-            mv[x][c] = max(mv[x][c], ev == 255 ? 0 : ev);
-            nan[x][c][i] = __ballot_sync(0xFFFFFFFFu, ev == 255);
-          }
+        for (int i = 0; i < kPer; ++i) {
+          const int32_t ek = (kw[i][c / 4] >> (8 * (c % 4))) & 0xFF;
+          const int32_t ev = (vw[i][c / 4] >> (8 * (c % 4))) & 0xFF;
+          mk = max(mk, ek == 255 ? 0 : ek);
+          mv[c] = max(mv[c], ev == 255 ? 0 : ev);
+          nan[c][i] = __ballot_sync(0xFFFFFFFFu, ev == 255);
+          any |= nan[c][i];
         }
       }
-      fetch(j0 + kBatch);
-      look_up(j0 + 2 * kBatch);
+      fetch(j + 1);
+      look_up(j + 2);
+      const int slot = (g + j) % kSlots, meta = (g + j) & (kMeta - 1);
+      mk = __reduce_max_sync(0xFFFFFFFFu, mk);
+      // lane c takes block c from here
+      int32_t top = 0;
+      uint32_t bits[kPer];
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) {
-        const int j = j0 + x;
-        if (j >= n || !ok) break;
-        const int slot = j % kSlots, meta = j & (kMeta - 1);
-        const int32_t top_k = __reduce_max_sync(0xFFFFFFFFu, mk[x]);
-        uint32_t up = 0, any = 0;
-        float fac[C];
+      for (int c = 0; c < C; ++c) {
+        const int32_t t = __reduce_max_sync(0xFFFFFFFFu, mv[c]);
+        if (lane == c) {
+          top = t;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          // values: running references, raised only when the headroom is used up
-          const int32_t top_v = __reduce_max_sync(0xFFFFFFFFu, mv[x][c]);
-          fac[c] = 1.0f;
-          if (rv[c] < 0) {
-            rv[c] = top_v;
-          } else if (top_v > rv[c] + kHeadroom) {
-            fac[c] = pow2i(rv[c] - top_v);
-            rv[c] = top_v;
-            up = 1;
-          }
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) any |= nan[x][c][i];
+          for (int i = 0; i < kPer; ++i) bits[i] = nan[c][i];
         }
-        // whoever used this place kMeta tiles ago is done once the slot is empty
-        ok = wait(&sh.kv_empty[slot], ((j / kSlots) & 1) ^ 1);
-        if (!ok) break;
-        if (lane == 0) {
-          sh.rk[meta] = top_k;
-          sh.raised[meta] = up;
-          sh.nan_any[meta] = any;
-#pragma unroll
-          for (int c = 0; c < C; ++c) {
-            sh.rv[meta][c] = rv[c];
-            sh.vfac[meta][c] = fac[c];
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) sh.nan_bits[meta][c][i] = nan[x][c][i];
-          }
-          mbar_arrive(&sh.ref_full[slot]);
-        }
-        __syncwarp();
       }
+      // values: running references, raised only when the headroom is used up
+      float fac = 1.0f;
+      const bool up = rv >= 0 && top > rv + kHeadroom;
+      if (up) fac = pow2i(rv - top);
+      if (up || rv < 0) rv = top;
+      const bool raised = __any_sync(0xFFFFFFFFu, lane < C && up);
+      // whoever used this place kMeta tiles ago is done once the slot is empty
+      ok = wait(&sh.kv_empty[slot], (((g + j) / kSlots) & 1) ^ 1);
+      if (!ok) break;
+      if (lane < C) {
+        sh.rv[meta][lane] = rv;
+        sh.vfac[meta][lane] = fac;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) sh.nan_bits[meta][lane][i] = bits[i];
+      }
+      if (lane == 0) {
+        sh.rk[meta] = mk;
+        sh.raised[meta] = raised;
+        sh.nan_any[meta] = any;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.ref_full[slot]);
     }
-  } else if (lane == 0) {
+    }
+  } else {
     // ------------------------------------------------------------ MMA issue
+    // The whole warp runs this and one thread is elected where it issues: the
+    // descriptors then stay in uniform registers (issued under lane == 0, an
+    // MMA took 25 instructions and the issuing warp was the bottleneck).
     constexpr uint32_t kIdS = (1u << 4) | (uint32_t(kTK >> 3) << 17) | (8u << 24);               // M = 128, N = kTK
     constexpr uint32_t kIdO = (1u << 4) | (1u << 16) | (uint32_t(D >> 3) << 17) | (8u << 24);    // N = D, B MN-major
     const int qt = warp - T::kWarpMma;
-    auto wait1 = [&](uint64_t* bar, uint32_t parity) -> bool {
-      if (mbar_wait_bounded(bar, parity, a.wait_limit_cycles, abort_flag)) return true;
-      sh.abort_flag = 1;
-      return false;
-    };
     const uint32_t q_lo = desc_lo(smem_u32(sq + qt * T::kQBytes), 16), k_lo = desc_lo(smem_u32(sk), 16),
                    v_lo = desc_lo(smem_u32(sv), kTK * 128);
     const uint32_t t_q = tmem + T::kS + qt * 2 * kTK, t_o = tmem + T::kO + qt * D;
-    auto scores = [&](int j) -> bool {
-      const int slot = j % kSlots;
-      if (!wait1(&sh.kv_full[slot], (j / kSlots) & 1)) return false;
+    auto scores = [&](int x) -> bool {
+      const int slot = x % kSlots;
+      if (!wait(&sh.kv_full[slot], (x / kSlots) & 1)) return false;
       tc_fence_after();
-      const uint32_t kb = k_lo + uint32_t(slot) * (T::kKvBytes >> 4), t_s = t_q + (j & 1) * kTK;
+      const uint32_t kb = k_lo + uint32_t(slot) * (T::kKvBytes >> 4), t_s = t_q + (x & 1) * kTK;
+      if (elect_one()) {
 #pragma unroll
-      for (int d = 0; d < D; d += 16)
-        mma_ss(t_s, q_lo + (d / 64) * (128 * 128 >> 4) + (d % 64) / 8, kb + (d / 64) * (kTK * 128 >> 4) + (d % 64) / 8,
-               kIdS, d > 0);
-      tc_commit(&sh.s_full[qt][j & 1]);
-      mbar_arrive(&sh.s_full[qt][j & 1]);  // hands on what the decoders wrote for the softmax
+        for (int d = 0; d < D; d += 16)
+          mma_ss(t_s, q_lo + (d / 64) * (128 * 128 >> 4) + (d % 64) / 8,
+                 kb + (d / 64) * (kTK * 128 >> 4) + (d % 64) / 8, kIdS, d > 0);
+        tc_commit(&sh.s_full[qt][x & 1]);
+        mbar_arrive(&sh.s_full[qt][x & 1]);  // hands on what the decoders wrote for the softmax
+      }
+      __syncwarp();
       return true;
     };
-    bool ok = n > 0 && wait1(&sh.q_full, 0) && scores(0) && (n == 1 || scores(1));
-    for (int j = 0; j < n && ok; ++j) {
-      if (!(ok = wait1(&sh.p_full[qt][j & 1], (j >> 1) & 1))) break;
-      tc_fence_after();
-      const uint32_t vb = v_lo + uint32_t(j % kSlots) * (T::kKvBytes >> 4), t_p = t_q + (j & 1) * kTK;
+    bool ok = true;
+    for (int seg = 0; ok && advance(wk, wk); ++seg) {
+      const int32_t n = __shfl_sync(0xFFFFFFFFu, wk.n, 0), g = __shfl_sync(0xFFFFFFFFu, wk.g, 0);
+      ok = wait(&sh.q_full[qt], seg & 1) && scores(g) && (n == 1 || scores(g + 1));
+      for (int j = 0; j < n && ok; ++j) {
+        const int x = g + j;
+        ok = wait(&sh.p_full[qt][x & 1], (x >> 1) & 1) &&
+             (j > 0 || seg == 0 || wait(&sh.o_empty[qt], (seg - 1) & 1));  // the outputs before are read
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t vb = v_lo + uint32_t(x % kSlots) * (T::kKvBytes >> 4), t_p = t_q + (x & 1) * kTK;
+        if (elect_one()) {
 #pragma unroll
-      for (int t = 0; t < kTK; t += 16) mma_ts(t_o, t_p + t / 2, vb + t * 8, kIdO, j > 0 || t > 0);
-      tc_commit(&sh.kv_empty[j % kSlots]);
-      if (j + 1 == n) tc_commit(&sh.o_full[qt]);
-      if (j + 2 < n) ok = scores(j + 2);  // into the buffer that p v has read
+          for (int t = 0; t < kTK; t += 16) mma_ts(t_o, t_p + t / 2, vb + t * 8, kIdO, j > 0 || t > 0);
+          tc_commit(&sh.kv_empty[x % kSlots]);
+          if (j + 1 == n) tc_commit(&sh.o_full[qt]);
+        }
+        __syncwarp();
+        if (j + 2 < n) ok = scores(x + 2);  // into the buffer that p v has read
+      }
     }
-    tc_commit(&sh.done);
+    if (elect_one()) tc_commit(&sh.done);
+    __syncwarp();
     if (!mbar_wait_bounded(&sh.done, 0, a.wait_limit_cycles, nullptr)) sh.abort_flag = 1;
   }
   tc_fence_before();
@@ -680,34 +784,54 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
   }
 }
 
+int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
+int64_t partial_rows(int32_t dim) { return 2 * int64_t(sm_count()) * (dim == 256 ? 128 : 256); }
+
 template <int D>
-nvfp4_status chunk_launch(const mxfp4_cache* cache, const AttnParams& p, int32_t max_queries, cudaStream_t stream) {
+nvfp4_status chunk_launch(const mxfp4_cache* cache, const SplitParams& p, cudaStream_t stream) {
   using T = Chunk<D>;
   auto kern = k_attn_chunk<D>;
   static std::atomic<uint64_t> ready{0};
   nvfp4_status st = allow_smem(reinterpret_cast<const void*>(kern), T::kSmem, ready);
   if (st != NVFP4_OK) return st;
-  const int64_t pairs = (int64_t(max_queries) * p.group + 128 * T::kNQ - 1) / (128 * T::kNQ);
-  AttnParams q = p;
-  for (int32_t b = 0; b < p.seqs; b += 65535) {  // the grid's z
-    q.seqs = std::min(65535, p.seqs - b);
-    q.table = p.table + int64_t(b) * p.table_ld;
-    q.lens = p.lens + b;
-    if (p.q_starts != nullptr) q.q_starts = p.q_starts + b;
-    st = launch("launch k_attn_chunk", kern, dim3(unsigned(pairs), unsigned(p.kv_heads), unsigned(q.seqs)),
-                dim3(T::kThreads), T::kSmem, 0, stream, static_cast<const uint8_t*>(cache->k_codes),
-                static_cast<const uint8_t*>(cache->v_codes), q);
-    if (st != NVFP4_OK) return st;
-  }
-  return NVFP4_OK;
+  st = launch("launch k_attn_chunk", kern, dim3(unsigned(p.workers)), dim3(T::kThreads), T::kSmem, 0, stream,
+              static_cast<const uint8_t*>(cache->k_codes), static_cast<const uint8_t*>(cache->v_codes), p);
+  if (st != NVFP4_OK) return st;
+  return attn_join(D, kTK, p, stream);
 }
 
 }  // namespace
 
-nvfp4_status attn_chunk(const mxfp4_cache* cache, const AttnParams& p, int32_t max_queries, cudaStream_t stream) {
-  if (cache->dim == 64) return chunk_launch<64>(cache, p, max_queries, stream);
-  if (cache->dim == 128) return chunk_launch<128>(cache, p, max_queries, stream);
-  return chunk_launch<256>(cache, p, max_queries, stream);
+int64_t attn_chunk_workspace(int32_t dim) {
+  return align256(partial_rows(dim) * dim * 4) + align256(partial_rows(dim) * 8) + align256((kMaxSeqs + 1) * 8) +
+         align256(sm_count() * int64_t(sizeof(Cursor)));
+}
+
+nvfp4_status attn_chunk(const mxfp4_cache* cache, const AttnParams& base, int32_t max_queries, void* workspace,
+                        cudaStream_t stream) {
+  const int32_t dim = cache->dim;
+  SplitParams sp;
+  sp.a = base;
+  sp.workers = sm_count();
+  sp.least = kLeast;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  sp.part_o = reinterpret_cast<float*>(ws);
+  sp.part_ml = reinterpret_cast<float2*>(ws + align256(partial_rows(dim) * dim * 4));
+  sp.prefix = reinterpret_cast<int64_t*>(ws + align256(partial_rows(dim) * dim * 4) + align256(partial_rows(dim) * 8));
+  sp.start = reinterpret_cast<Cursor*>(reinterpret_cast<uint8_t*>(sp.prefix) + align256((kMaxSeqs + 1) * 8));
+  // kMaxSeqs sequences a launch; the workspace is reused in stream order.
+  for (int32_t b = 0; b < base.seqs; b += kMaxSeqs) {
+    sp.a.seqs = std::min(kMaxSeqs, base.seqs - b);
+    sp.a.table = base.table + int64_t(b) * base.table_ld;
+    sp.a.lens = base.lens + b;
+    split_queries(sp.a, base, b);
+    nvfp4_status st;
+    if (dim == 64) st = chunk_launch<64>(cache, sp, stream);
+    else if (dim == 128) st = chunk_launch<128>(cache, sp, stream);
+    else st = chunk_launch<256>(cache, sp, stream);
+    if (st != NVFP4_OK) return st;
+  }
+  return NVFP4_OK;
 }
 
 }  // namespace nvfp4

@@ -37,14 +37,7 @@
 // .trans for V it gets 4 codes of token t in its low and of token t + 1 in
 // its high half.
 //
-// Work is dealt in equal runs of tiles over all warps of the grid, whatever
-// the sequences' lengths: the tiles of all (sequence, row tile, kv head)
-// segments in a row, worker w taking [total w / W, total (w+1) / W).  A worker
-// writes a segment's output itself if it has all of it, else its partial
-// (maximum, sum, unnormalised output) goes to the workspace: at most two a
-// worker, its first and its last segment.  k_attn_combine joins them in
-// worker order.  The split depends on the lengths alone, so results are
-// reproducible.
+// Work is dealt over all warps of the grid as SplitParams describes.
 #include <algorithm>
 #include <atomic>
 #include <string>
@@ -60,7 +53,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxSeqs = 1024;  // sequences of one launch (their tile counts sit in shared memory)
 
 // A stage of the ring holds kTok keys, worked off kSub at a time.
 template <int D, int kRows>
@@ -86,102 +78,7 @@ struct Tile {
   static_assert(kCtas * (kSmem + 1024) <= 233472, "blocks an SM");
 };
 
-constexpr float kWeightLog2 = 10.0f;  // weights are held times 2^10
 constexpr float kLag = 5.0f;          // the softmax reference may lag the maximum by 2^5
-
-struct StreamParams {
-  AttnParams a;
-  int32_t workers;
-  float* part_o;     // [2 * workers][kRows][D]
-  float2* part_ml;   // [2 * workers][kRows]  (maximum, sum)
-  int64_t* prefix;   // [seqs + 1] tiles before each sequence, written by block 0 for k_attn_combine
-};
-
-__device__ __forceinline__ int32_t seq_queries(const AttnParams& a, int32_t b) {
-  return a.q_starts != nullptr ? a.q_starts[b + 1] - a.q_starts[b] : 1;
-}
-
-// Span of row tile rt (rows [rt * rows, ...) of the nq * group rows).
-__device__ __forceinline__ Span row_span(const AttnParams& a, int32_t len, int32_t nq, int32_t rt, int32_t rows,
-                                         int32_t tok) {
-  const int32_t last = min((rt + 1) * rows, nq * a.group) - 1;
-  return span_of(a, len, nq, rt * rows / a.group, last / a.group, tok);
-}
-
-// Tiles of sequence b over all its row tiles and kv heads.
-__device__ __forceinline__ int64_t seq_tiles(const AttnParams& a, int32_t b, int32_t rows, int32_t tok) {
-  const int32_t len = a.lens[b], nq = seq_queries(a, b);
-  int64_t n = 0;
-  for (int32_t rt = 0; rt * rows < nq * a.group; ++rt) n += row_span(a, len, nq, rt, rows, tok).n;
-  return n * a.kv_heads;
-}
-
-// Workers that get a tile: with fewer tiles than warps, the first ones get one
-// each, so that all workers of a segment's range have a partial of it.
-__device__ __forceinline__ int32_t live_workers(int64_t total, int32_t workers) {
-  return int32_t(min(total, int64_t(workers)));
-}
-__device__ __forceinline__ int64_t worker_start(int64_t total, int32_t w, int32_t workers) {
-  return total * w / workers;
-}
-// The worker whose run holds tile x: the largest w with worker_start(w) <= x.
-__device__ __forceinline__ int32_t worker_of(int64_t total, int64_t x, int32_t workers) {
-  return int32_t(((x + 1) * workers - 1) / total);
-}
-
-// Position in the list of all tiles.
-struct Cursor {
-  int32_t b, rt, h, t;  // t: tile of the segment
-  int32_t len, nq, q0;
-  Span s;
-};
-
-__device__ __forceinline__ void cursor_seq(Cursor& c, const AttnParams& a) {
-  c.len = a.lens[c.b];
-  c.nq = seq_queries(a, c.b);
-  c.q0 = a.q_starts != nullptr ? a.q_starts[c.b] : c.b;
-}
-
-__device__ __forceinline__ void cursor_at(Cursor& c, const AttnParams& a, const int64_t* prefix, int64_t x,
-                                          int32_t rows, int32_t tok) {
-  int32_t lo = 0, hi = a.seqs;  // prefix[lo] <= x < prefix[hi]
-  while (hi - lo > 1) {
-    const int32_t mid = (lo + hi) >> 1;
-    if (prefix[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  c.b = lo;
-  cursor_seq(c, a);
-  int64_t rem = x - prefix[lo];
-  for (c.rt = 0;; ++c.rt) {
-    c.s = row_span(a, c.len, c.nq, c.rt, rows, tok);
-    const int64_t n = int64_t(c.s.n) * a.kv_heads;
-    if (rem < n) break;
-    rem -= n;
-  }
-  c.h = int32_t(rem / c.s.n);
-  c.t = int32_t(rem - int64_t(c.h) * c.s.n);
-}
-
-// The next tile; the caller knows that there is one.
-__device__ __forceinline__ void cursor_next(Cursor& c, const AttnParams& a, int32_t rows, int32_t tok) {
-  if (++c.t < c.s.n) return;
-  c.t = 0;
-  if (++c.h < a.kv_heads) return;
-  c.h = 0;
-  do {
-    if ((c.rt + 1) * rows < c.nq * a.group) {
-      ++c.rt;
-    } else {
-      c.rt = 0;
-      do {
-        ++c.b;
-        cursor_seq(c, a);
-      } while (c.nq <= 0);
-    }
-    c.s = row_span(a, c.len, c.nq, c.rt, rows, tok);
-  } while (c.s.n == 0);
-}
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -249,22 +146,6 @@ __device__ __forceinline__ void load_q8(const AttnParams& a, const uint16_t* src
     f[2 * i] = t.x, f[2 * i + 1] = t.y;
   }
 }
-__device__ __forceinline__ void store_o8(const AttnParams& a, uint16_t* dst, const float (&f)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = a.bf16 ? f32_to_word<__nv_bfloat16>(f[2 * i], f[2 * i + 1]) : f32_to_word<__half>(f[2 * i], f[2 * i + 1]);
-  if (a.o_vec) {
-    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      dst[2 * i] = uint16_t(w[i]);
-      dst[2 * i + 1] = uint16_t(w[i] >> 16);
-    }
-  }
-}
-
 // Scale word of a block in the high exponent bits: 2^(E-127) for 1 <= E <= 254,
 // 0 for E = 0 (a block below 2^-124 has no weight in a score), infinity for
 // 255, whose zero codes then give NaN.
@@ -276,7 +157,7 @@ __device__ __forceinline__ float e8m0_byte(uint32_t w, int i) {
 template <int D, int kRows>
 __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
     k_attn_stream(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                  const __grid_constant__ StreamParams sp) {
+                  const __grid_constant__ SplitParams sp) {
   using T = Tile<D, kRows>;
   constexpr int C = T::C, kTok = T::kTok, kSub = T::kSub, NT = kSub / 8;
   constexpr int R = kRows / 8;   // rows of a thread: g, and g + 8
@@ -300,48 +181,12 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
     prefetch_tmap(&tmap_v);
   }
   grid_wait();
-  // tiles before each sequence: every thread sums a run of sequences, the
-  // first warp scans the runs' sums
-  {
-    int64_t* run = prefix + kMaxSeqs + 1;
-    const int per = (a.seqs + kThreads - 1) / kThreads;
-    const int b0 = min(int(threadIdx.x) * per, a.seqs), b1 = min(b0 + per, a.seqs);
-    int64_t sum = 0;
-    for (int b = b0; b < b1; ++b) {
-      prefix[b] = sum;
-      sum += seq_tiles(a, b, kRows, kTok);
-    }
-    run[threadIdx.x] = sum;
-    __syncthreads();
-    if (warp == 0) {
-      int64_t v[kThreads / 32], s = 0;
-#pragma unroll
-      for (int i = 0; i < kThreads / 32; ++i) {
-        v[i] = s;
-        s += run[lane * (kThreads / 32) + i];
-      }
-      int64_t inc = s;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= o) inc += u;
-      }
-      const int64_t before = inc - s;
-#pragma unroll
-      for (int i = 0; i < kThreads / 32; ++i) run[lane * (kThreads / 32) + i] = before + v[i];
-      if (lane == 31) prefix[a.seqs] = inc;
-    }
-    __syncthreads();
-    for (int b = b0; b < b1; ++b) prefix[b] += run[threadIdx.x];
-    __syncthreads();
-    if (blockIdx.x == 0)
-      for (int b = threadIdx.x; b <= a.seqs; b += kThreads) sp.prefix[b] = prefix[b];
-  }
+  tile_counts<kThreads>(sp, prefix, kRows, kTok);
 
   const int64_t total = prefix[a.seqs];
   // the first workers lie in different blocks: few tiles spread over all SMs
   const int32_t worker = warp * int32_t(gridDim.x) + int32_t(blockIdx.x);
-  const int32_t workers = live_workers(total, sp.workers);
+  const int32_t workers = live_workers(sp, total);
   const int64_t x0 = worker < workers ? worker_start(total, worker, workers) : 0;
   const int32_t tiles = worker < workers ? int32_t(worker_start(total, worker + 1, workers) - x0) : 0;
   Cursor cu;
@@ -852,130 +697,21 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
   }
 }
 
-// Joins the partials of the segments that more than one worker had, and
-// writes the rows that see no key at all.  One block a segment: the rows'
-// weights of all partials first (a thread each), then the outputs, eight
-// columns a thread with the partials dealt over kSlices threads.
-constexpr int kCombineThreads = 256;
-constexpr int kMostParts = 512;  // partials whose weights are held at a time
-
 template <int D, int kRows>
-__global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_constant__ StreamParams sp) {
-  const AttnParams& a = sp.a;
-  constexpr int kTok = Tile<D, kRows>::kTok;
-  constexpr int kItems = kRows * D / 8;
-  constexpr int kSlices = kItems < kCombineThreads ? kCombineThreads / kItems : 1;
-  constexpr int kPass = kItems < kCombineThreads ? kItems : kCombineThreads;
-  __shared__ float weight[kMostParts / 8][kRows];
-  __shared__ float red_m[kCombineThreads / 32][kRows], row_m[kRows], row_l[kRows];
-  __shared__ float4 sum[kSlices > 1 ? (kSlices - 1) * kPass * 2 : 1];
-  grid_wait();
-  const int32_t h = blockIdx.x, rt = blockIdx.y, b = blockIdx.z;
-  const int32_t len = a.lens[b], nq = seq_queries(a, b);
-  const int32_t q0 = a.q_starts != nullptr ? a.q_starts[b] : b;
-  const int32_t live = min(kRows, nq * a.group - rt * kRows);
-  if (live <= 0) return;
-  int64_t first = sp.prefix[b];
-  for (int32_t r = 0; r < rt; ++r) first += int64_t(row_span(a, len, nq, r, kRows, kTok).n) * a.kv_heads;
-  const int32_t n = row_span(a, len, nq, rt, kRows, kTok).n;
-  first += int64_t(h) * n;
-  const int64_t total = sp.prefix[a.seqs];
-  const int32_t workers = live_workers(total, sp.workers);
-  int32_t w0 = 0, parts = 0, slot0 = 0;
-  if (n > 0) {
-    w0 = worker_of(total, first, workers);
-    parts = worker_of(total, first + n - 1, workers) - w0 + 1;
-    if (parts == 1) return;  // written by its worker
-    slot0 = worker_start(total, w0, workers) == first ? 0 : 1;
-  }
-  auto slot_of = [&](int32_t i) { return int64_t(w0 + i) * 2 + (i == 0 ? slot0 : 0); };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // the rows' maxima over all partials: kRows threads a partial
-  {
-    const int r = threadIdx.x % kRows;
-    float m = -INFINITY;
-    for (int32_t i = threadIdx.x / kRows; i < parts; i += kCombineThreads / kRows)
-      m = fmaxf(m, sp.part_ml[slot_of(i) * kRows + r].x);
-#pragma unroll
-    for (int o = kRows; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if (lane < kRows) red_m[warp][lane] = m;
-    __syncthreads();
-    if (threadIdx.x < kRows) {
-      m = red_m[0][threadIdx.x];
-#pragma unroll
-      for (int i = 1; i < kCombineThreads / 32; ++i) m = fmaxf(m, red_m[i][threadIdx.x]);
-      row_m[threadIdx.x] = m;
-    }
-    __syncthreads();
-  }
-  const int item = threadIdx.x % kPass, slice = threadIdx.x / kPass;
-  float lsum = 0.0f;  // of row threadIdx.x, in partial order (first kRows threads)
-  for (int32_t pass = 0; pass < kItems; pass += kPass) {
-    const int32_t r = (pass + item) / (D / 8), d = (pass + item) % (D / 8) * 8;
-    float f[8] = {};
-    for (int32_t i0 = 0; i0 < parts; i0 += kMostParts / 8) {
-      const int32_t cnt = min(parts - i0, kMostParts / 8);
-      for (int32_t i = threadIdx.x; i < cnt * kRows; i += kCombineThreads) {
-        const float m = row_m[i % kRows], pm = sp.part_ml[slot_of(i0 + i / kRows) * kRows + i % kRows].x;
-        weight[i / kRows][i % kRows] = exp2_approx(pm - (m == -INFINITY ? 0.0f : m));
-      }
-      __syncthreads();
-      if (pass == 0 && threadIdx.x < kRows)
-        for (int32_t i = 0; i < cnt; ++i)
-          lsum += sp.part_ml[slot_of(i0 + i) * kRows + threadIdx.x].y * weight[i][threadIdx.x];
-#pragma unroll 4
-      for (int32_t i = slice; i < cnt; i += kSlices) {
-        const float4* src = reinterpret_cast<const float4*>(sp.part_o + (slot_of(i0 + i) * kRows + r) * D + d);
-        const float4 u = src[0], v = src[1];
-        const float c = weight[i][r];
-        f[0] += u.x * c, f[1] += u.y * c, f[2] += u.z * c, f[3] += u.w * c;
-        f[4] += v.x * c, f[5] += v.y * c, f[6] += v.z * c, f[7] += v.w * c;
-      }
-      __syncthreads();
-    }
-    if (pass == 0 && threadIdx.x < kRows) row_l[threadIdx.x] = lsum;
-    if (kSlices > 1 && slice > 0) {
-      sum[((slice - 1) * kPass + item) * 2] = make_float4(f[0], f[1], f[2], f[3]);
-      sum[((slice - 1) * kPass + item) * 2 + 1] = make_float4(f[4], f[5], f[6], f[7]);
-    }
-    __syncthreads();
-    if (slice == 0 && r < live) {
-#pragma unroll
-      for (int x = 0; x < kSlices - 1; ++x) {
-        const float4 u = sum[(x * kPass + item) * 2], v = sum[(x * kPass + item) * 2 + 1];
-        f[0] += u.x, f[1] += u.y, f[2] += u.z, f[3] += u.w;
-        f[4] += v.x, f[5] += v.y, f[6] += v.z, f[7] += v.w;
-      }
-      const float l = row_l[r];
-      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] *= inv;
-      const int32_t row = rt * kRows + r, qi = row / a.group, hq = h * a.group + row - qi * a.group;
-      store_o8(a, static_cast<uint16_t*>(a.out) + int64_t(q0 + qi) * a.o_st + int64_t(hq) * a.o_sh + d, f);
-      if (d == 0 && a.lse != nullptr)
-        a.lse[int64_t(q0 + qi) * (a.kv_heads * a.group) + hq] =
-            l == 0.0f ? -INFINITY : (row_m[r] - kWeightLog2 + log2f(l)) * 0.6931471805599453f;
-    }
-    __syncthreads();
-  }
-}
-
-template <int D, int kRows>
-nvfp4_status stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, const StreamParams& sp, int row_tiles,
+nvfp4_status stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams& sp, int row_tiles,
                            cudaStream_t stream) {
   using T = Tile<D, kRows>;
   auto kern = k_attn_stream<D, kRows>;
   static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
   nvfp4_status st = allow_smem(reinterpret_cast<const void*>(kern), T::kSmem, ready);
   if (st != NVFP4_OK) return st;
-  StreamParams p = sp;
+  SplitParams p = sp;
   p.workers = T::kCtas * sm_count() * kWarps;
+  p.least = 1;
   st = launch("launch k_attn_stream", kern, dim3(unsigned(p.workers / kWarps)), dim3(kThreads), T::kSmem, 0, stream, tk,
               tv, p);
   if (st != NVFP4_OK) return st;
-  return launch("launch k_attn_combine", k_attn_combine<D, kRows>,
-                dim3(unsigned(p.a.kv_heads), unsigned(row_tiles), unsigned(p.a.seqs)), dim3(kCombineThreads), 0, 0,
-                stream, p);
+  return attn_combine(D, kRows, T::kTok, row_tiles, p, stream);
 }
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -1004,7 +740,7 @@ nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32
   if (st == NVFP4_OK)
     st = make_map(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, cache->v_codes, 3, dims, strides, bx, swz, "V codes");
   if (st != NVFP4_OK) return st;
-  StreamParams sp;
+  SplitParams sp;
   sp.a = base;
   const int64_t rows_max = int64_t(max_queries) * base.group;
   const int32_t rows = rows_max <= 8 ? 8 : 16;
@@ -1020,13 +756,7 @@ nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32
     sp.a.seqs = std::min(kMaxSeqs, base.seqs - b);
     sp.a.table = base.table + int64_t(b) * base.table_ld;
     sp.a.lens = base.lens + b;
-    if (base.q_starts != nullptr) {
-      sp.a.q_starts = base.q_starts + b;
-    } else {
-      sp.a.q = static_cast<const uint16_t*>(base.q) + int64_t(b) * base.q_st;
-      sp.a.out = static_cast<uint16_t*>(base.out) + int64_t(b) * base.o_st;
-      if (base.lse != nullptr) sp.a.lse = base.lse + int64_t(b) * base.kv_heads * base.group;
-    }
+    split_queries(sp.a, base, b);
     if (dim == 64) st = rows == 8 ? stream_launch<64, 8>(tk, tv, sp, int(row_tiles), stream)
                                   : stream_launch<64, 16>(tk, tv, sp, int(row_tiles), stream);
     else if (dim == 128) st = rows == 8 ? stream_launch<128, 8>(tk, tv, sp, int(row_tiles), stream)

@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     // lanes take a row, so that the loads are of whole rows (a thread that
     // loads its own row: 13,000 cycles for all rows).  Returns the factor of
     // this thread's scores.
-    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRound = 8;
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRound = kLanes < 16 ? kLanes : 16;
     auto load_q = [&](const Cursor& c) -> float {
       const int32_t row = c.rt * kRows + qt * 128 + r;
       int64_t off = -1;
@@ -357,7 +357,8 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     for (int seg = 0; ok; ++seg) {
     const Walk& w = sh.walk[warp][seg & 1];
     const Cursor& cu = w.seg;
-    const int32_t n = w.n, g = w.g;
+    const int32_t n = w.n, g = w.g, sink_tiles = cu.s.sink_tiles - cu.t, first_tile = cu.t,
+                  lo_tile = cu.s.lo_tile - sink_tiles;
     const int32_t row = cu.rt * kRows + qt * 128 + r;
     const bool real = row < cu.nq * a.group;
     const int32_t pos = cu.len - cu.nq + (real ? row / a.group : 0);
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
       }
       tc_fence_after();
       const int ms_ = x & (kMeta - 1);
-      const int32_t tok0 = cu.s.tile(cu.t + j) * kTK;
+      const int32_t tok0 = (j < sink_tiles ? j + first_tile : j + lo_tile) * kTK;
       const float c1 = qf * pow2i(sh.rk[ms_] - 127 - kLiftK);
       last_meta = ms_;
       const bool all = tok0 + kTK <= end && (tok0 >= from || tok0 + kTK <= a.sinks);

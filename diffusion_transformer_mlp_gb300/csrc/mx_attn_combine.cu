@@ -151,20 +151,19 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ Split
   const int32_t parts = worker_of(total, first + c.s.n - 1, workers) - (w - 1) + 1;
   const int32_t slot0 = worker_start(total, w - 1, workers) == first ? 0 : 1;
   auto part_of = [&](int32_t i) { return int64_t(w - 1 + i) * 2 + (i == 0 ? slot0 : 0); };
-  float m = -INFINITY;
-#pragma unroll 4
-  for (int32_t i = 0; i < parts; ++i) m = fmaxf(m, sp.part_ml[part_of(i) * kRows + r].x);
-  const float ref = m == -INFINITY ? 0.0f : m;
-  float f[8] = {}, l = 0.0f;
+  // in one pass, against the maximum so far
+  float f[8] = {}, l = 0.0f, m = -INFINITY;
 #pragma unroll 4
   for (int32_t i = 0; i < parts; ++i) {
     const float2 ml = sp.part_ml[part_of(i) * kRows + r];
     const float4* src = reinterpret_cast<const float4*>(sp.part_o) + (part_of(i) * (D / 4) + d / 4) * kRows + r;
     const float4 u = src[0], v = src[kRows];
-    const float g = exp2_approx(ml.x - ref);
-    l += ml.y * g;
-    f[0] += u.x * g, f[1] += u.y * g, f[2] += u.z * g, f[3] += u.w * g;
-    f[4] += v.x * g, f[5] += v.y * g, f[6] += v.z * g, f[7] += v.w * g;
+    const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.0f : top;
+    const float old = exp2_approx(m - ref), g = exp2_approx(ml.x - ref);
+    m = top;
+    l = l * old + ml.y * g;
+    f[0] = f[0] * old + u.x * g, f[1] = f[1] * old + u.y * g, f[2] = f[2] * old + u.z * g, f[3] = f[3] * old + u.w * g;
+    f[4] = f[4] * old + v.x * g, f[5] = f[5] * old + v.y * g, f[6] = f[6] * old + v.z * g, f[7] = f[7] * old + v.w * g;
   }
   const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
 #pragma unroll

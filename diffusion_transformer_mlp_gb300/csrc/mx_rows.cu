@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint64_t* done = empty + S::kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = p.split > 1 ? int(cluster_ctarank()) : 0;
   const int w_row = (int(blockIdx.x) / p.split) * kWRows;
   const int a_row = int(blockIdx.y) * NT;
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       if (++slot == S::kStages) slot = 0, phase ^= 1u;
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     // M = 128 weight rows, N = NT activation rows, both E2M1 and K-major
     constexpr uint32_t kIdesc =
         (1u << 7) | (1u << 10) | (uint32_t(NT >> 3) << 17) | kIdescE8m0 | (uint32_t(kWRows >> 4) << 24);
@@ -261,35 +261,39 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t phase = 0, sf_slot = 0;
     bool ok = true;
     for (int kt = kt0; kt < kt1; ++kt) {
-      if (!mbar_wait_bounded(&full[slot], phase, p.wait_limit_cycles, const_cast<const int*>(abort_flag))) {
-        ok = false;
-        break;
-      }
+      ok = mbar_wait_bounded(&full[slot], phase, p.wait_limit_cycles, const_cast<const int*>(abort_flag));
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
       tc_fence_after();
       const uint32_t st = smem_u32(ring + slot * S::kStage);
       const uint32_t sfw = tmem + NT + sf_slot * kSfCols, sfa = sfw + 8;
       const uint64_t dw = desc_k128(st), da = desc_k128(st + kWBytes);
       const int ng = 2 * kt + 1 < p.groups ? 2 : 1;
+      // elected: the descriptors stay in uniform registers (under lane == 0,
+      // 8 x 14,336 x 5,376: 12.5 us, now 10.2)
+      if (elect_one()) {
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        if (g >= ng) break;
-        tc_cp_scales(sfw + 4 * g, st + kWBytes + S::kABytes + 512 * g);
-        tc_cp_scales(sfa + 4 * g, st + kWBytes + S::kABytes + kSfBytes + 512 * g);
+        for (int g = 0; g < 2; ++g) {
+          if (g >= ng) break;
+          tc_cp_scales(sfw + 4 * g, st + kWBytes + S::kABytes + 512 * g);
+          tc_cp_scales(sfa + 4 * g, st + kWBytes + S::kABytes + kSfBytes + 512 * g);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          // K = 64 step: 32 bytes further along the row; its two scales are
-          // bytes 2h, 2h + 1 of the group's scale word
-          const uint32_t id = kIdesc | (uint32_t(2 * h) << 4) | (uint32_t(2 * h) << 29);
-          tc_mma_mxf4(tmem, dw + 4 * g + 2 * h, da + 4 * g + 2 * h, id, sfw + 4 * g, sfa + 4 * g,
-                      (kt > kt0 || g > 0 || h > 0) ? 1u : 0u);
+          for (int h = 0; h < 2; ++h) {
+            // K = 64 step: 32 bytes further along the row; its two scales are
+            // bytes 2h, 2h + 1 of the group's scale word
+            const uint32_t id = kIdesc | (uint32_t(2 * h) << 4) | (uint32_t(2 * h) << 29);
+            tc_mma_mxf4(tmem, dw + 4 * g + 2 * h, da + 4 * g + 2 * h, id, sfw + 4 * g, sfa + 4 * g,
+                        (kt > kt0 || g > 0 || h > 0) ? 1u : 0u);
+          }
         }
+        tc_commit(&empty[slot]);
       }
-      tc_commit(&empty[slot]);
+      __syncwarp();
       sf_slot ^= 1u;
       if (++slot == S::kStages) slot = 0, phase ^= 1u;
     }
     if (!ok) *abort_flag = 1;
-    tc_commit(done);
+    if (elect_one()) tc_commit(done);
   }
 
   // Quantised activation: thread t of warps 2..5 takes block t % 8 of row

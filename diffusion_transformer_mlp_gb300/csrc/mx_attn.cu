@@ -16,8 +16,17 @@ nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32
                          cudaStream_t stream);
 
 namespace {
-// Which kernel takes these rows of a (sequence, kv head): see attn_chunk.
-bool many_rows(int64_t max_queries, int64_t group) { return max_queries * group > 16; }
+// Which kernel takes the rows (queries x heads of the group) of a sequence's kv
+// head: k_attn_chunk works on 256 of them (dim 256: 128) at once, k_attn_stream
+// on 8 or 16, each time decoding the keys anew.  32 sequences of 8,000 keys, 8
+// kv heads, stream / chunk in us:
+//   rows        16         48         64        128
+//   dim  64   63 / 284  159 / 284  205 / 279  396 / 287
+//   dim 128   96 / 309  242 / 310  313 / 309  610 / 292
+//   dim 256  325 / 441  874 / 451 1121 / 447
+// (dim 256, 24 rows: 580 / 441).  One sequence of 16,000 keys, dim 128: 26 / 43,
+// 30 / 43, 38 / 43, 56 / 41.
+bool many_rows(int32_t dim, int64_t rows) { return rows > (dim == 256 ? 16 : 64); }
 }  // namespace
 
 }  // namespace nvfp4
@@ -27,7 +36,7 @@ using namespace nvfp4;
 extern "C" int64_t mxfp4_attention_workspace_bytes(int32_t kv_heads, int32_t q_heads, int32_t dim,
                                                    int32_t max_queries) {
   if (kv_heads < 1 || q_heads < 1 || max_queries < 1 || (dim != 64 && dim != 128 && dim != 256)) return 0;
-  return many_rows(max_queries, q_heads / kv_heads) ? attn_chunk_workspace(dim) : attn_stream_workspace(dim);
+  return many_rows(dim, int64_t(max_queries) * (q_heads / kv_heads)) ? attn_chunk_workspace(dim) : attn_stream_workspace(dim);
 }
 
 extern "C" nvfp4_status mxfp4_cache_attention(const mxfp4_cache* cache, const mxfp4_attention* args,
@@ -74,7 +83,7 @@ extern "C" nvfp4_status mxfp4_cache_attention(const mxfp4_cache* cache, const mx
   p.o_vec = aligned16(g.out) && g.o_st % 8 == 0 && g.o_sh % 8 == 0;
   p.scale_log2 = g.scale * 1.4426950408889634f;
   p.wait_limit_cycles = kAttnWaitLimitCycles;
-  if (many_rows(g.max_queries, group))
+  if (many_rows(cache->dim, int64_t(g.max_queries) * group))
     return attn_chunk(cache, p, g.max_queries, g.workspace, reinterpret_cast<cudaStream_t>(stream));
   return attn_stream(cache, p, g.max_queries, g.workspace, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -87,7 +87,7 @@ __device__ __forceinline__ void tma_load_3d_plain(void* dst, const CUtensorMap* 
 struct SplitParams {
   AttnParams a;
   int32_t workers;
-  int32_t least;     // tiles of a run, if there are that many
+  int32_t least, even;  // tiles of a run: at least, if there are that many; see live_workers
   float* part_o;     // [2 * workers][rows][D] (k_attn_chunk: [D / 4][rows][4]), not divided by the sum
   float2* part_ml;   // [2 * workers][rows]  (reference, sum)
   int64_t* prefix;   // [seqs + 1] tiles before each sequence, written by block 0 for k_attn_combine
@@ -105,10 +105,12 @@ __device__ __forceinline__ Span row_span(const AttnParams& a, int32_t len, int32
   return span_of(a, len, nq, rt * rows / a.group, last / a.group, tok);
 }
 
-// Workers that get tiles: with few tiles the first ones get `least` or more
-// each, so that all workers of a segment's range have a partial of it.
+// Workers that get tiles, all of them one or more, so that all workers of a
+// segment's range have a partial of it.  Of runs of up to `even` tiles all get
+// the longest: a worker less is partials less to join.
 __device__ __forceinline__ int32_t live_workers(const SplitParams& sp, int64_t total) {
-  return int32_t(min((total + sp.least - 1) / sp.least, int64_t(sp.workers)));
+  const int64_t run = max(int64_t(sp.least), (total + sp.workers - 1) / sp.workers);
+  return int32_t(run <= sp.even ? (total + run - 1) / run : min(int64_t(sp.workers), (total + sp.least - 1) / sp.least));
 }
 __device__ __forceinline__ int64_t worker_start(int64_t total, int32_t w, int32_t workers) {
   return total * w / workers;

@@ -809,7 +809,7 @@ nvfp4_status attn_chunk(const mxfp4_cache* cache, const AttnParams& base, int32_
   SplitParams sp;
   sp.a = base;
   sp.workers = sm_count();
-  sp.least = kLeast;
+  sp.least = kLeast, sp.even = 0;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   sp.part_o = reinterpret_cast<float*>(ws);
   sp.part_ml = reinterpret_cast<float2*>(ws + align256(partial_rows(dim) * dim * 4));

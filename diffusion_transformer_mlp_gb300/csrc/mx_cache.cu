@@ -37,15 +37,15 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t st = is_v ? v_st : k_st, sh = is_v ? v_sh : k_sh;
   uint8_t* codes = is_v ? vc : kc;
   uint8_t* scales = is_v ? vs : ks;
-  const int32_t lanes = c.dim / 16;  // lanes of one row: 4, 8 or 16, so a row never leaves its warp
-  const int64_t items = tokens * c.heads * lanes;
+  const int32_t lane_bits = c.dim == 64 ? 2 : (c.dim == 128 ? 3 : 4);  // a row never leaves its warp
+  const int64_t items = (tokens * c.heads) << lane_bits;
   // the whole warp stays in the loop for the shuffles
   for (int64_t i0 = int64_t(blockIdx.x) * kThreads + (threadIdx.x & ~31); i0 < items;
        i0 += int64_t(gridDim.x) * kThreads) {
     const int64_t i = i0 + (threadIdx.x & 31);
-    const int64_t rowi = i / lanes;
-    const int32_t s = int32_t(i - rowi * lanes);
-    const int64_t tok = rowi / c.heads;
+    const int64_t rowi = i >> lane_bits;
+    const int32_t s = int32_t(i - (rowi << lane_bits));
+    const int64_t tok = items <= 0x7FFFFFFF ? int64_t(uint32_t(rowi) / uint32_t(c.heads)) : rowi / c.heads;
     const int32_t head = int32_t(rowi - tok * c.heads);
     const bool in = i < items;
     const int64_t slot = in ? slots[tok] : -1;
@@ -110,15 +110,15 @@ __global__ void __launch_bounds__(kThreads)
     base[threadIdx.x] = cache_row(c, page, 0, int32_t(pos & ((1 << c.page_shift) - 1)));
   }
   __syncthreads();
-  const int32_t lanes = c.dim / 16;
-  const int32_t per_tok = c.heads * lanes;
+  const int32_t lane_bits = c.dim == 64 ? 2 : (c.dim == 128 ? 3 : 4);
+  const int32_t per_tok = c.heads << lane_bits;
   const int32_t items = n * per_tok;
   for (int32_t i = threadIdx.x; i < 2 * items; i += kThreads) {
     const bool is_v = i >= items;
     const int32_t r = is_v ? i - items : i;
-    const int32_t tok = r / per_tok;
+    const int32_t tok = int32_t(uint32_t(r) / uint32_t(per_tok));
     const int32_t hs = r - tok * per_tok;
-    const int32_t head = hs / lanes, s = hs - head * lanes;
+    const int32_t head = hs >> lane_bits, s = hs - (head << lane_bits);
     const int64_t row = base[tok] + (int64_t(head) << c.page_shift);
     const uint2 q = *reinterpret_cast<const uint2*>((is_v ? vc : kc) + row * (c.dim / 2) + s * 8);
     float f[16];

@@ -106,42 +106,54 @@ __device__ __forceinline__ uint32_t f32_to_word<__nv_bfloat16>(float lo, float h
   return bf16x2_rn(lo, hi);
 }
 
+// 32 bytes.  Written at once where the address allows it: two stores of 16
+// bytes by neighbouring lanes each touch half of every 32-byte sector (4,096 x
+// 14,336 to bf16: 38 us, at once 28).  Read they are two loads, of which the
+// second finds its sectors in L1 (quantising the same: 27 us, at once 33).
+__device__ __forceinline__ void load32b(const void* p, uint32_t (&w)[8]) {
+  const uint4 x = static_cast<const uint4*>(p)[0], y = static_cast<const uint4*>(p)[1];
+  w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+}
+__device__ __forceinline__ void store32b(void* p, const uint32_t (&w)[8]) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 // 16 consecutive elements at a 16-byte aligned address.
 template <typename T>
 __device__ __forceinline__ void load16(const T* __restrict__ p, float (&f)[16]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4* q = reinterpret_cast<const float4*>(p);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = q[i];
-      f[4 * i] = v.x, f[4 * i + 1] = v.y, f[4 * i + 2] = v.z, f[4 * i + 3] = v.w;
-    }
-  } else {
-    const uint4* q = reinterpret_cast<const uint4*>(p);
+  for (int h = 0; h < int(sizeof(T)) / 2; ++h) {
+    uint32_t w[8];
+    load32b(reinterpret_cast<const uint8_t*>(p) + 32 * h, w);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 v = q[i];
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 t = word_to_f32<T>(w[k]);
-        f[8 * i + 2 * k] = t.x, f[8 * i + 2 * k + 1] = t.y;
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        f[8 * h + i] = __uint_as_float(w[i]);
+      } else {
+        const float2 t = word_to_f32<T>(w[i]);
+        f[2 * i] = t.x, f[2 * i + 1] = t.y;
       }
     }
   }
 }
 template <typename T>
 __device__ __forceinline__ void store16(T* __restrict__ p, const float (&f)[16]) {
-  if constexpr (sizeof(T) == 4) {
-    float4* q = reinterpret_cast<float4*>(p);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-  } else {
-    uint4* q = reinterpret_cast<uint4*>(p);
+  for (int h = 0; h < int(sizeof(T)) / 2; ++h) {
+    uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      q[i] = make_uint4(f32_to_word<T>(f[8 * i], f[8 * i + 1]), f32_to_word<T>(f[8 * i + 2], f[8 * i + 3]),
-                        f32_to_word<T>(f[8 * i + 4], f[8 * i + 5]), f32_to_word<T>(f[8 * i + 6], f[8 * i + 7]));
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(f[8 * h + i]);
+      else w[i] = f32_to_word<T>(f[2 * i], f[2 * i + 1]);
+    }
+    store32b(reinterpret_cast<uint8_t*>(p) + 32 * h, w);
   }
 }
 

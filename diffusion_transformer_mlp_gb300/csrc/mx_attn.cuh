@@ -88,7 +88,7 @@ struct SplitParams {
   AttnParams a;
   int32_t workers;
   int32_t least, even;  // tiles of a run: at least, if there are that many; see live_workers
-  float* part_o;     // [2 * workers][rows][D] (k_attn_chunk: [D / 4][rows][4]), not divided by the sum
+  float* part_o;     // [2 * workers][rows][D] (k_attn_chunk: [D / 4][rows][4]); see part_exponent
   float2* part_ml;   // [2 * workers][rows]  (reference, sum)
   int64_t* prefix;   // [seqs + 1] tiles before each sequence, written by block 0 for k_attn_combine
   struct Cursor* start;  // [workers] first tiles of the runs, written by k_attn_chunk for k_attn_join
@@ -247,6 +247,16 @@ __device__ __forceinline__ void tile_counts(const SplitParams& sp, int64_t* pref
   __syncthreads();
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b <= a.seqs; b += kThreads) sp.prefix[b] = prefix[b];
+}
+
+// A partial is (reference + e, sum 2^-e, output 2^-e) with 2^e <= sum < 2^(e + 1):
+// an exact change, after which the output is no larger than twice the largest
+// value, however many keys it sums.  Where partials are joined, references stand
+// kJoinLog2 above the maximum, for as many partials.
+constexpr float kJoinLog2 = 12.0f;
+__device__ __forceinline__ int32_t part_exponent(float sum) {
+  const int32_t e = int32_t(__float_as_uint(sum) >> 23) & 0xFF;
+  return e == 0 || e == 255 ? 0 : e - 127;
 }
 
 // Eight consecutive 16-bit outputs of a row.

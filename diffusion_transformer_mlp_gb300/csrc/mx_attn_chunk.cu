@@ -477,7 +477,8 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     const bool whole = cu.t == 0 && w.n == cu.s.n;
     const int32_t qi = real ? row / a.group : 0, hq = cu.h * a.group + (real ? row - qi * a.group : 0);
     const float l = l2.x + l2.y;
-    const float inv = !whole ? 1.0f : (l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l));
+    const int32_t pe = part_exponent(l);
+    const float inv = !whole ? pow2i(-pe) : (l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l));
     const int64_t part = int64_t(blockIdx.x) * 2 + (seg > 0 ? 1 : 0);
     const int64_t off = real ? int64_t(cu.q0 + qi) * a.o_st + int64_t(hq) * a.o_sh : -1;
     uint8_t* stage = staging + warp * T::kStage;
@@ -529,7 +530,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
       __syncwarp();
     }
     if (!whole)
-      sp.part_ml[part * kRows + qt * 128 + r] = make_float2(m, l);
+      sp.part_ml[part * kRows + qt * 128 + r] = make_float2(m + float(pe), l * pow2i(-pe));
     else if (real && a.lse != nullptr)
       a.lse[int64_t(cu.q0 + qi) * (a.kv_heads * a.group) + hq] =
           l == 0.0f ? -INFINITY : (m - kWeightLog2 + log2f(l)) * 0.6931471805599453f;

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_c
     m = fmaxf(m, sp.part_ml[rows_of(i) + mine].x);
   over_rows(m, [](float x, float y) { return fmaxf(x, y); }, row_m);
   m = row_m[mine];
-  const float ref = m == -INFINITY ? 0.0f : m;
+  const float ref = m == -INFINITY ? 0.0f : m + kJoinLog2;
   const int item = threadIdx.x % kItems, slice = threadIdx.x / kItems;
   const int32_t r = item / (kCols / 8), d = col0 + item % (kCols / 8) * 8;
   float l = 0.0f;  // of this thread's partials
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_c
   store_o8(a, static_cast<uint16_t*>(a.out) + int64_t(q0 + qi) * a.o_st + int64_t(hq) * a.o_sh + d, f);
   if (d == 0 && a.lse != nullptr)
     a.lse[int64_t(q0 + qi) * (a.kv_heads * a.group) + hq] =
-        l == 0.0f ? -INFINITY : (row_m[r] - kWeightLog2 + log2f(l)) * 0.6931471805599453f;
+        l == 0.0f ? -INFINITY : (row_m[r] + kJoinLog2 - kWeightLog2 + log2f(l)) * 0.6931471805599453f;
 }
 
 // The same for segments of 128 or 256 rows.  Of those few are split, at most
@@ -161,8 +161,8 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ Split
     const float2 ml = sp.part_ml[part_of(i) * kRows + r];
     const float4* src = reinterpret_cast<const float4*>(sp.part_o) + (part_of(i) * (D / 4) + d / 4) * kRows + r;
     const float4 u = src[0], v = src[kRows];
-    const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.0f : top;
-    const float old = exp2_approx(m - ref), g = exp2_approx(ml.x - ref);
+    const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.0f : top + kJoinLog2;
+    const float old = top == -INFINITY ? 1.0f : exp2_approx(m - top), g = exp2_approx(ml.x - ref);
     m = top;
     l = l * old + ml.y * g;
     f[0] = f[0] * old + u.x * g, f[1] = f[1] * old + u.y * g, f[2] = f[2] * old + u.z * g, f[3] = f[3] * old + u.w * g;
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ Split
   const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
 #pragma unroll
   for (int k = 0; k < 8; ++k) f[k] *= inv;
-  write(c, f, l == 0.0f ? -INFINITY : (m - kWeightLog2 + log2f(l)) * 0.6931471805599453f);
+  write(c, f, l == 0.0f ? -INFINITY : (m + kJoinLog2 - kWeightLog2 + log2f(l)) * 0.6931471805599453f);
 }
 
 template <int D, int kRows>

@@ -308,10 +308,12 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
       const int32_t row = cu.rt * kRows + g + 8 * r;
       const float inv = l[r] > 0.0f ? 1.0f / l[r] : (l[r] == 0.0f ? 0.0f : l[r]);  // a NaN sum stays NaN
       const int32_t qi = row / a.group, hq = cu.h * a.group + row - qi * a.group;
+      const int32_t pe = part_exponent(l[r]);
+      const float fac = whole ? inv : pow2i(-pe);
 #pragma unroll
       for (int j = 0; j < C; ++j) {
         // the accumulators hold p 2^10 v 2^(127 - R), the sum p 2^10
-        const float s = pow2i(rmax[j] - 127) * (whole ? inv : 1.0f);
+        const float s = pow2i(rmax[j] - 127) * fac;
         float f[8];  // columns 32 j + 8 tig + 0 .. 7
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -335,7 +337,8 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
       }
       if (tig == 0) {
         if (!whole) {
-          sp.part_ml[(int64_t(worker) * 2 + slot) * kRows + g + 8 * r] = make_float2(m[r], l[r]);
+          sp.part_ml[(int64_t(worker) * 2 + slot) * kRows + g + 8 * r] =
+              make_float2(m[r] + float(pe), l[r] * pow2i(-pe));
         } else if (a.lse != nullptr && row < head_rows) {
           a.lse[int64_t(cu.q0 + qi) * (a.kv_heads * a.group) + hq] =
               l[r] == 0.0f ? -INFINITY : (m[r] - kWeightLog2 + log2f(l[r])) * 0.6931471805599453f;

@@ -81,16 +81,18 @@ __device__ __forceinline__ void tma_load_3d_plain(void* dst, const CUtensorMap* 
 // A launch whose work is dealt in equal runs of tiles over its workers (warps of
 // k_attn_stream, blocks of k_attn_chunk), whatever the sequences' lengths: the
 // tiles of all (sequence, row tile, kv head) segments in a row, worker w taking
-// [total w / W, total (w+1) / W).  A worker writes the output of a segment that
+// [total w / W, total (w+1) / W).  A segment may weigh `edge` tiles more than it
+// has: places of the list before its first tile.  A worker writes the output of a segment that
 // it has all of; of others a partial goes to the workspace, at most two a
 // worker: its first segment's to slot 0, a later one's to slot 1.
 struct SplitParams {
   AttnParams a;
   int32_t workers;
   int32_t least, even;  // tiles of a run: at least, if there are that many; see live_workers
+  int32_t edge;
   float* part_o;     // [2 * workers][rows][D] (k_attn_chunk: [D / 4][rows][4]); see part_exponent
   float2* part_ml;   // [2 * workers][rows]  (reference, sum)
-  int64_t* prefix;   // [seqs + 1] tiles before each sequence, written by block 0 for k_attn_combine
+  int64_t* prefix;   // [seqs + 1] places before each sequence, written by block 0 for k_attn_combine
   struct Cursor* start;  // [workers] first tiles of the runs, written by k_attn_chunk for k_attn_join
 };
 
@@ -120,7 +122,7 @@ __device__ __forceinline__ int32_t worker_of(int64_t total, int64_t x, int32_t w
   return int32_t(((x + 1) * workers - 1) / total);
 }
 
-// Position in the list of all tiles.
+// A tile of the list.
 struct Cursor {
   int32_t b, rt, h, t;  // t: tile of the segment
   int32_t len, nq, q0;
@@ -133,9 +135,10 @@ __device__ __forceinline__ void cursor_seq(Cursor& c, const AttnParams& a) {
   c.q0 = a.q_starts != nullptr ? a.q_starts[c.b] : c.b;
 }
 
-// The position of tile x, by a whole warp: 32 row tiles at a time.
-__device__ __forceinline__ void cursor_at(Cursor& c, const AttnParams& a, const int64_t* prefix, int64_t x,
-                                          int32_t rows, int32_t tok) {
+// The first tile at place x or behind it, by a whole warp: 32 row tiles at a
+// time.  Returns how far behind.
+__device__ __forceinline__ int32_t cursor_at(Cursor& c, const AttnParams& a, const int64_t* prefix, int64_t x,
+                                             int32_t rows, int32_t tok, int32_t edge) {
   const int lane = threadIdx.x & 31;
   int32_t lo = 0, hi = a.seqs;  // prefix[lo] <= x < prefix[hi]
   while (hi - lo > 1) {
@@ -147,8 +150,8 @@ __device__ __forceinline__ void cursor_at(Cursor& c, const AttnParams& a, const 
   cursor_seq(c, a);
   int64_t rem = x - prefix[lo];
   for (int32_t rt = 0;; rt += 32) {
-    const int64_t n = (rt + lane) * rows < c.nq * a.group
-                          ? int64_t(row_span(a, c.len, c.nq, rt + lane, rows, tok).n) * a.kv_heads : 0;
+    int64_t n = (rt + lane) * rows < c.nq * a.group ? row_span(a, c.len, c.nq, rt + lane, rows, tok).n : 0;
+    n = n > 0 ? (n + edge) * a.kv_heads : 0;
     int64_t upto = n;  // of this row tile and those before it
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -165,8 +168,10 @@ __device__ __forceinline__ void cursor_at(Cursor& c, const AttnParams& a, const 
     rem -= __shfl_sync(0xFFFFFFFFu, upto, 31);
   }
   c.s = row_span(a, c.len, c.nq, c.rt, rows, tok);
-  c.h = int32_t(rem / c.s.n);
-  c.t = int32_t(rem - int64_t(c.h) * c.s.n);
+  c.h = int32_t(rem / (c.s.n + edge));
+  const int32_t off = int32_t(rem - int64_t(c.h) * (c.s.n + edge));
+  c.t = max(off - edge, 0);
+  return max(edge - off, 0);
 }
 
 // The next tile; the caller knows that there is one.
@@ -189,7 +194,7 @@ __device__ __forceinline__ void cursor_next(Cursor& c, const AttnParams& a, int3
   } while (c.s.n == 0);
 }
 
-// Tiles before each sequence, in prefix[0 .. seqs] (kMaxSeqs + 1 + kThreads
+// Places before each sequence, in prefix[0 .. seqs] (kMaxSeqs + 1 + kThreads
 // entries of shared memory); block 0 leaves them for k_attn_combine.  With few
 // sequences up to 32 threads share the row tiles of one.  Then every thread sums
 // a run of sequences and the first warp scans the runs' sums.
@@ -207,7 +212,7 @@ __device__ __forceinline__ void tile_counts(const SplitParams& sp, int64_t* pref
     if (b < a.seqs) {
       const int32_t len = a.lens[b], nq = seq_queries(a, b);
       for (int32_t rt = int(threadIdx.x) % share; rt * rows < nq * a.group; rt += share)
-        n += row_span(a, len, nq, rt, rows, tok).n;
+        if (const int32_t t = row_span(a, len, nq, rt, rows, tok).n; t > 0) n += t + sp.edge;
     }
     for (int o = 1; o < share; o <<= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
     if (b < a.seqs && threadIdx.x % share == 0) prefix[b] = n * a.kv_heads;

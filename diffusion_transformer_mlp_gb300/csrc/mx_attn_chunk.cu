@@ -11,7 +11,7 @@
 //   warps 0-3, 4-7  softmax of row tile 0, 1: a thread is a row.  Scores come
 //                   from tensor memory, the weights go back there as FP16 over
 //                   the scores they came from (the A operand of p v)
-//   four warps      decode the tile's keys and values to FP16 in shared memory:
+//   4 or 8 warps    decode the tile's keys and values to FP16 in shared memory:
 //                   a thread takes one token (of kTK), loads its codes and
 //                   scales one tile ahead, and writes its rows under the
 //                   128-byte swizzle
@@ -45,6 +45,9 @@ namespace {
 
 constexpr float kLag = 5.0f;
 constexpr int kLeast = 4;      // tiles of a run at least
+// Tiles that a new segment costs: its queries, its outputs, the pipeline's
+// restart (2 chunks of 2,048 queries, 32 / 8 heads, dim 128: 294 us without, 270 with).
+constexpr int kEdge = 8;
 constexpr int kMeta = 8;       // tiles whose references are kept: the decoders are up to 6 ahead of the softmax
 constexpr int kTK = 64;        // keys of a tile
 constexpr int kHeadroom = 8;   // value scales may exceed their reference by 2^8 before it is raised
@@ -57,9 +60,11 @@ struct Chunk {
   static constexpr int kSlots = D == 256 ? 2 : 4;     // decoded tiles
   static constexpr int kQBytes = 128 * D * 2;         // one row tile
   static constexpr int kKvBytes = kTK * D * 2;        // one decoded tile of K or V
-  static constexpr int kWarpD = kNQ * 4, kWarpR = kWarpD + 4, kWarpMma = kWarpR + 1;
+  // one row tile leaves registers for eight decoding warps (dim 256)
+  static constexpr int kDecoders = kNQ == 1 ? 8 : 4;
+  static constexpr int kWarpD = kNQ * 4, kWarpR = kWarpD + kDecoders, kWarpMma = kWarpR + 1;
   static constexpr int kThreads = (kWarpMma + kNQ) * 32;
-  static constexpr int kPart = D * kTK / 128;         // elements of a decoding thread
+  static constexpr int kPart = D * kTK / (32 * kDecoders);  // elements of K (and V) of a decoding thread
   static constexpr int kStage = 32 * 64;              // a softmax warp's outputs on their way, 32 columns at a time
   static constexpr int kSmem = kNQ * kQBytes + 2 * kSlots * kKvBytes + kWarpD * kStage + 4096;
   static constexpr uint32_t kS = 0, kO = kNQ * 2 * kTK;  // tensor-memory columns: scores, outputs
@@ -69,7 +74,7 @@ struct Chunk {
 };
 
 // A warp's place in the run of its block: a segment, of which the n tiles from
-// seg.t on belong to the run, after g tiles of it; `left` with these to go.
+// seg.t on belong to the run, after g tiles of it; `left` places with these to go.
 struct Walk {
   Cursor seg;
   int32_t left, n, g;
@@ -85,6 +90,7 @@ struct Shared {
   uint32_t tmem;
   int abort_flag;
   Cursor first;                // of the run
+  int32_t places;              // from there to its end
   Walk walk[16][2];            // by warp; kept here, as registers are short
   int32_t rk[kMeta];           // reference of the keys' scales
   int32_t rv[kMeta][8];        // of the values' scales by block, as the outputs have it from this tile on
@@ -208,22 +214,25 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     const int32_t workers = live_workers(sp, total), w = int32_t(blockIdx.x);
     if (w < workers) {
       const int64_t x0 = worker_start(total, w, workers);
-      tiles = int32_t(worker_start(total, w + 1, workers) - x0);
       if (warp == 0) {
         Cursor first;
-        cursor_at(first, a, prefix, x0, kRows, kTK);
-        if (lane == 0) sh.first = first, sp.start[w] = first;
+        const int32_t skip = cursor_at(first, a, prefix, x0, kRows, kTK, sp.edge);
+        if (lane == 0) {
+          sh.first = first, sp.start[w] = first;
+          sh.places = int32_t(worker_start(total, w + 1, workers) - x0) - skip;
+        }
       }
+      __syncthreads();  // the counts are read, the first tile is known
+      tiles = sh.places;
     }
   }
-  if (tiles == 0) return;
-  __syncthreads();  // the counts are read, the first tile is known
+  if (tiles <= 0) return;  // no worker, or nothing but the room before a segment
 
   if (threadIdx.x == 0) {
     mbar_init(&sh.done, kNQ);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sh.ref_full[i], 1);
-      mbar_init(&sh.kv_full[i], 4);
+      mbar_init(&sh.kv_full[i], T::kDecoders);
       mbar_init(&sh.kv_empty[i], kNQ);
       mbar_init(&sh.s_full[i >> 1][i & 1], 2);
       mbar_init(&sh.p_full[i >> 1][i & 1], 4);
@@ -247,8 +256,10 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     Walk w = from;
     w.left -= w.n;
     w.g += w.n;
+    const bool next = w.n > 0;
+    if (next) w.left -= sp.edge;
     if (w.left > 0) {
-      if (w.n > 0) {
+      if (next) {
         w.seg.t += w.n - 1;
         cursor_next(w.seg, a, kRows, kTK);
       }
@@ -810,7 +821,7 @@ nvfp4_status attn_chunk(const mxfp4_cache* cache, const AttnParams& base, int32_
   SplitParams sp;
   sp.a = base;
   sp.workers = sm_count();
-  sp.least = kLeast, sp.even = 0;
+  sp.least = kLeast, sp.even = 0, sp.edge = kEdge;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   sp.part_o = reinterpret_cast<float*>(ws);
   sp.part_ml = reinterpret_cast<float2*>(ws + align256(partial_rows(dim) * dim * 4));

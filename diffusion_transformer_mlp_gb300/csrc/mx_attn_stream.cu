@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
   const int64_t x0 = worker < workers ? worker_start(total, worker, workers) : 0;
   const int32_t tiles = worker < workers ? int32_t(worker_start(total, worker + 1, workers) - x0) : 0;
   Cursor cu;
-  if (tiles > 0) cursor_at(cu, a, prefix, x0, kRows, kTok);
+  if (tiles > 0) cursor_at(cu, a, prefix, x0, kRows, kTok, 0);
   fence_proxy_async_smem();  // the counts are read, the TMA may write there
   __syncthreads();
   if (tiles <= 0) return;
@@ -710,7 +710,7 @@ nvfp4_status stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, const S
   if (st != NVFP4_OK) return st;
   SplitParams p = sp;
   p.workers = T::kCtas * sm_count() * kWarps;
-  p.least = 1, p.even = 4;  // 16,000 keys, 8 heads, dim 128: 24.2 us, without 29.0
+  p.least = 1, p.edge = 0, p.even = 4;  // 16,000 keys, 8 heads, dim 128: 24.2 us, without 29.0
   st = launch("launch k_attn_stream", kern, dim3(unsigned(p.workers / kWarps)), dim3(kThreads), T::kSmem, 0, stream, tk,
               tv, p);
   if (st != NVFP4_OK) return st;

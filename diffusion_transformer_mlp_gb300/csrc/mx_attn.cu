@@ -36,7 +36,8 @@ using namespace nvfp4;
 extern "C" int64_t mxfp4_attention_workspace_bytes(int32_t kv_heads, int32_t q_heads, int32_t dim,
                                                    int32_t max_queries) {
   if (kv_heads < 1 || q_heads < 1 || max_queries < 1 || (dim != 64 && dim != 128 && dim != 256)) return 0;
-  return many_rows(dim, int64_t(max_queries) * (q_heads / kv_heads)) ? attn_chunk_workspace(dim) : attn_stream_workspace(dim);
+  const int64_t rows = int64_t(max_queries) * (q_heads / kv_heads);
+  return many_rows(dim, rows) ? attn_chunk_workspace(dim) : attn_stream_workspace(dim);
 }
 
 extern "C" nvfp4_status mxfp4_cache_attention(const mxfp4_cache* cache, const mxfp4_attention* args,

@@ -112,7 +112,8 @@ __device__ __forceinline__ Span row_span(const AttnParams& a, int32_t len, int32
 // the longest: a worker less is partials less to join.
 __device__ __forceinline__ int32_t live_workers(const SplitParams& sp, int64_t total) {
   const int64_t run = max(int64_t(sp.least), (total + sp.workers - 1) / sp.workers);
-  return int32_t(run <= sp.even ? (total + run - 1) / run : min(int64_t(sp.workers), (total + sp.least - 1) / sp.least));
+  if (run <= sp.even) return int32_t((total + run - 1) / run);
+  return int32_t(min(int64_t(sp.workers), (total + sp.least - 1) / sp.least));
 }
 __device__ __forceinline__ int64_t worker_start(int64_t total, int32_t w, int32_t workers) {
   return total * w / workers;

@@ -23,16 +23,22 @@
 //
 // Every row tile has two score buffers: Q K^T of the next keys is under way
 // while the softmax of these runs, so that neither waits for the other's
-// latency (128 keys and one buffer: 4,300 cycles for 128 keys of both row
-// tiles; one issuing thread for both was slower still).
+// latency (128 keys and one buffer took 4,300 cycles for 128 keys of both row
+// tiles, this 3,400; the MMAs alone 2,050).
+//
+// What bounds it: the issue slots and latencies of the softmax and decoding
+// warps (58% of the slots used, tensor pipe 51%).  Two prompts' chunks of 2,048
+// queries on 4,099 and 8,192 keys, 32 / 8 heads, dim 128: 270 us, 1.1 PFLOP/s.
+// Five kinds of warps run at once, so the loops are kept short enough for the
+// instruction caches (fully unrolled: 430 us).
 //
 // FP16 operands are exact: a code times 2^(E - R + 13), R the tile's largest
 // key scale (its power of two goes onto the scores), is exact for E >= R - 36,
 // and a code times 2^(E - R + 5), R a running reference of the value scales of
 // its block column (its power of two goes onto the output's columns), for E >=
-// R - 28.  Q is scaled by a power of two per row.  Weights are held times 2^10 against a reference that lags the
-// running maximum by up to 2^5, so that the output is rarely rescaled (an
-// 11-bit rounding; sums and statistics in FP32).
+// R - 28.  Q is scaled by a power of two per row.  Weights are held times 2^10
+// against a reference that lags the running maximum by up to 2^5, so that the
+// output is rarely rescaled (an 11-bit rounding; sums and statistics in FP32).
 #include <algorithm>
 #include <atomic>
 #include <string>
@@ -361,191 +367,192 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     float qf = load_q(wk.seg);
     bool ok = true;
     for (int seg = 0; ok; ++seg) {
-    const Walk& w = sh.walk[warp][seg & 1];
-    const Cursor& cu = w.seg;
-    const int32_t n = w.n, g = w.g, sink_tiles = cu.s.sink_tiles - cu.t, first_tile = cu.t,
-                  lo_tile = cu.s.lo_tile - sink_tiles;
-    const int32_t row = cu.rt * kRows + qt * 128 + r;
-    const bool real = row < cu.nq * a.group;
-    const int32_t pos = cu.len - cu.nq + (real ? row / a.group : 0);
-    // the row sees keys j < end with j >= from or j < sinks
-    const int32_t end = !real ? 0 : (a.causal ? min(cu.len, pos + 1) : cu.len);
-    const int32_t from = a.window > 0 ? pos - a.window + 1 : 0;
-    float m = -INFINITY;
-    float2 l2 = make_float2(0.0f, 0.0f);
-    uint32_t nan_cols = 0;  // blocks of the output that are NaN
-    int last_meta = 0;
-    for (int j = 0; j < n; ++j) {
-      const int x = g + j;  // of the run's tiles
-      const uint32_t t_s = t_lane + T::kS + (qt * 2 + (x & 1)) * kTK;
-      if (!wait(&sh.s_full[qt][x & 1], (x >> 1) & 1)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const int ms_ = x & (kMeta - 1);
-      const int32_t tok0 = (j < sink_tiles ? j + first_tile : j + lo_tile) * kTK;
-      const float c1 = qf * pow2i(sh.rk[ms_] - 127 - kLiftK);
-      last_meta = ms_;
-      const bool all = tok0 + kTK <= end && (tok0 >= from || tok0 + kTK <= a.sinks);
-      const bool plain = __all_sync(0xFFFFFFFFu, all);
-      // keys of the tile that the row sees: [lo, hi) and [0, sk_)
-      const int32_t hi = end - tok0, lo = from - tok0, sk_ = a.sinks - tok0;
-      // Weights against the reference as it stands, in registers; where a
-      // row's maximum is too far ahead of it, it is raised and the weights are
-      // formed again (the scores are still there).
-      const uint64_t c1p = pair_const(c1);
-      bool raised = sh.raised[ms_] != 0;
-      float alpha = 1.0f;
-      // one pass; true if the weights are in place
-      auto weights = [&](auto masked) -> bool {
-        const float sub = kWeightLog2 - (m == -INFINITY ? 0.0f : m);
-        const uint64_t subp = pair_const(sub);
-        uint64_t sum = 0;
-        float top = -INFINITY;
-        uint32_t w[kTK / 32][16];
-#pragma unroll
-        for (int c = 0; c < kTK / 32; ++c) {
-          uint32_t v[32];
-          tmem_load32(t_s + 32 * c, v);
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float2 t = unpair(fma2(pair_of(v[i], v[i + 1]), c1p, subp));
-            if constexpr (decltype(masked)::value) {
-              const int y = 32 * c + i;
-              if (y >= hi || (y < lo && y >= sk_)) t.x = -INFINITY;
-              if (y + 1 >= hi || (y + 1 < lo && y + 1 >= sk_)) t.y = -INFINITY;
-            }
-            top = fmaxf(top, fmaxf(t.x, t.y));
-            t.x = exp2_approx(t.x), t.y = exp2_approx(t.y);
-            sum = add2(sum, pair_of(__float_as_uint(t.x), __float_as_uint(t.y)));
-            w[c][i / 2] = f32_to_word<__half>(t.x, t.y);
-          }
+      const Walk& w = sh.walk[warp][seg & 1];
+      const Cursor& cu = w.seg;
+      const int32_t n = w.n, g = w.g, sink_tiles = cu.s.sink_tiles - cu.t, first_tile = cu.t,
+                    lo_tile = cu.s.lo_tile - sink_tiles;
+      const int32_t row = cu.rt * kRows + qt * 128 + r;
+      const bool real = row < cu.nq * a.group;
+      const int32_t pos = cu.len - cu.nq + (real ? row / a.group : 0);
+      // the row sees keys j < end with j >= from or j < sinks
+      const int32_t end = !real ? 0 : (a.causal ? min(cu.len, pos + 1) : cu.len);
+      const int32_t from = a.window > 0 ? pos - a.window + 1 : 0;
+      float m = -INFINITY;
+      float2 l2 = make_float2(0.0f, 0.0f);
+      uint32_t nan_cols = 0;  // blocks of the output that are NaN
+      int last_meta = 0;
+      for (int j = 0; j < n; ++j) {
+        const int x = g + j;  // of the run's tiles
+        const uint32_t t_s = t_lane + T::kS + (qt * 2 + (x & 1)) * kTK;
+        if (!wait(&sh.s_full[qt][x & 1], (x >> 1) & 1)) {
+          ok = false;
+          break;
         }
-        top -= sub;  // back to the score's logarithm
-        const bool raise = top > m + kLag;
-        if (__any_sync(0xFFFFFFFFu, raise)) {
-          if (raise) {
-            // not below the maximum by its rounding either, however large it is
-            const float ref = fmaf(fabsf(top), 0x1p-22f, top);
-            alpha *= exp2_approx(m - ref);
-            m = ref;
-          }
-          raised = true;
-          return false;
-        }
-        l2.x = l2.x * alpha + unpair(sum).x, l2.y = l2.y * alpha + unpair(sum).y;
-        if (j > 0 && raised) {
-          // The p v of the tile before has to be complete (its slot is filled
-          // again only after the weights of this tile).
-          if (!wait(&sh.kv_empty[(x - 1) % kSlots], ((x - 1) / kSlots) & 1)) return true;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            const float f = alpha * sh.vfac[ms_][c / 32];
+        tc_fence_after();
+        const int ms_ = x & (kMeta - 1);
+        const int32_t tok0 = (j < sink_tiles ? j + first_tile : j + lo_tile) * kTK;
+        const float c1 = qf * pow2i(sh.rk[ms_] - 127 - kLiftK);
+        last_meta = ms_;
+        const bool all = tok0 + kTK <= end && (tok0 >= from || tok0 + kTK <= a.sinks);
+        const bool plain = __all_sync(0xFFFFFFFFu, all);
+        // keys of the tile that the row sees: [lo, hi) and [0, sk_)
+        const int32_t hi = end - tok0, lo = from - tok0, sk_ = a.sinks - tok0;
+        // Weights against the reference as it stands, in registers; where a
+        // row's maximum is too far ahead of it, it is raised and the weights are
+        // formed again (the scores are still there).
+        const uint64_t c1p = pair_const(c1);
+        bool raised = sh.raised[ms_] != 0;
+        float alpha = 1.0f;
+        // one pass; true if the weights are in place
+        auto weights = [&](auto masked) -> bool {
+          const float sub = kWeightLog2 - (m == -INFINITY ? 0.0f : m);
+          const uint64_t subp = pair_const(sub);
+          uint64_t sum = 0;
+          float top = -INFINITY;
+          uint32_t w[kTK / 32][16];
+#pragma unroll
+          for (int c = 0; c < kTK / 32; ++c) {
             uint32_t v[32];
-            tmem_load32(t_o + c, v);
+            tmem_load32(t_s + 32 * c, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-            tmem_st_32x32b_x32(t_o + c, v);
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < kTK / 32; ++c) tmem_st_x16(t_s + 16 * c, w[c]);
-        return true;
-      };
-      // the second pass finds every maximum in reach of its reference
-#pragma unroll 1
-      for (int attempt = 0; attempt < 3; ++attempt)
-        if (plain ? weights(std::false_type{}) : weights(std::true_type{})) break;
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full[qt][x & 1]);
-      if (sh.nan_any[ms_]) {
-        // a block of NaN among the values reaches the rows that see its key
-        for (int blk = 0; blk < C; ++blk)
-          for (int w = 0; w < kTK / 32; ++w) {
-            uint32_t bits = sh.nan_bits[ms_][blk][w];
-            while (bits != 0) {
-              const int32_t t = w * 32 + __ffs(bits) - 1;
-              bits &= bits - 1;
-              if (t < hi && (t >= lo || t < sk_)) nan_cols |= 1u << blk;
+            for (int i = 0; i < 32; i += 2) {
+              float2 t = unpair(fma2(pair_of(v[i], v[i + 1]), c1p, subp));
+              if constexpr (decltype(masked)::value) {
+                const int y = 32 * c + i;
+                if (y >= hi || (y < lo && y >= sk_)) t.x = -INFINITY;
+                if (y + 1 >= hi || (y + 1 < lo && y + 1 >= sk_)) t.y = -INFINITY;
+              }
+              top = fmaxf(top, fmaxf(t.x, t.y));
+              t.x = exp2_approx(t.x), t.y = exp2_approx(t.y);
+              sum = add2(sum, pair_of(__float_as_uint(t.x), __float_as_uint(t.y)));
+              w[c][i / 2] = f32_to_word<__half>(t.x, t.y);
             }
           }
-      }
-    }
-    if (!ok) break;
-    // the next segment's queries first: the MMAs that read this segment's are
-    // complete, and the next ones can start while the outputs are written
-    Walk& next = sh.walk[warp][(seg + 1) & 1];
-    const bool more = advance(w, next);
-    if (more) qf = load_q(next.seg);
-    // ---- output
-    ok = wait(&sh.o_full[qt], seg & 1);
-    tc_fence_after();
-    if (!ok) break;
-    const bool whole = cu.t == 0 && w.n == cu.s.n;
-    const int32_t qi = real ? row / a.group : 0, hq = cu.h * a.group + (real ? row - qi * a.group : 0);
-    const float l = l2.x + l2.y;
-    const int32_t pe = part_exponent(l);
-    const float inv = !whole ? pow2i(-pe) : (l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l));
-    const int64_t part = int64_t(blockIdx.x) * 2 + (seg > 0 ? 1 : 0);
-    const int64_t off = real ? int64_t(cu.q0 + qi) * a.o_st + int64_t(hq) * a.o_sh : -1;
-    uint8_t* stage = staging + warp * T::kStage;
+          top -= sub;  // back to the score's logarithm
+          const bool raise = top > m + kLag;
+          if (__any_sync(0xFFFFFFFFu, raise)) {
+            if (raise) {
+              // not below the maximum by its rounding either, however large it is
+              const float ref = fmaf(fabsf(top), 0x1p-22f, top);
+              alpha *= exp2_approx(m - ref);
+              m = ref;
+            }
+            raised = true;
+            return false;
+          }
+          l2.x = l2.x * alpha + unpair(sum).x, l2.y = l2.y * alpha + unpair(sum).y;
+          if (j > 0 && raised) {
+            // The p v of the tile before has to be complete (its slot is filled
+            // again only after the weights of this tile).
+            if (!wait(&sh.kv_empty[(x - 1) % kSlots], ((x - 1) / kSlots) & 1)) return true;
+            tc_fence_after();
 #pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
-      uint32_t v[32];
-      tmem_load32(t_o + c, v);
-      if (c + 32 == D) {
+            for (int c = 0; c < D; c += 32) {
+              const float f = alpha * sh.vfac[ms_][c / 32];
+              uint32_t v[32];
+              tmem_load32(t_o + c, v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+              tmem_st_32x32b_x32(t_o + c, v);
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < kTK / 32; ++c) tmem_st_x16(t_s + 16 * c, w[c]);
+          return true;
+        };
+        // the second pass finds every maximum in reach of its reference
+#pragma unroll 1
+        for (int attempt = 0; attempt < 3; ++attempt)
+          if (plain ? weights(std::false_type{}) : weights(std::true_type{})) break;
+        tc_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.o_empty[qt]);
-      }
-      // c / 32 is a reference's block, and its factor the same for all rows
-      const float fac = pow2i(sh.rv[last_meta][c / 32] - 127 - kLiftV) * inv;
-      if ((nan_cols >> (c / 32)) & 1u) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0x7FFFFFFFu;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * fac);
-      }
-      if (!whole) {
-        // [D / 4][rows] of four columns: a warp writes 512 bytes at a time
-        uint4* d = reinterpret_cast<uint4*>(sp.part_o) + (part * (D / 4) + c / 4) * kRows + qt * 128 + r;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i * kRows] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        continue;
-      }
-      // through shared memory, so that four lanes write 64 bytes of a row
-      // (a thread that writes its own row: 4,400 to 10,000 cycles)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t h[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float f0 = __uint_as_float(v[8 * i + 2 * x]), f1 = __uint_as_float(v[8 * i + 2 * x + 1]);
-          h[x] = a.bf16 ? f32_to_word<__nv_bfloat16>(f0, f1) : f32_to_word<__half>(f0, f1);
+        if (lane == 0) mbar_arrive(&sh.p_full[qt][x & 1]);
+        if (sh.nan_any[ms_]) {
+          // a block of NaN among the values reaches the rows that see its key
+          for (int blk = 0; blk < C; ++blk)
+            for (int w = 0; w < kTK / 32; ++w) {
+              uint32_t bits = sh.nan_bits[ms_][blk][w];
+              while (bits != 0) {
+                const int32_t t = w * 32 + __ffs(bits) - 1;
+                bits &= bits - 1;
+                if (t < hi && (t >= lo || t < sk_)) nan_cols |= 1u << blk;
+              }
+            }
         }
-        *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
       }
-      __syncwarp();
+      if (!ok) break;
+      // the next segment's queries first: the MMAs that read this segment's are
+      // complete, and the next ones can start while the outputs are written
+      Walk& next = sh.walk[warp][(seg + 1) & 1];
+      const bool more = advance(w, next);
+      if (more) qf = load_q(next.seg);
+      // ---- output
+      ok = wait(&sh.o_full[qt], seg & 1);
+      tc_fence_after();
+      if (!ok) break;
+      const bool whole = cu.t == 0 && w.n == cu.s.n;
+      const int32_t qi = real ? row / a.group : 0, hq = cu.h * a.group + (real ? row - qi * a.group : 0);
+      const float l = l2.x + l2.y;
+      const int32_t pe = part_exponent(l);
+      const float inv = !whole ? pow2i(-pe) : (l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l));
+      const int64_t part = int64_t(blockIdx.x) * 2 + (seg > 0 ? 1 : 0);
+      const int64_t off = real ? int64_t(cu.q0 + qi) * a.o_st + int64_t(hq) * a.o_sh : -1;
+      uint8_t* stage = staging + warp * T::kStage;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t v[32];
+        tmem_load32(t_o + c, v);
+        if (c + 32 == D) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.o_empty[qt]);
+        }
+        // c / 32 is a reference's block, and its factor the same for all rows
+        const float fac = pow2i(sh.rv[last_meta][c / 32] - 127 - kLiftV) * inv;
+        if ((nan_cols >> (c / 32)) & 1u) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int rr = i * 8 + lane / 4;
-        const uint4 h = *reinterpret_cast<const uint4*>(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
-        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, rr);
-        if (o >= 0) store_o8_words(a, static_cast<uint16_t*>(a.out) + o + c + (lane & 3) * 8, h);
+          for (int i = 0; i < 32; ++i) v[i] = 0x7FFFFFFFu;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * fac);
+        }
+        if (!whole) {
+          // [D / 4][rows] of four columns: a warp writes 512 bytes at a time
+          uint4* d = reinterpret_cast<uint4*>(sp.part_o) + (part * (D / 4) + c / 4) * kRows + qt * 128 + r;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i * kRows] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          continue;
+        }
+        // through shared memory, so that four lanes write 64 bytes of a row
+        // (a thread that writes its own row: 4,400 to 10,000 cycles)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t h[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float f0 = __uint_as_float(v[8 * i + 2 * x]), f1 = __uint_as_float(v[8 * i + 2 * x + 1]);
+            h[x] = a.bf16 ? f32_to_word<__nv_bfloat16>(f0, f1) : f32_to_word<__half>(f0, f1);
+          }
+          *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = i * 8 + lane / 4;
+          const uint4 h = *reinterpret_cast<const uint4*>(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+          const int64_t o = __shfl_sync(0xFFFFFFFFu, off, rr);
+          if (o >= 0) store_o8_words(a, static_cast<uint16_t*>(a.out) + o + c + (lane & 3) * 8, h);
+        }
+        __syncwarp();
       }
-      __syncwarp();
-    }
-    if (!whole)
-      sp.part_ml[part * kRows + qt * 128 + r] = make_float2(m + float(pe), l * pow2i(-pe));
-    else if (real && a.lse != nullptr)
-      a.lse[int64_t(cu.q0 + qi) * (a.kv_heads * a.group) + hq] =
-          l == 0.0f ? -INFINITY : (m - kWeightLog2 + log2f(l)) * 0.6931471805599453f;
-    if (!more) break;
+      if (!whole)
+        sp.part_ml[part * kRows + qt * 128 + r] = make_float2(m + float(pe), l * pow2i(-pe));
+      else if (real && a.lse != nullptr)
+        a.lse[int64_t(cu.q0 + qi) * (a.kv_heads * a.group) + hq] =
+            l == 0.0f ? -INFINITY : (m - kWeightLog2 + log2f(l)) * 0.6931471805599453f;
+      if (!more) break;
     }
   } else if (warp < T::kWarpR) {
     // ------------------------------------------------------------ decoding
@@ -554,79 +561,79 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     constexpr int kWords = T::kPart / 32;     // blocks of a share
     bool ok = true;
     while (ok && advance(wk, wk)) {
-    const Cursor cu = wk.seg;
-    const int32_t n = wk.n, g = wk.g;
-    const int32_t* table = a.table + int64_t(cu.b) * a.table_ld;
-    auto page_of = [&](int j) -> int32_t {
-      const int32_t at = cu.s.tile(cu.t + j) * kTK + tok;
-      return j < n && at < cu.s.hi ? table[min(at >> a.page_shift, int32_t(a.table_ld) - 1)] : 0;
-    };
-    uint4 raw[2][kWords];  // codes of K and V
-    uint32_t sc[2] = {0, 0};
-    auto fetch = [&](int j, int32_t page) {
-      const int32_t at = cu.s.tile(cu.t + j) * kTK + tok;
-      const bool in = j < n && at < cu.s.hi;
-      const int32_t z = min(max(page, 0), int32_t(a.pages) - 1) * a.kv_heads + cu.h;
-      const int64_t rowi = (int64_t(z) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
+      const Cursor cu = wk.seg;
+      const int32_t n = wk.n, g = wk.g;
+      const int32_t* table = a.table + int64_t(cu.b) * a.table_ld;
+      auto page_of = [&](int j) -> int32_t {
+        const int32_t at = cu.s.tile(cu.t + j) * kTK + tok;
+        return j < n && at < cu.s.hi ? table[min(at >> a.page_shift, int32_t(a.table_ld) - 1)] : 0;
+      };
+      uint4 raw[2][kWords];  // codes of K and V
+      uint32_t sc[2] = {0, 0};
+      auto fetch = [&](int j, int32_t page) {
+        const int32_t at = cu.s.tile(cu.t + j) * kTK + tok;
+        const bool in = j < n && at < cu.s.hi;
+        const int32_t z = min(max(page, 0), int32_t(a.pages) - 1) * a.kv_heads + cu.h;
+        const int64_t rowi = (int64_t(z) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const uint8_t* src = (kv ? v_codes : k_codes) + rowi * (D / 2) + part * (T::kPart / 2);
-        const uint8_t* s = (kv ? a.v_scales : a.k_scales) + rowi * C + part * kWords;
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint8_t* src = (kv ? v_codes : k_codes) + rowi * (D / 2) + part * (T::kPart / 2);
+          const uint8_t* s = (kv ? a.v_scales : a.k_scales) + rowi * C + part * kWords;
 #pragma unroll
-        for (int i = 0; i < kWords; ++i)
-          raw[kv][i] = in ? *reinterpret_cast<const uint4*>(src + 16 * i) : make_uint4(0, 0, 0, 0);
-        sc[kv] = 0;
-        if (in) {
-          if constexpr (kWords == 1) sc[kv] = *s;
-          else if constexpr (kWords == 2) sc[kv] = *reinterpret_cast<const uint16_t*>(s);
-          else sc[kv] = *reinterpret_cast<const uint32_t*>(s);
-        }
-      }
-    };
-    int32_t page = page_of(0);
-    fetch(0, page);
-    page = page_of(1);
-    for (int j = 0; j < n; ++j) {
-      const int x0 = g + j, slot = x0 % kSlots, meta = x0 & (kMeta - 1);
-      const uint32_t ph = (x0 / kSlots) & 1;
-      // this tile's codes make room for the next tile's, whose loads take as
-      // long as the decoding
-      uint4 cur[2][kWords];
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) cur[0][i] = raw[0][i], cur[1][i] = raw[1][i];
-      const uint32_t scale[2] = {sc[0], sc[1]};
-      fetch(j + 1, page);
-      page = page_of(j + 2);
-      // the references come after their writer has seen the slot empty
-      ok = wait(&sh.ref_full[slot], ph) && wait(&sh.kv_empty[slot], ph ^ 1);
-      if (!ok) break;
-      const int32_t rk = sh.rk[meta] - kLiftK;
-#pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv) {
-        uint8_t* dst = (kv ? sv : sk) + slot * T::kKvBytes + tok * 128;
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-          const int32_t e = ((kv ? scale[1] : scale[0]) >> (8 * i)) & 0xFF;
-          const int32_t ref = kv ? sh.rv[meta][part * kWords + i] - kLiftV : rk;
-          const float f = __uint_as_float(uint32_t(max(e - ref + 127, 0)) << 23);
-          uint32_t fw = f32_to_word<__half>(f, f);
-          if (e == 255) fw = kv ? 0u : 0x7FFF7FFFu;
-          const uint32_t w[4] = {kv ? cur[1][i].x : cur[0][i].x, kv ? cur[1][i].y : cur[0][i].y,
-                                 kv ? cur[1][i].z : cur[0][i].z, kv ? cur[1][i].w : cur[0][i].w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t h[4];
-            e2m1x8_to_half(w[x], h);
-            const int d = part * T::kPart + i * 32 + x * 8;
-            *reinterpret_cast<uint4*>(dst + (d / 64) * (kTK * 128) + ((((d % 64) / 8) ^ (tok & 7)) << 4)) =
-                make_uint4(hmul2(h[0], fw), hmul2(h[1], fw), hmul2(h[2], fw), hmul2(h[3], fw));
+          for (int i = 0; i < kWords; ++i)
+            raw[kv][i] = in ? *reinterpret_cast<const uint4*>(src + 16 * i) : make_uint4(0, 0, 0, 0);
+          sc[kv] = 0;
+          if (in) {
+            if constexpr (kWords == 1) sc[kv] = *s;
+            else if constexpr (kWords == 2) sc[kv] = *reinterpret_cast<const uint16_t*>(s);
+            else sc[kv] = *reinterpret_cast<const uint32_t*>(s);
           }
         }
+      };
+      int32_t page = page_of(0);
+      fetch(0, page);
+      page = page_of(1);
+      for (int j = 0; j < n; ++j) {
+        const int x0 = g + j, slot = x0 % kSlots, meta = x0 & (kMeta - 1);
+        const uint32_t ph = (x0 / kSlots) & 1;
+        // this tile's codes make room for the next tile's, whose loads take as
+        // long as the decoding
+        uint4 cur[2][kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) cur[0][i] = raw[0][i], cur[1][i] = raw[1][i];
+        const uint32_t scale[2] = {sc[0], sc[1]};
+        fetch(j + 1, page);
+        page = page_of(j + 2);
+        // the references come after their writer has seen the slot empty
+        ok = wait(&sh.ref_full[slot], ph) && wait(&sh.kv_empty[slot], ph ^ 1);
+        if (!ok) break;
+        const int32_t rk = sh.rk[meta] - kLiftK;
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          uint8_t* dst = (kv ? sv : sk) + slot * T::kKvBytes + tok * 128;
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) {
+            const int32_t e = ((kv ? scale[1] : scale[0]) >> (8 * i)) & 0xFF;
+            const int32_t ref = kv ? sh.rv[meta][part * kWords + i] - kLiftV : rk;
+            const float f = __uint_as_float(uint32_t(max(e - ref + 127, 0)) << 23);
+            uint32_t fw = f32_to_word<__half>(f, f);
+            if (e == 255) fw = kv ? 0u : 0x7FFF7FFFu;
+            const uint32_t w[4] = {kv ? cur[1][i].x : cur[0][i].x, kv ? cur[1][i].y : cur[0][i].y,
+                                   kv ? cur[1][i].z : cur[0][i].z, kv ? cur[1][i].w : cur[0][i].w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t h[4];
+              e2m1x8_to_half(w[x], h);
+              const int d = part * T::kPart + i * 32 + x * 8;
+              *reinterpret_cast<uint4*>(dst + (d / 64) * (kTK * 128) + ((((d % 64) / 8) ^ (tok & 7)) << 4)) =
+                  make_uint4(hmul2(h[0], fw), hmul2(h[1], fw), hmul2(h[2], fw), hmul2(h[3], fw));
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.kv_full[slot]);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.kv_full[slot]);
-    }
     }
   } else if (warp == T::kWarpR) {
     // ------------------------------------------------------------ references
@@ -635,105 +642,106 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     constexpr int kPer = kTK / 32, kW = (C + 3) / 4;
     bool ok = true;
     while (ok && advance(wk, wk)) {
-    const Cursor cu = wk.seg;
-    const int32_t n = wk.n, g = wk.g;
-    const int32_t* table = a.table + int64_t(cu.b) * a.table_ld;
-    uint32_t kw[kPer][kW], vw[kPer][kW];
-    int32_t pages[kPer];
-    auto look_up = [&](int j) {
+      const Cursor cu = wk.seg;
+      const int32_t n = wk.n, g = wk.g;
+      const int32_t* table = a.table + int64_t(cu.b) * a.table_ld;
+      uint32_t kw[kPer][kW], vw[kPer][kW];
+      int32_t pages[kPer];
+      auto look_up = [&](int j) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int32_t at = cu.s.tile(cu.t + j) * kTK + i * 32 + lane;
-        pages[i] = j < n && at < cu.s.hi ? table[min(at >> a.page_shift, int32_t(a.table_ld) - 1)] : 0;
-      }
-    };
-    auto fetch = [&](int j) {
+        for (int i = 0; i < kPer; ++i) {
+          const int32_t at = cu.s.tile(cu.t + j) * kTK + i * 32 + lane;
+          pages[i] = j < n && at < cu.s.hi ? table[min(at >> a.page_shift, int32_t(a.table_ld) - 1)] : 0;
+        }
+      };
+      auto fetch = [&](int j) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int32_t at = cu.s.tile(cu.t + j) * kTK + i * 32 + lane;
-        const int32_t z = min(max(pages[i], 0), int32_t(a.pages) - 1) * a.kv_heads + cu.h;
-        const int64_t at_s = ((int64_t(z) << a.page_shift) + (at & ((1 << a.page_shift) - 1))) * C;
+        for (int i = 0; i < kPer; ++i) {
+          const int32_t at = cu.s.tile(cu.t + j) * kTK + i * 32 + lane;
+          const int32_t z = min(max(pages[i], 0), int32_t(a.pages) - 1) * a.kv_heads + cu.h;
+          const int64_t at_s = ((int64_t(z) << a.page_shift) + (at & ((1 << a.page_shift) - 1))) * C;
 #pragma unroll
-        for (int y = 0; y < kW; ++y) {
-          kw[i][y] = vw[i][y] = 0;
-          if (j < n && at < cu.s.hi) {
-            if constexpr (C == 2) {
-              kw[i][0] = *reinterpret_cast<const uint16_t*>(a.k_scales + at_s);
-              vw[i][0] = *reinterpret_cast<const uint16_t*>(a.v_scales + at_s);
-            } else {
-              kw[i][y] = *reinterpret_cast<const uint32_t*>(a.k_scales + at_s + 4 * y);
-              vw[i][y] = *reinterpret_cast<const uint32_t*>(a.v_scales + at_s + 4 * y);
+          for (int y = 0; y < kW; ++y) {
+            kw[i][y] = vw[i][y] = 0;
+            if (j < n && at < cu.s.hi) {
+              if constexpr (C == 2) {
+                kw[i][0] = *reinterpret_cast<const uint16_t*>(a.k_scales + at_s);
+                vw[i][0] = *reinterpret_cast<const uint16_t*>(a.v_scales + at_s);
+              } else {
+                kw[i][y] = *reinterpret_cast<const uint32_t*>(a.k_scales + at_s + 4 * y);
+                vw[i][y] = *reinterpret_cast<const uint32_t*>(a.v_scales + at_s + 4 * y);
+              }
             }
           }
         }
-      }
-    };
-    int32_t rv = -1;  // of block `lane`
-    look_up(0);
-    fetch(0);
-    look_up(1);
+      };
+      int32_t rv = -1;  // of block `lane`
+      look_up(0);
+      fetch(0);
+      look_up(1);
 #pragma unroll 1
-    for (int j = 0; j < n; ++j) {
-      int32_t mk = 0, mv[C];
-      uint32_t nan[C][kPer], any = 0;
+      for (int j = 0; j < n; ++j) {
+        int32_t mk = 0, mv[C];
+        uint32_t nan[C][kPer], any = 0;
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        mv[c] = 0;
+        for (int c = 0; c < C; ++c) {
+          mv[c] = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int32_t ek = (kw[i][c / 4] >> (8 * (c % 4))) & 0xFF;
-          const int32_t ev = (vw[i][c / 4] >> (8 * (c % 4))) & 0xFF;
-          mk = max(mk, ek == 255 ? 0 : ek);
-          mv[c] = max(mv[c], ev == 255 ? 0 : ev);
-          nan[c][i] = __ballot_sync(0xFFFFFFFFu, ev == 255);
-          any |= nan[c][i];
+          for (int i = 0; i < kPer; ++i) {
+            const int32_t ek = (kw[i][c / 4] >> (8 * (c % 4))) & 0xFF;
+            const int32_t ev = (vw[i][c / 4] >> (8 * (c % 4))) & 0xFF;
+            mk = max(mk, ek == 255 ? 0 : ek);
+            mv[c] = max(mv[c], ev == 255 ? 0 : ev);
+            nan[c][i] = __ballot_sync(0xFFFFFFFFu, ev == 255);
+            any |= nan[c][i];
+          }
         }
-      }
-      fetch(j + 1);
-      look_up(j + 2);
-      const int slot = (g + j) % kSlots, meta = (g + j) & (kMeta - 1);
-      mk = __reduce_max_sync(0xFFFFFFFFu, mk);
-      // lane c takes block c from here
-      int32_t top = 0;
-      uint32_t bits[kPer];
+        fetch(j + 1);
+        look_up(j + 2);
+        const int slot = (g + j) % kSlots, meta = (g + j) & (kMeta - 1);
+        mk = __reduce_max_sync(0xFFFFFFFFu, mk);
+        // lane c takes block c from here
+        int32_t top = 0;
+        uint32_t bits[kPer];
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int32_t t = __reduce_max_sync(0xFFFFFFFFu, mv[c]);
-        if (lane == c) {
-          top = t;
+        for (int c = 0; c < C; ++c) {
+          const int32_t t = __reduce_max_sync(0xFFFFFFFFu, mv[c]);
+          if (lane == c) {
+            top = t;
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) bits[i] = nan[c][i];
+            for (int i = 0; i < kPer; ++i) bits[i] = nan[c][i];
+          }
         }
-      }
-      // values: running references, raised only when the headroom is used up
-      float fac = 1.0f;
-      const bool up = rv >= 0 && top > rv + kHeadroom;
-      if (up) fac = pow2i(rv - top);
-      if (up || rv < 0) rv = top;
-      const bool raised = __any_sync(0xFFFFFFFFu, lane < C && up);
-      // whoever used this place kMeta tiles ago is done once the slot is empty
-      ok = wait(&sh.kv_empty[slot], (((g + j) / kSlots) & 1) ^ 1);
-      if (!ok) break;
-      if (lane < C) {
-        sh.rv[meta][lane] = rv;
-        sh.vfac[meta][lane] = fac;
+        // values: running references, raised only when the headroom is used up
+        float fac = 1.0f;
+        const bool up = rv >= 0 && top > rv + kHeadroom;
+        if (up) fac = pow2i(rv - top);
+        if (up || rv < 0) rv = top;
+        const bool raised = __any_sync(0xFFFFFFFFu, lane < C && up);
+        // whoever used this place kMeta tiles ago is done once the slot is empty
+        ok = wait(&sh.kv_empty[slot], (((g + j) / kSlots) & 1) ^ 1);
+        if (!ok) break;
+        if (lane < C) {
+          sh.rv[meta][lane] = rv;
+          sh.vfac[meta][lane] = fac;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) sh.nan_bits[meta][lane][i] = bits[i];
+          for (int i = 0; i < kPer; ++i) sh.nan_bits[meta][lane][i] = bits[i];
+        }
+        if (lane == 0) {
+          sh.rk[meta] = mk;
+          sh.raised[meta] = raised;
+          sh.nan_any[meta] = any;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.ref_full[slot]);
       }
-      if (lane == 0) {
-        sh.rk[meta] = mk;
-        sh.raised[meta] = raised;
-        sh.nan_any[meta] = any;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.ref_full[slot]);
-    }
     }
   } else {
     // ------------------------------------------------------------ MMA issue
     // The whole warp runs this and one thread is elected where it issues: the
     // descriptors then stay in uniform registers (issued under lane == 0, an
-    // MMA took 25 instructions and the issuing warp was the bottleneck).
+    // MMA took 25 instructions and the issuing warp was the bottleneck: 336
+    // against 279 us).
     constexpr uint32_t kIdS = (1u << 4) | (uint32_t(kTK >> 3) << 17) | (8u << 24);               // M = 128, N = kTK
     constexpr uint32_t kIdO = (1u << 4) | (1u << 16) | (uint32_t(D >> 3) << 17) | (8u << 24);    // N = D, B MN-major
     const int qt = warp - T::kWarpMma;

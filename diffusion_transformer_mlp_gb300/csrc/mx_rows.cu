@@ -449,7 +449,7 @@ nvfp4_status rows_launch(const void* a_q, const void* w_q, int64_t m, int64_t n,
   // The largest split whose clusters run all at once and that leaves every CTA
   // a k-tile: a CTA alone draws about 33 GB/s of its SM's share, and a second
   // wave costs a whole pass.  1 x 5376 x 14336 (42 tiles): split 1 to 8 take
-  // 28.4, 17.3, 13.9, 12.9, 12.4, 12.2, 17.0 and 17.0 us; 7 and 8 do not fit.
+  // 23.0, 13.8, 10.9, 11.0, 11.0, 11.0, 14.6 and 14.0 us; 7 and 8 do not fit.
   static std::atomic<int32_t> fit[kMaxSplit] = {};
   int64_t split = 1;
   for (int c = std::min(tiles, kMaxSplit); c > 1; --c) {

@@ -248,7 +248,7 @@ static_assert(Nvfp4::SMEM_BYTES + kSiluSmemBytes <= 232448, "shared memory budge
 // the plain epilogue's output slots: one per warp, 32 rows x 16 BF16 columns
 constexpr int kOutSlotBytes = 32 * 16 * 2;
 static_assert(Nvfp4::SMEM_BYTES + EPI_WARPS * kOutSlotBytes <= 232448, "shared memory budget of the plain epilogue");
-// MXFP4: 32 rows x 16 columns of up to 4 bytes
+// MXFP4: 32 rows x 16 columns of 4 bytes, or 32 of 2
 constexpr int kMxSlotBytes = 32 * 16 * 4;
 static_assert(Mxfp4::SMEM_BYTES + EPI_WARPS * kMxSlotBytes <= 232448, "shared memory budget of the MXFP4 epilogue");
 static_assert((Nvfp4::SMEM_BYTES - 1024 - BAR_BYTES) % 1024 == 0 && BAR_BYTES % 128 == 0, "output slots 128-byte aligned");

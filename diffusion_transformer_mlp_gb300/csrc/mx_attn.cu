@@ -23,8 +23,8 @@ namespace {
 //   rows        16         48         64        128
 //   dim  64   63 / 284  159 / 284  205 / 279  396 / 287
 //   dim 128   96 / 309  242 / 310  313 / 309  610 / 292
-//   dim 256  325 / 441  874 / 451 1121 / 447
-// (dim 256, 24 rows: 580 / 441).  One sequence of 16,000 keys, dim 128: 26 / 43,
+//   dim 256  340 / 308  909 / 365 1175 / 362
+// (dim 256, 8 rows: 205 / 308).  One sequence of 16,000 keys, dim 128: 26 / 43,
 // 30 / 43, 38 / 43, 56 / 41.
 bool many_rows(int32_t dim, int64_t rows) { return rows > (dim == 256 ? 16 : 64); }
 }  // namespace

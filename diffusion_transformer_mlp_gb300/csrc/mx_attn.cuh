@@ -30,11 +30,16 @@ struct AttnParams {
 };
 
 // The keys that rows [i0, i1] (queries of one sequence) may see, in tiles of
-// `tok` keys: tiles [0, sink_tiles) and [lo_tile, hi_tile).
+// `tok` keys: tiles [0, sink_tiles) and [lo_tile, hi_tile).  The tiles at their
+// ends also hold keys that none of the rows sees, whose bytes may be anything
+// (pages that left the window are used again): those enter nothing.
 struct Span {
-  int32_t hi;          // keys >= hi are seen by none of the rows
+  int32_t lo, hi;      // seen by some row: keys of [lo, hi) and, with a window, those below p.sinks and hi
   int32_t lo_tile, sink_tiles, n;
   __device__ __forceinline__ int32_t tile(int32_t s) const { return s < sink_tiles ? s : s - sink_tiles + lo_tile; }
+  __device__ __forceinline__ bool has(const AttnParams& p, int32_t j) const {
+    return j < hi && (j >= lo || j < p.sinks);  // lo is 0 without a window
+  }
 };
 
 __device__ __forceinline__ Span span_of(const AttnParams& p, int32_t len, int32_t nq, int32_t i0, int32_t i1,
@@ -46,7 +51,7 @@ __device__ __forceinline__ Span span_of(const AttnParams& p, int32_t len, int32_
   int32_t lo = p.window > 0 ? base + i0 + 1 - p.window : 0;
   lo = min(max(lo, 0), hi);
   const int32_t hi_tile = (hi + tok - 1) / tok;
-  s.hi = hi;
+  s.lo = lo, s.hi = hi;
   s.lo_tile = lo / tok;
   s.sink_tiles = p.window > 0 ? min((min(p.sinks, hi) + tok - 1) / tok, s.lo_tile) : 0;
   s.n = s.sink_tiles + hi_tile - s.lo_tile;

@@ -580,13 +580,13 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
       const int32_t* table = a.table + int64_t(cu.b) * a.table_ld;
       auto page_of = [&](int j) -> int32_t {
         const int32_t at = cu.s.tile(cu.t + j) * kTK + tok;
-        return j < n && at < cu.s.hi ? table[min(at >> a.page_shift, int32_t(a.table_ld) - 1)] : 0;
+        return j < n && cu.s.has(a, at) ? table[min(at >> a.page_shift, int32_t(a.table_ld) - 1)] : 0;
       };
       uint4 raw[2][kWords];  // codes of K and V
       uint32_t sc[2] = {0, 0};
       auto fetch = [&](int j, int32_t page) {
         const int32_t at = cu.s.tile(cu.t + j) * kTK + tok;
-        const bool in = j < n && at < cu.s.hi;
+        const bool in = j < n && cu.s.has(a, at);  // keys that no row sees are zeros
         const int32_t z = min(max(page, 0), int32_t(a.pages) - 1) * a.kv_heads + cu.h;
         const int64_t rowi = (int64_t(z) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
 #pragma unroll
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int32_t at = cu.s.tile(cu.t + j) * kTK + i * 32 + lane;
-          pages[i] = j < n && at < cu.s.hi ? table[min(at >> a.page_shift, int32_t(a.table_ld) - 1)] : 0;
+          pages[i] = j < n && cu.s.has(a, at) ? table[min(at >> a.page_shift, int32_t(a.table_ld) - 1)] : 0;
         }
       };
       auto fetch = [&](int j) {
@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
 #pragma unroll
           for (int y = 0; y < kW; ++y) {
             kw[i][y] = vw[i][y] = 0;
-            if (j < n && at < cu.s.hi) {
+            if (j < n && cu.s.has(a, at)) {
               if constexpr (C == 2) {
                 kw[i][0] = *reinterpret_cast<const uint16_t*>(a.k_scales + at_s);
                 vw[i][0] = *reinterpret_cast<const uint16_t*>(a.v_scales + at_s);

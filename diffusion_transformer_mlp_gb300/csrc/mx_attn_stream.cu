@@ -355,7 +355,6 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
 
   // kSub keys from smem: `sub` of the stage at codes kc, vc, scales ks, vs
   auto work = [&](uint32_t kc, uint32_t vc, const uint8_t* ks, const uint8_t* vs, int32_t tok0) {
-    const int32_t lim = cu.s.hi - tok0;  // keys that some row may see: those below
     uint32_t nan_keys[U][C] = {};        // keys whose block holds NaN (E = 255)
     bool nan_scale = false;
     // scales: K as floats; V as FP16 factors against the running maximum
@@ -367,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
         if constexpr (C == 2) {
           const uint32_t kw = *reinterpret_cast<const uint16_t*>(ks + t * 2);
           uint32_t vw = *reinterpret_cast<const uint16_t*>(vs + t * 2);
-          if (t >= lim) vw = 0;  // a key that no row sees, whose bytes may be anything
+          if (!cu.s.has(a, tok0 + t)) vw = 0;  // no row sees it: no factor, no reference, no NaN
           *reinterpret_cast<float2*>(kf + pos * 2) = make_float2(e8m0_byte(kw, 0), e8m0_byte(kw, 1));
           e[u][0] = vw & 0xFF, e[u][1] = vw >> 8;
         } else {
@@ -375,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
           for (int h = 0; h < C / 4; ++h) {
             const uint32_t kw = *reinterpret_cast<const uint32_t*>(ks + t * C + 4 * h);
             uint32_t vw = *reinterpret_cast<const uint32_t*>(vs + t * C + 4 * h);
-            if (t >= lim) vw = 0;
+            if (!cu.s.has(a, tok0 + t)) vw = 0;
             *reinterpret_cast<float4*>(kf + pos * C + 4 * h) =
                 make_float4(e8m0_byte(kw, 0), e8m0_byte(kw, 1), e8m0_byte(kw, 2), e8m0_byte(kw, 3));
 #pragma unroll

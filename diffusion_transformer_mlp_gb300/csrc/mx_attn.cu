@@ -73,6 +73,8 @@ extern "C" nvfp4_status mxfp4_cache_attention(const mxfp4_cache* cache, const mx
   AttnParams p;
   p.q = g.q, p.out = g.out, p.lse = g.lse;
   p.table = g.table, p.lens = g.lens, p.q_starts = g.q_starts;
+  p.k_codes = static_cast<const uint8_t*>(cache->k_codes);
+  p.v_codes = static_cast<const uint8_t*>(cache->v_codes);
   p.k_scales = static_cast<const uint8_t*>(cache->k_scales);
   p.v_scales = static_cast<const uint8_t*>(cache->v_scales);
   p.dev_status = g.dev_status;

@@ -17,6 +17,8 @@ struct AttnParams {
   const int32_t* table;
   const int32_t* lens;
   const int32_t* q_starts;  // null: one query a sequence
+  const uint8_t* k_codes;
+  const uint8_t* v_codes;
   const uint8_t* k_scales;
   const uint8_t* v_scales;
   uint32_t* dev_status;
@@ -95,6 +97,7 @@ struct SplitParams {
   int32_t workers;
   int32_t least, even;  // tiles of a run: at least, if there are that many; see live_workers
   int32_t edge;
+  int32_t several;   // sequences may have several queries
   float* part_o;     // [2 * workers][rows][D] (k_attn_chunk: [D / 4][rows][4]); see part_exponent
   float2* part_ml;   // [2 * workers][rows]  (reference, sum)
   int64_t* prefix;   // [seqs + 1] places before each sequence, written by block 0 for k_attn_combine
@@ -285,6 +288,249 @@ __device__ __forceinline__ void store_o8(const AttnParams& a, uint16_t* dst, con
   for (int i = 0; i < 4; ++i)
     w[i] = a.bf16 ? f32_to_word<__nv_bfloat16>(f[2 * i], f[2 * i + 1]) : f32_to_word<__half>(f[2 * i], f[2 * i + 1]);
   store_o8_words(a, dst, make_uint4(w[0], w[1], w[2], w[3]));
+}
+
+// Keys that only some rows see.  Both kernels put the values of all rows of a
+// tile (k_attn_chunk the keys of a tile too) under one power of two, which comes
+// from the keys that some row sees.  Where the largest is one that not all see,
+// the others may lose bits to it: such segments (their parts that a worker has)
+// are worked once more at the end of the worker's run, a row at a time in
+// binary32 throughout (too_wide, wide_segment).  The kernels' loops only notice
+// where that may be so (Spread).
+//
+// The keys that the rows of a row tile have in common, of those that one has:
+// j < end with j >= from or j < sinks.
+struct Common {
+  int32_t end, from;
+  bool one;  // all rows are of one query
+};
+__device__ __forceinline__ Common common_of(const AttnParams& a, int32_t len, int32_t nq, int32_t rt, int32_t rows) {
+  const int32_t i0 = rt * rows / a.group, i1 = (min((rt + 1) * rows, nq * a.group) - 1) / a.group;
+  Common c;
+  c.one = i0 == i1;
+  c.end = a.causal ? min(len, len - nq + i0 + 1) : len;
+  c.from = a.window > 0 ? len - nq + i1 + 1 - a.window : 0;
+  return c;
+}
+// Whether all rows see all keys of [j, j + n).
+__device__ __forceinline__ bool all_see(const AttnParams& a, const Common& c, int32_t j, int32_t n) {
+  return j + n <= c.end && (j >= c.from || j + n <= a.sinks);
+}
+
+// A lane's block column of a segment, at its tiles (or parts of them) that not all
+// rows see.  Every row's largest scale code is at least `floor`, the largest of
+// keys that all rows see (0: none so far), or else `least`, the smallest code but
+// 0 of the keys that some see.
+struct Spread {
+  int32_t floor, least;
+  __device__ __forceinline__ void reset() { floor = 0, least = 255; }
+  __device__ __forceinline__ bool open() const { return floor == 0 && least < 255; }
+  // Codes of up to `top`, the smallest but 0 being `low`; those before had up to
+  // `old`.  False if some row's values may be more than `spread` below the others.
+  __device__ __forceinline__ bool some_see(int32_t old, int32_t top, int32_t low, int32_t spread) {
+    if (floor == 0 && least == 255) floor = old;  // all before were seen by all
+    if (floor == 0) least = min(least, low);
+    return max(old, top) <= (floor > 0 ? floor : least) + spread;
+  }
+  __device__ __forceinline__ bool all_see(int32_t old, int32_t top, int32_t spread) {
+    if (!open() || top == 0) return true;
+    floor = top;
+    return old <= top + spread;
+  }
+};
+
+// Row of key j of the segment at c in the cache.
+__device__ __forceinline__ int64_t key_row(const AttnParams& a, const Cursor& c, int32_t j) {
+  const int32_t page = a.table[int64_t(c.b) * a.table_ld + min(j >> a.page_shift, int32_t(a.table_ld) - 1)];
+  const int32_t z = min(max(page, 0), int32_t(a.pages) - 1) * a.kv_heads + c.h;
+  return (int64_t(z) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
+}
+
+// Whether n tiles from tile c.t on have to be worked once more, by a whole warp.
+// Every row sees the keys that all see, or else at least one of the others; so
+// no row's largest value is more than 2^spread_v below the reference if in each
+// block column the largest scale code of the others is no more than that above
+// the largest that all see or, where they see none, above the smallest (0 is the
+// code of no value).  The kernel's keys are exact within 2^spread_k of the largest
+// of their tile.
+// (Code that runs once costs its fetching, so it is kept short: a lane takes one
+// block column of every 32 / C-th key.)
+template <int D, int kRows>
+__device__ __forceinline__ bool too_wide(const AttnParams& a, const Cursor& c, int32_t n, int32_t tok, int32_t spread_v,
+                                         int32_t spread_k) {
+  constexpr int C = D / 32;
+  const int lane = threadIdx.x & 31;
+  const Common rows = common_of(a, c.len, c.nq, c.rt, kRows);
+  if (rows.one) return false;
+  int32_t all = 0, some = 0, least = 255;  // of this lane's keys
+  bool k_wide = false;
+  auto over_lanes = [&](int32_t v) {  // the largest of the lanes that have this block column
+#pragma unroll 1
+    for (int o = C; o < 32; o <<= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+  };
+  bool any = false, wide = false;
+  // first the tiles that not all see, whose other keys mostly tell already
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+    for (int32_t s = 0; s < n; ++s) {
+      if (pass == 0 && s % 32 == 0) {  // 32 tiles at a time
+        const int32_t mine = s + lane;
+        if (__all_sync(0xFFFFFFFFu, mine >= n || all_see(a, rows, c.s.tile(c.t + min(mine, n - 1)) * tok, tok))) {
+          s += 31;
+          continue;
+        }
+      }
+      const int32_t tok0 = c.s.tile(c.t + s) * tok;
+      if (all_see(a, rows, tok0, tok) != (pass == 1)) continue;
+      any = true;
+      int32_t kmax = 0, kmin = 255;
+#pragma unroll 4
+      for (int32_t i = lane / C; i < tok; i += 32 / C) {
+        const int32_t j = tok0 + i;
+        if (!c.s.has(a, j)) continue;
+        const int64_t at = key_row(a, c, j) * C + lane % C;
+        const int32_t v = a.v_scales[at], k = spread_k > 0 && pass == 0 ? a.k_scales[at] : 0;
+        const bool common = all_see(a, rows, j, 1);
+        if (v != 255 && common) all = max(all, v);
+        if (v != 255 && v > 0 && !common) some = max(some, v), least = min(least, v);
+        if (k != 255 && k > 0) kmax = max(kmax, k), kmin = min(kmin, k);
+      }
+      if (spread_k > 0 && pass == 0)
+        k_wide = k_wide || __reduce_min_sync(0xFFFFFFFFu, kmin) < __reduce_max_sync(0xFFFFFFFFu, kmax) - spread_k;
+      if (pass == 1) {
+        wide = __any_sync(0xFFFFFFFFu, over_lanes(some) > over_lanes(all) + spread_v);
+        if (!wide) return false;
+      }
+    }
+    if (k_wide) return true;
+    if (!any) return false;
+    wide = __any_sync(0xFFFFFFFFu, over_lanes(some) > over_lanes(all) + spread_v);
+    if (!wide) return false;
+  }
+  // no keys that all see: every row sees one of the others
+  if (__any_sync(0xFFFFFFFFu, all > 0)) return true;
+  return __any_sync(0xFFFFFFFFu, some > int32_t(__reduce_min_sync(0xFFFFFFFFu, least)) + spread_v);
+}
+
+// One row (of the segment at c) over n tiles of `tok` keys from tile c.t on, by a
+// whole warp: a lane is a key for the scores, column 32 c + lane for the outputs.
+// Slow (about 60 instructions a key), and rarely called.  part_o is null for a
+// row of the output, else column d of its partial lies at (d / 4) * part_step + d % 4.
+template <int D>
+__device__ __forceinline__ void wide_row(const AttnParams& a, const Cursor& cu, int32_t n, int32_t tok, int32_t row,
+                                         float* part_o, int64_t part_step, float2* part_ml) {
+  constexpr int C = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int32_t qi = row / a.group, hq = cu.h * a.group + row - qi * a.group, pos = cu.len - cu.nq + qi;
+  const int32_t end = a.causal ? min(cu.len, pos + 1) : cu.len, from = a.window > 0 ? pos - a.window + 1 : 0;
+  const uint16_t* q = static_cast<const uint16_t*>(a.q) + int64_t(cu.q0 + qi) * a.q_st + int64_t(hq) * a.q_sh;
+  float qv[C], o[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const uint32_t x = q[32 * c + lane];
+    qv[c] = a.bf16 ? word_to_f32<__nv_bfloat16>(x).x : word_to_f32<__half>(x).x;
+    o[c] = 0.0f;
+  }
+  float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
+  for (int32_t i = 0; i < n * (tok / 32); ++i) {
+    const int32_t t = i / (tok / 32);
+    const int32_t j = cu.s.tile(cu.t + t) * tok + (i - t * (tok / 32)) * 32 + lane;
+    const bool seen = j < end && (j >= from || j < a.sinks);
+    const uint32_t any = __ballot_sync(0xFFFFFFFFu, seen);
+    if (any == 0) continue;
+    int64_t at = 0;  // row of the key in the cache
+    if (seen) at = key_row(a, cu, j);
+    float s = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float part = 0.0f;
+#pragma unroll 1
+      for (int x = 0; x < 4; ++x) {
+        uint32_t h[4];
+        e2m1x8_to_half(reinterpret_cast<const uint32_t*>(a.k_codes + at * (D / 2))[4 * c + x], h);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const float2 k = word_to_f32<__half>(h[y]);
+          part = fmaf(k.x, __shfl_sync(0xFFFFFFFFu, qv[c], 8 * x + 2 * y), part);
+          part = fmaf(k.y, __shfl_sync(0xFFFFFFFFu, qv[c], 8 * x + 2 * y + 1), part);
+        }
+      }
+      s = fmaf(part, e8m0_value(a.k_scales[at * C + c]), s);
+    }
+    s = seen ? s * a.scale_log2 : -INFINITY;
+    float top = s;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+    top = fmaxf(top, m);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    const float alpha = exp2_approx(m - ref), p = exp2_approx(s - (ref - kWeightLog2));
+    m = top;
+    l = l * alpha + p;
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] *= alpha;
+#pragma unroll 1
+    for (uint32_t left = any; left != 0; left &= left - 1) {
+      const int u = __ffs(left) - 1;
+      const int64_t key = __shfl_sync(0xFFFFFFFFu, at, u);
+      const float pu = __shfl_sync(0xFFFFFFFFu, p, u);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        uint32_t h[4];
+        e2m1x8_to_half(uint32_t(a.v_codes[key * (D / 2) + 16 * c + lane / 2]) >> (4 * (lane & 1)), h);
+        o[c] = fmaf(pu, word_to_f32<__half>(h[0]).x * e8m0_value(a.v_scales[key * C + c]), o[c]);
+      }
+    }
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
+  const int32_t pe = part_exponent(l);
+  if (part_o != nullptr) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) part_o[(8 * c + lane / 4) * part_step + lane % 4] = o[c] * pow2i(-pe);
+    if (lane == 0) *part_ml = make_float2(m + float(pe), l * pow2i(-pe));
+    return;
+  }
+  const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+  uint16_t* out = static_cast<uint16_t*>(a.out) + int64_t(cu.q0 + qi) * a.o_st + int64_t(hq) * a.o_sh;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const float f = o[c] * inv;
+    out[32 * c + lane] = uint16_t(a.bf16 ? f32_to_word<__nv_bfloat16>(f, 0.0f) : f32_to_word<__half>(f, 0.0f));
+  }
+  if (lane == 0 && a.lse != nullptr)
+    a.lse[int64_t(cu.q0 + qi) * (a.kv_heads * a.group) + hq] =
+        l == 0.0f ? -INFINITY : (m - kWeightLog2 + log2f(l)) * 0.6931471805599453f;
+}
+
+// Calls f(segment, its tiles, its place among the workers' partials) for the
+// segments of the worker's run of `places` places from `first` on.
+template <int kRows, class F>
+__device__ __forceinline__ void walk_run(const SplitParams& sp, const Cursor& first, int32_t places, int32_t worker,
+                                         int32_t tok, F f) {
+  Cursor c = first;
+#pragma unroll 1
+  for (int64_t part = int64_t(worker) * 2;; part = int64_t(worker) * 2 + 1) {
+    const int32_t n = min(c.s.n - c.t, places);
+    f(c, n, part);
+    places -= n + sp.edge;
+    if (places <= 0) return;
+    c.t += n - 1;
+    cursor_next(c, sp.a, kRows, tok);
+  }
+}
+// Rows r0, r0 + dr, .. of a segment (or of the run's part of it) anew.
+template <int D, int kRows, bool kByColumns>
+__device__ __forceinline__ void wide_segment(const SplitParams& sp, const Cursor& c, int32_t n, int64_t part, int32_t tok,
+                                             int32_t r0, int32_t dr) {
+  const bool whole = c.t == 0 && n == c.s.n;
+#pragma unroll 1
+  for (int32_t r = r0; r < kRows && c.rt * kRows + r < c.nq * sp.a.group; r += dr)
+    wide_row<D>(sp.a, c, n, tok, c.rt * kRows + r,
+                whole ? nullptr : sp.part_o + (kByColumns ? (part * (D / 4) * kRows + r) * 4 : (part * kRows + r) * D),
+                kByColumns ? kRows * 4 : 4, sp.part_ml + part * kRows + r);
 }
 
 // The queries and outputs of the sequences from b on.

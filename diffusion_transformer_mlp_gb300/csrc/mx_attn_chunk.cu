@@ -58,6 +58,10 @@ constexpr int kMeta = 8;       // tiles whose references are kept: the decoders 
 constexpr int kTK = 64;        // keys of a tile
 constexpr int kHeadroom = 8;   // value scales may exceed their reference by 2^8 before it is raised
 constexpr int kLiftK = 13, kLiftV = 5;  // largest elements: 6 * 2^13
+// Where rows see different keys (see too_wide): keys down to 2^-36 of the tile's
+// largest are exact, and values down to 2^-28 of their reference, which leaves
+// 2^-12 of the largest that a row sees.
+constexpr int kSpreadK = 23 + kLiftK, kSpreadV = 16;
 
 template <int D>
 struct Chunk {
@@ -110,6 +114,8 @@ struct Shared {
   uint32_t raised[kMeta];      // the factors are not all 1
   uint32_t nan_any[kMeta];     // a block of values holds NaN
   uint32_t nan_bits[kMeta][8][kTK / 32];  // [block][32 tokens]
+  int check;                   // the run may have segments to work anew
+  uint32_t wide[32];           // those: a bit each, shared by those 1,024 apart
 };
 static_assert(sizeof(Shared) <= 4096, "shared state");
 
@@ -201,6 +207,28 @@ __device__ __noinline__ uint4 load_8x16(const uint16_t* e) {
                     uint32_t(e[4]) | uint32_t(e[5]) << 16, uint32_t(e[6]) | uint32_t(e[7]) << 16);
 }
 
+// After the run, by all warps: which segments have to be worked anew (a warp each),
+// and those over what was written.  Not inlined: the loops of the kernel are not to
+// make room for it.
+template <int D>
+__device__ __noinline__ void check_run(const SplitParams& sp, Shared& sh, int32_t places) {
+  using T = Chunk<D>;
+  constexpr int kRows = 128 * T::kNQ, kWarps = T::kThreads / 32;
+  const int warp = threadIdx.x >> 5;
+  for (int pass = 0; pass < 2; ++pass) {
+    int seg = 0;
+    walk_run<kRows>(sp, sh.first, places, int32_t(blockIdx.x), kTK, [&](const Cursor& c, int32_t n, int64_t part) {
+      const uint32_t bit = 1u << (seg / 32 & 31);
+      if (pass == 0 && seg % kWarps == warp && too_wide<D, kRows>(sp.a, c, n, kTK, kSpreadV, kSpreadK))
+        atomicOr(&sh.wide[seg & 31], bit);
+      if (pass == 1 && (sh.wide[seg & 31] & bit)) wide_segment<D, kRows, true>(sp, c, n, part, kTK, warp, kWarps);
+      ++seg;
+    });
+    __syncthreads();
+    if (!__any_sync(0xFFFFFFFFu, sh.wide[threadIdx.x & 31] != 0)) return;
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     k_attn_chunk(const uint8_t* __restrict__ k_codes, const uint8_t* __restrict__ v_codes,
@@ -258,6 +286,8 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
       mbar_init(&sh.o_empty[i], 4);
     }
     sh.abort_flag = 0;
+    for (uint32_t& w : sh.wide) w = 0;
+    sh.check = 0;
     fence_barrier_init();
   }
   if (warp == T::kWarpMma) tmem_alloc(&sh.tmem, T::kTmem);
@@ -580,14 +610,15 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
       const int32_t* table = a.table + int64_t(cu.b) * a.table_ld;
       auto page_of = [&](int j) -> int32_t {
         const int32_t at = cu.s.tile(cu.t + j) * kTK + tok;
-        return j < n && cu.s.has(a, at) ? table[min(at >> a.page_shift, int32_t(a.table_ld) - 1)] : 0;
+        // -1: a key that no row sees, which counts as zeros
+        return j < n && cu.s.has(a, at) ? max(table[min(at >> a.page_shift, int32_t(a.table_ld) - 1)], 0) : -1;
       };
       uint4 raw[2][kWords];  // codes of K and V
       uint32_t sc[2] = {0, 0};
       auto fetch = [&](int j, int32_t page) {
         const int32_t at = cu.s.tile(cu.t + j) * kTK + tok;
-        const bool in = j < n && cu.s.has(a, at);  // keys that no row sees are zeros
-        const int32_t z = min(max(page, 0), int32_t(a.pages) - 1) * a.kv_heads + cu.h;
+        const bool in = page >= 0;
+        const int32_t z = min(page, int32_t(a.pages) - 1) * a.kv_heads + cu.h;
         const int64_t rowi = (int64_t(z) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
@@ -679,19 +710,19 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int32_t at = cu.s.tile(cu.t + j) * kTK + i * 32 + lane;
-          pages[i] = j < n && cu.s.has(a, at) ? table[min(at >> a.page_shift, int32_t(a.table_ld) - 1)] : 0;
+          pages[i] = j < n && cu.s.has(a, at) ? max(table[min(at >> a.page_shift, int32_t(a.table_ld) - 1)], 0) : -1;
         }
       };
       auto fetch = [&](int j) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int32_t at = cu.s.tile(cu.t + j) * kTK + i * 32 + lane;
-          const int32_t z = min(max(pages[i], 0), int32_t(a.pages) - 1) * a.kv_heads + cu.h;
+          const int32_t z = min(pages[i], int32_t(a.pages) - 1) * a.kv_heads + cu.h;
           const int64_t at_s = ((int64_t(z) << a.page_shift) + (at & ((1 << a.page_shift) - 1))) * C;
 #pragma unroll
           for (int y = 0; y < kW; ++y) {
             kw[i][y] = vw[i][y] = 0;
-            if (j < n && cu.s.has(a, at)) {
+            if (pages[i] >= 0) {
               if constexpr (C == 2) {
                 kw[i][0] = *reinterpret_cast<const uint16_t*>(a.k_scales + at_s);
                 vw[i][0] = *reinterpret_cast<const uint16_t*>(a.v_scales + at_s);
@@ -704,6 +735,12 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
         }
       };
       int32_t rv = -1;  // of block `lane`
+      // largest scale of the values that all rows see, smallest but 0 (less 1) of
+      // all blocks of the others' tiles
+      const Common rows = common_of(a, cu.len, cu.nq, cu.rt, kRows);
+      int32_t common = 0;
+      uint32_t least = 254;
+      bool check = false;
       look_up(0);
       fetch(0);
       look_up(1);
@@ -724,10 +761,23 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
             any |= nan[c][i];
           }
         }
+        mk = __reduce_max_sync(0xFFFFFFFFu, mk);
+        const bool all = rows.one || all_see(a, rows, cu.s.tile(cu.t + j) * kTK, kTK);
+        if (!all) {
+          uint32_t lk = 254, lv = 254;
+#pragma unroll 1
+          for (int b = 0; b < 32; b += 8)
+#pragma unroll
+            for (int i = 0; i < kPer * kW; ++i) {
+              lk = min(lk, ((kw[i / kW][i % kW] >> b) & 0xFF) - 1);
+              lv = min(lv, ((vw[i / kW][i % kW] >> b) & 0xFF) - 1);
+            }
+          least = min(least, __reduce_min_sync(0xFFFFFFFFu, lv));
+          check = check || int32_t(__reduce_min_sync(0xFFFFFFFFu, lk)) + 1 < mk - kSpreadK;
+        }
         fetch(j + 1);
         look_up(j + 2);
         const int slot = (g + j) % kSlots, meta = (g + j) & (kMeta - 1);
-        mk = __reduce_max_sync(0xFFFFFFFFu, mk);
         // lane c takes block c from here
         int32_t top = 0;
         uint32_t bits[kPer];
@@ -745,6 +795,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
         const bool up = rv >= 0 && top > rv + kHeadroom;
         if (up) fac = pow2i(rv - top);
         if (up || rv < 0) rv = top;
+        if (all) common = max(common, top);
         const bool raised = __any_sync(0xFFFFFFFFu, lane < C && up);
         // whoever used this place kMeta tiles ago is done once the scores of
         // kSlots tiles ago are there
@@ -764,6 +815,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.ref_full[slot]);
       }
+      if (lane < C && !rows.one && (check || rv > (common > 0 ? common : int32_t(least) + 1) + kSpreadV)) sh.check = 1;
     }
   } else {
     // ------------------------------------------------------------ MMA issue
@@ -826,6 +878,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
   tc_fence_after();
   if (threadIdx.x == 0 && sh.abort_flag && a.dev_status != nullptr)
     atomicExch(a.dev_status, static_cast<uint32_t>(NVFP4_ETIMEOUT));
+  if (sh.check) check_run<D>(sp, sh, tiles);
   if (warp == T::kWarpMma) {
     __syncwarp();
     tmem_dealloc(tmem, T::kTmem);
@@ -861,6 +914,7 @@ nvfp4_status attn_chunk(const mxfp4_cache* cache, const AttnParams& base, int32_
   SplitParams sp;
   sp.a = base;
   sp.workers = sm_count();
+  sp.several = max_queries > 1;
   sp.least = kLeast, sp.even = 0, sp.edge = kEdge;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   sp.part_o = reinterpret_cast<float*>(ws);

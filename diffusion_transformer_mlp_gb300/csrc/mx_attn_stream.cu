@@ -60,8 +60,13 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 
-// A stage of the ring holds kTok keys, worked off kSub at a time.
-template <int D, int kRows>
+// The largest values that only some rows see may be this far above those that
+// all see: a row's weights down to 2^-27 are then kept by the FP16 of their factor.
+constexpr int kSpreadV = 8;
+
+// A stage of the ring holds kTok keys, worked off kSub at a time.  kSeveral: a
+// sequence may have several queries, so that rows may see different keys.
+template <int D, int kRows, bool kSeveral>
 struct Tile {
   static constexpr int C = D / 32;  // blocks of a row
   static constexpr int kTok = D == 256 ? 32 : (D == 128 ? 64 : 128);
@@ -78,7 +83,7 @@ struct Tile {
   // [warp codes x 4][warp rest x 4][barriers]; the tile counts of the
   // sequences lie where the codes go, before the first load
   static constexpr int kBars = kWarps * kStages * 8;
-  static constexpr int kSmem = kWarps * (kWarpCodes + kWarpRest) + kBars;
+  static constexpr int kSmem = kWarps * (kWarpCodes + kWarpRest + (kSeveral ? int(sizeof(Cursor)) : 0)) + kBars;
   static_assert((kMaxSeqs + 1 + kThreads) * 8 <= kWarps * kWarpCodes, "tile counts");
   static_assert(kCodes % 1024 == 0, "swizzle atoms");
   static_assert(kCtas * (kSmem + 1024) <= 233472, "blocks an SM");
@@ -160,11 +165,21 @@ __device__ __forceinline__ float e8m0_byte(uint32_t w, int i) {
   return __uint_as_float(v & 0x7F800000u);
 }
 
+// Keys that only some rows see, after a warp's run.  Not inlined: the loops of the
+// kernel are not to make room for it.
 template <int D, int kRows>
-__global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
+__device__ __noinline__ void check_run(const SplitParams& sp, const Cursor* start, int32_t tiles, int32_t worker) {
+  constexpr int kTok = Tile<D, kRows, true>::kTok;
+  walk_run<kRows>(sp, *start, tiles, worker, kTok, [&](const Cursor& c, int32_t n, int64_t part) {
+    if (too_wide<D, kRows>(sp.a, c, n, kTok, kSpreadV, 0)) wide_segment<D, kRows, false>(sp, c, n, part, kTok, 0, 1);
+  });
+}
+
+template <int D, int kRows, bool kSeveral>
+__global__ void __launch_bounds__(kThreads, Tile<D, kRows, kSeveral>::kCtas)
     k_attn_stream(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                   const __grid_constant__ SplitParams sp) {
-  using T = Tile<D, kRows>;
+  using T = Tile<D, kRows, kSeveral>;
   constexpr int C = T::C, kTok = T::kTok, kSub = T::kSub, NT = kSub / 8;
   constexpr int R = kRows / 8;   // rows of a thread: g, and g + 8
   constexpr int Y = 2 * R;       // accumulators of a block: 8 rows hold two columns in each
@@ -178,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
   uint8_t* vf = rest + T::kStages * 2 * T::kScales + T::kKf;
   uint8_t* tail = base + kWarps * (T::kWarpCodes + T::kWarpRest);
   uint64_t* full = reinterpret_cast<uint64_t*>(tail) + warp * T::kStages;
+  Cursor* start = reinterpret_cast<Cursor*>(tail + T::kBars) + warp;  // of this warp's run
   int64_t* prefix = reinterpret_cast<int64_t*>(base);
 
   if (threadIdx.x == 0) {
@@ -200,6 +216,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
   fence_proxy_async_smem();  // the counts are read, the TMA may write there
   __syncthreads();
   if (tiles <= 0) return;
+  if (kSeveral && lane == 0) *start = cu;
 
   // ---- loads: lane i < boxes takes box i of a tile (a page's share of it);
   // its page is looked up when the tile before is issued
@@ -253,7 +270,17 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
   float o[C][Y][4];  // block, MMA of the block, accumulator
   float m[R], l[R];  // softmax reference; sum of this lane's weights, times 2^10
   int32_t rmax[C];   // R of the block columns
+  // kSeveral only
+  Common rows;         // keys that all rows see
+  Spread spread;       // of block column `lane`
+  bool lag = false;    // some are open
+  bool check = false;  // of the whole run
   auto begin_segment = [&]() {
+    if constexpr (kSeveral) {
+      rows = common_of(a, cu.len, cu.nq, cu.rt, kRows);
+      spread.reset();
+      lag = false;
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int32_t row = cu.rt * kRows + g + 8 * r;
@@ -355,6 +382,9 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
 
   // kSub keys from smem: `sub` of the stage at codes kc, vc, scales ks, vs
   auto work = [&](uint32_t kc, uint32_t vc, const uint8_t* ks, const uint8_t* vs, int32_t tok0) {
+    // do all rows see all these keys?
+    const bool all = kSeveral ? all_see(a, rows, tok0, kSub)
+                              : tok0 + kSub <= end[0] && (tok0 >= from[0] || tok0 + kSub <= a.sinks);
     uint32_t nan_keys[U][C] = {};        // keys whose block holds NaN (E = 255)
     bool nan_scale = false;
     // scales: K as floats; V as FP16 factors against the running maximum
@@ -381,6 +411,23 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
             for (int i = 0; i < 4; ++i) e[u][(4 * h + i) % C] = (vw >> (8 * i)) & 0xFF;
           }
         }
+      }
+      if (kSeveral && (!all || lag) && !rows.one) {
+        int32_t top = 0, low = 255, old = 0;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          int32_t hi = 0, lo = 255;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            hi = max(hi, e[u][j] == 255 ? 0 : e[u][j]);
+            if (e[u][j] > 0) lo = min(lo, e[u][j]);
+          }
+          hi = __reduce_max_sync(0xFFFFFFFFu, hi), lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+          if (lane == j) top = hi, low = lo, old = rmax[j];
+        }
+        const bool fine = all ? spread.all_see(old, top, kSpreadV) : spread.some_see(old, top, low, kSpreadV);
+        check = check || __any_sync(0xFFFFFFFFu, !fine);
+        lag = __any_sync(0xFFFFFFFFu, spread.open());
       }
       bool up = false;
 #pragma unroll
@@ -494,16 +541,13 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
     // mask, reference, weights
     // 8 rows: words (p, 0) of the lane's two keys; 16 rows: pairs of the two keys
     uint32_t pw[NT][2];
-    bool all = true;  // do the rows see all these keys?
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      all = all && tok0 + kSub <= end[r] && (tok0 >= from[r] || tok0 + kSub <= a.sinks);
+    for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) s[nt][2 * r + e] *= qf[r];
-    }
-    if (!__all_sync(0xFFFFFFFFu, all)) {
+    if (!all) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -703,13 +747,17 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows>::kCtas)
       if (fresh) from_start = true, part_slot = 1;
     }
   }
+  if (kSeveral && check) {
+    __syncwarp();
+    check_run<D, kRows>(sp, start, tiles, worker);
+  }
 }
 
-template <int D, int kRows>
+template <int D, int kRows, bool kSeveral>
 nvfp4_status stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams& sp, int row_tiles,
                            cudaStream_t stream) {
-  using T = Tile<D, kRows>;
-  auto kern = k_attn_stream<D, kRows>;
+  using T = Tile<D, kRows, kSeveral>;
+  auto kern = k_attn_stream<D, kRows, kSeveral>;
   static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
   nvfp4_status st = allow_smem(reinterpret_cast<const void*>(kern), T::kSmem, ready);
   if (st != NVFP4_OK) return st;
@@ -720,6 +768,14 @@ nvfp4_status stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, const S
               tv, p);
   if (st != NVFP4_OK) return st;
   return attn_combine(D, kRows, T::kTok, row_tiles, p, stream);
+}
+
+template <int D>
+nvfp4_status launch_of(int rows, const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams& sp, int row_tiles,
+                       cudaStream_t stream) {
+  auto f = rows == 8 ? (sp.several ? stream_launch<D, 8, true> : stream_launch<D, 8, false>)
+                     : (sp.several ? stream_launch<D, 16, true> : stream_launch<D, 16, false>);
+  return f(tk, tv, sp, row_tiles, stream);
 }
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -750,6 +806,7 @@ nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32
   if (st != NVFP4_OK) return st;
   SplitParams sp;
   sp.a = base;
+  sp.several = max_queries > 1;
   const int64_t rows_max = int64_t(max_queries) * base.group;
   const int32_t rows = rows_max <= 8 ? 8 : 16;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -765,12 +822,8 @@ nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32
     sp.a.table = base.table + int64_t(b) * base.table_ld;
     sp.a.lens = base.lens + b;
     split_queries(sp.a, base, b);
-    if (dim == 64) st = rows == 8 ? stream_launch<64, 8>(tk, tv, sp, int(row_tiles), stream)
-                                  : stream_launch<64, 16>(tk, tv, sp, int(row_tiles), stream);
-    else if (dim == 128) st = rows == 8 ? stream_launch<128, 8>(tk, tv, sp, int(row_tiles), stream)
-                                        : stream_launch<128, 16>(tk, tv, sp, int(row_tiles), stream);
-    else st = rows == 8 ? stream_launch<256, 8>(tk, tv, sp, int(row_tiles), stream)
-                        : stream_launch<256, 16>(tk, tv, sp, int(row_tiles), stream);
+    auto launch = dim == 64 ? launch_of<64> : (dim == 128 ? launch_of<128> : launch_of<256>);
+    st = launch(rows, tk, tv, sp, int(row_tiles), stream);
     if (st != NVFP4_OK) return st;
   }
   return NVFP4_OK;

@@ -113,3 +113,71 @@ def test_pages_that_left_the_window_without_causality(dim):
         any_bytes(case, 150)
         case.run()
         case.check()
+
+
+@pytest.mark.parametrize("mul", [2.0 ** 30, 2.0 ** 60, 2.0 ** 120, 2.0 ** -60])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_later_tokens_leave_earlier_rows_alone(dim, mul):
+    """Tokens that only the last queries see have values, then keys, far from the
+    other tokens' sizes.  (The rows that see them are compared for the values of
+    2^30 and 2^60, whose outputs are in range.)"""
+    for lens, nq, hq, late in (([70, 300], [9, 4], 2, 3), ([8, 33], [8, 16], 1, 5), ([600, 90], [120, 90], 4, 40),
+                               ([1500], [500], 2, 300)):
+        for what in ("values", "keys"):
+            case = Case(lens, nq, hq, 1, dim, seed=dim + late)
+            at = 0
+            first = []
+            for b, n in enumerate(lens):
+                f = max(n - late, 1)
+                x = case.v if what == "values" else case.k
+                x[at + f:at + n] *= mul
+                first.append(f)
+                at += n
+            case.write()
+            case.run()
+            rows = torch.cat([case.positions(b)[:, 0] < first[b] for b in range(len(lens))])
+            if bool(rows.any()):
+                case.check(rows)
+            if what == "values" and mul <= 2.0 ** 60:
+                case.check()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_one_block_of_a_later_token(dim):
+    """The largest finite scale in one block of one token, by its bytes."""
+    for lens, nq, hq in (([80], [16], 1), ([300], [12], 1), ([300], [100], 2)):
+        for which in ("k_scales", "v_scales"):
+            case = Case(lens, nq, hq, 1, dim, seed=dim)
+            case.write()
+            first = lens[0] - 5
+            slot = case.slots(0)[first]
+            getattr(case.cache, which)[slot // 16, 0, slot % 16, 1] = 254
+            case.run()
+            case.check(case.positions(0)[:, 0] < first)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_older_tokens_leave_later_rows_alone(dim):
+    """The same at the other end: keys that the window of later rows has passed."""
+    for lens, nq, hq, window in (([300], [14], 1, 100), ([300], [7], 2, 130), ([900], [130], 2, 333), ([64], [16], 1, 4)):
+        for mul in (2.0 ** 30, 2.0 ** 100):
+            for what in ("values", "keys"):
+                case = Case(lens, nq, hq, 1, dim, seed=dim + window, window=window)
+                first = lens[0] - nq[0] - window + 1  # the oldest key of the first row
+                edge = first + nq[0] // 2
+                (case.v if what == "values" else case.k)[first:edge] *= mul
+                case.write()
+                case.run()
+                case.check(case.positions(0)[:, 0] - window >= edge - 1)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_rows_split_over_workers(dim):
+    """Long sequences whose keys many warps or blocks share, large values late."""
+    for nq, hq, late in ((4, 4, 2), (80, 2, 50)):
+        case = Case([9000], [nq], hq, 1, dim, page=64, seed=nq)
+        case.v[9000 - late:] *= 2.0 ** 50
+        case.k[9000 - late:, :, :32] *= 2.0 ** 50
+        case.write()
+        case.run()
+        case.check(case.positions(0)[:, 0] < 9000 - late)

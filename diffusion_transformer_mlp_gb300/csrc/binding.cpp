@@ -7,15 +7,17 @@
 // streams only; the C functions come by address from the loaded library
 // (bind), so this module links against no kernel.
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <map>
+#include <cmath>
+#include <cstring>
+#include <optional>
 #include <string>
-#include <tuple>
 
 #include "mxfp4.h"
 
@@ -77,15 +79,41 @@ void on(const Tensor& t, c10::DeviceIndex dev) {
 Tensor empty(at::IntArrayRef sizes, at::ScalarType t, c10::DeviceIndex dev) {
   return at::detail::empty_cuda(sizes, t, at::Device(at::kCUDA, dev), std::nullopt);
 }
-nvfp4_stream_t stream_of(PyObject* o, c10::DeviceIndex dev) {
-  if (o == Py_None) return reinterpret_cast<nvfp4_stream_t>(c10::cuda::getCurrentCUDAStream(dev).stream());
-  PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
-  if (!h) throw Raised();
-  const unsigned long long v = PyLong_AsUnsignedLongLong(h);
-  Py_DECREF(h);
-  if (PyErr_Occurred()) throw Raised();
-  return reinterpret_cast<nvfp4_stream_t>(v);
-}
+// Where a call runs: the current stream, or the given one, which is then the
+// current one for the call, so that the workspaces it takes and gives back and
+// the outputs it allocates belong to the stream that works in them.
+class Launch {
+ public:
+  Launch(PyObject* stream, c10::DeviceIndex dev) : device_(dev), caller_(c10::cuda::getCurrentCUDAStream(dev)) {
+    cudaStream_t s = caller_.stream();
+    if (stream != Py_None) {
+      PyObject* h = PyObject_GetAttrString(stream, "cuda_stream");
+      if (!h) throw Raised();
+      const unsigned long long v = PyLong_AsUnsignedLongLong(h);
+      Py_DECREF(h);
+      if (PyErr_Occurred()) throw Raised();
+      if (reinterpret_cast<cudaStream_t>(v) != s) {
+        s = reinterpret_cast<cudaStream_t>(v);
+        guard_.emplace(s == nullptr ? c10::cuda::getDefaultCUDAStream(dev) : c10::cuda::getStreamFromExternal(s, dev));
+      }
+    }
+    handle_ = reinterpret_cast<nvfp4_stream_t>(s);
+  }
+  nvfp4_stream_t handle() const { return handle_; }
+  // The tensor for the caller, who uses a new one on the stream that was current
+  // (`given`: it is the caller's own).
+  PyObject* result(const Tensor& t, bool given = false) const {
+    if (guard_ && !given && t.numel() > 0)
+      c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), caller_);
+    return THPVariable_Wrap(t);
+  }
+
+ private:
+  c10::cuda::CUDAGuard device_;
+  c10::cuda::CUDAStream caller_;
+  std::optional<c10::cuda::CUDAStreamGuard> guard_;
+  nvfp4_stream_t handle_;
+};
 void done(nvfp4_status st, const char* name) {
   if (st == NVFP4_OK) return;
   PyObject* r = PyObject_CallFunction(check_fn, "is", int(st), name);
@@ -203,7 +231,7 @@ PyObject* quantize(PyObject* const* a) {
   const Tensor& x = tensor(a[0], "x");
   const Mat m = matrix(x, "x");
   const c10::DeviceIndex dev = cuda_index(x);
-  c10::cuda::CUDAGuard guard(dev);
+  const Launch on_stream(a[3], dev);
   Tensor q, s;
   if (a[1] == Py_None) {
     const int64_t groups = (m.cols + 127) / 128;
@@ -217,24 +245,26 @@ PyObject* quantize(PyObject* const* a) {
     q = out.q, s = out.s;
   }
   if (m.rows > 0 && m.cols > 0)
-    done(api.quantize(x.data_ptr(), m.code, m.rows, m.cols, m.ld, q.data_ptr(), s.data_ptr(), stream_of(a[3], dev)),
+    done(api.quantize(x.data_ptr(), m.code, m.rows, m.cols, m.ld, q.data_ptr(), s.data_ptr(), on_stream.handle()),
          "mxfp4_quantize");
-  return Py_BuildValue("NNLL", THPVariable_Wrap(q), THPVariable_Wrap(s), (long long)m.rows, (long long)m.cols);
+  const bool given = a[1] != Py_None;
+  return Py_BuildValue("NNLL", on_stream.result(q, given), on_stream.result(s, given), (long long)m.rows,
+                       (long long)m.cols);
 }
 
 // dequantize(qdata, scales, rows, cols, dtype, out | None, stream) -> out
 PyObject* dequantize(PyObject* const* a) {
   const int64_t rows = whole(a[2]), cols = whole(a[3]);
   const c10::DeviceIndex dev = cuda_index(tensor(a[0], "t.qdata"));
-  c10::cuda::CUDAGuard guard(dev);
+  const Launch on_stream(a[6], dev);
   Out o = output(a[5], rows, cols, a[4], at::kBFloat16, dev);
   if (rows > 0 && cols > 0) {
     const Mx t = mx(a, "t");
     done(api.dequantize(t.q.data_ptr(), t.s.data_ptr(), rows, cols, o.t.data_ptr(), o.code, o.ld,
-                        stream_of(a[6], dev)),
+                        on_stream.handle()),
          "mxfp4_dequantize");
   }
-  return THPVariable_Wrap(o.t);
+  return on_stream.result(o.t, a[5] != Py_None);
 }
 
 // gemm(a: qdata, scales, rows, cols, w: qdata, scales, rows, cols, dtype, out | None, status | None, stream) -> out
@@ -243,12 +273,12 @@ PyObject* gemm(PyObject* const* a) {
   if (x.cols != w.cols) bad("activation and weight K differ");
   const c10::DeviceIndex dev = cuda_index(x.q);
   on(w.q, dev);
-  c10::cuda::CUDAGuard guard(dev);
+  const Launch on_stream(a[11], dev);
   Out o = output(a[9], x.rows, w.rows, a[8], at::kBFloat16, dev);
   done(api.gemm(x.q.data_ptr(), x.s.data_ptr(), w.q.data_ptr(), w.s.data_ptr(), x.rows, w.rows, x.cols,
-                o.t.data_ptr(), o.code, o.ld, status_of(a[10], dev), stream_of(a[11], dev)),
+                o.t.data_ptr(), o.code, o.ld, status_of(a[10], dev), on_stream.handle()),
        "mxfp4_gemm");
-  return THPVariable_Wrap(o.t);
+  return on_stream.result(o.t, a[9] != Py_None);
 }
 
 // linear(x, w: qdata, scales, rows, cols, dtype | None, out | None, status | None, stream) -> out
@@ -259,7 +289,7 @@ PyObject* linear(PyObject* const* a) {
   if (m.cols != w.cols) bad("activation and weight K differ");
   const c10::DeviceIndex dev = cuda_index(x);
   on(w.q, dev);
-  c10::cuda::CUDAGuard guard(dev);
+  const Launch on_stream(a[8], dev);
   Out o = output(a[6], m.rows, w.rows, a[5], x.scalar_type(), dev);
   if (m.rows > 0) {
     const int64_t need = api.linear_workspace_bytes(m.rows, m.cols);
@@ -267,10 +297,10 @@ PyObject* linear(PyObject* const* a) {
     if (need > 0) ws = empty({need}, at::kByte, dev);
     done(api.linear(x.data_ptr(), m.code, m.rows, m.ld, w.q.data_ptr(), w.s.data_ptr(), w.rows, m.cols,
                     o.t.data_ptr(), o.code, o.ld, need > 0 ? ws.data_ptr() : nullptr, need, status_of(a[7], dev),
-                    stream_of(a[8], dev)),
+                    on_stream.handle()),
          "mxfp4_linear");
   }
-  return THPVariable_Wrap(o.t);
+  return on_stream.result(o.t, a[6] != Py_None);
 }
 
 // cache_write(cache x 4, k, v, slots, stream)
@@ -282,9 +312,9 @@ PyObject* cache_write(PyObject* const* a) {
   const Tensor& slots = ints(a[6], at::kLong, 1, "slots", c.dev);
   if (slots.size(0) != k.size(0)) bad("slots must have an entry for each token");
   const int32_t code = code_of(k.scalar_type(), "k");
-  c10::cuda::CUDAGuard guard(c.dev);
+  const Launch on_stream(a[7], c.dev);
   done(api.cache_write(&c.c, k.data_ptr(), v.data_ptr(), code, k.size(0), k.stride(0), k.stride(1), v.stride(0),
-                       v.stride(1), static_cast<const int64_t*>(slots.data_ptr()), stream_of(a[7], c.dev)),
+                       v.stride(1), static_cast<const int64_t*>(slots.data_ptr()), on_stream.handle()),
        "mxfp4_cache_write");
   Py_RETURN_NONE;
 }
@@ -298,13 +328,13 @@ PyObject* cache_read(PyObject* const* a) {
   const int32_t code = code_of(t, "dtype");
   if (starts.size(0) != table.size(0) + 1) bad("starts must have an entry for each sequence and one more");
   if (total < 0) bad("total must not be negative");
-  c10::cuda::CUDAGuard guard(c.dev);
+  const Launch on_stream(a[8], c.dev);
   Tensor k = empty({total, c.c.kv_heads, c.c.dim}, t, c.dev), v = empty({total, c.c.kv_heads, c.c.dim}, t, c.dev);
   done(api.cache_read(&c.c, static_cast<const int32_t*>(table.data_ptr()), table.size(1), table.size(0),
                       static_cast<const int32_t*>(starts.data_ptr()), total, k.data_ptr(), v.data_ptr(), code,
-                      stream_of(a[8], c.dev)),
+                      on_stream.handle()),
        "mxfp4_cache_read");
-  return Py_BuildValue("NN", THPVariable_Wrap(k), THPVariable_Wrap(v));
+  return Py_BuildValue("NN", on_stream.result(k), on_stream.result(v));
 }
 
 // cache_attention(q, cache x 4, table, lens, q_starts | None, max_queries | None, scale | None, causal, window, sinks,
@@ -343,7 +373,7 @@ PyObject* cache_attention(PyObject* const* a) {
   }
   const int causal = PyObject_IsTrue(a[10]);
   if (causal < 0) throw Raised();
-  c10::cuda::CUDAGuard guard(c.dev);
+  const Launch on_stream(a[16], c.dev);
   Tensor out;
   if (a[13] == Py_None) {
     out = empty({total, heads, c.c.dim}, q.scalar_type(), c.dev);
@@ -377,9 +407,9 @@ PyObject* cache_attention(PyObject* const* a) {
     g.causal = causal;
     g.window = int32_t(window < 0x7FFFFFFF ? window : 0x7FFFFFFF);
     g.sinks = int32_t(sinks < 0x7FFFFFFF ? sinks : 0x7FFFFFFF);
-    done(api.cache_attention(&c.c, &g, stream_of(a[16], c.dev)), "mxfp4_cache_attention");
+    done(api.cache_attention(&c.c, &g, on_stream.handle()), "mxfp4_cache_attention");
   }
-  return THPVariable_Wrap(out);
+  return on_stream.result(out, a[13] != Py_None);
 }
 
 // Every function takes a fixed number of positional arguments, and no C++

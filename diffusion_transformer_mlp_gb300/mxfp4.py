@@ -10,10 +10,12 @@ block-scaled product, a paged KV cache held in 4 bits and attention over it.
 
 Each function forwards to the C entry point of the same name (mxfp4.h has the
 format, the layouts and the masks) through the compiled module _mxfp4, which
-checks the arguments; PyTorch provides device memory and the current stream.  Calls are asynchronous on that stream, or on ``stream``.
-Workspaces come from PyTorch's caching allocator; tensors used on another
-stream than the one they were allocated on need ``record_stream``, as any
-PyTorch tensor does.
+checks the arguments; PyTorch provides device memory and the current stream.
+Calls are asynchronous on that stream, or on ``stream``.  Workspaces and new
+outputs come from PyTorch's caching allocator and belong to the stream of the
+call; outputs are recorded on the current stream as well.  The caller orders
+the two streams, and calls ``record_stream`` for inputs that were allocated on
+another stream than the call's, as for any PyTorch tensor.
 """
 from __future__ import annotations
 

@@ -85,6 +85,19 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _new(make, dev, stream):
+    """What `make()` allocates, as memory of the stream that will write it; also
+    recorded on the current stream, where the caller uses it."""
+    if stream is None:
+        return make()
+    current = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        out = make()
+    for t in (out.qdata, out.scales, out.rec) if isinstance(out, NVFP4Tensor) else (out,):
+        t.record_stream(current)
+    return out
+
+
 def _ptr(t: torch.Tensor) -> ctypes.c_void_p:
     return ctypes.c_void_p(t.data_ptr())
 
@@ -126,7 +139,9 @@ def _bf16_matrix(x: torch.Tensor, name: str) -> torch.Tensor:
 def nvfp4_quantize_weight(w: torch.Tensor, out: NVFP4Tensor | None = None, stream=None) -> NVFP4Tensor:
     _bf16_matrix(w, "w")
     rows, cols = w.shape
-    out = _check_nvfp4(out, rows, cols, "out") if out is not None else empty_nvfp4(rows, cols, w.device)
+    if out is None:
+        out = _new(lambda: empty_nvfp4(rows, cols, w.device), w.device, stream)
+    _check_nvfp4(out, rows, cols, "out")
     dev = _check_dev(w, out.qdata, out.scales, out.rec)
     with torch.cuda.device(dev):
         _lib.check(load().nvfp4_quantize_weight(_ptr(w), rows, cols, w.stride(0), _ptr(out.qdata), _ptr(out.scales),
@@ -140,7 +155,9 @@ def swiglu_nvfp4_quantize(gate_up: torch.Tensor, out: NVFP4Tensor | None = None,
     if two_k % 2:
         raise ValueError("gate_up must have an even number of columns (gate | up)")
     k = two_k // 2
-    out = _check_nvfp4(out, m, k, "out") if out is not None else empty_nvfp4(m, k, gate_up.device)
+    if out is None:
+        out = _new(lambda: empty_nvfp4(m, k, gate_up.device), gate_up.device, stream)
+    _check_nvfp4(out, m, k, "out")
     dev = _check_dev(gate_up, out.qdata, out.scales, out.rec)
     with torch.cuda.device(dev):
         _lib.check(load().swiglu_nvfp4_quantize(_ptr(gate_up), m, k, gate_up.stride(0), _ptr(out.qdata),
@@ -157,7 +174,7 @@ def nvfp4_fc2_gemm(a: NVFP4Tensor, w: NVFP4Tensor, out: torch.Tensor | None = No
     _check_nvfp4(a, m, k, "a")
     _check_nvfp4(w, n, k, "w")
     if out is None:
-        out = torch.empty(m, n, dtype=torch.bfloat16, device=a.device)
+        out = _new(lambda: torch.empty(m, n, dtype=torch.bfloat16, device=a.device), a.device, stream)
     if out.dtype != torch.bfloat16 or out.dim() != 2 or out.shape[0] < m or out.shape[1] < n or out.stride(1) != 1:
         raise ValueError("out must be a bfloat16 [>=m, >=n] tensor with unit column stride")
     dev = _check_dev(a.qdata, a.scales, a.rec, w.qdata, w.scales, w.rec, out)
@@ -184,10 +201,12 @@ def nvfp4_fc1_swiglu(a: NVFP4Tensor, w1: NVFP4Tensor, h: torch.Tensor | None = N
     _check_nvfp4(a, m, k, "a")
     _check_nvfp4(w1, 2 * f, k, "w1")
     if h is None:
-        h = torch.empty(m, f, dtype=torch.bfloat16, device=a.device)
+        h = _new(lambda: torch.empty(m, f, dtype=torch.bfloat16, device=a.device), a.device, stream)
     if h.dtype != torch.bfloat16 or h.dim() != 2 or h.shape[0] < m or h.shape[1] < f or h.stride(1) != 1:
         raise ValueError("h must be a bfloat16 [>=m, >=f] tensor with unit column stride")
-    act = _check_nvfp4(act, m, f, "act") if act is not None else empty_nvfp4(m, f, a.device)
+    if act is None:
+        act = _new(lambda: empty_nvfp4(m, f, a.device), a.device, stream)
+    _check_nvfp4(act, m, f, "act")
     dev = _check_dev(a.qdata, a.scales, a.rec, w1.qdata, w1.scales, w1.rec, h, act.qdata, act.scales, act.rec)
     st_ptr = ctypes.c_void_p(status.data_ptr()) if status is not None else ctypes.c_void_p(0)
     with torch.cuda.device(dev):
@@ -232,9 +251,9 @@ def fc2_host(gate_up_host: torch.Tensor, w: NVFP4Tensor, workspace: dict | None 
     if ws.get("key") != key:
         ws.clear()
         ws["key"] = key
-        ws["x"] = torch.empty(m, two_k, dtype=torch.bfloat16, device=dev)
-        ws["act"] = empty_nvfp4(m, k, dev)
-        ws["out"] = torch.empty(m, n, dtype=torch.bfloat16, device=dev)
+        ws["x"] = _new(lambda: torch.empty(m, two_k, dtype=torch.bfloat16, device=dev), dev, stream)
+        ws["act"] = _new(lambda: empty_nvfp4(m, k, dev), dev, stream)
+        ws["out"] = _new(lambda: torch.empty(m, n, dtype=torch.bfloat16, device=dev), dev, stream)
     if out_host is None:
         out_host = torch.empty(m, n, dtype=torch.bfloat16, pin_memory=True)
     if (out_host.dtype != torch.bfloat16 or out_host.device.type != "cpu" or tuple(out_host.shape) != (m, n)

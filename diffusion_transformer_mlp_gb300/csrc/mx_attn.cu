@@ -82,6 +82,10 @@ extern "C" nvfp4_status mxfp4_cache_attention(const mxfp4_cache* cache, const mx
   p.pages = cache->pages;
   p.page_shift = sh, p.kv_heads = cache->kv_heads, p.group = int32_t(group), p.seqs = g.seqs, p.total_q = g.total_q;
   p.bf16 = g.dtype == MXFP4_BF16, p.causal = g.causal != 0, p.window = g.window, p.sinks = g.sinks;
+  // A window that reaches from a query (at -2^24 or later) past every key hides
+  // none; smaller ones leave the kernels' differences of positions in 32 bits.
+  const int64_t keys = g.table_ld * cache->page_size, most = (int64_t(1) << 31) - (int64_t(1) << 25);
+  if (g.window >= (keys < most ? keys : most)) p.window = p.sinks = 0;
   p.q_vec = aligned16(g.q) && g.q_st % 8 == 0 && g.q_sh % 8 == 0;
   p.o_vec = aligned16(g.out) && g.o_st % 8 == 0 && g.o_sh % 8 == 0;
   p.scale_log2 = g.scale * 1.4426950408889634f;

@@ -151,7 +151,8 @@ nvfp4_status mxfp4_cache_read(const mxfp4_cache* cache, const int32_t* table, in
  *           (natural logarithm of the sum of exponentials)
  *   q_starts device int32 [seqs + 1] or NULL: one query a sequence
  *   max_queries  an upper bound of n_b known to the host (1 for NULL);
- *           max_queries * q_heads / kv_heads <= 2^24, table_ld * page_size <= 2^31
+ *           max_queries * q_heads / kv_heads <= 2^24, table_ld * page_size <= 2^31,
+ *           lens[b] <= table_ld * page_size and < 2^31 - 2^25
  *   workspace    16-byte aligned, mxfp4_attention_workspace_bytes() bytes */
 typedef struct {
   const void* q;

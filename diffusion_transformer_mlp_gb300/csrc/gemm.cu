@@ -444,6 +444,7 @@ __device__ __forceinline__ void mx_store_fp32(const Params& p, uint32_t taddr, u
 #pragma unroll 1
   for (int c = 0; c < 128; c += 32) {
     uint32_t r[32];
+    __syncwarp();  // the load is by the whole warp, of which lanes past n have stored nothing
     tmem_ld_32x32b_x32(taddr + c, r);
     tc_wait_ld();
     tmem_ld_fence_regs<32>(r);
@@ -459,11 +460,11 @@ __device__ __forceinline__ void mx_store_fp32(const Params& p, uint32_t taddr, u
       float v[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = reinterpret_cast<const float*>(slot)[(2 * i + r0) * 16 + col];
-      if (x + col >= p.n) continue;
+      const bool in = x + col < p.n;
       float* dst = out + int64_t(y + r0) * p.ldo + x + col;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        if (y + r0 + 2 * i < p.m) *dst = v[i];
+        if (in && y + r0 + 2 * i < p.m) *dst = v[i];
         dst += 2 * p.ldo;
       }
     }

@@ -476,6 +476,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
               alpha *= exp2_approx(m - ref);
               m = ref;
             }
+            __syncwarp();
             raised = true;
             return false;
           }
@@ -546,6 +547,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t v[32];
+        __syncwarp();  // rows with and without NaN
         tmem_load32(t_o + c, v);
         if (c + 32 == D) {
           tc_fence_before();

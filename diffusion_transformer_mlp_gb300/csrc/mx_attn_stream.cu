@@ -630,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows, kSeveral>::kCtas)
           }
         }
       }
+      __syncwarp();  // the MMAs are by the whole warp
     }
 
     // output

@@ -365,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int c = 0; c < NT; c += 16) {
       if (c >= valid) break;
       uint32_t r[16];
+      __syncwarp();  // lanes past n have stored nothing
       tmem_ld_32x32b_x16(tmem + (uint32_t(q * 32) << 16) + c, r);
       tc_wait_ld();
       tmem_ld_fence_regs<16>(r);

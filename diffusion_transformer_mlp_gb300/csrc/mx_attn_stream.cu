@@ -601,7 +601,8 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows, kSeveral>::kCtas)
       }
     }
 
-    // a block of NaN reaches the rows that see its key, and only those
+    // a block of NaN reaches the rows that see its key, whatever its weight (0 times
+    // NaN), and only those
     if (nan_scale) {
 #pragma unroll
       for (int j = 0; j < C; ++j) {
@@ -611,12 +612,10 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows, kSeveral>::kCtas)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const bool bad = (nan_keys[nt / 4][j] >> ((nt % 4) * 8 + 2 * tig + e)) & 1u;
-            if constexpr (kRows == 8) {
-              hit[0] = hit[0] || (bad && pw[nt][e] != 0);
-            } else {
+            const int32_t key = tok0 + token_of<D>(nt * 8 + 2 * tig + e);
 #pragma unroll
-              for (int r = 0; r < R; ++r) hit[r] = hit[r] || (bad && (pw[nt][r] & (e ? 0xFFFF0000u : 0xFFFFu)) != 0);
-            }
+            for (int r = 0; r < R; ++r)
+              hit[r] = hit[r] || (bad && key < end[r] && (key >= from[r] || key < a.sinks));
           }
 #pragma unroll
         for (int r = 0; r < R; ++r) {

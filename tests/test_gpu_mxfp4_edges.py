@@ -22,3 +22,19 @@ def test_windows_past_every_key_hide_none(window, causal):
             case.check()
             case.mask["window"] = 0
             assert torch.equal(case.run(), out)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_nan_value_of_a_key_without_weight(dim):
+    """0 times NaN: a key that a row sees, however small its weight."""
+    for nq, hq in ((1, 4), (1, 16), (2, 8), (70, 2)):
+        case = Case([100], [nq], hq, 1, dim, seed=nq)
+        case.k[:] = 1.0
+        case.q[:] = 3.0
+        case.k[10] = -60.0   # scores of 3 * dim ** 0.5 and of -180 * dim ** 0.5
+        case.v[10, 0, 40] = math.nan
+        case.write()
+        out = case.run()
+        want = torch.zeros_like(out, dtype=torch.bool)
+        want[..., 32:64] = True
+        assert torch.equal(torch.isnan(out), want), (nq, hq)

@@ -158,11 +158,11 @@ __device__ __forceinline__ void load_q8(const AttnParams& a, const uint16_t* src
   }
 }
 // Scale word of a block in the high exponent bits: 2^(E-127) for 1 <= E <= 254,
-// 0 for E = 0 (a block below 2^-124 has no weight in a score), infinity for
-// 255, whose zero codes then give NaN.
+// 0 for E = 0 (a block below 2^-124 has no weight in a score), NaN for 255, where
+// the exponent and 1 carry into the sign bit.
 __device__ __forceinline__ float e8m0_byte(uint32_t w, int i) {
-  const uint32_t v = i == 0 ? w << 23 : (i == 1 ? w << 15 : (i == 2 ? w << 7 : w >> 1));
-  return __uint_as_float(v & 0x7F800000u);
+  const uint32_t v = (i == 0 ? w << 23 : (i == 1 ? w << 15 : (i == 2 ? w << 7 : w >> 1))) & 0x7F800000u;
+  return __uint_as_float(v | (v + 0x00800000u) >> 31);
 }
 
 // Keys that only some rows see, after a warp's run.  Not inlined: the loops of the

@@ -38,3 +38,18 @@ def test_nan_value_of_a_key_without_weight(dim):
         want = torch.zeros_like(out, dtype=torch.bool)
         want[..., 32:64] = True
         assert torch.equal(torch.isnan(out), want), (nq, hq)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_nan_scale_with_codes(dim):
+    """E = 255 is NaN whatever the codes beside it are, in a key too."""
+    for nq, hq in ((1, 4), (1, 16), (70, 2)):
+        for code in (0x22, 0xAA):  # 1 and -1 throughout
+            case = Case([100], [nq], hq, 1, dim, seed=nq)
+            case.q[:] = 1.0
+            case.write()
+            slot = case.slots(0)[10]
+            case.cache.k_codes[slot // 16, 0, slot % 16] = code
+            case.cache.k_scales[slot // 16, 0, slot % 16, 1] = 255
+            assert bool(torch.isnan(case.run()).all()), (nq, hq, code)
+            assert bool(torch.isnan(case.lse).all())

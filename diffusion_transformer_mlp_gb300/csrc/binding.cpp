@@ -196,6 +196,7 @@ Cache cache(PyObject* const* a) {
   for (int i = 0; i < 4; ++i)
     if (v.size(i) != k.size(i) || ks.size(i) != (i < 3 ? k.size(i) : k.size(3) / 16) || vs.size(i) != ks.size(i))
       bad("the cache's codes and scales do not fit together");
+  if (k.numel() == 0) bad("the cache must have pages, kv_heads, a page_size and a dim");
   const c10::DeviceIndex dev = cuda_index(k);
   for (const Tensor* t : {&k, &ks, &v, &vs}) {
     if (t->scalar_type() != at::kByte || !t->is_contiguous())

@@ -6,6 +6,7 @@
 // 9-21 us on the GPU's host.  PyTorch still provides device memory and
 // streams only; the C functions come by address from the loaded library
 // (bind), so this module links against no kernel.
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
@@ -127,6 +128,14 @@ uint32_t* status_of(PyObject* o, c10::DeviceIndex dev) {
   on(t, dev);
   if (t.element_size() < 4 || t.numel() < 1) bad("status must hold 32 bits");
   return static_cast<uint32_t*>(t.data_ptr());
+}
+
+// The operators have no backward pass: a result that looked differentiable would
+// cut the graph silently.  (Codes and scales are whole numbers, which have none.)
+void no_graph(const Tensor& t, const char* name) {
+  if (t.requires_grad() && at::GradMode::is_enabled())
+    bad(std::string(name) + " requires a gradient, which this operator does not have: detach it, or call under "
+        "torch.no_grad()");
 }
 
 struct Mat {
@@ -286,6 +295,7 @@ PyObject* gemm(PyObject* const* a) {
 PyObject* linear(PyObject* const* a) {
   const Tensor& x = tensor(a[0], "x");
   const Mat m = matrix(x, "x");
+  no_graph(x, "x");
   const Mx w = mx(a + 1, "w");
   if (m.cols != w.cols) bad("activation and weight K differ");
   const c10::DeviceIndex dev = cuda_index(x);
@@ -346,6 +356,7 @@ PyObject* cache_attention(PyObject* const* a) {
   if (q.dim() != 3 || q.size(2) != c.c.dim || q.size(1) == 0 || q.size(1) % c.c.kv_heads != 0)
     bad("q must be [total, multiple of " + std::to_string(c.c.kv_heads) + ", " + std::to_string(c.c.dim) + "]");
   if (q.stride(2) != 1) bad("q must have unit stride along its last dimension");
+  no_graph(q, "q");
   on(q, c.dev);
   const Tensor &table = ints(a[5], at::kInt, 2, "table", c.dev), &lens = ints(a[6], at::kInt, 1, "lens", c.dev);
   const int64_t seqs = lens.size(0), total = q.size(0), heads = q.size(1);

@@ -15,7 +15,8 @@ Calls are asynchronous on that stream, or on ``stream``.  Workspaces and new
 outputs come from PyTorch's caching allocator and belong to the stream of the
 call; outputs are recorded on the current stream as well.  The caller orders
 the two streams, and calls ``record_stream`` for inputs that were allocated on
-another stream than the call's, as for any PyTorch tensor.
+another stream than the call's, as for any PyTorch tensor.  There is no backward
+pass: mxfp4_linear and mxfp4_cache_attention refuse inputs that require one.
 """
 from __future__ import annotations
 

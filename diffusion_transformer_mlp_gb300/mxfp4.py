@@ -150,7 +150,7 @@ def mxfp4_linear(x: torch.Tensor, w: MXFP4Tensor, out: torch.Tensor | None = Non
 
 def mxfp4_cache_write(cache: MXFP4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
     """Quantises k and v [tokens, kv_heads, dim] into slots [tokens] (int64,
-    page * page_size + offset; negative slots are skipped)."""
+    page * page_size + offset; negative slots are skipped, the others have to differ)."""
     _ext.cache_write(cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales, k, v, slots, stream)
 
 

@@ -119,7 +119,8 @@ typedef struct {
  *   k, v   [tokens, kv_heads, dim] of `dtype`, unit stride along dim, strides
  *          in elements along tokens (k_st, v_st) and heads (k_sh, v_sh)
  *   slots  device int64 [tokens]: page * page_size + offset; a slot below 0
- *          or past the cache is skipped; of equal slots an unspecified one stays
+ *          or past the cache is skipped.  The others have to differ: tokens of
+ *          one slot leave a mixture of their codes and scales there
  * tokens may be 0. */
 nvfp4_status mxfp4_cache_write(const mxfp4_cache* cache, const void* k, const void* v, int32_t dtype, int64_t tokens,
                                int64_t k_st, int64_t k_sh, int64_t v_st, int64_t v_sh, const int64_t* slots,

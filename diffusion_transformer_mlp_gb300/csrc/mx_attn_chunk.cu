@@ -59,9 +59,9 @@ constexpr int kTK = 64;        // keys of a tile
 constexpr int kHeadroom = 8;   // value scales may exceed their reference by 2^8 before it is raised
 constexpr int kLiftK = 13, kLiftV = 5;  // largest elements: 6 * 2^13
 // Where rows see different keys (see too_wide): keys down to 2^-36 of the tile's
-// largest are exact, and values down to 2^-28 of their reference, which leaves
-// 2^-12 of the largest that a row sees.
-constexpr int kSpreadK = 23 + kLiftK, kSpreadV = 16;
+// largest are exact, and values down to 2^-28 of their reference, which is up to
+// 2^8 above the largest that a row sees.
+constexpr int kSpreadK = 23 + kLiftK, kSpreadV = 8;
 
 template <int D>
 struct Chunk {

@@ -410,8 +410,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// Clusters of c CTAs of `kernel` that are resident at once (asked once for
-// each kernel and c: the devices of one process are of one kind here).
+// Clusters of c CTAs of `kernel` that are resident at once on the current device.
 template <class K>
 nvfp4_status resident_clusters(K kernel, int smem, int c, int32_t* most) {
   cudaLaunchConfig_t cfg = {};
@@ -447,19 +446,23 @@ nvfp4_status rows_launch(const void* a_q, const void* w_q, int64_t m, int64_t n,
   static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
   st = allow_smem(reinterpret_cast<const void*>(kernel), S::kSmem, ready);
   if (st != NVFP4_OK) return st;
-  // The largest split whose clusters run all at once and that leaves every CTA
-  // a k-tile: a CTA alone draws about 33 GB/s of its SM's share, and a second
-  // wave costs a whole pass.  1 x 5376 x 14336 (42 tiles): split 1 to 8 take
-  // 23.0, 13.8, 10.9, 11.0, 11.0, 11.0, 14.6 and 14.0 us; 7 and 8 do not fit.
-  static std::atomic<int32_t> fit[kMaxSplit] = {};
+  // The largest split that leaves every CTA a k-tile and whose clusters run all at
+  // once by the runtime's count, which is of one CTA an SM: 46, 36, 28, 23 and 15
+  // clusters of 3, 4, 5, 6 and 7.  (Two CTAs fit, but more than one draw little
+  // more; what costs is a second wave.)  1 x 5376 x 14336 (42 tiles, split 3):
+  // split 1 to 8 take 23.2, 13.9, 10.9, 10.8, 11.1, 10.7, 14.6 and 13.9 us.
+  // 61 x 21504 x 5376 (168 tiles, split 1): 15.6, 23.2, 21.3, 25.6, 26.1 us.
+  static std::atomic<int32_t> fit[64][kMaxSplit] = {};  // asked once for each device
+  int dev = 0;
+  if ((st = cuda_check(cudaGetDevice(&dev), "cudaGetDevice")) != NVFP4_OK) return st;
   int64_t split = 1;
   for (int c = std::min(tiles, kMaxSplit); c > 1; --c) {
     if (w_tiles * a_tiles * c > 2 * int64_t(sm_count())) continue;
-    int32_t most = fit[c - 1].load(std::memory_order_relaxed);
+    int32_t most = dev < 64 ? fit[dev][c - 1].load(std::memory_order_relaxed) : 0;
     if (most == 0) {
       st = resident_clusters(kernel, S::kSmem, c, &most);
       if (st != NVFP4_OK) return st;
-      fit[c - 1].store(most, std::memory_order_relaxed);
+      if (dev < 64) fit[dev][c - 1].store(most, std::memory_order_relaxed);
     }
     if (w_tiles * a_tiles <= most) {
       split = c;

@@ -23,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 GEN = os.path.join(BUILD, "gen")
 LIB = os.path.join(BUILD, "libnvfp4fc2.so")
+BINDING = os.path.join(BUILD, "_mxfp4.so")
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "mma_peak.cu", "tc_read.cu", "noalloc.cu",
            "mx_quant.cu", "mx_cache.cu", "mx_rows.cu", "mx_linear.cu", "mx_attn.cu", "mx_attn_stream.cu",
            "mx_attn_chunk.cu", "mx_attn_combine.cu"]
@@ -39,20 +40,34 @@ def nvcc() -> str:
 
 
 def _binding_job():
-    """(target, command) of the Python module."""
+    """Command that makes the Python module."""
     import sysconfig
 
     import torch
     t = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    out = os.path.join(BUILD, "_mxfp4.so")
     inc = [INCLUDE, os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + [a for i in inc for a in ("-I", i)]
-           + [os.path.join(CSRC, "binding.cpp"), "-o", out + f".tmp{os.getpid()}", "-L", os.path.join(t, "lib"),
+           + [os.path.join(CSRC, "binding.cpp"), "-o", BINDING + f".tmp{os.getpid()}", "-L", os.path.join(t, "lib"),
               "-lc10", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-lc10_cuda"])
-    return out, cmd
+    return cmd
+
+
+def _torch_stamp() -> str:
+    import torch
+    return f"{torch.__version__} {sys.implementation.cache_tag}"
+
+
+def binding_is_current() -> bool:
+    """The Python module exists and was compiled against this PyTorch and Python,
+    whose binary interfaces it uses."""
+    try:
+        with open(BINDING + ".torch") as f:
+            return os.path.exists(BINDING) and f.read() == _torch_stamp()
+    except OSError:
+        return False
 
 
 def _newer(target: str, deps: list[str]) -> bool:
@@ -76,10 +91,9 @@ def build(verbose: bool = False, force: bool = False) -> str:
         subprocess.check_call([sys.executable, gen, table])
     deps = _headers() + [table]
     objs, jobs = [], []
-    ext = os.path.join(BUILD, "_mxfp4.so")
-    binding = force or _newer(ext, [os.path.join(CSRC, "binding.cpp")] + deps)
+    binding = force or not binding_is_current() or _newer(BINDING, [os.path.join(CSRC, "binding.cpp")] + deps)
     if binding:
-        jobs.append(("binding.cpp", _binding_job()[1]))
+        jobs.append(("binding.cpp", _binding_job()))
     for src in SOURCES:
         s = os.path.join(CSRC, src)
         o = os.path.join(BUILD, src.replace(".cu", ".o"))
@@ -103,7 +117,9 @@ def build(verbose: bool = False, force: bool = False) -> str:
             if verbose:
                 print(log)
     if binding:
-        os.replace(ext + f".tmp{os.getpid()}", ext)
+        os.replace(BINDING + f".tmp{os.getpid()}", BINDING)
+        with open(BINDING + ".torch", "w") as f:
+            f.write(_torch_stamp())
     if force or jobs or not os.path.exists(LIB):
         tmp = LIB + f".tmp{os.getpid()}"
         subprocess.check_call([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs)

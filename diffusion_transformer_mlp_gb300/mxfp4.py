@@ -22,13 +22,12 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
-import os
 import threading
 from dataclasses import dataclass
 
 import torch
 
-from . import _lib
+from . import _lib, build
 
 __all__ = ["MXFP4Tensor", "MXFP4Cache", "empty_mxfp4", "empty_mxfp4_cache", "mxfp4_padded_cols", "mxfp4_scale_bytes",
            "mxfp4_scale_offset", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm", "mxfp4_linear",
@@ -48,11 +47,9 @@ class _Unloaded:
         with _lock:
             if isinstance(_ext, _Unloaded):
                 L = _lib.load()
-                path = os.path.join(os.path.dirname(_lib.LIB_PATH), "_mxfp4.so")
-                if not os.path.exists(path):
-                    from . import build
+                if not build.binding_is_current():
                     build.build()
-                spec = importlib.util.spec_from_file_location("_mxfp4", path)
+                spec = importlib.util.spec_from_file_location("_mxfp4", build.BINDING)
                 module = importlib.util.module_from_spec(spec)
                 spec.loader.exec_module(module)
                 module.bind(_lib.check, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in _FUNCTIONS))

@@ -19,13 +19,15 @@ namespace {
 // Which kernel takes the rows (queries x heads of the group) of a sequence's kv
 // head: k_attn_chunk works on 256 of them (dim 256: 128) at once, k_attn_stream
 // on 8 or 16, each time decoding the keys anew.  32 sequences of 8,000 keys, 8
-// kv heads, stream / chunk in us:
-//   rows        16         48         64        128
-//   dim  64   63 / 284  159 / 284  205 / 279  396 / 287
-//   dim 128   96 / 309  242 / 310  313 / 309  610 / 292
-//   dim 256  340 / 308  909 / 365 1175 / 362
-// (dim 256, 8 rows: 205 / 308).  One sequence of 16,000 keys, dim 128: 26 / 43,
-// 30 / 43, 38 / 43, 56 / 41.
+// kv heads, one query, stream / chunk in us:
+//   rows         8         16         48         64        128
+//   dim  64   51 / 283   62 / 283  155 / 268  200 / 265  385 / 250
+//   dim 128   83 / 333   96 / 333  247 / 321  319 / 315  619 / 315
+//   dim 256  184 / 338  345 / 339  931 / 396 1193 / 393 2371 / 317
+// One sequence of 16,000 keys, dim 128: 16 rows 25 / 44, 64 rows 35 / 45, 128 rows
+// 53 / 44.  At 16 rows of dim 256 the two differ by 5% at most from 2,000 keys on
+// (16 sequences of 4,000: 117 / 115; 4 queries of 4 heads: 121 / 116), and short
+// sequences are the stream kernel's (8 of 500 keys: 27 / 35; 64 of 300: 71 / 91).
 bool many_rows(int32_t dim, int64_t rows) { return rows > (dim == 256 ? 16 : 64); }
 }  // namespace
 

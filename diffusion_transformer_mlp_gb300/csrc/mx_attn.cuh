@@ -60,11 +60,6 @@ __device__ __forceinline__ Span span_of(const AttnParams& p, int32_t len, int32_
   return s;
 }
 
-// Whether the query at position pos sees key j (j < len is the caller's).
-__device__ __forceinline__ bool sees(const AttnParams& p, int32_t pos, int32_t j) {
-  return (!p.causal || j <= pos) && (p.window <= 0 || j > pos - p.window || j < p.sinks);
-}
-
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

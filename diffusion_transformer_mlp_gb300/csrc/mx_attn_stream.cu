@@ -780,7 +780,7 @@ nvfp4_status launch_of(int rows, const CUtensorMap& tk, const CUtensorMap& tv, c
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 // Rows of partials: two a worker, the most of any variant (16 rows of 2 blocks
-// an SM, 8 rows of 4).
+// an SM; 8 rows of 3 have fewer).
 int64_t partial_rows() { return 2 * int64_t(sm_count()) * kWarps * 32; }
 
 }  // namespace

@@ -339,6 +339,7 @@ PyObject* cache_read(PyObject* const* a) {
   const int32_t code = code_of(t, "dtype");
   if (starts.size(0) != table.size(0) + 1) bad("starts must have an entry for each sequence and one more");
   if (total < 0) bad("total must not be negative");
+  if (total > 0 && table.size(0) == 0) bad("total must be 0 without sequences");
   const Launch on_stream(a[8], c.dev);
   Tensor k = empty({total, c.c.kv_heads, c.c.dim}, t, c.dev), v = empty({total, c.c.kv_heads, c.c.dim}, t, c.dev);
   done(api.cache_read(&c.c, static_cast<const int32_t*>(table.data_ptr()), table.size(1), table.size(0),
@@ -375,6 +376,7 @@ PyObject* cache_attention(PyObject* const* a) {
   }
   const int64_t window = whole(a[11]), sinks = whole(a[12]);
   if (most < 0 || window < 0 || sinks < 0) bad("max_queries, window and sinks must not be negative");
+  if (total > 0 && (seqs == 0 || most == 0)) bad("q has rows, but lens or max_queries leave no query");
   if (total > 0x7FFFFFFF || seqs > 0x7FFFFFFF || heads > 0x7FFFFFFF) bad("q is too large");
   if (a[9] == Py_None) {
     g.scale = float(1.0 / std::sqrt(double(c.c.dim)));
@@ -394,6 +396,7 @@ PyObject* cache_attention(PyObject* const* a) {
     if (out.dim() != 3 || out.size(0) != total || out.size(1) != heads || out.size(2) != c.c.dim ||
         out.scalar_type() != q.scalar_type() || out.stride(2) != 1)
       bad("out must have q's shape and type and unit stride along its last dimension");
+    if ((total > 1 && out.stride(0) == 0) || (heads > 1 && out.stride(1) == 0)) bad("out must not overlap itself");
     on(out, c.dev);
   }
   if (a[14] != Py_None) {

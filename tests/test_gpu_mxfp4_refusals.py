@@ -39,3 +39,26 @@ def test_gradients():
         fc2.mxfp4_cache_attention(q, cache, table, lens)
     with torch.inference_mode():
         fc2.mxfp4_cache_attention(q, cache, table, lens)
+
+
+def test_rows_that_nothing_would_fill():
+    """Outputs that no sequence or query writes, or that rows share."""
+    cache = fc2.empty_mxfp4_cache(1, 16, 1, 64)
+    for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales):
+        t.zero_()
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    table, lens = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), i32(1)
+    q = torch.randn(2, 2, 64, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="no query"):
+        fc2.mxfp4_cache_attention(q, cache, table[:0], lens[:0], i32(0), 2)
+    with pytest.raises(ValueError, match="no query"):
+        fc2.mxfp4_cache_attention(q, cache, table, lens, i32(0, 2), 0)
+    for out in (q[:1].expand(2, 2, 64), q[:, :1].expand(2, 2, 64)):
+        with pytest.raises(ValueError, match="overlap"):
+            fc2.mxfp4_cache_attention(q, cache, table, lens, i32(0, 2), 2, out=out)
+    with pytest.raises(ValueError, match="without sequences"):
+        fc2.mxfp4_cache_read(cache, table[:0], i32(0), 3)
+    # nothing to do is no error
+    assert fc2.mxfp4_cache_attention(q[:0], cache, table[:0], lens[:0]).shape == (0, 2, 64)
+    assert fc2.mxfp4_cache_attention(q[:0], cache, table, lens, i32(0, 0), 0).shape == (0, 2, 64)
+    assert fc2.mxfp4_cache_read(cache, table[:0], i32(0), 0)[0].shape == (0, 1, 64)

@@ -99,8 +99,13 @@ struct SplitParams {
   struct Cursor* start;  // [workers] first tiles of the runs, written by k_attn_chunk for k_attn_join
 };
 
+// First query row of sequence b, and the number of its queries: none outside of
+// the rows that there are, whatever q_starts holds.
+__device__ __forceinline__ int32_t seq_start(const AttnParams& a, int32_t b) {
+  return a.q_starts != nullptr ? min(max(a.q_starts[b], 0), a.total_q) : b;
+}
 __device__ __forceinline__ int32_t seq_queries(const AttnParams& a, int32_t b) {
-  return a.q_starts != nullptr ? a.q_starts[b + 1] - a.q_starts[b] : 1;
+  return a.q_starts != nullptr ? max(min(a.q_starts[b + 1], a.total_q) - seq_start(a, b), 0) : 1;
 }
 
 // Span of row tile rt (rows [rt * rows, ...) of the nq * group rows).
@@ -136,7 +141,7 @@ struct Cursor {
 __device__ __forceinline__ void cursor_seq(Cursor& c, const AttnParams& a) {
   c.len = a.lens[c.b];
   c.nq = seq_queries(a, c.b);
-  c.q0 = a.q_starts != nullptr ? a.q_starts[c.b] : c.b;
+  c.q0 = seq_start(a, c.b);
 }
 
 // The first tile at place x or behind it, by a whole warp: 32 row tiles at a

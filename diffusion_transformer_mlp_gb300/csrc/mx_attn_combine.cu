@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_c
   const int32_t h = blockIdx.x / (D / kCols), col0 = int32_t(blockIdx.x % (D / kCols)) * kCols;
   const int32_t rt = blockIdx.y, b = blockIdx.z;
   const int32_t len = a.lens[b], nq = seq_queries(a, b);
-  const int32_t q0 = a.q_starts != nullptr ? a.q_starts[b] : b;
+  const int32_t q0 = seq_start(a, b);
   const int32_t live = min(kRows, nq * a.group - rt * kRows);
   if (live <= 0) return;
   int64_t first = sp.prefix[b];

@@ -157,7 +157,8 @@ nvfp4_status mxfp4_cache_read(const mxfp4_cache* cache, const int32_t* table, in
  *           q_sh in elements (unit along dim)
  *   out     as q, strides o_st, o_sh;  lse  float32 [total_q, q_heads] or NULL
  *           (natural logarithm of the sum of exponentials)
- *   q_starts device int32 [seqs + 1] or NULL: one query a sequence
+ *   q_starts device int32 [seqs + 1], not decreasing, or NULL: one query a
+ *           sequence; what lies outside 0 .. total_q counts as its ends
  *   max_queries  an upper bound of n_b known to the host (1 for NULL);
  *           max_queries * q_heads / kv_heads <= 2^24, table_ld * page_size <= 2^31,
  *           lens[b] <= table_ld * page_size and < 2^31 - 2^25

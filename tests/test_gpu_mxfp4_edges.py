@@ -53,3 +53,29 @@ def test_nan_scale_with_codes(dim):
             case.cache.k_scales[slot // 16, 0, slot % 16, 1] = 255
             assert bool(torch.isnan(case.run()).all()), (nq, hq, code)
             assert bool(torch.isnan(case.lse).all())
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_query_rows_past_the_tensor(dim):
+    """Starts that lie outside of the query's rows read and write none there."""
+    for n, hq in ((5, 2), (60, 4)):
+        case = Case([300, 90], [n, n], hq, 1, dim, seed=n)
+        case.write()
+        want = case.run().clone()
+        rows = 2 * n
+        lens = torch.tensor(case.lens, dtype=torch.int32, device="cuda")
+        buf = torch.full((rows + 40, hq, dim), 3.0, dtype=case.q.dtype, device="cuda")
+        for starts in ((0, n, rows + 30), (0, n, 2 ** 31 - 1), (-7, n, rows), (-2 ** 31, n, 2 ** 30)):
+            buf.fill_(3.0)
+            fc2.mxfp4_cache_attention(case.q, case.cache, case.table, lens,
+                                      torch.tensor(starts, dtype=torch.int32, device="cuda"), n, out=buf[20:20 + rows])
+            assert torch.equal(buf[20:20 + rows], want)
+            assert bool((buf[:20] == 3).all()) and bool((buf[20 + rows:] == 3).all())
+        # a second sequence that ends in front of its start has none
+        outs = []
+        for starts in ((0, n, 0), (0, n, n)):
+            buf.fill_(3.0)
+            fc2.mxfp4_cache_attention(case.q, case.cache, case.table, lens,
+                                      torch.tensor(starts, dtype=torch.int32, device="cuda"), n, out=buf[20:20 + rows])
+            outs.append(buf.clone())
+        assert torch.equal(outs[0], outs[1]) and bool((buf[20 + n:] == 3).all())

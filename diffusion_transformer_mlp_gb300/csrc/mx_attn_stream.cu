@@ -713,6 +713,11 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows, kSeveral>::kCtas)
       if (lane == 0) ok = mbar_wait_bounded(&full[slot], phase, a.wait_limit_cycles, nullptr);
       if (__shfl_sync(0xFFFFFFFFu, ok, 0) == 0) {
         if (lane == 0 && a.dev_status != nullptr) atomicExch(a.dev_status, static_cast<uint32_t>(NVFP4_ETIMEOUT));
+        // the warp's later copies may still land in the block's shared memory
+        for (++n; n < issued; ++n) {
+          if (++slot == T::kStages) slot = 0, phase ^= 1u;
+          mbar_wait_bounded(&full[slot], phase, a.wait_limit_cycles, nullptr);
+        }
         return;
       }
     }

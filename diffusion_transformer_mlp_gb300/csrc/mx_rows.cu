@@ -237,6 +237,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int kt = kt0; kt < kt1; ++kt) {
       if (!mbar_wait_bounded(&empty[slot], phase ^ 1u, p.wait_limit_cycles, const_cast<const int*>(abort_flag))) {
         *abort_flag = 1;
+        // the copies under way: the phase of each stage that was filled last
+        for (int i = 0; i < min(kt - kt0, S::kStages); ++i) {
+          if (--slot < 0) slot = S::kStages - 1, phase ^= 1u;
+          mbar_wait_bounded(&full[slot], phase, p.wait_limit_cycles, nullptr);
+        }
         break;
       }
       uint8_t* st = ring + slot * S::kStage;

@@ -27,8 +27,8 @@
 // tiles, this 3,400; the MMAs alone 2,050).
 //
 // What bounds it: the issue slots and latencies of the softmax and decoding
-// warps (58% of the slots used, tensor pipe 51%).  Two prompts' chunks of 2,048
-// queries on 4,099 and 8,192 keys, 32 / 8 heads, dim 128: 270 us, 1.1 PFLOP/s.
+// warps (57% of the slots used, tensor pipe 50%).  Two prompts' chunks of 2,048
+// queries on 4,099 and 8,192 keys, 32 / 8 heads, dim 128: 277 us, 1.1 PFLOP/s.
 // Five kinds of warps run at once, so the loops are kept short enough for the
 // instruction caches (fully unrolled: 430 us).
 //
@@ -59,9 +59,11 @@ constexpr int kTK = 64;        // keys of a tile
 constexpr int kHeadroom = 8;   // value scales may exceed their reference by 2^8 before it is raised
 constexpr int kLiftK = 13, kLiftV = 5;  // largest elements: 6 * 2^13
 // Where rows see different keys (see too_wide): keys down to 2^-36 of the tile's
-// largest are exact, and values down to 2^-28 of their reference, which is up to
-// 2^8 above the largest that a row sees.
-constexpr int kSpreadK = 23 + kLiftK, kSpreadV = 8;
+// largest are exact, and values down to 2^-28 of their reference, which may be 2^16
+// above the largest that a row sees: a row keeps those down to 2^-12 of its own,
+// and the first rows of a prompt, whose first token often has values 2^6 to 2^10
+// below the others', need no second pass.
+constexpr int kSpreadK = 23 + kLiftK, kSpreadV = 16;
 
 template <int D>
 struct Chunk {

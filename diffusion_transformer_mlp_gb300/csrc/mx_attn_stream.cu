@@ -39,11 +39,13 @@
 //
 // Work is dealt over all warps of the grid as SplitParams describes.
 //
-// What bounds it: the decoding and scaling instructions of three warps a
-// scheduler (45% of the issue slots, ALU and MMA pipes 33% each).  32
-// conversations of 257 to 32,767 keys, 8 rows of 8 heads, dim 128 (246 MB): 82
-// us, 3.0 TB/s; with the join 92 us.  Three blocks an SM at 168 registers are 5
-// to 17% faster than two at 231, although a few registers spill.
+// What bounds it: latency.  Three warps a scheduler issue in 48% of the cycles, no
+// pipe is above 37% and DRAM at 42%; each works through the chain ldmatrix, cvt,
+// MMA, FMA, ex2, cvt, MMA of 32 keys at a time, and more warps do not fit beside Q,
+// the scores and the output in registers.  32 conversations of 257 to 32,767 keys,
+// 8 rows of 8 heads, dim 128 (246 MB): 73 us, 3.4 TB/s; with the join 83 us.  Three
+// blocks an SM at 168 registers are 5 to 17% faster than two at 231, although a few
+// registers spill.
 #include <algorithm>
 #include <atomic>
 #include <string>

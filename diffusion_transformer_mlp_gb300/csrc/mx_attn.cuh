@@ -415,20 +415,23 @@ __device__ __forceinline__ bool too_wide(const AttnParams& a, const Cursor& c, i
 }
 
 // One row (of the segment at c) over n tiles of `tok` keys from tile c.t on, by a
-// whole warp: a lane is a key for the scores, column 32 c + lane for the outputs.
-// Slow (about 60 instructions a key; 16 sequences of 4,000 keys, 4 queries of 32
-// heads: 3.1 ms instead of 38 us; 2 x 512 queries on 4,096 keys: 28 ms instead of
-// 78 us), and rarely called.  part_o is null for a
-// row of the output, else column d of its partial lies at (d / 4) * part_step + d % 4.
+// whole warp: a lane is a key for the scores and has D / 32 columns of the output.
+// part_o is null for a row of the output, else column d of its partial lies at
+// (d / 4) * part_step + d % 4.  Rarely called, and slow: where a last token 2^30
+// times as large sends all rows here, 16 sequences of 4,000 keys with 4 queries of
+// 32 heads take 1.1 ms instead of 39 us, 2 x 512 queries on 4,096 keys 10.7 ms
+// instead of 78 us (with a load at a time 3.1 and 28 ms).
 template <int D>
 __device__ __forceinline__ void wide_row(const AttnParams& a, const Cursor& cu, int32_t n, int32_t tok, int32_t row,
                                          float* part_o, int64_t part_step, float2* part_ml) {
   constexpr int C = D / 32;
+  constexpr int kAtOnce = 8;  // keys of p v whose loads are under way
   const int lane = threadIdx.x & 31;
   const int32_t qi = row / a.group, hq = cu.h * a.group + row - qi * a.group, pos = cu.len - cu.nq + qi;
   const int32_t end = a.causal ? min(cu.len, pos + 1) : cu.len, from = a.window > 0 ? pos - a.window + 1 : 0;
   const uint16_t* q = static_cast<const uint16_t*>(a.q) + int64_t(cu.q0 + qi) * a.q_st + int64_t(hq) * a.q_sh;
-  float qv[C], o[C];
+  float qv[C];  // element 32 c + lane
+  float o[C];   // column C lane + c
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const uint32_t x = q[32 * c + lane];
@@ -443,16 +446,23 @@ __device__ __forceinline__ void wide_row(const AttnParams& a, const Cursor& cu, 
     const bool seen = j < end && (j >= from || j < a.sinks);
     const uint32_t any = __ballot_sync(0xFFFFFFFFu, seen);
     if (any == 0) continue;
-    int64_t at = 0;  // row of the key in the cache
-    if (seen) at = key_row(a, cu, j);
+    const int64_t at = seen ? key_row(a, cu, j) : 0;  // of the others any row that there is
+    uint4 codes[C];
+    uint32_t scales[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      codes[c] = reinterpret_cast<const uint4*>(a.k_codes + at * (D / 2))[c];
+      scales[c] = a.k_scales[at * C + c];
+    }
     float s = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
+      const uint32_t w[4] = {codes[c].x, codes[c].y, codes[c].z, codes[c].w};
       float part = 0.0f;
-#pragma unroll 1
+#pragma unroll
       for (int x = 0; x < 4; ++x) {
         uint32_t h[4];
-        e2m1x8_to_half(reinterpret_cast<const uint32_t*>(a.k_codes + at * (D / 2))[4 * c + x], h);
+        e2m1x8_to_half(w[x], h);
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           const float2 k = word_to_f32<__half>(h[y]);
@@ -460,7 +470,7 @@ __device__ __forceinline__ void wide_row(const AttnParams& a, const Cursor& cu, 
           part = fmaf(k.y, __shfl_sync(0xFFFFFFFFu, qv[c], 8 * x + 2 * y + 1), part);
         }
       }
-      s = fmaf(part, e8m0_value(a.k_scales[at * C + c]), s);
+      s = fmaf(part, e8m0_value(scales[c]), s);
     }
     s = seen ? s * a.scale_log2 : -INFINITY;
     float top = s;
@@ -474,15 +484,30 @@ __device__ __forceinline__ void wide_row(const AttnParams& a, const Cursor& cu, 
 #pragma unroll
     for (int c = 0; c < C; ++c) o[c] *= alpha;
 #pragma unroll 1
-    for (uint32_t left = any; left != 0; left &= left - 1) {
-      const int u = __ffs(left) - 1;
-      const int64_t key = __shfl_sync(0xFFFFFFFFu, at, u);
-      const float pu = __shfl_sync(0xFFFFFFFFu, p, u);
+    for (int u0 = 0; u0 < 32; u0 += kAtOnce) {
+      if ((any >> u0 & ((1u << kAtOnce) - 1)) == 0) continue;
+      uint32_t v[kAtOnce], e[kAtOnce];
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int64_t key = __shfl_sync(0xFFFFFFFFu, at, u0 + u);
+        const uint8_t* src = a.v_codes + key * (D / 2) + lane * (C / 2);
+        if constexpr (C == 2) v[u] = *src;
+        else if constexpr (C == 4) v[u] = *reinterpret_cast<const uint16_t*>(src);
+        else v[u] = *reinterpret_cast<const uint32_t*>(src);
+        e[u] = a.v_scales[key * C + lane * C / 32];
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const float pu = __shfl_sync(0xFFFFFFFFu, p, u0 + u);
+        if (!(any >> (u0 + u) & 1)) continue;  // what is not seen may be NaN
         uint32_t h[4];
-        e2m1x8_to_half(uint32_t(a.v_codes[key * (D / 2) + 16 * c + lane / 2]) >> (4 * (lane & 1)), h);
-        o[c] = fmaf(pu, word_to_f32<__half>(h[0]).x * e8m0_value(a.v_scales[key * C + c]), o[c]);
+        e2m1x8_to_half(v[u], h);
+        const float f = e8m0_value(e[u]);
+#pragma unroll
+        for (int c = 0; c < C; c += 2) {
+          const float2 x = word_to_f32<__half>(h[c / 2]);
+          o[c] = fmaf(pu, x.x * f, o[c]), o[c + 1] = fmaf(pu, x.y * f, o[c + 1]);
+        }
       }
     }
   }
@@ -491,16 +516,16 @@ __device__ __forceinline__ void wide_row(const AttnParams& a, const Cursor& cu, 
   const int32_t pe = part_exponent(l);
   if (part_o != nullptr) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) part_o[(8 * c + lane / 4) * part_step + lane % 4] = o[c] * pow2i(-pe);
+    for (int c = 0; c < C; ++c) part_o[(lane * C + c) / 4 * part_step + (lane * C + c) % 4] = o[c] * pow2i(-pe);
     if (lane == 0) *part_ml = make_float2(m + float(pe), l * pow2i(-pe));
     return;
   }
   const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-  uint16_t* out = static_cast<uint16_t*>(a.out) + int64_t(cu.q0 + qi) * a.o_st + int64_t(hq) * a.o_sh;
+  uint16_t* out = static_cast<uint16_t*>(a.out) + int64_t(cu.q0 + qi) * a.o_st + int64_t(hq) * a.o_sh + lane * C;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const float f = o[c] * inv;
-    out[32 * c + lane] = uint16_t(a.bf16 ? f32_to_word<__nv_bfloat16>(f, 0.0f) : f32_to_word<__half>(f, 0.0f));
+    out[c] = uint16_t(a.bf16 ? f32_to_word<__nv_bfloat16>(f, 0.0f) : f32_to_word<__half>(f, 0.0f));
   }
   if (lane == 0 && a.lse != nullptr)
     a.lse[int64_t(cu.q0 + qi) * (a.kv_heads * a.group) + hq] =

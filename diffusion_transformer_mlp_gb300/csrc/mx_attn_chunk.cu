@@ -60,9 +60,9 @@ constexpr int kHeadroom = 8;   // value scales may exceed their reference by 2^8
 constexpr int kLiftK = 13, kLiftV = 5;  // largest elements: 6 * 2^13
 // Where rows see different keys (see too_wide): keys down to 2^-36 of the tile's
 // largest are exact, and values down to 2^-28 of their reference, which may be 2^16
-// above the largest that a row sees: a row keeps those down to 2^-12 of its own,
-// and the first rows of a prompt, whose first token often has values 2^6 to 2^10
-// below the others', need no second pass.
+// above the largest that a row sees: a row keeps those down to 2^-12 of its own.
+// (2^8, as with few rows, would work more of the first rows of prompts anew, which
+// see little but a first token whose values may be small.)
 constexpr int kSpreadK = 23 + kLiftK, kSpreadV = 16;
 
 template <int D>

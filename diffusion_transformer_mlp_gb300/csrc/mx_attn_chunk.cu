@@ -72,7 +72,8 @@ struct Chunk {
   static constexpr int kSlots = D == 256 ? 2 : 4;     // decoded tiles
   // Keys and values of a tile handed on apart, so that with two slots the next
   // keys need not wait for this tile's p v (2 x 2,048 queries on 8,192 keys,
-  // dim 256: 1,336 -> 984 us; with four slots it only costs, dim 128: 366 -> 409).
+  // dim 256: 1,336 -> 984 us, 1,021 with the check for what rows see; with four
+  // slots it only costs, dim 128: 366 -> 409).
   static constexpr bool kApart = kSlots == 2;
   static constexpr int kQBytes = 128 * D * 2;         // one row tile
   static constexpr int kKvBytes = kTK * D * 2;        // one decoded tile of K or V

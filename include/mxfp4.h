@@ -151,9 +151,9 @@ nvfp4_status mxfp4_cache_read(const mxfp4_cache* cache, const int32_t* table, in
  * much larger ones small keys and values count as rounded, too: keys to 2^-40
  * of the largest of the 64 around them, values to 2^-16 of the largest that
  * the query sees in their block of 32 columns (2^-24 where all queries of the
- * call see that one).  Where queries of a call see
- * very different ones, each is worked out by itself, slowly, so that this
- * holds for what each of them sees.
+ * call see that one).  Where queries of a call see very different ones, each
+ * is worked out by itself, slowly, so that this holds for what each of them
+ * sees.
  *   q       [total_q, q_heads, dim] of `dtype` (BF16 or FP16), strides q_st,
  *           q_sh in elements (unit along dim)
  *   out     as q, strides o_st, o_sh;  lse  float32 [total_q, q_heads] or NULL

@@ -34,7 +34,10 @@ EXPORTED = ["nvfp4_padded_rows", "nvfp4_qdata_bytes", "nvfp4_scale_bytes", "nvfp
             "nvfp4_fc2_host_noalloc", "nvfp4_diag_fc2_gemm_clock",
             "mxfp4_padded_cols", "mxfp4_qdata_bytes", "mxfp4_scale_bytes", "mxfp4_scale_offset", "mxfp4_quantize",
             "mxfp4_dequantize", "mxfp4_gemm", "mxfp4_linear_workspace_bytes", "mxfp4_linear", "mxfp4_cache_write",
-            "mxfp4_cache_read", "mxfp4_attention_workspace_bytes", "mxfp4_cache_attention"]
+            "mxfp4_cache_read", "mxfp4_attention_workspace_bytes", "mxfp4_cache_attention",
+            "mxfp4_attention_shared_workspace_bytes", "mxfp4_cache_attention_shared", "head_norm_rotary",
+            "mxfp4_cache_write_rotary", "mxfp4_pages_workspace_bytes", "mxfp4_pages_select", "mxfp4_pages_extend",
+            "mxfp4_pages_compact", "mxfp4_cache_copy"]
 
 _lock = threading.Lock()
 _lib = None
@@ -134,6 +137,25 @@ def load(path: str | None = None) -> ctypes.CDLL:
         L.mxfp4_attention_workspace_bytes.argtypes = [i32, i32, i32, i32]
         L.mxfp4_cache_attention.restype = st
         L.mxfp4_cache_attention.argtypes = [vp, vp, vp]
+        f32 = ctypes.c_float
+        L.mxfp4_attention_shared_workspace_bytes.restype = i64
+        L.mxfp4_attention_shared_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i64, i32, i32]
+        L.mxfp4_cache_attention_shared.restype = st
+        L.mxfp4_cache_attention_shared.argtypes = [vp, vp, vp, vp]
+        L.head_norm_rotary.restype = st
+        L.head_norm_rotary.argtypes = [vp, vp, vp, i32, i32, i64, i32, f32, vp]
+        L.mxfp4_cache_write_rotary.restype = st
+        L.mxfp4_cache_write_rotary.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i64, f32, vp]
+        L.mxfp4_pages_workspace_bytes.restype = i64
+        L.mxfp4_pages_workspace_bytes.argtypes = [vp]
+        L.mxfp4_pages_select.restype = st
+        L.mxfp4_pages_select.argtypes = [vp, vp, vp, i64, vp]
+        L.mxfp4_pages_extend.restype = st
+        L.mxfp4_pages_extend.argtypes = [vp, vp, i64, vp, vp, vp, vp, i64, vp]
+        L.mxfp4_pages_compact.restype = st
+        L.mxfp4_pages_compact.argtypes = [vp, vp, vp, vp, i64, vp]
+        L.mxfp4_cache_copy.restype = st
+        L.mxfp4_cache_copy.argtypes = [vp, vp, vp, i64, vp]
         _lib = L
         return _lib
 

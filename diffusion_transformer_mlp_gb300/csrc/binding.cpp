@@ -36,6 +36,15 @@ struct Api {
   decltype(&mxfp4_cache_read) cache_read;
   decltype(&mxfp4_attention_workspace_bytes) attention_workspace_bytes;
   decltype(&mxfp4_cache_attention) cache_attention;
+  decltype(&mxfp4_attention_shared_workspace_bytes) attention_shared_workspace_bytes;
+  decltype(&mxfp4_cache_attention_shared) cache_attention_shared;
+  decltype(&head_norm_rotary) norm_rotary;
+  decltype(&mxfp4_cache_write_rotary) cache_write_rotary;
+  decltype(&mxfp4_pages_workspace_bytes) pages_workspace_bytes;
+  decltype(&mxfp4_pages_select) pages_select;
+  decltype(&mxfp4_pages_extend) pages_extend;
+  decltype(&mxfp4_pages_compact) pages_compact;
+  decltype(&mxfp4_cache_copy) cache_copy;
 };
 Api api = {};
 PyObject* check_fn = nullptr;  // _lib.check: raises for a status
@@ -351,7 +360,8 @@ PyObject* cache_read(PyObject* const* a) {
 
 // cache_attention(q, cache x 4, table, lens, q_starts | None, max_queries | None, scale | None, causal, window, sinks,
 //                 out | None, lse | None, status | None, stream) -> out
-PyObject* cache_attention(PyObject* const* a) {
+// cache_attention_shared(the same, groups, shared, max_group | None) -> out
+PyObject* attend(PyObject* const* a, bool with_groups) {
   const Cache c = cache(a + 1);
   const Tensor& q = tensor(a[0], "q");
   if (q.dim() != 3 || q.size(2) != c.c.dim || q.size(1) == 0 || q.size(1) % c.c.kv_heads != 0)
@@ -387,6 +397,17 @@ PyObject* cache_attention(PyObject* const* a) {
   }
   const int causal = PyObject_IsTrue(a[10]);
   if (causal < 0) throw Raised();
+  mxfp4_shared s = {};
+  if (with_groups) {
+    const Tensor &groups = ints(a[17], at::kInt, 1, "groups", c.dev), &shared = ints(a[18], at::kInt, 1, "shared", c.dev);
+    if (groups.size(0) != shared.size(0) + 1) bad("groups must have an entry for each group and one more");
+    if (shared.size(0) > 0x7FFFFFFF) bad("too many groups");
+    const int64_t most_group = a[19] == Py_None ? total : whole(a[19]);
+    if (most_group < 0) bad("max_group must not be negative");
+    if (total > 0 && shared.size(0) > 0 && most_group == 0) bad("q has rows, but max_group leaves no query");
+    s.groups = static_cast<const int32_t*>(groups.data_ptr()), s.shared = static_cast<const int32_t*>(shared.data_ptr());
+    s.count = int32_t(shared.size(0)), s.max_group = int32_t(most_group < total ? most_group : total);
+  }
   const Launch on_stream(a[16], c.dev);
   Tensor out;
   if (a[13] == Py_None) {
@@ -408,7 +429,11 @@ PyObject* cache_attention(PyObject* const* a) {
     g.lse = static_cast<float*>(lse.data_ptr());
   }
   if (total > 0 && seqs > 0 && most > 0) {
-    const int64_t need = api.attention_workspace_bytes(c.c.kv_heads, int32_t(heads), c.c.dim, int32_t(most));
+    const int64_t need =
+        with_groups ? api.attention_shared_workspace_bytes(c.c.kv_heads, int32_t(heads), c.c.dim, int32_t(total),
+                                                           int32_t(most), int32_t(seqs), table.size(1), s.count,
+                                                           s.max_group)
+                    : api.attention_workspace_bytes(c.c.kv_heads, int32_t(heads), c.c.dim, int32_t(most));
     Tensor ws = empty({need}, at::kByte, c.dev);
     g.q = q.data_ptr(), g.out = out.data_ptr();
     g.table = static_cast<const int32_t*>(table.data_ptr());
@@ -422,9 +447,216 @@ PyObject* cache_attention(PyObject* const* a) {
     g.causal = causal;
     g.window = int32_t(window < 0x7FFFFFFF ? window : 0x7FFFFFFF);
     g.sinks = int32_t(sinks < 0x7FFFFFFF ? sinks : 0x7FFFFFFF);
-    done(api.cache_attention(&c.c, &g, on_stream.handle()), "mxfp4_cache_attention");
+    if (with_groups)
+      done(api.cache_attention_shared(&c.c, &g, &s, on_stream.handle()), "mxfp4_cache_attention_shared");
+    else
+      done(api.cache_attention(&c.c, &g, on_stream.handle()), "mxfp4_cache_attention");
   }
   return on_stream.result(out, a[13] != Py_None);
+}
+PyObject* cache_attention(PyObject* const* a) { return attend(a, false); }
+PyObject* cache_attention_shared(PyObject* const* a) { return attend(a, true); }
+
+struct Rotary {
+  mxfp4_rotary r;
+  int32_t weight_code;
+  float eps;
+};
+// The rotation and the norm in args: turns, axis | None, interleaved, positions, q_weight | None, k_weight | None, eps.
+Rotary rotary_of(PyObject* const* a, const Tensor& x, c10::DeviceIndex dev) {
+  Rotary o = {};
+  const Tensor& turns = ints(a[0], at::kLong, 1, "rotary.turns", dev);
+  if (turns.size(0) > 0x7FFFFFFF) bad("rotary.turns is too large");
+  o.r.turns = static_cast<const int64_t*>(turns.data_ptr());
+  o.r.pairs = int32_t(turns.size(0));
+  if (a[1] != Py_None) {
+    const Tensor& axis = ints(a[1], at::kInt, 1, "rotary.axis", dev);
+    if (axis.size(0) != turns.size(0)) bad("rotary.axis must have an entry for each of rotary.turns");
+    o.r.axis = static_cast<const int32_t*>(axis.data_ptr());
+  }
+  o.r.interleaved = PyObject_IsTrue(a[2]);
+  if (o.r.interleaved < 0) throw Raised();
+  const Tensor& pos = tensor(a[3], "positions");
+  if (pos.scalar_type() != at::kInt || !pos.is_contiguous() || pos.dim() < 1 || pos.dim() > 2 ||
+      pos.size(0) != x.size(0) || (pos.dim() == 2 && (pos.size(1) < 1 || pos.size(1) > 65536)))
+    bad("positions must be a contiguous int32 [tokens] or [tokens, axes] tensor");
+  on(pos, dev);
+  o.r.positions = static_cast<const int32_t*>(pos.data_ptr());
+  o.r.axes = pos.dim() == 2 ? int32_t(pos.size(1)) : 1;
+  o.weight_code = code_of(x.scalar_type(), "q");
+  bool one = false;
+  for (int i = 4; i < 6; ++i) {
+    if (a[i] == Py_None) continue;
+    const char* name = i == 4 ? "q_weight" : "k_weight";
+    const Tensor& w = tensor(a[i], name);
+    if (w.dim() != 1 || w.size(0) != x.size(2) || !w.is_contiguous())
+      bad(std::string(name) + " must be a contiguous [" + std::to_string(x.size(2)) + "] tensor");
+    if (w.scalar_type() != x.scalar_type() && w.scalar_type() != at::kFloat)
+      bad(std::string(name) + " must be float32 or of the heads' type");
+    const int32_t code = code_of(w.scalar_type(), name);
+    if (one && code != o.weight_code) bad("q_weight and k_weight must have one type");
+    one = true, o.weight_code = code;
+    no_graph(w, name);
+    on(w, dev);
+  }
+  const double eps = PyFloat_AsDouble(a[6]);
+  if (eps == -1.0 && PyErr_Occurred()) throw Raised();
+  o.eps = float(eps);
+  return o;
+}
+// Heads [tokens, heads, dim] of one type; the sizes are checked against `like`.
+mxfp4_heads heads_in(const Tensor& x, const Tensor& like, const char* name, c10::DeviceIndex dev) {
+  if (x.dim() != 3 || x.size(0) != like.size(0) || x.size(2) != like.size(2) || x.scalar_type() != like.scalar_type())
+    bad(std::string(name) + " must be [tokens, heads, dim], of one type and with the tokens and dim of q");
+  if (x.stride(2) != 1 && x.size(2) > 1) bad(std::string(name) + " must have unit stride along its last dimension");
+  if (x.size(1) > 65535) bad(std::string(name) + " has too many heads");
+  no_graph(x, name);
+  on(x, dev);
+  mxfp4_heads h = {};
+  h.x = x.data_ptr(), h.st = x.stride(0), h.sh = x.stride(1), h.heads = int32_t(x.size(1));
+  return h;
+}
+const void* weight_at(PyObject* o) { return o == Py_None ? nullptr : THPVariable_Unpack(o).data_ptr(); }
+// Where the heads go: the given tensor, checked, or a new one.
+Tensor heads_out(PyObject* o, const Tensor& x, const char* name, c10::DeviceIndex dev, mxfp4_heads& h) {
+  Tensor t;
+  if (o == Py_None) {
+    t = empty({x.size(0), x.size(1), x.size(2)}, x.scalar_type(), dev);
+  } else {
+    t = tensor(o, name);
+    if (t.dim() != 3 || t.sizes() != x.sizes() || t.scalar_type() != x.scalar_type() || t.stride(2) != 1)
+      bad(std::string(name) + " must have the heads' shape and type and unit stride along its last dimension");
+    if ((t.size(0) > 1 && t.stride(0) == 0) || (t.size(1) > 1 && t.stride(1) == 0))
+      bad(std::string(name) + " must not overlap itself");
+    if (t.data_ptr() == x.data_ptr() && t.strides() != x.strides() && x.numel() > 0)
+      bad(std::string(name) + " may be the heads themselves only with their strides");
+    on(t, dev);
+    no_graph(t, name);
+  }
+  h.out = t.data_ptr(), h.o_st = t.stride(0), h.o_sh = t.stride(1);
+  return t;
+}
+
+// norm_rotary(q, k | None, turns, axis | None, interleaved, positions, q_weight | None, k_weight | None, eps,
+//             q_out | None, k_out | None, stream) -> (q_out, k_out | None)
+PyObject* norm_rotary(PyObject* const* a) {
+  const Tensor& q = tensor(a[0], "q");
+  const c10::DeviceIndex dev = cuda_index(q);
+  const bool both = a[1] != Py_None;
+  if (q.dim() != 3) bad("q must be [tokens, heads, dim]");
+  const int32_t code = code_of(q.scalar_type(), "q");
+  mxfp4_heads hq = heads_in(q, q, "q", dev), hk = {};
+  if (both) hk = heads_in(tensor(a[1], "k"), q, "k", dev);
+  else if (a[7] != Py_None || a[10] != Py_None) bad("k_weight and k_out are for a k");
+  const Rotary r = rotary_of(a + 2, q, dev);
+  hq.weight = weight_at(a[6]), hk.weight = weight_at(a[7]);
+  if (q.size(2) > 256) bad("dim must be a multiple of 16 up to 256");
+  const Launch on_stream(a[11], dev);
+  Tensor tq = heads_out(a[9], q, "q_out", dev, hq), tk;
+  if (both) tk = heads_out(a[10], THPVariable_Unpack(a[1]), "k_out", dev, hk);
+  done(api.norm_rotary(&hq, both ? &hk : nullptr, &r.r, code, r.weight_code, q.size(0), int32_t(q.size(2)), r.eps,
+                       on_stream.handle()),
+       "head_norm_rotary");
+  PyObject* ok = Py_None;
+  if (both) ok = on_stream.result(tk, a[10] != Py_None);
+  else Py_INCREF(ok);
+  return Py_BuildValue("NN", on_stream.result(tq, a[9] != Py_None), ok);
+}
+
+// cache_write_rotary(cache x 4, q, k, v, slots, turns, axis | None, interleaved, positions, q_weight | None,
+//                    k_weight | None, eps, q_out | None, stream) -> q_out
+PyObject* cache_write_rotary(PyObject* const* a) {
+  const Cache c = cache(a);
+  const Tensor& q = tensor(a[4], "q");
+  if (q.dim() != 3 || q.size(2) != c.c.dim) bad("q must be [tokens, heads, " + std::to_string(c.c.dim) + "]");
+  const int32_t code = code_of(q.scalar_type(), "q", false);
+  mxfp4_heads hq = heads_in(q, q, "q", c.dev), hk = heads_in(heads_of(a[5], c.c, "k", c.dev), q, "k", c.dev),
+              hv = heads_in(heads_of(a[6], c.c, "v", c.dev), q, "v", c.dev);
+  const Tensor& slots = ints(a[7], at::kLong, 1, "slots", c.dev);
+  if (slots.size(0) != q.size(0)) bad("slots must have an entry for each token");
+  const Rotary r = rotary_of(a + 8, q, c.dev);
+  hq.weight = weight_at(a[12]), hk.weight = weight_at(a[13]);
+  const Launch on_stream(a[16], c.dev);
+  Tensor out = heads_out(a[15], q, "q_out", c.dev, hq);
+  done(api.cache_write_rotary(&c.c, &hq, &hk, &hv, static_cast<const int64_t*>(slots.data_ptr()), &r.r, code,
+                              r.weight_code, q.size(0), r.eps, on_stream.handle()),
+       "mxfp4_cache_write_rotary");
+  return on_stream.result(out, a[15] != Py_None);
+}
+
+struct Pages {
+  mxfp4_pages p;
+  c10::DeviceIndex dev;
+};
+// The pages in args[0..3]: refs, table, lens, page_size.
+Pages pages_of(PyObject* const* a) {
+  const c10::DeviceIndex dev = cuda_index(tensor(a[0], "pages.refs"));
+  const Tensor &refs = ints(a[0], at::kInt, 1, "pages.refs", dev), &table = ints(a[1], at::kInt, 2, "pages.table", dev),
+               &lens = ints(a[2], at::kInt, 1, "pages.lens", dev);
+  if (table.size(0) != lens.size(0)) bad("pages.table must have a row for each of pages.lens");
+  if (refs.numel() == 0 || table.numel() == 0) bad("there must be pages, rows and room in the rows");
+  if (lens.size(0) > 0x7FFFFFFF) bad("pages.table has too many rows");
+  const int64_t size = whole(a[3]);
+  if (size < 1 || size > 0x7FFFFFFF) bad("page_size must be 16, 32, 64, 128 or 256");
+  return {{static_cast<int32_t*>(refs.data_ptr()), static_cast<int32_t*>(table.data_ptr()),
+           static_cast<int32_t*>(lens.data_ptr()), refs.size(0), table.size(1), int32_t(lens.size(0)), int32_t(size)},
+          dev};
+}
+
+// pages_select(pages x 4, sources, stream)
+PyObject* pages_select(PyObject* const* a) {
+  const Pages g = pages_of(a);
+  const Tensor& sources = ints(a[4], at::kInt, 1, "sources", g.dev);
+  if (sources.size(0) != g.p.rows) bad("sources must have an entry for each row");
+  const Launch on_stream(a[5], g.dev);
+  const int64_t need = api.pages_workspace_bytes(&g.p);
+  Tensor ws = empty({need}, at::kByte, g.dev);
+  done(api.pages_select(&g.p, static_cast<const int32_t*>(sources.data_ptr()), ws.data_ptr(), need, on_stream.handle()),
+       "mxfp4_pages_select");
+  Py_RETURN_NONE;
+}
+
+// pages_extend(pages x 4, counts, total, stream) -> (slots, copies, missing)
+PyObject* pages_extend(PyObject* const* a) {
+  const Pages g = pages_of(a);
+  const Tensor& counts = ints(a[4], at::kInt, 1, "counts", g.dev);
+  if (counts.size(0) != g.p.rows) bad("counts must have an entry for each row");
+  const int64_t total = whole(a[5]);
+  if (total < 0 || total > 0x7FFFFFFF) bad("total must be from 0 to 2^31 - 1");
+  const Launch on_stream(a[6], g.dev);
+  const int64_t need = api.pages_workspace_bytes(&g.p);
+  Tensor ws = empty({need}, at::kByte, g.dev), slots = empty({total}, at::kLong, g.dev),
+         copies = empty({int64_t(g.p.rows), 2}, at::kInt, g.dev), missing = empty({1}, at::kInt, g.dev);
+  done(api.pages_extend(&g.p, static_cast<const int32_t*>(counts.data_ptr()), total,
+                        static_cast<int64_t*>(slots.data_ptr()), static_cast<int32_t*>(copies.data_ptr()),
+                        static_cast<int32_t*>(missing.data_ptr()), ws.data_ptr(), need, on_stream.handle()),
+       "mxfp4_pages_extend");
+  return Py_BuildValue("NNN", on_stream.result(slots), on_stream.result(copies), on_stream.result(missing));
+}
+
+// pages_compact(pages x 4, stream) -> (moves, used)
+PyObject* pages_compact(PyObject* const* a) {
+  const Pages g = pages_of(a);
+  const Launch on_stream(a[4], g.dev);
+  const int64_t need = api.pages_workspace_bytes(&g.p);
+  Tensor ws = empty({need}, at::kByte, g.dev), moves = empty({g.p.pages / 2, 2}, at::kInt, g.dev),
+         used = empty({1}, at::kInt, g.dev);
+  done(api.pages_compact(&g.p, static_cast<int32_t*>(moves.data_ptr()), static_cast<int32_t*>(used.data_ptr()),
+                         ws.data_ptr(), need, on_stream.handle()),
+       "mxfp4_pages_compact");
+  return Py_BuildValue("NN", on_stream.result(moves), on_stream.result(used));
+}
+
+// cache_copy(cache x 4, source x 4, pairs, stream)
+PyObject* cache_copy(PyObject* const* a) {
+  const Cache c = cache(a), s = cache(a + 4);
+  if (c.dev != s.dev) bad(kOneDevice);
+  const Tensor& pairs = ints(a[8], at::kInt, 2, "pairs", c.dev);
+  if (pairs.size(1) != 2) bad("pairs must be [n, 2]");
+  const Launch on_stream(a[9], c.dev);
+  done(api.cache_copy(&c.c, &s.c, static_cast<const int32_t*>(pairs.data_ptr()), pairs.size(0), on_stream.handle()),
+       "mxfp4_cache_copy");
+  Py_RETURN_NONE;
 }
 
 // Every function takes a fixed number of positional arguments, and no C++
@@ -480,6 +712,13 @@ PyMethodDef methods[] = {{"bind", (PyCFunction)(void*)bind, METH_FASTCALL, nullp
                          ENTRY(cache_write, 8),
                          ENTRY(cache_read, 9),
                          ENTRY(cache_attention, 17),
+                         ENTRY(cache_attention_shared, 20),
+                         ENTRY(norm_rotary, 12),
+                         ENTRY(cache_write_rotary, 17),
+                         ENTRY(pages_select, 6),
+                         ENTRY(pages_extend, 7),
+                         ENTRY(pages_compact, 5),
+                         ENTRY(cache_copy, 10),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mxfp4", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -42,9 +42,10 @@ extern "C" int64_t mxfp4_attention_workspace_bytes(int32_t kv_heads, int32_t q_h
   return many_rows(dim, rows) ? attn_chunk_workspace(dim) : attn_stream_workspace(dim);
 }
 
-extern "C" nvfp4_status mxfp4_cache_attention(const mxfp4_cache* cache, const mxfp4_attention* args,
-                                              nvfp4_stream_t stream) {
-  const std::string nm("mxfp4_cache_attention");
+namespace nvfp4 {
+
+nvfp4_status attn_params(const mxfp4_cache* cache, const mxfp4_attention* args, int64_t workspace_bytes,
+                         const std::string& nm, AttnParams& p) {
   int sh = 0;
   const nvfp4_status st = check_cache(cache, &sh, nm);
   if (st != NVFP4_OK) return st;
@@ -56,6 +57,7 @@ extern "C" nvfp4_status mxfp4_cache_attention(const mxfp4_cache* cache, const mx
   if (g.q_heads < 1 || g.q_heads % cache->kv_heads != 0)
     return fail(NVFP4_EINVAL, nm + ": q_heads must be a positive multiple of kv_heads");
   if (!std::isfinite(g.scale)) return fail(NVFP4_EINVAL, nm + ": scale must be finite");
+  p = {};
   if (g.seqs == 0 || g.total_q == 0 || g.max_queries == 0) return NVFP4_OK;
   if (!g.q || !g.out || !g.table || !g.lens || !g.workspace) return fail(NVFP4_EINVAL, nm + ": null pointer");
   if (g.table_ld < 1) return fail(NVFP4_EINVAL, nm + ": a block table row needs an entry");
@@ -69,10 +71,8 @@ extern "C" nvfp4_status mxfp4_cache_attention(const mxfp4_cache* cache, const mx
       reinterpret_cast<uintptr_t>(g.lens) % 4 != 0 || reinterpret_cast<uintptr_t>(g.q_starts) % 4 != 0 ||
       reinterpret_cast<uintptr_t>(g.lse) % 4 != 0)
     return fail(NVFP4_EALIGN, nm + ": workspace must be 16-byte aligned, the others aligned to their elements");
-  const int64_t need = mxfp4_attention_workspace_bytes(cache->kv_heads, g.q_heads, cache->dim, g.max_queries);
-  if (g.workspace_bytes < need)
-    return fail(NVFP4_EINVAL, nm + ": workspace too small, " + std::to_string(need) + " bytes are needed");
-  AttnParams p;
+  if (g.workspace_bytes < workspace_bytes)
+    return fail(NVFP4_EINVAL, nm + ": workspace too small, " + std::to_string(workspace_bytes) + " bytes are needed");
   p.q = g.q, p.out = g.out, p.lse = g.lse;
   p.table = g.table, p.lens = g.lens, p.q_starts = g.q_starts;
   p.k_codes = static_cast<const uint8_t*>(cache->k_codes);
@@ -92,7 +92,24 @@ extern "C" nvfp4_status mxfp4_cache_attention(const mxfp4_cache* cache, const mx
   p.o_vec = aligned16(g.out) && g.o_st % 8 == 0 && g.o_sh % 8 == 0;
   p.scale_log2 = g.scale * 1.4426950408889634f;
   p.wait_limit_cycles = kAttnWaitLimitCycles;
-  if (many_rows(cache->dim, int64_t(g.max_queries) * group))
-    return attn_chunk(cache, p, g.max_queries, g.workspace, reinterpret_cast<cudaStream_t>(stream));
-  return attn_stream(cache, p, g.max_queries, g.workspace, reinterpret_cast<cudaStream_t>(stream));
+  return NVFP4_OK;
+}
+
+nvfp4_status attn_run(const mxfp4_cache* cache, const AttnParams& p, int32_t max_queries, void* workspace,
+                      cudaStream_t stream) {
+  if (many_rows(cache->dim, int64_t(max_queries) * p.group)) return attn_chunk(cache, p, max_queries, workspace, stream);
+  return attn_stream(cache, p, max_queries, workspace, stream);
+}
+
+}  // namespace nvfp4
+
+extern "C" nvfp4_status mxfp4_cache_attention(const mxfp4_cache* cache, const mxfp4_attention* args,
+                                              nvfp4_stream_t stream) {
+  AttnParams p;
+  const int64_t need = cache && args ? mxfp4_attention_workspace_bytes(cache->kv_heads, args->q_heads, cache->dim,
+                                                                       args->max_queries)
+                                     : 0;
+  const nvfp4_status st = attn_params(cache, args, need, "mxfp4_cache_attention", p);
+  if (st != NVFP4_OK || p.seqs == 0) return st;
+  return attn_run(cache, p, args->max_queries, args->workspace, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -2,6 +2,8 @@
 // masks' geometry, small PTX helpers.
 #pragma once
 
+#include <string>
+
 #include "mx_common.cuh"
 
 namespace nvfp4 {
@@ -27,6 +29,7 @@ struct AttnParams {
   int32_t page_shift, kv_heads, group, seqs, total_q;
   int32_t bf16, causal, window, sinks;
   int32_t q_vec, o_vec;  // 16-byte accesses to q / out are aligned
+  int32_t o_f32;         // out is binary32 whatever q is, and 16-byte accesses are aligned (a part, to be joined)
   float scale_log2;      // softmax scale times log2(e)
   uint64_t wait_limit_cycles;
 };
@@ -282,12 +285,19 @@ __device__ __forceinline__ void store_o8_words(const AttnParams& a, uint16_t* ds
     dst[4] = uint16_t(w.z), dst[5] = uint16_t(w.z >> 16), dst[6] = uint16_t(w.w), dst[7] = uint16_t(w.w >> 16);
   }
 }
-__device__ __forceinline__ void store_o8(const AttnParams& a, uint16_t* dst, const float (&f)[8]) {
+// The same at element `off` of the output, from binary32.
+__device__ __forceinline__ void store_o8(const AttnParams& a, int64_t off, const float (&f)[8]) {
+  if (a.o_f32) {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + off);
+    dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+    dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+    return;
+  }
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     w[i] = a.bf16 ? f32_to_word<__nv_bfloat16>(f[2 * i], f[2 * i + 1]) : f32_to_word<__half>(f[2 * i], f[2 * i + 1]);
-  store_o8_words(a, dst, make_uint4(w[0], w[1], w[2], w[3]));
+  store_o8_words(a, static_cast<uint16_t*>(a.out) + off, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
 // Keys that only some rows see.  Both kernels put the values of all rows of a
@@ -521,11 +531,15 @@ __device__ __forceinline__ void wide_row(const AttnParams& a, const Cursor& cu, 
     return;
   }
   const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-  uint16_t* out = static_cast<uint16_t*>(a.out) + int64_t(cu.q0 + qi) * a.o_st + int64_t(hq) * a.o_sh + lane * C;
+  const int64_t out = int64_t(cu.q0 + qi) * a.o_st + int64_t(hq) * a.o_sh + lane * C;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const float f = o[c] * inv;
-    out[c] = uint16_t(a.bf16 ? f32_to_word<__nv_bfloat16>(f, 0.0f) : f32_to_word<__half>(f, 0.0f));
+    if (a.o_f32)
+      static_cast<float*>(a.out)[out + c] = f;
+    else
+      static_cast<uint16_t*>(a.out)[out + c] =
+          uint16_t(a.bf16 ? f32_to_word<__nv_bfloat16>(f, 0.0f) : f32_to_word<__half>(f, 0.0f));
   }
   if (lane == 0 && a.lse != nullptr)
     a.lse[int64_t(cu.q0 + qi) * (a.kv_heads * a.group) + hq] =
@@ -567,12 +581,19 @@ inline void split_queries(AttnParams& a, const AttnParams& base, int32_t b) {
     return;
   }
   a.q = static_cast<const uint16_t*>(base.q) + int64_t(b) * base.q_st;
-  a.out = static_cast<uint16_t*>(base.out) + int64_t(b) * base.o_st;
+  a.out = static_cast<uint8_t*>(base.out) + int64_t(b) * base.o_st * (base.o_f32 ? 4 : 2);
   if (base.lse != nullptr) a.lse = base.lse + int64_t(b) * base.kv_heads * base.group;
 }
 
 // mx_attn_combine.cu: the partials of k_attn_stream (rows: 8 or 16), of k_attn_chunk.
 nvfp4_status attn_combine(int dim, int rows, int tok, int row_tiles, const SplitParams& sp, cudaStream_t stream);
 nvfp4_status attn_join(int dim, int tok, const SplitParams& sp, cudaStream_t stream);
+
+// mx_attn.cu: the kernel for the rows that there may be, and its workspace.
+nvfp4_status attn_run(const mxfp4_cache* cache, const AttnParams& p, int32_t max_queries, void* workspace,
+                      cudaStream_t stream);
+// What an entry point of that name checks of its arguments; the parameters they give.
+nvfp4_status attn_params(const mxfp4_cache* cache, const mxfp4_attention* args, int64_t workspace_bytes,
+                         const std::string& nm, AttnParams& p);
 
 }  // namespace nvfp4

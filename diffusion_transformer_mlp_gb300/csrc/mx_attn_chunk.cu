@@ -573,6 +573,14 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
           for (int i = 0; i < 8; ++i) d[i * kRows] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           continue;
         }
+        if (a.o_f32) {
+          if (off >= 0) {
+            uint4* d = reinterpret_cast<uint4*>(static_cast<float*>(a.out) + off + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+          continue;
+        }
         // through shared memory, so that four lanes write 64 bytes of a row
         // (a thread that writes its own row: 4,400 to 10,000 cycles)
 #pragma unroll

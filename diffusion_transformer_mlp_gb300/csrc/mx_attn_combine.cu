@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_c
 #pragma unroll
   for (int k = 0; k < 8; ++k) f[k] *= inv;
   const int32_t row = rt * kRows + r, qi = row / a.group, hq = h * a.group + row - qi * a.group;
-  store_o8(a, static_cast<uint16_t*>(a.out) + int64_t(q0 + qi) * a.o_st + int64_t(hq) * a.o_sh + d, f);
+  store_o8(a, int64_t(q0 + qi) * a.o_st + int64_t(hq) * a.o_sh + d, f);
   if (d == 0 && a.lse != nullptr)
     a.lse[int64_t(q0 + qi) * (a.kv_heads * a.group) + hq] =
         l == 0.0f ? -INFINITY : (row_m[r] + kJoinLog2 - kWeightLog2 + log2f(l)) * 0.6931471805599453f;
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ Split
     const int32_t row = c.rt * kRows + r;
     if (row >= c.nq * a.group) return;
     const int32_t qi = row / a.group, hq = c.h * a.group + row - qi * a.group;
-    store_o8(a, static_cast<uint16_t*>(a.out) + int64_t(c.q0 + qi) * a.o_st + int64_t(hq) * a.o_sh + d, f);
+    store_o8(a, int64_t(c.q0 + qi) * a.o_st + int64_t(hq) * a.o_sh + d, f);
     if (d == 0 && a.lse != nullptr) a.lse[int64_t(c.q0 + qi) * (a.kv_heads * a.group) + hq] = lse;
   };
   grid_wait();

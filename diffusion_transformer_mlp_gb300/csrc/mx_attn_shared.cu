@@ -1,0 +1,222 @@
+// Attention of sequences that share a prefix, over the paged MXFP4 cache.
+//
+// softmax over the keys [prefix | own] joins from the softmaxes over both parts:
+//
+//   out = (e^(l1 - m) o1 + e^(l2 - m) o2) / (e^(l1 - m) + e^(l2 - m)),  m = max(l1, l2)
+//
+// with l the logarithm of a part's sum of exponentials.  The prefix is one
+// sequence whose queries are those of all sequences of the group, every one of
+// which sees all of it: its keys are read and decoded once for many rows, which
+// is work for k_attn_chunk where they are more than 64.  What a sequence has of
+// its own is a sequence whose block table begins behind the prefix; positions
+// only count relative to its end, so nothing else changes.  That takes whole
+// pages, hence the prefix is rounded down to them.
+//
+// k_shared_parts writes the two sets of lengths and tables, attention runs for
+// each with binary32 outputs, and k_shared_join joins them.
+#include <algorithm>
+#include <string>
+
+#include "mx_attn.cuh"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct SharedParams {
+  AttnParams a;  // of the call
+  const int32_t* groups;
+  const int32_t* shared;
+  int32_t count;
+  // of the groups' prefixes, of the sequences' own tokens
+  int32_t *table1, *lens1, *starts1;
+  int32_t *table2, *lens2;
+  int32_t* before;  // [seqs] tokens of the prefix
+  float *o1, *o2, *l1, *l2;
+};
+
+__device__ __forceinline__ int32_t group_start(const SharedParams& p, int32_t g) {
+  return min(max(p.groups[g], 0), p.a.seqs);
+}
+
+// Tokens that the sequences of group g share, by a whole block.
+__device__ int32_t prefix_of(const SharedParams& p, int32_t g, int32_t* red) {
+  const AttnParams& a = p.a;
+  const int32_t s0 = group_start(p, g), s1 = group_start(p, g + 1);
+  int32_t n = s0 < s1 ? min(p.shared[g], a.lens[s0]) : 0;  // the first one's table names it
+  for (int32_t b = s0 + int32_t(threadIdx.x); b < s1; b += kThreads) {
+    const int32_t nq = seq_queries(a, b);
+    if (nq > 0) n = min(n, a.causal ? a.lens[b] - nq : a.lens[b]);
+  }
+  n = __reduce_min_sync(0xFFFFFFFFu, n);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = n;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) n = min(n, red[i]);
+  const int64_t room = a.table_ld << a.page_shift;
+  return int32_t(min(int64_t(max(n, 0)), room)) & ~((1 << a.page_shift) - 1);
+}
+
+// A block for each group, then one for each sequence.
+__global__ void __launch_bounds__(kThreads) k_shared_parts(const __grid_constant__ SharedParams p) {
+  __shared__ int32_t red[kThreads / 32];
+  const AttnParams& a = p.a;
+  grid_wait();
+  if (int32_t(blockIdx.x) < p.count) {
+    const int32_t g = blockIdx.x, s0 = group_start(p, g), n = prefix_of(p, g, red);
+    if (threadIdx.x == 0) {
+      p.lens1[g] = n;
+      p.starts1[g] = s0 < a.seqs ? seq_start(a, s0) : a.total_q;
+      if (g + 1 == p.count) {
+        const int32_t s1 = max(group_start(p, p.count), s0);
+        // of the queries of the last sequence, the rows behind which may be nobody's
+        p.starts1[p.count] = s1 > 0 ? seq_start(a, s1 - 1) + seq_queries(a, s1 - 1) : 0;
+      }
+    }
+    const int32_t* src = a.table + s0 * a.table_ld;
+    for (int32_t i = threadIdx.x; i < n >> a.page_shift; i += kThreads) p.table1[g * a.table_ld + i] = src[i];
+    return;
+  }
+  const int32_t b = int32_t(blockIdx.x) - p.count;
+  int32_t n = 0;
+  if (b >= group_start(p, 0) && b < group_start(p, p.count)) {
+    int32_t lo = 0, hi = p.count;  // groups[lo] <= b < groups[hi]
+    while (hi - lo > 1) {
+      const int32_t mid = (lo + hi) >> 1;
+      if (group_start(p, mid) <= b) lo = mid;
+      else hi = mid;
+    }
+    n = prefix_of(p, lo, red);
+    n = min(n, max(a.lens[b], 0) & ~((1 << a.page_shift) - 1));  // without queries it limits nothing
+  }
+  const int32_t len = a.lens[b] - n;
+  if (threadIdx.x == 0) p.before[b] = n, p.lens2[b] = len;
+  const int64_t skip = n >> a.page_shift, most = a.table_ld - skip;
+  const int64_t pages = min((int64_t(max(len, 0)) + (int64_t(1) << a.page_shift) - 1) >> a.page_shift, most);
+  for (int64_t i = threadIdx.x; i < pages; i += kThreads) p.table2[b * a.table_ld + i] = a.table[b * a.table_ld + skip + i];
+}
+
+// Eight columns of a row and head a thread; the rows of sequence blockIdx.x.
+template <int D>
+__global__ void __launch_bounds__(kThreads) k_shared_join(const __grid_constant__ SharedParams p) {
+  const AttnParams& a = p.a;
+  grid_wait();
+  const int32_t b = blockIdx.x, heads = a.kv_heads * a.group;
+  const int64_t q0 = seq_start(a, b), items = int64_t(seq_queries(a, b)) * heads * (D / 8);
+  const bool prefix = p.before[b] > 0;
+  for (int64_t i = int64_t(blockIdx.y) * kThreads + threadIdx.x; i < items; i += int64_t(gridDim.y) * kThreads) {
+    const int64_t rh = q0 * heads + i / (D / 8);  // (row, head)
+    const int32_t d = int32_t(i % (D / 8)) * 8;
+    const float l2 = p.l2[rh], l1 = prefix ? p.l1[rh] : -INFINITY;
+    const float4* s2 = reinterpret_cast<const float4*>(p.o2 + rh * D + d);
+    float4 u = s2[0], v = s2[1];
+    float f[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+    float lse = l2;
+    if (prefix) {
+      const float4* s1 = reinterpret_cast<const float4*>(p.o1 + rh * D + d);
+      u = s1[0], v = s1[1];
+      const float g[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+      const float m = fmaxf(l1, l2), ref = m == -INFINITY ? 0.0f : m;
+      const float w1 = expf(l1 - ref), w2 = expf(l2 - ref), sum = w1 + w2;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      // zeros where a part has no keys
+#pragma unroll
+      for (int x = 0; x < 8; ++x) f[x] = (w1 * g[x] + w2 * f[x]) * inv;
+      lse = m == -INFINITY ? m : ref + logf(sum);
+    }
+    const int64_t row = rh / heads, h = rh - row * heads;
+    store_o8(a, row * a.o_st + h * a.o_sh + d, f);
+    if (d == 0 && a.lse != nullptr) a.lse[rh] = lse;
+  }
+}
+
+int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// Places in the workspace, from its start on; returns its size.
+int64_t layout(SharedParams& p, uint8_t* ws, int64_t attention, int64_t rows, int64_t heads, int32_t dim, int64_t seqs,
+               int64_t table_ld) {
+  int64_t at = align256(attention);
+  auto take = [&](auto*& ptr, int64_t n) {
+    ptr = reinterpret_cast<std::remove_reference_t<decltype(ptr)>>(ws + at);
+    at += align256(n * 4);
+  };
+  take(p.o1, rows * heads * dim);
+  take(p.o2, rows * heads * dim);
+  take(p.l1, rows * heads);
+  take(p.l2, rows * heads);
+  take(p.table1, p.count * table_ld);
+  take(p.lens1, p.count);
+  take(p.starts1, p.count + 1);
+  take(p.table2, seqs * table_ld);
+  take(p.lens2, seqs);
+  take(p.before, seqs);
+  return at;
+}
+
+}  // namespace
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" int64_t mxfp4_attention_shared_workspace_bytes(int32_t kv_heads, int32_t q_heads, int32_t dim,
+                                                          int32_t total_q, int32_t max_queries, int32_t seqs,
+                                                          int64_t table_ld, int32_t count, int32_t max_group) {
+  if (total_q < 1 || seqs < 1 || table_ld < 1 || count < 0 || max_queries < 1) return 0;
+  const int64_t own = mxfp4_attention_workspace_bytes(kv_heads, q_heads, dim, max_queries);
+  if (own == 0 || count == 0 || max_group < 1) return own;
+  SharedParams p;
+  p.count = count;
+  return layout(p, nullptr, std::max(own, mxfp4_attention_workspace_bytes(kv_heads, q_heads, dim, max_group)), total_q,
+                q_heads, dim, seqs, table_ld);
+}
+
+extern "C" nvfp4_status mxfp4_cache_attention_shared(const mxfp4_cache* cache, const mxfp4_attention* args,
+                                                     const mxfp4_shared* shared, nvfp4_stream_t stream) {
+  const std::string nm("mxfp4_cache_attention_shared");
+  if (!cache || !args || !shared) return fail(NVFP4_EINVAL, nm + ": null pointer");
+  if (args->window != 0) return fail(NVFP4_EUNSUPPORTED, nm + ": a window would hide the prefix");
+  if (shared->count < 0 || shared->max_group < 0) return fail(NVFP4_EINVAL, nm + ": negative size");
+  const int32_t max_group = std::min(shared->max_group, args->total_q);
+  const int64_t need =
+      mxfp4_attention_shared_workspace_bytes(cache->kv_heads, args->q_heads, cache->dim, args->total_q,
+                                             args->max_queries, args->seqs, args->table_ld, shared->count, max_group);
+  SharedParams p = {};
+  const nvfp4_status bad = attn_params(cache, args, need, nm, p.a);
+  if (bad != NVFP4_OK || p.a.seqs == 0) return bad;
+  p.a.sinks = 0;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (shared->count == 0 || max_group == 0) return attn_run(cache, p.a, args->max_queries, args->workspace, s);
+  if (!shared->groups || !shared->shared) return fail(NVFP4_EINVAL, nm + ": null pointer");
+  if (reinterpret_cast<uintptr_t>(shared->groups) % 4 != 0 || reinterpret_cast<uintptr_t>(shared->shared) % 4 != 0)
+    return fail(NVFP4_EALIGN, nm + ": groups and shared must be aligned to their elements");
+  if (int64_t(max_group) * p.a.group > (int64_t(1) << 24) || int64_t(shared->count) + args->seqs > 0x7FFFFFFF)
+    return fail(NVFP4_EUNSUPPORTED, nm + ": problem too large");
+  const int64_t heads = args->q_heads;
+  const int32_t dim = cache->dim;
+  p.groups = shared->groups, p.shared = shared->shared, p.count = shared->count;
+  layout(p, static_cast<uint8_t*>(args->workspace),
+         std::max(mxfp4_attention_workspace_bytes(cache->kv_heads, args->q_heads, dim, args->max_queries),
+                  mxfp4_attention_workspace_bytes(cache->kv_heads, args->q_heads, dim, max_group)),
+         args->total_q, heads, dim, args->seqs, args->table_ld);
+  nvfp4_status st = launch("launch k_shared_parts", k_shared_parts, dim3(unsigned(p.count + args->seqs)), dim3(kThreads),
+                           0, 0, s, p);
+  if (st != NVFP4_OK) return st;
+  AttnParams part = p.a;
+  part.o_f32 = 1, part.o_vec = 1;
+  part.o_st = heads * dim, part.o_sh = dim;
+  part.out = p.o1, part.lse = p.l1;
+  part.table = p.table1, part.lens = p.lens1, part.q_starts = p.starts1;
+  part.seqs = p.count, part.causal = 0;
+  st = attn_run(cache, part, max_group, args->workspace, s);
+  if (st != NVFP4_OK) return st;
+  part.out = p.o2, part.lse = p.l2;
+  part.table = p.table2, part.lens = p.lens2, part.q_starts = args->q_starts;
+  part.seqs = args->seqs, part.causal = p.a.causal;
+  st = attn_run(cache, part, args->max_queries, args->workspace, s);
+  if (st != NVFP4_OK) return st;
+  const int64_t items = args->max_queries * heads * (dim / 8);
+  const unsigned y = unsigned(std::min<int64_t>((items + kThreads - 1) / kThreads, 1024));
+  auto join = dim == 64 ? k_shared_join<64> : (dim == 128 ? k_shared_join<128> : k_shared_join<256>);
+  return launch("launch k_shared_join", join, dim3(unsigned(args->seqs), y), dim3(kThreads), 0, 0, s, p);
+}

@@ -359,10 +359,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows, kSeveral>::kCtas)
         }
         if (whole) {
           if (row < head_rows)
-            store_o8(a,
-                     static_cast<uint16_t*>(a.out) + int64_t(cu.q0 + qi) * a.o_st + int64_t(hq) * a.o_sh + 32 * j +
-                         8 * tig,
-                     f);
+            store_o8(a, int64_t(cu.q0 + qi) * a.o_st + int64_t(hq) * a.o_sh + 32 * j + 8 * tig, f);
         } else {
           float4* d = reinterpret_cast<float4*>(sp.part_o + ((int64_t(worker) * 2 + slot) * kRows + g + 8 * r) * D +
                                                 32 * j + 8 * tig);

@@ -1,0 +1,530 @@
+// The pages of the paged cache: reference counts, block table and lengths on the
+// device, and copies of pages.
+//
+// The state is small (a few hundred KB of counts and table entries), so what
+// counts is launches.  Growing and compacting need ranks of free or held pages
+// over the whole pool: one cluster of eight blocks takes the pool in eight
+// contiguous parts, a warp a contiguous piece of one, and the parts' counts meet
+// behind a cluster barrier, where separate kernels would meet at a launch.  Free
+// pages are taken in the order of their ids, so that the same state gives the
+// same ids whatever the timing; counts are changed by atomics whose sums do not
+// depend on their order.
+//
+// What one block writes and another reads inside a kernel is read from L2
+// (__ldcg): the barrier orders it, and L1 may hold what was there before.
+#include <algorithm>
+#include <string>
+
+#include "mx_common.cuh"
+
+namespace nvfp4 {
+
+nvfp4_status check_cache(const mxfp4_cache* cache, int* page_shift, const std::string& nm);
+
+namespace {
+
+constexpr int kCluster = 8;
+constexpr int kThreads = 1024;  // of a block of the cluster
+constexpr int kWarps = kThreads / 32;
+constexpr int kGridThreads = 256;  // of the kernels over rows, tokens and bytes
+
+struct PagesParams {
+  int32_t* refs;
+  int32_t* table;
+  int32_t* lens;
+  int64_t pages, table_ld;
+  int32_t rows, shift;
+  // arguments
+  const int32_t* in;  // sources or counts
+  int64_t total;
+  int64_t* slots;
+  int32_t* pairs;   // copies [rows, 2] or moves [pages / 2, 2]
+  int32_t* number;  // missing or used
+  // workspace
+  int64_t* need;     // [rows + 1] pages that the rows before need; of select: new lengths as int32
+  int64_t* tokens;   // [rows + 1] new tokens of the rows before
+  int64_t* part;     // [kCluster + 1] free or held pages of the parts
+  int32_t* list;     // [pages] free ids in order; of compact: held ids in order
+  int32_t* writers;  // [pages] rows that go on in a shared page; of compact: holes in order
+  int32_t* lowest;   // [pages] the first of them; of compact: where a page goes
+  int32_t* taken;    // [rows, table_ld] of select
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Pages of a row of `len` tokens.
+__device__ __forceinline__ int64_t held(const PagesParams& p, int64_t len) {
+  const int64_t n = (max(len, int64_t(0)) + (int64_t(1) << p.shift) - 1) >> p.shift;
+  return min(n, p.table_ld);
+}
+__device__ __forceinline__ bool is_page(const PagesParams& p, int32_t page) { return page >= 0 && page < p.pages; }
+
+// How a row grows.
+struct Growth {
+  int64_t have, want;  // pages
+  int32_t count;       // tokens
+  int32_t last;        // the page that the next token goes into, if it holds some already; else -1
+};
+__device__ __forceinline__ Growth growth_of(const PagesParams& p, int32_t b) {
+  Growth g;
+  const int32_t len = max(p.lens[b], 0);
+  g.count = max(p.in[b], 0);
+  g.have = (int64_t(len) + (int64_t(1) << p.shift) - 1) >> p.shift;
+  g.want = (int64_t(len) + g.count + (int64_t(1) << p.shift) - 1) >> p.shift;
+  g.last = -1;
+  if (g.count > 0 && (len & ((1 << p.shift) - 1)) != 0 && g.have <= p.table_ld)
+    g.last = p.table[int64_t(b) * p.table_ld + g.have - 1];
+  return g;
+}
+
+// This warp's piece of the pool: the ids [lo, hi).
+struct Piece {
+  int64_t lo, hi;
+};
+__device__ __forceinline__ Piece piece_of(int64_t pages, int rank, int warp) {
+  const int64_t each = (pages + kCluster * kWarps - 1) / (kCluster * kWarps);
+  const int64_t lo = min(pages, (int64_t(rank) * kWarps + warp) * each);
+  return {lo, min(pages, lo + each)};
+}
+// Ids of the piece for which `held` is (or is not) so.
+__device__ __forceinline__ int32_t count_piece(const PagesParams& p, const Piece& w, bool want_held) {
+  const int lane = threadIdx.x & 31;
+  int32_t n = 0;
+#pragma unroll 8
+  for (int64_t i = w.lo + lane; i < w.hi; i += 32) n += (p.refs[i] > 0) == want_held;
+  return __reduce_add_sync(0xFFFFFFFFu, n);
+}
+// The pieces' counts: the ones before this warp's of the block (its own total to
+// part[rank]); the other blocks' are there behind the next cluster barrier.
+__device__ __forceinline__ int64_t before_in_block(const PagesParams& p, int32_t mine, int rank, int64_t* shared) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) shared[warp] = mine;
+  __syncthreads();
+  if (warp == 0) {
+    const int64_t v = shared[lane];
+    int64_t upto = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += u;
+    }
+    shared[lane] = upto - v;
+    if (lane == 31) p.part[rank] = upto;
+  }
+  __syncthreads();
+  return shared[warp];
+}
+
+// The slots of new tokens i0, i0 + step, .. below `upto`, by one warp for 32
+// neighbours at a time.
+__device__ __forceinline__ void write_slots(const PagesParams& p, int64_t i0, int64_t upto, int64_t step, bool ok) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t base = i0; base < upto; base += step) {
+    const int64_t i = base + lane;
+    if (i >= upto) continue;
+    int64_t slot = -1;
+    if (ok && i < __ldcg(p.tokens + p.rows)) {
+      int32_t lo = 0, hi = p.rows;  // tokens[lo] <= i < tokens[hi]
+      while (hi - lo > 1) {
+        const int32_t mid = (lo + hi) >> 1;
+        if (__ldcg(p.tokens + mid) <= i) lo = mid;
+        else hi = mid;
+      }
+      // the lengths count the new tokens already
+      const int64_t t = int64_t(__ldcg(p.lens + lo)) - (__ldcg(p.tokens + lo + 1) - i);
+      slot = (int64_t(__ldcg(p.table + lo * p.table_ld + (t >> p.shift))) << p.shift) + (t & ((1 << p.shift) - 1));
+    }
+    p.slots[i] = slot;
+  }
+}
+
+// Up to so many new tokens get their slots from the cluster itself.
+constexpr int64_t kInline = 4 * kCluster * kThreads;
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+    k_pages_extend(const __grid_constant__ PagesParams p) {
+  __shared__ int64_t shared[kWarps], sums[2][kWarps];
+  const int rank = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t thread = rank * kThreads + int32_t(threadIdx.x);
+  grid_wait();
+
+  // Rows that go on in a page that others hold too: how many, and the first.
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int32_t b = thread; b < p.rows; b += kCluster * kThreads) {
+      const Growth g = growth_of(p, b);
+      if (!is_page(p, g.last) || p.refs[g.last] <= 1) continue;
+      if (pass == 0) {
+        __stcg(p.writers + g.last, 0);
+        __stcg(p.lowest + g.last, p.rows);
+      } else {
+        atomicAdd(p.writers + g.last, 1);
+        atomicMin(p.lowest + g.last, b);
+      }
+    }
+    cluster_sync();
+  }
+
+  // Pages and tokens of the rows before each row; every block for itself.
+  int64_t pages = 0, tokens = 0;
+  bool bad = false;
+  for (int32_t b0 = 0; b0 < p.rows; b0 += kThreads) {
+    const int32_t b = b0 + int32_t(threadIdx.x);
+    int64_t need = 0, count = 0;
+    if (b < p.rows) {
+      const Growth g = growth_of(p, b);
+      count = g.count;
+      if (count > 0) {
+        need = g.want - g.have;
+        bad = bad || g.want > p.table_ld;
+        if (is_page(p, g.last)) {
+          const int32_t owners = p.refs[g.last];
+          if (owners > 1 && !(__ldcg(p.writers + g.last) == owners && __ldcg(p.lowest + g.last) == b)) ++need;
+        }
+      }
+    }
+    int64_t n = need, c = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t un = __shfl_up_sync(0xFFFFFFFFu, n, o), uc = __shfl_up_sync(0xFFFFFFFFu, c, o);
+      if (lane >= o) n += un, c += uc;
+    }
+    if (lane == 31) sums[0][warp] = n, sums[1][warp] = c;
+    __syncthreads();
+    if (warp < 2) {
+      int64_t v = sums[warp][lane], upto = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += u;
+      }
+      sums[warp][lane] = upto;
+    }
+    __syncthreads();
+    if (warp > 0) n += sums[0][warp - 1], c += sums[1][warp - 1];
+    if (rank == 0 && b < p.rows) p.need[b] = pages + n - need, p.tokens[b] = tokens + c - count;
+    pages += sums[0][kWarps - 1], tokens += sums[1][kWarps - 1];
+    __syncthreads();
+  }
+  if (rank == 0 && threadIdx.x == 0) p.need[p.rows] = pages, p.tokens[p.rows] = tokens;
+  bad = __syncthreads_or(bad || tokens > p.total);
+
+  // Free pages, as many as are needed.
+  const Piece mine = piece_of(p.pages, rank, warp);
+  int64_t at = before_in_block(p, count_piece(p, mine, false), rank, shared);
+  cluster_sync();
+  int64_t there = 0;
+#pragma unroll
+  for (int i = 0; i < kCluster; ++i) {
+    const int64_t n = __ldcg(p.part + i);
+    if (i < rank) at += n;
+    there += n;
+  }
+  const bool ok = !bad && pages <= there;
+  if (thread == 0) *p.number = bad ? -1 : int32_t(max(pages - there, int64_t(0)));
+  if (ok && at < pages) {
+#pragma unroll 4
+    for (int64_t i0 = mine.lo; i0 < mine.hi; i0 += 32) {
+      const int64_t i = i0 + lane;
+      const bool is_free = i < mine.hi && p.refs[i] <= 0;
+      const uint32_t all = __ballot_sync(0xFFFFFFFFu, is_free);
+      const int64_t k = at + __popc(all & ((1u << lane) - 1));
+      if (is_free && k < pages) p.list[k] = int32_t(i);
+      at += __popc(all);
+    }
+  }
+  cluster_sync();
+
+  // A warp a row.
+  for (int32_t b = rank * kWarps + warp; b < p.rows; b += kCluster * kWarps) {
+    int2 copy = make_int2(-1, -1);
+    if (ok) {
+      const Growth g = growth_of(p, b);
+      __syncwarp();  // all lanes have read the length
+      if (g.count > 0) {
+        const int64_t first = __ldcg(p.need + b), own = __ldcg(p.need + b + 1) - first - (g.want - g.have);
+        int32_t* row = p.table + int64_t(b) * p.table_ld;
+        for (int64_t i = lane; i < own + g.want - g.have; i += 32) {
+          const int32_t page = __ldcg(p.list + first + i);
+          row[g.have - own + i] = page;
+          p.refs[page] = 1;
+          if (i < own) {
+            copy = make_int2(g.last, page);
+            atomicSub(p.refs + g.last, 1);
+          }
+        }
+        if (lane == 0) p.lens[b] = max(p.lens[b], 0) + g.count;
+      }
+    }
+    if (lane == 0) p.pairs[2 * int64_t(b)] = copy.x, p.pairs[2 * int64_t(b) + 1] = copy.y;
+  }
+  if (p.total > kInline) return;  // k_pages_slots
+  cluster_sync();
+  write_slots(p, int64_t(thread & ~31), p.total, kCluster * kThreads, ok);
+}
+
+__global__ void __launch_bounds__(kGridThreads) k_pages_slots(const __grid_constant__ PagesParams p) {
+  grid_wait();
+  const int64_t step = int64_t(gridDim.x) * kGridThreads;
+  write_slots(p, int64_t(blockIdx.x) * kGridThreads + (threadIdx.x & ~31), p.total, step, __ldcg(p.number) == 0);
+}
+
+// Rows that change: what they take, and the pages' counts.  (One row may be the
+// source of another and change itself, so the table follows in a second launch.)
+__device__ __forceinline__ int32_t* new_lens(const PagesParams& p) { return reinterpret_cast<int32_t*>(p.need); }
+
+__global__ void __launch_bounds__(kGridThreads) k_pages_take(const __grid_constant__ PagesParams p) {
+  grid_wait();
+  const int32_t b = blockIdx.x, src = p.in[b];
+  if (src == b) return;
+  const bool some = src >= 0 && src < p.rows;
+  const int64_t had = held(p, p.lens[b]), has = some ? held(p, p.lens[src]) : 0;
+  const int32_t* old = p.table + b * p.table_ld;
+  const int32_t* from = p.table + (some ? src : 0) * p.table_ld;
+  for (int64_t i = threadIdx.x; i < max(had, has); i += kGridThreads) {
+    const int32_t leave = i < had ? old[i] : -1, take = i < has ? from[i] : -1;
+    if (i < has) p.taken[b * p.table_ld + i] = take;
+    if (leave == take) continue;
+    if (is_page(p, leave)) atomicSub(p.refs + leave, 1);
+    if (is_page(p, take)) atomicAdd(p.refs + take, 1);
+  }
+  if (threadIdx.x == 0) new_lens(p)[b] = some ? max(p.lens[src], 0) : 0;
+}
+__global__ void __launch_bounds__(kGridThreads) k_pages_put(const __grid_constant__ PagesParams p) {
+  grid_wait();
+  const int32_t b = blockIdx.x;
+  if (p.in[b] == b) return;
+  const int32_t len = new_lens(p)[b];
+  for (int64_t i = threadIdx.x; i < held(p, len); i += kGridThreads)
+    p.table[b * p.table_ld + i] = p.taken[b * p.table_ld + i];
+  if (threadIdx.x == 0) p.lens[b] = len;
+}
+
+// Held pages in order, and the free ids below their number, which those from
+// there on go to.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+    k_pages_compact(const __grid_constant__ PagesParams p) {
+  __shared__ int64_t shared[kWarps];
+  const int rank = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t thread = rank * kThreads + int32_t(threadIdx.x);
+  grid_wait();
+  const Piece mine = piece_of(p.pages, rank, warp);
+  int64_t at = before_in_block(p, count_piece(p, mine, true), rank, shared);
+  cluster_sync();
+  int64_t used = 0;
+#pragma unroll
+  for (int i = 0; i < kCluster; ++i) {
+    const int64_t n = __ldcg(p.part + i);
+    if (i < rank) at += n;
+    used += n;
+  }
+  if (thread == 0) {
+    *p.number = int32_t(used);
+    if (used == p.pages) p.part[kCluster] = used;
+  }
+#pragma unroll 4
+  for (int64_t i0 = mine.lo; i0 < mine.hi; i0 += 32) {
+    const int64_t i = i0 + lane;
+    const bool some = i < mine.hi && p.refs[i] > 0;
+    const uint32_t all = __ballot_sync(0xFFFFFFFFu, some);
+    const int64_t k = at + __popc(all & ((1u << lane) - 1));  // held pages below i
+    if (some) p.list[k] = int32_t(i);
+    else if (i < min(mine.hi, used)) p.writers[i - k] = int32_t(i);
+    if (i < mine.hi && i == used) p.part[kCluster] = k;
+    at += __popc(all);
+  }
+  cluster_sync();
+  const int64_t stay = __ldcg(p.part + kCluster), moves = used - stay;
+  for (int64_t j = thread; j < p.pages / 2; j += kCluster * kThreads) {
+    int2 pair = make_int2(-1, -1);
+    if (j < moves) {
+      pair = make_int2(__ldcg(p.list + stay + j), __ldcg(p.writers + j));
+      p.refs[pair.y] = p.refs[pair.x];
+      p.refs[pair.x] = 0;
+      p.lowest[pair.x] = pair.y;
+    }
+    p.pairs[2 * j] = pair.x, p.pairs[2 * j + 1] = pair.y;
+  }
+}
+__global__ void __launch_bounds__(kGridThreads) k_pages_renumber(const __grid_constant__ PagesParams p) {
+  grid_wait();
+  const int32_t used = *p.number, b = blockIdx.x;
+  int32_t* row = p.table + b * p.table_ld;
+  for (int64_t i = threadIdx.x; i < held(p, p.lens[b]); i += kGridThreads) {
+    const int32_t page = row[i];
+    if (page >= used && page < p.pages) row[i] = p.lowest[page];
+  }
+}
+
+// ------------------------------------------------------------------ copies --
+
+constexpr int64_t kPieceBytes = 16384;  // of a page, that a block copies at a time
+
+struct CopyParams {
+  const uint8_t* src[4];
+  uint8_t* dst[4];
+  int64_t bytes[4];   // of a page
+  int32_t pieces[4];  // of a page
+  int32_t all;        // their sum
+  int64_t src_pages, dst_pages, count;
+  const int32_t* pairs;
+};
+
+__global__ void __launch_bounds__(kGridThreads) k_cache_copy(const __grid_constant__ CopyParams p) {
+  constexpr int kEach = int(kPieceBytes / 16 / kGridThreads);
+  grid_wait();
+  for (int64_t u = blockIdx.x; u < p.count * p.all; u += gridDim.x) {
+    const int64_t pair = u / p.all;
+    const int32_t from = p.pairs[2 * pair], to = p.pairs[2 * pair + 1];
+    if (from < 0 || from >= p.src_pages || to < 0 || to >= p.dst_pages) continue;
+    int32_t piece = int32_t(u - pair * p.all), t = 0;
+    while (piece >= p.pieces[t]) piece -= p.pieces[t], ++t;
+    const int64_t at = piece * kPieceBytes, n = min(kPieceBytes, p.bytes[t] - at) / 16;
+    const uint4* src = reinterpret_cast<const uint4*>(p.src[t] + from * p.bytes[t] + at);
+    uint4* dst = reinterpret_cast<uint4*>(p.dst[t] + to * p.bytes[t] + at);
+    uint4 v[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (int(threadIdx.x) + i * kGridThreads < n) v[i] = __ldcs(src + threadIdx.x + i * kGridThreads);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (int(threadIdx.x) + i * kGridThreads < n) dst[threadIdx.x + i * kGridThreads] = v[i];
+  }
+}
+
+// ------------------------------------------------------------------ checks --
+
+int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
+
+nvfp4_status check_pages(const mxfp4_pages* g, const void* workspace, int64_t workspace_bytes, const std::string& nm,
+                         PagesParams& p) {
+  if (!g || !g->refs || !g->table || !g->lens || !workspace) return fail(NVFP4_EINVAL, nm + ": null pointer");
+  if (g->pages < 1 || g->rows < 1 || g->table_ld < 1 || g->page_size < 1)
+    return fail(NVFP4_EINVAL, nm + ": pages, rows, table_ld and page_size must be positive");
+  int sh = 0;
+  while ((1 << sh) < g->page_size) ++sh;
+  if ((1 << sh) != g->page_size || g->page_size < 16 || g->page_size > 256)
+    return fail(NVFP4_EUNSUPPORTED, nm + ": page_size must be 16, 32, 64, 128 or 256");
+  if (g->pages > (int64_t(1) << 30) || g->rows > (1 << 20) ||
+      g->table_ld > ((int64_t(1) << 31) - (int64_t(1) << 25)) / g->page_size ||
+      g->table_ld > (int64_t(1) << 31) / g->rows)
+    return fail(NVFP4_EUNSUPPORTED, nm + ": too many pages, rows or table entries");
+  if (!aligned16(workspace) || reinterpret_cast<uintptr_t>(g->refs) % 4 != 0 ||
+      reinterpret_cast<uintptr_t>(g->table) % 4 != 0 || reinterpret_cast<uintptr_t>(g->lens) % 4 != 0)
+    return fail(NVFP4_EALIGN, nm + ": workspace must be 16-byte aligned, the others aligned to their elements");
+  const int64_t need = mxfp4_pages_workspace_bytes(g);
+  if (workspace_bytes < need)
+    return fail(NVFP4_EINVAL, nm + ": workspace too small, " + std::to_string(need) + " bytes are needed");
+  p = {};
+  p.refs = g->refs, p.table = g->table, p.lens = g->lens;
+  p.pages = g->pages, p.table_ld = g->table_ld, p.rows = g->rows, p.shift = sh;
+  uint8_t* ws = static_cast<uint8_t*>(const_cast<void*>(workspace));
+  auto take = [&](int64_t bytes) {
+    uint8_t* at = ws;
+    ws += align256(bytes);
+    return at;
+  };
+  p.need = reinterpret_cast<int64_t*>(take((int64_t(g->rows) + 1) * 8));
+  p.tokens = reinterpret_cast<int64_t*>(take((int64_t(g->rows) + 1) * 8));
+  p.part = reinterpret_cast<int64_t*>(take((kCluster + 1) * 8));
+  p.taken = p.list = reinterpret_cast<int32_t*>(ws);
+  p.writers = p.list + g->pages;
+  p.lowest = p.writers + g->pages;
+  return NVFP4_OK;
+}
+
+}  // namespace
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" int64_t mxfp4_pages_workspace_bytes(const mxfp4_pages* g) {
+  if (!g || g->pages < 1 || g->rows < 1 || g->table_ld < 1) return 0;
+  return 2 * align256((int64_t(g->rows) + 1) * 8) + align256((kCluster + 1) * 8) +
+         align256(4 * std::max(3 * g->pages, g->rows * g->table_ld));
+}
+
+extern "C" nvfp4_status mxfp4_pages_select(const mxfp4_pages* pages, const int32_t* sources, void* workspace,
+                                           int64_t workspace_bytes, nvfp4_stream_t stream) {
+  const std::string nm("mxfp4_pages_select");
+  PagesParams p;
+  nvfp4_status st = check_pages(pages, workspace, workspace_bytes, nm, p);
+  if (st != NVFP4_OK) return st;
+  if (!sources) return fail(NVFP4_EINVAL, nm + ": null pointer");
+  if (reinterpret_cast<uintptr_t>(sources) % 4 != 0)
+    return fail(NVFP4_EALIGN, nm + ": sources must be aligned to its elements");
+  p.in = sources;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = launch("launch k_pages_take", k_pages_take, dim3(unsigned(p.rows)), dim3(kGridThreads), 0, 0, s, p);
+  if (st != NVFP4_OK) return st;
+  return launch("launch k_pages_put", k_pages_put, dim3(unsigned(p.rows)), dim3(kGridThreads), 0, 0, s, p);
+}
+
+extern "C" nvfp4_status mxfp4_pages_extend(const mxfp4_pages* pages, const int32_t* counts, int64_t total,
+                                           int64_t* slots, int32_t* copies, int32_t* missing, void* workspace,
+                                           int64_t workspace_bytes, nvfp4_stream_t stream) {
+  const std::string nm("mxfp4_pages_extend");
+  PagesParams p;
+  nvfp4_status st = check_pages(pages, workspace, workspace_bytes, nm, p);
+  if (st != NVFP4_OK) return st;
+  if (total < 0) return fail(NVFP4_EINVAL, nm + ": total must not be negative");
+  if (total > 0x7FFFFFFF) return fail(NVFP4_EUNSUPPORTED, nm + ": too many tokens");
+  if (!counts || (total > 0 && !slots) || !copies || !missing) return fail(NVFP4_EINVAL, nm + ": null pointer");
+  if (reinterpret_cast<uintptr_t>(counts) % 4 != 0 || reinterpret_cast<uintptr_t>(slots) % 8 != 0 ||
+      reinterpret_cast<uintptr_t>(copies) % 4 != 0 || reinterpret_cast<uintptr_t>(missing) % 4 != 0)
+    return fail(NVFP4_EALIGN, nm + ": counts, slots, copies and missing must be aligned to their elements");
+  p.in = counts, p.total = total, p.slots = slots, p.pairs = copies, p.number = missing;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = launch("launch k_pages_extend", k_pages_extend, dim3(kCluster), dim3(kThreads), 0, 0, s, p);
+  if (st != NVFP4_OK || total <= kInline) return st;
+  const int64_t blocks = (total + kGridThreads - 1) / kGridThreads, most = int64_t(sm_count()) * 8;
+  return launch("launch k_pages_slots", k_pages_slots, dim3(unsigned(std::min(blocks, most))), dim3(kGridThreads), 0, 0,
+                s, p);
+}
+
+extern "C" nvfp4_status mxfp4_pages_compact(const mxfp4_pages* pages, int32_t* moves, int32_t* used, void* workspace,
+                                            int64_t workspace_bytes, nvfp4_stream_t stream) {
+  const std::string nm("mxfp4_pages_compact");
+  PagesParams p;
+  nvfp4_status st = check_pages(pages, workspace, workspace_bytes, nm, p);
+  if (st != NVFP4_OK) return st;
+  if ((pages->pages > 1 && !moves) || !used) return fail(NVFP4_EINVAL, nm + ": null pointer");
+  if (reinterpret_cast<uintptr_t>(moves) % 4 != 0 || reinterpret_cast<uintptr_t>(used) % 4 != 0)
+    return fail(NVFP4_EALIGN, nm + ": moves and used must be aligned to their elements");
+  p.pairs = moves, p.number = used;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = launch("launch k_pages_compact", k_pages_compact, dim3(kCluster), dim3(kThreads), 0, 0, s, p);
+  if (st != NVFP4_OK) return st;
+  return launch("launch k_pages_renumber", k_pages_renumber, dim3(unsigned(p.rows)), dim3(kGridThreads), 0, 0, s, p);
+}
+
+extern "C" nvfp4_status mxfp4_cache_copy(const mxfp4_cache* cache, const mxfp4_cache* source, const int32_t* pairs,
+                                         int64_t count, nvfp4_stream_t stream) {
+  const std::string nm("mxfp4_cache_copy");
+  int sh = 0, src_sh = 0;
+  nvfp4_status st = check_cache(cache, &sh, nm);
+  if (st == NVFP4_OK) st = check_cache(source, &src_sh, nm);
+  if (st != NVFP4_OK) return st;
+  if (sh != src_sh || cache->kv_heads != source->kv_heads || cache->dim != source->dim)
+    return fail(NVFP4_EINVAL, nm + ": both caches must have one page_size, kv_heads and dim");
+  if (count < 0) return fail(NVFP4_EINVAL, nm + ": count must not be negative");
+  if (count == 0) return NVFP4_OK;
+  if (!pairs) return fail(NVFP4_EINVAL, nm + ": null pointer");
+  if (count > 0x7FFFFFFF) return fail(NVFP4_EUNSUPPORTED, nm + ": too many pairs");
+  if (reinterpret_cast<uintptr_t>(pairs) % 4 != 0)
+    return fail(NVFP4_EALIGN, nm + ": pairs must be aligned to its elements");
+  CopyParams p = {};
+  const void* src[4] = {source->k_codes, source->v_codes, source->k_scales, source->v_scales};
+  void* dst[4] = {cache->k_codes, cache->v_codes, cache->k_scales, cache->v_scales};
+  for (int i = 0; i < 4; ++i) {
+    p.src[i] = static_cast<const uint8_t*>(src[i]), p.dst[i] = static_cast<uint8_t*>(dst[i]);
+    p.bytes[i] = int64_t(cache->kv_heads) * cache->page_size * (cache->dim / (i < 2 ? 2 : 32));
+    p.pieces[i] = int32_t((p.bytes[i] + kPieceBytes - 1) / kPieceBytes);
+    p.all += p.pieces[i];
+  }
+  p.src_pages = source->pages, p.dst_pages = cache->pages, p.count = count, p.pairs = pairs;
+  const int64_t most = int64_t(sm_count()) * 8;
+  return launch("launch k_cache_copy", k_cache_copy, dim3(unsigned(std::min(count * p.all, most))), dim3(kGridThreads),
+                0, 0, reinterpret_cast<cudaStream_t>(stream), p);
+}

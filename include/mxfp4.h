@@ -10,6 +10,11 @@
  *   k, v, slots         --mxfp4_cache_write----> codes and scales in the paged cache
  *   cache, block table  --mxfp4_cache_read-----> k, v of whole sequences
  *   q, cache            --mxfp4_cache_attention> softmax(scale q k^T + mask) v
+ *   q, cache, groups    --mxfp4_cache_attention_shared> the same, what a group shares read once
+ *   q, k, positions     --head_norm_rotary-----> normed and rotated heads
+ *   q, k, v, positions  --mxfp4_cache_write_rotary> rotated q; codes and scales of rotated k, and of v
+ *   refs, table, lens   --mxfp4_pages_*--------> pages of rows: grown, forked, freed, made compact
+ *   cache, page pairs   --mxfp4_cache_copy-----> copies of pages
  *
  * MXFP4 recipe (32 consecutive elements of a row share one scale):
  *   E     = clamp(floor(log2 max|x|) - 2 + 127, 0, 254), 0 for an all-zero block
@@ -193,6 +198,152 @@ typedef struct {
 int64_t mxfp4_attention_workspace_bytes(int32_t kv_heads, int32_t q_heads, int32_t dim, int32_t max_queries);
 
 nvfp4_status mxfp4_cache_attention(const mxfp4_cache* cache, const mxfp4_attention* args, nvfp4_stream_t stream);
+
+/* Attention of sequences that share a prefix: the result of
+ * mxfp4_cache_attention (causal or not, without a window) on the same
+ * arguments, but tokens that the sequences of a group have in common are read
+ * once for all of them.  Sequences groups[g] .. groups[g+1] - 1 share their
+ * first shared[g] tokens: what their block tables name there has to hold the
+ * same bytes, as after mxfp4_pages_select, and is read through the first one's.
+ * Whole pages of them are shared, and only as many as lie before every query
+ * of the group (not causal: as every sequence has); the others are read by
+ * each sequence.  Sequences before groups[0] and from groups[count] on share
+ * nothing.
+ *   groups    device int32 [count + 1], not decreasing; what lies outside
+ *             0 .. seqs counts as its ends
+ *   shared    device int32 [count]
+ *   max_group an upper bound of the queries of a group known to the host
+ *   args      as above, window and sinks 0, workspace_bytes of the query below
+ * Precision: as above for each part; the parts are binary32 and joined in it. */
+typedef struct {
+  const int32_t* groups;
+  const int32_t* shared;
+  int32_t count;
+  int32_t max_group;
+} mxfp4_shared;
+
+/* Bytes of workspace that mxfp4_cache_attention_shared needs. */
+int64_t mxfp4_attention_shared_workspace_bytes(int32_t kv_heads, int32_t q_heads, int32_t dim, int32_t total_q,
+                                               int32_t max_queries, int32_t seqs, int64_t table_ld, int32_t count,
+                                               int32_t max_group);
+
+nvfp4_status mxfp4_cache_attention_shared(const mxfp4_cache* cache, const mxfp4_attention* args,
+                                          const mxfp4_shared* shared, nvfp4_stream_t stream);
+
+/* Heads of tokens: x [tokens, heads, dim], unit stride along dim, strides in
+ * elements along tokens (st) and heads (sh); out alike (o_st, o_sh), and may be
+ * x itself with the same strides.  weight [dim] of the norm, or NULL for none. */
+typedef struct {
+  const void* x;
+  void* out;
+  const void* weight;
+  int64_t st, sh, o_st, o_sh;
+  int32_t heads;
+  int32_t reserved;
+} mxfp4_heads;
+
+/* Rotary positions.  The first 2 * pairs elements of a head are pairs, the
+ * others stay as they are.  Pair i is elements 2i and 2i + 1 (interleaved) or i
+ * and i + pairs, and turns by position * frequency:
+ *   (a, b) -> (a cos t - b sin t, b cos t + a sin t)
+ *   t = 2 pi 2^-64 (positions[token, axis[i]] * turns[i] mod 2^64)
+ *   turns      device int64 [pairs]: frequency / 2 pi in units of 2^-64
+ *   axis       device int32 [pairs], or NULL for 0; clamped to 0 .. axes - 1
+ *   positions  device int32 [tokens, axes]
+ *   pairs      a multiple of 8, 2 * pairs <= dim; 0: no rotation */
+typedef struct {
+  const int64_t* turns;
+  const int32_t* axis;
+  const int32_t* positions;
+  int32_t pairs;
+  int32_t axes;
+  int32_t interleaved;
+  int32_t reserved;
+} mxfp4_rotary;
+
+/* out = rotation(norm(x)) for the heads of q, and of k unless it is NULL, with
+ * norm(x) = x / sqrt(mean(x^2) + eps) * weight over each head.  Binary32, the
+ * result rounded once.
+ *   dtype         of x and out; weight_dtype: the same, or MXFP4_FP32
+ *   dim           a multiple of 16 up to 256;  eps 1e-12 .. 1
+ * tokens may be 0. */
+nvfp4_status head_norm_rotary(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_rotary* rotary, int32_t dtype,
+                              int32_t weight_dtype, int64_t tokens, int32_t dim, float eps, nvfp4_stream_t stream);
+
+/* head_norm_rotary of q into its out, and of k into its slots of the cache in
+ * MXFP4 (quantised from binary32), where v goes as mxfp4_cache_write would put
+ * it.  dtype BF16 or FP16; k->out and v->out are not used, v->weight is NULL;
+ * slots as for mxfp4_cache_write (a token without one still has its q). */
+nvfp4_status mxfp4_cache_write_rotary(const mxfp4_cache* cache, const mxfp4_heads* q, const mxfp4_heads* k,
+                                      const mxfp4_heads* v, const int64_t* slots, const mxfp4_rotary* rotary,
+                                      int32_t dtype, int32_t weight_dtype, int64_t tokens, float eps,
+                                      nvfp4_stream_t stream);
+
+/* The pages of a cache (of the caches of all layers that share a block table),
+ * held on the device:
+ *   refs   int32 [pages]: how many rows hold the page; 0 for a free one
+ *   table  int32 [rows, table_ld]: row b of lens[b] tokens holds its first
+ *          ceil(lens[b] / page_size) pages, each once
+ *   lens   int32 [rows]
+ * The functions change all three in place, in stream order, and touch no
+ * cache.  Rows, lengths and page ids outside their ranges count as their ends
+ * (lengths) or as no page.  Page ids come out the same for the same state.
+ *   pages 1 .. 2^30, rows 1 .. 2^20, table_ld * page_size <= 2^31 - 2^25,
+ *   page_size as for a cache; rows * table_ld <= 2^31 */
+typedef struct {
+  int32_t* refs;
+  int32_t* table;
+  int32_t* lens;
+  int64_t pages;
+  int64_t table_ld;
+  int32_t rows;
+  int32_t page_size;
+} mxfp4_pages;
+
+/* Bytes of workspace (16-byte aligned) that each of the three needs. */
+int64_t mxfp4_pages_workspace_bytes(const mxfp4_pages* pages);
+
+/* Every row becomes what row sources[b] was before the call, its pages then
+ * held by both; -1 (or no row): empty.  sources[b] = b leaves a row alone.
+ * Table entries behind a row's pages stay as they were.
+ *   sources  device int32 [rows] */
+nvfp4_status mxfp4_pages_select(const mxfp4_pages* pages, const int32_t* sources, void* workspace,
+                                int64_t workspace_bytes, nvfp4_stream_t stream);
+
+/* Pages for counts[b] more tokens of every row, which its length then counts.
+ * New pages are the free ones of the lowest ids, row by row.  Where a row's
+ * next token goes into a page that holds some and other rows hold it too, the
+ * row gets a copy of its own: copies[b] = (that page, new page), which
+ * mxfp4_cache_copy has to copy in every cache before new tokens are written;
+ * (-1, -1) elsewhere.  If all the rows that hold a page go on in it, the first
+ * of them keeps it.
+ *   counts   device int32 [rows]; below 0 counts as 0
+ *   slots    device int64 [total]: the new tokens' slots, row by row; -1 behind
+ *            the last one
+ *   copies   device int32 [rows, 2]
+ *   missing  device int32 [1]: 0; or the free pages that are lacking; or -1 if
+ *            a row of the table is too short, or `total`: then slots and copies
+ *            are -1 and nothing has changed */
+nvfp4_status mxfp4_pages_extend(const mxfp4_pages* pages, const int32_t* counts, int64_t total, int64_t* slots,
+                                int32_t* copies, int32_t* missing, void* workspace, int64_t workspace_bytes,
+                                nvfp4_stream_t stream);
+
+/* Moves the pages that are held to the ids 0 .. used - 1: those from `used` on,
+ * in their order, to the free ids below it.
+ *   moves  device int32 [pages / 2, 2]: (from, to) for mxfp4_cache_copy, which
+ *          has to be called for every cache; (-1, -1) behind the last one
+ *   used   device int32 [1] */
+nvfp4_status mxfp4_pages_compact(const mxfp4_pages* pages, int32_t* moves, int32_t* used, void* workspace,
+                                 int64_t workspace_bytes, nvfp4_stream_t stream);
+
+/* Copies pages: page pairs[i][0] of `source` to page pairs[i][1] of `cache`
+ * (which may be the same).  Pairs with an id outside of its cache are skipped.
+ * No page is the target of two pairs, nor the target of one and the source of
+ * another in the same cache.
+ *   pairs  device int32 [count, 2]; count may be 0
+ *   source has the cache's page_size, kv_heads and dim */
+nvfp4_status mxfp4_cache_copy(const mxfp4_cache* cache, const mxfp4_cache* source, const int32_t* pairs,
+                              int64_t count, nvfp4_stream_t stream);
 
 #ifdef __cplusplus
 }

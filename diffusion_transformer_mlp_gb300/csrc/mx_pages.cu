@@ -13,6 +13,7 @@
 // What one block writes and another reads inside a kernel is read from L2
 // (__ldcg): the barrier orders it, and L1 may hold what was there before.
 #include <algorithm>
+#include <atomic>
 #include <string>
 
 #include "mx_common.cuh"
@@ -27,6 +28,7 @@ constexpr int kCluster = 8;
 constexpr int kThreads = 1024;  // of a block of the cluster
 constexpr int kWarps = kThreads / 32;
 constexpr int kGridThreads = 256;  // of the kernels over rows, tokens and bytes
+constexpr int64_t kSmallTable = 1 << 16;  // table entries that one cluster works on
 
 struct PagesParams {
   int32_t* refs;
@@ -117,38 +119,203 @@ __device__ __forceinline__ int64_t before_in_block(const PagesParams& p, int32_t
   return shared[warp];
 }
 
-// The slots of new tokens i0, i0 + step, .. below `upto`, by one warp for 32
-// neighbours at a time.
-__device__ __forceinline__ void write_slots(const PagesParams& p, int64_t i0, int64_t upto, int64_t step, bool ok) {
-  const int lane = threadIdx.x & 31;
-  for (int64_t base = i0; base < upto; base += step) {
-    const int64_t i = base + lane;
-    if (i >= upto) continue;
-    int64_t slot = -1;
-    if (ok && i < __ldcg(p.tokens + p.rows)) {
-      int32_t lo = 0, hi = p.rows;  // tokens[lo] <= i < tokens[hi]
-      while (hi - lo > 1) {
-        const int32_t mid = (lo + hi) >> 1;
-        if (__ldcg(p.tokens + mid) <= i) lo = mid;
-        else hi = mid;
-      }
-      // the lengths count the new tokens already
-      const int64_t t = int64_t(__ldcg(p.lens + lo)) - (__ldcg(p.tokens + lo + 1) - i);
-      slot = (int64_t(__ldcg(p.table + lo * p.table_ld + (t >> p.shift))) << p.shift) + (t & ((1 << p.shift) - 1));
-    }
-    p.slots[i] = slot;
+// The row of new token i: tokens[lo] <= i < tokens[lo + 1].
+template <class F>
+__device__ __forceinline__ int32_t row_of(int32_t rows, int64_t i, F tokens) {
+  int32_t lo = 0, hi = rows;
+  while (hi - lo > 1) {
+    const int32_t mid = (lo + hi) >> 1;
+    if (tokens(mid) <= i) lo = mid;
+    else hi = mid;
   }
+  return lo;
 }
 
 // Up to so many new tokens get their slots from the cluster itself.
 constexpr int64_t kInline = 4 * kCluster * kThreads;
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+// Sums over the rows of a block's threads: n and c become those up to this one.
+__device__ __forceinline__ void scan_rows(int64_t& n, int64_t& c, int64_t (&sums)[2][kWarps]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t un = __shfl_up_sync(0xFFFFFFFFu, n, o), uc = __shfl_up_sync(0xFFFFFFFFu, c, o);
+    if (lane >= o) n += un, c += uc;
+  }
+  if (lane == 31) sums[0][warp] = n, sums[1][warp] = c;
+  __syncthreads();
+  if (warp < 2) {
+    int64_t upto = sums[warp][lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += u;
+    }
+    sums[warp][lane] = upto;
+  }
+  __syncthreads();
+  if (warp > 0) n += sums[0][warp - 1], c += sums[1][warp - 1];
+}
+
+// The free pages that are needed: take(k, page) for the k-th of them.  `free_here`
+// are in this warp's piece, `pages` are needed in all.  False, and none is taken,
+// if there are too few (or `bad`).
+template <class F>
+__device__ __forceinline__ bool take_free(const PagesParams& p, int32_t free_here, int64_t pages, bool bad, int rank,
+                                          int64_t (&shared)[kWarps], F take) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Piece mine = piece_of(p.pages, rank, warp);
+  int64_t at = before_in_block(p, free_here, rank, shared);
+  cluster_sync();
+  int64_t there = 0;
+#pragma unroll
+  for (int i = 0; i < kCluster; ++i) {
+    const int64_t n = __ldcg(p.part + i);
+    if (i < rank) at += n;
+    there += n;
+  }
+  const bool ok = !bad && pages <= there;
+  if (rank == 0 && threadIdx.x == 0) *p.number = bad ? -1 : int32_t(max(pages - there, int64_t(0)));
+  if (!ok) return false;
+  constexpr int kAtOnce = 8;  // loads under way: what is taken is stored between them
+  for (int64_t i0 = mine.lo; i0 < mine.hi && at < pages; i0 += 32 * kAtOnce) {
+    bool is_free[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int64_t i = i0 + 32 * u + lane;
+      is_free[u] = i < mine.hi && p.refs[i] <= 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const uint32_t all = __ballot_sync(0xFFFFFFFFu, is_free[u]);
+      const int64_t k = at + __popc(all & ((1u << lane) - 1));
+      if (is_free[u] && k < pages) take(k, int32_t(i0 + 32 * u + lane));
+      at += __popc(all);
+    }
+  }
+  return true;
+}
+
+// Row b takes its pages from place `first` of the list on, the copy (`own`) before
+// the others; by a warp.
+__device__ __forceinline__ void grow_row(const PagesParams& p, int32_t b, const Growth& g, int32_t len, int64_t first,
+                                         int64_t own, bool ok) {
+  const int lane = threadIdx.x & 31;
+  int2 copy = make_int2(-1, -1);
+  if (ok && g.count > 0) {
+    int32_t* row = p.table + int64_t(b) * p.table_ld;
+    const int64_t n = own + g.want - g.have;
+    constexpr int kAtOnce = 8;
+    for (int64_t i0 = lane; i0 < n; i0 += 32 * kAtOnce) {
+      int32_t page[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+        if (i0 + 32 * u < n) page[u] = __ldcg(p.list + first + i0 + 32 * u);
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+        if (i0 + 32 * u < n) row[g.have - own + i0 + 32 * u] = page[u];
+      if (i0 < own) {
+        copy = make_int2(g.last, page[0]);
+        atomicSub(p.refs + g.last, 1);
+      }
+    }
+    if (lane == 0) p.lens[b] = len + g.count;
+  }
+  if (lane == 0) p.pairs[2 * int64_t(b)] = copy.x, p.pairs[2 * int64_t(b) + 1] = copy.y;
+}
+
+// Up to kThreads rows: every block has all of them, a thread a row, and what the
+// rows need of one another stays in its shared memory.  The blocks meet to rank the
+// free pages, and whoever finds one that is needed puts it into its row; they meet
+// again only where the new tokens' slots are written here, too.
+struct FewRows {
+  static constexpr int kSlots = 2 * kThreads;  // of a hash table of shared pages
+  int64_t need[kThreads + 1], tokens[kThreads + 1];
+  int32_t len[kThreads], last[kThreads], have[kThreads], own[kThreads];
+  int32_t page[kSlots], writers[kSlots], lowest[kSlots];
+};
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
+    k_pages_extend_few(const __grid_constant__ PagesParams p) {
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  FewRows& f = *reinterpret_cast<FewRows*>(dynamic);
+  __shared__ int64_t shared[kWarps], sums[2][kWarps];
+  const int rank = blockIdx.x, warp = threadIdx.x >> 5;
+  const int32_t b = int32_t(threadIdx.x);
+  for (int i = b; i < FewRows::kSlots; i += kThreads) f.page[i] = -1, f.writers[i] = 0, f.lowest[i] = kThreads;
+  grid_wait();
+  const int32_t free_here = count_piece(p, piece_of(p.pages, rank, warp), false);
+  Growth g = {};
+  g.last = -1;
+  int32_t owners = 0;
+  if (b < p.rows) {
+    g = growth_of(p, b);
+    f.len[b] = max(p.lens[b], 0), f.last[b] = g.last, f.have[b] = int32_t(min(g.have, p.table_ld));
+    if (is_page(p, g.last)) owners = p.refs[g.last];
+  }
+  __syncthreads();
+  // rows that go on in a page that others hold too: how many, and the first
+  int at = -1;
+  if (owners > 1) {
+    at = int((uint32_t(g.last) * 2654435761u) >> 21) & (FewRows::kSlots - 1);
+    for (;;) {  // at most half of the slots are taken
+      const int32_t was = atomicCAS(&f.page[at], -1, g.last);
+      if (was == -1 || was == g.last) break;
+      at = (at + 1) & (FewRows::kSlots - 1);
+    }
+    atomicAdd(&f.writers[at], 1);
+    atomicMin(&f.lowest[at], b);
+  }
+  __syncthreads();
+  const bool copy = owners > 1 && !(f.writers[at] == owners && f.lowest[at] == b);
+  const int64_t need = g.count > 0 ? g.want - g.have + copy : 0, count = g.count;
+  int64_t n = need, c = count;
+  scan_rows(n, c, sums);
+  f.need[b] = n - need, f.tokens[b] = c - count, f.own[b] = copy;
+  const int64_t pages = sums[0][kWarps - 1], tokens = sums[1][kWarps - 1];
+  if (b == 0) f.need[kThreads] = pages, f.tokens[kThreads] = tokens;
+  if (rank == 0) {  // for k_pages_slots
+    if (b < p.rows) p.tokens[b] = c - count;
+    if (b == 0) p.tokens[p.rows] = tokens;
+  }
+  const bool bad = __syncthreads_or((count > 0 && g.want > p.table_ld) || tokens > p.total);
+  const bool listed = p.total <= kInline;  // else k_pages_slots finds the pages in the table
+  const bool ok = take_free(p, free_here, pages, bad, rank, shared, [&](int64_t k, int32_t page) {
+    const int32_t r = row_of(p.rows, k, [&](int32_t x) { return f.need[x]; });
+    const int64_t place = f.have[r] + k - f.need[r] - f.own[r];
+    p.refs[page] = 1;
+    p.table[r * p.table_ld + place] = page;
+    if (listed) p.list[k] = page;
+    if (place < f.have[r]) {
+      p.pairs[2 * r] = f.last[r], p.pairs[2 * r + 1] = page;
+      atomicSub(p.refs + f.last[r], 1);
+    }
+  });
+  if (b < p.rows && b % kCluster == rank) {
+    if (ok && g.count > 0) p.lens[b] = f.len[b] + g.count;
+    if (!ok || !copy) p.pairs[2 * b] = -1, p.pairs[2 * b + 1] = -1;
+  }
+  if (!listed) return;
+  cluster_sync();
+  for (int64_t i = rank * kThreads + b; i < p.total; i += kCluster * kThreads) {
+    int64_t slot = -1;
+    if (ok && i < tokens) {
+      const int32_t r = row_of(p.rows, i, [&](int32_t x) { return f.tokens[x]; });
+      const int64_t t = f.len[r] + i - f.tokens[r], place = t >> p.shift, old = f.have[r] - f.own[r];
+      const int32_t page = __ldcg(place >= old ? p.list + f.need[r] + place - old : p.table + r * p.table_ld + place);
+      slot = (int64_t(page) << p.shift) + (t & ((1 << p.shift) - 1));
+    }
+    p.slots[i] = slot;
+  }
+}
+
+// Any number of rows.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     k_pages_extend(const __grid_constant__ PagesParams p) {
   __shared__ int64_t shared[kWarps], sums[2][kWarps];
-  const int rank = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x, warp = threadIdx.x >> 5;
   const int32_t thread = rank * kThreads + int32_t(threadIdx.x);
   grid_wait();
+  const int32_t free_here = count_piece(p, piece_of(p.pages, rank, warp), false);
 
   // Rows that go on in a page that others hold too: how many, and the first.
   for (int pass = 0; pass < 2; ++pass) {
@@ -185,125 +352,129 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
       }
     }
     int64_t n = need, c = count;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t un = __shfl_up_sync(0xFFFFFFFFu, n, o), uc = __shfl_up_sync(0xFFFFFFFFu, c, o);
-      if (lane >= o) n += un, c += uc;
-    }
-    if (lane == 31) sums[0][warp] = n, sums[1][warp] = c;
-    __syncthreads();
-    if (warp < 2) {
-      int64_t v = sums[warp][lane], upto = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-        if (lane >= o) upto += u;
-      }
-      sums[warp][lane] = upto;
-    }
-    __syncthreads();
-    if (warp > 0) n += sums[0][warp - 1], c += sums[1][warp - 1];
+    scan_rows(n, c, sums);
     if (rank == 0 && b < p.rows) p.need[b] = pages + n - need, p.tokens[b] = tokens + c - count;
     pages += sums[0][kWarps - 1], tokens += sums[1][kWarps - 1];
     __syncthreads();
   }
   if (rank == 0 && threadIdx.x == 0) p.need[p.rows] = pages, p.tokens[p.rows] = tokens;
   bad = __syncthreads_or(bad || tokens > p.total);
-
-  // Free pages, as many as are needed.
-  const Piece mine = piece_of(p.pages, rank, warp);
-  int64_t at = before_in_block(p, count_piece(p, mine, false), rank, shared);
+  const bool ok = take_free(p, free_here, pages, bad, rank, shared, [&](int64_t k, int32_t page) {
+    p.list[k] = page;
+    p.refs[page] = 1;
+  });
   cluster_sync();
-  int64_t there = 0;
-#pragma unroll
-  for (int i = 0; i < kCluster; ++i) {
-    const int64_t n = __ldcg(p.part + i);
-    if (i < rank) at += n;
-    there += n;
-  }
-  const bool ok = !bad && pages <= there;
-  if (thread == 0) *p.number = bad ? -1 : int32_t(max(pages - there, int64_t(0)));
-  if (ok && at < pages) {
-#pragma unroll 4
-    for (int64_t i0 = mine.lo; i0 < mine.hi; i0 += 32) {
-      const int64_t i = i0 + lane;
-      const bool is_free = i < mine.hi && p.refs[i] <= 0;
-      const uint32_t all = __ballot_sync(0xFFFFFFFFu, is_free);
-      const int64_t k = at + __popc(all & ((1u << lane) - 1));
-      if (is_free && k < pages) p.list[k] = int32_t(i);
-      at += __popc(all);
-    }
-  }
-  cluster_sync();
-
-  // A warp a row.
   for (int32_t b = rank * kWarps + warp; b < p.rows; b += kCluster * kWarps) {
-    int2 copy = make_int2(-1, -1);
-    if (ok) {
-      const Growth g = growth_of(p, b);
-      __syncwarp();  // all lanes have read the length
-      if (g.count > 0) {
-        const int64_t first = __ldcg(p.need + b), own = __ldcg(p.need + b + 1) - first - (g.want - g.have);
-        int32_t* row = p.table + int64_t(b) * p.table_ld;
-        for (int64_t i = lane; i < own + g.want - g.have; i += 32) {
-          const int32_t page = __ldcg(p.list + first + i);
-          row[g.have - own + i] = page;
-          p.refs[page] = 1;
-          if (i < own) {
-            copy = make_int2(g.last, page);
-            atomicSub(p.refs + g.last, 1);
-          }
-        }
-        if (lane == 0) p.lens[b] = max(p.lens[b], 0) + g.count;
-      }
-    }
-    if (lane == 0) p.pairs[2 * int64_t(b)] = copy.x, p.pairs[2 * int64_t(b) + 1] = copy.y;
+    const Growth g = growth_of(p, b);
+    const int32_t len = max(p.lens[b], 0);
+    __syncwarp();  // all lanes have read the length
+    const int64_t first = __ldcg(p.need + b), n = __ldcg(p.need + b + 1) - first;
+    grow_row(p, b, g, len, first, n - (g.count > 0 ? g.want - g.have : 0), ok);
   }
-  if (p.total > kInline) return;  // k_pages_slots
-  cluster_sync();
-  write_slots(p, int64_t(thread & ~31), p.total, kCluster * kThreads, ok);
 }
 
+// The slots of new tokens, once lengths and table have them: a warp takes 256
+// neighbours, of which most lie in one row, and looks for that at 32 places at a time.
+constexpr int kSlotsEach = 8;  // of a thread
 __global__ void __launch_bounds__(kGridThreads) k_pages_slots(const __grid_constant__ PagesParams p) {
   grid_wait();
-  const int64_t step = int64_t(gridDim.x) * kGridThreads;
-  write_slots(p, int64_t(blockIdx.x) * kGridThreads + (threadIdx.x & ~31), p.total, step, __ldcg(p.number) == 0);
+  const int lane = threadIdx.x & 31;
+  const int64_t first = (int64_t(blockIdx.x) * (kGridThreads / 32) + (threadIdx.x >> 5)) * kSlotsEach * 32;
+  const bool ok = *p.number == 0;
+  const int64_t tokens = ok ? p.tokens[p.rows] : 0;
+  int32_t row = 0, hi = p.rows;
+  while (hi - row > 1) {
+    const int32_t step = (hi - row + 31) / 32, x = row + lane * step;
+    const uint32_t below = __ballot_sync(0xFFFFFFFFu, x < hi && p.tokens[min(x, hi)] <= first);
+    row += max(__popc(below) - 1, 0) * step;
+    hi = min(row + step, hi);
+  }
+  int64_t end = p.tokens[row + 1], len = p.lens[row];  // the row's last token, its length with them
+#pragma unroll
+  for (int k = 0; k < kSlotsEach; ++k) {
+    const int64_t i = first + k * 32 + lane;
+    if (i >= p.total) return;
+    int64_t slot = -1;
+    if (i < tokens) {
+      if (i >= end) {
+        row = row_of(p.rows, i, [&](int32_t x) { return p.tokens[x]; });
+        end = p.tokens[row + 1], len = p.lens[row];
+      }
+      const int64_t t = len - (end - i);
+      slot = (int64_t(p.table[row * p.table_ld + (t >> p.shift)]) << p.shift) + (t & ((1 << p.shift) - 1));
+    }
+    p.slots[i] = slot;
+  }
 }
 
 // Rows that change: what they take, and the pages' counts.  (One row may be the
 // source of another and change itself, so the table follows in a second launch.)
 __device__ __forceinline__ int32_t* new_lens(const PagesParams& p) { return reinterpret_cast<int32_t*>(p.need); }
 
-__global__ void __launch_bounds__(kGridThreads) k_pages_take(const __grid_constant__ PagesParams p) {
-  grid_wait();
-  const int32_t b = blockIdx.x, src = p.in[b];
+
+constexpr int kRowEach = 4;  // entries of a thread whose loads are under way
+
+__device__ __forceinline__ void take_row(const PagesParams& p, int32_t b, int32_t first, int32_t step) {
+  const int32_t src = p.in[b];
   if (src == b) return;
   const bool some = src >= 0 && src < p.rows;
   const int64_t had = held(p, p.lens[b]), has = some ? held(p, p.lens[src]) : 0;
   const int32_t* old = p.table + b * p.table_ld;
   const int32_t* from = p.table + (some ? src : 0) * p.table_ld;
-  for (int64_t i = threadIdx.x; i < max(had, has); i += kGridThreads) {
-    const int32_t leave = i < had ? old[i] : -1, take = i < has ? from[i] : -1;
-    if (i < has) p.taken[b * p.table_ld + i] = take;
-    if (leave == take) continue;
-    if (is_page(p, leave)) atomicSub(p.refs + leave, 1);
-    if (is_page(p, take)) atomicAdd(p.refs + take, 1);
+  for (int64_t i0 = first; i0 < max(had, has); i0 += kRowEach * step) {
+    int32_t leave[kRowEach], take[kRowEach];
+#pragma unroll
+    for (int u = 0; u < kRowEach; ++u) {
+      const int64_t i = i0 + u * step;
+      leave[u] = i < had ? old[i] : -1, take[u] = i < has ? from[i] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kRowEach; ++u) {
+      const int64_t i = i0 + u * step;
+      if (i < has) p.taken[b * p.table_ld + i] = take[u];
+      if (leave[u] == take[u]) continue;
+      if (is_page(p, leave[u])) atomicSub(p.refs + leave[u], 1);
+      if (is_page(p, take[u])) atomicAdd(p.refs + take[u], 1);
+    }
   }
-  if (threadIdx.x == 0) new_lens(p)[b] = some ? max(p.lens[src], 0) : 0;
+  if (first == 0) new_lens(p)[b] = some ? max(p.lens[src], 0) : 0;
+}
+__device__ __forceinline__ void put_row(const PagesParams& p, int32_t b, int32_t first, int32_t step) {
+  if (p.in[b] == b) return;
+  const int32_t len = __ldcg(new_lens(p) + b);
+  const int64_t has = held(p, len);
+  for (int64_t i0 = first; i0 < has; i0 += kRowEach * step) {
+    int32_t take[kRowEach];
+#pragma unroll
+    for (int u = 0; u < kRowEach; ++u)
+      if (i0 + u * step < has) take[u] = __ldcg(p.taken + b * p.table_ld + i0 + u * step);
+#pragma unroll
+    for (int u = 0; u < kRowEach; ++u)
+      if (i0 + u * step < has) p.table[b * p.table_ld + i0 + u * step] = take[u];
+  }
+  if (first == 0) p.lens[b] = len;
+}
+__global__ void __launch_bounds__(kGridThreads) k_pages_take(const __grid_constant__ PagesParams p) {
+  grid_wait();
+  take_row(p, blockIdx.x, threadIdx.x, kGridThreads);
 }
 __global__ void __launch_bounds__(kGridThreads) k_pages_put(const __grid_constant__ PagesParams p) {
   grid_wait();
-  const int32_t b = blockIdx.x;
-  if (p.in[b] == b) return;
-  const int32_t len = new_lens(p)[b];
-  for (int64_t i = threadIdx.x; i < held(p, len); i += kGridThreads)
-    p.table[b * p.table_ld + i] = p.taken[b * p.table_ld + i];
-  if (threadIdx.x == 0) p.lens[b] = len;
+  put_row(p, blockIdx.x, threadIdx.x, kGridThreads);
+}
+// Both, of a small table: a warp a row, and a cluster barrier for the launch between.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
+    k_pages_select(const __grid_constant__ PagesParams p) {
+  const int32_t w = int32_t(blockIdx.x) * kWarps + int32_t(threadIdx.x >> 5);
+  grid_wait();
+  for (int32_t b = w; b < p.rows; b += kCluster * kWarps) take_row(p, b, threadIdx.x & 31, 32);
+  cluster_sync();
+  for (int32_t b = w; b < p.rows; b += kCluster * kWarps) put_row(p, b, threadIdx.x & 31, 32);
 }
 
 // Held pages in order, and the free ids below their number, which those from
 // there on go to.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     k_pages_compact(const __grid_constant__ PagesParams p) {
   __shared__ int64_t shared[kWarps];
   const int rank = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -359,37 +530,55 @@ __global__ void __launch_bounds__(kGridThreads) k_pages_renumber(const __grid_co
 
 // ------------------------------------------------------------------ copies --
 
-constexpr int64_t kPieceBytes = 16384;  // of a page, that a block copies at a time
+// A page's four buffers in a row, in chunks of 16 bytes; a block copies kUnit of
+// them at a time, four a thread.
+constexpr int kUnitEach = 4;
+constexpr int kUnit = kUnitEach * kGridThreads;
 
 struct CopyParams {
-  const uint8_t* src[4];
-  uint8_t* dst[4];
-  int64_t bytes[4];   // of a page
-  int32_t pieces[4];  // of a page
-  int32_t all;        // their sum
+  const uint4* src[4];
+  uint4* dst[4];
+  int32_t chunks[4];  // of a page's buffer
+  int32_t units;      // of a page
   int64_t src_pages, dst_pages, count;
   const int32_t* pairs;
 };
 
+// Lists of pairs are mostly empty behind their first entries, or here and there:
+// a warp looks up its block's next 32 units at once and passes over the empty ones.
 __global__ void __launch_bounds__(kGridThreads) k_cache_copy(const __grid_constant__ CopyParams p) {
-  constexpr int kEach = int(kPieceBytes / 16 / kGridThreads);
+  const int lane = threadIdx.x & 31;
+  const int64_t all = p.count * p.units;
   grid_wait();
-  for (int64_t u = blockIdx.x; u < p.count * p.all; u += gridDim.x) {
-    const int64_t pair = u / p.all;
-    const int32_t from = p.pairs[2 * pair], to = p.pairs[2 * pair + 1];
-    if (from < 0 || from >= p.src_pages || to < 0 || to >= p.dst_pages) continue;
-    int32_t piece = int32_t(u - pair * p.all), t = 0;
-    while (piece >= p.pieces[t]) piece -= p.pieces[t], ++t;
-    const int64_t at = piece * kPieceBytes, n = min(kPieceBytes, p.bytes[t] - at) / 16;
-    const uint4* src = reinterpret_cast<const uint4*>(p.src[t] + from * p.bytes[t] + at);
-    uint4* dst = reinterpret_cast<uint4*>(p.dst[t] + to * p.bytes[t] + at);
-    uint4 v[kEach];
+  for (int64_t u0 = blockIdx.x; u0 < all; u0 += int64_t(gridDim.x) * 32) {
+    const int64_t u = u0 + int64_t(gridDim.x) * lane, pair = u / p.units;
+    int32_t from = -1, to = -1;
+    if (u < all) from = p.pairs[2 * pair], to = p.pairs[2 * pair + 1];
+    uint32_t live =
+        __ballot_sync(0xFFFFFFFFu, from >= 0 && from < p.src_pages && to >= 0 && to < p.dst_pages);
+    const int32_t part = int32_t(u - pair * p.units);
+    while (live != 0) {
+      const int k = __ffs(live) - 1;
+      live &= live - 1;
+      const int64_t from_k = __shfl_sync(0xFFFFFFFFu, from, k), to_k = __shfl_sync(0xFFFFFFFFu, to, k);
+      const int32_t first = __shfl_sync(0xFFFFFFFFu, part, k) * kUnit + int32_t(threadIdx.x);
+      uint4 v[kUnitEach];
+      uint4* dst[kUnitEach];
 #pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (int(threadIdx.x) + i * kGridThreads < n) v[i] = __ldcs(src + threadIdx.x + i * kGridThreads);
+      for (int i = 0; i < kUnitEach; ++i) {
+        int32_t c = first + i * kGridThreads, t = 0;
+        dst[i] = nullptr;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (int(threadIdx.x) + i * kGridThreads < n) dst[threadIdx.x + i * kGridThreads] = v[i];
+        for (int x = 0; x < 3; ++x)
+          if (t == x && c >= p.chunks[x]) c -= p.chunks[x], t = x + 1;
+        if (c >= p.chunks[t]) continue;
+        v[i] = __ldcs(p.src[t] + from_k * p.chunks[t] + c);
+        dst[i] = p.dst[t] + to_k * p.chunks[t] + c;
+      }
+#pragma unroll
+      for (int i = 0; i < kUnitEach; ++i)
+        if (dst[i] != nullptr) *dst[i] = v[i];
+    }
   }
 }
 
@@ -456,6 +645,8 @@ extern "C" nvfp4_status mxfp4_pages_select(const mxfp4_pages* pages, const int32
     return fail(NVFP4_EALIGN, nm + ": sources must be aligned to its elements");
   p.in = sources;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (p.rows * p.table_ld <= kSmallTable)
+    return launch("launch k_pages_select", k_pages_select, dim3(kCluster), dim3(kThreads), 0, 0, s, p);
   st = launch("launch k_pages_take", k_pages_take, dim3(unsigned(p.rows)), dim3(kGridThreads), 0, 0, s, p);
   if (st != NVFP4_OK) return st;
   return launch("launch k_pages_put", k_pages_put, dim3(unsigned(p.rows)), dim3(kGridThreads), 0, 0, s, p);
@@ -476,11 +667,18 @@ extern "C" nvfp4_status mxfp4_pages_extend(const mxfp4_pages* pages, const int32
     return fail(NVFP4_EALIGN, nm + ": counts, slots, copies and missing must be aligned to their elements");
   p.in = counts, p.total = total, p.slots = slots, p.pairs = copies, p.number = missing;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  st = launch("launch k_pages_extend", k_pages_extend, dim3(kCluster), dim3(kThreads), 0, 0, s, p);
-  if (st != NVFP4_OK || total <= kInline) return st;
-  const int64_t blocks = (total + kGridThreads - 1) / kGridThreads, most = int64_t(sm_count()) * 8;
-  return launch("launch k_pages_slots", k_pages_slots, dim3(unsigned(std::min(blocks, most))), dim3(kGridThreads), 0, 0,
-                s, p);
+  if (p.rows <= kThreads) {
+    static std::atomic<uint64_t> ready{0};
+    st = allow_smem(reinterpret_cast<const void*>(k_pages_extend_few), int(sizeof(FewRows)), ready);
+    if (st == NVFP4_OK)
+      st = launch("launch k_pages_extend_few", k_pages_extend_few, dim3(kCluster), dim3(kThreads), sizeof(FewRows), 0, s, p);
+    if (total <= kInline) return st;
+  } else {
+    st = launch("launch k_pages_extend", k_pages_extend, dim3(kCluster), dim3(kThreads), 0, 0, s, p);
+  }
+  if (st != NVFP4_OK || total == 0) return st;
+  const int64_t each = kGridThreads * kSlotsEach, blocks = (total + each - 1) / each;
+  return launch("launch k_pages_slots", k_pages_slots, dim3(unsigned(blocks)), dim3(kGridThreads), 0, 0, s, p);
 }
 
 extern "C" nvfp4_status mxfp4_pages_compact(const mxfp4_pages* pages, int32_t* moves, int32_t* used, void* workspace,
@@ -517,14 +715,15 @@ extern "C" nvfp4_status mxfp4_cache_copy(const mxfp4_cache* cache, const mxfp4_c
   CopyParams p = {};
   const void* src[4] = {source->k_codes, source->v_codes, source->k_scales, source->v_scales};
   void* dst[4] = {cache->k_codes, cache->v_codes, cache->k_scales, cache->v_scales};
+  int32_t chunks = 0;
   for (int i = 0; i < 4; ++i) {
-    p.src[i] = static_cast<const uint8_t*>(src[i]), p.dst[i] = static_cast<uint8_t*>(dst[i]);
-    p.bytes[i] = int64_t(cache->kv_heads) * cache->page_size * (cache->dim / (i < 2 ? 2 : 32));
-    p.pieces[i] = int32_t((p.bytes[i] + kPieceBytes - 1) / kPieceBytes);
-    p.all += p.pieces[i];
+    p.src[i] = static_cast<const uint4*>(src[i]), p.dst[i] = static_cast<uint4*>(dst[i]);
+    p.chunks[i] = int32_t(int64_t(cache->kv_heads) * cache->page_size * (cache->dim / (i < 2 ? 2 : 32)) / 16);
+    chunks += p.chunks[i];
   }
+  p.units = (chunks + kUnit - 1) / kUnit;
   p.src_pages = source->pages, p.dst_pages = cache->pages, p.count = count, p.pairs = pairs;
   const int64_t most = int64_t(sm_count()) * 8;
-  return launch("launch k_cache_copy", k_cache_copy, dim3(unsigned(std::min(count * p.all, most))), dim3(kGridThreads),
+  return launch("launch k_cache_copy", k_cache_copy, dim3(unsigned(std::min(count * p.units, most))), dim3(kGridThreads),
                 0, 0, reinterpret_cast<cudaStream_t>(stream), p);
 }

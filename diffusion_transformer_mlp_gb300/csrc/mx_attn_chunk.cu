@@ -176,34 +176,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// Pairs of binary32 in 64 bits.  A pair of equal constants is made once, by a
-// volatile move: left to the compiler it is made again at every use.
-__device__ __forceinline__ uint64_t pair_const(float v) {
-  uint64_t r;
-  asm volatile("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t pair_of(uint32_t x, uint32_t y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // Eight 16-bit elements without the alignment of one load.
 __device__ __noinline__ uint4 load_8x16(const uint16_t* e) {
   return make_uint4(uint32_t(e[0]) | uint32_t(e[1]) << 16, uint32_t(e[2]) | uint32_t(e[3]) << 16,
@@ -405,6 +377,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
       if (lane == 0) mbar_arrive(&sh.q_full[qt]);
       return fabsf(a.scale_log2) * pow2i(-mine);
     };
+    auto live_rows = [&](const Cursor& c) { return c.rt * kRows + qt * 128 + q * 32 < c.nq * a.group; };
     advance(wk, wk);
     float qf = load_q(wk.seg);
     bool ok = true;
@@ -413,6 +386,24 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
       const Cursor& cu = w.seg;
       const int32_t n = w.n, g = w.g, sink_tiles = cu.s.sink_tiles - cu.t, first_tile = cu.t,
                     lo_tile = cu.s.lo_tile - sink_tiles;
+      // A warp behind the segment's last row: the barriers go on, and nothing is worked
+      // out, which would be masked throughout (rows of 64 to a kv head: 1.45 us a tile,
+      // so 0.8).  Whatever is in its lanes of tensor memory stays in them.
+      if (!live_rows(cu)) {
+        for (int j = 0; ok && j < n; ++j) {
+          const int x = g + j;
+          ok = wait(&sh.s_full[qt][x & 1], (x >> 1) & 1);
+          if (lane == 0 && ok) mbar_arrive(&sh.p_full[qt][x & 1]);
+        }
+        if (!ok) break;
+        Walk& next = sh.walk[warp][(seg + 1) & 1];
+        const bool more = advance(w, next);
+        if (more) qf = load_q(next.seg);
+        ok = wait(&sh.o_full[qt], seg & 1);
+        if (lane == 0 && ok) mbar_arrive(&sh.o_empty[qt]);
+        if (!ok || !more) break;
+        continue;
+      }
       const int32_t row = cu.rt * kRows + qt * 128 + r;
       const bool real = row < cu.nq * a.group;
       const int32_t pos = cu.len - cu.nq + (real ? row / a.group : 0);
@@ -569,8 +560,10 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
         if (!whole) {
           // [D / 4][rows] of four columns: a warp writes 512 bytes at a time
           uint4* d = reinterpret_cast<uint4*>(sp.part_o) + (part * (D / 4) + c / 4) * kRows + qt * 128 + r;
+          if (real) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) d[i * kRows] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            for (int i = 0; i < 8; ++i) d[i * kRows] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
           continue;
         }
         if (a.o_f32) {
@@ -842,16 +835,19 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     const uint32_t q_lo = desc_lo(smem_u32(sq + qt * T::kQBytes), 16), k_lo = desc_lo(smem_u32(sk), 16),
                    v_lo = desc_lo(smem_u32(sv), kTK * 128);
     const uint32_t t_q = tmem + T::kS + qt * 2 * kTK, t_o = tmem + T::kO + qt * D;
+    bool live = true;  // the row tile has rows in this segment; a second one of few rows has none
     auto scores = [&](int x) -> bool {
       const int slot = x % kSlots;
       if (!wait(&sh.k_full[slot], (x / kSlots) & 1)) return false;
       tc_fence_after();
       const uint32_t kb = k_lo + uint32_t(slot) * (T::kKvBytes >> 4), t_s = t_q + (x & 1) * kTK;
       if (elect_one()) {
+        if (live) {
 #pragma unroll
-        for (int d = 0; d < D; d += 16)
-          mma_ss(t_s, q_lo + (d / 64) * (128 * 128 >> 4) + (d % 64) / 8,
-                 kb + (d / 64) * (kTK * 128 >> 4) + (d % 64) / 8, kIdS, d > 0);
+          for (int d = 0; d < D; d += 16)
+            mma_ss(t_s, q_lo + (d / 64) * (128 * 128 >> 4) + (d % 64) / 8,
+                   kb + (d / 64) * (kTK * 128 >> 4) + (d % 64) / 8, kIdS, d > 0);
+        }
         tc_commit(&sh.s_full[qt][x & 1]);
         if constexpr (T::kApart) tc_commit(&sh.k_empty[slot]);
         mbar_arrive(&sh.s_full[qt][x & 1]);  // hands on what the decoders wrote for the softmax
@@ -862,6 +858,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     bool ok = true;
     for (int seg = 0; ok && advance(wk, wk); ++seg) {
       const int32_t n = __shfl_sync(0xFFFFFFFFu, wk.n, 0), g = __shfl_sync(0xFFFFFFFFu, wk.g, 0);
+      live = kNQ == 1 || __shfl_sync(0xFFFFFFFFu, wk.seg.rt * kRows + qt * 128 < wk.seg.nq * a.group, 0);
       ok = wait(&sh.q_full[qt], seg & 1) && scores(g) && (n == 1 || scores(g + 1));
       for (int j = 0; j < n && ok; ++j) {
         const int x = g + j;
@@ -872,8 +869,10 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
         tc_fence_after();
         const uint32_t vb = v_lo + uint32_t(x % kSlots) * (T::kKvBytes >> 4), t_p = t_q + (x & 1) * kTK;
         if (elect_one()) {
+          if (live) {
 #pragma unroll
-          for (int t = 0; t < kTK; t += 16) mma_ts(t_o, t_p + t / 2, vb + t * 8, kIdO, j > 0 || t > 0);
+            for (int t = 0; t < kTK; t += 16) mma_ts(t_o, t_p + t / 2, vb + t * 8, kIdO, j > 0 || t > 0);
+          }
           tc_commit(&sh.v_empty[x % kSlots]);
           if constexpr (T::kApart) tc_commit(&sh.pv_done[qt]);
           if (j + 1 == n) tc_commit(&sh.o_full[qt]);

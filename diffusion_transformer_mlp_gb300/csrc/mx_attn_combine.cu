@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ Split
   const int32_t parts = worker_of(total, first + c.s.n - 1, workers) - (w - 1) + 1;
   const int32_t slot0 = worker_start(total, w - 1, workers) >= first - sp.edge ? 0 : 1;
   auto part_of = [&](int32_t i) { return int64_t(w - 1 + i) * 2 + (i == 0 ? slot0 : 0); };
+  if (c.rt * kRows + r >= c.nq * a.group) return;  // no row, and no partial of it
   // in one pass, against the maximum so far
   float f[8] = {}, l = 0.0f, m = -INFINITY;
 #pragma unroll 4

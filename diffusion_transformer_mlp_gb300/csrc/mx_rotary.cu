@@ -11,8 +11,7 @@
 //
 // A warp takes (a slice of) one token's heads.  Its lanes work out the token's
 // cosines and sines once, 32 pairs at a time, and pass them through shared
-// memory; then 32 / L heads go at a time, L = dim / 16 (to the next power of
-// two) lanes a head.  A lane holds two chunks of eight elements: in halves
+// memory; then 32 / L heads go at a time, L = dim / 16 lanes a head.  A lane holds two chunks of eight elements: in halves
 // pairs (i, i + rot / 2) chunk c and chunk c + rot / 16, so that both elements
 // of a pair meet in one lane without a shuffle; neighbours are in one chunk
 // anyway, and the chunks lie dim / 2 apart, so that the lanes of a load are
@@ -33,7 +32,7 @@ nvfp4_status check_cache(const mxfp4_cache* cache, int* page_shift, const std::s
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;  // small blocks, as warps end when their token does (256: 2% slower)
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxPairs = 128;
 
@@ -42,8 +41,9 @@ struct Rows {  // heads of one kind
   void* out;
   const void* weight;
   int64_t st, sh, o_st, o_sh;
+  int64_t step, o_step;  // strides of a warp's step: the heads that it takes at a time
   int32_t heads;
-  int32_t steps;  // of a warp: heads / (heads at a time), rounded up
+  int32_t steps;  // heads / (heads at a time), rounded up
 };
 
 struct RotaryParams {
@@ -51,9 +51,11 @@ struct RotaryParams {
   const int64_t* turns;
   const int32_t* axis;
   const int32_t* positions;
-  int32_t pairs, axes, dim, lane_bits;
+  int32_t pairs, axes, dim;
+  int32_t lanes, at_once;  // of a head; heads of a warp
   int32_t wide_weights;  // the weights are binary32, the heads are not
-  float eps;
+  int32_t weight_vec;    // 16-byte accesses to them are aligned
+  float eps, inv_dim;
   int64_t tokens;
   int32_t slices, per_slice;  // of a token's steps
   // of the cache
@@ -128,12 +130,11 @@ __device__ __forceinline__ void store_chunk(T* p, const float* f) {
 
 // kVec: 16-byte accesses to the heads are aligned.
 template <typename T, bool kCache, bool kNeighbours, bool kVec>
-__global__ void __launch_bounds__(kThreads) k_head_norm_rotary(const __grid_constant__ RotaryParams p) {
-  __shared__ float2 turned[kWarps][kMaxPairs];
-  __shared__ float most[kCache ? kWarps : 1][kCache ? 64 : 1];
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && !kCache ? 14 : 8) k_head_norm_rotary(const __grid_constant__ RotaryParams p) {
+  __shared__ __align__(16) float2 turned[kWarps][kMaxPairs];
+  __shared__ __align__(16) float most[kCache ? kWarps : 1][kCache ? 64 : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int lanes = 1 << p.lane_bits, at_once = 32 >> p.lane_bits, head_of = lane >> p.lane_bits,
-            s = lane & (lanes - 1);
+  const int lanes = p.lanes, at_once = p.at_once, head_of = lane / lanes, s = lane - head_of * lanes;
   const int64_t unit = int64_t(blockIdx.x) * kWarps + warp;
   grid_wait();
   if (unit >= p.tokens * p.slices) return;
@@ -150,144 +151,164 @@ __global__ void __launch_bounds__(kThreads) k_head_norm_rotary(const __grid_cons
     cb = s + eighth;
     if (s >= eighth) ca = 2 * s, cb = 2 * s + 1;  // behind the rotated ones: 2 eighth + 2 (s - eighth)
   }
-  const bool lane_in = 2 * s < chunks;
+  const bool lane_in = head_of < at_once;
+  const bool by_halves = (lanes & (lanes - 1)) == 0;
 
-  auto kind_of = [&](int32_t step) { return step < p.rows[0].steps ? 0 : (step < rotated || !kCache ? 1 : 2); };
-  auto head_at = [&](int32_t step, int kind) {
-    return (step - (kind > 0 ? p.rows[0].steps : 0) - (kind > 1 ? p.rows[1].steps : 0)) * at_once + head_of;
-  };
-  Chunk8<T> raw_a = {}, raw_b = {};
-  auto fetch = [&](int32_t step) {
-    const int kind = kind_of(step);
-    const Rows& r = p.rows[kind];
-    const int32_t head = head_at(step, kind);
-    if (lane_in && head < r.heads) {
-      const T* src = static_cast<const T*>(r.x) + token * r.st + head * r.sh;
-      raw_a = load_chunk<T, kVec>(src + 8 * ca);
-      raw_b = load_chunk<T, kVec>(src + 8 * cb);
-    }
-  };
-  if (first < end) fetch(first);
 
   // the token's cosines and sines
-  float c[8], n[8];
   if (first < rotated) {
-    for (int i = lane; i < p.pairs; i += 32) {
-      const int32_t ax = p.axis == nullptr ? 0 : min(max(p.axis[i], 0), p.axes - 1);
-      turned[warp][i] = turn_to_cos_sin(uint64_t(int64_t(p.positions[token * p.axes + ax])) * uint64_t(p.turns[i]));
+    for (int i = lane; i < p.dim / 2; i += 32) {
+      float2 t = make_float2(1.0f, 0.0f);  // behind the pairs nothing turns
+      if (i < p.pairs) {
+        const int32_t ax = p.axis == nullptr ? 0 : min(max(p.axis[i], 0), p.axes - 1);
+        t = turn_to_cos_sin(uint64_t(int64_t(p.positions[token * p.axes + ax])) * uint64_t(p.turns[i]));
+      }
+      turned[warp][i] = t;
     }
     __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      // halves: pair 8 s + j; neighbours: 4 of each chunk
-      const int pair = kNeighbours ? 4 * (j < 4 ? ca : cb) + (j & 3) : 8 * s + j;
-      const float2 t = lane_in && pair < p.pairs ? turned[warp][pair] : make_float2(1.0f, 0.0f);
-      c[j] = t.x, n[j] = t.y;
-    }
   }
-
   const int64_t slot = kCache ? p.slots[token] : 0;
   const bool held = kCache && slot >= 0 && slot < (p.pages << p.page_shift);
-  float w[16];
-  int have = -1;
-  for (int32_t step = first; step < end; ++step) {
-    const int kind = kind_of(step);
+
+  int32_t behind = 0;  // steps of the kinds before
+#pragma unroll
+  for (int kind = 0; kind < (kCache ? 3 : 2); ++kind) {  // unrolled, so that its fields are constants
     const Rows& r = p.rows[kind];
-    const int32_t head = head_at(step, kind);
-    const bool live = lane_in && head < r.heads;
-    float f[16];
-    unpack<T>(raw_a, f);
-    unpack<T>(raw_b, f + 8);
-    if (!live) {
+    const int32_t from = max(first - behind, 0), to = min(end - behind, r.steps);
+    behind += r.steps;
+    if (from >= to) continue;
+    int32_t head = from * at_once + head_of;
+    const T* src = static_cast<const T*>(r.x) + token * r.st + head * r.sh;
+    T* dst = static_cast<T*>(r.out) + token * r.o_st + head * r.o_sh;  // not used on the way into the cache
+    Chunk8<T> raw_a = {}, raw_b = {};
+    auto fetch = [&](bool there) {
+      if (lane_in && there) raw_a = load_chunk<T, kVec>(src + 8 * ca), raw_b = load_chunk<T, kVec>(src + 8 * cb);
+      src += r.step;
+    };
+    fetch(head < r.heads);
+    // (a, b) -> a (wa cos, wa sin) + b (-wb sin, wb cos)
+    uint64_t of_a[8], of_b[8];
+    const bool norm = r.weight != nullptr;
+    if (!kCache || kind < 2) {
+      float w[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) f[i] = 0.0f;
-    }
-    if (step + 1 < end) fetch(step + 1);
-    if (kind < 2) {
-      if (r.weight != nullptr) {
-        if (have != kind) {
-          have = kind;
-          if (lane_in) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int at = 8 * (i < 8 ? ca : cb) + (i & 7);
-              w[i] = p.wide_weights ? static_cast<const float*>(r.weight)[at] : to_f32(static_cast<const T*>(r.weight)[at]);
-            }
+      for (int i = 0; i < 16; ++i) w[i] = 1.0f;
+      if (norm && lane_in) {
+        auto load = [&](auto vec) {
+          constexpr bool kV = decltype(vec)::value;
+          if (p.wide_weights) {
+            const float* src = static_cast<const float*>(r.weight);
+            unpack<float>(load_chunk<float, kV>(src + 8 * ca), w);
+            unpack<float>(load_chunk<float, kV>(src + 8 * cb), w + 8);
+          } else {
+            const T* src = static_cast<const T*>(r.weight);
+            unpack<T>(load_chunk<T, kV>(src + 8 * ca), w);
+            unpack<T>(load_chunk<T, kV>(src + 8 * cb), w + 8);
           }
-        }
-        auto mean = [&]() {
-          float sum = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) sum = fmaf(f[i], f[i], sum);
-          for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-          return sum / float(p.dim);
         };
-        float m = mean(), eps = p.eps;
-        // squares past the range: 2^-72 of the elements has them within it
-        const bool over = __isinff(m);
-        if (__any_sync(0xFFFFFFFFu, over)) {
-          if (over) {
-            eps = 0.0f;
+        if (p.weight_vec) load(std::true_type{});
+        else load(std::false_type{});
+      }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] *= 0x1p-72f;
+      for (int j = 0; j < 8; ++j) {
+        // halves: pair 8 s + j; neighbours: four of each chunk
+        const float2 t = turned[warp][kNeighbours ? 4 * (j < 4 ? ca : cb) + (j & 3) : 8 * s + j];
+        const float wa = w[kNeighbours ? 2 * j : j], wb = w[kNeighbours ? 2 * j + 1 : 8 + j];
+        of_a[j] = pair_of(wa * t.x, wa * t.y), of_b[j] = pair_of(-wb * t.y, wb * t.x);
+      }
+    }
+#pragma unroll 1
+    for (int32_t step = from; step < to; ++step, head += at_once, dst += r.o_step) {
+      const bool live = lane_in && head < r.heads;  // the others go along with what they have
+      float f[16];
+      unpack<T>(raw_a, f);
+      unpack<T>(raw_b, f + 8);
+      if (step + 1 < to) fetch(head + at_once < r.heads);
+      if (!kCache || kind < 2) {
+        if (norm) {
+          auto mean = [&]() {
+            uint64_t sum2 = 0;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const uint64_t x = pair_of(f[i], f[i + 1]);
+              sum2 = fma2(x, x, sum2);
+            }
+            float sum = unpair(sum2).x + unpair(sum2).y;
+            if (by_halves) {
+#pragma unroll
+              for (int o = 1; o < 16; o <<= 1)
+                if (o < lanes) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            } else {
+              const float mine = sum;
+              sum = 0.0f;
+              for (int o = 0; o < lanes; ++o) sum += __shfl_sync(0xFFFFFFFFu, mine, head_of * lanes + o);
+            }
+            return sum * p.inv_dim;
+          };
+          float m = mean(), eps = p.eps;
+          // squares past the range: 2^-72 of the elements has them within it
+          const bool over = __isinff(m);
+          if (__any_sync(0xFFFFFFFFu, over)) {
+            if (over) {
+              eps = 0.0f;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) f[i] *= 0x1p-72f;
+            }
+            m = mean();
           }
-          m = mean();
-        }
-        const float inv = rsqrtf(m + eps);
+          const float inv = rsqrtf(m + eps);
+          const uint64_t inv2 = pair_of(inv, inv);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = f[i] * inv * w[i];
-      }
-      if (kNeighbours) {
+          for (int i = 0; i < 16; i += 2) {
+            const float2 x = unpair(mul2(pair_of(f[i], f[i + 1]), inv2));
+            f[i] = x.x, f[i + 1] = x.y;
+          }
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float a = f[2 * j], b = f[2 * j + 1];
-          f[2 * j] = a * c[j] - b * n[j], f[2 * j + 1] = b * c[j] + a * n[j];
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float a = f[j], b = f[8 + j];
-          f[j] = a * c[j] - b * n[j], f[8 + j] = b * c[j] + a * n[j];
+          float& a = f[kNeighbours ? 2 * j : j];
+          float& b = f[kNeighbours ? 2 * j + 1 : 8 + j];
+          const float2 y = unpair(fma2(pair_of(a, a), of_a[j], mul2(pair_of(b, b), of_b[j])));
+          a = y.x, b = y.y;
         }
       }
-    }
-    if (!kCache || kind == 0) {
-      if (live) {
-        T* dst = static_cast<T*>(r.out) + token * r.o_st + head * r.o_sh;
-        store_chunk<T, kVec>(dst + 8 * ca, f);
-        store_chunk<T, kVec>(dst + 8 * cb, f + 8);
-      }
-      continue;
-    }
-    if constexpr (kCache) {
-      float ma = 0.0f, mb = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ma = max_nan(ma, fabsf(f[i])), mb = max_nan(mb, fabsf(f[8 + i]));
-      float* row = most[warp] + head_of * chunks;  // dim is 16 times the lanes here
-      row[ca] = ma, row[cb] = mb;
-      __syncwarp();
-      const int64_t at = ((((slot >> p.page_shift) * p.kv_heads) + head) << p.page_shift) +
-                         (slot & ((int64_t(1) << p.page_shift) - 1));
-      uint8_t* codes = kind == 1 ? p.k_codes : p.v_codes;
-      uint8_t* scales = kind == 1 ? p.k_scales : p.v_scales;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int ch = h ? cb : ca;
-        const float4 m4 = *reinterpret_cast<const float4*>(row + (ch & ~3));
-        const float am = max_nan(max_nan(m4.x, m4.y), max_nan(m4.z, m4.w));
-        const uint32_t eb = (__float_as_uint(am) >> 23) & 0xFFu;
-        const uint32_t e = eb == 255u ? 255u : (eb > 2u ? eb - 2u : 0u);
-        const float inv = __uint_as_float((254u - min(e, 252u)) << 23);
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = f[8 * h + i] * inv;
-        const uint32_t q = eb == 255u ? 0u : e2m1x8(y);
-        if (live && held) {
-          *reinterpret_cast<uint32_t*>(codes + at * (p.dim / 2) + ch * 4) = q;
-          if ((ch & 3) == 0) scales[at * (p.dim / 32) + (ch >> 2)] = uint8_t(e);
+      if (!kCache || kind == 0) {
+        if (live) {
+          store_chunk<T, kVec>(dst + 8 * ca, f);
+          store_chunk<T, kVec>(dst + 8 * cb, f + 8);
         }
+        continue;
       }
-      __syncwarp();  // the maxima are read
+      if constexpr (kCache) {
+        float ma = 0.0f, mb = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ma = max_nan(ma, fabsf(f[i])), mb = max_nan(mb, fabsf(f[8 + i]));
+        float* row = most[warp] + head_of * chunks;  // dim is 16 times the lanes here
+        row[ca] = ma, row[cb] = mb;
+        __syncwarp();
+        const int64_t at = ((((slot >> p.page_shift) * p.kv_heads) + head) << p.page_shift) +
+                           (slot & ((int64_t(1) << p.page_shift) - 1));
+        uint8_t* codes = kind == 1 ? p.k_codes : p.v_codes;
+        uint8_t* scales = kind == 1 ? p.k_scales : p.v_scales;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int ch = h ? cb : ca;
+          const float4 m4 = *reinterpret_cast<const float4*>(row + (ch & ~3));
+          const float am = max_nan(max_nan(m4.x, m4.y), max_nan(m4.z, m4.w));
+          const uint32_t eb = (__float_as_uint(am) >> 23) & 0xFFu;
+          const uint32_t e = eb == 255u ? 255u : (eb > 2u ? eb - 2u : 0u);
+          const float inv = __uint_as_float((254u - min(e, 252u)) << 23);
+          float y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = f[8 * h + i] * inv;
+          const uint32_t q = eb == 255u ? 0u : e2m1x8(y);
+          if (live && held) {
+            *reinterpret_cast<uint32_t*>(codes + at * (p.dim / 2) + ch * 4) = q;
+            if ((ch & 3) == 0) scales[at * (p.dim / 32) + (ch >> 2)] = uint8_t(e);
+          }
+        }
+        __syncwarp();  // the maxima are read
+      }
     }
   }
 }
@@ -297,8 +318,11 @@ __global__ void __launch_bounds__(kThreads) k_head_norm_rotary(const __grid_cons
 nvfp4_status launch_rotary(RotaryParams& p, int32_t dtype, int32_t weight_dtype, bool cache, bool neighbours, bool vec,
                            cudaStream_t s) {
   int32_t steps = 0;
-  const int at_once = 32 >> p.lane_bits;
-  for (Rows& r : p.rows) r.steps = (r.heads + at_once - 1) / at_once, steps += r.steps;
+  for (Rows& r : p.rows) {
+    r.steps = (r.heads + p.at_once - 1) / p.at_once;
+    r.step = p.at_once * r.sh, r.o_step = p.at_once * r.o_sh;
+    steps += r.steps;
+  }
   const int64_t want = int64_t(sm_count()) * 16;
   int64_t slices = (want + p.tokens - 1) / p.tokens;
   slices = slices > steps ? steps : slices;
@@ -318,6 +342,8 @@ nvfp4_status launch_rotary(RotaryParams& p, int32_t dtype, int32_t weight_dtype,
     }
     return launch("launch k_head_norm_rotary", kern, dim3(unsigned(blocks)), dim3(kThreads), 0, 0, s, p);
   };
+  p.weight_vec = 1;
+  for (const Rows& r : p.rows) p.weight_vec = p.weight_vec && aligned16(r.weight);
   p.wide_weights = weight_dtype == MXFP4_FP32 && dtype != MXFP4_FP32;
   if (dtype == MXFP4_FP32) return go(float());
   return dtype == MXFP4_BF16 ? go(__nv_bfloat16()) : go(__half());
@@ -345,9 +371,8 @@ nvfp4_status check_rotary(const mxfp4_rotary* rotary, int32_t dtype, int32_t wei
     return fail(NVFP4_EALIGN, nm + ": turns, axis and positions must be aligned to their elements");
   p.turns = rotary->turns, p.axis = rotary->axis, p.positions = rotary->positions;
   p.pairs = rotary->pairs, p.axes = rotary->axes;
-  p.dim = dim, p.eps = eps, p.tokens = tokens;
-  p.lane_bits = 0;
-  while ((16 << p.lane_bits) < dim) ++p.lane_bits;
+  p.dim = dim, p.inv_dim = 1.0f / float(dim), p.eps = eps, p.tokens = tokens;
+  p.lanes = dim / 16, p.at_once = 32 / p.lanes;
   return NVFP4_OK;
 }
 
@@ -358,7 +383,7 @@ nvfp4_status check_rows(const mxfp4_heads* h, int32_t dtype, int32_t weight_dtyp
   if (reinterpret_cast<uintptr_t>(h->x) % es != 0 || reinterpret_cast<uintptr_t>(h->weight) % ws != 0 ||
       (out && reinterpret_cast<uintptr_t>(h->out) % es != 0))
     return fail(NVFP4_EALIGN, nm + ": heads and weights must be aligned to their elements");
-  r = {h->x, out ? h->out : nullptr, h->weight, h->st, h->sh, h->o_st, h->o_sh, h->heads, 0};
+  r = {h->x, out ? h->out : nullptr, h->weight, h->st, h->sh, h->o_st, h->o_sh, 0, 0, h->heads, 0};
   const int64_t el = int64_t(16 / es);
   vec = vec && aligned16(h->x) && h->st % el == 0 && h->sh % el == 0;
   if (out) vec = vec && aligned16(h->out) && h->o_st % el == 0 && h->o_sh % el == 0;

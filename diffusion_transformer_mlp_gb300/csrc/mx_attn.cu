@@ -31,6 +31,8 @@ namespace {
 bool many_rows(int32_t dim, int64_t rows) { return rows > (dim == 256 ? 16 : 64); }
 }  // namespace
 
+bool attn_has_many_rows(int32_t dim, int64_t rows) { return many_rows(dim, rows); }
+
 }  // namespace nvfp4
 
 using namespace nvfp4;
@@ -83,6 +85,7 @@ nvfp4_status attn_params(const mxfp4_cache* cache, const mxfp4_attention* args, 
   p.q_st = g.q_st, p.q_sh = g.q_sh, p.o_st = g.o_st, p.o_sh = g.o_sh, p.table_ld = g.table_ld;
   p.pages = cache->pages;
   p.page_shift = sh, p.kv_heads = cache->kv_heads, p.group = int32_t(group), p.seqs = g.seqs, p.total_q = g.total_q;
+  p.q_rows = g.total_q;
   p.bf16 = g.dtype == MXFP4_BF16, p.causal = g.causal != 0, p.window = g.window, p.sinks = g.sinks;
   // A window that reaches from a query (at -2^24 or later) past every key hides
   // none; smaller ones leave the kernels' differences of positions in 32 bits.

@@ -27,6 +27,7 @@ struct AttnParams {
   int64_t q_st, q_sh, o_st, o_sh, table_ld;
   int64_t pages;
   int32_t page_shift, kv_heads, group, seqs, total_q;
+  int32_t q_rows;        // of q; output row i >= q_rows is of query i - q_rows (see mx_attn_shared.cu)
   int32_t bf16, causal, window, sinks;
   int32_t q_vec, o_vec;  // 16-byte accesses to q / out are aligned
   int32_t o_f32;         // out is binary32 whatever q is, and 16-byte accesses are aligned (a part, to be joined)
@@ -109,6 +110,11 @@ __device__ __forceinline__ int32_t seq_start(const AttnParams& a, int32_t b) {
 }
 __device__ __forceinline__ int32_t seq_queries(const AttnParams& a, int32_t b) {
   return a.q_starts != nullptr ? max(min(a.q_starts[b + 1], a.total_q) - seq_start(a, b), 0) : 1;
+}
+
+// The row of q for output row i.
+__device__ __forceinline__ int64_t query_row(const AttnParams& a, int32_t i) {
+  return i < a.q_rows ? i : i - a.q_rows;
 }
 
 // Span of row tile rt (rows [rt * rows, ...) of the nq * group rows).
@@ -439,7 +445,7 @@ __device__ __forceinline__ void wide_row(const AttnParams& a, const Cursor& cu, 
   const int lane = threadIdx.x & 31;
   const int32_t qi = row / a.group, hq = cu.h * a.group + row - qi * a.group, pos = cu.len - cu.nq + qi;
   const int32_t end = a.causal ? min(cu.len, pos + 1) : cu.len, from = a.window > 0 ? pos - a.window + 1 : 0;
-  const uint16_t* q = static_cast<const uint16_t*>(a.q) + int64_t(cu.q0 + qi) * a.q_st + int64_t(hq) * a.q_sh;
+  const uint16_t* q = static_cast<const uint16_t*>(a.q) + query_row(a, cu.q0 + qi) * a.q_st + int64_t(hq) * a.q_sh;
   float qv[C];  // element 32 c + lane
   float o[C];   // column C lane + c
 #pragma unroll
@@ -592,6 +598,7 @@ nvfp4_status attn_join(int dim, int tok, const SplitParams& sp, cudaStream_t str
 // mx_attn.cu: the kernel for the rows that there may be, and its workspace.
 nvfp4_status attn_run(const mxfp4_cache* cache, const AttnParams& p, int32_t max_queries, void* workspace,
                       cudaStream_t stream);
+bool attn_has_many_rows(int32_t dim, int64_t rows);  // k_attn_chunk's rather than k_attn_stream's
 // What an entry point of that name checks of its arguments; the parameters they give.
 nvfp4_status attn_params(const mxfp4_cache* cache, const mxfp4_attention* args, int64_t workspace_bytes,
                          const std::string& nm, AttnParams& p);

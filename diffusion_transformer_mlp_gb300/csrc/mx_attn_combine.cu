@@ -118,16 +118,22 @@ __global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_c
         l == 0.0f ? -INFINITY : (row_m[r] + kJoinLog2 - kWeightLog2 + log2f(l)) * 0.6931471805599453f;
 }
 
-// The same for segments of 128 or 256 rows.  Of those few are split, at most
-// one for each boundary between two workers' runs: block y takes the segment
-// that worker y's run starts inside of, if no run before does so too.  A
-// thread is a row and eight columns.  Blocks behind those write the row tiles
-// that see no key: the first ones of a sequence that has fewer keys than queries.
+// The same for segments of 128 or 256 rows.  Of those few are split, at the
+// boundaries between two workers' runs: blocks (x, w) are for the segment that
+// worker w's run starts inside of, whose columns they share with the blocks of
+// the other runs that start inside of it.  A thread is a row and eight columns
+// at a time.  (Blocks of all columns for the first of these runs, which left the
+// others' without work: 9.5 us for 19 partials of 16 segments, so XX.)  Blocks
+// behind those write the row tiles that see no key: the first ones of a sequence
+// that has fewer keys than queries.
+constexpr int kJoinBlocks = 4;  // for each worker
+
 template <int D, int kRows>
 __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ SplitParams sp, int32_t tok) {
+  constexpr int kCols = 256 / kRows * 8;  // of a block at a time
   const AttnParams& a = sp.a;
-  const int32_t r = threadIdx.x % kRows, d = (int(blockIdx.x) * (256 / kRows) + int(threadIdx.x) / kRows) * 8;
-  auto write = [&](const Cursor& c, const float (&f)[8], float lse) {
+  const int32_t r = threadIdx.x % kRows, d0 = int32_t(threadIdx.x) / kRows * 8;
+  auto write = [&](const Cursor& c, int32_t d, const float (&f)[8], float lse) {
     const int32_t row = c.rt * kRows + r;
     if (row >= c.nq * a.group) return;
     const int32_t qi = row / a.group, hq = c.h * a.group + row - qi * a.group;
@@ -142,37 +148,42 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ Split
     cursor_seq(c, a);
     const float zero[8] = {};
     for (c.rt = 0; c.rt * kRows < c.nq * a.group && row_span(a, c.len, c.nq, c.rt, kRows, tok).n == 0; ++c.rt)
-      for (c.h = 0; c.h < a.kv_heads; ++c.h) write(c, zero, -INFINITY);
+      for (c.h = 0; c.h < a.kv_heads; ++c.h)
+        for (int32_t d = int32_t(blockIdx.x) * kCols; d < D; d += kJoinBlocks * kCols) write(c, d + d0, zero, -INFINITY);
     return;
   }
   const int64_t total = sp.prefix[a.seqs];
   const int32_t workers = live_workers(sp, total);
   if (w == 0 || w >= workers) return;
   c = sp.start[w];
-  const int64_t first = worker_start(total, w, workers) - c.t;  // place of the segment's first tile
-  if (c.t == 0 || worker_start(total, w - 1, workers) > first) return;
-  const int32_t parts = worker_of(total, first + c.s.n - 1, workers) - (w - 1) + 1;
-  const int32_t slot0 = worker_start(total, w - 1, workers) >= first - sp.edge ? 0 : 1;
-  auto part_of = [&](int32_t i) { return int64_t(w - 1 + i) * 2 + (i == 0 ? slot0 : 0); };
+  if (c.t == 0) return;  // its run starts with the segment
   if (c.rt * kRows + r >= c.nq * a.group) return;  // no row, and no partial of it
-  // in one pass, against the maximum so far
-  float f[8] = {}, l = 0.0f, m = -INFINITY;
+  const int64_t first = worker_start(total, w, workers) - c.t;  // place of the segment's first tile
+  const int32_t begin = worker_of(total, first, workers);
+  const int32_t parts = worker_of(total, first + c.s.n - 1, workers) - begin + 1;
+  const int32_t slot0 = worker_start(total, begin, workers) >= first - sp.edge ? 0 : 1;
+  auto part_of = [&](int32_t i) { return int64_t(begin + i) * 2 + (i == 0 ? slot0 : 0); };
+  const int32_t mine = (w - begin - 1) * kJoinBlocks + int32_t(blockIdx.x), all = (parts - 1) * kJoinBlocks;
+  for (int32_t d = mine * kCols + d0; d < D; d += all * kCols) {
+    // in one pass, against the maximum so far
+    float f[8] = {}, l = 0.0f, m = -INFINITY;
 #pragma unroll 4
-  for (int32_t i = 0; i < parts; ++i) {
-    const float2 ml = sp.part_ml[part_of(i) * kRows + r];
-    const float4* src = reinterpret_cast<const float4*>(sp.part_o) + (part_of(i) * (D / 4) + d / 4) * kRows + r;
-    const float4 u = src[0], v = src[kRows];
-    const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.0f : top + kJoinLog2;
-    const float old = top == -INFINITY ? 1.0f : exp2_approx(m - top), g = exp2_approx(ml.x - ref);
-    m = top;
-    l = l * old + ml.y * g;
-    f[0] = f[0] * old + u.x * g, f[1] = f[1] * old + u.y * g, f[2] = f[2] * old + u.z * g, f[3] = f[3] * old + u.w * g;
-    f[4] = f[4] * old + v.x * g, f[5] = f[5] * old + v.y * g, f[6] = f[6] * old + v.z * g, f[7] = f[7] * old + v.w * g;
-  }
-  const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+    for (int32_t i = 0; i < parts; ++i) {
+      const float2 ml = sp.part_ml[part_of(i) * kRows + r];
+      const float4* src = reinterpret_cast<const float4*>(sp.part_o) + (part_of(i) * (D / 4) + d / 4) * kRows + r;
+      const float4 u = src[0], v = src[kRows];
+      const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.0f : top + kJoinLog2;
+      const float old = top == -INFINITY ? 1.0f : exp2_approx(m - top), g = exp2_approx(ml.x - ref);
+      m = top;
+      l = l * old + ml.y * g;
+      f[0] = f[0] * old + u.x * g, f[1] = f[1] * old + u.y * g, f[2] = f[2] * old + u.z * g, f[3] = f[3] * old + u.w * g;
+      f[4] = f[4] * old + v.x * g, f[5] = f[5] * old + v.y * g, f[6] = f[6] * old + v.z * g, f[7] = f[7] * old + v.w * g;
+    }
+    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] *= inv;
-  write(c, f, l == 0.0f ? -INFINITY : (m + kJoinLog2 - kWeightLog2 + log2f(l)) * 0.6931471805599453f);
+    for (int k = 0; k < 8; ++k) f[k] *= inv;
+    write(c, d, f, l == 0.0f ? -INFINITY : (m + kJoinLog2 - kWeightLog2 + log2f(l)) * 0.6931471805599453f);
+  }
 }
 
 template <int D, int kRows>
@@ -186,7 +197,7 @@ nvfp4_status combine_launch(int tok, int row_tiles, const SplitParams& sp, cudaS
 template <int D, int kRows>
 nvfp4_status join_launch(int tok, const SplitParams& sp, cudaStream_t stream) {
   return launch("launch k_attn_join", k_attn_join<D, kRows>,
-                dim3(unsigned(D * kRows / (8 * 256)), unsigned(sp.workers + sp.a.seqs)), dim3(256), 0, 0, stream, sp,
+                dim3(unsigned(kJoinBlocks), unsigned(sp.workers + sp.a.seqs)), dim3(256), 0, 0, stream, sp,
                 int32_t(tok));
 }
 

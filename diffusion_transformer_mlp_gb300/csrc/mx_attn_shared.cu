@@ -13,7 +13,11 @@
 // pages, hence the prefix is rounded down to them.
 //
 // k_shared_parts writes the two sets of lengths and tables, attention runs for
-// each with binary32 outputs, and k_shared_join joins them.
+// each with binary32 outputs, and k_shared_join joins them.  Where both parts are
+// k_attn_stream's and every sequence has one query, which sees all keys of either
+// part, both sets are one list of sequences for one launch: rows total_q and
+// above of the outputs are the own tokens' (4 samples of a prompt of 2,049
+// tokens: 32.1 us in two launches, so XX).
 #include <algorithm>
 #include <string>
 
@@ -29,11 +33,11 @@ struct SharedParams {
   const int32_t* groups;
   const int32_t* shared;
   int32_t count;
-  // of the groups' prefixes, of the sequences' own tokens
-  int32_t *table1, *lens1, *starts1;
-  int32_t *table2, *lens2;
+  // The groups' prefixes, one sequence of no keys for the queries behind them, and
+  // the sequences' own tokens: count + 1 + seqs sequences.
+  int32_t *table, *lens, *starts;
   int32_t* before;  // [seqs] tokens of the prefix
-  float *o1, *o2, *l1, *l2;
+  float *o, *l;     // [2 * total_q] rows: of the prefixes, of the own tokens
 };
 
 __device__ __forceinline__ int32_t group_start(const SharedParams& p, int32_t g) {
@@ -66,16 +70,17 @@ __global__ void __launch_bounds__(kThreads) k_shared_parts(const __grid_constant
   if (int32_t(blockIdx.x) < p.count) {
     const int32_t g = blockIdx.x, s0 = group_start(p, g), n = prefix_of(p, g, red);
     if (threadIdx.x == 0) {
-      p.lens1[g] = n;
-      p.starts1[g] = s0 < a.seqs ? seq_start(a, s0) : a.total_q;
+      p.lens[g] = n;
+      p.starts[g] = s0 < a.seqs ? seq_start(a, s0) : a.total_q;
       if (g + 1 == p.count) {
         const int32_t s1 = max(group_start(p, p.count), s0);
-        // of the queries of the last sequence, the rows behind which may be nobody's
-        p.starts1[p.count] = s1 > 0 ? seq_start(a, s1 - 1) + seq_queries(a, s1 - 1) : 0;
+        // behind the queries of the last sequence of a group
+        p.starts[p.count] = s1 > 0 ? seq_start(a, s1 - 1) + seq_queries(a, s1 - 1) : 0;
+        p.lens[p.count] = 0;
       }
     }
     const int32_t* src = a.table + s0 * a.table_ld;
-    for (int32_t i = threadIdx.x; i < n >> a.page_shift; i += kThreads) p.table1[g * a.table_ld + i] = src[i];
+    for (int32_t i = threadIdx.x; i < n >> a.page_shift; i += kThreads) p.table[g * a.table_ld + i] = src[i];
     return;
   }
   const int32_t b = int32_t(blockIdx.x) - p.count;
@@ -91,10 +96,15 @@ __global__ void __launch_bounds__(kThreads) k_shared_parts(const __grid_constant
     n = min(n, max(a.lens[b], 0) & ~((1 << a.page_shift) - 1));  // without queries it limits nothing
   }
   const int32_t len = a.lens[b] - n;
-  if (threadIdx.x == 0) p.before[b] = n, p.lens2[b] = len;
+  const int32_t own = p.count + 1 + b;
+  if (threadIdx.x == 0) {
+    p.before[b] = n, p.lens[own] = len;
+    p.starts[own] = a.total_q + seq_start(a, b);
+    if (b + 1 == a.seqs) p.starts[own + 1] = a.total_q + seq_start(a, b) + seq_queries(a, b);
+  }
   const int64_t skip = n >> a.page_shift, most = a.table_ld - skip;
   const int64_t pages = min((int64_t(max(len, 0)) + (int64_t(1) << a.page_shift) - 1) >> a.page_shift, most);
-  for (int64_t i = threadIdx.x; i < pages; i += kThreads) p.table2[b * a.table_ld + i] = a.table[b * a.table_ld + skip + i];
+  for (int64_t i = threadIdx.x; i < pages; i += kThreads) p.table[own * a.table_ld + i] = a.table[b * a.table_ld + skip + i];
 }
 
 // Eight columns of a row and head a thread; the rows of sequence blockIdx.x.
@@ -108,13 +118,14 @@ __global__ void __launch_bounds__(kThreads) k_shared_join(const __grid_constant_
   for (int64_t i = int64_t(blockIdx.y) * kThreads + threadIdx.x; i < items; i += int64_t(gridDim.y) * kThreads) {
     const int64_t rh = q0 * heads + i / (D / 8);  // (row, head)
     const int32_t d = int32_t(i % (D / 8)) * 8;
-    const float l2 = p.l2[rh], l1 = prefix ? p.l1[rh] : -INFINITY;
-    const float4* s2 = reinterpret_cast<const float4*>(p.o2 + rh * D + d);
+    const int64_t own = int64_t(a.total_q) * heads + rh;
+    const float l2 = p.l[own], l1 = prefix ? p.l[rh] : -INFINITY;
+    const float4* s2 = reinterpret_cast<const float4*>(p.o + own * D + d);
     float4 u = s2[0], v = s2[1];
     float f[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
     float lse = l2;
     if (prefix) {
-      const float4* s1 = reinterpret_cast<const float4*>(p.o1 + rh * D + d);
+      const float4* s1 = reinterpret_cast<const float4*>(p.o + rh * D + d);
       u = s1[0], v = s1[1];
       const float g[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
       const float m = fmaxf(l1, l2), ref = m == -INFINITY ? 0.0f : m;
@@ -141,15 +152,11 @@ int64_t layout(SharedParams& p, uint8_t* ws, int64_t attention, int64_t rows, in
     ptr = reinterpret_cast<std::remove_reference_t<decltype(ptr)>>(ws + at);
     at += align256(n * 4);
   };
-  take(p.o1, rows * heads * dim);
-  take(p.o2, rows * heads * dim);
-  take(p.l1, rows * heads);
-  take(p.l2, rows * heads);
-  take(p.table1, p.count * table_ld);
-  take(p.lens1, p.count);
-  take(p.starts1, p.count + 1);
-  take(p.table2, seqs * table_ld);
-  take(p.lens2, seqs);
+  take(p.o, 2 * rows * heads * dim);
+  take(p.l, 2 * rows * heads);
+  take(p.table, (p.count + 1 + seqs) * table_ld);
+  take(p.lens, p.count + 1 + seqs);
+  take(p.starts, p.count + 2 + seqs);
   take(p.before, seqs);
   return at;
 }
@@ -190,7 +197,8 @@ extern "C" nvfp4_status mxfp4_cache_attention_shared(const mxfp4_cache* cache, c
   if (!shared->groups || !shared->shared) return fail(NVFP4_EINVAL, nm + ": null pointer");
   if (reinterpret_cast<uintptr_t>(shared->groups) % 4 != 0 || reinterpret_cast<uintptr_t>(shared->shared) % 4 != 0)
     return fail(NVFP4_EALIGN, nm + ": groups and shared must be aligned to their elements");
-  if (int64_t(max_group) * p.a.group > (int64_t(1) << 24) || int64_t(shared->count) + args->seqs > 0x7FFFFFFF)
+  if (int64_t(max_group) * p.a.group > (int64_t(1) << 24) || int64_t(shared->count) + args->seqs > 0x7FFFFF00 ||
+      args->total_q > 0x3FFFFFFF)
     return fail(NVFP4_EUNSUPPORTED, nm + ": problem too large");
   const int64_t heads = args->q_heads;
   const int32_t dim = cache->dim;
@@ -205,16 +213,24 @@ extern "C" nvfp4_status mxfp4_cache_attention_shared(const mxfp4_cache* cache, c
   AttnParams part = p.a;
   part.o_f32 = 1, part.o_vec = 1;
   part.o_st = heads * dim, part.o_sh = dim;
-  part.out = p.o1, part.lse = p.l1;
-  part.table = p.table1, part.lens = p.lens1, part.q_starts = p.starts1;
-  part.seqs = p.count, part.causal = 0;
-  st = attn_run(cache, part, max_group, args->workspace, s);
-  if (st != NVFP4_OK) return st;
-  part.out = p.o2, part.lse = p.l2;
-  part.table = p.table2, part.lens = p.lens2, part.q_starts = args->q_starts;
-  part.seqs = args->seqs, part.causal = p.a.causal;
-  st = attn_run(cache, part, args->max_queries, args->workspace, s);
-  if (st != NVFP4_OK) return st;
+  part.out = p.o, part.lse = p.l;
+  part.table = p.table, part.lens = p.lens, part.q_starts = p.starts;
+  part.causal = 0;
+  if (args->max_queries == 1 && !attn_has_many_rows(dim, int64_t(max_group) * part.group)) {
+    part.seqs = p.count + 1 + args->seqs, part.total_q = 2 * args->total_q;
+    st = attn_run(cache, part, max_group, args->workspace, s);
+    if (st != NVFP4_OK) return st;
+  } else {
+    part.seqs = p.count;
+    st = attn_run(cache, part, max_group, args->workspace, s);
+    if (st != NVFP4_OK) return st;
+    part.out = p.o + args->total_q * heads * dim, part.lse = p.l + args->total_q * heads;
+    part.table = p.table + (p.count + 1) * args->table_ld, part.lens = p.lens + p.count + 1;
+    part.q_starts = args->q_starts;
+    part.seqs = args->seqs, part.causal = p.a.causal;
+    st = attn_run(cache, part, args->max_queries, args->workspace, s);
+    if (st != NVFP4_OK) return st;
+  }
   const int64_t items = args->max_queries * heads * (dim / 8);
   const unsigned y = unsigned(std::min<int64_t>((items + kThreads - 1) / kThreads, 1024));
   auto join = dim == 64 ? k_shared_join<64> : (dim == 128 ? k_shared_join<128> : k_shared_join<256>);

@@ -291,7 +291,8 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows, kSeveral>::kCtas)
       const int32_t pos = cu.len - cu.nq + qi;
       end[r] = a.causal ? min(cu.len, pos + 1) : cu.len;
       from[r] = a.window > 0 ? pos - a.window + 1 : 0;
-      const uint16_t* src = static_cast<const uint16_t*>(a.q) + int64_t(cu.q0 + qi) * a.q_st + int64_t(hq) * a.q_sh;
+      const uint16_t* src =
+          static_cast<const uint16_t*>(a.q) + query_row(a, cu.q0 + qi) * a.q_st + int64_t(hq) * a.q_sh;
       float am = 0.0f;
 #pragma unroll
       for (int pass = 0; pass < 2; ++pass) {  // the row's largest element, then its fragments

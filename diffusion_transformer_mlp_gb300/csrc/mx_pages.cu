@@ -45,15 +45,25 @@ struct PagesParams {
   // workspace
   int64_t* need;     // [rows + 1] pages that the rows before need; of select: new lengths as int32
   int64_t* tokens;   // [rows + 1] new tokens of the rows before
-  int64_t* part;     // [kCluster + 1] free or held pages of the parts
+  int64_t* part;     // of compact: held pages below their number
   int32_t* list;     // [pages] free ids in order; of compact: held ids in order
   int32_t* writers;  // [pages] rows that go on in a shared page; of compact: holes in order
   int32_t* lowest;   // [pages] the first of them; of compact: where a page goes
   int32_t* taken;    // [rows, table_ld] of select
 };
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
+}
+// The same place in the shared memory of block `rank` of the cluster.
+__device__ __forceinline__ void store_there(int64_t* mine, int rank, int64_t v) {
+  asm volatile("{\n\t.reg .b32 there;\n\tmapa.shared::cluster.u32 there, %0, %1;\n\t"
+               "st.shared::cluster.b64 [there], %2;\n\t}" ::"r"(smem_u32(mine)),
+               "r"(rank), "l"(v)
+               : "memory");
 }
 
 // Pages of a row of `len` tokens.
@@ -98,25 +108,40 @@ __device__ __forceinline__ int32_t count_piece(const PagesParams& p, const Piece
   for (int64_t i = w.lo + lane; i < w.hi; i += 32) n += (p.refs[i] > 0) == want_held;
   return __reduce_add_sync(0xFFFFFFFFu, n);
 }
-// The pieces' counts: the ones before this warp's of the block (its own total to
-// part[rank]); the other blocks' are there behind the next cluster barrier.
-__device__ __forceinline__ int64_t before_in_block(const PagesParams& p, int32_t mine, int rank, int64_t* shared) {
+// Ranks over the pool: `n` are in this warp's piece.  Returns those in the pieces
+// before it; `all` gets the pool's.  The blocks push their sums into one another's
+// shared memory (a round through L2 took 1.2 us instead of 0.4); they have arrived
+// at the cluster's barrier once before, so that all are there.
+struct Ranks {
+  int64_t warp[kWarps], block[kCluster];
+};
+__device__ __forceinline__ int64_t rank_pieces(int32_t n, int rank, Ranks& r, int64_t& all) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) shared[warp] = mine;
+  if (lane == 0) r.warp[warp] = n;
   __syncthreads();
+  cluster_wait();
   if (warp == 0) {
-    const int64_t v = shared[lane];
+    const int64_t v = r.warp[lane];
     int64_t upto = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t u = __shfl_up_sync(0xFFFFFFFFu, upto, o);
       if (lane >= o) upto += u;
     }
-    shared[lane] = upto - v;
-    if (lane == 31) p.part[rank] = upto;
+    r.warp[lane] = upto - v;
+    const int64_t sum = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    if (lane < kCluster) store_there(&r.block[rank], lane, sum);
+    __syncwarp();
   }
-  __syncthreads();
-  return shared[warp];
+  cluster_sync();
+  int64_t before = r.warp[warp];
+  all = 0;
+#pragma unroll
+  for (int i = 0; i < kCluster; ++i) {
+    if (i < rank) before += r.block[i];
+    all += r.block[i];
+  }
+  return before;
 }
 
 // The row of new token i: tokens[lo] <= i < tokens[lo + 1].
@@ -162,34 +187,27 @@ __device__ __forceinline__ void scan_rows(int64_t& n, int64_t& c, int64_t (&sums
 // if there are too few (or `bad`).
 template <class F>
 __device__ __forceinline__ bool take_free(const PagesParams& p, int32_t free_here, int64_t pages, bool bad, int rank,
-                                          int64_t (&shared)[kWarps], F take) {
+                                          Ranks& ranks, F take) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Piece mine = piece_of(p.pages, rank, warp);
-  int64_t at = before_in_block(p, free_here, rank, shared);
-  cluster_sync();
-  int64_t there = 0;
-#pragma unroll
-  for (int i = 0; i < kCluster; ++i) {
-    const int64_t n = __ldcg(p.part + i);
-    if (i < rank) at += n;
-    there += n;
-  }
+  int64_t there, at = rank_pieces(free_here, rank, ranks, there);
   const bool ok = !bad && pages <= there;
   if (rank == 0 && threadIdx.x == 0) *p.number = bad ? -1 : int32_t(max(pages - there, int64_t(0)));
   if (!ok) return false;
   constexpr int kAtOnce = 8;  // loads under way: what is taken is stored between them
   for (int64_t i0 = mine.lo; i0 < mine.hi && at < pages; i0 += 32 * kAtOnce) {
-    bool is_free[kAtOnce];
+    uint32_t of_lane = 0;  // lane u: which of the u-th 32 are free
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
       const int64_t i = i0 + 32 * u + lane;
-      is_free[u] = i < mine.hi && p.refs[i] <= 0;
+      const uint32_t all = __ballot_sync(0xFFFFFFFFu, i < mine.hi && p.refs[i] <= 0);
+      if (lane == u) of_lane = all;
     }
-#pragma unroll
+#pragma unroll 1  // code that runs once costs its fetching (unrolled: 2.5 us more)
     for (int u = 0; u < kAtOnce; ++u) {
-      const uint32_t all = __ballot_sync(0xFFFFFFFFu, is_free[u]);
+      const uint32_t all = __shfl_sync(0xFFFFFFFFu, of_lane, u);
       const int64_t k = at + __popc(all & ((1u << lane) - 1));
-      if (is_free[u] && k < pages) take(k, int32_t(i0 + 32 * u + lane));
+      if ((all >> lane & 1) && k < pages) take(k, int32_t(i0 + 32 * u + lane));
       at += __popc(all);
     }
   }
@@ -238,9 +256,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     k_pages_extend_few(const __grid_constant__ PagesParams p) {
   extern __shared__ __align__(16) uint8_t dynamic[];
   FewRows& f = *reinterpret_cast<FewRows*>(dynamic);
-  __shared__ int64_t shared[kWarps], sums[2][kWarps];
+  __shared__ Ranks ranks;
+  __shared__ int64_t sums[2][kWarps];
   const int rank = blockIdx.x, warp = threadIdx.x >> 5;
   const int32_t b = int32_t(threadIdx.x);
+  cluster_arrive();
   for (int i = b; i < FewRows::kSlots; i += kThreads) f.page[i] = -1, f.writers[i] = 0, f.lowest[i] = kThreads;
   grid_wait();
   const int32_t free_here = count_piece(p, piece_of(p.pages, rank, warp), false);
@@ -279,7 +299,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   }
   const bool bad = __syncthreads_or((count > 0 && g.want > p.table_ld) || tokens > p.total);
   const bool listed = p.total <= kInline;  // else k_pages_slots finds the pages in the table
-  const bool ok = take_free(p, free_here, pages, bad, rank, shared, [&](int64_t k, int32_t page) {
+  const bool ok = take_free(p, free_here, pages, bad, rank, ranks, [&](int64_t k, int32_t page) {
     const int32_t r = row_of(p.rows, k, [&](int32_t x) { return f.need[x]; });
     const int64_t place = f.have[r] + k - f.need[r] - f.own[r];
     p.refs[page] = 1;
@@ -311,7 +331,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
 // Any number of rows.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     k_pages_extend(const __grid_constant__ PagesParams p) {
-  __shared__ int64_t shared[kWarps], sums[2][kWarps];
+  __shared__ Ranks ranks;
+  __shared__ int64_t sums[2][kWarps];
   const int rank = blockIdx.x, warp = threadIdx.x >> 5;
   const int32_t thread = rank * kThreads + int32_t(threadIdx.x);
   grid_wait();
@@ -332,6 +353,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     }
     cluster_sync();
   }
+
+  cluster_arrive();
 
   // Pages and tokens of the rows before each row; every block for itself.
   int64_t pages = 0, tokens = 0;
@@ -359,7 +382,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   }
   if (rank == 0 && threadIdx.x == 0) p.need[p.rows] = pages, p.tokens[p.rows] = tokens;
   bad = __syncthreads_or(bad || tokens > p.total);
-  const bool ok = take_free(p, free_here, pages, bad, rank, shared, [&](int64_t k, int32_t page) {
+  const bool ok = take_free(p, free_here, pages, bad, rank, ranks, [&](int64_t k, int32_t page) {
     p.list[k] = page;
     p.refs[page] = 1;
   });
@@ -476,23 +499,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
 // there on go to.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     k_pages_compact(const __grid_constant__ PagesParams p) {
-  __shared__ int64_t shared[kWarps];
+  __shared__ Ranks ranks;
   const int rank = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t thread = rank * kThreads + int32_t(threadIdx.x);
+  cluster_arrive();
   grid_wait();
   const Piece mine = piece_of(p.pages, rank, warp);
-  int64_t at = before_in_block(p, count_piece(p, mine, true), rank, shared);
-  cluster_sync();
-  int64_t used = 0;
-#pragma unroll
-  for (int i = 0; i < kCluster; ++i) {
-    const int64_t n = __ldcg(p.part + i);
-    if (i < rank) at += n;
-    used += n;
-  }
+  int64_t used, at = rank_pieces(count_piece(p, mine, true), rank, ranks, used);
   if (thread == 0) {
     *p.number = int32_t(used);
-    if (used == p.pages) p.part[kCluster] = used;
+    if (used == p.pages) *p.part = used;
   }
 #pragma unroll 4
   for (int64_t i0 = mine.lo; i0 < mine.hi; i0 += 32) {
@@ -502,11 +518,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     const int64_t k = at + __popc(all & ((1u << lane) - 1));  // held pages below i
     if (some) p.list[k] = int32_t(i);
     else if (i < min(mine.hi, used)) p.writers[i - k] = int32_t(i);
-    if (i < mine.hi && i == used) p.part[kCluster] = k;
+    if (i < mine.hi && i == used) *p.part = k;
     at += __popc(all);
   }
   cluster_sync();
-  const int64_t stay = __ldcg(p.part + kCluster), moves = used - stay;
+  const int64_t stay = __ldcg(p.part), moves = used - stay;
   for (int64_t j = thread; j < p.pages / 2; j += kCluster * kThreads) {
     int2 pair = make_int2(-1, -1);
     if (j < moves) {
@@ -616,7 +632,7 @@ nvfp4_status check_pages(const mxfp4_pages* g, const void* workspace, int64_t wo
   };
   p.need = reinterpret_cast<int64_t*>(take((int64_t(g->rows) + 1) * 8));
   p.tokens = reinterpret_cast<int64_t*>(take((int64_t(g->rows) + 1) * 8));
-  p.part = reinterpret_cast<int64_t*>(take((kCluster + 1) * 8));
+  p.part = reinterpret_cast<int64_t*>(take(8));
   p.taken = p.list = reinterpret_cast<int32_t*>(ws);
   p.writers = p.list + g->pages;
   p.lowest = p.writers + g->pages;
@@ -630,7 +646,7 @@ using namespace nvfp4;
 
 extern "C" int64_t mxfp4_pages_workspace_bytes(const mxfp4_pages* g) {
   if (!g || g->pages < 1 || g->rows < 1 || g->table_ld < 1) return 0;
-  return 2 * align256((int64_t(g->rows) + 1) * 8) + align256((kCluster + 1) * 8) +
+  return 2 * align256((int64_t(g->rows) + 1) * 8) + align256(8) +
          align256(4 * std::max(3 * g->pages, g->rows * g->table_ld));
 }
 

@@ -314,9 +314,9 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     const uint32_t t_o = t_lane + T::kO + qt * D;
     // The warp's queries into shared memory, a row's largest element going to
     // [2^13, 2^14) and the sign of the softmax scale onto the elements.  D / 8
-    // lanes take a row, so that the loads are of whole rows (a thread that
-    // loads its own row: 13,000 cycles for all rows).  Returns the factor of
-    // this thread's scores.
+    // lanes load a row, so that the loads are of whole rows (a thread that
+    // loads its own row: 13,000 cycles for all rows); then a thread scales its own
+    // row in place.  Returns the factor of this thread's scores.
     constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRound = kLanes < 16 ? kLanes : 16;
     auto load_q = [&](const Cursor& c) -> float {
       const int32_t row = c.rt * kRows + qt * 128 + r;
@@ -327,13 +327,11 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
       }
       const int col = lane % kLanes;
       const uint16_t* src = static_cast<const uint16_t*>(a.q) + 8 * col;
-      uint8_t* dst = sq + qt * T::kQBytes + (col / 8) * (128 * 128);
-      int32_t mine = 0;
-      auto place = [&](int i) {
-        const int rq = q * 32 + i * kAtOnce + lane / kLanes;
-        return reinterpret_cast<uint4*>(dst + rq * 128 + (((col & 7) ^ (rq & 7)) << 4));
+      uint8_t* dst = sq + qt * T::kQBytes;
+      // chunk `ch` of eight elements of the row rq
+      auto place = [&](int rq, int ch) {
+        return reinterpret_cast<uint4*>(dst + (ch / 8) * (128 * 128) + rq * 128 + (((ch & 7) ^ (rq & 7)) << 4));
       };
-      // raw first, then scaled in place (by the threads that loaded them): two
       // small loops, as straight-line code that runs once is slow to fetch
 #pragma unroll 1
       for (int i0 = 0; i0 < kLanes; i0 += kRound) {
@@ -346,36 +344,38 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
           if (o >= 0) v[i] = a.q_vec ? *reinterpret_cast<const uint4*>(e) : load_8x16(e);
         }
 #pragma unroll
-        for (int i = 0; i < kRound; ++i) *place(i0 + i) = v[i];
+        for (int i = 0; i < kRound; ++i) *place(q * 32 + (i0 + i) * kAtOnce + lane / kLanes, col) = v[i];
       }
+      __syncwarp();
+      // magnitudes of 16-bit floats are in the order of their bits (NaN above all)
+      uint32_t top = 0;
 #pragma unroll 2
       for (int i = 0; i < kLanes; ++i) {
-        const uint4 v = *place(i);
+        const uint4 v = *place(r, i);
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                     __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+      }
+      top = max(top & 0xFFFFu, top >> 16);
+      auto value = [&](uint32_t x) { return a.bf16 ? word_to_f32<__nv_bfloat16>(x) : word_to_f32<__half>(x); };
+      const int32_t eb = int32_t(__float_as_uint(value(top).x) >> 23) & 0xFF;
+      const int32_t up = (eb == 0 || eb == 255) ? 0 : min(126, 140 - eb);
+      const float mul = a.scale_log2 < 0.0f ? -pow2i(up) : pow2i(up);
+#pragma unroll 2
+      for (int i = 0; i < kLanes; ++i) {
+        const uint4 v = *place(r, i);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        // magnitudes of 16-bit floats are in the order of their bits (NaN above all)
-        uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
-                                __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
-#pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        top = max(top & 0xFFFFu, top >> 16);
-        auto value = [&](uint32_t x) { return a.bf16 ? word_to_f32<__nv_bfloat16>(x) : word_to_f32<__half>(x); };
-        const int32_t eb = int32_t(__float_as_uint(value(top).x) >> 23) & 0xFF;
-        const int32_t up = (eb == 0 || eb == 255) ? 0 : min(126, 140 - eb);
-        const float mul = a.scale_log2 < 0.0f ? -pow2i(up) : pow2i(up);
         uint32_t h[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const float2 t = value(w[x]);
           h[x] = f32_to_word<__half>(t.x * mul, t.y * mul);
         }
-        *place(i) = make_uint4(h[0], h[1], h[2], h[3]);
-        const int32_t theirs = __shfl_sync(0xFFFFFFFFu, up, (lane % kAtOnce) * kLanes);
-        if (lane / kAtOnce == i) mine = theirs;
+        *place(r, i) = make_uint4(h[0], h[1], h[2], h[3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_full[qt]);
-      return fabsf(a.scale_log2) * pow2i(-mine);
+      return fabsf(a.scale_log2) * pow2i(-up);
     };
     auto live_rows = [&](const Cursor& c) { return c.rt * kRows + qt * 128 + q * 32 < c.nq * a.group; };
     advance(wk, wk);

@@ -129,11 +129,11 @@ __global__ void __launch_bounds__(kThreads) k_shared_join(const __grid_constant_
       u = s1[0], v = s1[1];
       const float g[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
       const float m = fmaxf(l1, l2), ref = m == -INFINITY ? 0.0f : m;
-      const float w1 = expf(l1 - ref), w2 = expf(l2 - ref), sum = w1 + w2;
+      const float e1 = expf(l1 - ref), e2 = expf(l2 - ref), sum = e1 + e2;
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      // zeros where a part has no keys
+      const float w1 = e1 * inv, w2 = e2 * inv;  // no more than 1 together: values near the end of the range stay in it
 #pragma unroll
-      for (int x = 0; x < 8; ++x) f[x] = (w1 * g[x] + w2 * f[x]) * inv;
+      for (int x = 0; x < 8; ++x) f[x] = w1 * g[x] + w2 * f[x];
       lse = m == -INFINITY ? m : ref + logf(sum);
     }
     const int64_t row = rh / heads, h = rh - row * heads;

@@ -147,6 +147,8 @@ def test_many_sequences_and_groups():
     c = Shared([1] * n, [16 + i % 20 for i in range(n)], [40 + i % 50 for i in range(n)], [1] * n, 2, 1, 64, seed=9)
     c.run()
     c.check()
+    c.run(max_group=1)  # few rows: prefixes and own tokens in one list
+    c.check()
     c = Shared([n], [64], [65 + i % 50 for i in range(n)], [1] * n, 2, 1, 64, seed=10)
     c.run(max_group=n)
     c.check()
@@ -167,6 +169,32 @@ def test_no_other_bytes_matter():
     assert torch.equal(c.run(), want)
     c.table[1:, :4] = 1 << 30  # read through the first sequence's row
     assert torch.equal(c.run(), want)
+
+
+@pytest.mark.parametrize("n,nq", [(4, 1), (20, 1), (3, 2)])
+def test_nan_blocks(n, nq):
+    """NaN keys and values of the prefix reach all rows, own ones their sequence's."""
+    c = Shared([n], [64], [90 + i for i in range(n)], [nq] * n, 8, 2, 64, seed=n)
+    page, off = int(c.table[0, 1]), 5
+    c.cache.v_scales[page, 0, off, 1] = 255
+    c.cache.k_scales[int(c.table[1, 5]), 1, 2] = 255  # key 82 of sequence 1
+    c.run()
+    c.check()
+    assert bool(torch.isnan(c.out[:, :4, 32:]).all()) and bool(torch.isfinite(c.out[:, :4, :32]).all())
+    assert bool(torch.isnan(c.out[c.starts[1]:c.starts[2], 4:]).all()) and bool(torch.isfinite(c.out[:nq, 4:]).all())
+
+
+@pytest.mark.parametrize("n", [4, 40])
+def test_values_at_the_end_of_the_range(n):
+    """Parts of large values join without leaving the range."""
+    c = Shared([n], [64], [80 + i for i in range(n)], [1] * n, 8, 2, 64, seed=n)
+    c.cache.v_scales.fill_(252)  # up to 6 2^125, 0.75 of the largest binary32
+    c.cache.v_codes.fill_(0x77)
+    c.run()
+    assert bool(torch.isfinite(c.out).all())
+    want = torch.full_like(c.out, 6 * 2.0 ** 125)
+    # weights of 11 bits each, sums of them, one rounding to bf16
+    assert float((c.out.double() / want.double() - 1).abs().max()) < 2.0 ** -8
 
 
 def test_strided_queries_and_outputs():

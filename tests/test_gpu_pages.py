@@ -121,7 +121,8 @@ def select(host, dev, sources):
 
 
 @pytest.mark.parametrize("pages,page,rows,per_row", [(1, 16, 1, 1), (7, 16, 3, 2), (300, 16, 40, 12), (260, 64, 1, 300),
-                                                     (5000, 256, 70, 90), (20000, 16, 1500, 20), (2000, 32, 9000, 3)])
+                                                     (5000, 256, 70, 90), (20000, 16, 1500, 20), (2000, 32, 9000, 3),
+                                                     (6000, 16, 1024, 9), (6000, 16, 1025, 9), (3000, 16, 300, 400)])
 def test_random_operations(pages, page, rows, per_row):
     rng = random.Random(pages + rows)
     host, dev = both(pages, page, rows, per_row)

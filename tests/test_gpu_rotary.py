@@ -255,3 +255,44 @@ def test_sections_and_frequencies():
             fc2.head_rotary(bad)
     with pytest.raises(ValueError):
         fc2.rotary_frequencies((3,))
+
+
+def test_past_32_bits():
+    """More than 2^32 bytes of heads, and pages behind 4 GB of codes."""
+    n, h, dim = 70000, 256, 128
+    freq, axis, rotary = make_rotary(64, 1, False, None)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    q = torch.empty(n, h, dim, dtype=torch.bfloat16, device="cuda").normal_()
+    w = torch.ones(dim, device="cuda")
+    out, _ = fc2.head_norm_rotary(q, None, rotary, pos, w)
+    for rows in (slice(0, 2), slice(n // 2, n // 2 + 2), slice(n - 2, n)):
+        check(out[rows], formula(q[rows], w, freq, axis, False, pos[rows]))
+    del out
+    cache = fc2.empty_mxfp4_cache(2300, 256, 64, 256)
+    assert cache.k_codes.numel() > 1 << 32
+    x = torch.randn(3, 64, 256, dtype=torch.bfloat16, device="cuda")
+    slots = torch.tensor([2299 * 256 + 255, 5, 1200 * 256 + 7], device="cuda")
+    _, _, rotary = make_rotary(128, 1, True, None)
+    fc2.mxfp4_cache_write_rotary(cache, x, x, x, slots, rotary, pos[:3] * 0)
+    at, off = slots // 256, slots % 256
+    for codes, scales in ((cache.k_codes, cache.k_scales), (cache.v_codes, cache.v_scales)):
+        assert torch.equal(mx.decode(mx.unpack(codes[at, :, off]), scales[at, :, off]), mx.values(x))
+
+
+def test_same_bits_from_a_graph():
+    """Captured calls give the bits of the calls, whatever the number of tokens
+    makes of a token's share of a warp."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    freq, axis, rotary = make_rotary(64, 1, False, g)
+    w = 1 + 0.1 * torch.randn(128, generator=g, device="cuda")
+    q = heads(5000, 40, 128, g, torch.bfloat16)
+    pos = torch.arange(5000, dtype=torch.int32, device="cuda")
+    whole, _ = fc2.head_norm_rotary(q, None, rotary, pos, w)
+    for n in (1, 7, 300):
+        assert torch.equal(fc2.head_norm_rotary(q[:n], None, rotary, pos[:n], w)[0], whole[:n])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, _ = fc2.head_norm_rotary(q, None, rotary, pos, w)
+    out.zero_()
+    graph.replay()
+    assert torch.equal(out, whole)

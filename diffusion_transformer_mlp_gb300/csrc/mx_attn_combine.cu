@@ -17,6 +17,7 @@ namespace {
 // keys: 16.9 us, with 32 columns 19.4).
 constexpr int kCombineThreads = 256;
 constexpr int kMostParts = 512;  // weights held at a time
+constexpr int kFewParts = 4;
 
 template <int D, int kRows, int kCols>
 __global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_constant__ SplitParams sp, int32_t tok) {
@@ -47,8 +48,62 @@ __global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_c
     if (parts == 1) return;  // written by its worker
     slot0 = worker_start(total, w0, workers) == first ? 0 : 1;
   }
+  auto write = [&](int32_t r, int32_t d, const float (&f)[8], float lse) {
+    const int32_t row = rt * kRows + r, qi = row / a.group, hq = h * a.group + row - qi * a.group;
+    store_o8(a, int64_t(q0 + qi) * a.o_st + int64_t(hq) * a.o_sh + d, f);
+    if (d == 0 && a.lse != nullptr) a.lse[int64_t(q0 + qi) * (a.kv_heads * a.group) + hq] = lse;
+  };
   // first row of the i-th partial
   auto rows_of = [&](int32_t i) { return (int64_t(w0 + i) * 2 + (i == 0 ? slot0 : 0)) * kRows; };
+  if (parts <= kFewParts) {
+    // Short sequences: a thread an item, with all its loads at once and no barrier.
+    // The sums are those of the way below, in its order and with its roundings, so
+    // that results do not depend on where a run ends (192 sequences of 33 to 1,025
+    // keys, 8 heads: 14.6 us without this, so XX).
+    const int item = threadIdx.x;
+    const int32_t r = item / (kCols / 8), d = col0 + item % (kCols / 8) * 8;
+    if (item >= kItems || r >= live) return;
+    float2 ml[kFewParts];
+    float4 u[kFewParts], v[kFewParts];
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kFewParts; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.0f);
+      u[i] = v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (i < parts) {
+        const float4* src = reinterpret_cast<const float4*>(sp.part_o + (rows_of(i) + r) * D + d);
+        ml[i] = sp.part_ml[rows_of(i) + r], u[i] = src[0], v[i] = src[1];
+      }
+      m = fmaxf(m, ml[i].x);
+    }
+    const float ref = m == -INFINITY ? 0.0f : m + kJoinLog2;
+    float w[kFewParts], l[kFewParts];
+#pragma unroll
+    for (int i = 0; i < kFewParts; ++i) {
+      w[i] = i < parts ? exp2_approx(ml[i].x - ref) : 0.0f;
+      l[i] = __fmul_rn(ml[i].y, w[i]);
+    }
+    const float sum = __fadd_rn(__fadd_rn(l[0], l[1]), __fadd_rn(l[2], l[3]));
+    const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+    float f[8];
+#pragma unroll
+    for (int s = 0; s < kSlices; ++s) {
+      float t[8] = {};
+#pragma unroll
+      for (int i = s; i < kFewParts; i += kSlices) {
+        if (i >= parts) break;
+        const float x[8] = {u[i].x, u[i].y, u[i].z, u[i].w, v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t[k] = __fmaf_rn(x[k], w[i], t[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = s == 0 ? t[k] : __fadd_rn(f[k], t[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] *= inv;
+    write(r, d, f, sum == 0.0f ? -INFINITY : (m + kJoinLog2 - kWeightLog2 + log2f(sum)) * 0.6931471805599453f);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = threadIdx.x % kRows;
   // `v` of all threads of a row, into out[row]
   auto over_rows = [&](float v, auto op, float* out) {
@@ -111,11 +166,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_c
   const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
 #pragma unroll
   for (int k = 0; k < 8; ++k) f[k] *= inv;
-  const int32_t row = rt * kRows + r, qi = row / a.group, hq = h * a.group + row - qi * a.group;
-  store_o8(a, int64_t(q0 + qi) * a.o_st + int64_t(hq) * a.o_sh + d, f);
-  if (d == 0 && a.lse != nullptr)
-    a.lse[int64_t(q0 + qi) * (a.kv_heads * a.group) + hq] =
-        l == 0.0f ? -INFINITY : (row_m[r] + kJoinLog2 - kWeightLog2 + log2f(l)) * 0.6931471805599453f;
+  write(r, d, f, l == 0.0f ? -INFINITY : (row_m[r] + kJoinLog2 - kWeightLog2 + log2f(l)) * 0.6931471805599453f);
 }
 
 // The same for segments of 128 or 256 rows.  Of those few are split, at the

@@ -130,7 +130,7 @@ __device__ __forceinline__ void store_chunk(T* p, const float* f) {
 
 // kVec: 16-byte accesses to the heads are aligned.
 template <typename T, bool kCache, bool kNeighbours, bool kVec>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && !kCache ? 14 : 8) k_head_norm_rotary(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && !kCache ? 10 : 8) k_head_norm_rotary(const __grid_constant__ RotaryParams p) {
   __shared__ __align__(16) float2 turned[kWarps][kMaxPairs];
   __shared__ __align__(16) float most[kCache ? kWarps : 1][kCache ? 64 : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -180,12 +180,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && !kCache ? 14 : 8) 
     int32_t head = from * at_once + head_of;
     const T* src = static_cast<const T*>(r.x) + token * r.st + head * r.sh;
     T* dst = static_cast<T*>(r.out) + token * r.o_st + head * r.o_sh;  // not used on the way into the cache
-    Chunk8<T> raw_a = {}, raw_b = {};
-    auto fetch = [&](bool there) {
-      if (lane_in && there) raw_a = load_chunk<T, kVec>(src + 8 * ca), raw_b = load_chunk<T, kVec>(src + 8 * cb);
+    // Loads of kAhead heads of 16 bits are under way, each in registers of its own: they
+    // are not moved, which would wait for them, hence the unrolled loop.
+    constexpr int kAhead = sizeof(T) == 2 && !kCache ? 2 : 1;
+    Chunk8<T> raw_a[kAhead] = {}, raw_b[kAhead] = {};
+    auto fetch = [&](int32_t at, int u) {
+      if (lane_in && at < r.heads) raw_a[u] = load_chunk<T, kVec>(src + 8 * ca), raw_b[u] = load_chunk<T, kVec>(src + 8 * cb);
       src += r.step;
     };
-    fetch(head < r.heads);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (from + u < to) fetch(head + u * at_once, u);
     // (a, b) -> a (wa cos, wa sin) + b (-wb sin, wb cos)
     uint64_t of_a[8], of_b[8];
     const bool norm = r.weight != nullptr;
@@ -218,12 +223,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && !kCache ? 14 : 8) 
       }
     }
 #pragma unroll 1
-    for (int32_t step = from; step < to; ++step, head += at_once, dst += r.o_step) {
+    for (int32_t step0 = from; step0 < to; step0 += kAhead)
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u, head += at_once, dst += r.o_step) {
+      const int32_t step = step0 + u;
+      if (kAhead > 1 && step >= to) break;
       const bool live = lane_in && head < r.heads;  // the others go along with what they have
       float f[16];
-      unpack<T>(raw_a, f);
-      unpack<T>(raw_b, f + 8);
-      if (step + 1 < to) fetch(head + at_once < r.heads);
+      unpack<T>(raw_a[u], f);
+      unpack<T>(raw_b[u], f + 8);
+      if (step + kAhead < to) fetch(head + kAhead * at_once, u);
       if (!kCache || kind < 2) {
         if (norm) {
           auto mean = [&]() {

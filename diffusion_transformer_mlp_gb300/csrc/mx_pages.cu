@@ -10,6 +10,14 @@
 // same ids whatever the timing; counts are changed by atomics whose sums do not
 // depend on their order.
 //
+// What bounds them: latency.  Growing 60 forked rows by a token takes 5 us (7.9 under a
+// profiler: 2 to the growth of each row, 1 to their sums, 1 to the pool's counts, 1.5 to
+// take the pages, 1.5 for the slots), 56 rows by 27,000 pages of a pool of 48,000 and
+// 440,000 slots 11.6 + 4.9 us; selecting rows 2.5 to 3.5 us, making a pool of 9,000
+// pages compact 5.4 + 2.4 us.  Code that runs once costs its fetching, so loops stay
+// loops.  Copies are bound by HBM: 1,500 pages of 69 KB (208 MB moved) in 32.6 us, 94%
+// of the copy rate.
+//
 // What one block writes and another reads inside a kernel is read from L2
 // (__ldcg): the barrier orders it, and L1 may hold what was there before.
 #include <algorithm>

@@ -18,9 +18,19 @@
 // side by side either way.  Sums are binary32; the result is rounded once, to
 // the output's type or to MXFP4.
 //
-// What goes into the cache needs the largest of 32 elements, four chunks that
-// may lie in any lanes and places when only part of a head is rotated: chunk
-// maxima go through shared memory too.
+// What goes into the cache needs the largest of 32 elements, four chunks: those of
+// four neighbouring lanes, or, where only part of a head is rotated, of any, whose
+// maxima then go through shared memory.
+//
+// What bounds it: HBM, 37,810 tokens of 84 heads of 128 in BF16 (1.63 GB) in 261 us,
+// 92% of the copy rate (FP32: 95%); with few heads or narrow ones a token's own work,
+// its angles and their products with the weights, which takes a warp about as long as
+// five steps of heads (60,000 tokens of 40 heads of 64: 121 us, 75%).  Registers decide:
+// with 96 two heads' loads are under way and nothing spills; ten blocks an SM 261 us,
+// eight 289, twelve (80 registers, spills) 275, one head under way 276.  Into the cache
+// 37,810 tokens of 32 + 8 + 8 heads (0.82 GB) 163 us, where rotating queries and keys
+// and then writing the cache take 132 + 37; twelve blocks an SM, ten 173 us, eight 196.
+// Several tokens to a warp, in turn: 271 to 293 us instead of 261.  One token: 2.9 us.
 #include <string>
 #include <type_traits>
 
@@ -32,7 +42,7 @@ nvfp4_status check_cache(const mxfp4_cache* cache, int* page_shift, const std::s
 
 namespace {
 
-constexpr int kThreads = 64;  // small blocks, as warps end when their token does (256: 2% slower)
+constexpr int kThreads = 64;  // small blocks, as warps end when their token does (256 threads: 2% slower)
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxPairs = 128;
 
@@ -130,7 +140,8 @@ __device__ __forceinline__ void store_chunk(T* p, const float* f) {
 
 // kVec: 16-byte accesses to the heads are aligned.
 template <typename T, bool kCache, bool kNeighbours, bool kVec>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && !kCache ? 10 : 8) k_head_norm_rotary(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (kCache ? 12 : 10) : 8)
+    k_head_norm_rotary(const __grid_constant__ RotaryParams p) {
   __shared__ __align__(16) float2 turned[kWarps][kMaxPairs];
   __shared__ __align__(16) float most[kCache ? kWarps : 1][kCache ? 64 : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -146,14 +157,19 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && !kCache ? 10 : 8) 
   // this lane's chunks
   const int eighth = p.pairs >> 3;
   const int chunks = p.dim >> 3;
-  int ca = s, cb = s + (chunks >> 1);
+  int turned_a = s, turned_b = s + (chunks >> 1);
   if (!kNeighbours) {
-    cb = s + eighth;
-    if (s >= eighth) ca = 2 * s, cb = 2 * s + 1;  // behind the rotated ones: 2 eighth + 2 (s - eighth)
+    turned_b = s + eighth;
+    if (s >= eighth) turned_a = 2 * s, turned_b = 2 * s + 1;  // behind the rotated ones: 2 eighth + 2 (s - eighth)
   }
+  // a block's four chunks are in four neighbouring lanes (of values they always are)
+  const bool aligned = kNeighbours || 2 * eighth == chunks;
   const bool lane_in = head_of < at_once;
   const bool by_halves = (lanes & (lanes - 1)) == 0;
-
+  const int64_t slot = kCache ? p.slots[token] : 0;
+  const bool held = kCache && slot >= 0 && slot < (p.pages << p.page_shift);
+  const int64_t row0 = (((slot >> p.page_shift) * p.kv_heads) << p.page_shift) +  // of head 0
+                       (slot & ((int64_t(1) << p.page_shift) - 1));
 
   // the token's cosines and sines
   if (first < rotated) {
@@ -167,8 +183,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && !kCache ? 10 : 8) 
     }
     __syncwarp();
   }
-  const int64_t slot = kCache ? p.slots[token] : 0;
-  const bool held = kCache && slot >= 0 && slot < (p.pages << p.page_shift);
 
   int32_t behind = 0;  // steps of the kinds before
 #pragma unroll
@@ -177,6 +191,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && !kCache ? 10 : 8) 
     const int32_t from = max(first - behind, 0), to = min(end - behind, r.steps);
     behind += r.steps;
     if (from >= to) continue;
+    const int ca = kind < 2 ? turned_a : s, cb = kind < 2 ? turned_b : s + (chunks >> 1);
+    const bool whole = kind == 2 || aligned;
     int32_t head = from * at_once + head_of;
     const T* src = static_cast<const T*>(r.x) + token * r.st + head * r.sh;
     T* dst = static_cast<T*>(r.out) + token * r.o_st + head * r.o_sh;  // not used on the way into the cache
@@ -185,7 +201,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && !kCache ? 10 : 8) 
     constexpr int kAhead = sizeof(T) == 2 && !kCache ? 2 : 1;
     Chunk8<T> raw_a[kAhead] = {}, raw_b[kAhead] = {};
     auto fetch = [&](int32_t at, int u) {
-      if (lane_in && at < r.heads) raw_a[u] = load_chunk<T, kVec>(src + 8 * ca), raw_b[u] = load_chunk<T, kVec>(src + 8 * cb);
+      if (lane_in && at < r.heads)
+        raw_a[u] = load_chunk<T, kVec>(src + 8 * ca), raw_b[u] = load_chunk<T, kVec>(src + 8 * cb);
       src += r.step;
     };
 #pragma unroll
@@ -292,31 +309,58 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && !kCache ? 10 : 8) 
         float ma = 0.0f, mb = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) ma = max_nan(ma, fabsf(f[i])), mb = max_nan(mb, fabsf(f[8 + i]));
-        float* row = most[warp] + head_of * chunks;  // dim is 16 times the lanes here
-        row[ca] = ma, row[cb] = mb;
-        __syncwarp();
-        const int64_t at = ((((slot >> p.page_shift) * p.kv_heads) + head) << p.page_shift) +
-                           (slot & ((int64_t(1) << p.page_shift) - 1));
-        uint8_t* codes = kind == 1 ? p.k_codes : p.v_codes;
-        uint8_t* scales = kind == 1 ? p.k_scales : p.v_scales;
+        // the largest of the four chunks of a block
+        if (whole) {  // they lie in four neighbouring lanes
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) {
+            ma = max_nan(ma, __shfl_xor_sync(0xFFFFFFFFu, ma, o));
+            mb = max_nan(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, o));
+          }
+        } else {
+          float* row = most[warp] + head_of * chunks;
+          row[ca] = ma, row[cb] = mb;
+          __syncwarp();
+          const float4 x = *reinterpret_cast<const float4*>(row + (ca & ~3));
+          const float4 y = *reinterpret_cast<const float4*>(row + (cb & ~3));
+          ma = max_nan(max_nan(x.x, x.y), max_nan(x.z, x.w)), mb = max_nan(max_nan(y.x, y.y), max_nan(y.z, y.w));
+          __syncwarp();  // before the next heads' are written
+        }
+        uint32_t e[2], q[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int ch = h ? cb : ca;
-          const float4 m4 = *reinterpret_cast<const float4*>(row + (ch & ~3));
-          const float am = max_nan(max_nan(m4.x, m4.y), max_nan(m4.z, m4.w));
-          const uint32_t eb = (__float_as_uint(am) >> 23) & 0xFFu;
-          const uint32_t e = eb == 255u ? 255u : (eb > 2u ? eb - 2u : 0u);
-          const float inv = __uint_as_float((254u - min(e, 252u)) << 23);
+          const uint32_t eb = (__float_as_uint(h ? mb : ma) >> 23) & 0xFFu;
+          e[h] = eb == 255u ? 255u : (eb > 2u ? eb - 2u : 0u);
+          const float inv = __uint_as_float((254u - min(e[h], 252u)) << 23);
           float y[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) y[i] = f[8 * h + i] * inv;
-          const uint32_t q = eb == 255u ? 0u : e2m1x8(y);
-          if (live && held) {
-            *reinterpret_cast<uint32_t*>(codes + at * (p.dim / 2) + ch * 4) = q;
-            if ((ch & 3) == 0) scales[at * (p.dim / 32) + (ch >> 2)] = uint8_t(e);
+          q[h] = eb == 255u ? 0u : e2m1x8(y);
+        }
+        // a head's scales in one word of each of its halves, where they are in order
+        uint32_t half_a = e[0], half_b = e[1];
+        if (whole && p.dim > 64) {
+          half_a |= __shfl_down_sync(0xFFFFFFFFu, half_a, 4) << 8;
+          half_b |= __shfl_down_sync(0xFFFFFFFFu, half_b, 4) << 8;
+          if (p.dim > 128) {
+            half_a |= __shfl_down_sync(0xFFFFFFFFu, half_a, 8) << 16;
+            half_b |= __shfl_down_sync(0xFFFFFFFFu, half_b, 8) << 16;
           }
         }
-        __syncwarp();  // the maxima are read
+        if (live && held) {
+          const int64_t at = row0 + (int64_t(head) << p.page_shift);
+          uint8_t* codes = (kind == 1 ? p.k_codes : p.v_codes) + at * (p.dim / 2);
+          uint8_t* scales = (kind == 1 ? p.k_scales : p.v_scales) + at * (p.dim / 32);
+          *reinterpret_cast<uint32_t*>(codes + ca * 4) = q[0];
+          *reinterpret_cast<uint32_t*>(codes + cb * 4) = q[1];
+          if (!whole) {
+            if ((ca & 3) == 0) scales[ca >> 2] = uint8_t(e[0]);
+            if ((cb & 3) == 0) scales[cb >> 2] = uint8_t(e[1]);
+          } else if (s == 0) {
+            if (p.dim == 64) *reinterpret_cast<uint16_t*>(scales) = uint16_t(half_a | half_b << 8);
+            else if (p.dim == 128) *reinterpret_cast<uint32_t*>(scales) = (half_a & 0xFFFFu) | half_b << 16;
+            else *reinterpret_cast<uint2*>(scales) = make_uint2(half_a, half_b);
+          }
+        }
       }
     }
   }

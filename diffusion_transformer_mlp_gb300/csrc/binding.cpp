@@ -360,7 +360,7 @@ PyObject* cache_read(PyObject* const* a) {
 
 // cache_attention(q, cache x 4, table, lens, q_starts | None, max_queries | None, scale | None, causal, window, sinks,
 //                 out | None, lse | None, status | None, stream) -> out
-// cache_attention_shared(the same, groups, shared, max_group | None) -> out
+// cache_attention_shared(the same, groups, shared, max_group | None, always) -> out
 PyObject* attend(PyObject* const* a, bool with_groups) {
   const Cache c = cache(a + 1);
   const Tensor& q = tensor(a[0], "q");
@@ -406,6 +406,8 @@ PyObject* attend(PyObject* const* a, bool with_groups) {
     if (most_group < 0) bad("max_group must not be negative");
     if (total > 0 && shared.size(0) > 0 && most_group == 0) bad("q has rows, but max_group leaves no query");
     s.groups = static_cast<const int32_t*>(groups.data_ptr()), s.shared = static_cast<const int32_t*>(shared.data_ptr());
+    s.always = PyObject_IsTrue(a[20]);
+    if (s.always < 0) throw Raised();
     s.count = int32_t(shared.size(0)), s.max_group = int32_t(most_group < total ? most_group : total);
   }
   const Launch on_stream(a[16], c.dev);
@@ -712,7 +714,7 @@ PyMethodDef methods[] = {{"bind", (PyCFunction)(void*)bind, METH_FASTCALL, nullp
                          ENTRY(cache_write, 8),
                          ENTRY(cache_read, 9),
                          ENTRY(cache_attention, 17),
-                         ENTRY(cache_attention_shared, 20),
+                         ENTRY(cache_attention_shared, 21),
                          ENTRY(norm_rotary, 12),
                          ENTRY(cache_write_rotary, 17),
                          ENTRY(pages_select, 6),

@@ -32,6 +32,9 @@ bool many_rows(int32_t dim, int64_t rows) { return rows > (dim == 256 ? 16 : 64)
 }  // namespace
 
 bool attn_has_many_rows(int32_t dim, int64_t rows) { return many_rows(dim, rows); }
+int64_t attn_workspace(int32_t dim, bool many) {
+  return many ? attn_chunk_workspace(dim) : attn_stream_workspace(dim);
+}
 
 }  // namespace nvfp4
 
@@ -41,7 +44,7 @@ extern "C" int64_t mxfp4_attention_workspace_bytes(int32_t kv_heads, int32_t q_h
                                                    int32_t max_queries) {
   if (kv_heads < 1 || q_heads < 1 || max_queries < 1 || (dim != 64 && dim != 128 && dim != 256)) return 0;
   const int64_t rows = int64_t(max_queries) * (q_heads / kv_heads);
-  return many_rows(dim, rows) ? attn_chunk_workspace(dim) : attn_stream_workspace(dim);
+  return attn_workspace(dim, many_rows(dim, rows));
 }
 
 namespace nvfp4 {
@@ -98,10 +101,9 @@ nvfp4_status attn_params(const mxfp4_cache* cache, const mxfp4_attention* args, 
   return NVFP4_OK;
 }
 
-nvfp4_status attn_run(const mxfp4_cache* cache, const AttnParams& p, int32_t max_queries, void* workspace,
+nvfp4_status attn_run(const mxfp4_cache* cache, const AttnParams& p, int32_t max_queries, bool many, void* workspace,
                       cudaStream_t stream) {
-  if (many_rows(cache->dim, int64_t(max_queries) * p.group)) return attn_chunk(cache, p, max_queries, workspace, stream);
-  return attn_stream(cache, p, max_queries, workspace, stream);
+  return many ? attn_chunk(cache, p, max_queries, workspace, stream) : attn_stream(cache, p, max_queries, workspace, stream);
 }
 
 }  // namespace nvfp4
@@ -114,5 +116,6 @@ extern "C" nvfp4_status mxfp4_cache_attention(const mxfp4_cache* cache, const mx
                                      : 0;
   const nvfp4_status st = attn_params(cache, args, need, "mxfp4_cache_attention", p);
   if (st != NVFP4_OK || p.seqs == 0) return st;
-  return attn_run(cache, p, args->max_queries, args->workspace, reinterpret_cast<cudaStream_t>(stream));
+  return attn_run(cache, p, args->max_queries, many_rows(cache->dim, int64_t(args->max_queries) * p.group),
+                  args->workspace, reinterpret_cast<cudaStream_t>(stream));
 }

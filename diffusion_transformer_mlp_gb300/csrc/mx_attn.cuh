@@ -601,10 +601,12 @@ inline void split_queries(AttnParams& a, const AttnParams& base, int32_t b) {
 nvfp4_status attn_combine(int dim, int rows, int tok, int row_tiles, const SplitParams& sp, cudaStream_t stream);
 nvfp4_status attn_join(int dim, int tok, const SplitParams& sp, cudaStream_t stream);
 
-// mx_attn.cu: the kernel for the rows that there may be, and its workspace.
-nvfp4_status attn_run(const mxfp4_cache* cache, const AttnParams& p, int32_t max_queries, void* workspace,
+// mx_attn.cu: whether rows of a kv head are k_attn_chunk's rather than
+// k_attn_stream's; attention by the one that `many` says, in a workspace for it.
+bool attn_has_many_rows(int32_t dim, int64_t rows);
+nvfp4_status attn_run(const mxfp4_cache* cache, const AttnParams& p, int32_t max_queries, bool many, void* workspace,
                       cudaStream_t stream);
-bool attn_has_many_rows(int32_t dim, int64_t rows);  // k_attn_chunk's rather than k_attn_stream's
+int64_t attn_workspace(int32_t dim, bool many);
 // What an entry point of that name checks of its arguments; the parameters they give.
 nvfp4_status attn_params(const mxfp4_cache* cache, const mxfp4_attention* args, int64_t workspace_bytes,
                          const std::string& nm, AttnParams& p);

@@ -22,9 +22,10 @@
 // What bounds it: the latencies of six launches and of k_attn_chunk's first and last
 // tiles, before the work itself.  Two prompts of 16,001 and 12,001 tokens, 32 and 16
 // sequences, 32 / 8 heads of 128: parts 3.7, prefixes 35, their join 7.1, own tokens
-// 11.1, their join 6.3, this join 2.9 us; the pass 63 us, where mxfp4_cache_attention
-// reads the prompts once a sequence and takes NOSHARE us.  One of 32,769 tokens, 128
-// sequences of 64 heads: 166 us, 119 of them k_attn_chunk at 61% of the tensor rate.
+// 11.1, their join 6.3, this join 2.9 us; the pass 63 us, 185 if each sequence reads
+// its prompt.  One of 32,769 tokens, 128 sequences of 64 heads: 166 us instead of
+// 1,009; 118 of them are k_attn_chunk at 61% of the tensor rate.  Where reading
+// prefixes each time is as fast, that is done (plan_of).
 #include <algorithm>
 #include <string>
 
@@ -149,6 +150,53 @@ __global__ void __launch_bounds__(kThreads) k_shared_join(const __grid_constant_
   }
 }
 
+// How to work: every sequence for itself, or prefixes (by either kernel) and own
+// tokens, in one launch or two.
+struct Plan {
+  bool share, one_list, prefix_many, own_many;
+};
+
+// The host knows the sizes of the tables, not the lengths: times in us as if all
+// tables were full and all of them shared, which is the most that sharing can save.
+// Rates are key heads (keys times kv heads) a us and row tile (of 8 or 16 rows, of 256
+// or 128), measured with 2 to 32 sequences of 1 and 6 queries on prefixes of 512 to
+// 32,768 keys, 4 and 8 kv heads, groups of 4 and 8.  Each for itself / shared:
+//   dim 128, 4 sequences, 1 query      12.7 / 19.0   15.2 / 20.1   23.8 / 26.4   46.1 / 35.9
+//   16 sequences                       14.8 / 21.2   23.6 / 24.0   45.5 / 34.8  138.5 / 82.8
+//   32 sequences                       19.0 / 38.4   31.7 / 37.4   77.8 / 45.5  260.9 / 64.4
+//   8 sequences, 6 queries             18.2 / 41.2   28.2 / 41.0   54.0 / 49.6  170.3 / 71.6
+//   dim 64, 32 sequences, 1 query      13.0 / 30.9   19.0 / 32.3   30.8 / 40.3   83.9 / 51.6
+//   dim 256, 8 sequences, 1 query      15.0 / 41.8   20.1 / 41.7   35.0 / 50.5   90.6 / 65.3
+// (prefixes of 512, 2,048, 8,192, 32,768 keys).  Where a sequence has rows for whole
+// tiles there is nothing to save: the work is the rows', and they are as many.
+Plan plan_of(int32_t dim, int64_t kv_heads, int64_t group, int64_t total_q, int64_t max_queries, int64_t seqs,
+             int64_t capacity, int64_t count, int64_t max_group) {
+  const int i = dim == 64 ? 0 : (dim == 128 ? 1 : 2);
+  const double few8[3] = {58e3, 33e3, 14e3}, few16[3] = {40e3, 24e3, 9e3}, many[3] = {10e3, 10e3, 6e3};
+  // in one list the own tokens' short segments come last, to workers of their own
+  const double list8[3] = {16e3, 15e3, 9e3}, list16[3] = {20e3, 16e3, 4e3};
+  auto stream = [&](int64_t n, int64_t rows, const double* rate8, const double* rate16) {  // n sequences' keys
+    const double work = double(n) * double(capacity) * double(kv_heads);
+    return rows <= 8 ? work / rate8[i] : work * double((rows + 15) / 16) / rate16[i];
+  };
+  auto chunk = [&](int64_t n, int64_t rows) {
+    const int64_t tile = dim == 256 ? 128 : 256;
+    return double(n) * double(capacity) * double(kv_heads) * double((rows + tile - 1) / tile) / many[i];
+  };
+  const int64_t own_rows = max_queries * group, most_rows = max_group * group;
+  const int64_t rows = std::min(most_rows, (total_q + count - 1) / count * group);  // of a group, about
+  Plan p = {};
+  p.own_many = attn_has_many_rows(dim, own_rows);
+  const double apart = p.own_many ? 25.0 + chunk(seqs, own_rows) : 12.0 + stream(seqs, own_rows, few8, few16);
+  const bool one = max_queries == 1;
+  const double by_stream = one ? 18.0 + stream(count, rows, list8, list16) : 30.0 + stream(count, rows, few8, few16);
+  const double by_chunk = (dim == 256 ? 48.0 : 40.0) + chunk(count, rows);
+  p.prefix_many = attn_has_many_rows(dim, most_rows) || by_chunk < by_stream;
+  p.one_list = one && !p.prefix_many;
+  p.share = (p.prefix_many ? by_chunk : by_stream) < apart;
+  return p;
+}
+
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
 // Places in the workspace, from its start on; returns its size.
@@ -181,8 +229,8 @@ extern "C" int64_t mxfp4_attention_shared_workspace_bytes(int32_t kv_heads, int3
   if (own == 0 || count == 0 || max_group < 1) return own;
   SharedParams p;
   p.count = count;
-  return layout(p, nullptr, std::max(own, mxfp4_attention_workspace_bytes(kv_heads, q_heads, dim, max_group)), total_q,
-                q_heads, dim, seqs, table_ld);
+  return layout(p, nullptr, std::max(attn_workspace(dim, false), attn_workspace(dim, true)), total_q, q_heads, dim, seqs,
+                table_ld);
 }
 
 extern "C" nvfp4_status mxfp4_cache_attention_shared(const mxfp4_cache* cache, const mxfp4_attention* args,
@@ -200,19 +248,25 @@ extern "C" nvfp4_status mxfp4_cache_attention_shared(const mxfp4_cache* cache, c
   if (bad != NVFP4_OK || p.a.seqs == 0) return bad;
   p.a.sinks = 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (shared->count == 0 || max_group == 0) return attn_run(cache, p.a, args->max_queries, args->workspace, s);
-  if (!shared->groups || !shared->shared) return fail(NVFP4_EINVAL, nm + ": null pointer");
-  if (reinterpret_cast<uintptr_t>(shared->groups) % 4 != 0 || reinterpret_cast<uintptr_t>(shared->shared) % 4 != 0)
-    return fail(NVFP4_EALIGN, nm + ": groups and shared must be aligned to their elements");
-  if (int64_t(max_group) * p.a.group > (int64_t(1) << 24) || int64_t(shared->count) + args->seqs > 0x7FFFFF00 ||
-      args->total_q > 0x3FFFFFFF)
-    return fail(NVFP4_EUNSUPPORTED, nm + ": problem too large");
+  if (shared->count > 0 && max_group > 0) {
+    if (!shared->groups || !shared->shared) return fail(NVFP4_EINVAL, nm + ": null pointer");
+    if (reinterpret_cast<uintptr_t>(shared->groups) % 4 != 0 || reinterpret_cast<uintptr_t>(shared->shared) % 4 != 0)
+      return fail(NVFP4_EALIGN, nm + ": groups and shared must be aligned to their elements");
+    if (int64_t(max_group) * p.a.group > (int64_t(1) << 24) || int64_t(shared->count) + args->seqs > 0x7FFFFF00 ||
+        args->total_q > 0x3FFFFFFF)
+      return fail(NVFP4_EUNSUPPORTED, nm + ": problem too large");
+  }
   const int64_t heads = args->q_heads;
   const int32_t dim = cache->dim;
+  Plan plan = {};
+  plan.own_many = attn_has_many_rows(dim, int64_t(args->max_queries) * p.a.group);
+  if (shared->count > 0 && max_group > 0)
+    plan = plan_of(dim, cache->kv_heads, p.a.group, args->total_q, args->max_queries, args->seqs,
+                   args->table_ld * cache->page_size, shared->count, max_group);
+  if (shared->count > 0 && max_group > 0 && shared->always != 0) plan.share = true;
+  if (!plan.share) return attn_run(cache, p.a, args->max_queries, plan.own_many, args->workspace, s);
   p.groups = shared->groups, p.shared = shared->shared, p.count = shared->count;
-  layout(p, static_cast<uint8_t*>(args->workspace),
-         std::max(mxfp4_attention_workspace_bytes(cache->kv_heads, args->q_heads, dim, args->max_queries),
-                  mxfp4_attention_workspace_bytes(cache->kv_heads, args->q_heads, dim, max_group)),
+  layout(p, static_cast<uint8_t*>(args->workspace), std::max(attn_workspace(dim, false), attn_workspace(dim, true)),
          args->total_q, heads, dim, args->seqs, args->table_ld);
   nvfp4_status st = launch("launch k_shared_parts", k_shared_parts, dim3(unsigned(p.count + args->seqs)), dim3(kThreads),
                            0, 0, s, p);
@@ -223,19 +277,19 @@ extern "C" nvfp4_status mxfp4_cache_attention_shared(const mxfp4_cache* cache, c
   part.out = p.o, part.lse = p.l;
   part.table = p.table, part.lens = p.lens, part.q_starts = p.starts;
   part.causal = 0;
-  if (args->max_queries == 1 && !attn_has_many_rows(dim, int64_t(max_group) * part.group)) {
+  if (plan.one_list) {
     part.seqs = p.count + 1 + args->seqs, part.total_q = 2 * args->total_q;
-    st = attn_run(cache, part, max_group, args->workspace, s);
+    st = attn_run(cache, part, max_group, false, args->workspace, s);
     if (st != NVFP4_OK) return st;
   } else {
     part.seqs = p.count;
-    st = attn_run(cache, part, max_group, args->workspace, s);
+    st = attn_run(cache, part, max_group, plan.prefix_many, args->workspace, s);
     if (st != NVFP4_OK) return st;
     part.out = p.o + args->total_q * heads * dim, part.lse = p.l + args->total_q * heads;
     part.table = p.table + (p.count + 1) * args->table_ld, part.lens = p.lens + p.count + 1;
     part.q_starts = args->q_starts;
     part.seqs = args->seqs, part.causal = p.a.causal;
-    st = attn_run(cache, part, args->max_queries, args->workspace, s);
+    st = attn_run(cache, part, args->max_queries, plan.own_many, args->workspace, s);
     if (st != NVFP4_OK) return st;
   }
   const int64_t items = args->max_queries * heads * (dim / 8);

@@ -197,20 +197,22 @@ def mxfp4_cache_attention(q: torch.Tensor, cache: MXFP4Cache, table: torch.Tenso
 def mxfp4_cache_attention_shared(q: torch.Tensor, cache: MXFP4Cache, table: torch.Tensor, lens: torch.Tensor,
                                  groups: torch.Tensor, shared: torch.Tensor, q_starts: torch.Tensor | None = None,
                                  max_queries: int | None = None, max_group: int | None = None,
-                                 scale: float | None = None, causal: bool = True, out: torch.Tensor | None = None,
-                                 lse: torch.Tensor | None = None, status: torch.Tensor | None = None,
-                                 stream=None) -> torch.Tensor:
+                                 scale: float | None = None, causal: bool = True, always: bool = False,
+                                 out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                                 status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """mxfp4_cache_attention of sequences that share a prefix, which is read once
     for all queries of a group.
 
     groups [n + 1] int32: first sequence of each group; shared [n] int32: tokens
     that the sequences of a group have in common (their block tables name pages
     with the same bytes there, as after mxfp4_pages_select); max_group an upper
-    bound of a group's queries (default: all of q).  The other arguments are those
-    of mxfp4_cache_attention; there is no window."""
+    bound of a group's queries (default: all of q).  Where reading the prefix by
+    every sequence is estimated to be as fast (few sequences, small block tables),
+    that is done, but with `always`.  The other arguments are those of
+    mxfp4_cache_attention; there is no window."""
     return _ext.cache_attention_shared(q, cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales, table, lens,
                                        q_starts, max_queries, scale, causal, 0, 0, out, lse, status, stream, groups,
-                                       shared, max_group)
+                                       shared, max_group, always)
 
 
 @dataclass

@@ -203,16 +203,17 @@ nvfp4_status mxfp4_cache_attention(const mxfp4_cache* cache, const mxfp4_attenti
  * mxfp4_cache_attention (causal or not, without a window) on the same
  * arguments, but tokens that the sequences of a group have in common are read
  * once for all of them.  Sequences groups[g] .. groups[g+1] - 1 share their
- * first shared[g] tokens: what their block tables name there has to hold the
- * same bytes, as after mxfp4_pages_select, and is read through the first one's.
- * Whole pages of them are shared, and only as many as lie before every query
- * of the group (not causal: as every sequence has); the others are read by
- * each sequence.  Sequences before groups[0] and from groups[count] on share
- * nothing.
+ * first shared[g] tokens: what their block tables name there holds the same
+ * bytes, as after mxfp4_pages_select, and is read through any one's.  Whole
+ * pages of them are shared, and only as many as lie before every query of the
+ * group (not causal: as every sequence has); the others are read by each
+ * sequence.  Sequences before groups[0] and from groups[count] on share nothing.
  *   groups    device int32 [count + 1], not decreasing; what lies outside
  *             0 .. seqs counts as its ends
  *   shared    device int32 [count]
  *   max_group an upper bound of the queries of a group known to the host
+ *   always    0: every sequence reads for itself where that is estimated to be
+ *             as fast, from the sizes and as if the block tables were full; 1: never
  *   args      as above, window and sinks 0, workspace_bytes of the query below
  * Precision: as above for each part; the parts are binary32 and joined in it. */
 typedef struct {
@@ -220,6 +221,8 @@ typedef struct {
   const int32_t* shared;
   int32_t count;
   int32_t max_group;
+  int32_t always;
+  int32_t reserved;
 } mxfp4_shared;
 
 /* Bytes of workspace that mxfp4_cache_attention_shared needs. */

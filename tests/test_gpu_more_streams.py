@@ -31,7 +31,7 @@ def shared(nq, n):
     def make(seed):
         c = Shared([n], [500], [600 + i for i in range(n)], [nq] * n, 8, 2, 64, seed=seed)
         args = c.q, c.cache, c.table, i32(c.lens), i32(c.groups), i32(c.prefixes), i32(c.starts), nq
-        return lambda **kw: fc2.mxfp4_cache_attention_shared(*args, **kw)
+        return lambda **kw: fc2.mxfp4_cache_attention_shared(*args, always=True, **kw)
     return make
 
 

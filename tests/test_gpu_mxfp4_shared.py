@@ -1,5 +1,6 @@
 """Attention over a shared prefix: the result of the ordinary attention, whatever
-is shared.  Compared with the binary64 definition under the bound of the cache's
+is shared, and whether the call finds that worth it or not (which changes bits, so
+that each case runs both ways).  Compared with the binary64 definition under the bound of the cache's
 tests (each part is within it, and the join's binary32 work is 2^-20 beside)."""
 import math
 
@@ -55,21 +56,27 @@ class Shared:
             self.starts.append(self.starts[-1] + n)
         self.q = torch.randn(self.starts[-1], hq, dim, generator=g, device="cuda").to(dtype)
 
-    def run(self, q=None, **kw):
+    def run(self, q=None, always=True, **kw):
         q = self.q if q is None else q
         self.lse = torch.full((len(q), q.shape[1]), 7.0, device="cuda")
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
-        starts = None if all(n == 1 for n in self.nq) and not kw.pop("explicit", False) else i32(self.starts)
+        explicit = kw.pop("explicit", False)
+        starts = None if all(n == 1 for n in self.nq) and not explicit else i32(self.starts)
         self.out = fc2.mxfp4_cache_attention_shared(q, self.cache, self.table, i32(self.lens), i32(self.groups),
                                                     i32(self.prefixes), starts, max(self.nq), lse=self.lse,
-                                                    status=status, **kw)
+                                                    status=status, always=always, **kw)
         assert int(status) == 0
         return self.out
 
     def check(self, causal=True):
         kc, vc = cache_values(self.cache)
-        check(self.out, self.lse, *mx.attention(self.q.double(), kc, vc, self.table, self.lens, self.starts, self.page,
-                                                self.dim ** -0.5, causal=causal))
+        want = mx.attention(self.q.double(), kc, vc, self.table, self.lens, self.starts, self.page, self.dim ** -0.5,
+                            causal=causal)
+        check(self.out, self.lse, *want)
+        kept = self.out, self.lse
+        self.run(always=False, causal=causal)
+        check(self.out, self.lse, *want)
+        self.out, self.lse = kept
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
@@ -167,8 +174,6 @@ def test_no_other_bytes_matter():
         s.transpose(1, 2)[~used] = 255
     c.table[1:, :4] = c.table[0, :4]
     assert torch.equal(c.run(), want)
-    c.table[1:, :4] = 1 << 30  # read through the first sequence's row
-    assert torch.equal(c.run(), want)
 
 
 @pytest.mark.parametrize("n,nq", [(4, 1), (20, 1), (3, 2)])
@@ -218,10 +223,24 @@ def test_same_bits_again_and_in_a_graph():
     for _ in range(2):  # two graphs of one pool, replayed in turn
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g, pool=graphs[0][0].pool() if graphs else None):
-            graphs.append((g, fc2.mxfp4_cache_attention_shared(*args)))
+            graphs.append((g, fc2.mxfp4_cache_attention_shared(*args, always=True)))
     for g, out in graphs + graphs:
         g.replay()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("hq,dim,n,nq", [(32, 128, 24, 1), (8, 64, 60, 1), (16, 64, 10, 3), (8, 256, 20, 1)])
+def test_by_the_estimate(hq, dim, n, nq):
+    """Large block tables are worth sharing, small ones are not: the bits of the one
+    way or of the other."""
+    c = Shared([n], [96], [100 + i for i in range(n)], [nq] * n, hq, 2, dim, seed=n)
+    shared = c.run().clone()
+    apart = c.run(always=False).clone()
+    starts = i32(c.starts)
+    assert torch.equal(apart, fc2.mxfp4_cache_attention(c.q, c.cache, c.table, i32(c.lens), starts, nq))
+    c.table = torch.cat((c.table, torch.zeros(n, 20000, dtype=torch.int32, device="cuda")), 1)
+    assert torch.equal(c.run(always=False, explicit=True), c.run(explicit=True))
+    assert not torch.equal(shared, apart)
 
 
 def test_refusals():

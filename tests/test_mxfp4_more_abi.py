@@ -28,7 +28,7 @@ class Pages(ctypes.Structure):
 
 
 class SharedArgs(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_void_p) for n in ("groups", "shared")] + [(n, ctypes.c_int32) for n in ("count", "max_group")]
+    _fields_ = [(n, ctypes.c_void_p) for n in ("groups", "shared")] + [(n, ctypes.c_int32) for n in ("count", "max_group", "always", "reserved")]
 
 
 def made(cls, defaults, kw):

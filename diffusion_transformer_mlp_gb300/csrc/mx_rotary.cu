@@ -22,15 +22,16 @@
 // four neighbouring lanes, or, where only part of a head is rotated, of any, whose
 // maxima then go through shared memory.
 //
-// What bounds it: HBM, 37,810 tokens of 84 heads of 128 in BF16 (1.63 GB) in 261 us,
-// 92% of the copy rate (FP32: 95%); with few heads or narrow ones a token's own work,
-// its angles and their products with the weights, which takes a warp about as long as
-// five steps of heads (60,000 tokens of 40 heads of 64: 121 us, 75%).  Registers decide:
-// with 96 two heads' loads are under way and nothing spills; ten blocks an SM 261 us,
-// eight 289, twelve (80 registers, spills) 275, one head under way 276.  Into the cache
-// 37,810 tokens of 32 + 8 + 8 heads (0.82 GB) 163 us, where rotating queries and keys
-// and then writing the cache take 132 + 37; twelve blocks an SM, ten 173 us, eight 196.
-// Several tokens to a warp, in turn: 271 to 293 us instead of 261.  One token: 2.9 us.
+// What bounds it: HBM, 37,810 tokens of 84 heads of 128 in BF16 (1.63 GB) in 264 us,
+// 91% of the copy rate (FP32: 94%; without a norm 96%); with few heads or narrow ones a
+// token's own work, its angles and their products with the weights, which takes a warp
+// about as long as five steps of heads (60,000 tokens of 40 heads of 64: 125 us, 73%).
+// Registers decide: with 96 two heads' loads are under way and next to nothing spills;
+// ten blocks an SM 264 us, eight 287, nine 275, eleven 346.  Into the cache 37,810 tokens
+// of 32 + 8 + 8 heads (0.82 GB) 159 us in neighbouring pairs and 167 in halves, where
+// rotating queries and keys and then writing the cache take 132 + 37; twelve blocks an
+// SM, ten 169 and 173, eight 196.  Several tokens to a warp, in turn: 271 to 293 us for
+// the first.  One token: 2.9 us.
 #include <string>
 #include <type_traits>
 
@@ -162,6 +163,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (kCache ? 12 : 10) 
     turned_b = s + eighth;
     if (s >= eighth) turned_a = 2 * s, turned_b = 2 * s + 1;  // behind the rotated ones: 2 eighth + 2 (s - eighth)
   }
+  // chunks that are not rotated
+  const bool still_a = turned_a >= 2 * eighth, still_b = turned_b >= 2 * eighth;
   // a block's four chunks are in four neighbouring lanes (of values they always are)
   const bool aligned = kNeighbours || 2 * eighth == chunks;
   const bool lane_in = head_of < at_once;
@@ -290,13 +293,21 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (kCache ? 12 : 10) 
             f[i] = x.x, f[i + 1] = x.y;
           }
         }
+        auto turn = [&](auto part) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float& a = f[kNeighbours ? 2 * j : j];
-          float& b = f[kNeighbours ? 2 * j + 1 : 8 + j];
-          const float2 y = unpair(fma2(pair_of(a, a), of_a[j], mul2(pair_of(b, b), of_b[j])));
-          a = y.x, b = y.y;
-        }
+          for (int j = 0; j < 8; ++j) {
+            float& a = f[kNeighbours ? 2 * j : j];
+            float& b = f[kNeighbours ? 2 * j + 1 : 8 + j];
+            if (decltype(part)::value && (kNeighbours && j >= 4 ? still_b : still_a)) {
+              a *= unpair(of_a[j]).x, b *= unpair(of_b[j]).y;  // an infinity stays in its place
+            } else {
+              const float2 y = unpair(fma2(pair_of(a, a), of_a[j], mul2(pair_of(b, b), of_b[j])));
+              a = y.x, b = y.y;
+            }
+          }
+        };
+        if (2 * eighth == chunks) turn(std::false_type{});
+        else turn(std::true_type{});
       }
       if (!kCache || kind == 0) {
         if (live) {

@@ -139,6 +139,26 @@ def test_large_and_special_values():
     assert int(torch.isnan(plain[5]).sum()) == 2 and bool(torch.isfinite(plain[5, 0, :60]).all())
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_what_is_not_rotated_stays_in_its_place(interleaved):
+    """An infinity or a NaN behind the pairs reaches no other element, signs of
+    zeros are kept there, and rotated ones stay in their pair."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    freq, axis, rotary = make_rotary(8, 1, interleaved, g)
+    pos = torch.arange(1, 5, device="cuda", dtype=torch.int32)
+    q = heads(4, 3, 64, g, torch.float32)
+    q[0, 0, 16], q[1, 1, 63], q[2, 2, 40], q[3, 0, 17] = math.inf, math.nan, -0.0, -math.inf
+    got, _ = fc2.head_norm_rotary(q, None, rotary, pos)
+    assert torch.equal(torch.isfinite(got), torch.isfinite(q))
+    bits = lambda t: torch.where(torch.isnan(t), 0, t.view(torch.int32))
+    assert torch.equal(bits(got)[..., 16:], bits(q)[..., 16:])
+    q[0, 1, 3] = math.inf
+    got, _ = fc2.head_norm_rotary(q, None, rotary, pos)
+    assert int((~torch.isfinite(got[0, 1])).sum()) == 2
+    none = fc2.head_rotary(torch.zeros(0))
+    assert torch.equal(bits(fc2.head_norm_rotary(q, None, none, pos)[0]), bits(q))
+
+
 def quantised_between(got, y, e):
     """got [..., dim] are MXFP4 values of y with each element off by up to e:
     blocks whose scale is certain, and in those every value between the two ends'."""

@@ -99,8 +99,8 @@ struct SplitParams {
   int32_t several;   // sequences may have several queries
   float* part_o;     // [2 * workers][rows][D] (k_attn_chunk: [D / 4][rows][4]); see part_exponent
   float2* part_ml;   // [2 * workers][rows]  (reference, sum)
-  int64_t* prefix;   // [seqs + 1] places before each sequence, written by block 0 for k_attn_combine
-  struct Cursor* start;  // [workers] first tiles of the runs, written by k_attn_chunk for k_attn_join
+  int64_t* prefix;   // [seqs + 1] places before each sequence, written by block 0 for what joins
+  struct Cursor* start;  // [workers] first tiles of the runs, written for what joins by boundaries (or null)
 };
 
 // First query row of sequence b, and the number of its queries: none outside of
@@ -219,7 +219,7 @@ __device__ __forceinline__ void cursor_next(Cursor& c, const AttnParams& a, int3
 }
 
 // Places before each sequence, in prefix[0 .. seqs] (kMaxSeqs + 1 + kThreads
-// entries of shared memory); block 0 leaves them for k_attn_combine.  With few
+// entries of shared memory); block 0 leaves them for what joins.  With few
 // sequences up to 32 threads share the row tiles of one.  Then every thread sums
 // a run of sequences and the first warp scans the runs' sums.
 template <int kThreads>
@@ -310,6 +310,24 @@ __device__ __forceinline__ void store_o8(const AttnParams& a, int64_t off, const
   for (int i = 0; i < 4; ++i)
     w[i] = a.bf16 ? f32_to_word<__nv_bfloat16>(f[2 * i], f[2 * i + 1]) : f32_to_word<__half>(f[2 * i], f[2 * i + 1]);
   store_o8_words(a, static_cast<uint16_t*>(a.out) + off, make_uint4(w[0], w[1], w[2], w[3]));
+}
+
+// Four of them.
+__device__ __forceinline__ void store_o4(const AttnParams& a, int64_t off, const float (&f)[4]) {
+  if (a.o_f32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + off) = make_float4(f[0], f[1], f[2], f[3]);
+    return;
+  }
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    w[i] = a.bf16 ? f32_to_word<__nv_bfloat16>(f[2 * i], f[2 * i + 1]) : f32_to_word<__half>(f[2 * i], f[2 * i + 1]);
+  uint16_t* dst = static_cast<uint16_t*>(a.out) + off;
+  if (a.o_vec) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  } else {
+    dst[0] = uint16_t(w[0]), dst[1] = uint16_t(w[0] >> 16), dst[2] = uint16_t(w[1]), dst[3] = uint16_t(w[1] >> 16);
+  }
 }
 
 // Keys that only some rows see.  Both kernels put the values of all rows of a

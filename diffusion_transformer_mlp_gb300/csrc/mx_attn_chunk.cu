@@ -28,7 +28,7 @@
 //
 // What bounds it: the issue slots and latencies of the softmax and decoding
 // warps (57% of the slots used, tensor pipe 50%).  Two prompts' chunks of 2,048
-// queries on 4,099 and 8,192 keys, 32 / 8 heads, dim 128: 277 us, 1.1 PFLOP/s.
+// queries on 4,099 and 8,192 keys, 32 / 8 heads, dim 128: 273 us, 1.1 PFLOP/s.
 // Five kinds of warps run at once, so the loops are kept short enough for the
 // instruction caches (fully unrolled: 430 us).
 //

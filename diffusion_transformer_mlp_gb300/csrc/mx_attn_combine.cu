@@ -58,8 +58,8 @@ __global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_c
   if (parts <= kFewParts) {
     // Short sequences: a thread an item, with all its loads at once and no barrier.
     // The sums are those of the way below, in its order and with its roundings, so
-    // that results do not depend on where a run ends (192 sequences of 33 to 1,025
-    // keys, 8 heads: 14.6 us without this, so 13.2).
+    // that results do not depend on where a run ends (120 sequences of 32 to 1,025
+    // keys, 8 heads: the pass 41.6 us without this, so 39.7; 16 of them 15.2 and 14.7).
     const int item = threadIdx.x;
     const int32_t r = item / (kCols / 8), d = col0 + item % (kCols / 8) * 8;
     if (item >= kItems || r >= live) return;
@@ -169,6 +169,122 @@ __global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_c
   write(r, d, f, l == 0.0f ? -INFINITY : (row_m[r] + kJoinLog2 - kWeightLog2 + log2f(l)) * 0.6931471805599453f);
 }
 
+// The same where segments are many and thus short: not a block for each of them, most
+// of which a worker has all of, but warps for each boundary between two workers' runs
+// that lies in a segment; those of a segment of several such boundaries share its rows.
+// A lane is a row and four columns.  A row's weights are worked out by its kLanes
+// lanes, a partial each at a time, and passed on by shuffles.  All sums are in the
+// order, and with the roundings, of k_attn_combine's, so that a result does not depend
+// on which of them joins it.  Warps behind those write the rows that see no key.
+// 192 sequences of 33 to 1,025 keys, 8 heads: writing and attending 54.9 us by
+// segments, most of whose instructions looked for partials that were not there, and
+// 49.5 so (with eight columns a lane 49.7, but a long sequence among short ones up to
+// 13 us slower).
+constexpr int kBoundaryThreads = 128, kUnder = 8;  // loads under way
+
+template <int D, int kRows>
+__global__ void __launch_bounds__(kBoundaryThreads)
+    k_attn_combine_boundaries(const __grid_constant__ SplitParams sp, int32_t tok) {
+  constexpr int kLanes = D == 64 ? 16 : 32, kAtOnce = 32 / kLanes;  // lanes of a row, rows of a warp
+  constexpr int kPieces = D / 4 / kLanes;  // of a row
+  constexpr int kSlices = 32 / kRows, kSums = 256 / kRows;  // of k_attn_combine's threads: partials of a row's outputs, sums
+  constexpr int kAtATime = kLanes < kSums ? kLanes : kSums;  // partials
+  constexpr int kHeld = kSums / kAtATime;
+  constexpr int kSplit = 4;  // warps of a boundary
+  const AttnParams& a = sp.a;
+  const int lane = threadIdx.x & 31, col = lane % kLanes, lane0 = lane - col;
+  const int32_t unit = int32_t(blockIdx.x * (kBoundaryThreads / 32) + (threadIdx.x >> 5)), w = unit / kSplit,
+                part_of_unit = unit - w * kSplit;
+  grid_wait();
+  Cursor c;
+  auto write = [&](int32_t row, int32_t d, const float (&f)[4], float lse) {
+    if (row >= c.nq * a.group) return;
+    const int32_t qi = row / a.group, hq = c.h * a.group + row - qi * a.group;
+    store_o4(a, int64_t(c.q0 + qi) * a.o_st + int64_t(hq) * a.o_sh + d, f);
+    if (d == 0 && a.lse != nullptr) a.lse[int64_t(c.q0 + qi) * (a.kv_heads * a.group) + hq] = lse;
+  };
+  if (w >= sp.workers) {
+    c.b = w - sp.workers;
+    if (c.b >= a.seqs) return;
+    cursor_seq(c, a);
+    const float zero[4] = {};
+    for (c.rt = 0; c.rt * kRows < c.nq * a.group && row_span(a, c.len, c.nq, c.rt, kRows, tok).n == 0; ++c.rt)
+      for (c.h = part_of_unit; c.h < a.kv_heads; c.h += kSplit)
+        for (int32_t i = lane; i < kRows * (D / 4); i += 32)
+          write(c.rt * kRows + i / (D / 4), i % (D / 4) * 4, zero, -INFINITY);
+    return;
+  }
+  const int64_t total = sp.prefix[a.seqs];
+  c = sp.start[w];  // not written of workers without a run, and not looked at
+  const int32_t workers = live_workers(sp, total);
+  if (w == 0 || w >= workers || c.t == 0) return;
+  const int64_t first = worker_start(total, w, workers) - c.t;  // place of the segment's first tile
+  const int32_t begin = worker_of(total, first, workers);
+  const int32_t parts = worker_of(total, first + c.s.n - 1, workers) - begin + 1;
+  const int32_t slot0 = worker_start(total, begin, workers) == first ? 0 : 1;
+  auto row_of = [&](int32_t i, int32_t r) { return (int64_t(begin + i) * 2 + (i == 0 ? slot0 : 0)) * kRows + r; };
+  const int32_t live = min(kRows, c.nq * a.group - c.rt * kRows);
+  for (int32_t x0 = (w - begin - 1) * kSplit + part_of_unit; x0 * kAtOnce < live * kPieces; x0 += (parts - 1) * kSplit) {
+    const int32_t r = x0 / kPieces * kAtOnce + lane / kLanes;  // less than kRows
+    const int32_t d = (x0 % kPieces * kLanes + col) * 4;
+    float m = -INFINITY;
+    for (int32_t i = col; i < parts; i += kLanes) m = fmaxf(m, sp.part_ml[row_of(i, r)].x);
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const float ref = m == -INFINITY ? 0.0f : m + kJoinLog2;
+    float l[kHeld] = {}, f[kSlices][4] = {};
+    for (int32_t i0 = 0; i0 < parts; i0 += kSums) {
+#pragma unroll
+      for (int x = 0; x < kHeld; ++x) {
+        const int32_t from = i0 + x * kAtATime;
+        if (from >= parts) break;
+        float weight = 0.0f;
+        if (col < kAtATime && from + col < parts) {
+          const float2 ml = sp.part_ml[row_of(from + col, r)];
+          weight = exp2_approx(ml.x - ref);
+          l[x] = __fmaf_rn(ml.y, weight, l[x]);
+        }
+        const int32_t n = min(parts - from, kAtATime);
+#pragma unroll 1
+        for (int32_t i = 0; i < n; i += kUnder) {
+          float4 u[kUnder];
+#pragma unroll
+          for (int k = 0; k < kUnder; ++k) {
+            if (i + k >= n) break;
+            u[k] = *reinterpret_cast<const float4*>(sp.part_o + row_of(from + i + k, r) * D + d);
+          }
+#pragma unroll
+          for (int k = 0; k < kUnder; ++k) {
+            if (i + k >= n) break;
+            const float g = __shfl_sync(0xFFFFFFFFu, weight, lane0 + i + k);
+            const float y[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[k % kSlices][e] = __fmaf_rn(y[e], g, f[k % kSlices][e]);
+          }
+        }
+      }
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int x = 0; x < kHeld; ++x) {
+      if (x * kAtATime >= parts) break;
+#pragma unroll
+      for (int o = 1; o < kSlices; o <<= 1) l[x] += __shfl_xor_sync(0xFFFFFFFFu, l[x], o);
+      for (int32_t i = 0; i < min(parts - x * kAtATime, kAtATime); i += kSlices)
+        sum = __fadd_rn(sum, __shfl_sync(0xFFFFFFFFu, l[x], lane0 + i));
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+      for (int x = 1; x < kSlices; ++x) f[0][e] = __fadd_rn(f[0][e], f[x][e]);
+      f[0][e] *= inv;
+    }
+    if (r < live)
+      write(c.rt * kRows + r, d, f[0], sum == 0.0f ? -INFINITY : (m + kJoinLog2 - kWeightLog2 + log2f(sum)) * 0.6931471805599453f);
+  }
+}
+
 // The same for segments of 128 or 256 rows.  Of those few are split, at the
 // boundaries between two workers' runs: blocks (x, w) are for the segment that
 // worker w's run starts inside of, whose columns they share with the blocks of
@@ -240,6 +356,12 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ Split
 
 template <int D, int kRows>
 nvfp4_status combine_launch(int tok, int row_tiles, const SplitParams& sp, cudaStream_t stream) {
+  if (sp.start != nullptr) {
+    constexpr int64_t kSplit = 4, kWarps = kBoundaryThreads / 32;
+    return launch("launch k_attn_combine_boundaries", k_attn_combine_boundaries<D, kRows>,
+                  dim3(unsigned((kSplit * (sp.workers + sp.a.seqs) + kWarps - 1) / kWarps)), dim3(kBoundaryThreads), 0, 0,
+                  stream, sp, int32_t(tok));
+  }
   const bool few = int64_t(sp.a.kv_heads) * row_tiles * sp.a.seqs < 128;
   return launch("launch k_attn_combine", few ? k_attn_combine<D, kRows, 32> : k_attn_combine<D, kRows, 64>,
                 dim3(unsigned(sp.a.kv_heads) * (D / (few ? 32 : 64)), unsigned(row_tiles), unsigned(sp.a.seqs)),

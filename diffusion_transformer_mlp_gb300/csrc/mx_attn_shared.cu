@@ -23,8 +23,8 @@
 // tiles, before the work itself.  Two prompts of 16,001 and 12,001 tokens, 32 and 16
 // sequences, 32 / 8 heads of 128: parts 3.7, prefixes 35, their join 7.1, own tokens
 // 11.1, their join 6.3, this join 2.9 us; the pass 63 us, 185 if each sequence reads
-// its prompt.  One of 32,769 tokens, 128 sequences of 64 heads: 166 us instead of
-// 1,009; 118 of them are k_attn_chunk at 61% of the tensor rate.  Where reading
+// its prompt.  One of 32,769 tokens, 128 sequences of 64 heads: 163 us instead of
+// 1,009; 117 of them are k_attn_chunk at 61% of the tensor rate.  Where reading
 // prefixes each time is as fast, that is done (plan_of).
 #include <algorithm>
 #include <string>

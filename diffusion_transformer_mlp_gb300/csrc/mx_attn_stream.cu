@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows, kSeveral>::kCtas)
   __syncthreads();
   if (tiles <= 0) return;
   if (kSeveral && lane == 0) *start = cu;
+  if (sp.start != nullptr && lane == 0) sp.start[worker] = cu;
 
   // ---- loads: lane i < boxes takes box i of a tile (a page's share of it);
   // its page is looked up when the tile before is issued
@@ -758,6 +759,13 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows, kSeveral>::kCtas)
   }
 }
 
+// From so many segments on (sequences times kv heads times row tiles) partials are joined
+// by boundaries between runs (k_attn_combine_boundaries), below by segments.  8 heads of
+// 128, sequences of 32 to 1,025 keys, by boundaries / segments: 32 of them 20.5 / 20.3 us,
+// 128 38.7 / 41.0, 512 112 / 131; with one of 20,000 keys among them 34.0 / 29.7,
+// 50.2 / 50.4, 112 / 131: a long one has many partials, for which a block is better.
+constexpr int64_t kManySegments = 1024;
+
 template <int D, int kRows, bool kSeveral>
 nvfp4_status stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams& sp, int row_tiles,
                            cudaStream_t stream) {
@@ -768,6 +776,7 @@ nvfp4_status stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, const S
   if (st != NVFP4_OK) return st;
   SplitParams p = sp;
   p.workers = T::kCtas * sm_count() * kWarps;
+  if (int64_t(p.a.kv_heads) * row_tiles * p.a.seqs < kManySegments) p.start = nullptr;
   p.least = 1, p.edge = 0, p.even = 4;  // 16,000 keys, 8 heads, dim 128: 24.2 us, without 29.0
   st = launch("launch k_attn_stream", kern, dim3(unsigned(p.workers / kWarps)), dim3(kThreads), T::kSmem, 0, stream, tk,
               tv, p);
@@ -787,11 +796,13 @@ int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 // Rows of partials: two a worker, the most of any variant (16 rows of 2 blocks
 // an SM; 8 rows of 3 have fewer).
 int64_t partial_rows() { return 2 * int64_t(sm_count()) * kWarps * 32; }
+int64_t most_workers() { return 3 * int64_t(sm_count()) * kWarps; }
 
 }  // namespace
 
 int64_t attn_stream_workspace(int32_t dim) {
-  return align256(partial_rows() * dim * 4) + align256(partial_rows() * 8) + align256((kMaxSeqs + 1) * 8);
+  return align256(partial_rows() * dim * 4) + align256(partial_rows() * 8) + align256((kMaxSeqs + 1) * 8) +
+         align256(most_workers() * int64_t(sizeof(Cursor)));
 }
 
 nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32_t max_queries, void* workspace,
@@ -819,6 +830,7 @@ nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32
   sp.part_ml = reinterpret_cast<float2*>(ws + align256(partial_rows() * dim * 4));
   sp.prefix =
       reinterpret_cast<int64_t*>(ws + align256(partial_rows() * dim * 4) + align256(partial_rows() * 8));
+  sp.start = reinterpret_cast<Cursor*>(reinterpret_cast<uint8_t*>(sp.prefix) + align256((kMaxSeqs + 1) * 8));
   const int64_t row_tiles = (rows_max + rows - 1) / rows;
   if (row_tiles > 65535) return fail(NVFP4_EUNSUPPORTED, "mxfp4_cache_attention: too many query rows a sequence");
   // kMaxSeqs sequences a launch; the workspace is reused in stream order

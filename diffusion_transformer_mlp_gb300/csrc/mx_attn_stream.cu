@@ -43,7 +43,7 @@
 // pipe is above 37% and DRAM at 42%; each works through the chain ldmatrix, cvt,
 // MMA, FMA, ex2, cvt, MMA of 32 keys at a time, and more warps do not fit beside Q,
 // the scores and the output in registers.  32 conversations of 257 to 32,767 keys,
-// 8 rows of 8 heads, dim 128 (246 MB): 73 us, 3.4 TB/s; with the join 83 us.  Three
+// 8 rows of 8 heads, dim 128 (246 MB): 73 us, 3.4 TB/s; with the join 82 us.  Three
 // blocks an SM at 168 registers are 5 to 17% faster than two at 231, although a few
 // registers spill.
 #include <algorithm>
@@ -177,7 +177,9 @@ __device__ __noinline__ void check_run(const SplitParams& sp, const Cursor* star
   });
 }
 
-template <int D, int kRows, bool kSeveral>
+// kFew: up to 32 sequences, which each warp counts for itself.  (A branch instead of a
+// variant: the tiles' loop is compiled differently, and 192 sequences take 1 us more.)
+template <int D, int kRows, bool kSeveral, bool kFew>
 __global__ void __launch_bounds__(kThreads, Tile<D, kRows, kSeveral>::kCtas)
     k_attn_stream(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                   const __grid_constant__ SplitParams sp) {
@@ -205,17 +207,31 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows, kSeveral>::kCtas)
     prefetch_tmap(&tmap_v);
   }
   grid_wait();
-  tile_counts<kThreads>(sp, prefix, kRows, kTok);
-
-  const int64_t total = prefix[a.seqs];
+  WarpCounts counts;
+  int64_t total;
+  if constexpr (kFew) {
+    counts = warp_counts(sp, kRows, kTok);
+    total = __shfl_sync(0xFFFFFFFFu, counts.upto, 31);
+  } else {
+    tile_counts<kThreads>(sp, prefix, kRows, kTok);
+    total = prefix[a.seqs];
+  }
   // the first workers lie in different blocks: few tiles spread over all SMs
   const int32_t worker = warp * int32_t(gridDim.x) + int32_t(blockIdx.x);
   const int32_t workers = live_workers(sp, total);
   const int64_t x0 = worker < workers ? worker_start(total, worker, workers) : 0;
   const int32_t tiles = worker < workers ? int32_t(worker_start(total, worker + 1, workers) - x0) : 0;
   Cursor cu;
-  if (tiles > 0) cursor_at(cu, a, prefix, x0, kRows, kTok, 0);
-  fence_proxy_async_smem();  // the counts are read, the TMA may write there
+  if constexpr (kFew) {
+    if (tiles > 0) cursor_at(cu, a, counts, x0, kRows, kTok, 0);
+    if (worker == 0) {
+      if (lane < a.seqs) sp.prefix[lane] = counts.upto - counts.n;
+      if (lane == 31) sp.prefix[a.seqs] = total;
+    }
+  } else {
+    if (tiles > 0) cursor_at(cu, a, prefix, x0, kRows, kTok, 0);
+    fence_proxy_async_smem();  // the counts are read, the TMA may write there
+  }
   __syncthreads();
   if (tiles <= 0) return;
   if (kSeveral && lane == 0) *start = cu;
@@ -766,11 +782,11 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows, kSeveral>::kCtas)
 // 50.2 / 50.4, 112 / 131: a long one has many partials, for which a block is better.
 constexpr int64_t kManySegments = 1024;
 
-template <int D, int kRows, bool kSeveral>
+template <int D, int kRows, bool kSeveral, bool kFew = false>
 nvfp4_status stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams& sp, int row_tiles,
                            cudaStream_t stream) {
   using T = Tile<D, kRows, kSeveral>;
-  auto kern = k_attn_stream<D, kRows, kSeveral>;
+  auto kern = k_attn_stream<D, kRows, kSeveral, kFew>;
   static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
   nvfp4_status st = allow_smem(reinterpret_cast<const void*>(kern), T::kSmem, ready);
   if (st != NVFP4_OK) return st;
@@ -787,7 +803,8 @@ nvfp4_status stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, const S
 template <int D>
 nvfp4_status launch_of(int rows, const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams& sp, int row_tiles,
                        cudaStream_t stream) {
-  auto f = rows == 8 ? (sp.several ? stream_launch<D, 8, true> : stream_launch<D, 8, false>)
+  auto f = rows == 8 ? (sp.several ? stream_launch<D, 8, true>
+                                : (sp.a.seqs <= 32 ? stream_launch<D, 8, false, true> : stream_launch<D, 8, false>))
                      : (sp.several ? stream_launch<D, 16, true> : stream_launch<D, 16, false>);
   return f(tk, tv, sp, row_tiles, stream);
 }

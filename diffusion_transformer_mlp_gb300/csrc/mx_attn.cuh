@@ -204,23 +204,26 @@ __device__ __forceinline__ int32_t cursor_at(Cursor& c, const AttnParams& a, con
   return cursor_in(c, a, x - prefix[lo], rows, tok, edge);
 }
 
-// Up to 32 sequences, one a lane: every warp counts for itself, without shared memory
-// and barriers (decoding 1 to 32 sequences takes 0.7 to 1.1 us less: one of 1,023 keys
-// 12.6 us instead of 13.5, 32 of 257 to 32,767 81.7 instead of 82.4).
+// Up to 32 sequences, each in `share` lanes (a power of two) that have its row tiles in
+// turn: a warp counts for itself, without shared memory and barriers (decoding 1 to 32
+// sequences takes 0.7 to 1.1 us less: one of 1,023 keys 12.6 us instead of 13.5, 32 of
+// 257 to 32,767 81.7 instead of 82.4).
 struct WarpCounts {
-  int32_t len, nq, q0;
-  int64_t n, upto;  // places of the sequence, and with those before it
+  int32_t share, len, nq, q0;
+  int64_t n, upto;  // places of the sequence (in its first lane), and with those before it
 };
-__device__ __forceinline__ WarpCounts warp_counts(const SplitParams& sp, int32_t rows, int32_t tok) {
+__device__ __forceinline__ WarpCounts warp_counts(const SplitParams& sp, int32_t rows, int32_t tok, int32_t share) {
   const AttnParams& a = sp.a;
-  const int lane = threadIdx.x & 31;
-  WarpCounts w = {0, 0, 0, 0, 0};
-  if (lane < a.seqs) {
-    w.len = a.lens[lane], w.nq = seq_queries(a, lane), w.q0 = seq_start(a, lane);
-    for (int32_t rt = 0; rt * rows < w.nq * a.group; ++rt)
+  const int lane = threadIdx.x & 31, b = lane / share;
+  WarpCounts w = {share, 0, 0, 0, 0, 0};
+  if (b < a.seqs) {
+    w.len = a.lens[b], w.nq = seq_queries(a, b), w.q0 = seq_start(a, b);
+    for (int32_t rt = lane & (share - 1); rt * rows < w.nq * a.group; rt += share)
       if (const int32_t t = row_span(a, w.len, w.nq, rt, rows, tok).n; t > 0) w.n += t + sp.edge;
     w.n *= a.kv_heads;
   }
+  for (int o = 1; o < share; o <<= 1) w.n += __shfl_xor_sync(0xFFFFFFFFu, w.n, o);
+  if ((lane & (share - 1)) != 0) w.n = 0;
   w.upto = w.n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -229,12 +232,19 @@ __device__ __forceinline__ WarpCounts warp_counts(const SplitParams& sp, int32_t
   }
   return w;
 }
+__device__ __forceinline__ int64_t all_places(const WarpCounts& w) { return __shfl_sync(0xFFFFFFFFu, w.upto, 31); }
+__device__ __forceinline__ void leave_places(const SplitParams& sp, const WarpCounts& w) {  // for what joins
+  const int lane = threadIdx.x & 31, b = lane / w.share;
+  if ((lane & (w.share - 1)) == 0 && b < sp.a.seqs) sp.prefix[b] = w.upto - w.n;
+  if (lane == 31) sp.prefix[sp.a.seqs] = w.upto;
+}
 __device__ __forceinline__ int32_t cursor_at(Cursor& c, const AttnParams& a, const WarpCounts& w, int64_t x, int32_t rows,
                                              int32_t tok, int32_t edge) {
-  c.b = max(__ffs(__ballot_sync(0xFFFFFFFFu, x < w.upto)) - 1, 0);
-  c.len = __shfl_sync(0xFFFFFFFFu, w.len, c.b), c.nq = __shfl_sync(0xFFFFFFFFu, w.nq, c.b);
-  c.q0 = __shfl_sync(0xFFFFFFFFu, w.q0, c.b);
-  return cursor_in(c, a, x - __shfl_sync(0xFFFFFFFFu, w.upto - w.n, c.b), rows, tok, edge);
+  const int at = max(__ffs(__ballot_sync(0xFFFFFFFFu, x < w.upto)) - 1, 0);
+  c.b = at / w.share;
+  c.len = __shfl_sync(0xFFFFFFFFu, w.len, at), c.nq = __shfl_sync(0xFFFFFFFFu, w.nq, at);
+  c.q0 = __shfl_sync(0xFFFFFFFFu, w.q0, at);
+  return cursor_in(c, a, x - __shfl_sync(0xFFFFFFFFu, w.upto - w.n, at), rows, tok, edge);
 }
 
 // The next tile; the caller knows that there is one.

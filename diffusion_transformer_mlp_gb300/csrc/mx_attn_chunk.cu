@@ -218,32 +218,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
   uint8_t* staging = sv + kSlots * T::kKvBytes;
   Shared& sh = *reinterpret_cast<Shared*>(staging + T::kWarpD * T::kStage);
   const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  grid_wait();
-
-  // this block's run of tiles
-  int32_t tiles = 0;
-  {
-    int64_t* prefix = reinterpret_cast<int64_t*>(smem);
-    tile_counts<T::kThreads>(sp, prefix, kRows, kTK);
-    const int64_t total = prefix[a.seqs];
-    const int32_t workers = live_workers(sp, total), w = int32_t(blockIdx.x);
-    if (w < workers) {
-      const int64_t x0 = worker_start(total, w, workers);
-      if (warp == 0) {
-        Cursor first;
-        const int32_t skip = cursor_at(first, a, prefix, x0, kRows, kTK, sp.edge);
-        if (lane == 0) {
-          sh.first = first, sp.start[w] = first;
-          sh.places = int32_t(worker_start(total, w + 1, workers) - x0) - skip;
-        }
-      }
-      __syncthreads();  // the counts are read, the first tile is known
-      tiles = sh.places;
-    }
-  }
-  if (tiles <= 0) return;  // no worker, or nothing but the room before a segment
-
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 32) {
     mbar_init(&sh.done, kNQ);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sh.ref_full[i], 1);
@@ -265,10 +240,43 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     sh.check = 0;
     fence_barrier_init();
   }
+  grid_wait();
   if (warp == T::kWarpMma) tmem_alloc(&sh.tmem, T::kTmem);
+
+  // this block's run of tiles: up to 32 sequences are counted by the first warp alone
+  auto begin_at = [&](int64_t total, const auto& counts) {
+    const int32_t workers = live_workers(sp, total), w = int32_t(blockIdx.x);
+    int32_t places = 0;
+    if (w < workers) {
+      const int64_t x0 = worker_start(total, w, workers);
+      Cursor first;
+      const int32_t skip = cursor_at(first, a, counts, x0, kRows, kTK, sp.edge);
+      places = int32_t(worker_start(total, w + 1, workers) - x0) - skip;
+      if (lane == 0) sh.first = first, sp.start[w] = first;
+    }
+    if (lane == 0) sh.places = places;
+  };
+  if (a.seqs <= 32) {
+    if (warp == 0) {
+      int share = 1;
+      while (a.seqs * share * 2 <= 32) share *= 2;
+      const WarpCounts counts = warp_counts(sp, kRows, kTK, share);
+      if (blockIdx.x == 0) leave_places(sp, counts);
+      begin_at(all_places(counts), counts);
+    }
+  } else {
+    int64_t* prefix = reinterpret_cast<int64_t*>(smem);
+    tile_counts<T::kThreads>(sp, prefix, kRows, kTK);
+    if (warp == 0) begin_at(prefix[a.seqs], prefix);
+  }
   tc_fence_before();
-  __syncthreads();
+  __syncthreads();  // the counts are read, the first tile is known
   tc_fence_after();
+  const int32_t tiles = sh.places;
+  if (tiles <= 0) {  // no worker, or nothing but the room before a segment
+    if (warp == T::kWarpMma) tmem_dealloc(sh.tmem, T::kTmem);
+    return;
+  }
   const uint32_t tmem = sh.tmem;
   const volatile int* abort_flag = &sh.abort_flag;
   // Every warp walks the segments of the run for itself.

@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows, kSeveral>::kCtas)
   WarpCounts counts;
   int64_t total;
   if constexpr (kFew) {
-    counts = warp_counts(sp, kRows, kTok);
-    total = __shfl_sync(0xFFFFFFFFu, counts.upto, 31);
+    counts = warp_counts(sp, kRows, kTok, 1);
+    total = all_places(counts);
   } else {
     tile_counts<kThreads>(sp, prefix, kRows, kTok);
     total = prefix[a.seqs];
@@ -224,10 +224,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows, kSeveral>::kCtas)
   Cursor cu;
   if constexpr (kFew) {
     if (tiles > 0) cursor_at(cu, a, counts, x0, kRows, kTok, 0);
-    if (worker == 0) {
-      if (lane < a.seqs) sp.prefix[lane] = counts.upto - counts.n;
-      if (lane == 31) sp.prefix[a.seqs] = total;
-    }
+    if (worker == 0) leave_places(sp, counts);
   } else {
     if (tiles > 0) cursor_at(cu, a, prefix, x0, kRows, kTok, 0);
     fence_proxy_async_smem();  // the counts are read, the TMA may write there

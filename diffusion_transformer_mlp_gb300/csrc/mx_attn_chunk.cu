@@ -28,7 +28,7 @@
 //
 // What bounds it: the issue slots and latencies of the softmax and decoding
 // warps (57% of the slots used, tensor pipe 50%).  Two prompts' chunks of 2,048
-// queries on 4,099 and 8,192 keys, 32 / 8 heads, dim 128: 273 us, 1.1 PFLOP/s.
+// queries on 4,099 and 8,192 keys, 32 / 8 heads, dim 128: 266 us, 1.2 PFLOP/s.
 // Five kinds of warps run at once, so the loops are kept short enough for the
 // instruction caches (fully unrolled: 430 us).
 //
@@ -323,9 +323,11 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
     // The warp's queries into shared memory, a row's largest element going to
     // [2^13, 2^14) and the sign of the softmax scale onto the elements.  D / 8
     // lanes load a row, so that the loads are of whole rows (a thread that
-    // loads its own row: 13,000 cycles for all rows); then a thread scales its own
-    // row in place.  Returns the factor of this thread's scores.
-    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRound = kLanes < 16 ? kLanes : 16;
+    // loads its own row: 13,000 cycles for all rows), by asynchronous copies
+    // (through registers, 16 of them under way: the two prompts 272 us instead of
+    // 266); then a thread scales its own row in place.  Returns the factor of this
+    // thread's scores.
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kAhead = D == 64 ? 4 : 2;
     auto load_q = [&](const Cursor& c) -> float {
       const int32_t row = c.rt * kRows + qt * 128 + r;
       int64_t off = -1;
@@ -341,23 +343,29 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
         return reinterpret_cast<uint4*>(dst + (ch / 8) * (128 * 128) + rq * 128 + (((ch & 7) ^ (rq & 7)) << 4));
       };
       // small loops, as straight-line code that runs once is slow to fetch
-#pragma unroll 1
-      for (int i0 = 0; i0 < kLanes; i0 += kRound) {
-        uint4 v[kRound];
-#pragma unroll
-        for (int i = 0; i < kRound; ++i) {
-          const int64_t o = __shfl_sync(0xFFFFFFFFu, off, (i0 + i) * kAtOnce + lane / kLanes);
-          const uint16_t* e = src + o;
-          v[i] = make_uint4(0, 0, 0, 0);
-          if (o >= 0) v[i] = a.q_vec ? *reinterpret_cast<const uint4*>(e) : load_8x16(e);
+      if (a.q_vec) {
+#pragma unroll 2
+        for (int i = 0; i < kLanes; ++i) {
+          const int64_t o = __shfl_sync(0xFFFFFFFFu, off, i * kAtOnce + lane / kLanes);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           smem_u32(place(q * 32 + i * kAtOnce + lane / kLanes, col))),
+                       "l"(src + max(o, int64_t(0))), "r"(o >= 0 ? 16 : 0)
+                       : "memory");
         }
-#pragma unroll
-        for (int i = 0; i < kRound; ++i) *place(q * 32 + (i0 + i) * kAtOnce + lane / kLanes, col) = v[i];
+        asm volatile("cp.async.wait_all;" ::: "memory");
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kLanes; ++i) {
+          const int64_t o = __shfl_sync(0xFFFFFFFFu, off, i * kAtOnce + lane / kLanes);
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (o >= 0) v = load_8x16(src + o);
+          *place(q * 32 + i * kAtOnce + lane / kLanes, col) = v;
+        }
       }
       __syncwarp();
       // magnitudes of 16-bit floats are in the order of their bits (NaN above all)
       uint32_t top = 0;
-#pragma unroll 2
+#pragma unroll kAhead
       for (int i = 0; i < kLanes; ++i) {
         const uint4 v = *place(r, i);
         top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
@@ -368,7 +376,7 @@ __global__ void __launch_bounds__(Chunk<D>::kThreads, 1)
       const int32_t eb = int32_t(__float_as_uint(value(top).x) >> 23) & 0xFF;
       const int32_t up = (eb == 0 || eb == 255) ? 0 : min(126, 140 - eb);
       const float mul = a.scale_log2 < 0.0f ? -pow2i(up) : pow2i(up);
-#pragma unroll 2
+#pragma unroll kAhead
       for (int i = 0; i < kLanes; ++i) {
         const uint4 v = *place(r, i);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};

@@ -4,6 +4,7 @@ workers' runs; a long sequence among them has many."""
 import pytest
 import torch
 
+import diffusion_transformer_mlp_gb300 as fc2
 from test_gpu_mxfp4_cache import check, run_attention
 
 pytestmark = pytest.mark.gpu
@@ -44,3 +45,14 @@ def test_rows_of_several_tiles():
 def test_window_and_sinks():
     lens = lengths(40, 11, [(7, 6000), (30, 9000)])
     check(*run_attention(lens, [1] * 40, 64, 32, 64, 64, torch.bfloat16, seed=12, window=2500, sinks=3)[:5])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_queries_at_odd_places(dim):
+    """Rows of a kv head by the hundred, whose loads are not aligned to 16 bytes: the same bits."""
+    out, lse, _, _, _, (q, cache, table, lens, starts, most) = run_attention(
+        [300, 77, 5], [200, 77, 9], 6, 2, dim, 16, torch.bfloat16, seed=15)
+    wide = torch.zeros(len(q), 6, dim + 3, dtype=q.dtype, device="cuda")
+    wide[..., 1:dim + 1] = q
+    odd = fc2.mxfp4_cache_attention(wide[..., 1:dim + 1], cache, table, lens, q_starts=starts, max_queries=most)
+    assert torch.equal(odd.view(torch.int16), out.view(torch.int16))

@@ -254,3 +254,23 @@ def test_refusals():
             f(c.q, c.cache, c.table, lens, *args, **kw)
     with pytest.raises(ValueError, match="gradient"):
         f(c.q.clone().requires_grad_(), c.cache, c.table, lens, groups, shared)
+
+
+@pytest.mark.parametrize("hq,nq", [(8, 1), (256, 1), (32, 5)])
+def test_pages_past_32_bits(hq, nq):
+    """Pages behind 4 GB of codes: the bits of the same pages in a small cache."""
+    big, small = fc2.empty_mxfp4_cache(16420, 256, 8, 256), fc2.empty_mxfp4_cache(24, 256, 8, 256)
+    assert big.k_codes.numel() > 1 << 32
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for name in ("k_codes", "v_codes", "k_scales", "v_scales"):
+        t = getattr(small, name)
+        t.random_(0, 256, generator=g) if "codes" in name else t.random_(118, 128, generator=g)
+        getattr(big, name)[16396:] = t
+    table = torch.randperm(24, generator=torch.Generator().manual_seed(4)).to(torch.int32).reshape(3, 8)
+    table[1:, :4] = table[0, :4]
+    q = torch.randn(3 * nq, hq, 256, generator=g, device="cuda").bfloat16()
+    args = i32([0, 3]), i32([1024]), i32([0, nq, 2 * nq, 3 * nq]), nq
+    for always in (False, True):
+        out = [fc2.mxfp4_cache_attention_shared(q, c, (table + add).cuda(), i32([2000, 1500, 1100]), *args,
+                                                always=always) for c, add in ((small, 0), (big, 16396))]
+        assert torch.equal(out[0].view(torch.int16), out[1].view(torch.int16))

@@ -10,10 +10,10 @@ namespace nvfp4 {
 nvfp4_status check_cache(const mxfp4_cache* cache, int* page_shift, const std::string& nm);
 int64_t attn_stream_workspace(int32_t dim);
 int64_t attn_chunk_workspace(int32_t dim);
-nvfp4_status attn_chunk(const mxfp4_cache* cache, const AttnParams& base, int32_t max_queries, void* workspace,
-                        cudaStream_t stream);
-nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32_t max_queries, void* workspace,
-                         cudaStream_t stream);
+nvfp4_status attn_chunk(const mxfp4_cache* cache, const AttnParams& base, int32_t b, int32_t max_queries,
+                        void* workspace, cudaStream_t stream, Pending& w);
+nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32_t b, int32_t max_queries,
+                         void* workspace, cudaStream_t stream, Pending& w);
 
 namespace {
 // Which kernel takes the rows (queries x heads of the group) of a sequence's kv
@@ -101,9 +101,23 @@ nvfp4_status attn_params(const mxfp4_cache* cache, const mxfp4_attention* args, 
   return NVFP4_OK;
 }
 
+nvfp4_status attn_begin(const mxfp4_cache* cache, const AttnParams& p, int32_t b, int32_t max_queries, bool many,
+                        void* workspace, cudaStream_t stream, Pending& w) {
+  w = {};
+  return many ? attn_chunk(cache, p, b, max_queries, workspace, stream, w)
+              : attn_stream(cache, p, b, max_queries, workspace, stream, w);
+}
+
 nvfp4_status attn_run(const mxfp4_cache* cache, const AttnParams& p, int32_t max_queries, bool many, void* workspace,
                       cudaStream_t stream) {
-  return many ? attn_chunk(cache, p, max_queries, workspace, stream) : attn_stream(cache, p, max_queries, workspace, stream);
+  // kMaxSeqs sequences a launch; the workspace is reused in stream order
+  for (int32_t b = 0; b < p.seqs; b += kMaxSeqs) {
+    Pending w;
+    nvfp4_status st = attn_begin(cache, p, b, max_queries, many, workspace, stream, w);
+    if (st == NVFP4_OK) st = attn_finish(cache->dim, w, stream);
+    if (st != NVFP4_OK) return st;
+  }
+  return NVFP4_OK;
 }
 
 }  // namespace nvfp4

@@ -664,9 +664,15 @@ inline void split_queries(AttnParams& a, const AttnParams& base, int32_t b) {
   if (base.lse != nullptr) a.lse = base.lse + int64_t(b) * base.kv_heads * base.group;
 }
 
-// mx_attn_combine.cu: the partials of k_attn_stream (rows: 8 or 16), of k_attn_chunk.
-nvfp4_status attn_combine(int dim, int rows, int tok, int row_tiles, const SplitParams& sp, cudaStream_t stream);
-nvfp4_status attn_join(int dim, int tok, const SplitParams& sp, cudaStream_t stream);
+// A launch whose partials are not joined yet.
+struct Pending {
+  SplitParams sp;
+  int32_t tok, rows, row_tiles;  // keys and rows of a tile, row tiles of a sequence at the most
+  bool many;                     // k_attn_chunk's
+};
+// mx_attn_combine.cu: joins them; both at once, of k_attn_chunk and of k_attn_stream.
+nvfp4_status attn_finish(int dim, const Pending& w, cudaStream_t stream);
+nvfp4_status attn_finish_both(int dim, const Pending& many, const Pending& few, cudaStream_t stream);
 
 // mx_attn.cu: whether rows of a kv head are k_attn_chunk's rather than
 // k_attn_stream's; attention by the one that `many` says, in a workspace for it.
@@ -674,6 +680,9 @@ bool attn_has_many_rows(int32_t dim, int64_t rows);
 nvfp4_status attn_run(const mxfp4_cache* cache, const AttnParams& p, int32_t max_queries, bool many, void* workspace,
                       cudaStream_t stream);
 int64_t attn_workspace(int32_t dim, bool many);
+// The launch for the sequences from b on, kMaxSeqs of them at the most; to be joined.
+nvfp4_status attn_begin(const mxfp4_cache* cache, const AttnParams& p, int32_t b, int32_t max_queries, bool many,
+                        void* workspace, cudaStream_t stream, Pending& w);
 // What an entry point of that name checks of its arguments; the parameters they give.
 nvfp4_status attn_params(const mxfp4_cache* cache, const mxfp4_attention* args, int64_t workspace_bytes,
                          const std::string& nm, AttnParams& p);

@@ -923,10 +923,8 @@ nvfp4_status chunk_launch(const mxfp4_cache* cache, const SplitParams& p, cudaSt
   static std::atomic<uint64_t> ready{0};
   nvfp4_status st = allow_smem(reinterpret_cast<const void*>(kern), T::kSmem, ready);
   if (st != NVFP4_OK) return st;
-  st = launch("launch k_attn_chunk", kern, dim3(unsigned(p.workers)), dim3(T::kThreads), T::kSmem, 0, stream,
-              static_cast<const uint8_t*>(cache->k_codes), static_cast<const uint8_t*>(cache->v_codes), p);
-  if (st != NVFP4_OK) return st;
-  return attn_join(D, kTK, p, stream);
+  return launch("launch k_attn_chunk", kern, dim3(unsigned(p.workers)), dim3(T::kThreads), T::kSmem, 0, stream,
+                static_cast<const uint8_t*>(cache->k_codes), static_cast<const uint8_t*>(cache->v_codes), p);
 }
 
 }  // namespace
@@ -936,10 +934,11 @@ int64_t attn_chunk_workspace(int32_t dim) {
          align256(sm_count() * int64_t(sizeof(Cursor)));
 }
 
-nvfp4_status attn_chunk(const mxfp4_cache* cache, const AttnParams& base, int32_t max_queries, void* workspace,
-                        cudaStream_t stream) {
+nvfp4_status attn_chunk(const mxfp4_cache* cache, const AttnParams& base, int32_t b, int32_t max_queries,
+                        void* workspace, cudaStream_t stream, Pending& pending) {
   const int32_t dim = cache->dim;
-  SplitParams sp;
+  pending.tok = kTK, pending.many = true;
+  SplitParams& sp = pending.sp;
   sp.a = base;
   sp.workers = sm_count();
   sp.several = max_queries > 1;
@@ -949,19 +948,12 @@ nvfp4_status attn_chunk(const mxfp4_cache* cache, const AttnParams& base, int32_
   sp.part_ml = reinterpret_cast<float2*>(ws + align256(partial_rows(dim) * dim * 4));
   sp.prefix = reinterpret_cast<int64_t*>(ws + align256(partial_rows(dim) * dim * 4) + align256(partial_rows(dim) * 8));
   sp.start = reinterpret_cast<Cursor*>(reinterpret_cast<uint8_t*>(sp.prefix) + align256((kMaxSeqs + 1) * 8));
-  // kMaxSeqs sequences a launch; the workspace is reused in stream order.
-  for (int32_t b = 0; b < base.seqs; b += kMaxSeqs) {
-    sp.a.seqs = std::min(kMaxSeqs, base.seqs - b);
-    sp.a.table = base.table + int64_t(b) * base.table_ld;
-    sp.a.lens = base.lens + b;
-    split_queries(sp.a, base, b);
-    nvfp4_status st;
-    if (dim == 64) st = chunk_launch<64>(cache, sp, stream);
-    else if (dim == 128) st = chunk_launch<128>(cache, sp, stream);
-    else st = chunk_launch<256>(cache, sp, stream);
-    if (st != NVFP4_OK) return st;
-  }
-  return NVFP4_OK;
+  sp.a.seqs = std::min(kMaxSeqs, base.seqs - b);
+  sp.a.table = base.table + int64_t(b) * base.table_ld;
+  sp.a.lens = base.lens + b;
+  split_queries(sp.a, base, b);
+  if (dim == 64) return chunk_launch<64>(cache, sp, stream);
+  return dim == 128 ? chunk_launch<128>(cache, sp, stream) : chunk_launch<256>(cache, sp, stream);
 }
 
 }  // namespace nvfp4

@@ -20,7 +20,7 @@ constexpr int kMostParts = 512;  // weights held at a time
 constexpr int kFewParts = 4;
 
 template <int D, int kRows, int kCols>
-__global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_constant__ SplitParams sp, int32_t tok) {
+__device__ __forceinline__ void combine_block(const SplitParams& sp, int32_t tok, int32_t bx, int32_t rt, int32_t b) {
   const AttnParams& a = sp.a;
   constexpr int kItems = kRows * kCols / 8;
   constexpr int kSlices = kCombineThreads / kItems;
@@ -28,9 +28,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_c
   __shared__ float weight[kHeld][kRows];
   __shared__ float red[kCombineThreads / 32][kRows], row_m[kRows], row_l[kRows];
   __shared__ float4 sum[(kSlices - 1) * kItems * 2];
-  grid_wait();
-  const int32_t h = blockIdx.x / (D / kCols), col0 = int32_t(blockIdx.x % (D / kCols)) * kCols;
-  const int32_t rt = blockIdx.y, b = blockIdx.z;
+  const int32_t h = bx / (D / kCols), col0 = bx % (D / kCols) * kCols;
   const int32_t len = a.lens[b], nq = seq_queries(a, b);
   const int32_t q0 = seq_start(a, b);
   const int32_t live = min(kRows, nq * a.group - rt * kRows);
@@ -169,6 +167,12 @@ __global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_c
   write(r, d, f, l == 0.0f ? -INFINITY : (row_m[r] + kJoinLog2 - kWeightLog2 + log2f(l)) * 0.6931471805599453f);
 }
 
+template <int D, int kRows, int kCols>
+__global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_constant__ SplitParams sp, int32_t tok) {
+  grid_wait();
+  combine_block<D, kRows, kCols>(sp, tok, blockIdx.x, blockIdx.y, blockIdx.z);
+}
+
 // The same where segments are many and thus short: not a block for each of them, most
 // of which a worker has all of, but warps for each boundary between two workers' runs
 // that lies in a segment; those of a segment of several such boundaries share its rows.
@@ -181,21 +185,18 @@ __global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_c
 // 49.5 so (with eight columns a lane 49.7, but a long sequence among short ones up to
 // 13 us slower).
 constexpr int kBoundaryThreads = 128, kUnder = 8;  // loads under way
+constexpr int kSplit = 4;                          // warps of a boundary
 
 template <int D, int kRows>
-__global__ void __launch_bounds__(kBoundaryThreads)
-    k_attn_combine_boundaries(const __grid_constant__ SplitParams sp, int32_t tok) {
+__device__ __forceinline__ void combine_boundary(const SplitParams& sp, int32_t tok, int32_t unit) {
   constexpr int kLanes = D == 64 ? 16 : 32, kAtOnce = 32 / kLanes;  // lanes of a row, rows of a warp
   constexpr int kPieces = D / 4 / kLanes;  // of a row
   constexpr int kSlices = 32 / kRows, kSums = 256 / kRows;  // of k_attn_combine's threads: partials of a row's outputs, sums
   constexpr int kAtATime = kLanes < kSums ? kLanes : kSums;  // partials
   constexpr int kHeld = kSums / kAtATime;
-  constexpr int kSplit = 4;  // warps of a boundary
   const AttnParams& a = sp.a;
   const int lane = threadIdx.x & 31, col = lane % kLanes, lane0 = lane - col;
-  const int32_t unit = int32_t(blockIdx.x * (kBoundaryThreads / 32) + (threadIdx.x >> 5)), w = unit / kSplit,
-                part_of_unit = unit - w * kSplit;
-  grid_wait();
+  const int32_t w = unit / kSplit, part_of_unit = unit - w * kSplit;
   Cursor c;
   auto write = [&](int32_t row, int32_t d, const float (&f)[4], float lse) {
     if (row >= c.nq * a.group) return;
@@ -285,6 +286,13 @@ __global__ void __launch_bounds__(kBoundaryThreads)
   }
 }
 
+template <int D, int kRows>
+__global__ void __launch_bounds__(kBoundaryThreads)
+    k_attn_combine_boundaries(const __grid_constant__ SplitParams sp, int32_t tok) {
+  grid_wait();
+  combine_boundary<D, kRows>(sp, tok, int32_t(blockIdx.x * (kBoundaryThreads / 32) + (threadIdx.x >> 5)));
+}
+
 // The same for segments of 128 or 256 rows.  Of those few are split, at the
 // boundaries between two workers' runs: blocks (x, w) are for the segment that
 // worker w's run starts inside of, whose columns they share with the blocks of
@@ -297,7 +305,7 @@ __global__ void __launch_bounds__(kBoundaryThreads)
 constexpr int kJoinBlocks = 4;  // for each worker
 
 template <int D, int kRows>
-__global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ SplitParams sp, int32_t tok) {
+__device__ __forceinline__ void join_block(const SplitParams& sp, int32_t tok, int32_t bx, int32_t w) {
   constexpr int kCols = 256 / kRows * 8;  // of a block at a time
   const AttnParams& a = sp.a;
   const int32_t r = threadIdx.x % kRows, d0 = int32_t(threadIdx.x) / kRows * 8;
@@ -308,8 +316,6 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ Split
     store_o8(a, int64_t(c.q0 + qi) * a.o_st + int64_t(hq) * a.o_sh + d, f);
     if (d == 0 && a.lse != nullptr) a.lse[int64_t(c.q0 + qi) * (a.kv_heads * a.group) + hq] = lse;
   };
-  grid_wait();
-  const int32_t w = blockIdx.y;
   Cursor c;
   if (w >= sp.workers) {
     c.b = w - sp.workers;
@@ -317,7 +323,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ Split
     const float zero[8] = {};
     for (c.rt = 0; c.rt * kRows < c.nq * a.group && row_span(a, c.len, c.nq, c.rt, kRows, tok).n == 0; ++c.rt)
       for (c.h = 0; c.h < a.kv_heads; ++c.h)
-        for (int32_t d = int32_t(blockIdx.x) * kCols; d < D; d += kJoinBlocks * kCols) write(c, d + d0, zero, -INFINITY);
+        for (int32_t d = bx * kCols; d < D; d += kJoinBlocks * kCols) write(c, d + d0, zero, -INFINITY);
     return;
   }
   const int64_t total = sp.prefix[a.seqs];
@@ -331,7 +337,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ Split
   const int32_t parts = worker_of(total, first + c.s.n - 1, workers) - begin + 1;
   const int32_t slot0 = worker_start(total, begin, workers) >= first - sp.edge ? 0 : 1;
   auto part_of = [&](int32_t i) { return int64_t(begin + i) * 2 + (i == 0 ? slot0 : 0); };
-  const int32_t mine = (w - begin - 1) * kJoinBlocks + int32_t(blockIdx.x), all = (parts - 1) * kJoinBlocks;
+  const int32_t mine = (w - begin - 1) * kJoinBlocks + bx, all = (parts - 1) * kJoinBlocks;
   for (int32_t d = mine * kCols + d0; d < D; d += all * kCols) {
     // in one pass, against the maximum so far
     float f[8] = {}, l = 0.0f, m = -INFINITY;
@@ -355,43 +361,77 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ Split
 }
 
 template <int D, int kRows>
-nvfp4_status combine_launch(int tok, int row_tiles, const SplitParams& sp, cudaStream_t stream) {
-  if (sp.start != nullptr) {
-    constexpr int64_t kSplit = 4, kWarps = kBoundaryThreads / 32;
-    return launch("launch k_attn_combine_boundaries", k_attn_combine_boundaries<D, kRows>,
-                  dim3(unsigned((kSplit * (sp.workers + sp.a.seqs) + kWarps - 1) / kWarps)), dim3(kBoundaryThreads), 0, 0,
-                  stream, sp, int32_t(tok));
-  }
-  const bool few = int64_t(sp.a.kv_heads) * row_tiles * sp.a.seqs < 128;
-  return launch("launch k_attn_combine", few ? k_attn_combine<D, kRows, 32> : k_attn_combine<D, kRows, 64>,
-                dim3(unsigned(sp.a.kv_heads) * (D / (few ? 32 : 64)), unsigned(row_tiles), unsigned(sp.a.seqs)),
-                dim3(kCombineThreads), 0, 0, stream, sp, int32_t(tok));
+__global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ SplitParams sp, int32_t tok) {
+  grid_wait();
+  join_block<D, kRows>(sp, tok, blockIdx.x, blockIdx.y);
+}
+
+// Both at once, of two launches that went before: k_attn_join's blocks, then
+// k_attn_combine's or (kBoundaries) the others'.
+template <int D, int kRows, bool kBoundaries>
+__global__ void __launch_bounds__(256)
+    k_attn_join_both(const __grid_constant__ SplitParams many, const __grid_constant__ SplitParams few, int32_t many_tok,
+                     int32_t few_tok, int32_t joins, int32_t bx, int32_t by) {
+  grid_wait();
+  const int32_t i = blockIdx.x, j = i - joins;
+  if (j < 0)
+    join_block<D, D == 256 ? 128 : 256>(many, many_tok, i % kJoinBlocks, i / kJoinBlocks);
+  else if constexpr (kBoundaries)
+    combine_boundary<D, kRows>(few, few_tok, j * 8 + int32_t(threadIdx.x >> 5));
+  else
+    combine_block<D, kRows, 64>(few, few_tok, j % bx, j / bx % by, j / bx / by);
 }
 
 template <int D, int kRows>
-nvfp4_status join_launch(int tok, const SplitParams& sp, cudaStream_t stream) {
-  return launch("launch k_attn_join", k_attn_join<D, kRows>,
-                dim3(unsigned(kJoinBlocks), unsigned(sp.workers + sp.a.seqs)), dim3(256), 0, 0, stream, sp,
-                int32_t(tok));
+nvfp4_status combine_launch(const Pending& w, cudaStream_t stream) {
+  const SplitParams& sp = w.sp;
+  if (sp.start != nullptr) {
+    constexpr int64_t kWarps = kBoundaryThreads / 32;
+    return launch("launch k_attn_combine_boundaries", k_attn_combine_boundaries<D, kRows>,
+                  dim3(unsigned((kSplit * (sp.workers + sp.a.seqs) + kWarps - 1) / kWarps)), dim3(kBoundaryThreads), 0, 0,
+                  stream, sp, w.tok);
+  }
+  const bool few = int64_t(sp.a.kv_heads) * w.row_tiles * sp.a.seqs < 128;
+  return launch("launch k_attn_combine", few ? k_attn_combine<D, kRows, 32> : k_attn_combine<D, kRows, 64>,
+                dim3(unsigned(sp.a.kv_heads) * (D / (few ? 32 : 64)), unsigned(w.row_tiles), unsigned(sp.a.seqs)),
+                dim3(kCombineThreads), 0, 0, stream, sp, w.tok);
+}
+
+template <int D>
+nvfp4_status join_launch(const Pending& w, cudaStream_t stream) {
+  return launch("launch k_attn_join", k_attn_join<D, D == 256 ? 128 : 256>,
+                dim3(unsigned(kJoinBlocks), unsigned(w.sp.workers + w.sp.a.seqs)), dim3(256), 0, 0, stream, w.sp, w.tok);
+}
+
+template <int D, int kRows>
+nvfp4_status both_launch(const Pending& many, const Pending& few, cudaStream_t stream) {
+  const SplitParams& sp = few.sp;
+  const int64_t segments = int64_t(sp.a.kv_heads) * few.row_tiles * sp.a.seqs, bx = sp.a.kv_heads * int64_t(D / 64);
+  const int64_t joins = int64_t(kJoinBlocks) * (many.sp.workers + many.sp.a.seqs);
+  const int64_t blocks = sp.start != nullptr ? (int64_t(kSplit) * (sp.workers + sp.a.seqs) + 7) / 8 : segments * (D / 64);
+  if (segments < 128 || joins + blocks > 0x7FFFFFFF) {  // blocks of fewer columns; too large
+    const nvfp4_status st = join_launch<D>(many, stream);
+    return st != NVFP4_OK ? st : combine_launch<D, kRows>(few, stream);
+  }
+  return launch("launch k_attn_join_both",
+                sp.start != nullptr ? k_attn_join_both<D, kRows, true> : k_attn_join_both<D, kRows, false>,
+                dim3(unsigned(joins + blocks)), dim3(256), 0, 0, stream, many.sp, sp, many.tok, few.tok, int32_t(joins),
+                int32_t(bx), few.row_tiles);
 }
 
 }  // namespace
 
-nvfp4_status attn_join(int dim, int tok, const SplitParams& sp, cudaStream_t stream) {
-  if (dim == 64) return join_launch<64, 256>(tok, sp, stream);
-  if (dim == 128) return join_launch<128, 256>(tok, sp, stream);
-  return join_launch<256, 128>(tok, sp, stream);
+nvfp4_status attn_finish(int dim, const Pending& w, cudaStream_t stream) {
+  if (w.many) return dim == 64 ? join_launch<64>(w, stream) : (dim == 128 ? join_launch<128>(w, stream) : join_launch<256>(w, stream));
+  auto f = w.rows == 8 ? (dim == 64 ? combine_launch<64, 8> : (dim == 128 ? combine_launch<128, 8> : combine_launch<256, 8>))
+                       : (dim == 64 ? combine_launch<64, 16> : (dim == 128 ? combine_launch<128, 16> : combine_launch<256, 16>));
+  return f(w, stream);
 }
 
-nvfp4_status attn_combine(int dim, int rows, int tok, int row_tiles, const SplitParams& sp, cudaStream_t stream) {
-  if (rows == 8) {
-    if (dim == 64) return combine_launch<64, 8>(tok, row_tiles, sp, stream);
-    if (dim == 128) return combine_launch<128, 8>(tok, row_tiles, sp, stream);
-    return combine_launch<256, 8>(tok, row_tiles, sp, stream);
-  }
-  if (dim == 64) return combine_launch<64, 16>(tok, row_tiles, sp, stream);
-  if (dim == 128) return combine_launch<128, 16>(tok, row_tiles, sp, stream);
-  return combine_launch<256, 16>(tok, row_tiles, sp, stream);
+nvfp4_status attn_finish_both(int dim, const Pending& many, const Pending& few, cudaStream_t stream) {
+  auto f = few.rows == 8 ? (dim == 64 ? both_launch<64, 8> : (dim == 128 ? both_launch<128, 8> : both_launch<256, 8>))
+                         : (dim == 64 ? both_launch<64, 16> : (dim == 128 ? both_launch<128, 16> : both_launch<256, 16>));
+  return f(many, few, stream);
 }
 
 }  // namespace nvfp4

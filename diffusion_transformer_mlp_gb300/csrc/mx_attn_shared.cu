@@ -19,13 +19,13 @@
 // above of the outputs are the own tokens' (4 samples of a prompt of 2,049
 // tokens: 32 us in two launches, so 20).
 //
-// What bounds it: the latencies of six launches and of k_attn_chunk's first and last
+// What bounds it: the latencies of five launches and of k_attn_chunk's first and last
 // tiles, before the work itself.  Two prompts of 16,001 and 12,001 tokens, 32 and 16
-// sequences, 32 / 8 heads of 128: parts 3.7, prefixes 35, their join 7.1, own tokens
-// 11.1, their join 6.3, this join 2.9 us; the pass 63 us, 185 if each sequence reads
-// its prompt.  One of 32,769 tokens, 128 sequences of 64 heads: 163 us instead of
-// 1,009; 117 of them are k_attn_chunk at 61% of the tensor rate.  Where reading
-// prefixes each time is as fast, that is done (plan_of).
+// sequences, 32 / 8 heads of 128: parts 3.7, prefixes 33, own tokens 11.1, the joins of
+// both 10.1 (in two launches 7.0 + 6.1), this join 2.8 us; the pass 58 us, 185 if each
+// sequence reads its prompt.  One of 32,769 tokens, 128 sequences of 64 heads: 162 us
+// instead of 1,009; 116 of them are k_attn_chunk at 61% of the tensor rate.  Where
+// reading prefixes each time is as fast, that is done (plan_of).
 #include <algorithm>
 #include <string>
 
@@ -161,12 +161,12 @@ struct Plan {
 // Rates are key heads (keys times kv heads) a us and row tile (of 8 or 16 rows, of 256
 // or 128), measured with 2 to 32 sequences of 1 and 6 queries on prefixes of 512 to
 // 32,768 keys, 4 and 8 kv heads, groups of 4 and 8.  Each for itself / shared:
-//   dim 128, 4 sequences, 1 query      12.7 / 19.0   15.2 / 20.1   23.8 / 26.4   46.1 / 35.9
-//   16 sequences                       14.8 / 21.2   23.6 / 24.0   45.5 / 34.8  138.5 / 82.8
-//   32 sequences                       19.0 / 38.4   31.7 / 37.4   77.8 / 45.5  260.9 / 64.4
-//   8 sequences, 6 queries             18.2 / 41.2   28.2 / 41.0   54.0 / 49.6  170.3 / 71.6
-//   dim 64, 32 sequences, 1 query      13.0 / 30.9   19.0 / 32.3   30.8 / 40.3   83.9 / 51.6
-//   dim 256, 8 sequences, 1 query      15.0 / 41.8   20.1 / 41.7   35.0 / 50.5   90.6 / 65.3
+//   dim 128, 4 sequences, 1 query      11.8 / 19.9   14.1 / 20.5   22.6 / 26.0   45.0 / 36.1
+//   16 sequences                       13.8 / 20.9   22.5 / 23.9   44.7 / 34.9  137.4 / 55.9
+//   32 sequences                       17.8 / 33.2   30.5 / 33.0   76.5 / 38.4  260.0 / 56.1
+//   8 sequences, 6 queries             18.1 / 36.6   28.2 / 35.9   54.5 / 43.9  170.4 / 66.4
+//   dim 64, 32 sequences, 1 query      11.9 / 28.3   18.0 / 28.9   29.7 / 36.5   82.5 / 47.7
+//   dim 256, 8 sequences, 1 query      14.4 / 40.2   19.4 / 39.5   34.0 / 47.6   89.7 / 62.6
 // (prefixes of 512, 2,048, 8,192, 32,768 keys).  Where a sequence has rows for whole
 // tiles there is nothing to save: the work is the rows', and they are as many.
 Plan plan_of(int32_t dim, int64_t kv_heads, int64_t group, int64_t total_q, int64_t max_queries, int64_t seqs,
@@ -190,7 +190,7 @@ Plan plan_of(int32_t dim, int64_t kv_heads, int64_t group, int64_t total_q, int6
   const double apart = p.own_many ? 25.0 + chunk(seqs, own_rows) : 12.0 + stream(seqs, own_rows, few8, few16);
   const bool one = max_queries == 1;
   const double by_stream = one ? 18.0 + stream(count, rows, list8, list16) : 30.0 + stream(count, rows, few8, few16);
-  const double by_chunk = (dim == 256 ? 48.0 : 40.0) + chunk(count, rows);
+  const double by_chunk = (dim == 256 ? 44.0 : 36.0) + chunk(count, rows);
   p.prefix_many = attn_has_many_rows(dim, most_rows) || by_chunk < by_stream;
   p.one_list = one && !p.prefix_many;
   p.share = (p.prefix_many ? by_chunk : by_stream) < apart;
@@ -229,7 +229,7 @@ extern "C" int64_t mxfp4_attention_shared_workspace_bytes(int32_t kv_heads, int3
   if (own == 0 || count == 0 || max_group < 1) return own;
   SharedParams p;
   p.count = count;
-  return layout(p, nullptr, std::max(attn_workspace(dim, false), attn_workspace(dim, true)), total_q, q_heads, dim, seqs,
+  return layout(p, nullptr, align256(attn_workspace(dim, true)) + attn_workspace(dim, false), total_q, q_heads, dim, seqs,
                 table_ld);
 }
 
@@ -266,7 +266,7 @@ extern "C" nvfp4_status mxfp4_cache_attention_shared(const mxfp4_cache* cache, c
   if (shared->count > 0 && max_group > 0 && shared->always != 0) plan.share = true;
   if (!plan.share) return attn_run(cache, p.a, args->max_queries, plan.own_many, args->workspace, s);
   p.groups = shared->groups, p.shared = shared->shared, p.count = shared->count;
-  layout(p, static_cast<uint8_t*>(args->workspace), std::max(attn_workspace(dim, false), attn_workspace(dim, true)),
+  layout(p, static_cast<uint8_t*>(args->workspace), align256(attn_workspace(dim, true)) + attn_workspace(dim, false),
          args->total_q, heads, dim, args->seqs, args->table_ld);
   nvfp4_status st = launch("launch k_shared_parts", k_shared_parts, dim3(unsigned(p.count + args->seqs)), dim3(kThreads),
                            0, 0, s, p);
@@ -282,14 +282,24 @@ extern "C" nvfp4_status mxfp4_cache_attention_shared(const mxfp4_cache* cache, c
     st = attn_run(cache, part, max_group, false, args->workspace, s);
     if (st != NVFP4_OK) return st;
   } else {
+    // of k_attn_chunk and k_attn_stream the partials are joined at once, from workspaces of their own
+    const bool both = plan.prefix_many && !plan.own_many && p.count <= kMaxSeqs && args->seqs <= kMaxSeqs;
+    Pending prefix, own;
     part.seqs = p.count;
-    st = attn_run(cache, part, max_group, plan.prefix_many, args->workspace, s);
+    st = both ? attn_begin(cache, part, 0, max_group, true, args->workspace, s, prefix)
+              : attn_run(cache, part, max_group, plan.prefix_many, args->workspace, s);
     if (st != NVFP4_OK) return st;
     part.out = p.o + args->total_q * heads * dim, part.lse = p.l + args->total_q * heads;
     part.table = p.table + (p.count + 1) * args->table_ld, part.lens = p.lens + p.count + 1;
     part.q_starts = args->q_starts;
     part.seqs = args->seqs, part.causal = p.a.causal;
-    st = attn_run(cache, part, args->max_queries, plan.own_many, args->workspace, s);
+    if (both) {
+      uint8_t* ws = static_cast<uint8_t*>(args->workspace) + align256(attn_workspace(dim, true));
+      st = attn_begin(cache, part, 0, args->max_queries, false, ws, s, own);
+      if (st == NVFP4_OK) st = attn_finish_both(dim, prefix, own, s);
+    } else {
+      st = attn_run(cache, part, args->max_queries, plan.own_many, args->workspace, s);
+    }
     if (st != NVFP4_OK) return st;
   }
   const int64_t items = args->max_queries * heads * (dim / 8);

@@ -780,30 +780,28 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows, kSeveral>::kCtas)
 constexpr int64_t kManySegments = 1024;
 
 template <int D, int kRows, bool kSeveral, bool kFew = false>
-nvfp4_status stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams& sp, int row_tiles,
-                           cudaStream_t stream) {
+nvfp4_status stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, Pending& w, cudaStream_t stream) {
   using T = Tile<D, kRows, kSeveral>;
   auto kern = k_attn_stream<D, kRows, kSeveral, kFew>;
   static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
   nvfp4_status st = allow_smem(reinterpret_cast<const void*>(kern), T::kSmem, ready);
   if (st != NVFP4_OK) return st;
-  SplitParams p = sp;
+  SplitParams& p = w.sp;
+  w.tok = T::kTok;
   p.workers = T::kCtas * sm_count() * kWarps;
-  if (int64_t(p.a.kv_heads) * row_tiles * p.a.seqs < kManySegments) p.start = nullptr;
+  if (int64_t(p.a.kv_heads) * w.row_tiles * p.a.seqs < kManySegments) p.start = nullptr;
   p.least = 1, p.edge = 0, p.even = 4;  // 16,000 keys, 8 heads, dim 128: 24.2 us, without 29.0
-  st = launch("launch k_attn_stream", kern, dim3(unsigned(p.workers / kWarps)), dim3(kThreads), T::kSmem, 0, stream, tk,
-              tv, p);
-  if (st != NVFP4_OK) return st;
-  return attn_combine(D, kRows, T::kTok, row_tiles, p, stream);
+  return launch("launch k_attn_stream", kern, dim3(unsigned(p.workers / kWarps)), dim3(kThreads), T::kSmem, 0, stream, tk,
+                tv, p);
 }
 
 template <int D>
-nvfp4_status launch_of(int rows, const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams& sp, int row_tiles,
-                       cudaStream_t stream) {
-  auto f = rows == 8 ? (sp.several ? stream_launch<D, 8, true>
+nvfp4_status launch_of(const CUtensorMap& tk, const CUtensorMap& tv, Pending& w, cudaStream_t stream) {
+  const SplitParams& sp = w.sp;
+  auto f = w.rows == 8 ? (sp.several ? stream_launch<D, 8, true>
                                 : (sp.a.seqs <= 32 ? stream_launch<D, 8, false, true> : stream_launch<D, 8, false>))
                      : (sp.several ? stream_launch<D, 16, true> : stream_launch<D, 16, false>);
-  return f(tk, tv, sp, row_tiles, stream);
+  return f(tk, tv, w, stream);
 }
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -819,8 +817,8 @@ int64_t attn_stream_workspace(int32_t dim) {
          align256(most_workers() * int64_t(sizeof(Cursor)));
 }
 
-nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32_t max_queries, void* workspace,
-                         cudaStream_t stream) {
+nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32_t b, int32_t max_queries,
+                         void* workspace, cudaStream_t stream, Pending& w) {
   const int32_t dim = cache->dim;
   CUtensorMap tk, tv;
   const int box = std::min(cache->page_size, dim == 64 ? 128 : (dim == 128 ? 64 : 32));
@@ -834,7 +832,7 @@ nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32
   if (st == NVFP4_OK)
     st = make_map(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, cache->v_codes, 3, dims, strides, bx, swz, "V codes");
   if (st != NVFP4_OK) return st;
-  SplitParams sp;
+  SplitParams& sp = w.sp;
   sp.a = base;
   sp.several = max_queries > 1;
   const int64_t rows_max = int64_t(max_queries) * base.group;
@@ -847,17 +845,13 @@ nvfp4_status attn_stream(const mxfp4_cache* cache, const AttnParams& base, int32
   sp.start = reinterpret_cast<Cursor*>(reinterpret_cast<uint8_t*>(sp.prefix) + align256((kMaxSeqs + 1) * 8));
   const int64_t row_tiles = (rows_max + rows - 1) / rows;
   if (row_tiles > 65535) return fail(NVFP4_EUNSUPPORTED, "mxfp4_cache_attention: too many query rows a sequence");
-  // kMaxSeqs sequences a launch; the workspace is reused in stream order
-  for (int32_t b = 0; b < base.seqs; b += kMaxSeqs) {
-    sp.a.seqs = std::min(kMaxSeqs, base.seqs - b);
-    sp.a.table = base.table + int64_t(b) * base.table_ld;
-    sp.a.lens = base.lens + b;
-    split_queries(sp.a, base, b);
-    auto launch = dim == 64 ? launch_of<64> : (dim == 128 ? launch_of<128> : launch_of<256>);
-    st = launch(rows, tk, tv, sp, int(row_tiles), stream);
-    if (st != NVFP4_OK) return st;
-  }
-  return NVFP4_OK;
+  w.rows = rows, w.row_tiles = int32_t(row_tiles), w.many = false;
+  sp.a.seqs = std::min(kMaxSeqs, base.seqs - b);
+  sp.a.table = base.table + int64_t(b) * base.table_ld;
+  sp.a.lens = base.lens + b;
+  split_queries(sp.a, base, b);
+  auto launch = dim == 64 ? launch_of<64> : (dim == 128 ? launch_of<128> : launch_of<256>);
+  return launch(tk, tv, w, stream);
 }
 
 }  // namespace nvfp4

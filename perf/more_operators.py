@@ -641,7 +641,7 @@ def _run_own(state):
         rotary = fc2.HeadRotary(state["turns"], state["axis"], case["pairs"] == "neighbours")
         if op == "rotate":
             out = fc2.head_norm_rotary(state["q"], state["k"], rotary, state["positions"], state["q_weight"],
-                                       state["k_weight"], _EPS)
+                                       None if state["k"] is None else state["k_weight"], _EPS)
             return [t for t in out if t is not None]
     if op != "rotate":
         cache = fc2.MXFP4Cache(*(state[n] for n in _CACHE)) if op != "admit" else None

@@ -182,10 +182,11 @@ __global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const __grid_c
 // on which of them joins it.  Warps behind those write the rows that see no key.
 // 192 sequences of 33 to 1,025 keys, 8 heads: writing and attending 54.9 us by
 // segments, most of whose instructions looked for partials that were not there, and
-// 49.5 so (with eight columns a lane 49.7, but a long sequence among short ones up to
-// 13 us slower).
+// 48.0 so (with eight columns a lane a long sequence among short ones was up to 13 us
+// slower).
 constexpr int kBoundaryThreads = 128, kUnder = 8;  // loads under way
-constexpr int kSplit = 4;                          // warps of a boundary
+// Warps of a boundary (192 sequences of 8 rows with four of them 1.1 us more).
+__host__ __device__ constexpr int32_t split_of(int rows) { return rows / 4; }
 
 template <int D, int kRows>
 __device__ __forceinline__ void combine_boundary(const SplitParams& sp, int32_t tok, int32_t unit) {
@@ -194,6 +195,7 @@ __device__ __forceinline__ void combine_boundary(const SplitParams& sp, int32_t 
   constexpr int kSlices = 32 / kRows, kSums = 256 / kRows;  // of k_attn_combine's threads: partials of a row's outputs, sums
   constexpr int kAtATime = kLanes < kSums ? kLanes : kSums;  // partials
   constexpr int kHeld = kSums / kAtATime;
+  constexpr int32_t kSplit = split_of(kRows);
   const AttnParams& a = sp.a;
   const int lane = threadIdx.x & 31, col = lane % kLanes, lane0 = lane - col;
   const int32_t w = unit / kSplit, part_of_unit = unit - w * kSplit;
@@ -386,7 +388,7 @@ template <int D, int kRows>
 nvfp4_status combine_launch(const Pending& w, cudaStream_t stream) {
   const SplitParams& sp = w.sp;
   if (sp.start != nullptr) {
-    constexpr int64_t kWarps = kBoundaryThreads / 32;
+    constexpr int64_t kSplit = split_of(kRows), kWarps = kBoundaryThreads / 32;
     return launch("launch k_attn_combine_boundaries", k_attn_combine_boundaries<D, kRows>,
                   dim3(unsigned((kSplit * (sp.workers + sp.a.seqs) + kWarps - 1) / kWarps)), dim3(kBoundaryThreads), 0, 0,
                   stream, sp, w.tok);
@@ -408,7 +410,7 @@ nvfp4_status both_launch(const Pending& many, const Pending& few, cudaStream_t s
   const SplitParams& sp = few.sp;
   const int64_t segments = int64_t(sp.a.kv_heads) * few.row_tiles * sp.a.seqs, bx = sp.a.kv_heads * int64_t(D / 64);
   const int64_t joins = int64_t(kJoinBlocks) * (many.sp.workers + many.sp.a.seqs);
-  const int64_t blocks = sp.start != nullptr ? (int64_t(kSplit) * (sp.workers + sp.a.seqs) + 7) / 8 : segments * (D / 64);
+  const int64_t blocks = sp.start != nullptr ? (int64_t(split_of(kRows)) * (sp.workers + sp.a.seqs) + 7) / 8 : segments * (D / 64);
   if (segments < 128 || joins + blocks > 0x7FFFFFFF) {  // blocks of fewer columns; too large
     const nvfp4_status st = join_launch<D>(many, stream);
     return st != NVFP4_OK ? st : combine_launch<D, kRows>(few, stream);

@@ -773,10 +773,12 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kRows, kSeveral>::kCtas)
 }
 
 // From so many segments on (sequences times kv heads times row tiles) partials are joined
-// by boundaries between runs (k_attn_combine_boundaries), below by segments.  8 heads of
-// 128, sequences of 32 to 1,025 keys, by boundaries / segments: 32 of them 20.5 / 20.3 us,
-// 128 38.7 / 41.0, 512 112 / 131; with one of 20,000 keys among them 34.0 / 29.7,
-// 50.2 / 50.4, 112 / 131: a long one has many partials, for which a block is better.
+// by boundaries between runs (k_attn_combine_boundaries), below by segments: 1,024 of 8
+// rows, and twice as many of 16, which have twice the rows to join.  8 heads of 128,
+// sequences of 32 to 1,025 keys, by boundaries / segments: 32 of them 20.5 / 20.3 us,
+// 128 36.7 / 41.0, 512 110 / 131; with one of 20,000 keys among them 34.0 / 29.7,
+// 50.0 / 50.4, 110 / 131: a long one has many partials, for which a block is better.
+// 4 heads, 16 rows: 256 of them 73.0 / 71.7, 512 122 / 124.
 constexpr int64_t kManySegments = 1024;
 
 template <int D, int kRows, bool kSeveral, bool kFew = false>
@@ -789,7 +791,7 @@ nvfp4_status stream_launch(const CUtensorMap& tk, const CUtensorMap& tv, Pending
   SplitParams& p = w.sp;
   w.tok = T::kTok;
   p.workers = T::kCtas * sm_count() * kWarps;
-  if (int64_t(p.a.kv_heads) * w.row_tiles * p.a.seqs < kManySegments) p.start = nullptr;
+  if (int64_t(p.a.kv_heads) * w.row_tiles * p.a.seqs < kManySegments * (kRows / 8)) p.start = nullptr;
   p.least = 1, p.edge = 0, p.even = 4;  // 16,000 keys, 8 heads, dim 128: 24.2 us, without 29.0
   return launch("launch k_attn_stream", kern, dim3(unsigned(p.workers / kWarps)), dim3(kThreads), T::kSmem, 0, stream, tk,
                 tv, p);

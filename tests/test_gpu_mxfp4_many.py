@@ -17,7 +17,7 @@ def lengths(n, seed, longer=()):
     return lens
 
 
-@pytest.mark.parametrize("dim,hq,hkv,n", [(64, 32, 32, 33), (128, 64, 16, 67), (256, 64, 32, 34)])
+@pytest.mark.parametrize("dim,hq,hkv,n", [(64, 32, 32, 32), (64, 32, 32, 33), (128, 64, 16, 67), (256, 64, 32, 34)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 def test_short_sequences(dim, hq, hkv, n, dtype):
     check(*run_attention(lengths(n, n), [1] * n, hq, hkv, dim, 32, dtype, seed=n)[:5])

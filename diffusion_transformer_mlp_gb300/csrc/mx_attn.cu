@@ -80,6 +80,7 @@ nvfp4_status attn_params(const mxfp4_cache* cache, const mxfp4_attention* args, 
     return fail(NVFP4_EINVAL, nm + ": workspace too small, " + std::to_string(workspace_bytes) + " bytes are needed");
   p.q = g.q, p.out = g.out, p.lse = g.lse;
   p.table = g.table, p.lens = g.lens, p.q_starts = g.q_starts;
+  p.q_ends = g.q_starts != nullptr ? g.q_starts + 1 : nullptr;
   p.k_codes = static_cast<const uint8_t*>(cache->k_codes);
   p.v_codes = static_cast<const uint8_t*>(cache->v_codes);
   p.k_scales = static_cast<const uint8_t*>(cache->k_scales);

@@ -19,6 +19,7 @@ struct AttnParams {
   const int32_t* table;
   const int32_t* lens;
   const int32_t* q_starts;  // null: one query a sequence
+  const int32_t* q_ends;    // q_starts + 1 where sequences' queries follow on one another
   const uint8_t* k_codes;
   const uint8_t* v_codes;
   const uint8_t* k_scales;
@@ -109,7 +110,7 @@ __device__ __forceinline__ int32_t seq_start(const AttnParams& a, int32_t b) {
   return a.q_starts != nullptr ? min(max(a.q_starts[b], 0), a.total_q) : b;
 }
 __device__ __forceinline__ int32_t seq_queries(const AttnParams& a, int32_t b) {
-  return a.q_starts != nullptr ? max(min(a.q_starts[b + 1], a.total_q) - seq_start(a, b), 0) : 1;
+  return a.q_starts != nullptr ? max(min(a.q_ends[b], a.total_q) - seq_start(a, b), 0) : 1;
 }
 
 // The row of q for output row i.
@@ -656,7 +657,7 @@ __device__ __forceinline__ void wide_segment(const SplitParams& sp, const Cursor
 // The queries and outputs of the sequences from b on.
 inline void split_queries(AttnParams& a, const AttnParams& base, int32_t b) {
   if (base.q_starts != nullptr) {
-    a.q_starts = base.q_starts + b;
+    a.q_starts = base.q_starts + b, a.q_ends = base.q_ends + b;
     return;
   }
   a.q = static_cast<const uint16_t*>(base.q) + int64_t(b) * base.q_st;

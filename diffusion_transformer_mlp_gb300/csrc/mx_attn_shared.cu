@@ -41,9 +41,8 @@ struct SharedParams {
   const int32_t* groups;
   const int32_t* shared;
   int32_t count;
-  // The groups' prefixes, one sequence of no keys for the queries behind them, and
-  // the sequences' own tokens: count + 1 + seqs sequences.
-  int32_t *table, *lens, *starts;
+  // The groups' prefixes and the sequences' own tokens: count + seqs sequences.
+  int32_t *table, *lens, *starts, *ends;
   int32_t* before;  // [seqs] tokens of the prefix
   float *o, *l;     // [2 * total_q] rows: of the prefixes, of the own tokens
 };
@@ -78,14 +77,10 @@ __global__ void __launch_bounds__(kThreads) k_shared_parts(const __grid_constant
   if (int32_t(blockIdx.x) < p.count) {
     const int32_t g = blockIdx.x, s0 = group_start(p, g), n = prefix_of(p, g, red);
     if (threadIdx.x == 0) {
+      const int32_t s1 = group_start(p, g + 1);
       p.lens[g] = n;
-      p.starts[g] = s0 < a.seqs ? seq_start(a, s0) : a.total_q;
-      if (g + 1 == p.count) {
-        const int32_t s1 = max(group_start(p, p.count), s0);
-        // behind the queries of the last sequence of a group
-        p.starts[p.count] = s1 > 0 ? seq_start(a, s1 - 1) + seq_queries(a, s1 - 1) : 0;
-        p.lens[p.count] = 0;
-      }
+      p.starts[g] = s0 < s1 ? seq_start(a, s0) : 0;
+      p.ends[g] = s0 < s1 ? seq_start(a, s1 - 1) + seq_queries(a, s1 - 1) : 0;
     }
     const int32_t* src = a.table + s0 * a.table_ld;
     for (int32_t i = threadIdx.x; i < n >> a.page_shift; i += kThreads) p.table[g * a.table_ld + i] = src[i];
@@ -104,11 +99,11 @@ __global__ void __launch_bounds__(kThreads) k_shared_parts(const __grid_constant
     n = min(n, max(a.lens[b], 0) & ~((1 << a.page_shift) - 1));  // without queries it limits nothing
   }
   const int32_t len = a.lens[b] - n;
-  const int32_t own = p.count + 1 + b;
+  const int32_t own = p.count + b;
   if (threadIdx.x == 0) {
     p.before[b] = n, p.lens[own] = len;
     p.starts[own] = a.total_q + seq_start(a, b);
-    if (b + 1 == a.seqs) p.starts[own + 1] = a.total_q + seq_start(a, b) + seq_queries(a, b);
+    p.ends[own] = a.total_q + seq_start(a, b) + seq_queries(a, b);
   }
   const int64_t skip = n >> a.page_shift, most = a.table_ld - skip;
   const int64_t pages = min((int64_t(max(len, 0)) + (int64_t(1) << a.page_shift) - 1) >> a.page_shift, most);
@@ -209,9 +204,10 @@ int64_t layout(SharedParams& p, uint8_t* ws, int64_t attention, int64_t rows, in
   };
   take(p.o, 2 * rows * heads * dim);
   take(p.l, 2 * rows * heads);
-  take(p.table, (p.count + 1 + seqs) * table_ld);
-  take(p.lens, p.count + 1 + seqs);
-  take(p.starts, p.count + 2 + seqs);
+  take(p.table, (p.count + seqs) * table_ld);
+  take(p.lens, p.count + seqs);
+  take(p.starts, p.count + seqs);
+  take(p.ends, p.count + seqs);
   take(p.before, seqs);
   return at;
 }
@@ -275,10 +271,10 @@ extern "C" nvfp4_status mxfp4_cache_attention_shared(const mxfp4_cache* cache, c
   part.o_f32 = 1, part.o_vec = 1;
   part.o_st = heads * dim, part.o_sh = dim;
   part.out = p.o, part.lse = p.l;
-  part.table = p.table, part.lens = p.lens, part.q_starts = p.starts;
+  part.table = p.table, part.lens = p.lens, part.q_starts = p.starts, part.q_ends = p.ends;
   part.causal = 0;
   if (plan.one_list) {
-    part.seqs = p.count + 1 + args->seqs, part.total_q = 2 * args->total_q;
+    part.seqs = p.count + args->seqs, part.total_q = 2 * args->total_q;
     st = attn_run(cache, part, max_group, false, args->workspace, s);
     if (st != NVFP4_OK) return st;
   } else {
@@ -290,8 +286,8 @@ extern "C" nvfp4_status mxfp4_cache_attention_shared(const mxfp4_cache* cache, c
               : attn_run(cache, part, max_group, plan.prefix_many, args->workspace, s);
     if (st != NVFP4_OK) return st;
     part.out = p.o + args->total_q * heads * dim, part.lse = p.l + args->total_q * heads;
-    part.table = p.table + (p.count + 1) * args->table_ld, part.lens = p.lens + p.count + 1;
-    part.q_starts = args->q_starts;
+    part.table = p.table + p.count * args->table_ld, part.lens = p.lens + p.count;
+    part.q_starts = p.a.q_starts, part.q_ends = p.a.q_ends;
     part.seqs = args->seqs, part.causal = p.a.causal;
     if (both) {
       uint8_t* ws = static_cast<uint8_t*>(args->workspace) + align256(attn_workspace(dim, true));

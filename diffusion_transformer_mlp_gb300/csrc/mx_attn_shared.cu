@@ -164,6 +164,11 @@ struct Plan {
 //   dim 256, 8 sequences, 1 query      14.4 / 40.2   19.4 / 39.5   34.0 / 47.6   89.7 / 62.6
 // (prefixes of 512, 2,048, 8,192, 32,768 keys).  Where a sequence has rows for whole
 // tiles there is nothing to save: the work is the rows', and they are as many.
+//
+// Sequences outside of the groups are read either way, and at most count * max_group
+// queries lie in one.  In one list they go through the rows' kernel of the groups, which
+// takes twice as long for them if it is that of 16 rows: 512 sequences of up to 1,000
+// keys, 8 of them behind 16,000 common ones, 146 us for itself and 189 in one list.
 Plan plan_of(int32_t dim, int64_t kv_heads, int64_t group, int64_t total_q, int64_t max_queries, int64_t seqs,
              int64_t capacity, int64_t count, int64_t max_group) {
   const int i = dim == 64 ? 0 : (dim == 128 ? 1 : 2);
@@ -179,13 +184,19 @@ Plan plan_of(int32_t dim, int64_t kv_heads, int64_t group, int64_t total_q, int6
     return double(n) * double(capacity) * double(kv_heads) * double((rows + tile - 1) / tile) / many[i];
   };
   const int64_t own_rows = max_queries * group, most_rows = max_group * group;
-  const int64_t rows = std::min(most_rows, (total_q + count - 1) / count * group);  // of a group, about
+  const int64_t grouped = std::min(total_q, count * max_group);
+  const int64_t rows = (grouped + count - 1) / count * group;                   // of a group, about
+  const int64_t readers = int64_t(double(seqs) * double(grouped) / double(total_q) + 0.5);  // of prefixes, about
   Plan p = {};
   p.own_many = attn_has_many_rows(dim, own_rows);
-  const double apart = p.own_many ? 25.0 + chunk(seqs, own_rows) : 12.0 + stream(seqs, own_rows, few8, few16);
+  auto own = [&](int64_t n) { return p.own_many ? chunk(n, own_rows) : stream(n, own_rows, few8, few16); };
+  const double others = own(seqs - readers);
+  const double apart = (p.own_many ? 25.0 : 12.0) + own(readers) + others;
   const bool one = max_queries == 1;
-  const double by_stream = one ? 18.0 + stream(count, rows, list8, list16) : 30.0 + stream(count, rows, few8, few16);
-  const double by_chunk = (dim == 256 ? 44.0 : 36.0) + chunk(count, rows);
+  const double others_listed = most_rows <= 8 ? others : stream(seqs - readers, 16, list8, list16);
+  const double by_stream = one ? 18.0 + stream(count, rows, list8, list16) + others_listed
+                               : 30.0 + stream(count, rows, few8, few16) + others;
+  const double by_chunk = (dim == 256 ? 44.0 : 36.0) + chunk(count, rows) + others;
   p.prefix_many = attn_has_many_rows(dim, most_rows) || by_chunk < by_stream;
   p.one_list = one && !p.prefix_many;
   p.share = (p.prefix_many ? by_chunk : by_stream) < apart;

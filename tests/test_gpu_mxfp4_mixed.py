@@ -74,3 +74,21 @@ def test_nothing_is_worked_out_for_queries_outside(hq, hkv, dim, grouped, others
     c.check()
     zeros = int((workspace.view(torch.int32) == 0).sum())
     assert zeros < others * hq * dim // 8
+
+
+@pytest.mark.parametrize("hq,hkv,dim,grouped,others,nq", [(32, 8, 128, 2, 126, 1), (32, 8, 128, 8, 300, 1),
+                                                          (8, 8, 64, 2, 150, 1), (16, 4, 256, 3, 90, 1), (8, 4, 64, 2, 60, 3),
+                                                          (32, 8, 128, 4, 124, 4)])
+def test_sequences_outside_save_nothing(hq, hkv, dim, grouped, others, nq):
+    """A small group among many sequences is not worth sharing, however large the
+    block tables are: the bits of the ordinary attention.  One that most belong to is."""
+    c = mixed(grouped, others, 5, hq, hkv, dim, nq=nq, seed=grouped)
+    c.table = torch.cat((c.table, torch.zeros(len(c.lens), 1000 - c.table.shape[1], dtype=torch.int32, device="cuda")), 1)
+    apart = fc2.mxfp4_cache_attention(c.q, c.cache, c.table, i32(c.lens), i32(c.starts), max(c.nq))
+    assert not torch.equal(c.run(max_group=sum(c.nq[5:5 + grouped])), apart)
+    assert torch.equal(c.run(always=False, max_group=sum(c.nq[5:5 + grouped])), apart)
+    c = mixed(others, grouped, 1, hq, hkv, dim, nq=nq, seed=grouped)
+    c.table = torch.cat((c.table, torch.zeros(len(c.lens), 1000 - c.table.shape[1], dtype=torch.int32, device="cuda")), 1)
+    kw = dict(max_group=sum(c.nq[1:1 + others]))
+    shared = c.run(**kw).clone()
+    assert torch.equal(c.run(always=False, **kw), shared)

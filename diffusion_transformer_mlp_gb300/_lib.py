@@ -35,7 +35,8 @@ EXPORTED = ["nvfp4_padded_rows", "nvfp4_qdata_bytes", "nvfp4_scale_bytes", "nvfp
             "mxfp4_padded_cols", "mxfp4_qdata_bytes", "mxfp4_scale_bytes", "mxfp4_scale_offset", "mxfp4_quantize",
             "mxfp4_dequantize", "mxfp4_gemm", "mxfp4_linear_workspace_bytes", "mxfp4_linear", "mxfp4_cache_write",
             "mxfp4_cache_read", "mxfp4_attention_workspace_bytes", "mxfp4_cache_attention",
-            "mxfp4_attention_shared_workspace_bytes", "mxfp4_cache_attention_shared", "head_norm_rotary",
+            "mxfp4_attention_shared_workspace_bytes", "mxfp4_attention_shared_call_workspace_bytes",
+            "mxfp4_cache_attention_shared", "head_norm_rotary",
             "mxfp4_cache_write_rotary", "mxfp4_pages_workspace_bytes", "mxfp4_pages_select", "mxfp4_pages_extend",
             "mxfp4_pages_compact", "mxfp4_cache_copy"]
 
@@ -140,6 +141,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
         f32 = ctypes.c_float
         L.mxfp4_attention_shared_workspace_bytes.restype = i64
         L.mxfp4_attention_shared_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i64, i32, i32]
+        L.mxfp4_attention_shared_call_workspace_bytes.restype = i64
+        L.mxfp4_attention_shared_call_workspace_bytes.argtypes = [vp, vp, vp]
         L.mxfp4_cache_attention_shared.restype = st
         L.mxfp4_cache_attention_shared.argtypes = [vp, vp, vp, vp]
         L.head_norm_rotary.restype = st

@@ -36,7 +36,7 @@ struct Api {
   decltype(&mxfp4_cache_read) cache_read;
   decltype(&mxfp4_attention_workspace_bytes) attention_workspace_bytes;
   decltype(&mxfp4_cache_attention) cache_attention;
-  decltype(&mxfp4_attention_shared_workspace_bytes) attention_shared_workspace_bytes;
+  decltype(&mxfp4_attention_shared_call_workspace_bytes) attention_shared_call_workspace_bytes;
   decltype(&mxfp4_cache_attention_shared) cache_attention_shared;
   decltype(&head_norm_rotary) norm_rotary;
   decltype(&mxfp4_cache_write_rotary) cache_write_rotary;
@@ -431,10 +431,10 @@ PyObject* attend(PyObject* const* a, bool with_groups) {
     g.lse = static_cast<float*>(lse.data_ptr());
   }
   if (total > 0 && seqs > 0 && most > 0) {
+    g.table_ld = table.size(1);
+    g.seqs = int32_t(seqs), g.total_q = int32_t(total), g.max_queries = int32_t(most), g.q_heads = int32_t(heads);
     const int64_t need =
-        with_groups ? api.attention_shared_workspace_bytes(c.c.kv_heads, int32_t(heads), c.c.dim, int32_t(total),
-                                                           int32_t(most), int32_t(seqs), table.size(1), s.count,
-                                                           s.max_group)
+        with_groups ? api.attention_shared_call_workspace_bytes(&c.c, &g, &s)
                     : api.attention_workspace_bytes(c.c.kv_heads, int32_t(heads), c.c.dim, int32_t(most));
     Tensor ws = empty({need}, at::kByte, c.dev);
     g.q = q.data_ptr(), g.out = out.data_ptr();
@@ -443,9 +443,7 @@ PyObject* attend(PyObject* const* a, bool with_groups) {
     g.workspace = ws.data_ptr();
     g.dev_status = status_of(a[15], c.dev);
     g.q_st = q.stride(0), g.q_sh = q.stride(1), g.o_st = out.stride(0), g.o_sh = out.stride(1);
-    g.table_ld = table.size(1);
     g.workspace_bytes = need;
-    g.seqs = int32_t(seqs), g.total_q = int32_t(total), g.max_queries = int32_t(most), g.q_heads = int32_t(heads);
     g.causal = causal;
     g.window = int32_t(window < 0x7FFFFFFF ? window : 0x7FFFFFFF);
     g.sinks = int32_t(sinks < 0x7FFFFFFF ? sinks : 0x7FFFFFFF);

@@ -222,6 +222,28 @@ int64_t layout(SharedParams& p, uint8_t* ws, int64_t attention, int64_t rows, in
   take(p.before, seqs);
   return at;
 }
+int64_t parts_workspace(int32_t dim) { return align256(attn_workspace(dim, true)) + attn_workspace(dim, false); }
+
+// How the call works, and the bytes of workspace that this takes.
+Plan plan_call(const mxfp4_cache* cache, const mxfp4_attention* args, const mxfp4_shared* shared, int64_t* bytes) {
+  Plan plan = {};
+  *bytes = 0;
+  if (args->total_q < 1 || args->seqs < 1 || args->table_ld < 1 || args->max_queries < 1) return plan;
+  *bytes = mxfp4_attention_workspace_bytes(cache->kv_heads, args->q_heads, cache->dim, args->max_queries);
+  if (*bytes == 0) return plan;
+  const int32_t dim = cache->dim, max_group = std::min(shared->max_group, args->total_q);
+  const int64_t group = args->q_heads / cache->kv_heads;
+  plan.own_many = attn_has_many_rows(dim, args->max_queries * group);
+  if (shared->count < 1 || max_group < 1) return plan;
+  plan = plan_of(dim, cache->kv_heads, group, args->total_q, args->max_queries, args->seqs,
+                 args->table_ld * cache->page_size, shared->count, max_group);
+  if (shared->always != 0) plan.share = true;
+  SharedParams p;
+  p.count = shared->count;
+  if (plan.share)
+    *bytes = layout(p, nullptr, parts_workspace(dim), args->total_q, args->q_heads, dim, args->seqs, args->table_ld);
+  return plan;
+}
 
 }  // namespace
 }  // namespace nvfp4
@@ -236,8 +258,15 @@ extern "C" int64_t mxfp4_attention_shared_workspace_bytes(int32_t kv_heads, int3
   if (own == 0 || count == 0 || max_group < 1) return own;
   SharedParams p;
   p.count = count;
-  return layout(p, nullptr, align256(attn_workspace(dim, true)) + attn_workspace(dim, false), total_q, q_heads, dim, seqs,
-                table_ld);
+  return layout(p, nullptr, parts_workspace(dim), total_q, q_heads, dim, seqs, table_ld);
+}
+
+extern "C" int64_t mxfp4_attention_shared_call_workspace_bytes(const mxfp4_cache* cache, const mxfp4_attention* args,
+                                                               const mxfp4_shared* shared) {
+  if (!cache || !args || !shared) return 0;
+  int64_t bytes;
+  plan_call(cache, args, shared, &bytes);
+  return bytes;
 }
 
 extern "C" nvfp4_status mxfp4_cache_attention_shared(const mxfp4_cache* cache, const mxfp4_attention* args,
@@ -247,9 +276,8 @@ extern "C" nvfp4_status mxfp4_cache_attention_shared(const mxfp4_cache* cache, c
   if (args->window != 0) return fail(NVFP4_EUNSUPPORTED, nm + ": a window would hide the prefix");
   if (shared->count < 0 || shared->max_group < 0) return fail(NVFP4_EINVAL, nm + ": negative size");
   const int32_t max_group = std::min(shared->max_group, args->total_q);
-  const int64_t need =
-      mxfp4_attention_shared_workspace_bytes(cache->kv_heads, args->q_heads, cache->dim, args->total_q,
-                                             args->max_queries, args->seqs, args->table_ld, shared->count, max_group);
+  int64_t need;
+  const Plan plan = plan_call(cache, args, shared, &need);
   SharedParams p = {};
   const nvfp4_status bad = attn_params(cache, args, need, nm, p.a);
   if (bad != NVFP4_OK || p.a.seqs == 0) return bad;
@@ -265,16 +293,10 @@ extern "C" nvfp4_status mxfp4_cache_attention_shared(const mxfp4_cache* cache, c
   }
   const int64_t heads = args->q_heads;
   const int32_t dim = cache->dim;
-  Plan plan = {};
-  plan.own_many = attn_has_many_rows(dim, int64_t(args->max_queries) * p.a.group);
-  if (shared->count > 0 && max_group > 0)
-    plan = plan_of(dim, cache->kv_heads, p.a.group, args->total_q, args->max_queries, args->seqs,
-                   args->table_ld * cache->page_size, shared->count, max_group);
-  if (shared->count > 0 && max_group > 0 && shared->always != 0) plan.share = true;
   if (!plan.share) return attn_run(cache, p.a, args->max_queries, plan.own_many, args->workspace, s);
   p.groups = shared->groups, p.shared = shared->shared, p.count = shared->count;
-  layout(p, static_cast<uint8_t*>(args->workspace), align256(attn_workspace(dim, true)) + attn_workspace(dim, false),
-         args->total_q, heads, dim, args->seqs, args->table_ld);
+  layout(p, static_cast<uint8_t*>(args->workspace), parts_workspace(dim), args->total_q, heads, dim, args->seqs,
+         args->table_ld);
   nvfp4_status st = launch("launch k_shared_parts", k_shared_parts, dim3(unsigned(p.count + args->seqs)), dim3(kThreads),
                            0, 0, s, p);
   if (st != NVFP4_OK) return st;

@@ -48,7 +48,7 @@ __all__ = ["MXFP4Tensor", "MXFP4Cache", "empty_mxfp4", "empty_mxfp4_cache", "mxf
 
 _FUNCTIONS = ("mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm", "mxfp4_linear_workspace_bytes", "mxfp4_linear",
               "mxfp4_cache_write", "mxfp4_cache_read", "mxfp4_attention_workspace_bytes", "mxfp4_cache_attention",
-              "mxfp4_attention_shared_workspace_bytes", "mxfp4_cache_attention_shared", "head_norm_rotary",
+              "mxfp4_attention_shared_call_workspace_bytes", "mxfp4_cache_attention_shared", "head_norm_rotary",
               "mxfp4_cache_write_rotary", "mxfp4_pages_workspace_bytes", "mxfp4_pages_select", "mxfp4_pages_extend",
               "mxfp4_pages_compact", "mxfp4_cache_copy")
 _lock = threading.Lock()

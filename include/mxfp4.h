@@ -214,7 +214,7 @@ nvfp4_status mxfp4_cache_attention(const mxfp4_cache* cache, const mxfp4_attenti
  *   max_group an upper bound of the queries of a group known to the host
  *   always    0: every sequence reads for itself where that is estimated to be
  *             as fast, from the sizes and as if the block tables were full; 1: never
- *   args      as above, window and sinks 0, workspace_bytes of the query below
+ *   args      as above, window and sinks 0, workspace_bytes of either query below
  * Precision: as above for each part; the parts are binary32 and joined in it. */
 typedef struct {
   const int32_t* groups;
@@ -225,10 +225,16 @@ typedef struct {
   int32_t reserved;
 } mxfp4_shared;
 
-/* Bytes of workspace that mxfp4_cache_attention_shared needs. */
+/* Bytes of workspace that mxfp4_cache_attention_shared needs at the most, whatever
+ * page_size and `always` are. */
 int64_t mxfp4_attention_shared_workspace_bytes(int32_t kv_heads, int32_t q_heads, int32_t dim, int32_t total_q,
                                                int32_t max_queries, int32_t seqs, int64_t table_ld, int32_t count,
                                                int32_t max_group);
+/* Bytes that it needs for these arguments (from the sizes among them; no pointer in
+ * them is followed): those of mxfp4_cache_attention where nothing is shared, while the
+ * parts take two binary32 outputs. */
+int64_t mxfp4_attention_shared_call_workspace_bytes(const mxfp4_cache* cache, const mxfp4_attention* args,
+                                                    const mxfp4_shared* shared);
 
 nvfp4_status mxfp4_cache_attention_shared(const mxfp4_cache* cache, const mxfp4_attention* args,
                                           const mxfp4_shared* shared, nvfp4_stream_t stream);

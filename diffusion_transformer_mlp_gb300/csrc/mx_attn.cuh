@@ -125,26 +125,20 @@ __device__ __forceinline__ Span row_span(const AttnParams& a, int32_t len, int32
   return span_of(a, len, nq, rt * rows / a.group, last / a.group, tok);
 }
 
-// a / b of what is not negative, in 32 bits where that is enough: nearly always, and
-// the long division's latency is that of a load.
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
-}
-
 // Workers that get tiles, all of them one or more, so that all workers of a
 // segment's range have a partial of it.  Of runs of up to `even` tiles all get
 // the longest: a worker less is partials less to join.
 __device__ __forceinline__ int32_t live_workers(const SplitParams& sp, int64_t total) {
-  const int64_t run = max(int64_t(sp.least), quotient(total + sp.workers - 1, sp.workers));
-  if (run <= sp.even) return int32_t(quotient(total + run - 1, run));
-  return int32_t(min(int64_t(sp.workers), quotient(total + sp.least - 1, sp.least)));
+  const int64_t run = max(int64_t(sp.least), (total + sp.workers - 1) / sp.workers);
+  if (run <= sp.even) return int32_t((total + run - 1) / run);
+  return int32_t(min(int64_t(sp.workers), (total + sp.least - 1) / sp.least));
 }
 __device__ __forceinline__ int64_t worker_start(int64_t total, int32_t w, int32_t workers) {
-  return quotient(total * w, workers);
+  return total * w / workers;
 }
 // The worker whose run holds tile x: the largest w with worker_start(w) <= x.
 __device__ __forceinline__ int32_t worker_of(int64_t total, int64_t x, int32_t workers) {
-  return int32_t(quotient((x + 1) * workers - 1, total));
+  return int32_t(((x + 1) * workers - 1) / total);
 }
 
 // A tile of the list.
@@ -187,7 +181,7 @@ __device__ __forceinline__ int32_t cursor_in(Cursor& c, const AttnParams& a, int
     }
   }
   c.s = row_span(a, c.len, c.nq, c.rt, rows, tok);
-  c.h = int32_t(quotient(rem, c.s.n + edge));
+  c.h = int32_t(rem / (c.s.n + edge));
   const int32_t off = int32_t(rem - int64_t(c.h) * (c.s.n + edge));
   c.t = max(off - edge, 0);
   return max(edge - off, 0);

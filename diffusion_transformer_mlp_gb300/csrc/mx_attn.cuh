@@ -341,9 +341,11 @@ __device__ __forceinline__ void store_o8_words(const AttnParams& a, uint16_t* ds
     dst[4] = uint16_t(w.z), dst[5] = uint16_t(w.z >> 16), dst[6] = uint16_t(w.w), dst[7] = uint16_t(w.w >> 16);
   }
 }
-// The same at element `off` of the output, from binary32.
+// The same at element `off` of the output, from binary32.  kF32: whether the output is,
+// where that is known when compiled, else below 0.
+template <int kF32 = -1>
 __device__ __forceinline__ void store_o8(const AttnParams& a, int64_t off, const float (&f)[8]) {
-  if (a.o_f32) {
+  if (kF32 < 0 ? a.o_f32 != 0 : kF32 != 0) {
     float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + off);
     dst[0] = make_float4(f[0], f[1], f[2], f[3]);
     dst[1] = make_float4(f[4], f[5], f[6], f[7]);

@@ -92,3 +92,13 @@ def test_sequences_outside_save_nothing(hq, hkv, dim, grouped, others, nq):
     kw = dict(max_group=sum(c.nq[1:1 + others]))
     shared = c.run(**kw).clone()
     assert torch.equal(c.run(always=False, **kw), shared)
+
+
+@pytest.mark.parametrize("hq,hkv,dim,page", [(8, 2, 64, 16), (8, 2, 128, 64), (6, 2, 256, 32), (32, 2, 128, 16)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_chunks_behind_a_prefix(hq, hkv, dim, page, causal):
+    """Hundreds of queries a sequence, beside sequences that decode and one outside."""
+    lens, nq = [700, 1201, 513, 400, 90], [300, 801, 1, 17, 33]
+    c = Shared([4], [383], lens, nq, hq, hkv, dim, page, seed=dim + page)
+    c.run(causal=causal)
+    c.check(causal)

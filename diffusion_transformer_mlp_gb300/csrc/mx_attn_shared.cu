@@ -6,8 +6,9 @@
 //
 // with l the logarithm of a part's sum of exponentials.  The prefix is one
 // sequence whose queries are those of all sequences of the group, every one of
-// which sees all of it: its keys are read and decoded once for many rows, which
-// is work for k_attn_chunk where they are more than 64.  What a sequence has of
+// which sees all of it: its keys are read and decoded once for many rows, which is
+// work for k_attn_chunk where they are more than k_attn_stream is made for (64, dim
+// 256: 16) or where it is estimated to be quicker (plan_of).  What a sequence has of
 // its own is a sequence whose block table begins behind the prefix; positions
 // only count relative to its end, so nothing else changes.  That takes whole
 // pages, hence the prefix is rounded down to them.
@@ -17,7 +18,8 @@
 // k_attn_stream's and every sequence has one query, which sees all keys of either
 // part, both sets are one list of sequences for one launch: rows total_q and
 // above of the outputs are the own tokens' (4 samples of a prompt of 2,049
-// tokens: 32 us in two launches, so 20).
+// tokens: 32 us in two launches, so 20).  Queries outside of the groups are rows
+// between those of the prefixes and the own ones, and of no sequence.
 //
 // What bounds it: the latencies of five launches and of k_attn_chunk's first and last
 // tiles, before the work itself.  Two prompts of 16,001 and 12,001 tokens, 32 and 16

@@ -206,9 +206,11 @@ def mxfp4_cache_attention_shared(q: torch.Tensor, cache: MXFP4Cache, table: torc
     groups [n + 1] int32: first sequence of each group; shared [n] int32: tokens
     that the sequences of a group have in common (their block tables name pages
     with the same bytes there, as after mxfp4_pages_select); max_group an upper
-    bound of a group's queries (default: all of q).  Where reading the prefix by
-    every sequence is estimated to be as fast (few sequences, small block tables),
-    that is done, but with `always`.  The other arguments are those of
+    bound of a group's queries (default: all of q; give it where most sequences are
+    in no group).  Where reading the prefix by every sequence is estimated to be as
+    fast (few sequences that share, small block tables), that is done, but with
+    `always`; the estimate takes the tables for full, so for short prefixes in wide
+    tables call mxfp4_cache_attention.  The other arguments are those of
     mxfp4_cache_attention; there is no window."""
     return _ext.cache_attention_shared(q, cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales, table, lens,
                                        q_starts, max_queries, scale, causal, 0, 0, out, lse, status, stream, groups,
@@ -263,7 +265,7 @@ def head_norm_rotary(q: torch.Tensor, k: torch.Tensor | None, rotary: HeadRotary
 
     q and k [tokens, heads, dim] bfloat16, float16 or float32, any strides along
     tokens and heads; weights [dim] of the same type or float32.  The outputs may
-    be q and k themselves."""
+    be q and k themselves (q_out is q, k_out is k), and share memory with nothing else."""
     return _ext.norm_rotary(q, k, rotary.turns, rotary.axis, rotary.interleaved, positions, q_weight, k_weight, eps,
                             q_out, k_out, stream)
 

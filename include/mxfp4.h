@@ -211,9 +211,13 @@ nvfp4_status mxfp4_cache_attention(const mxfp4_cache* cache, const mxfp4_attenti
  *   groups    device int32 [count + 1], not decreasing; what lies outside
  *             0 .. seqs counts as its ends
  *   shared    device int32 [count]
- *   max_group an upper bound of the queries of a group known to the host
+ *   max_group an upper bound of the queries of a group known to the host; the
+ *             estimate below takes count * max_group queries, if there are as
+ *             many, for those that share
  *   always    0: every sequence reads for itself where that is estimated to be
- *             as fast, from the sizes and as if the block tables were full; 1: never
+ *             as fast, from the sizes and as if the block tables were full (for
+ *             short prefixes in tables of long ones mxfp4_cache_attention is the
+ *             quicker call); 1: never
  *   args      as above, window and sinks 0, workspace_bytes of either query below
  * Precision: as above for each part; the parts are binary32 and joined in it. */
 typedef struct {
@@ -241,7 +245,8 @@ nvfp4_status mxfp4_cache_attention_shared(const mxfp4_cache* cache, const mxfp4_
 
 /* Heads of tokens: x [tokens, heads, dim], unit stride along dim, strides in
  * elements along tokens (st) and heads (sh); out alike (o_st, o_sh), and may be
- * x itself with the same strides.  weight [dim] of the norm, or NULL for none. */
+ * x itself with the same strides, but shares memory with no other heads of the
+ * call.  weight [dim] of the norm, or NULL for none. */
 typedef struct {
   const void* x;
   void* out;
